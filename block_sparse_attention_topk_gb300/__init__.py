@@ -22,6 +22,8 @@ from . import build as _build
 BSA_OK = 0
 BSA_DTYPE_BF16 = 0
 BSA_DTYPE_FP32 = 1
+BSA_DTYPE_E4M3 = 2
+BSA_DTYPE_E5M2 = 3
 BSA_PATH_ROW = 0
 BSA_PATH_SPLIT = 1
 BSA_PATH_GROUP = 2
@@ -44,7 +46,8 @@ EXPORTED = [
     "bsa_topk_workspace_bytes", "bsa_topk_select", "bsa_build_sparse_block_table",
     "bsa_topk_select_sparse_table", "bsa_select_policy", "bsa_topk_select_noalloc",
     "bsa_index_score_topk_select", "bsa_sparse_decode_attention", "bsa_set_status_word",
-    "bsa_read_status",
+    "bsa_read_status", "bsa_rope", "bsa_append_kv_decode", "bsa_append_kv_varlen",
+    "bsa_attention_q8_workspace_bytes", "bsa_sparse_decode_attention_q8",
 ]
 # bits of the device status word (bsa_set_status_word)
 BSA_STATUS_BAD_BLOCK_ID = 0x1
@@ -53,6 +56,10 @@ BSA_STATUS_BAD_CONTEXT = 0x4
 MAX_ATTN_GROUP = 8
 MAX_INDEX_DIM = 1024
 MAX_INDEX_QUERIES = 16
+MAX_ATTN_Q8_GROUP = 16
+MAX_CACHE_DIM = 256
+BSA_ROPE_INTERLEAVED = 1
+BSA_ROPE_INVERSE = 2
 
 
 class BsaError(RuntimeError):
@@ -71,6 +78,21 @@ class LaunchPolicy(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class AppendArgs(ctypes.Structure):
+    """bsa_append_args_t of include/bsa_topk.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "q")]
+                + [(n, ctypes.c_int64) for n in ("T", "H", "Hq", "D", "k_token_stride",
+                                                 "k_head_stride", "v_token_stride",
+                                                 "v_head_stride", "q_token_stride",
+                                                 "q_head_stride")]
+                + [(n, ctypes.c_void_p) for n in ("q_out", "positions", "inv_freq", "freq_axis")]
+                + [(n, ctypes.c_int32) for n in ("axes", "rot_dim", "flags", "cache_dtype")]
+                + [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                   ("num_pages", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
+                   ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                   ("num_reqs", ctypes.c_int64), ("max_blocks", ctypes.c_int64)])
 
 
 _lib = None
@@ -116,8 +138,18 @@ def lib() -> ctypes.CDLL:
                                                       i32, ctypes.c_float, vp, vp]
             L.bsa_set_status_word.argtypes = [vp]
             L.bsa_read_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32, vp]
+            L.bsa_rope.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i32, vp, vp, i32, i32, vp,
+                                   i64, i64, vp]
+            args = ctypes.POINTER(AppendArgs)
+            L.bsa_append_kv_decode.argtypes = [args, vp, i32, vp]
+            L.bsa_append_kv_varlen.argtypes = [args, vp, vp, vp]
+            L.bsa_attention_q8_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
+            L.bsa_attention_q8_workspace_bytes.restype = sz
+            L.bsa_sparse_decode_attention_q8.argtypes = [vp, vp, vp, i32, vp, vp, i64, vp, vp, i64,
+                                                         i64, i64, i64, i32, ctypes.c_float, vp, vp,
+                                                         sz, vp]
             for name in EXPORTED[1:]:
-                if name != "bsa_topk_workspace_bytes":
+                if not name.endswith("_workspace_bytes"):
                     getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -132,6 +164,8 @@ def _call(fn: str, device: torch.device, *args):
     """Calls C entry point `fn` with `device` current: the library takes the
     launch policy's SM count, the workspace size and its scratch address from
     the current device."""
+    if device.index == torch.cuda.current_device():
+        return _check(fn, getattr(lib(), fn)(*args))
     with torch.cuda.device(device):
         _check(fn, getattr(lib(), fn)(*args))
 
@@ -184,7 +218,10 @@ def _score_dtype(scores: torch.Tensor) -> int:
 # One workspace per (device, stream), grown on demand (the library clears the
 # parts it needs cleared on every call).  Calls on one stream run in order,
 # so they may share it; calls on different streams get different buffers.
+# A buffer handed out during a graph capture stays alive: replays write to it
+# even after a later call has needed, and cached, a larger one.
 _ws_cache: dict = {}
+_ws_captured: list = []
 _ws_lock = threading.Lock()
 
 
@@ -197,6 +234,8 @@ def _workspace(device: torch.device, nbytes: int) -> torch.Tensor | None:
         if ws is None or ws.numel() < nbytes:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
             _ws_cache[key] = ws
+        if torch.cuda.is_current_stream_capturing() and all(w is not ws for w in _ws_captured):
+            _ws_captured.append(ws)
         return ws
 
 
@@ -509,3 +548,244 @@ def bsa_read_status(clear: bool = True, device: torch.device | None = None) -> i
     out = ctypes.c_uint32(0)
     _call("bsa_read_status", dev, ctypes.byref(out), int(bool(clear)), _stream(dev))
     return int(out.value)
+
+
+_CACHE_DTYPES = {torch.bfloat16: BSA_DTYPE_BF16, torch.float8_e4m3fn: BSA_DTYPE_E4M3,
+                 torch.float8_e5m2: BSA_DTYPE_E5M2}
+
+
+def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, T: int | None,
+           D: int | None):
+    """A [T, heads, D] CUDA tensor whose head rows are contiguous; any token
+    and head strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or t.dtype != dtype \
+            or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor [T, heads, D] on {device}")
+    if (T is not None and t.shape[0] != T) or (D is not None and t.shape[2] != D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{T}, heads, {D}]")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    return t.stride(0), t.stride(1)
+
+
+def _rope_args(T: int, device: torch.device, positions: torch.Tensor | None,
+               inv_freq: torch.Tensor | None, freq_axis: torch.Tensor | None):
+    """(positions, axes, inv_freq, freq_axis, rot_dim) as the C calls take them."""
+    axes, half = 1, 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float32 \
+                or inv_freq.device != device or inv_freq.dim() != 1 \
+                or not inv_freq.is_contiguous():
+            raise ValueError(f"inv_freq must be a contiguous fp32 tensor [rot_dim / 2] on {device}")
+        half = inv_freq.shape[0]
+    if positions is not None:
+        if isinstance(positions, torch.Tensor) and positions.dim() == 2:
+            axes = positions.shape[0]
+            _dev_i32(positions, "positions", device, (axes, T))
+        else:
+            _dev_i32(positions, "positions", device, (T,))
+    if freq_axis is not None:
+        _dev_i32(freq_axis, "freq_axis", device, (half,))
+    elif axes > 1 and half:
+        raise ValueError("freq_axis is needed with several position axes")
+    return (0 if positions is None else positions.data_ptr(), axes,
+            0 if inv_freq is None else inv_freq.data_ptr(),
+            0 if freq_axis is None else freq_axis.data_ptr(), 2 * half)
+
+
+def bsa_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+             freq_axis: torch.Tensor | None = None, interleaved: bool = False,
+             inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotary positions.  x bf16 or fp32 [T, H, D] (head rows contiguous, any
+    strides), positions int32 [T] or [axes, T], inv_freq fp32 [rot_dim / 2],
+    freq_axis int32 [rot_dim / 2] (the axis each frequency turns with; needed
+    with several axes).  Returns out, by default a new contiguous tensor; x
+    itself rotates in place.  ``inverse`` turns back: applied to the gradient
+    of the output it gives the gradient of x."""
+    dt = _score_dtype(x) if isinstance(x, torch.Tensor) else None
+    dev = x.device
+    xs = _heads(x, "x", x.dtype, dev, None, None)
+    T, H, D = x.shape
+    if positions is None or inv_freq is None:
+        raise ValueError("positions and inv_freq are needed")
+    pos, axes, inv, axis, rot = _rope_args(T, dev, positions, inv_freq, freq_axis)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+    os_ = _heads(out, "out", x.dtype, dev, T, D)
+    if out.shape[1] != H:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, H, D)}")
+    _call("bsa_rope", dev, x.data_ptr(), dt, T, H, D, *xs, pos, axes, inv, axis, rot,
+          (BSA_ROPE_INTERLEAVED if interleaved else 0) | (BSA_ROPE_INVERSE if inverse else 0),
+          out.data_ptr(), *os_, _stream(dev))
+    return out
+
+
+def _cache(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype,
+           shape: tuple) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype \
+            or not t.is_contiguous() or t.dim() != len(shape) + 1 or tuple(t.shape[1:]) != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [num_pages, "
+                         f"{', '.join(map(str, shape))}] on {device}")
+    return t
+
+
+def _q8_caches(k_cache, v_cache, k_scale, v_scale, device, H, D):
+    """(cache dtype code, num_pages) of a checked pair of caches and scales."""
+    code = _CACHE_DTYPES.get(getattr(k_cache, "dtype", None))
+    if code is None:
+        raise ValueError("k_cache must be bfloat16, float8_e4m3fn or float8_e5m2")
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _cache(c, name, device, k_cache.dtype, (PAGES_PER_SPARSE_BLOCK * 2, H, D))
+    n = k_cache.shape[0]
+    if v_cache.shape[0] != n:
+        raise ValueError("k_cache and v_cache hold different page counts")
+    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if code == BSA_DTYPE_BF16:
+            if s is not None:
+                raise ValueError(f"{name} must be None with a bfloat16 cache")
+        else:
+            _cache(s, name, device, torch.float32, (H,))
+            if s.shape[0] != n:
+                raise ValueError(f"{name} has {s.shape[0]} pages, expected {n}")
+    return code, n
+
+
+def _append(k, v, k_cache, v_cache, block_table, num_reqs, q, inv_freq, positions, freq_axis,
+            interleaved, k_scale, v_scale, q_out):
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a bf16 CUDA tensor [T, H, D]")
+    dev = k.device
+    ks = _heads(k, "k", torch.bfloat16, dev, None, None)
+    T, H, D = k.shape
+    vs = _heads(v, "v", torch.bfloat16, dev, T, D)
+    if v.shape[1] != H:
+        raise ValueError(f"v has {v.shape[1]} heads, expected {H}")
+    Hq, qs = 0, (0, 0)
+    if q is not None:
+        qs = _heads(q, "q", torch.bfloat16, dev, T, D)
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        if not isinstance(q_out, torch.Tensor) or q_out.dtype != torch.bfloat16 \
+                or q_out.device != dev or tuple(q_out.shape) != (T, Hq, D) \
+                or not q_out.is_contiguous():
+            raise ValueError(f"q_out must be a contiguous bf16 tensor [{T}, {Hq}, {D}] on {dev}")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    code, pages = _q8_caches(k_cache, v_cache, k_scale, v_scale, dev, H, D)
+    _dev_i32(block_table, "block_table", dev)
+    if block_table.dim() != 2 or block_table.shape[0] != num_reqs:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected "
+                         f"[{num_reqs}, max_blocks]")
+    pos, axes, inv, axis, rot = _rope_args(T, dev, positions, inv_freq, freq_axis)
+    args = AppendArgs(
+        k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(), T, H, Hq, D, *ks, *vs,
+        *qs, None if q is None else q_out.data_ptr(), pos, inv, axis, axes, rot,
+        BSA_ROPE_INTERLEAVED if interleaved else 0, code, k_cache.data_ptr(), v_cache.data_ptr(),
+        pages, None if k_scale is None else k_scale.data_ptr(),
+        None if v_scale is None else v_scale.data_ptr(), block_table.data_ptr(), num_reqs,
+        block_table.shape[1])
+    return dev, args, q_out
+
+
+def bsa_append_kv_decode(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, block_table: torch.Tensor,
+                         seq_lens: torch.Tensor, decode_query_len: int,
+                         q: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None,
+                         positions: torch.Tensor | None = None,
+                         freq_axis: torch.Tensor | None = None, interleaved: bool = False,
+                         k_scale: torch.Tensor | None = None,
+                         v_scale: torch.Tensor | None = None,
+                         q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Appends the decode rows' keys, rotated, and values to the paged cache
+    and rotates their queries.  k, v bf16 [T, H, D] and q bf16 [T, Hq, D]
+    (head rows contiguous, any strides, e.g. parts of one fused buffer);
+    k_cache, v_cache [num_pages, 16, H, D] in bf16, float8_e4m3fn or
+    float8_e5m2, the last two with fp32 k_scale, v_scale [num_pages, H];
+    block_table int32 [num_reqs, max_blocks]; seq_lens int32 [num_reqs], the
+    appended tokens counted.  Rotary arguments as for bsa_rope; positions
+    defaults to the position in the sequence, inv_freq None rotates nothing.
+    Returns q_out bf16 [T, Hq, D] (None without q)."""
+    _dev_i32(seq_lens, "seq_lens")
+    if seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be 1-D [num_reqs]")
+    dev, args, q_out = _append(k, v, k_cache, v_cache, block_table, seq_lens.shape[0], q, inv_freq,
+                               positions, freq_axis, interleaved, k_scale, v_scale, q_out)
+    if seq_lens.device != dev:
+        raise ValueError(f"seq_lens is on {seq_lens.device}, expected {dev}")
+    _call("bsa_append_kv_decode", dev, args, seq_lens.data_ptr(), decode_query_len, _stream(dev))
+    return q_out
+
+
+def bsa_append_kv_varlen(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, block_table: torch.Tensor,
+                         cu_seqlens_q: torch.Tensor, prefix_lens: torch.Tensor,
+                         q: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None,
+                         positions: torch.Tensor | None = None,
+                         freq_axis: torch.Tensor | None = None, interleaved: bool = False,
+                         k_scale: torch.Tensor | None = None,
+                         v_scale: torch.Tensor | None = None,
+                         q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """bsa_append_kv_decode for rows of varying count: sequence i owns rows
+    [cu_seqlens_q[i], cu_seqlens_q[i + 1]) and its j-th token sits at position
+    prefix_lens[i] + j (int32 [num_seqs + 1] and [num_seqs])."""
+    _dev_i32(prefix_lens, "prefix_lens")
+    if prefix_lens.dim() != 1:
+        raise ValueError("prefix_lens must be 1-D [num_seqs]")
+    N = prefix_lens.shape[0]
+    dev, args, q_out = _append(k, v, k_cache, v_cache, block_table, N, q, inv_freq, positions,
+                               freq_axis, interleaved, k_scale, v_scale, q_out)
+    if prefix_lens.device != dev:
+        raise ValueError(f"prefix_lens is on {prefix_lens.device}, expected {dev}")
+    _dev_i32(cu_seqlens_q, "cu_seqlens_q", dev, (N + 1,))
+    _call("bsa_append_kv_varlen", dev, args, cu_seqlens_q.data_ptr(), prefix_lens.data_ptr(),
+          _stream(dev))
+    return q_out
+
+
+def bsa_attention_q8_workspace_bytes(T: int, H: int, G: int, D: int, K: int,
+                                     device: torch.device | None = None) -> int:
+    """Workspace bytes of bsa_sparse_decode_attention_q8 on `device` (default:
+    the current one)."""
+    if device is None or device.index == torch.cuda.current_device():
+        return int(lib().bsa_attention_q8_workspace_bytes(T, H, G, D, K))
+    with torch.cuda.device(device):
+        return int(lib().bsa_attention_q8_workspace_bytes(T, H, G, D, K))
+
+
+def bsa_sparse_decode_attention_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   k_scale: torch.Tensor, v_scale: torch.Tensor,
+                                   sparse_bt: torch.Tensor, sparse_ctx: torch.Tensor,
+                                   scale: float | None = None, out: torch.Tensor | None = None,
+                                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Sparse decode attention over the page-16 table and a cache held in 8
+    bits.  q bf16 [T, H, G, D]; k_cache, v_cache float8_e4m3fn or float8_e5m2
+    [num_pages, 16, H, D] with fp32 k_scale, v_scale [num_pages, H];
+    sparse_bt int32 [T, H, K*8], sparse_ctx int32 [T, H]; returns bf16
+    [T, H, G, D].  The scale defaults to 1 / sqrt(D)."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4 \
+            or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [T, H, G, D]")
+    dev = q.device
+    T, H, G, D = q.shape
+    code, pages = _q8_caches(k_cache, v_cache, k_scale, v_scale, dev, H, D)
+    if code == BSA_DTYPE_BF16:
+        raise ValueError("the caches must be float8_e4m3fn or float8_e5m2")
+    _dev_i32(sparse_bt, "sparse_bt", dev)
+    if sparse_bt.dim() != 3 or tuple(sparse_bt.shape[:2]) != (T, H) or sparse_bt.shape[2] % 8:
+        raise ValueError(f"sparse_bt must be [{T}, {H}, K*8]")
+    K = sparse_bt.shape[2] // PAGES_PER_SPARSE_BLOCK
+    _dev_i32(sparse_ctx, "sparse_ctx", dev, (T, H))
+    if out is None:
+        out = torch.empty((T, H, G, D), dtype=torch.bfloat16, device=dev)
+    if out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous() \
+            or tuple(out.shape) != (T, H, G, D):
+        raise ValueError(f"out must be a contiguous bf16 tensor [{T}, {H}, {G}, {D}] on {dev}")
+    need = bsa_attention_q8_workspace_bytes(T, H, G, D, K, dev)
+    workspace, wbytes = _workspace_arg(workspace, dev, need)
+    _call("bsa_sparse_decode_attention_q8", dev, q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), code, k_scale.data_ptr(), v_scale.data_ptr(), pages,
+          sparse_bt.data_ptr(), sparse_ctx.data_ptr(), T, H, G, D, K,
+          D ** -0.5 if scale is None else scale, out.data_ptr(),
+          0 if workspace is None else workspace.data_ptr(), wbytes, _stream(dev))
+    return out

@@ -307,10 +307,10 @@ const char* bsa_status_string(int status) {
         case BSA_ERR_NULL: return "a required pointer is NULL";
         case BSA_ERR_SHAPE: return "invalid size or stride";
         case BSA_ERR_TOPK: return "invalid topk / num_init / num_local";
-        case BSA_ERR_DTYPE: return "unknown score dtype";
+        case BSA_ERR_DTYPE: return "unknown element type";
         case BSA_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
         case BSA_ERR_ROWS: return "T != num_reqs * decode_query_len";
-        case BSA_ERR_ALIGN: return "scores pointer not aligned to its element size";
+        case BSA_ERR_ALIGN: return "a pointer or stride is not aligned as the call needs";
         case BSA_ERR_CAPACITY: return "request needs more scratch than the built-in array holds";
         default: break;
     }

@@ -71,6 +71,9 @@ extern "C" {
 /* score element types */
 #define BSA_DTYPE_BF16 0
 #define BSA_DTYPE_FP32 1
+/* element types of a key/value cache held in 8 bits */
+#define BSA_DTYPE_E4M3 2    /* 4 exponent bits, largest value 448, no infinities */
+#define BSA_DTYPE_E5M2 3    /* 5 exponent bits, largest value 57344              */
 
 /* selector paths chosen by the launch policy */
 #define BSA_PATH_ROW 0      /* one warp streams a whole row                 */
@@ -268,6 +271,140 @@ int bsa_sparse_decode_attention(const void* q, const void* k_cache, const void* 
                                 const int32_t* sparse_ctx, int64_t T, int64_t H, int64_t G,
                                 int64_t D, int32_t K, float scale, float* out, void* stream);
 
+/* ---- the cache around the sparse attention ------------------------------- */
+/* The reports name the paged cache and the rotated queries and keys only as
+ * inputs of their kernels; the operators below fill and read such a cache.
+ *
+ * Rotary positions.  rot_dim values of each head (an even number, the first
+ * ones) form rot_dim / 2 pairs; pair i of a row at position p turns by
+ * angle = p * inv_freq[i]:
+ *   a' = a cos(angle) - b sin(angle),  b' = b cos(angle) + a sin(angle).
+ * The pair is (i, i + rot_dim / 2), or (2i, 2i + 1) with
+ * BSA_ROPE_INTERLEAVED; the values from rot_dim on pass through.  With
+ * several position axes (time, height, width), positions is int32
+ * [axes, T] and pair i turns with axis freq_axis[i] (clamped into
+ * [0, axes)); freq_axis may be NULL when axes is 1.  The product
+ * p * inv_freq[i] is reduced to a fraction of a turn in 64-bit fixed point,
+ * so far positions lose nothing.  inv_freq: float[rot_dim / 2]. */
+#define BSA_ROPE_INTERLEAVED 1
+#define BSA_ROPE_INVERSE 2      /* turn back: the gradient of the rotation */
+#define BSA_MAX_ROPE_DIM 1024
+#define BSA_MAX_ROPE_AXES 8
+
+/* Rotates T rows of H heads: x and out hold element (t, h, d) at
+ * t * token_stride + h * head_stride + d, dtype BSA_DTYPE_BF16 or
+ * BSA_DTYPE_FP32, 1 <= D <= BSA_MAX_ROPE_DIM, any element alignment; 32-bit
+ * arithmetic, rounded once.  out may be x itself with the same strides (in
+ * place) and must not overlap it otherwise; its rows must not overlap.
+ * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_DTYPE, BSA_ERR_ALIGN. */
+int bsa_rope(const void* x, int32_t dtype, int64_t T, int64_t H, int64_t D,
+             int64_t token_stride, int64_t head_stride, const int32_t* positions, int32_t axes,
+             const float* inv_freq, const int32_t* freq_axis, int32_t rot_dim, int32_t flags,
+             void* out, int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/* Appending a step's keys and values to the paged cache, the keys rotated on
+ * the way, with the step's queries rotated in the same launch (HOST struct
+ * of device pointers, read during the call). */
+#define BSA_MAX_CACHE_DIM 256
+typedef struct bsa_append_args {
+    /* bf16 [T, H, D] keys and values and (or NULL) [T, Hq, D] queries:
+     * element (t, h, d) at t * token_stride + h * head_stride + d; pointers
+     * 16-byte aligned, strides and D multiples of 8 (D of 16), D <=
+     * BSA_MAX_CACHE_DIM.  They may be parts of one fused buffer. */
+    const void* k;
+    const void* v;
+    const void* q;
+    int64_t T, H, Hq, D;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t q_token_stride, q_head_stride;
+    /* rotated queries, bf16 [T, Hq, D] contiguous, 16-byte aligned (NULL
+     * exactly when q is).  Rows of no sequence or at a negative position
+     * are padding: their queries are written as zeros. */
+    void* q_out;
+    /* rotary positions as above; positions NULL: the position in the
+     * sequence (axes 1).  rot_dim 0: no rotation (inv_freq may be NULL). */
+    const int32_t* positions;
+    const float* inv_freq;
+    const int32_t* freq_axis;
+    int32_t axes, rot_dim, flags;
+    /* the cache, [num_pages, 16, H, D] contiguous, 16-byte aligned, of
+     * cache_dtype BSA_DTYPE_BF16, BSA_DTYPE_E4M3 or BSA_DTYPE_E5M2 */
+    int32_t cache_dtype;
+    void* k_cache;
+    void* v_cache;
+    int64_t num_pages;
+    /* 8 bits: float [num_pages, H], one scale per page and head (NULL for bf16) */
+    float* k_scale;
+    float* v_scale;
+    /* int32 [num_reqs, max_blocks]: physical 128-token blocks; max_blocks < 2^24 */
+    const int32_t* block_table;
+    int64_t num_reqs, max_blocks;
+} bsa_append_args_t;
+
+/* The token of sequence i at position p >= 0 goes to page
+ * block_table[i, p / 128] * 8 + p % 128 / 16, slot p % 16.  In 8 bits a
+ * stored value is code * scale, with the scale of its page and head a power
+ * of two: a page's scale becomes
+ *   s = max(s_old, s_new),  s_new = the smallest power of two >= 2^-126 with
+ *   max |finite value of the call's tokens in the page| / s_new <= the type's
+ *   largest value (no bound from all-zero tokens),
+ * where s_old is the page's scale if the call's first token in the page has a
+ * slot above 0 (tokens before it are kept) and 0 otherwise (a fresh page);
+ * s = 1 when both are 0.  New codes are value / s rounded to nearest, finite
+ * and infinite values beyond the range going to its end and NaN staying NaN.
+ * When s > s_old > 0, the codes of the slots before the call's first become
+ * code * s_old / s, rounded again (exact except in the type's subnormals).
+ * Slots after the call's tokens are left as they are.  A page is written
+ * for one sequence only: sequences that share pages must not append to them.
+ * A token whose position lies past max_blocks * 128 (BSA_STATUS_BAD_CONTEXT)
+ * or whose page lies outside [0, num_pages) (BSA_STATUS_BAD_BLOCK_ID) is not
+ * stored; its query is rotated all the same.
+ *
+ * _decode: T = num_reqs * decode_query_len rows, row t of request
+ *   t / decode_query_len at position seq_lens[req] - decode_query_len +
+ *   t % decode_query_len (seq_lens counts the appended tokens), as in
+ *   bsa_num_valid_pages_decode.
+ * _varlen: sequence i owns rows [cu_seqlens_q[i], cu_seqlens_q[i + 1]), the
+ *   j-th at position prefix_lens[i] + j, as in bsa_num_valid_pages_varlen.
+ * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_DTYPE, BSA_ERR_ALIGN,
+ * BSA_ERR_ROWS. */
+int bsa_append_kv_decode(const bsa_append_args_t* args, const int32_t* seq_lens,
+                         int32_t decode_query_len, void* stream);
+int bsa_append_kv_varlen(const bsa_append_args_t* args, const int32_t* cu_seqlens_q,
+                         const int32_t* prefix_lens, void* stream);
+
+/* Largest number of query heads per KV head of the 8-bit attention. */
+#define BSA_MAX_ATTN_Q8_GROUP 16
+
+/* Device workspace of bsa_sparse_decode_attention_q8 for these sizes on the
+ * current device (0 when every row is taken by one CTA).  Host-only. */
+size_t bsa_attention_q8_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t D, int32_t K);
+
+/* bsa_sparse_decode_attention over a cache held in 8 bits with one scale per
+ * 16-token page and head:
+ *   k_j = k_cache[page, slot, h] * k_scale[page, h], v_j likewise,
+ *   out[t, h, g] = sum_j softmax_j(scale * q[t, h, g] . k_j) v_j
+ * over the first sparse_ctx[t, h] table tokens, with the page, slot, empty
+ * and out-of-range rules (and status bits) of bsa_sparse_decode_attention.
+ *   q, out: bf16 [T, H, G, D], 16-byte aligned; k_cache, v_cache: dtype
+ *   BSA_DTYPE_E4M3 or BSA_DTYPE_E5M2, [num_pages, 16, H, D], 16-byte aligned,
+ *   num_pages < 2^27; k_scale, v_scale: float [num_pages, H], positive; D in
+ *   {64, 128, 256}; 1 <= G <= BSA_MAX_ATTN_Q8_GROUP.  The slots of a page
+ *   past the context may hold anything, NaN codes included.
+ *   workspace: at least bsa_attention_q8_workspace_bytes(...) bytes, 256-byte
+ *   aligned, any contents; may be NULL when that is 0.  Calls that share a
+ *   workspace must not overlap on the GPU.
+ * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_TOPK (K < 1 or > BSA_MAX_TOPK),
+ * BSA_ERR_DTYPE, BSA_ERR_ALIGN, BSA_ERR_WORKSPACE. */
+int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache, const void* v_cache,
+                                   int32_t cache_dtype, const float* k_scale,
+                                   const float* v_scale, int64_t num_pages,
+                                   const int32_t* sparse_bt, const int32_t* sparse_ctx,
+                                   int64_t T, int64_t H, int64_t G, int64_t D, int32_t K,
+                                   float scale, void* out, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /* Size of the device scratch array behind bsa_topk_select_noalloc. */
 #define BSA_NOALLOC_SCRATCH_BYTES (16u << 20)
 
@@ -321,12 +458,16 @@ int bsa_select_policy(int64_t rows, int64_t M, int32_t K, int32_t dtype, int32_t
  *                            BSA_MAX_PHYS_BLOCK (its page ids phys * 8 + p are
  *                            still written as computed); or the index scoring
  *                            met an entry of a causal block below max_blocks
- *                            outside [0, num_phys_blocks) (scored -inf).
+ *                            outside [0, num_phys_blocks) (scored -inf); or
+                            the append met a token whose page lies outside
+                            the cache (not stored).
  *   BSA_STATUS_BAD_PAGE      the sparse decode attention met a table entry of
  *                            a context token outside [0, num_pages) (the token
  *                            takes no part).
  *   BSA_STATUS_BAD_CONTEXT   the sparse decode attention met a sparse_ctx
- *                            entry below 0 or above K * 128 (clamped). */
+ *                            entry below 0 or above K * 128 (clamped); or the
+ *                            append met a token past the block table (not
+ *                            stored). */
 #define BSA_STATUS_BAD_BLOCK_ID 0x1u
 #define BSA_STATUS_BAD_PAGE 0x2u
 #define BSA_STATUS_BAD_CONTEXT 0x4u

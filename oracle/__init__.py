@@ -66,7 +66,21 @@ def _declare(lib):
     lib.oracle_sparse_decode_attention.argtypes = [u16p, u16p, u16p, i64, i32p, i32p, i64, i64,
                                                    i64, i64, i32, ctypes.c_double,
                                                    ctypes.POINTER(ctypes.c_double)]
-    for name in ("oracle_num_valid_pages_decode", "oracle_num_valid_pages_varlen",
+    f64p, f32p = ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_float)
+    u8p = ctypes.POINTER(ctypes.c_uint8)
+    lib.oracle_code_value.argtypes = [ctypes.c_uint8, ctypes.c_int]
+    lib.oracle_code_value.restype = ctypes.c_double
+    lib.oracle_code_of.argtypes = [ctypes.c_double, ctypes.c_int]
+    lib.oracle_code_of.restype = ctypes.c_uint8
+    lib.oracle_rope.argtypes = [f64p, i64, i64, i64, i32p, f32p, i32p, i32, ctypes.c_int,
+                                ctypes.c_int, f64p]
+    lib.oracle_append.argtypes = [f64p, i64, i64, i64, i32p, i32p, i32p, i64, ctypes.c_int, i64,
+                                  f64p, f32p, u8p]
+    lib.oracle_sparse_decode_attention_q8.argtypes = [
+        u16p, u8p, u8p, ctypes.c_int, f32p, f32p, i64, i32p, i32p, i64, i64, i64, i64, i32,
+        ctypes.c_double, f64p]
+    for name in ("oracle_rope", "oracle_append", "oracle_sparse_decode_attention_q8",
+                 "oracle_num_valid_pages_decode", "oracle_num_valid_pages_varlen",
                  "oracle_topk_select", "oracle_build_sparse_block_table",
                  "oracle_topk_select_sparse_table", "oracle_index_scores",
                  "oracle_sparse_decode_attention"):
@@ -274,4 +288,82 @@ def sparse_decode_attention(q, k_cache, v_cache, sparse_bt, sparse_ctx, scale: f
         _ptr(ctx), T, H, G, D, K, float(scale), out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)))
     if rc != 0:
         raise ValueError(f"oracle_sparse_decode_attention rc={rc}")
+    return out
+
+
+# ---- the cache around the sparse attention ---------------------------------
+
+E4M3, E5M2 = 2, 3
+
+
+def _as(a, dtype, ctype):
+    a = np.ascontiguousarray(a, dtype=dtype)
+    return a, a.ctypes.data_as(ctypes.POINTER(ctype))
+
+
+def code_values(kind: int) -> np.ndarray:
+    """The value of each of the 256 codes of an 8-bit type."""
+    return np.array([_load().oracle_code_value(c, kind) for c in range(256)])
+
+
+def codes_of(x, kind: int) -> np.ndarray:
+    """The nearest code of each value (brute force over the codes)."""
+    lib = _load()
+    x = np.asarray(x, dtype=np.float64)
+    return np.array([lib.oracle_code_of(float(v), kind) for v in x.ravel()],
+                    dtype=np.uint8).reshape(x.shape)
+
+
+def rope(x, positions, inv_freq, freq_axis=None, interleaved=False, inverse=False) -> np.ndarray:
+    """x [T, H, D] (any real type), positions int32 [T] or [axes, T] -> double."""
+    x, xp = _as(x, np.float64, ctypes.c_double)
+    pos, pp = _as(np.atleast_2d(np.asarray(positions)), np.int32, ctypes.c_int32)
+    f, fp = _as(inv_freq, np.float32, ctypes.c_float)
+    ap = None
+    if freq_axis is not None:
+        ax, ap = _as(freq_axis, np.int32, ctypes.c_int32)
+    y = np.empty_like(x)
+    T, H, D = x.shape
+    assert pos.shape[1] == T
+    _load().oracle_rope(xp, T, H, D, pp, fp, ap, 2 * f.size, int(interleaved), int(inverse),
+                        y.ctypes.data_as(ctypes.POINTER(ctypes.c_double)))
+    return y
+
+
+def append(x, req, pos, block_table, kind, cache, scales):
+    """Appends x double [T, H, D] to a cache given as the values of its codes;
+    returns (values in code units, scales, fresh [num_pages, 16])."""
+    x, xp = _as(x, np.float64, ctypes.c_double)
+    T, H, D = x.shape
+    r, rp = _as(req, np.int32, ctypes.c_int32)
+    p, pp = _as(pos, np.int32, ctypes.c_int32)
+    t, tp = _as(block_table, np.int32, ctypes.c_int32)
+    c = np.array(cache, dtype=np.float64)
+    s = np.array(scales if scales is not None else np.ones(1), dtype=np.float32)
+    fresh = np.zeros(c.shape[:2], dtype=np.uint8)
+    _load().oracle_append(xp, T, H, D, rp, pp, tp, t.shape[1], kind, c.shape[0],
+                          c.ctypes.data_as(ctypes.POINTER(ctypes.c_double)),
+                          s.ctypes.data_as(ctypes.POINTER(ctypes.c_float)),
+                          fresh.ctypes.data_as(ctypes.POINTER(ctypes.c_uint8)))
+    return c, s, fresh
+
+
+def sparse_decode_attention_q8(q, k_codes, v_codes, kind, k_scale, v_scale, sparse_bt, sparse_ctx,
+                               scale) -> np.ndarray:
+    """q bf16 [T, H, G, D] (torch tensor or bits); codes uint8 [num_pages, 16, H, D]."""
+    qb, dt = _score_bits(q)
+    assert dt == BF16
+    T, H, G, D = qb.shape
+    k, kp = _as(k_codes, np.uint8, ctypes.c_uint8)
+    v, vp = _as(v_codes, np.uint8, ctypes.c_uint8)
+    ks, ksp = _as(k_scale, np.float32, ctypes.c_float)
+    vs, vsp = _as(v_scale, np.float32, ctypes.c_float)
+    bt, btp = _as(sparse_bt, np.int32, ctypes.c_int32)
+    ctx, cp = _as(sparse_ctx, np.int32, ctypes.c_int32)
+    out = np.empty((T, H, G, D))
+    rc = _load().oracle_sparse_decode_attention_q8(
+        qb.ctypes.data_as(ctypes.POINTER(ctypes.c_uint16)), kp, vp, kind, ksp, vsp, k.shape[0], btp,
+        cp, T, H, G, D, bt.shape[2] // 8, float(scale),
+        out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)))
+    assert rc == 0
     return out

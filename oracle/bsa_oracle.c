@@ -428,3 +428,172 @@ int oracle_sparse_decode_attention(const uint16_t* q, const uint16_t* k_cache,
     free(s);
     return 0;
 }
+
+/* ------------------------------------------------------------------------ */
+/* The cache around the sparse attention: rotary positions, append, 8 bits   */
+/* ------------------------------------------------------------------------ */
+
+/* The value of an 8-bit floating-point code: kind 2 has 4 exponent and 3
+ * fraction bits (bias 7, no infinities, all ones is NaN), kind 3 has 5 and 2
+ * (bias 15, IEEE infinities and NaNs). */
+static double code_value(uint8_t c, int kind) {
+    const int fb = kind == 2 ? 3 : 2, bias = kind == 2 ? 7 : 15, top = kind == 2 ? 15 : 31;
+    const int e = (c >> fb) & top, f = c & ((1 << fb) - 1);
+    double v;
+    if (kind == 2 && e == top && f == 7) v = NAN;
+    else if (kind == 3 && e == top) v = f ? NAN : INFINITY;
+    else if (e == 0) v = ldexp((double)f, 1 - bias - fb);
+    else v = ldexp((double)((1 << fb) + f), e - bias - fb);
+    return (c & 0x80) ? -v : v;
+}
+
+double oracle_code_value(uint8_t c, int kind) { return code_value(c, kind); }
+
+/* The code nearest to x, found by trying every finite code: ties go to the
+ * even fraction, values beyond the range to its end, NaN to a NaN. */
+uint8_t oracle_code_of(double x, int kind) {
+    const uint8_t sign = signbit(x) ? 0x80 : 0;
+    if (isnan(x)) return (uint8_t)(sign | 0x7F);
+    const double a = fabs(x) < 1e6 ? fabs(x) : 1e6;   /* beyond both types' range */
+    int best = 0;
+    double off = INFINITY;
+    for (int c = 0; c < 128; ++c) {
+        const double v = code_value((uint8_t)c, kind);
+        if (!isfinite(v)) continue;
+        const double d = fabs(a - v);
+        if (d < off || (d == off && (c & 1) == 0)) {
+            best = c;
+            off = d;
+        }
+    }
+    return (uint8_t)(sign | best);
+}
+
+/* One head's row of D values, the first `rot` of them rotated: pair i turns
+ * by positions[axis[i]] * inv_freq[i] (times -1 when inverse). */
+static void rotate_row(const double* x, double* y, int64_t D, const int32_t* place,
+                       int64_t place_stride, const float* inv_freq, const int32_t* axis, int32_t rot,
+                       int interleaved, int inverse) {
+    for (int64_t d = 0; d < D; ++d) y[d] = x[d];
+    for (int32_t i = 0; i < rot / 2; ++i) {
+        const int64_t a = interleaved ? 2 * i : i;
+        const int64_t b = interleaved ? 2 * i + 1 : i + rot / 2;
+        const double angle = (double)place[(axis ? axis[i] : 0) * place_stride] * (double)inv_freq[i];
+        const double c = cos(angle), s = inverse ? -sin(angle) : sin(angle);
+        y[a] = x[a] * c - x[b] * s;
+        y[b] = x[b] * c + x[a] * s;
+    }
+}
+
+/* x: double [T, H, D] contiguous; positions int32 [axes, T]; y: double [T, H, D]. */
+int oracle_rope(const double* x, int64_t T, int64_t H, int64_t D, const int32_t* positions,
+                const float* inv_freq, const int32_t* axis, int32_t rot, int interleaved,
+                int inverse, double* y) {
+    for (int64_t t = 0; t < T; ++t)
+        for (int64_t h = 0; h < H; ++h)
+            rotate_row(x + (t * H + h) * D, y + (t * H + h) * D, D, positions + t, T, inv_freq, axis,
+                       rot, interleaved, inverse);
+    return 0;
+}
+
+/* Appends rows to one 8-bit or bf16 cache (called once with rotated keys and
+ * once with values).  x: double [T, H, D]; req, pos: int32 [T], pos < 0 for
+ * padding.  kind 0: bf16 (scales unused).  cache: double [num_pages, 16, H,
+ * D], on entry the stored codes' values, on return what the slot's code
+ * stands for before its own rounding (new tokens: value / scale) or exactly
+ * (kept and untouched ones); fresh: uint8 [num_pages, 16], 1 for new tokens. */
+int oracle_append(const double* x, int64_t T, int64_t H, int64_t D, const int32_t* req,
+                  const int32_t* pos, const int32_t* block_table, int64_t max_blocks, int kind,
+                  int64_t num_pages, double* cache, float* scales, uint8_t* fresh) {
+    const double top = kind == 2 ? 448.0 : 57344.0;
+    for (int64_t t = 0; t < T; ++t) {
+        if (pos[t] < 0 || pos[t] / ORACLE_PAGE_SIZE >= max_blocks) continue;
+        const int64_t phys = block_table[req[t] * max_blocks + pos[t] / ORACLE_PAGE_SIZE];
+        const int64_t page = phys * ORACLE_PAGES_PER_BLOCK + pos[t] % ORACLE_PAGE_SIZE / ORACLE_SUB_PAGE;
+        if (phys < 0 || page >= num_pages) continue;
+        const int first = pos[t] % ORACLE_SUB_PAGE;
+        if (first > 0 && t > 0 && req[t - 1] == req[t] && pos[t - 1] == pos[t] - 1) continue;  /* not the page's first */
+        int64_t n = 1;
+        while (first + n < ORACLE_SUB_PAGE && t + n < T && req[t + n] == req[t] && pos[t + n] == pos[t] + n) ++n;
+        for (int64_t h = 0; h < H; ++h) {
+            double s = 1.0;
+            if (kind != 0) {
+                const double old = first > 0 ? (double)scales[page * H + h] : 0.0;
+                double amax = 0.0, need = 0.0;
+                for (int64_t j = 0; j < n; ++j)
+                    for (int64_t d = 0; d < D; ++d) {
+                        const double a = fabs(x[((t + j) * H + h) * D + d]);
+                        if (a <= 3.402823466e38 && a > amax) amax = a;
+                    }
+                if (amax > 0.0) {
+                    need = ldexp(1.0, -126);
+                    while (amax / need > top) need *= 2.0;
+                }
+                s = old > need ? old : need;
+                if (!(s > 0.0)) s = 1.0;
+                for (int64_t j = 0; j < first; ++j)
+                    for (int64_t d = 0; d < D; ++d) {
+                        double* c = cache + ((page * ORACLE_SUB_PAGE + j) * H + h) * D + d;
+                        if (old != s) *c = code_value(oracle_code_of(*c * (old / s), kind), kind);
+                    }
+                scales[page * H + h] = (float)s;
+            }
+            for (int64_t j = 0; j < n; ++j) {
+                fresh[page * ORACLE_SUB_PAGE + first + j] = 1;
+                for (int64_t d = 0; d < D; ++d)
+                    cache[((page * ORACLE_SUB_PAGE + first + j) * H + h) * D + d] =
+                        x[((t + j) * H + h) * D + d] / s;
+            }
+        }
+    }
+    return 0;
+}
+
+/* oracle_sparse_decode_attention over 8-bit codes with a scale per page and
+ * head. */
+int oracle_sparse_decode_attention_q8(const uint16_t* q, const uint8_t* k_cache,
+                                      const uint8_t* v_cache, int kind, const float* k_scale,
+                                      const float* v_scale, int64_t num_pages,
+                                      const int32_t* sparse_bt, const int32_t* sparse_ctx,
+                                      int64_t T, int64_t H, int64_t G, int64_t D, int32_t K,
+                                      double scale, double* out) {
+    const int64_t width = (int64_t)K * ORACLE_PAGES_PER_BLOCK;
+    double* s = (double*)malloc(sizeof(double) * (size_t)(width * ORACLE_SUB_PAGE));
+    double lut[256];
+    if (!s) return -2;
+    for (int c = 0; c < 256; ++c) lut[c] = code_value((uint8_t)c, kind);
+    for (int64_t r = 0; r < T * H; ++r) {
+        const int64_t h = r % H;
+        const int32_t* bt = sparse_bt + r * width;
+        const int64_t cap = width * ORACLE_SUB_PAGE;
+        const int64_t ctx = sparse_ctx[r] < 0 ? 0 : (sparse_ctx[r] > cap ? cap : sparse_ctx[r]);
+        for (int64_t g = 0; g < G; ++g) {
+            double* o = out + (r * G + g) * D;
+            double mx = -INFINITY, sum = 0.0;
+            int64_t live = 0;
+            for (int64_t d = 0; d < D; ++d) o[d] = 0.0;
+            for (int64_t j = 0; j != ctx; ++j) {
+                const int64_t page = bt[j / ORACLE_SUB_PAGE];
+                if (page < 0 || page >= num_pages) continue;
+                const int64_t at = ((page * ORACLE_SUB_PAGE + j % ORACLE_SUB_PAGE) * H + h) * D;
+                double dot = 0.0;
+                for (int64_t d = 0; d < D; ++d) dot += decode_bits(q[(r * G + g) * D + d], 8, 7).value * lut[k_cache[at + d]];
+                s[j] = dot * (double)k_scale[page * H + h] * scale;
+                if (s[j] > mx) mx = s[j];
+                ++live;
+            }
+            if (live == 0) continue;
+            for (int64_t j = 0; j != ctx; ++j) {
+                const int64_t page = bt[j / ORACLE_SUB_PAGE];
+                if (page < 0 || page >= num_pages) continue;
+                const int64_t at = ((page * ORACLE_SUB_PAGE + j % ORACLE_SUB_PAGE) * H + h) * D;
+                const double p = exp(s[j] - mx);
+                sum += p;
+                for (int64_t d = 0; d < D; ++d) o[d] += p * (double)v_scale[page * H + h] * lut[v_cache[at + d]];
+            }
+            for (int64_t d = 0; d < D; ++d) o[d] /= sum;
+        }
+    }
+    free(s);
+    return 0;
+}
