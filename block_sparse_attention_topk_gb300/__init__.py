@@ -53,6 +53,7 @@ EXPORTED = [
 BSA_STATUS_BAD_BLOCK_ID = 0x1
 BSA_STATUS_BAD_PAGE = 0x2
 BSA_STATUS_BAD_CONTEXT = 0x4
+BSA_STATUS_TIMEOUT = 0x8
 MAX_ATTN_GROUP = 8
 MAX_INDEX_DIM = 1024
 MAX_INDEX_QUERIES = 16

@@ -467,10 +467,14 @@ int bsa_select_policy(int64_t rows, int64_t M, int32_t K, int32_t dtype, int32_t
  *   BSA_STATUS_BAD_CONTEXT   the sparse decode attention met a sparse_ctx
  *                            entry below 0 or above K * 128 (clamped); or the
  *                            append met a token past the block table (not
- *                            stored). */
+ *                            stored).
+ *   BSA_STATUS_TIMEOUT       a wait inside the 8-bit attention ran out and the
+ *                            call's outputs are incomplete (a defect or a
+ *                            device problem, never an input's doing). */
 #define BSA_STATUS_BAD_BLOCK_ID 0x1u
 #define BSA_STATUS_BAD_PAGE 0x2u
 #define BSA_STATUS_BAD_CONTEXT 0x4u
+#define BSA_STATUS_TIMEOUT 0x8u
 #define BSA_MAX_PHYS_BLOCK 0x0FFFFFFF  /* largest block id whose page ids fit int32 */
 
 /* Registers `word`, a DEVICE pointer to one uint32 on the current device
