@@ -18,21 +18,23 @@
 //    of the row's largest p_j vs_j, which is scaled to 256.
 // The sums, maxima and accumulators are fp32.
 //
-// The work: a CTA takes an item (a row, or a share of its 128-token blocks
-// when rows are few) and walks it in chunks of as many blocks as their scores
-// fit in 256 TMEM columns (16 blocks up to 8 query heads, 8 up to 16).  A
+// The work: a CTA takes items (a row, or a share of its 128-token blocks when
+// rows are few) and walks each in chunks of as many blocks as their scores
+// fit in 192 TMEM columns (12 blocks up to 8 query heads, 6 up to 16).  A
 // chunk's scores are complete before its probabilities are formed, so there
 // is one maximum per chunk and no correction of accumulators in TMEM.
+//  warps 0-3  thread i is token i of a block (probabilities) and dimension i
+//             of the head (output),
 //  warp 4     copies blocks by TMA into a ring of shared-memory stages: the
 //             chunk's key blocks, then its value blocks, a box per page;
 //             pages outside the context or the cache are boxes past the end
 //             of the tensor, which arrive as zeros,
 //  warp 5     issues the MMAs and frees the stages,
-//  warps 0-3  thread i is token i of a block (probabilities) and dimension i
-//             of the head (output).
-// Values behind the context's end in its last page are set to zero in shared
-// memory (they may be NaN codes); such keys only reach their own scores.
-// The kernel is bound by the copies: 2 D bytes a token.
+//  warp 6     reads the next chunk's page scales and the next item's queries.
+// Two CTAs share an SM, so that one's copies and MMAs run through the other's
+// softmax.  Values behind the context's end in its last page are set to zero
+// in shared memory (they may be NaN codes); such keys only reach their own
+// scores.  The kernel is bound by the copies: 2 D bytes a token.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -49,9 +51,11 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kSoftmaxThreads = 128;
-constexpr int kQ8Threads = kSoftmaxThreads + 64;
-constexpr int kScoreCols = 256;          // TMEM columns of a chunk's scores
-constexpr int kTmemCols = 512;
+constexpr int kQ8Threads = kSoftmaxThreads + 96;
+constexpr int kQ8Ctas = 2;               // per SM
+constexpr int kScoreCols = 192;          // TMEM columns of a chunk's scores
+constexpr int kTmemCols = 256;
+constexpr int kQ8Smem = 115712;          // half an SM's shared memory, less 1 KB a CTA
 
 template <int D, int GP>
 struct Q8Cfg {
@@ -59,13 +63,14 @@ struct Q8Cfg {
     static constexpr int NB = kScoreCols / N;         // blocks per chunk
     static constexpr int PANELS = D == 256 ? 2 : 1;   // 128-byte parts of a head's row
     static constexpr int ROWB = D / PANELS;           // bytes of a row in a panel: 64 or 128
-    static constexpr int PANEL_BYTES = 128 * ROWB;
-    static constexpr int STAGE = 128 * D;
-    static constexpr int RING = 184320 / STAGE;       // 22, 11 or 5 stages of 8, 16 or 32 KB
-    static constexpr int P_BYTES = NB * N * 128;      // 32 KB
+    static constexpr int STAGE = 128 * ROWB;          // a panel of a block: 8 or 16 KB
+    static constexpr int P_BYTES = NB * N * 128;      // 24 KB
     static constexpr int Q_PANEL = N * ROWB;
     static constexpr int Q_BYTES = PANELS * Q_PANEL;
-    static constexpr int SMEM = RING * STAGE + P_BYTES + Q_BYTES + 1024;
+    static constexpr int PAGES = NB * kPagesPerBlock;
+    static constexpr int STATIC = 2 * PAGES * 16 + 1280;   // scales, barriers and the rest
+    static constexpr int RING = (kQ8Smem - STATIC - 1024 - P_BYTES - 2 * Q_BYTES) / STAGE;
+    static constexpr int SMEM = RING * STAGE + P_BYTES + 2 * Q_BYTES + 1024;
     static constexpr uint32_t SWIZZLE = ROWB == 128 ? 2 : 4;
     static constexpr uint32_t ATOM = 8 * ROWB;        // 8 rows: the swizzle's period
 };
@@ -87,8 +92,8 @@ struct Q8Params {
 };
 
 // floats of one partial result: G x D outputs, then per head the largest
-// score, the largest weighted score and the sum
-__host__ __device__ inline int64_t part_floats(int G, int D) { return (int64_t)G * D + 3 * G; }
+// weighted score and the sum
+__host__ __device__ inline int64_t part_floats(int G, int D) { return (int64_t)G * D + 2 * G; }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -123,10 +128,12 @@ __device__ __forceinline__ float2 unpack_e4m3(uint32_t c) {
     return f;
 }
 
-// The blocks [b0, b1) of an item.
+// The blocks [b0, b1) of an item, and how it is cut into chunks of at most NB
+// blocks of even size.
 struct Item {
-    int row, split, ctx, b0, b1;
+    int row, split, ctx, b0, b1, step;
 };
+template <int NB>
 __device__ __forceinline__ Item load_item(const Q8Params& A, int i) {
     Item it;
     it.row = i / A.splits;
@@ -135,25 +142,46 @@ __device__ __forceinline__ Item load_item(const Q8Params& A, int i) {
     const int n = (it.ctx + kPageSize - 1) / kPageSize;
     it.b0 = (int)((int64_t)n * it.split / A.splits);
     it.b1 = (int)((int64_t)n * (it.split + 1) / A.splits);
+    const int len = it.b1 - it.b0;
+    const int chunks = (len + NB - 1) / NB;
+    it.step = chunks > 0 ? (len + chunks - 1) / chunks : 1;
     return it;
 }
 
+// A chunk as warp 6 hands it on.
+struct Chunk {
+    int row, ctx, c0, nb;    // nb < 0: no more
+    int item, qbuf, first, last;
+};
+
+template <int GP>
+__device__ __forceinline__ void load_cols(uint32_t addr, float (&s)[2 * GP]) {
+    if constexpr (GP == 4) tmem_ld8(addr, s);
+    else if constexpr (GP == 8) tmem_ld16(addr, s);
+    else {
+        tmem_ld16(addr, *reinterpret_cast<float(*)[16]>(s));
+        tmem_ld16(addr + 16, *reinterpret_cast<float(*)[16]>(s + 16));
+    }
+}
+
 template <int D, int GP>
-__global__ void __launch_bounds__(kQ8Threads, 1)
+__global__ void __launch_bounds__(kQ8Threads, kQ8Ctas)
 attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap) {
     using C = Q8Cfg<D, GP>;
-    constexpr int N = C::N, NB = C::NB, RING = C::RING;
+    constexpr int N = C::N, NB = C::NB, RING = C::RING, PANELS = C::PANELS;
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* psm = ring + RING * C::STAGE;     // [NB][N][128] swizzled, K-major
-    uint8_t* qsm = psm + C::P_BYTES;           // [PANELS][N][ROWB] swizzled, K-major
-    __shared__ uint64_t full[RING], empty[RING], s_full[NB], p_full[NB], q_full, o_full, drained;
+    uint8_t* qsm = psm + C::P_BYTES;           // [2][PANELS][N][ROWB] swizzled, K-major
+    // ks * scale * log2 e, log2 vs (-inf: no page), 1 / vs of the pages of two chunks
+    __shared__ float4 page_scale[2][C::PAGES];
+    __shared__ uint64_t full[RING], empty[RING], s_full[NB], p_full[NB], c_full[2], c_empty[2], o_full, drained;
+    __shared__ Chunk chunk[2];
+    __shared__ float qinv[2][GP];
+    __shared__ float red[4][GP];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up;
-    __shared__ float2 page_scale[NB * kPagesPerBlock];   // ks * scale * log2 e, log2 vs (-inf: no page)
-    __shared__ float qinv[GP];
-    __shared__ float red[4][2 * GP];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == 5) tmem_alloc(&tmem_base, kTmemCols);
@@ -166,14 +194,17 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], kSoftmaxThreads);
         }
-        mbar_init(&q_full, kSoftmaxThreads);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c_full[i], 32);
+            mbar_init(&c_empty[i], kSoftmaxThreads);
+        }
         mbar_init(&o_full, 1);
         mbar_init(&drained, 1);
         gave_up = 0;
         mbar_fence_init();
     }
     // columns of heads past G stay zero
-    for (int i = tid; i < (C::P_BYTES + C::Q_BYTES) / 16; i += kQ8Threads)
+    for (int i = tid; i < (C::P_BYTES + 2 * C::Q_BYTES) / 16; i += kQ8Threads)
         reinterpret_cast<uint4*>(psm)[i] = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     tc_fence_before();
@@ -190,19 +221,19 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
             tma_prefetch_map(&vmap);
         }
         const int outside = (int)max((int64_t)1, A.num_pages) * kSubPage;   // past the tensor's end
-        uint32_t n = 0;   // blocks copied so far: stage n % RING
+        uint32_t n = 0;   // panels copied so far: stage n % RING
         bool ok = true;
         for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item it = load_item(A, i);
+            const Item it = load_item<NB>(A, i);
             const int h = it.row % A.H;
             const int32_t* bt = A.bt + (int64_t)it.row * A.width;
             const int used = (it.ctx + kSubPage - 1) / kSubPage;      // pages of the context
-            for (int c0 = it.b0; ok && c0 < it.b1; c0 += NB) {
-                const int nb = min(NB, it.b1 - c0);
+            for (int c0 = it.b0; ok && c0 < it.b1; c0 += it.step) {
+                const int nb = min(it.step, it.b1 - c0);
                 // the chunk's page coordinates, page p of the chunk in lane p % 32
-                int z[NB * kPagesPerBlock / 32];
+                int z[(C::PAGES + 31) / 32];
 #pragma unroll
-                for (int r = 0; r < NB * kPagesPerBlock / 32; ++r) {
+                for (int r = 0; r < (C::PAGES + 31) / 32; ++r) {
                     const int p = c0 * kPagesPerBlock + r * 32 + lane;
                     int pg = -1;
                     if (p < used && r * 32 + lane < nb * kPagesPerBlock) pg = __ldg(bt + p);
@@ -214,19 +245,19 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
                     for (int b = 0; b < NB; ++b) {
                         // page b * 8 + lane % 8 sits in register b / 4 of lane b % 4 * 8 + lane % 8
                         const int zc = __shfl_sync(kFull, z[b / 4], (b & 3) * 8 + (lane & 7));
-                        if (b < nb && ok) {
-                            const uint32_t st = n % RING;
-                            ok = n < RING || mbar_wait(&empty[st], (n / RING - 1) & 1, quit);
-                            ok = __all_sync(kFull, ok);
-                            if (ok) {
+                        if (b < nb) {
+#pragma unroll
+                            for (int panel = 0; panel < PANELS; ++panel) {
+                                if (!ok) break;
+                                const uint32_t st = n % RING;
+                                ok = n < RING || mbar_wait(&empty[st], (n / RING - 1) & 1, quit);
+                                ok = __all_sync(kFull, ok);
+                                if (!ok) break;
                                 if (lane == 0) mbar_expect(&full[st], C::STAGE);
                                 __syncwarp();
-                                if (lane < kPagesPerBlock * C::PANELS) {
-                                    const int panel = lane / kPagesPerBlock;
-                                    tma_load_3d(ring + st * C::STAGE + panel * C::PANEL_BYTES +
-                                                    (lane & 7) * kSubPage * C::ROWB,
-                                                map, panel * 128, h, zc, &full[st]);
-                                }
+                                if (lane < kPagesPerBlock)
+                                    tma_load_3d(ring + st * C::STAGE + lane * kSubPage * C::ROWB, map, panel * 128, h,
+                                                zc, &full[st]);
                                 ++n;
                             }
                         }
@@ -247,53 +278,51 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
             constexpr uint32_t kSteps = C::ROWB / 32;
             const uint32_t q0 = smem_addr(qsm), p0 = smem_addr(psm), r0 = smem_addr(ring);
             const uint32_t o_cols = tmem + kScoreCols;
-            uint32_t n = 0, items_done = 0, p_phase = 0;
+            uint32_t n = 0, p_phase = 0;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-                const Item it = load_item(A, i);
-                if (it.b0 == it.b1) continue;
-                ok = mbar_wait(&q_full, items_done & 1, quit);
-                ++items_done;
-                for (int c0 = it.b0; ok && c0 < it.b1; c0 += NB) {
-                    const int nb = min(NB, it.b1 - c0);
-                    for (int b = 0; ok && b < nb; ++b, ++n) {
+            for (uint32_t c = 0; ok; ++c) {
+                ok = mbar_wait(&c_full[c & 1], (c >> 1) & 1, quit);
+                if (!ok) break;
+                const int nb = chunk[c & 1].nb;
+                if (nb < 0) break;
+                const uint32_t qb = q0 + chunk[c & 1].qbuf * C::Q_BYTES;
+                for (int b = 0; ok && b < nb; ++b) {
+#pragma unroll
+                    for (int panel = 0; panel < PANELS; ++panel, ++n) {
                         const uint32_t st = n % RING;
-                        ok = mbar_wait(&full[st], (n / RING) & 1, quit);
+                        ok = ok && mbar_wait(&full[st], (n / RING) & 1, quit);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
-                        for (int panel = 0; panel < C::PANELS; ++panel)
-#pragma unroll
-                            for (uint32_t k = 0; k < kSteps; ++k)
-                                mma_f8(tmem + b * N,
-                                       smem_desc(r0 + st * C::STAGE + panel * C::PANEL_BYTES + k * 32, 0, C::ATOM, C::SWIZZLE),
-                                       smem_desc(q0 + panel * C::Q_PANEL + k * 32, 0, C::ATOM, C::SWIZZLE), A.k_idesc,
-                                       panel + k > 0);
+                        for (uint32_t k = 0; k < kSteps; ++k)
+                            mma_f8(tmem + b * N, smem_desc(r0 + st * C::STAGE + k * 32, 0, C::ATOM, C::SWIZZLE),
+                                   smem_desc(qb + panel * C::Q_PANEL + k * 32, 0, C::ATOM, C::SWIZZLE), A.k_idesc,
+                                   panel + k > 0);
                         tc_commit(&empty[st]);
-                        tc_commit(&s_full[b]);
                     }
-                    for (int b = 0; ok && b < nb; ++b, ++n) {
+                    if (ok) tc_commit(&s_full[b]);
+                }
+                for (int b = 0; ok && b < nb; ++b) {
+                    ok = mbar_wait(&p_full[b], (p_phase >> b) & 1, quit);
+                    p_phase ^= 1u << b;
+#pragma unroll
+                    for (int panel = 0; panel < PANELS; ++panel, ++n) {
                         const uint32_t st = n % RING;
-                        ok = mbar_wait(&p_full[b], (p_phase >> b) & 1, quit) &&
-                             mbar_wait(&full[st], (n / RING) & 1, quit);
+                        ok = ok && mbar_wait(&full[st], (n / RING) & 1, quit);
                         if (!ok) break;
-                        p_phase ^= 1u << b;
                         tc_fence_after();
                         // values: 32 tokens a step; the head's dimensions run along
                         // the rows.  A 64-byte row fills 64 of the 128 MMA rows;
                         // the leading offset 0 reads it again for the others.
 #pragma unroll
-                        for (int panel = 0; panel < C::PANELS; ++panel)
-#pragma unroll
-                            for (uint32_t k = 0; k < 4; ++k)
-                                mma_f8(o_cols + panel * N,
-                                       smem_desc(r0 + st * C::STAGE + panel * C::PANEL_BYTES + k * 32 * C::ROWB, 0,
-                                                 C::ATOM, C::SWIZZLE),
-                                       smem_desc(p0 + b * N * 128 + k * 32, 0, 1024, 2), A.v_idesc, b > 0 || k > 0);
+                        for (uint32_t k = 0; k < 4; ++k)
+                            mma_f8(o_cols + panel * N,
+                                   smem_desc(r0 + st * C::STAGE + k * 32 * C::ROWB, 0, C::ATOM, C::SWIZZLE),
+                                   smem_desc(p0 + b * N * 128 + k * 32, 0, 1024, 2), A.v_idesc, b > 0 || k > 0);
                         tc_commit(&empty[st]);
                     }
-                    if (ok) tc_commit(&o_full);
                 }
+                if (ok && nb > 0) tc_commit(&o_full);
             }
             // no MMA runs on into the release of its memory
             if (!ok) {
@@ -303,150 +332,188 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
             }
         }
         __syncwarp();
-    } else {
-        // ------------------------------------------------ softmax and output
-        const uint32_t lanes = tmem + ((uint32_t)warp << 21);    // this warp's 32 TMEM lanes
-        const int chunk16 = tid >> 4;                              // byte tid's 16-byte part of a P row
-        uint32_t n = 0, s_phase = 0, chunks = 0;
-        // These warps meet in barriers, so none leaves early: after a wait
-        // that ran out they go through their loops on what there is, and
-        // write NaN.
-        for (int i = blockIdx.x; i < items; i += gridDim.x) {
-            const Item it = load_item(A, i);
+    } else if (warp == 6) {
+        // ------------------------------------------------ scales and queries
+        uint32_t c = 0;
+        int qbuf = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item it = load_item<NB>(A, i);
             const int h = it.row % A.H;
             const int32_t* bt = A.bt + (int64_t)it.row * A.width;
-            if (tid == 0 && it.split == 0)
+            if (lane == 0 && it.split == 0)
                 report_status(A.status, __ldg(A.ctx + it.row) != it.ctx, BSA_STATUS_BAD_CONTEXT);
-            float acc[C::PANELS][GP], my[GP], mt[GP], l[GP];
+            int c0 = it.b0;
+            do {
+                const int nb = min(it.step, it.b1 - c0);
+                const int buf = c & 1;
+                ok = c < 2 || mbar_wait(&c_empty[buf], ((c >> 1) - 1) & 1, quit);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
 #pragma unroll
-            for (int g = 0; g < GP; ++g) {
-#pragma unroll
-                for (int p = 0; p < C::PANELS; ++p) acc[p][g] = 0.f;
-                my[g] = mt[g] = -INFINITY;
-                l[g] = 0.f;
-            }
-            if (it.b0 < it.b1) {
-                // the queries as two e4m3 terms
-                for (int g = warp; g < A.G; g += 4) {
-                    const uint16_t* q = A.q + ((int64_t)it.row * A.G + g) * D;
-                    constexpr int QL = D / 32;         // values per lane, contiguous
-                    float x[QL], m = 0.f;
-#pragma unroll
-                    for (int k = 0; k < QL; ++k) {
-                        x[k] = __uint_as_float((uint32_t)__ldg(q + lane * QL + k) << 16);
-                        m = fmaxf(m, fabsf(x[k]));
-                    }
-                    m = max_warp(m);
-                    // scale by a power of two: the largest magnitude to [128, 256)
-                    const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
-                    const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-#pragma unroll
-                    for (int k = 0; k < QL; k += 2) {
-                        // an infinite query has no finite result: NaN
-                        const float a = (x[k] - x[k] == 0.f) ? x[k] * up : NAN;
-                        const float b = (x[k + 1] - x[k + 1] == 0.f) ? x[k + 1] * up : NAN;
-                        const uint32_t hi = pack_e4m3(a, b);
-                        const float2 f = unpack_e4m3(hi);
-                        const uint32_t lo = pack_e4m3((a - f.x) * 16.f, (b - f.y) * 16.f);
-                        const int d = lane * QL + k, panel = d / C::ROWB, dc = d % C::ROWB;
-#pragma unroll
-                        for (int term = 0; term < 2; ++term) {
-                            const int row = term * GP + g;
-                            const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
-                            uint8_t* dst = qsm + panel * C::Q_PANEL + row * C::ROWB + (((dc >> 4) ^ sw) << 4) + (dc & 15);
-                            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)(term ? lo : hi);
-                        }
-                    }
-                    if (lane == 0) qinv[g] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
-                }
-                for (int g = tid; g < GP; g += kSoftmaxThreads)
-                    if (g >= A.G) qinv[g] = 0.f;
-                fence_async_smem();
-                mbar_arrive(&q_full);
-            }
-            for (int c0 = it.b0; c0 < it.b1; c0 += NB) {
-                const int nb = min(NB, it.b1 - c0);
-                softmax_sync();                  // the last chunk's page_scale and red have been read
-                if (tid < nb * kPagesPerBlock) {
-                    const int p = c0 * kPagesPerBlock + tid;
-                    float2 sc = make_float2(0.f, -INFINITY);
-                    if (p * kSubPage < it.ctx) {
-                        const int32_t pg = __ldg(bt + p);
+                for (int r = 0; r < (C::PAGES + 31) / 32; ++r) {
+                    const int p = r * 32 + lane;
+                    if (p >= nb * kPagesPerBlock) continue;
+                    float4 sc = make_float4(0.f, -INFINITY, 0.f, 0.f);
+                    if ((c0 * kPagesPerBlock + p) * kSubPage < it.ctx) {
+                        const int32_t pg = __ldg(bt + c0 * kPagesPerBlock + p);
                         const bool good = pg >= 0 && pg < A.num_pages;
                         report_status(A.status, !good, BSA_STATUS_BAD_PAGE);
                         if (good) {
-                            sc.x = __ldg(A.ks + (int64_t)pg * A.H + h) * A.scale_log2e;
-                            sc.y = log2f(fmaxf(__ldg(A.vs + (int64_t)pg * A.H + h), 0x1p-126f));
+                            const float vs = fmaxf(__ldg(A.vs + (int64_t)pg * A.H + h), 0x1p-100f);
+                            sc = make_float4(__ldg(A.ks + (int64_t)pg * A.H + h) * A.scale_log2e, log2f(vs),
+                                             __frcp_rn(vs), 0.f);
                         }
                     }
-                    page_scale[tid] = sc;
+                    page_scale[buf][p] = sc;
                 }
-                softmax_sync();
-                float qi[GP];
+                if (c0 == it.b0 && nb > 0) {
+                    // the queries as two e4m3 terms
+                    qbuf ^= 1;
+                    uint8_t* qd = qsm + qbuf * C::Q_BYTES;
+                    constexpr int QL = D / 32;         // values per lane, contiguous
+                    const int d = lane * QL, panel = d / C::ROWB, dc = d % C::ROWB;
+#pragma unroll 4
+                    for (int g = 0; g < A.G; ++g) {
+                        const uint16_t* q = A.q + ((int64_t)it.row * A.G + g) * D + d;
+                        uint32_t w[QL / 2];
+                        if constexpr (QL == 2) w[0] = __ldg(reinterpret_cast<const unsigned*>(q));
+                        else if constexpr (QL == 4) {
+                            const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
+                            w[0] = v.x, w[1] = v.y;
+                        } else {
+                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q));
+                            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                        }
+                        float x[QL], m = 0.f;
 #pragma unroll
-                for (int g = 0; g < GP; ++g) qi[g] = qinv[g];
+                        for (int k = 0; k < QL; ++k) {
+                            x[k] = __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+                            m = fmaxf(m, fabsf(x[k]));
+                        }
+                        m = max_warp(m);
+                        // scale by a power of two: the largest magnitude to [128, 256)
+                        const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
+                        const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+                        uint32_t hi[QL / 2], lo[QL / 2];
+#pragma unroll
+                        for (int k = 0; k < QL; k += 2) {
+                            // an infinite query has no finite result: NaN
+                            const float a = (x[k] - x[k] == 0.f) ? x[k] * up : NAN;
+                            const float b = (x[k + 1] - x[k + 1] == 0.f) ? x[k + 1] * up : NAN;
+                            hi[k / 2] = pack_e4m3(a, b);
+                            const float2 f = unpack_e4m3(hi[k / 2]);
+                            lo[k / 2] = pack_e4m3((a - f.x) * 16.f, (b - f.y) * 16.f);
+                        }
+#pragma unroll
+                        for (int term = 0; term < 2; ++term) {
+                            const uint32_t* v = term ? lo : hi;
+                            const int row = term * GP + g;
+                            const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
+                            uint8_t* dst = qd + panel * C::Q_PANEL + row * C::ROWB + (((dc >> 4) ^ sw) << 4) + (dc & 15);
+                            if constexpr (QL == 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)v[0];
+                            else if constexpr (QL == 4) *reinterpret_cast<uint32_t*>(dst) = v[0] | v[1] << 16;
+                            else *reinterpret_cast<uint2*>(dst) = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+                        }
+                        if (lane == 0) qinv[qbuf][g] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+                    }
+                    if (lane >= A.G && lane < GP) qinv[qbuf][lane] = 0.f;
+                }
+                if (lane == 0)
+                    chunk[buf] = Chunk{it.row, it.ctx, c0, nb, i, qbuf, c0 == it.b0, c0 + nb == it.b1};
+                fence_async_smem();
+                mbar_arrive(&c_full[buf]);
+                ++c;
+                c0 += it.step;
+            } while (c0 < it.b1);
+        }
+        if (ok) ok = c < 2 || mbar_wait(&c_empty[c & 1], ((c >> 1) - 1) & 1, quit);
+        __syncwarp();
+        if (lane == 0) chunk[c & 1].nb = -1;
+        __syncwarp();
+        mbar_arrive(&c_full[c & 1]);
+    } else {
+        // ------------------------------------------------ softmax and output
+        const uint32_t lanes = tmem + ((uint32_t)warp << 21);    // this warp's 32 TMEM lanes
+        const int part16 = tid >> 4;                               // byte tid's 16-byte part of a P row
+        uint32_t n = 0, s_phase = 0, o_phase = 0;
+        float acc[PANELS][GP], mt[GP], l[GP];
+        // These warps meet in barriers, so none leaves alone: a wait that ran
+        // out anywhere ends at the next chunk for all, or lets the loops go on
+        // with what there is; outputs are NaN then.
+        for (uint32_t c = 0;; ++c) {
+            mbar_wait(&c_full[c & 1], (c >> 1) & 1, quit);
+            softmax_sync();                  // also: red has been read
+            const bool gone = *quit;
+            const Chunk ch = chunk[c & 1];
+            int stop = gone || ch.nb < 0;
+            // one answer for the four warps
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %0, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                         : "+r"(stop)::"memory");
+            if (stop) break;
+            const float4* scales = page_scale[c & 1];
+            const int nb = ch.nb;
+            if (ch.first) {
+#pragma unroll
+                for (int g = 0; g < GP; ++g) {
+#pragma unroll
+                    for (int p = 0; p < PANELS; ++p) acc[p][g] = 0.f;
+                    mt[g] = -INFINITY;
+                    l[g] = 0.f;
+                }
+            }
+            if (nb > 0) {
+                float qi[GP], ct[GP];
+#pragma unroll
+                for (int g = 0; g < GP; ++g) {
+                    qi[g] = qinv[ch.qbuf][g];
+                    ct[g] = -INFINITY;
+                }
                 // ---- the chunk's maxima, block by block as scores complete ----
-                float cy[GP], ct[GP];
-#pragma unroll
-                for (int g = 0; g < GP; ++g) cy[g] = ct[g] = -INFINITY;
                 for (int b = 0; b < nb; ++b) {
                     mbar_wait(&s_full[b], (s_phase >> b) & 1, quit);
                     __syncwarp();
                     tc_fence_after();
                     float s[2 * GP];
-                    if constexpr (GP == 4) tmem_ld8(lanes + b * N, s);
-                    else if constexpr (GP == 8) tmem_ld16(lanes + b * N, s);
-                    else {
-                        tmem_ld16(lanes + b * N, *reinterpret_cast<float(*)[16]>(s));
-                        tmem_ld16(lanes + b * N + 16, *reinterpret_cast<float(*)[16]>(s + 16));
-                    }
-                    const float2 sc = page_scale[b * kPagesPerBlock + (tid >> 4)];
-                    const bool live = (c0 + b) * kPageSize + tid < it.ctx && sc.y != -INFINITY;
+                    load_cols<GP>(lanes + b * N, s);
+                    const float4 sc = scales[b * kPagesPerBlock + part16];
+                    const bool live = (ch.c0 + b) * kPageSize + tid < ch.ctx && sc.y != -INFINITY;
                     if (live) {
 #pragma unroll
-                        for (int g = 0; g < GP; ++g) {
-                            const float y = fmaf(s[GP + g], 0.0625f, s[g]) * (qi[g] * sc.x);
-                            cy[g] = fmaxf(cy[g], y);
-                            ct[g] = fmaxf(ct[g], y + sc.y);
-                        }
+                        for (int g = 0; g < GP; ++g)
+                            ct[g] = fmaxf(ct[g], fmaf(fmaf(s[GP + g], 0.0625f, s[g]), qi[g] * sc.x, sc.y));
                     }
                 }
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
-                    const float a = max_warp(cy[g]), t = max_warp(ct[g]);
-                    if (lane == 0) {
-                        red[warp][2 * g] = a;
-                        red[warp][2 * g + 1] = t;
-                    }
+                    const float t = max_warp(ct[g]);
+                    if (lane == 0) red[warp][g] = t;
                 }
                 softmax_sync();
+                float keep[GP], add[GP];
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
-                    const float a = fmaxf(fmaxf(red[0][2 * g], red[1][2 * g]), fmaxf(red[2][2 * g], red[3][2 * g]));
-                    ct[g] = fmaxf(fmaxf(red[0][2 * g + 1], red[1][2 * g + 1]),
-                                  fmaxf(red[2][2 * g + 1], red[3][2 * g + 1]));
-                    const float top = fmaxf(my[g], a);
-                    l[g] *= top == -INFINITY ? 1.f : ex2(my[g] - top);
-                    my[g] = top;
+                    ct[g] = fmaxf(fmaxf(red[0][g], red[1][g]), fmaxf(red[2][g], red[3][g]));
+                    const float top = fmaxf(mt[g], ct[g]);
+                    keep[g] = top == -INFINITY ? 1.f : ex2(mt[g] - top);
+                    add[g] = top == -INFINITY ? 0.f : ex2(ct[g] - top);
+                    mt[g] = top;
+                    l[g] *= keep[g];
+                    ct[g] = 8.f - ct[g];         // probabilities in units of 2^-8 of the largest
                 }
                 // ---- the probabilities ----
                 for (int b = 0; b < nb; ++b) {
                     float s[2 * GP];
-                    if constexpr (GP == 4) tmem_ld8(lanes + b * N, s);
-                    else if constexpr (GP == 8) tmem_ld16(lanes + b * N, s);
-                    else {
-                        tmem_ld16(lanes + b * N, *reinterpret_cast<float(*)[16]>(s));
-                        tmem_ld16(lanes + b * N + 16, *reinterpret_cast<float(*)[16]>(s + 16));
-                    }
-                    const float2 sc = page_scale[b * kPagesPerBlock + (tid >> 4)];
-                    const int left = it.ctx - (c0 + b) * kPageSize;       // context tokens from this block on
+                    load_cols<GP>(lanes + b * N, s);
+                    const float4 sc = scales[b * kPagesPerBlock + part16];
+                    const int left = ch.ctx - (ch.c0 + b) * kPageSize;       // context tokens from this block on
                     const bool live = tid < left && sc.y != -INFINITY;
                     float w[GP];
 #pragma unroll
                     for (int g = 0; g < GP; ++g) {
-                        const float y = fmaf(s[GP + g], 0.0625f, s[g]) * (qi[g] * sc.x);
-                        l[g] += live ? ex2(y - my[g]) : 0.f;
-                        w[g] = live ? ex2(y + sc.y - ct[g] + 8.f) : 0.f;
+                        const float t = fmaf(fmaf(s[GP + g], 0.0625f, s[g]), qi[g] * sc.x, sc.y + ct[g]);
+                        w[g] = live ? ex2(t) : 0.f;
+                        l[g] = fmaf(w[g] * sc.z, add[g], l[g]);
                     }
                     uint8_t* pb = psm + b * N * 128 + (tid & 15);
 #pragma unroll
@@ -455,20 +522,23 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
                         const float2 f = unpack_e4m3(hi);
                         const uint32_t lo = pack_e4m3((w[g] - f.x) * 16.f, (w[g + 1] - f.y) * 16.f);
                         const int r0 = g, r1 = g + 1, r2 = GP + g, r3 = GP + g + 1;
-                        pb[r0 * 128 + ((chunk16 ^ (r0 & 7)) << 4)] = (uint8_t)hi;
-                        pb[r1 * 128 + ((chunk16 ^ (r1 & 7)) << 4)] = (uint8_t)(hi >> 8);
-                        pb[r2 * 128 + ((chunk16 ^ (r2 & 7)) << 4)] = (uint8_t)lo;
-                        pb[r3 * 128 + ((chunk16 ^ (r3 & 7)) << 4)] = (uint8_t)(lo >> 8);
+                        pb[r0 * 128 + ((part16 ^ (r0 & 7)) << 4)] = (uint8_t)hi;
+                        pb[r1 * 128 + ((part16 ^ (r1 & 7)) << 4)] = (uint8_t)(hi >> 8);
+                        pb[r2 * 128 + ((part16 ^ (r2 & 7)) << 4)] = (uint8_t)lo;
+                        pb[r3 * 128 + ((part16 ^ (r3 & 7)) << 4)] = (uint8_t)(lo >> 8);
                     }
                     if (left < kPageSize) {
                         // the last block: no value behind the context's end
-                        const uint32_t k = n + nb + b, st = k % RING;
-                        mbar_wait(&full[st], (k / RING) & 1, quit);
-                        if (tid >= left) {
 #pragma unroll
-                            for (int x = 0; x < D / 16; ++x)
-                                *reinterpret_cast<uint4*>(ring + st * C::STAGE + (x * 16 / C::ROWB) * C::PANEL_BYTES +
-                                                          tid * C::ROWB + (x * 16 % C::ROWB)) = make_uint4(0, 0, 0, 0);
+                        for (int panel = 0; panel < PANELS; ++panel) {
+                            const uint32_t k = n + (nb + b) * PANELS + panel, st = k % RING;
+                            mbar_wait(&full[st], (k / RING) & 1, quit);
+                            if (tid >= left) {
+#pragma unroll
+                                for (int x = 0; x < C::ROWB / 16; ++x)
+                                    *reinterpret_cast<uint4*>(ring + st * C::STAGE + tid * C::ROWB + x * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                            }
                         }
                         __syncwarp();
                     }
@@ -477,74 +547,57 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
                     mbar_arrive(&p_full[b]);
                 }
                 s_phase ^= (1u << nb) - 1;
-                n += 2 * nb;
+                n += 2 * nb * PANELS;
                 // ---- the chunk's outputs join the item's ----
-                mbar_wait(&o_full, chunks & 1, quit);
+                mbar_wait(&o_full, o_phase, quit);
                 __syncwarp();
-                ++chunks;
+                o_phase ^= 1;
                 tc_fence_after();
-                float keep[GP], add[GP];
 #pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    const float top = fmaxf(mt[g], ct[g]);
-                    keep[g] = top == -INFINITY ? 1.f : ex2(mt[g] - top);
-                    add[g] = top == -INFINITY ? 0.f : ex2(ct[g] - top);
-                    mt[g] = top;
-                }
-#pragma unroll
-                for (int p = 0; p < C::PANELS; ++p) {
+                for (int p = 0; p < PANELS; ++p) {
                     float s[2 * GP];
-                    const uint32_t at = lanes + kScoreCols + p * N;
-                    if constexpr (GP == 4) tmem_ld8(at, s);
-                    else if constexpr (GP == 8) tmem_ld16(at, s);
-                    else {
-                        tmem_ld16(at, *reinterpret_cast<float(*)[16]>(s));
-                        tmem_ld16(at + 16, *reinterpret_cast<float(*)[16]>(s + 16));
-                    }
+                    load_cols<GP>(lanes + kScoreCols + p * N, s);
 #pragma unroll
                     for (int g = 0; g < GP; ++g)
                         acc[p][g] = acc[p][g] * keep[g] + fmaf(s[GP + g], 0.0625f, s[g]) * add[g];
                 }
                 tc_fence_before();
             }
-            // ---- the item's result: the sums over the four warps' tokens ----
-            softmax_sync();
-#pragma unroll
-            for (int g = 0; g < GP; ++g) {
-                const float a = sum_warp(l[g]);
-                if (lane == 0) red[warp][g] = a;
-            }
-            softmax_sync();
-            if (A.part == nullptr) {
-                uint16_t* o = A.out + (int64_t)it.row * A.G * D;
+            if (ch.last) {
+                // ---- the item's result: the sums over the four warps' tokens ----
+                softmax_sync();
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
-                    if (g >= A.G) break;
-                    float sum = red[0][g] + red[1][g] + red[2][g] + red[3][g];
-                    if (*quit) sum = NAN;
-                    const float f = sum == 0.f ? 0.f : ex2(mt[g] - my[g] - 8.f) / sum;
-#pragma unroll
-                    for (int p = 0; p < C::PANELS; ++p)
-                        if (tid < C::ROWB)
-                            o[g * D + p * 128 + tid] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : acc[p][g] * f));
+                    const float a = sum_warp(l[g]);
+                    if (lane == 0) red[warp][g] = a;
                 }
-            } else {
-                float* o = A.part + (int64_t)i * part_floats(A.G, D);
+                softmax_sync();
+                const bool bad = *quit;
+                uint16_t* o16 = A.out + (int64_t)ch.row * A.G * D;
+                float* o32 = A.part + (int64_t)ch.item * part_floats(A.G, D);
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
                     if (g >= A.G) break;
+                    const float sum = bad ? NAN : red[0][g] + red[1][g] + red[2][g] + red[3][g];
+                    if (A.part == nullptr) {
+                        const float f = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-                    for (int p = 0; p < C::PANELS; ++p)
-                        if (tid < C::ROWB) o[g * D + p * 128 + tid] = acc[p][g];
-                    if (tid == 0) {
-                        o[A.G * D + g] = my[g];
-                        o[A.G * D + A.G + g] = mt[g];
-                        o[A.G * D + 2 * A.G + g] =
-                            *quit ? NAN : red[0][g] + red[1][g] + red[2][g] + red[3][g];
+                        for (int p = 0; p < PANELS; ++p)
+                            if (tid < C::ROWB)
+                                o16[g * D + p * 128 + tid] =
+                                    __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : acc[p][g] * f));
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < PANELS; ++p)
+                            if (tid < C::ROWB) o32[g * D + p * 128 + tid] = acc[p][g];
+                        if (tid == 0) {
+                            o32[A.G * D + g] = mt[g];
+                            o32[A.G * D + A.G + g] = sum;
+                        }
                     }
                 }
             }
+            mbar_arrive(&c_empty[c & 1]);
         }
     }
     tc_fence_before();
@@ -553,29 +606,39 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
     if (warp == 5) tmem_free(tmem, kTmemCols);
 }
 
-// Joins the partial results of a split row: one CTA per row.
+// Joins the partial results of a split row, head by head: a thread per
+// dimension.
 __global__ void __launch_bounds__(256)
-attention_q8_join_kernel(const float* part, uint16_t* out, int splits, int G, int D) {
+attention_q8_join_kernel(const float* __restrict__ part, uint16_t* __restrict__ out, int splits, int G, int D) {
+    extern __shared__ float weight[];          // [splits]
+    __shared__ float total[2];
     const int64_t row = blockIdx.x;
+    const int g = blockIdx.y, tid = threadIdx.x;
     const int64_t len = part_floats(G, D);
     const float* base = part + row * splits * len;
-    for (int i = threadIdx.x; i < G * D; i += 256) {
-        const int g = i / D;
-        float my = -INFINITY, mt = -INFINITY;
-        for (int s = 0; s < splits; ++s) {
-            my = fmaxf(my, base[s * len + G * D + g]);
-            mt = fmaxf(mt, base[s * len + G * D + G + g]);
+    if (tid < 32) {
+        float m = -INFINITY, sum = 0.f;
+        for (int s = tid; s < splits; s += 32) m = fmaxf(m, base[s * len + G * D + g]);
+        m = max_warp(m);
+        for (int s = tid; s < splits; s += 32) {
+            const float l = base[s * len + G * D + G + g];
+            const float w = l == 0.f ? 0.f : ex2(base[s * len + G * D + g] - m);
+            weight[s] = w;
+            sum += l * w;
         }
-        float sum = 0.f, o = 0.f;
-        for (int s = 0; s < splits; ++s) {
-            const float l = base[s * len + G * D + 2 * G + g];
-            if (l == 0.f) continue;
-            sum += l * ex2(base[s * len + G * D + g] - my);
-            o += base[s * len + i] * ex2(base[s * len + G * D + G + g] - mt);
-        }
-        out[row * G * D + i] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o * (ex2(mt - my - 8.f) / sum)));
+        sum = sum_warp(sum);
+        if (tid == 0) total[0] = sum;
     }
+    __syncthreads();
+    const float sum = total[0];
+    float o = 0.f;
+    const float* src = base + g * D + tid;
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {
+        const float w = weight[s];
+        o = fmaf(w == 0.f ? 0.f : src[s * len], w, o);
+    }
+    out[(row * G + g) * D + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o / sum));
 }
 
 // ---- host ------------------------------------------------------------------
@@ -619,7 +682,9 @@ cudaError_t launch_q8(Q8Params& A, const CUtensorMap& km, const CUtensorMap& vm,
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)A.rows * A.splits;
-    kern<<<(unsigned)(items < sms ? items : sms), kQ8Threads, C::SMEM, st>>>(A, km, vm);
+    const int64_t slots = (int64_t)sms * kQ8Ctas;
+    static_assert(C::RING >= 4 && C::SMEM + C::STATIC <= kQ8Smem, "the ring fits beside another CTA");
+    kern<<<(unsigned)(items < slots ? items : slots), kQ8Threads, C::SMEM, st>>>(A, km, vm);
     return cudaGetLastError();
 }
 
@@ -640,9 +705,10 @@ bool sizes_ok(int64_t T, int64_t H, int64_t G, int64_t D) {
 int pick_splits(int64_t rows, int64_t D, int32_t K, int sms) {
     int best = 1;
     double least = 0;
+    const int64_t slots = (int64_t)sms * kQ8Ctas;
     for (int s = 1; s <= K; ++s) {
-        const int64_t waves = (rows * s + sms - 1) / sms;
-        const double us = waves * ((K + s - 1) / s * (D / 128.0) * 0.75 + 1.5) + (s > 1 ? 3.0 + 0.02 * s : 0.0);
+        const int64_t waves = (rows * s + slots - 1) / slots;
+        const double us = waves * ((K + s - 1) / s * (D / 128.0) * 1.5 + 1.5) + (s > 1 ? 3.0 + 0.02 * s : 0.0);
         if (s == 1 || us < least) {
             best = s;
             least = us;
@@ -718,7 +784,8 @@ extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache
     else if (D == 128) e = launch_q8_g<128>(A, km, vm, e4m3, sms, st);
     else e = launch_q8_g<256>(A, km, vm, e4m3, sms, st);
     if (e == cudaSuccess && A.splits > 1) {
-        attention_q8_join_kernel<<<(unsigned)A.rows, 256, 0, st>>>(A.part, A.out, A.splits, A.G, (int)D);
+        attention_q8_join_kernel<<<dim3((unsigned)A.rows, (unsigned)A.G), (unsigned)D, A.splits * sizeof(float), st>>>(
+            A.part, A.out, A.splits, A.G, (int)D);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? BSA_OK : (int)e;
