@@ -2,9 +2,19 @@
 // bf16 or in 8 bits with a scale per page and head; the step's queries are
 // rotated in the same launch.
 //
-// One CTA per token row.  The row that is the call's first in its page (its
-// leader) takes all of the call's tokens in that page: at most 16, which
-// follow it.  So a page has one writer and its scale is one maximum.
+// One CTA takes a tile of token rows: it forms the rows' cosines and sines once
+// in shared memory, rotates the rows' query heads slot by slot (bsa_rope.cuh),
+// and appends page by page: the row that is the call's first in its page (its
+// leader) stands for all of the call's tokens in that page, at most 16, which
+// follow it, possibly into the next tile.  A warp takes such a page's keys or
+// values of one head: it holds the tokens in registers, as they came, takes the
+// maximum of the rotated values, then rotates again to round them with the
+// page's scale (rotating twice costs two products per value; holding fp32
+// values would double the registers).  So a page has one writer, and the result
+// does not depend on how the work is spread.
+// Bound by memory in long calls (the queries' read and write are the most of
+// it) and by its chain of dependent loads (length, table entry, scale) in single
+// steps.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -16,7 +26,9 @@
 namespace bsa {
 namespace {
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256;
+constexpr int kAppendTile = 16;         // rows per CTA at most
+constexpr int kPageRows = BSA_SUB_PAGE_SIZE;
 
 struct AppendParams {
     bsa_append_args_t a;
@@ -26,12 +38,8 @@ struct AppendParams {
     const int32_t* cu;         // varlen form
     const int32_t* prefix;
     uint32_t* status;
+    int32_t tile;
 };
-
-__device__ __forceinline__ float bf(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-__device__ __forceinline__ uint16_t to_bf(float f) {
-    return __bfloat16_as_ushort(__float2bfloat16_rn(f));
-}
 
 // The 8-bit types.  The power-of-two scale of a maximum m = f * 2^e, f in
 // [1, 2), is 2^(e - 8) or 2^(e - 15), one more when f > 1.75 (both types end
@@ -40,9 +48,16 @@ template <int FMT>
 struct Code {
     static constexpr int kTop = FMT == BSA_DTYPE_E4M3 ? 8 : 15;
     static constexpr __nv_fp8_interpretation_t kKind = FMT == BSA_DTYPE_E4M3 ? __NV_E4M3 : __NV_E5M2;
-    __device__ static uint8_t pack(float x) { return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, kKind); }
-    __device__ static float unpack(uint8_t c) {
-        return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, kKind)));
+    // four codes, the first in the low byte
+    __device__ static uint32_t pack(float a, float b, float c, float d) {
+        return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, kKind) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, kKind) << 16;
+    }
+    __device__ static uint32_t scaled(uint32_t c, float f) {
+        const __half2 lo = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xFFFF), kKind));
+        const __half2 hi = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), kKind));
+        const float2 x = __half22float2(lo), y = __half22float2(hi);
+        return pack(x.x * f, x.y * f, y.x * f, y.y * f);
     }
     // scale of the largest magnitude (0: none)
     __device__ static float scale(float amax) {
@@ -87,125 +102,266 @@ __device__ Row find_row(const AppendParams& P, int64_t t) {
     return r;
 }
 
-// value d of a head's row, rotated by the row's (cos, sin) table
-__device__ __forceinline__ float turned(const uint16_t* x, int d, const float2* cs,
-                                        const RopeParams& R) {
-    const int half = R.half;
-    if (d >= 2 * half) return bf(x[d]);
-    const int i = R.interleaved ? d >> 1 : (d < half ? d : d - half);
-    const int ia = R.interleaved ? 2 * i : i;
-    const int ib = R.interleaved ? 2 * i + 1 : i + half;
-    const float a = bf(x[ia]), b = bf(x[ib]);
-    const float2 c = cs[i];
-    return d == ia ? a * c.x - b * c.y : b * c.x + a * c.y;
-}
+// The call's tokens of one page.
+struct Segment {
+    int64_t page;
+    int32_t row;      // the leader, counted from the tile's first row
+    int32_t n, off;   // tokens, first slot
+};
 
-__device__ float block_max(float m, float* red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = red[0];
-#pragma unroll
-    for (int w = 1; w < kAppendThreads / 32; ++w) m = fmaxf(m, red[w]);
-    return m;
-}
-
-// n tokens of one head into page slots [off, off + n); cs null: not rotated
-template <int FMT>
-__device__ void store_page(const AppendParams& P, const uint16_t* x, int64_t ts, int n, int off,
-                           int64_t page, int h, const float2* cs, void* cache, float* scales, float* red) {
-    const int D = (int)P.a.D;
+// One page's n tokens of one head, rows x + t * ts, into slots [off, off + n).
+// SL: slots of two 8-element groups a lane holds, of the page's 16 * D / 16.
+template <int FMT, int SL, bool PAIRS>
+__device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t* __restrict__ x, int64_t ts,
+                                           const Segment& S, int h, const float* cs, bool rotate, void* cache,
+                                           float* scales) {
+    const int lane = threadIdx.x & 31;
+    const int D = (int)P.a.D, ks = D / 16, half = rotate ? P.r.half : 0;
+    const bool inter = P.r.interleaved != 0;
     const int64_t row = P.a.H * D;
-    const int64_t base = page * BSA_SUB_PAGE_SIZE * row + (int64_t)h * D;
-    auto value = [&](int i) {
-        const int t = i / D, d = i - t * D;
-        const uint16_t* xr = x + t * ts;
-        return cs != nullptr ? turned(xr, d, cs + t * P.r.half, P.r) : bf(xr[d]);
+    const int64_t base = S.page * kPageRows * row + (int64_t)h * D + S.off * row;
+    float* sp = FMT == BSA_DTYPE_BF16 ? nullptr : scales + S.page * P.a.H + h;
+    float old = 0.f;
+    if (FMT != BSA_DTYPE_BF16 && S.off > 0) old = *sp;
+    uint4 a[SL], b[SL];
+    int at[SL];                     // token << 8 | slot, or -1
+#pragma unroll
+    for (int j = 0; j < SL; ++j) {
+        const int i = j * 32 + lane;
+        const int t = i / ks, k = i - t * ks;
+        at[j] = t < S.n ? t << 8 | k : -1;
+        if (at[j] >= 0) {
+            int o0, o1;
+            slot_groups<PAIRS, 8>(k, half, o0, o1);
+            a[j] = __ldg(reinterpret_cast<const uint4*>(x + t * ts + o0));
+            b[j] = __ldg(reinterpret_cast<const uint4*>(x + t * ts + o1));
+        }
+    }
+    auto value = [&](int j, float(&fa)[8], float(&fb)[8]) {
+        widen16(a[j], fa);
+        widen16(b[j], fb);
+        const int t = at[j] >> 8;
+        slot_rotate<PAIRS>(x + t * ts, at[j] & 255, cs + t * 2 * P.r.half, half, inter, fa, fb);
     };
     if constexpr (FMT == BSA_DTYPE_BF16) {
         uint16_t* c = static_cast<uint16_t*>(cache) + base;
-        for (int i = threadIdx.x; i < n * D; i += kAppendThreads)
-            c[(off + i / D) * row + i % D] = to_bf(value(i));
+#pragma unroll
+        for (int j = 0; j < SL; ++j) {
+            if (at[j] < 0) continue;
+            float fa[8], fb[8];
+            value(j, fa, fb);
+            int o0, o1;
+            slot_groups<PAIRS, 8>(at[j] & 255, half, o0, o1);
+            uint16_t* d = c + (at[j] >> 8) * row;
+            *reinterpret_cast<uint4*>(d + o0) = narrow16(fa);
+            *reinterpret_cast<uint4*>(d + o1) = narrow16(fb);
+        }
     } else {
         using F = Code<FMT>;
         uint8_t* c = static_cast<uint8_t*>(cache) + base;
         float m = 0.f;
-        for (int i = threadIdx.x; i < n * D; i += kAppendThreads) {
-            const float a = fabsf(value(i));
-            if (a <= 3.402823466e38f) m = fmaxf(m, a);
-        }
-        m = block_max(m, red);
-        float* sp = scales + page * P.a.H + h;
-        const float old = off > 0 ? *sp : 0.f;
-        float s = fmaxf(old, F::scale(m));
-        if (!(s > 0.f)) s = 1.f;
-        if (s != old && off > 0) {
-            const float ratio = old / s;
-            for (int i = threadIdx.x; i < off * D; i += kAppendThreads) {
-                uint8_t* p = c + (i / D) * row + i % D;
-                *p = F::pack(F::unpack(*p) * ratio);
+#pragma unroll
+        for (int j = 0; j < SL; ++j) {
+            if (at[j] < 0) continue;
+            float fa[8], fb[8];
+            value(j, fa, fb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float u = fabsf(fa[e]), v = fabsf(fb[e]);
+                if (u <= 3.402823466e38f) m = fmaxf(m, u);      // finite values only
+                if (v <= 3.402823466e38f) m = fmaxf(m, v);
             }
         }
-        for (int i = threadIdx.x; i < n * D; i += kAppendThreads)
-            c[(off + i / D) * row + i % D] = F::pack(value(i) / s);
-        __syncthreads();                 // every thread has read the old scale
-        if (threadIdx.x == 0) *sp = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float s = fmaxf(old, F::scale(m));
+        if (!(s > 0.f)) s = 1.f;
+        if (s != old && S.off > 0) {
+            // the kept codes follow the page's new scale
+            const float ratio = old / s;
+            const int parts = D / 16;
+            for (int i = lane; i < S.off * parts; i += 32) {
+                const int t = i / parts;
+                uint4* p = reinterpret_cast<uint4*>(c + (int64_t)(t - S.off) * row) + (i - t * parts);
+                uint4 v = *p;
+                v.x = F::scaled(v.x, ratio);
+                v.y = F::scaled(v.y, ratio);
+                v.z = F::scaled(v.z, ratio);
+                v.w = F::scaled(v.w, ratio);
+                *p = v;
+            }
+        }
+        const float inv = 1.f / s;      // exact: s is a power of two
+#pragma unroll
+        for (int j = 0; j < SL; ++j) {
+            if (at[j] < 0) continue;
+            float fa[8], fb[8];
+            value(j, fa, fb);
+            int o0, o1;
+            slot_groups<PAIRS, 8>(at[j] & 255, half, o0, o1);
+            uint8_t* d = c + (at[j] >> 8) * row;
+            *reinterpret_cast<uint2*>(d + o0) =
+                make_uint2(F::pack(fa[0] * inv, fa[1] * inv, fa[2] * inv, fa[3] * inv),
+                           F::pack(fa[4] * inv, fa[5] * inv, fa[6] * inv, fa[7] * inv));
+            *reinterpret_cast<uint2*>(d + o1) =
+                make_uint2(F::pack(fb[0] * inv, fb[1] * inv, fb[2] * inv, fb[3] * inv),
+                           F::pack(fb[4] * inv, fb[5] * inv, fb[6] * inv, fb[7] * inv));
+        }
+        __syncwarp();                    // every lane has read the old scale
+        if (lane == 0) *sp = s;
     }
 }
 
-template <int FMT>
+template <int FMT, int SL, bool PAIRS>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams P) {
-    extern __shared__ __align__(16) float2 cs[];      // [16][half]
-    __shared__ float red[kAppendThreads / 32];
-    __shared__ Row sh;
-    const int64_t t = blockIdx.x;
-    if (threadIdx.x == 0) sh = find_row(P, t);
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ Row rows[kAppendTile];
+    __shared__ Segment segs[kAppendTile];
+    __shared__ int nseg, more;
+    const int half = P.r.half, D = (int)P.a.D, tid = threadIdx.x;
+    float* cs = reinterpret_cast<float*>(smem);      // [tile + 15][2 half]
+    unsigned long long* steps = reinterpret_cast<unsigned long long*>(cs + (P.tile + kPageRows - 1) * 2 * half);
+    const int64_t t0 = (int64_t)blockIdx.x * P.tile;
+    const int nt = (int)min((int64_t)P.tile, P.a.T - t0);
+    if (tid == 0) nseg = more = 0;
     __syncthreads();
-    const Row r = sh;
-    const int D = (int)P.a.D, half = P.r.half;
-    const int off = r.pos & 15;
-    const bool leader = r.pos >= 0 && (r.index == 0 || off == 0);
-    const int n = leader ? min(16 - off, r.left) : 1;
-    if (r.pos >= 0) {
-        for (int i = threadIdx.x; i < n * half; i += kAppendThreads) {
-            const int j = i / half, f = i - j * half;
-            const int32_t p = P.r.positions == nullptr
-                                  ? r.pos + j
-                                  : __ldg(P.r.positions + rope_axis(P.r, f) * P.a.T + t + j);
-            float2 c = rope_turn(p, rope_step(__ldg(P.r.inv_freq + f)));
-            if (P.r.inverse) c.y = -c.y;
-            cs[i] = c;
+    // warp 0: the rows' places; the others: the frequencies' steps
+    Segment seg{-1, 0, 0, 0};
+    int64_t entry = -1;                              // the leader's block-table entry
+    if (tid < nt) {
+        const Row r = find_row(P, t0 + tid);
+        rows[tid] = r;
+        const int off = r.pos & (kPageRows - 1);
+        if (r.pos >= 0 && (r.index == 0 || off == 0)) {
+            seg.row = tid;
+            seg.off = off;
+            seg.n = min(kPageRows - off, r.left);
+            const int64_t b = r.pos >> kLogPageSize;
+            report_status(P.status, b >= P.a.max_blocks, BSA_STATUS_BAD_CONTEXT);
+            if (b < P.a.max_blocks) entry = r.req * P.a.max_blocks + b;
+            if (tid + seg.n > nt) more = tid + seg.n - nt;       // the tile's last segment alone
+        }
+    } else if (tid >= 32) {
+        for (int i = tid - 32; i < half; i += kAppendThreads - 32) steps[i] = rope_step(__ldg(P.r.inv_freq + i));
+    }
+    const int32_t phys = entry >= 0 ? __ldg(P.a.block_table + entry) : -1;
+    __syncthreads();
+    if (entry >= 0) {
+        seg.page = (int64_t)phys * kPagesPerBlock + ((rows[tid].pos & (kPageSize - 1)) >> 4);
+        const bool good = phys >= 0 && seg.page < P.a.num_pages;
+        report_status(P.status, !good, BSA_STATUS_BAD_BLOCK_ID);
+        if (good) segs[atomicAdd(&nseg, 1)] = seg;
+    }
+    const int filled = nt + more;                    // table rows: the tile's and the last segment's
+    for (int i = tid; i < filled * half; i += kAppendThreads) {
+        const int t = i / half, f = i - t * half;
+        int32_t p;
+        if (P.r.positions != nullptr) {
+            p = __ldg(P.r.positions + rope_axis(P.r, f) * P.a.T + t0 + t);
+        } else {
+            p = t < nt ? rows[t].pos : rows[nt - 1].pos + (t - nt + 1);
+        }
+        const float2 c = rope_turn(p, steps[f]);
+        cs[t * 2 * half + f] = c.x;
+        cs[t * 2 * half + half + f] = P.r.inverse ? -c.y : c.y;
+    }
+    __syncthreads();
+    // ---- pages: a warp per page, head and side ----
+    const int warp = tid >> 5;
+    for (int u = warp; u < nseg * 2 * P.a.H; u += kAppendThreads / 32) {
+        const int side = u & 1, sh = u >> 1;
+        const int i = sh / (int)P.a.H, h = sh - i * (int)P.a.H;
+        const Segment S = segs[i];
+        const int64_t t = t0 + S.row;
+        const float* c = cs + S.row * 2 * half;
+        if (side == 0)
+            store_page<FMT, SL, PAIRS>(P, static_cast<const uint16_t*>(P.a.k) + t * P.a.k_token_stride + h * P.a.k_head_stride,
+                                       P.a.k_token_stride, S, h, c, true, P.a.k_cache, P.a.k_scale);
+        else
+            store_page<FMT, SL, true>(P, static_cast<const uint16_t*>(P.a.v) + t * P.a.v_token_stride + h * P.a.v_head_stride,
+                                      P.a.v_token_stride, S, h, c, false, P.a.v_cache, P.a.v_scale);
+    }
+    // ---- queries: slots of two groups ----
+    if (P.a.q == nullptr) return;
+    constexpr int B = 4;                             // slots in flight per thread
+    const int ks = D / 16, Hq = (int)P.a.Hq, total = nt * Hq * ks;
+    const uint16_t* __restrict__ q = static_cast<const uint16_t*>(P.a.q) + t0 * P.a.q_token_stride;
+    uint16_t* __restrict__ o = static_cast<uint16_t*>(P.a.q_out) + t0 * Hq * D;
+    // (row, head, slot) of this thread, advanced by the CTA's width; the
+    // pages took the first warps' time, so the count starts at the last thread
+    const int first = kAppendThreads - 1 - tid;
+    int k = first % ks, th = first / ks;
+    int h = Hq > 0 ? th % Hq : 0, t = Hq > 0 ? th / Hq : 0;
+    const int dk = kAppendThreads % ks, dth = kAppendThreads / ks;
+    const int dh = Hq > 0 ? dth % Hq : 0, dt = Hq > 0 ? dth / Hq : 0;
+    for (int i = first; i < total; i += B * kAppendThreads) {
+        uint4 a[B], b[B];
+        int kk[B], tt[B], hh[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            kk[j] = k;
+            tt[j] = t;
+            hh[j] = h;
+            if (i + j * kAppendThreads < total) {
+                const uint16_t* xr = q + t * P.a.q_token_stride + h * P.a.q_head_stride;
+                int o0, o1;
+                slot_groups<PAIRS, 8>(k, half, o0, o1);
+                a[j] = __ldg(reinterpret_cast<const uint4*>(xr + o0));
+                b[j] = __ldg(reinterpret_cast<const uint4*>(xr + o1));
+            }
+            k += dk;
+            h += dh;
+            t += dt;
+            if (k >= ks) {
+                k -= ks;
+                ++h;
+            }
+            if (h >= Hq) {
+                h -= Hq;
+                ++t;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            if (i + j * kAppendThreads >= total) break;
+            const uint16_t* xr = q + tt[j] * P.a.q_token_stride + hh[j] * P.a.q_head_stride;
+            uint16_t* orow = o + ((int64_t)tt[j] * Hq + hh[j]) * D;
+            int o0, o1;
+            slot_groups<PAIRS, 8>(kk[j], half, o0, o1);
+            if (rows[tt[j]].pos < 0) {
+                // padding: zeros, whatever the query holds
+                *reinterpret_cast<uint4*>(orow + o0) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(orow + o1) = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            float fa[8], fb[8];
+            widen16(a[j], fa);
+            widen16(b[j], fb);
+            slot_rotate<PAIRS>(xr, kk[j], cs + tt[j] * 2 * half, half, P.r.interleaved != 0, fa, fb);
+            *reinterpret_cast<uint4*>(orow + o0) = narrow16(fa);
+            *reinterpret_cast<uint4*>(orow + o1) = narrow16(fb);
         }
     }
-    __syncthreads();
-    if (P.a.q != nullptr) {
-        const uint16_t* q = static_cast<const uint16_t*>(P.a.q) + t * P.a.q_token_stride;
-        uint16_t* o = static_cast<uint16_t*>(P.a.q_out) + t * P.a.Hq * D;
-        for (int i = threadIdx.x; i < P.a.Hq * D; i += kAppendThreads) {
-            const int h = i / D, d = i - h * D;
-            o[i] = r.pos >= 0 ? to_bf(turned(q + h * P.a.q_head_stride, d, cs, P.r)) : (uint16_t)0;
-        }
+}
+
+template <int FMT, int SL>
+cudaError_t launch_pairs(const AppendParams& P, unsigned grid, size_t smem, cudaStream_t st) {
+    // pairs within a slot when half a head's rotated part is whole groups
+    const bool pairs = !P.r.interleaved && P.r.half % 8 == 0;
+    auto kern = pairs ? append_kernel<FMT, SL, true> : append_kernel<FMT, SL, false>;
+    if (smem > 48 * 1024 - 2048) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
     }
-    if (!leader) return;
-    const int64_t b = r.pos >> kLogPageSize;
-    if (b >= P.a.max_blocks) {
-        if (threadIdx.x == 0) report_status(P.status, true, BSA_STATUS_BAD_CONTEXT);
-        return;
-    }
-    const int32_t phys = __ldg(P.a.block_table + r.req * P.a.max_blocks + b);
-    const int64_t page = (int64_t)phys * kPagesPerBlock + ((r.pos & (kPageSize - 1)) >> 4);
-    if (phys < 0 || page >= P.a.num_pages) {
-        if (threadIdx.x == 0) report_status(P.status, true, BSA_STATUS_BAD_BLOCK_ID);
-        return;
-    }
-    for (int h = 0; h < P.a.H; ++h) {
-        store_page<FMT>(P, static_cast<const uint16_t*>(P.a.k) + t * P.a.k_token_stride + h * P.a.k_head_stride,
-                        P.a.k_token_stride, n, off, page, h, half > 0 ? cs : nullptr, P.a.k_cache, P.a.k_scale, red);
-        store_page<FMT>(P, static_cast<const uint16_t*>(P.a.v) + t * P.a.v_token_stride + h * P.a.v_head_stride,
-                        P.a.v_token_stride, n, off, page, h, nullptr, P.a.v_cache, P.a.v_scale, red);
-    }
+    kern<<<grid, kAppendThreads, smem, st>>>(P);
+    return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_width(const AppendParams& P, unsigned grid, size_t smem, cudaStream_t st) {
+    if (P.a.D <= 64) return launch_pairs<FMT, 2>(P, grid, smem, st);
+    if (P.a.D <= 128) return launch_pairs<FMT, 4>(P, grid, smem, st);
+    return launch_pairs<FMT, 8>(P, grid, smem, st);
 }
 
 int check_append(const bsa_append_args_t* a) {
@@ -243,12 +399,18 @@ int launch_append(AppendParams& P, cudaStream_t st) {
     P.r = RopeParams{P.a.positions, P.a.T, P.a.inv_freq, P.a.freq_axis, P.a.axes, P.a.rot_dim / 2,
                      (P.a.flags & BSA_ROPE_INTERLEAVED) != 0, (P.a.flags & BSA_ROPE_INVERSE) != 0};
     P.status = current_status_word();
-    const size_t smem = (size_t)16 * P.r.half * sizeof(float2);
-    const unsigned grid = (unsigned)P.a.T;
-    if (P.a.cache_dtype == BSA_DTYPE_BF16) append_kernel<BSA_DTYPE_BF16><<<grid, kAppendThreads, smem, st>>>(P);
-    else if (P.a.cache_dtype == BSA_DTYPE_E4M3) append_kernel<BSA_DTYPE_E4M3><<<grid, kAppendThreads, smem, st>>>(P);
-    else append_kernel<BSA_DTYPE_E5M2><<<grid, kAppendThreads, smem, st>>>(P);
-    const cudaError_t e = cudaGetLastError();
+    if (P.a.q == nullptr) P.a.Hq = 0;
+    // rows per CTA: a page's worth in long calls, fewer while SMs would idle
+    int tile = kAppendTile;
+    const int64_t want = 2 * (int64_t)device_sm_count();
+    while (tile > 1 && (P.a.T + tile - 1) / tile < want) tile /= 2;
+    P.tile = tile;
+    const size_t smem = (size_t)(tile + kPageRows - 1) * 2 * P.r.half * sizeof(float) + P.r.half * sizeof(unsigned long long);
+    const unsigned grid = (unsigned)((P.a.T + tile - 1) / tile);
+    cudaError_t e;
+    if (P.a.cache_dtype == BSA_DTYPE_BF16) e = launch_width<BSA_DTYPE_BF16>(P, grid, smem, st);
+    else if (P.a.cache_dtype == BSA_DTYPE_E4M3) e = launch_width<BSA_DTYPE_E4M3>(P, grid, smem, st);
+    else e = launch_width<BSA_DTYPE_E5M2>(P, grid, smem, st);
     return e == cudaSuccess ? BSA_OK : (int)e;
 }
 

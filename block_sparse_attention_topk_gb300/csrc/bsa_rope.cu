@@ -1,11 +1,16 @@
 // bsa_rope.cu -- rotary positions with one or several axes, forward and
 // inverse (the inverse rotation is the gradient of the forward one).
 //
-// One CTA takes a few tokens and all their heads.  The tokens' (cos, sin)
-// pairs are formed once in shared memory and serve every head; each thread
-// then loads both halves of its pairs before it stores either, so the call
-// may run in place.  The work is bound by memory: one read and one write of
-// each element.
+// One CTA takes a few tokens and all their heads.  The tokens' cosines and
+// sines are formed once in shared memory and serve every head.  The work is
+// bound by memory: one read and one write of each element.
+//  rope_slots_kernel   16-byte loads and stores, four slots of two groups in
+//                      flight per thread (rows and strides aligned to 16
+//                      bytes, D a multiple of two groups); partners within
+//                      the slot, or single loads where half a head's pairs
+//                      are no multiple of a group (not in place then: a
+//                      partner may belong to another thread),
+//  rope_kernel         pair by pair: any alignment, in place.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,7 +21,9 @@ namespace bsa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTable = 2048;    // (cos, sin) entries per CTA: 16 KB
+constexpr int kRopeTable = 4096;    // cosines or sines per CTA at most (32 KB both)
+constexpr int kRopeTile = 16;       // tokens per CTA at most
+constexpr int kRopeBatch = 4;       // slots in flight per thread
 
 struct RopeArgs {
     RopeParams r;
@@ -27,29 +34,96 @@ struct RopeArgs {
     int32_t H, D, tile;
 };
 
-__device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-__device__ __forceinline__ float widen(float f) { return f; }
 __device__ __forceinline__ void narrow(float f, float& o) { o = f; }
 __device__ __forceinline__ void narrow(float f, uint16_t& o) {
     o = __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs A) {
-    extern __shared__ __align__(16) float2 cs[];
-    unsigned long long* steps = reinterpret_cast<unsigned long long*>(cs + A.tile * A.r.half);
+// The tile's table: cs[t][0 .. half) cosines, cs[t][half .. 2 half) sines.
+__device__ __forceinline__ void rope_table(const RopeArgs& A, int64_t t0, int nt, float* cs,
+                                           unsigned long long* steps) {
     const int half = A.r.half;
-    const int64_t t0 = (int64_t)blockIdx.x * A.tile;
-    const int nt = (int)min((int64_t)A.tile, A.T - t0);
     for (int i = threadIdx.x; i < half; i += kRopeThreads) steps[i] = rope_step(__ldg(A.r.inv_freq + i));
     __syncthreads();
     for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
         const int t = i / half, f = i - t * half;
-        float2 c = rope_turn(__ldg(A.r.positions + rope_axis(A.r, f) * A.T + t0 + t), steps[f]);
-        if (A.r.inverse) c.y = -c.y;
-        cs[i] = c;
+        const float2 c = rope_turn(__ldg(A.r.positions + rope_axis(A.r, f) * A.T + t0 + t), steps[f]);
+        cs[t * 2 * half + f] = c.x;
+        cs[t * 2 * half + half + f] = A.r.inverse ? -c.y : c.y;
     }
     __syncthreads();
+}
+
+template <bool PAIRS, typename E>
+__global__ void __launch_bounds__(kRopeThreads) rope_slots_kernel(const RopeArgs A) {
+    constexpr int GE = 16 / (int)sizeof(E);
+    extern __shared__ __align__(16) unsigned char smem[];
+    float* cs = reinterpret_cast<float*>(smem);
+    const int half = A.r.half;
+    const int64_t t0 = (int64_t)blockIdx.x * A.tile;
+    const int nt = (int)min((int64_t)A.tile, A.T - t0);
+    rope_table(A, t0, nt, cs, reinterpret_cast<unsigned long long*>(cs + A.tile * 2 * half));
+    const E* x = static_cast<const E*>(A.x);
+    E* out = static_cast<E*>(A.out);
+    const int ks = A.D / (2 * GE);
+    const int total = nt * A.H * ks;
+    // (token, head, slot) of this thread, advanced by the CTA's width
+    int k = threadIdx.x % ks, th = threadIdx.x / ks;
+    int h = th % A.H, t = th / A.H;
+    const int dk = kRopeThreads % ks, dth = kRopeThreads / ks;
+    const int dh = dth % A.H, dt = dth / A.H;
+    for (int i = threadIdx.x; i < total; i += kRopeBatch * kRopeThreads) {
+        uint4 a[kRopeBatch], b[kRopeBatch];
+        int kk[kRopeBatch], tt[kRopeBatch], hh[kRopeBatch];
+#pragma unroll
+        for (int j = 0; j < kRopeBatch; ++j) {
+            kk[j] = k;
+            tt[j] = t;
+            hh[j] = h;
+            if (i + j * kRopeThreads < total) {
+                const E* xr = x + (t0 + t) * A.xts + h * A.xhs;
+                int o0, o1;
+                slot_groups<PAIRS, GE>(k, half, o0, o1);
+                a[j] = *reinterpret_cast<const uint4*>(xr + o0);
+                b[j] = *reinterpret_cast<const uint4*>(xr + o1);
+            }
+            k += dk;
+            h += dh;
+            t += dt;
+            if (k >= ks) {
+                k -= ks;
+                ++h;
+            }
+            if (h >= A.H) {
+                h -= A.H;
+                ++t;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kRopeBatch; ++j) {
+            if (i + j * kRopeThreads >= total) break;
+            const E* xr = x + (t0 + tt[j]) * A.xts + hh[j] * A.xhs;
+            E* orow = out + (t0 + tt[j]) * A.ots + hh[j] * A.ohs;
+            float fa[GE], fb[GE];
+            widen16(a[j], fa);
+            widen16(b[j], fb);
+            slot_rotate<PAIRS>(xr, kk[j], cs + tt[j] * 2 * half, half, A.r.interleaved != 0, fa, fb);
+            int o0, o1;
+            slot_groups<PAIRS, GE>(kk[j], half, o0, o1);
+            *reinterpret_cast<uint4*>(orow + o0) = narrow16(fa);
+            *reinterpret_cast<uint4*>(orow + o1) = narrow16(fb);
+        }
+    }
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs A) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    float* cs = reinterpret_cast<float*>(smem);
+    const int half = A.r.half;
+    const int64_t t0 = (int64_t)blockIdx.x * A.tile;
+    const int nt = (int)min((int64_t)A.tile, A.T - t0);
+    rope_table(A, t0, nt, cs, reinterpret_cast<unsigned long long*>(cs + A.tile * 2 * half));
     const int units = A.D - half;      // pairs, then values that pass through
     const E* x = static_cast<const E*>(A.x);
     E* out = static_cast<E*>(A.out);
@@ -62,9 +136,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs A) {
             const int ia = A.r.interleaved ? 2 * u : u;
             const int ib = A.r.interleaved ? 2 * u + 1 : u + half;
             const float a = widen(xr[ia]), b = widen(xr[ib]);
-            const float2 c = cs[t * half + u];
-            narrow(a * c.x - b * c.y, orow[ia]);
-            narrow(b * c.x + a * c.y, orow[ib]);
+            const float c = cs[t * 2 * half + u], s = cs[t * 2 * half + half + u];
+            narrow(turn_first(a, b, c, s), orow[ia]);
+            narrow(turn_second(a, b, c, s), orow[ib]);
         } else {
             orow[u + half] = xr[u + half];
         }
@@ -79,6 +153,23 @@ bool rows_apart(int64_t T, int64_t H, int64_t D, int64_t ts, int64_t hs) {
     if (H <= 1) return ts >= D;
     if (ts >= hs) return hs >= D && ts >= (H - 1) * hs + D;
     return ts >= D && hs >= (T - 1) * ts + D;
+}
+
+template <typename E>
+void launch_rope(const RopeArgs& A, cudaStream_t st) {
+    constexpr int GE = 16 / (int)sizeof(E);
+    const int half = A.r.half;
+    const size_t smem = (size_t)A.tile * 2 * half * sizeof(float) + half * sizeof(unsigned long long);
+    const unsigned grid = (unsigned)((A.T + A.tile - 1) / A.tile);
+    const bool wide = A.D % (2 * GE) == 0 &&
+                      ((A.xts | A.xhs | A.ots | A.ohs) % GE) == 0 &&
+                      ((reinterpret_cast<uintptr_t>(A.x) | reinterpret_cast<uintptr_t>(A.out)) & 15) == 0;
+    if (wide && !A.r.interleaved && half % GE == 0)
+        rope_slots_kernel<true, E><<<grid, kRopeThreads, smem, st>>>(A);
+    else if (wide && (A.r.interleaved || A.x != A.out))
+        rope_slots_kernel<false, E><<<grid, kRopeThreads, smem, st>>>(A);
+    else
+        rope_kernel<E><<<grid, kRopeThreads, smem, st>>>(A);
 }
 
 }  // namespace
@@ -110,21 +201,23 @@ extern "C" int bsa_rope(const void* x, int32_t dtype, int64_t T, int64_t H, int6
                      (flags & BSA_ROPE_INTERLEAVED) != 0, (flags & BSA_ROPE_INVERSE) != 0};
     A.x = x;
     A.out = out;
-    A.xts = token_stride;
-    A.xhs = head_stride;
-    A.ots = out_token_stride;
-    A.ohs = out_head_stride;
+    // strides of dimensions of one entry never matter
+    A.xts = T > 1 ? token_stride : 0;
+    A.xhs = H > 1 ? head_stride : 0;
+    A.ots = T > 1 ? out_token_stride : 0;
+    A.ohs = H > 1 ? out_head_stride : 0;
     A.T = T;
     A.H = (int32_t)H;
     A.D = (int32_t)D;
-    int tile = rot_dim > 0 ? kRopeTable / (rot_dim / 2) : 16;
-    if (tile > 16) tile = 16;
+    // tokens per CTA: as many as share a table, fewer while SMs would idle
+    int tile = rot_dim > 0 ? kRopeTable / (rot_dim / 2) : kRopeTile;
+    if (tile > kRopeTile) tile = kRopeTile;
+    const int64_t want = 4 * (int64_t)device_sm_count();
+    while (tile > 1 && (T + tile - 1) / tile < want) tile /= 2;
     A.tile = tile;
-    const size_t smem = (size_t)tile * A.r.half * sizeof(float2) + A.r.half * sizeof(unsigned long long);
-    const unsigned grid = (unsigned)((T + tile - 1) / tile);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == BSA_DTYPE_BF16) rope_kernel<uint16_t><<<grid, kRopeThreads, smem, st>>>(A);
-    else rope_kernel<float><<<grid, kRopeThreads, smem, st>>>(A);
+    if (dtype == BSA_DTYPE_BF16) launch_rope<uint16_t>(A, st);
+    else launch_rope<float>(A, st);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? BSA_OK : (int)e;
 }

@@ -44,6 +44,112 @@ __device__ __forceinline__ int rope_axis(const RopeParams& R, int i) {
     if (R.freq_axis == nullptr) return 0;
     return min(max(__ldg(R.freq_axis + i), 0), R.axes - 1);
 }
+
+// ---- 16-byte groups ----------------------------------------------------------
+// The kernels move heads as slots of two 16-byte groups of GE elements.  With
+// pairs (i, i + half) and half a multiple of GE, a slot's two groups are the two
+// sides of GE pairs (PAIRS); otherwise they are neighbours.
+__device__ __forceinline__ void widen16(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void widen16(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ uint4 narrow16(const float (&f)[8]) {
+    return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+}
+__device__ __forceinline__ uint4 narrow16(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float widen(float f) { return f; }
+
+// The two sides of a pair after the turn, rounded the same way in every kernel
+// (left to the compiler, the contraction of the products differs between them).
+__device__ __forceinline__ float turn_first(float a, float b, float c, float s) {
+    return fmaf(a, c, -__fmul_rn(b, s));
+}
+__device__ __forceinline__ float turn_second(float a, float b, float c, float s) {
+    return fmaf(b, c, __fmul_rn(a, s));
+}
+
+// element offsets of slot k's two groups
+template <bool PAIRS, int GE>
+__device__ __forceinline__ void slot_groups(int k, int half, int& o0, int& o1) {
+    if (PAIRS && GE * k < half) {
+        o0 = GE * k;
+        o1 = o0 + half;
+    } else {
+        o0 = 2 * GE * k;                      // PAIRS: half / GE slots cover 2 half elements
+        o1 = o0 + GE;
+    }
+}
+
+// Rotates slot k of a head's row at `x` (its groups' values in a and b; x is
+// read again only for partners outside the slot).  cs: the row's cosines, then
+// its sines at cs + half.
+template <bool PAIRS, typename E, int GE>
+__device__ __forceinline__ void slot_rotate(const E* x, int k, const float* cs, int half, bool interleaved,
+                                            float (&a)[GE], float (&b)[GE]) {
+    const float* sn = cs + half;
+    if constexpr (PAIRS) {
+        if (GE * k >= half) return;
+#pragma unroll
+        for (int i = 0; i < GE; i += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(cs + GE * k + i);
+            const float4 s = *reinterpret_cast<const float4*>(sn + GE * k + i);
+            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float u = a[i + j], v = b[i + j];
+                a[i + j] = turn_first(u, v, cc[j], ss[j]);
+                b[i + j] = turn_second(u, v, cc[j], ss[j]);
+            }
+        }
+    } else if (interleaved) {
+        const int d0 = 2 * GE * k;
+#pragma unroll
+        for (int i = 0; i < GE; i += 2) {
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                float* f = side ? b : a;
+                const int p = (d0 + side * GE + i) >> 1;
+                if (p < half) {
+                    const float c = cs[p], s = sn[p];
+                    const float u = f[i], v = f[i + 1];
+                    f[i] = turn_first(u, v, c, s);
+                    f[i + 1] = turn_second(u, v, c, s);
+                }
+            }
+        }
+    } else {
+        const int d0 = 2 * GE * k;
+#pragma unroll
+        for (int i = 0; i < 2 * GE; ++i) {
+            const int d = d0 + i;
+            if (d < 2 * half) {
+                float& f = i < GE ? a[i] : b[i - GE];
+                const bool first = d < half;
+                const int p = first ? d : d - half;
+                const float c = cs[p], s = sn[p];
+                const float o = widen(x[first ? d + half : p]);
+                f = first ? turn_first(f, o, c, s) : turn_second(o, f, c, s);
+            }
+        }
+    }
+}
 #endif
 
 // Checks shared by the entry points: BSA_OK or an error code.
