@@ -107,6 +107,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """The loaded CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lib_lock:
         if _lib is None:
             path = _build.LIB_PATH
@@ -153,7 +155,7 @@ def lib() -> ctypes.CDLL:
                 if not name.endswith("_workspace_bytes"):
                     getattr(L, name).restype = ctypes.c_int
             _lib = L
-    return _lib
+        return _lib
 
 
 def _check(fn: str, status: int):
@@ -171,8 +173,10 @@ def _call(fn: str, device: torch.device, *args):
         _check(fn, getattr(lib(), fn)(*args))
 
 
-def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device: torch.device) -> int:
+    """The device's current stream as a cudaStream_t."""
+    index = torch.cuda.current_device() if device.index is None else device.index
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ptr(t: torch.Tensor | None):
@@ -188,7 +192,7 @@ def _dev_i32(t: torch.Tensor, name: str, device: torch.device | None = None,
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t
 
@@ -229,7 +233,7 @@ _ws_lock = threading.Lock()
 def _workspace(device: torch.device, nbytes: int) -> torch.Tensor | None:
     if nbytes == 0:
         return None
-    key = (device.type, device.index, torch.cuda.current_stream(device).cuda_stream)
+    key = (device.type, device.index, _stream(device))
     with _ws_lock:
         ws = _ws_cache.get(key)
         if ws is None or ws.numel() < nbytes:
@@ -558,15 +562,16 @@ _CACHE_DTYPES = {torch.bfloat16: BSA_DTYPE_BF16, torch.float8_e4m3fn: BSA_DTYPE_
 def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, T: int | None,
            D: int | None):
     """A [T, heads, D] CUDA tensor whose head rows are contiguous; any token
-    and head strides."""
+    and head strides, which are returned."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or t.dtype != dtype \
             or t.device != device:
         raise ValueError(f"{name} must be a {dtype} tensor [T, heads, D] on {device}")
-    if (T is not None and t.shape[0] != T) or (D is not None and t.shape[2] != D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{T}, heads, {D}]")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    shape, stride = t.shape, t.stride()
+    if (T is not None and shape[0] != T) or (D is not None and shape[2] != D):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{T}, heads, {D}]")
+    if shape[2] > 1 and stride[2] != 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
-    return t.stride(0), t.stride(1)
+    return stride[0], stride[1]
 
 
 def _rope_args(T: int, device: torch.device, positions: torch.Tensor | None,
@@ -621,33 +626,30 @@ def bsa_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     return out
 
 
-def _cache(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype,
-           shape: tuple) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype \
-            or not t.is_contiguous() or t.dim() != len(shape) + 1 or tuple(t.shape[1:]) != shape:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor [num_pages, "
-                         f"{', '.join(map(str, shape))}] on {device}")
-    return t
+def _whole(t, dtype: torch.dtype, device: torch.device, shape: tuple) -> bool:
+    """Whether t is a contiguous tensor of this type, place and shape."""
+    return isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype \
+        and t.device == device and t.is_contiguous()
 
 
 def _q8_caches(k_cache, v_cache, k_scale, v_scale, device, H, D):
     """(cache dtype code, num_pages) of a checked pair of caches and scales."""
-    code = _CACHE_DTYPES.get(getattr(k_cache, "dtype", None))
+    dtype = getattr(k_cache, "dtype", None)
+    code = _CACHE_DTYPES.get(dtype)
     if code is None:
         raise ValueError("k_cache must be bfloat16, float8_e4m3fn or float8_e5m2")
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _cache(c, name, device, k_cache.dtype, (PAGES_PER_SPARSE_BLOCK * 2, H, D))
-    n = k_cache.shape[0]
-    if v_cache.shape[0] != n:
-        raise ValueError("k_cache and v_cache hold different page counts")
-    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if code == BSA_DTYPE_BF16:
-            if s is not None:
-                raise ValueError(f"{name} must be None with a bfloat16 cache")
-        else:
-            _cache(s, name, device, torch.float32, (H,))
-            if s.shape[0] != n:
-                raise ValueError(f"{name} has {s.shape[0]} pages, expected {n}")
+    n = k_cache.shape[0] if k_cache.dim() == 4 else -1
+    shape = (n, PAGES_PER_SPARSE_BLOCK * 2, H, D)
+    if not _whole(k_cache, dtype, device, shape) or not _whole(v_cache, dtype, device, shape):
+        raise ValueError(f"k_cache and v_cache must be contiguous {dtype} tensors [num_pages, "
+                         f"{shape[1]}, {H}, {D}] on {device} with one page count")
+    if code == BSA_DTYPE_BF16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale must be None with a bfloat16 cache")
+    elif not _whole(k_scale, torch.float32, device, (n, H)) \
+            or not _whole(v_scale, torch.float32, device, (n, H)):
+        raise ValueError(f"k_scale and v_scale must be contiguous fp32 tensors [{n}, {H}] on "
+                         f"{device}")
     return code, n
 
 
@@ -667,9 +669,7 @@ def _append(k, v, k_cache, v_cache, block_table, num_reqs, q, inv_freq, position
         Hq = q.shape[1]
         if q_out is None:
             q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        if not isinstance(q_out, torch.Tensor) or q_out.dtype != torch.bfloat16 \
-                or q_out.device != dev or tuple(q_out.shape) != (T, Hq, D) \
-                or not q_out.is_contiguous():
+        if not _whole(q_out, torch.bfloat16, dev, (T, Hq, D)):
             raise ValueError(f"q_out must be a contiguous bf16 tensor [{T}, {Hq}, {D}] on {dev}")
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -773,14 +773,14 @@ def bsa_sparse_decode_attention_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     if code == BSA_DTYPE_BF16:
         raise ValueError("the caches must be float8_e4m3fn or float8_e5m2")
     _dev_i32(sparse_bt, "sparse_bt", dev)
-    if sparse_bt.dim() != 3 or tuple(sparse_bt.shape[:2]) != (T, H) or sparse_bt.shape[2] % 8:
+    width = sparse_bt.shape[2] if sparse_bt.dim() == 3 else 1
+    if width % PAGES_PER_SPARSE_BLOCK or sparse_bt.shape != (T, H, width):
         raise ValueError(f"sparse_bt must be [{T}, {H}, K*8]")
-    K = sparse_bt.shape[2] // PAGES_PER_SPARSE_BLOCK
+    K = width // PAGES_PER_SPARSE_BLOCK
     _dev_i32(sparse_ctx, "sparse_ctx", dev, (T, H))
     if out is None:
         out = torch.empty((T, H, G, D), dtype=torch.bfloat16, device=dev)
-    if out.dtype != torch.bfloat16 or out.device != dev or not out.is_contiguous() \
-            or tuple(out.shape) != (T, H, G, D):
+    elif not _whole(out, torch.bfloat16, dev, (T, H, G, D)):
         raise ValueError(f"out must be a contiguous bf16 tensor [{T}, {H}, {G}, {D}] on {dev}")
     need = bsa_attention_q8_workspace_bytes(T, H, G, D, K, dev)
     workspace, wbytes = _workspace_arg(workspace, dev, need)

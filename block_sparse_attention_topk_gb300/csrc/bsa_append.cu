@@ -349,10 +349,6 @@ cudaError_t launch_pairs(const AppendParams& P, unsigned grid, size_t smem, cuda
     // pairs within a slot when half a head's rotated part is whole groups
     const bool pairs = !P.r.interleaved && P.r.half % 8 == 0;
     auto kern = pairs ? append_kernel<FMT, SL, true> : append_kernel<FMT, SL, false>;
-    if (smem > 48 * 1024 - 2048) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
     kern<<<grid, kAppendThreads, smem, st>>>(P);
     return cudaGetLastError();
 }

@@ -19,22 +19,28 @@
 // The sums, maxima and accumulators are fp32.
 //
 // The work: a CTA takes items (a row, or a share of its 128-token blocks when
-// rows are few) and walks each in chunks of as many blocks as their scores
-// fit in 192 TMEM columns (12 blocks up to 8 query heads, 6 up to 16).  A
-// chunk's scores are complete before its probabilities are formed, so there
-// is one maximum per chunk and no correction of accumulators in TMEM.
-//  warps 0-3  thread i is token i of a block (probabilities) and dimension i
-//             of the head (output),
-//  warp 4     copies blocks by TMA into a ring of shared-memory stages: the
-//             chunk's key blocks, then its value blocks, a box per page;
-//             pages outside the context or the cache are boxes past the end
-//             of the tensor, which arrive as zeros,
-//  warp 5     issues the MMAs and frees the stages,
-//  warp 6     reads the next chunk's page scales and the next item's queries.
-// Two CTAs share an SM, so that one's copies and MMAs run through the other's
-// softmax.  Values behind the context's end in its last page are set to zero
-// in shared memory (they may be NaN codes); such keys only reach their own
-// scores.  The kernel is bound by the copies: 2 D bytes a token.
+// rows are few) and walks each in chunks of up to 6 blocks.  A chunk's scores are
+// complete in TMEM before its probabilities are formed, so there is one maximum
+// per chunk and the accumulators in TMEM start anew with each chunk.
+//  softmax    thread i of a group of four warps is token i of a block
+//             (probabilities) and dimension i of the head (output); a second
+//             group takes query heads 8 to 15,
+//  copies     one warp copies blocks by TMA into a ring of shared-memory stages:
+//             the next chunk's key blocks, then this chunk's value blocks.  A
+//             block whose eight pages follow one another in the cache, as the
+//             selector's table has them, is one box; other blocks, and the
+//             context's last, are a box per page (issuing eight boxes a block
+//             throughout took longer than their bytes), with pages outside the
+//             context or the cache as boxes past the end of the tensor, which
+//             arrive as zeros,
+//  MMAs       one warp issues the next chunk's scores, then this chunk's
+//             output, and frees the stages: the scores of one chunk are formed
+//             under the softmax of the one before (two score buffers),
+//  ahead      one warp reads later chunks' page scales and later items' queries.
+// Up to 8 query heads two CTAs share an SM.  Values behind the context's end in
+// its last page are set to zero in shared memory (they may be NaN codes); such
+// keys only reach their own scores.  The kernel is bound by the copies, 2 D
+// bytes a token.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -50,29 +56,35 @@ namespace bsa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kSoftmaxThreads = 128;
-constexpr int kQ8Threads = kSoftmaxThreads + 96;
-constexpr int kQ8Ctas = 2;               // per SM
-constexpr int kScoreCols = 192;          // TMEM columns of a chunk's scores
-constexpr int kTmemCols = 256;
-constexpr int kQ8Smem = 115712;          // half an SM's shared memory, less 1 KB a CTA
+constexpr int kDepth = 4;                // chunks announced ahead
+constexpr int kSmSmem = 233472;          // an SM's shared memory; 1 KB of it goes to each CTA
 
 template <int D, int GP>
 struct Q8Cfg {
+    static constexpr int HG = GP < 8 ? GP : 8;        // heads a softmax group takes
+    static constexpr int GROUPS = GP / HG;
+    static constexpr int CTAS = GROUPS == 1 ? 2 : 1;  // per SM
+    static constexpr int SOFTMAX = 128 * GROUPS;
+    static constexpr int THREADS = SOFTMAX + 96;
     static constexpr int N = GP <= 8 ? 16 : 32;       // MMA columns: two terms of each head
-    static constexpr int NB = kScoreCols / N;         // blocks per chunk
+    static constexpr int NB = 6;                      // blocks per chunk
+    static constexpr int S_COLS = NB * N;             // TMEM columns of a chunk's scores
+    static constexpr int TMEM = 512 / CTAS;
     static constexpr int PANELS = D == 256 ? 2 : 1;   // 128-byte parts of a head's row
     static constexpr int ROWB = D / PANELS;           // bytes of a row in a panel: 64 or 128
     static constexpr int STAGE = 128 * ROWB;          // a panel of a block: 8 or 16 KB
-    static constexpr int P_BYTES = NB * N * 128;      // 24 KB
+    static constexpr int P_BYTES = NB * N * 128;
     static constexpr int Q_PANEL = N * ROWB;
     static constexpr int Q_BYTES = PANELS * Q_PANEL;
     static constexpr int PAGES = NB * kPagesPerBlock;
-    static constexpr int STATIC = 2 * PAGES * 16 + 1280;   // scales, barriers and the rest
-    static constexpr int RING = (kQ8Smem - STATIC - 1024 - P_BYTES - 2 * Q_BYTES) / STAGE;
-    static constexpr int SMEM = RING * STAGE + P_BYTES + 2 * Q_BYTES + 1024;
+    static constexpr int STATIC = kDepth * (PAGES + 4) * 16 + 1664;   // scales, barriers and the rest
+    static constexpr int FIXED = P_BYTES + kDepth * Q_BYTES + 1024;
+    static constexpr int RING = (kSmSmem / CTAS - 1024 - STATIC - FIXED) / STAGE;
+    static constexpr int SMEM = RING * STAGE + FIXED;
     static constexpr uint32_t SWIZZLE = ROWB == 128 ? 2 : 4;
     static constexpr uint32_t ATOM = 8 * ROWB;        // 8 rows: the swizzle's period
+    static_assert(2 * S_COLS + PANELS * N <= TMEM, "two score buffers and the outputs fit");
+    static_assert(RING >= 4, "the ring holds two blocks of the widest heads");
 };
 
 struct Q8Params {
@@ -89,6 +101,11 @@ struct Q8Params {
     uint32_t k_idesc, v_idesc;
     float scale_log2e;
     uint32_t* status;
+};
+
+// The caches as tensors read in boxes of one page and of one block of a head.
+struct Q8Maps {
+    CUtensorMap k_page, v_page, k_block, v_block;
 };
 
 // floats of one partial result: G x D outputs, then per head the largest
@@ -110,7 +127,19 @@ __device__ __forceinline__ float sum_warp(float x) {
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
     return x;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// barrier 1 + group of a softmax group's 128 threads
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
+__device__ __forceinline__ bool group_any(int group, bool x) {
+    int r = x;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %0, 0;\n\tbar.red.popc.u32 %0, %1, 128, p;\n\t}"
+        : "+r"(r)
+        : "r"(1 + group)
+        : "memory");
+    return r != 0;
+}
 
 // two values as e4m3 codes: a in the low byte
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
@@ -134,11 +163,11 @@ struct Item {
     int row, split, ctx, b0, b1, step;
 };
 template <int NB>
-__device__ __forceinline__ Item load_item(const Q8Params& A, int i) {
+__device__ __forceinline__ Item make_item(const Q8Params& A, int i, int ctx) {
     Item it;
     it.row = i / A.splits;
     it.split = i - it.row * A.splits;
-    it.ctx = max(0, min(__ldg(A.ctx + it.row), A.width * kSubPage));
+    it.ctx = max(0, min(ctx, A.width * kSubPage));
     const int n = (it.ctx + kPageSize - 1) / kPageSize;
     it.b0 = (int)((int64_t)n * it.split / A.splits);
     it.b1 = (int)((int64_t)n * (it.split + 1) / A.splits);
@@ -148,181 +177,276 @@ __device__ __forceinline__ Item load_item(const Q8Params& A, int i) {
     return it;
 }
 
-// A chunk as warp 6 hands it on.
-struct Chunk {
-    int row, ctx, c0, nb;    // nb < 0: no more
-    int item, qbuf, first, last;
+// The chunks of a CTA's items in order, each item's context length read one
+// item ahead and each chunk's page ids one chunk ahead (page p of the chunk in
+// register p / 32 of lane p % 32; INT32_MIN outside the context).
+template <int NB>
+struct Walk {
+    static constexpr int R = (NB * kPagesPerBlock + 31) / 32;
+    int i, items, c0, ctx_next, ctx_raw;
+    Item it;
+    int32_t page[R];
+
+    __device__ __forceinline__ bool done() const { return i >= items; }
+    __device__ __forceinline__ int blocks() const { return min(it.step, it.b1 - c0); }
+    __device__ __forceinline__ void enter(const Q8Params& A) {
+        ctx_raw = ctx_next;
+        it = make_item<NB>(A, i, ctx_raw);
+        c0 = it.b0;
+        const int next = i + (int)gridDim.x;
+        if (next < items) ctx_next = __ldg(A.ctx + next / A.splits);
+    }
+    __device__ __forceinline__ void read(const Q8Params& A) {
+        const int lane = threadIdx.x & 31;
+        const int32_t* bt = A.bt + (int64_t)it.row * A.width + c0 * kPagesPerBlock;
+        const int n = min(blocks() * kPagesPerBlock, (it.ctx + kSubPage - 1) / kSubPage - c0 * kPagesPerBlock);
+#pragma unroll
+        for (int r = 0; r < R; ++r) page[r] = r * 32 + lane < n ? max(__ldg(bt + r * 32 + lane), -1) : INT32_MIN;
+    }
+    __device__ __forceinline__ void begin(const Q8Params& A) {
+        items = A.rows * A.splits;
+        i = blockIdx.x;
+        if (done()) return;
+        ctx_next = __ldg(A.ctx + i / A.splits);
+        enter(A);
+        read(A);
+    }
+    __device__ __forceinline__ void advance(const Q8Params& A) {
+        c0 += it.step;
+        if (c0 >= it.b1) {
+            i += gridDim.x;
+            if (done()) return;
+            enter(A);
+        }
+        read(A);
+    }
 };
 
-template <int GP>
-__device__ __forceinline__ void load_cols(uint32_t addr, float (&s)[2 * GP]) {
-    if constexpr (GP == 4) tmem_ld8(addr, s);
-    else if constexpr (GP == 8) tmem_ld16(addr, s);
-    else {
-        tmem_ld16(addr, *reinterpret_cast<float(*)[16]>(s));
-        tmem_ld16(addr + 16, *reinterpret_cast<float(*)[16]>(s + 16));
-    }
+// A chunk as it is announced to the other warps.
+struct Chunk {
+    int row, ctx, c0, nb;    // nb < 0: no more
+    int item, qbuf, last;
+};
+
+// two terms of HG heads: columns [0, HG) and [GP, GP + HG) at addr
+template <int HG, int GP>
+__device__ __forceinline__ void load_terms(uint32_t addr, float (&s)[2 * HG]) {
+    if constexpr (HG == GP && GP == 4) tmem_ld8(addr, s);
+    else if constexpr (HG == GP) tmem_ld16(addr, s);
+    else tmem_ld8x2(addr, addr + GP, s);
 }
 
 template <int D, int GP>
-__global__ void __launch_bounds__(kQ8Threads, kQ8Ctas)
-attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap vmap) {
+__global__ void __launch_bounds__(Q8Cfg<D, GP>::THREADS, Q8Cfg<D, GP>::CTAS)
+attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
     using C = Q8Cfg<D, GP>;
-    constexpr int N = C::N, NB = C::NB, RING = C::RING, PANELS = C::PANELS;
+    constexpr int N = C::N, NB = C::NB, RING = C::RING, PANELS = C::PANELS, HG = C::HG;
+    constexpr int kCopyWarp = C::SOFTMAX / 32, kMmaWarp = kCopyWarp + 1, kAheadWarp = kCopyWarp + 2;
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* psm = ring + RING * C::STAGE;     // [NB][N][128] swizzled, K-major
-    uint8_t* qsm = psm + C::P_BYTES;           // [2][PANELS][N][ROWB] swizzled, K-major
-    // ks * scale * log2 e, log2 vs (-inf: no page), 1 / vs of the pages of two chunks
-    __shared__ float4 page_scale[2][C::PAGES];
-    __shared__ uint64_t full[RING], empty[RING], s_full[NB], p_full[NB], c_full[2], c_empty[2], o_full, drained;
-    __shared__ Chunk chunk[2];
-    __shared__ float qinv[2][GP];
-    __shared__ float red[4][GP];
+    uint8_t* qsm = psm + C::P_BYTES;           // [kDepth][PANELS][N][ROWB] swizzled, K-major
+    // ks * scale * log2 e, log2 vs (-inf: no page), 1 / vs of the announced chunks' pages
+    __shared__ float4 page_scale[kDepth][C::PAGES];
+    __shared__ uint64_t full[RING], empty[RING], s_full[2][NB], p_full[NB], c_full[kDepth], c_empty[kDepth];
+    __shared__ uint64_t o_full, drained;
+    __shared__ Chunk chunk[kDepth];
+    __shared__ float qinv[kDepth][GP];
+    __shared__ float red[C::GROUPS][4][HG];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up;
+    __shared__ int box_z[2][C::PAGES];          // page coordinates of the copied chunks
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (warp == 5) tmem_alloc(&tmem_base, kTmemCols);
+    // the first chunk's pages are on their way while the CTA sets itself up
+    Walk<NB> walk;
+    if (warp == kCopyWarp || warp == kAheadWarp) walk.begin(A);
+    if (warp == kMmaWarp) tmem_alloc(&tmem_base, C::TMEM);
     if (tid == 0) {
         for (int i = 0; i < RING; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < NB; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], kSoftmaxThreads);
+            mbar_init(&s_full[0][i], 1);
+            mbar_init(&s_full[1][i], 1);
+            mbar_init(&p_full[i], C::SOFTMAX);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kDepth; ++i) {
             mbar_init(&c_full[i], 32);
-            mbar_init(&c_empty[i], kSoftmaxThreads);
+            mbar_init(&c_empty[i], C::SOFTMAX + 1);      // and the MMA warp
         }
         mbar_init(&o_full, 1);
         mbar_init(&drained, 1);
         gave_up = 0;
         mbar_fence_init();
     }
-    // columns of heads past G stay zero
-    for (int i = tid; i < (C::P_BYTES + 2 * C::Q_BYTES) / 16; i += kQ8Threads)
+    // query columns past G and, with 4 heads, the upper half of the
+    // probabilities' columns stay zero
+    for (int i = tid; i < (C::P_BYTES + kDepth * C::Q_BYTES) / 16; i += C::THREADS)
         reinterpret_cast<uint4*>(psm)[i] = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t tmem = tmem_base;
-    const int items = A.rows * A.splits;
     volatile int* quit = &gave_up;
 
-    if (warp == 4) {
+    if (warp == kCopyWarp) {
         // ------------------------------------------------ copies
-        if (lane == 0) {
-            tma_prefetch_map(&kmap);
-            tma_prefetch_map(&vmap);
+        if (elect_one()) {
+            tma_prefetch_map(&M.k_block);
+            tma_prefetch_map(&M.v_block);
+            tma_prefetch_map(&M.k_page);
+            tma_prefetch_map(&M.v_page);
         }
+        __syncwarp();
         const int outside = (int)max((int64_t)1, A.num_pages) * kSubPage;   // past the tensor's end
         uint32_t n = 0;   // panels copied so far: stage n % RING
-        bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item it = load_item<NB>(A, i);
-            const int h = it.row % A.H;
-            const int32_t* bt = A.bt + (int64_t)it.row * A.width;
-            const int used = (it.ctx + kSubPage - 1) / kSubPage;      // pages of the context
-            for (int c0 = it.b0; ok && c0 < it.b1; c0 += it.step) {
-                const int nb = min(it.step, it.b1 - c0);
-                // the chunk's page coordinates, page p of the chunk in lane p % 32
-                int z[(C::PAGES + 31) / 32];
+        uint32_t issued = 0;      // the same as the elected thread counts them
+        // One thread: nb blocks with page coordinates z; bit b of `runs`: block
+        // b's pages follow one another.  Panels from number n on.
+        auto copy = [&](const CUtensorMap* page_map, const CUtensorMap* block_map, const int* z, uint32_t runs, int h,
+                        int nb, uint32_t n) {
+            uint32_t st = n % RING, use = n / RING;
+            for (int b = 0; b < nb; ++b) {
 #pragma unroll
-                for (int r = 0; r < (C::PAGES + 31) / 32; ++r) {
-                    const int p = c0 * kPagesPerBlock + r * 32 + lane;
-                    int pg = -1;
-                    if (p < used && r * 32 + lane < nb * kPagesPerBlock) pg = __ldg(bt + p);
-                    z[r] = pg >= 0 && pg < A.num_pages ? pg * kSubPage : outside;
+                for (int panel = 0; panel < PANELS; ++panel) {
+                    if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1, quit)) return;
+                    uint8_t* dst = ring + st * C::STAGE;
+                    mbar_expect(&full[st], C::STAGE);
+                    if (runs >> b & 1) {
+                        tma_load_3d(dst, block_map, panel * 128, h, z[b * kPagesPerBlock], &full[st]);
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < kPagesPerBlock; ++p)
+                            tma_load_3d(dst + p * kSubPage * C::ROWB, page_map, panel * 128, h,
+                                        z[b * kPagesPerBlock + p], &full[st]);
+                    }
+                    ++issued;
+                    if (++st == RING) {
+                        st = 0;
+                        ++use;
+                    }
                 }
-                for (int kv = 0; ok && kv < 2; ++kv) {
-                    const CUtensorMap* map = kv == 0 ? &kmap : &vmap;
+            }
+        };
+        int hv = 0, nbv = 0;      // the chunk whose values are still to come
+        uint32_t runsv = 0, buf = 0;
+        for (; !walk.done() && !__any_sync(kFull, *quit); buf ^= 1) {
+            const int h = walk.it.row % A.H, nb = walk.blocks();
+            // the chunk's coordinates, and which blocks are runs
+            uint32_t runs = 0;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        // page b * 8 + lane % 8 sits in register b / 4 of lane b % 4 * 8 + lane % 8
-                        const int zc = __shfl_sync(kFull, z[b / 4], (b & 3) * 8 + (lane & 7));
-                        if (b < nb) {
+            for (int r = 0; r < Walk<NB>::R; ++r) {
+                const int pg = walk.page[r];
+                const int z = pg >= 0 && pg < A.num_pages ? pg * kSubPage : outside;
+                if (r * 32 + lane < C::PAGES) box_z[buf][r * 32 + lane] = z;
+                const int first = __shfl_sync(kFull, z, lane & 24);
+                const uint32_t follow = __ballot_sync(kFull, z < outside && z == first + (lane & 7) * kSubPage);
 #pragma unroll
-                            for (int panel = 0; panel < PANELS; ++panel) {
-                                if (!ok) break;
-                                const uint32_t st = n % RING;
-                                ok = n < RING || mbar_wait(&empty[st], (n / RING - 1) & 1, quit);
-                                ok = __all_sync(kFull, ok);
-                                if (!ok) break;
-                                if (lane == 0) mbar_expect(&full[st], C::STAGE);
-                                __syncwarp();
-                                if (lane < kPagesPerBlock)
-                                    tma_load_3d(ring + st * C::STAGE + lane * kSubPage * C::ROWB, map, panel * 128, h,
-                                                zc, &full[st]);
-                                ++n;
-                            }
+                for (int b = 0; b < 4; ++b)
+                    if ((follow >> (8 * b) & 255u) == 255u) runs |= 1u << (4 * r + b);
+            }
+            __syncwarp();
+            walk.advance(A);
+            if (elect_one()) {
+                copy(&M.k_page, &M.k_block, box_z[buf], runs, h, nb, n);
+                copy(&M.v_page, &M.v_block, box_z[buf ^ 1], runsv, hv, nbv, n + nb * PANELS);
+            }
+            __syncwarp();
+            n += (nb + nbv) * PANELS;
+            runsv = runs;
+            hv = h;
+            nbv = nb;
+        }
+        if (elect_one()) copy(&M.v_page, &M.v_block, box_z[buf ^ 1], runsv, hv, nbv, n);
+        __syncwarp();
+        // after a wait that ran out: the copies in flight land before the CTA's
+        // memory goes away
+        if (elect_one() && *quit) {
+            int none = 0;
+            for (uint32_t k = issued > RING ? issued - RING : 0; k < issued; ++k)
+                mbar_wait(&full[k % RING], (k / RING) & 1, &none);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------ MMAs
+        if (elect_one()) {
+            constexpr uint32_t kSteps = C::ROWB / 32;
+            // operand descriptors; a byte offset adds offset / 16
+            const uint64_t k_desc = smem_desc(smem_addr(ring), 0, C::ATOM, C::SWIZZLE);
+            const uint64_t q_desc = smem_desc(smem_addr(qsm), 0, C::ATOM, C::SWIZZLE);
+            const uint64_t p_desc = smem_desc(smem_addr(psm), 0, 1024, 2);
+            const uint32_t o_cols = tmem + 2 * C::S_COLS;
+            uint32_t st = 0, use = 0, p_phase = 0, c = 0, s = 0;      // s: chunks with blocks so far
+            int nbv = 0, leftv = 0;              // the chunk whose output is to come: blocks, context tokens
+            bool ok = true, more = true;
+            while (ok && more) {
+                ok = mbar_wait(&c_full[c % kDepth], (c / kDepth) & 1, quit);
+                if (!ok) break;
+                const Chunk ch = chunk[c % kDepth];
+                const int nb = ch.nb;
+                more = nb >= 0;
+                const uint64_t qb = q_desc + ch.qbuf * (C::Q_BYTES / 16);
+                mbar_arrive(&c_empty[c % kDepth]);
+                ++c;
+                // ---- the new chunk's scores ----
+                for (int b = 0; ok && b < nb; ++b) {
+#pragma unroll
+                    for (int panel = 0; panel < PANELS; ++panel) {
+                        ok = ok && mbar_wait(&full[st], use & 1, quit);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t kd = k_desc + st * (C::STAGE / 16);
+#pragma unroll
+                        for (uint32_t k = 0; k < kSteps; ++k)
+                            mma_f8(tmem + (s & 1) * C::S_COLS + b * N, kd + k * 2, qb + panel * (C::Q_PANEL / 16) + k * 2,
+                                   A.k_idesc, panel + k > 0);
+                        tc_commit(&empty[st]);
+                        if (panel == PANELS - 1) tc_commit(&s_full[s & 1][b]);
+                        if (++st == RING) {
+                            st = 0;
+                            ++use;
                         }
                     }
                 }
-            }
-        }
-        // the copies in flight land before the CTA's memory goes away
-        if (!ok) {
-            for (uint32_t k = n > RING ? n - RING : 0; k < n; ++k) {
-                int none = 0;
-                mbar_wait(&full[k % RING], (k / RING) & 1, &none);
-            }
-        }
-    } else if (warp == 5) {
-        // ------------------------------------------------ MMAs
-        if (lane == 0) {
-            constexpr uint32_t kSteps = C::ROWB / 32;
-            const uint32_t q0 = smem_addr(qsm), p0 = smem_addr(psm), r0 = smem_addr(ring);
-            const uint32_t o_cols = tmem + kScoreCols;
-            uint32_t n = 0, p_phase = 0;
-            bool ok = true;
-            for (uint32_t c = 0; ok; ++c) {
-                ok = mbar_wait(&c_full[c & 1], (c >> 1) & 1, quit);
-                if (!ok) break;
-                const int nb = chunk[c & 1].nb;
-                if (nb < 0) break;
-                const uint32_t qb = q0 + chunk[c & 1].qbuf * C::Q_BYTES;
-                for (int b = 0; ok && b < nb; ++b) {
-#pragma unroll
-                    for (int panel = 0; panel < PANELS; ++panel, ++n) {
-                        const uint32_t st = n % RING;
-                        ok = ok && mbar_wait(&full[st], (n / RING) & 1, quit);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (uint32_t k = 0; k < kSteps; ++k)
-                            mma_f8(tmem + b * N, smem_desc(r0 + st * C::STAGE + k * 32, 0, C::ATOM, C::SWIZZLE),
-                                   smem_desc(qb + panel * C::Q_PANEL + k * 32, 0, C::ATOM, C::SWIZZLE), A.k_idesc,
-                                   panel + k > 0);
-                        tc_commit(&empty[st]);
-                    }
-                    if (ok) tc_commit(&s_full[b]);
-                }
-                for (int b = 0; ok && b < nb; ++b) {
+                // ---- the last chunk's output ----
+                for (int b = 0; ok && b < nbv; ++b) {
                     ok = mbar_wait(&p_full[b], (p_phase >> b) & 1, quit);
                     p_phase ^= 1u << b;
+                    const int left = leftv - b * kPageSize;
 #pragma unroll
-                    for (int panel = 0; panel < PANELS; ++panel, ++n) {
-                        const uint32_t st = n % RING;
-                        ok = ok && mbar_wait(&full[st], (n / RING) & 1, quit);
+                    for (int panel = 0; panel < PANELS; ++panel) {
+                        ok = ok && mbar_wait(&full[st], use & 1, quit);
                         if (!ok) break;
+                        if (left < kPageSize && left % kSubPage != 0) {
+                            // the context ends in a page: the page's other values are not the row's
+                            uint4* v = reinterpret_cast<uint4*>(ring + st * C::STAGE + left * C::ROWB);
+                            const int n = (kSubPage - left % kSubPage) * (C::ROWB / 16);
+                            for (int i = 0; i < n; ++i) v[i] = make_uint4(0, 0, 0, 0);
+                            fence_async_smem();
+                        }
                         tc_fence_after();
                         // values: 32 tokens a step; the head's dimensions run along
                         // the rows.  A 64-byte row fills 64 of the 128 MMA rows;
                         // the leading offset 0 reads it again for the others.
+                        const uint64_t vd = k_desc + st * (C::STAGE / 16), pd = p_desc + b * (N * 128 / 16);
 #pragma unroll
                         for (uint32_t k = 0; k < 4; ++k)
-                            mma_f8(o_cols + panel * N,
-                                   smem_desc(r0 + st * C::STAGE + k * 32 * C::ROWB, 0, C::ATOM, C::SWIZZLE),
-                                   smem_desc(p0 + b * N * 128 + k * 32, 0, 1024, 2), A.v_idesc, b > 0 || k > 0);
+                            mma_f8(o_cols + panel * N, vd + k * (32 * C::ROWB / 16), pd + k * 2, A.v_idesc, b > 0 || k > 0);
                         tc_commit(&empty[st]);
+                        if (++st == RING) {
+                            st = 0;
+                            ++use;
+                        }
                     }
                 }
-                if (ok && nb > 0) tc_commit(&o_full);
+                if (ok && nbv > 0) tc_commit(&o_full);
+                if (nb > 0) ++s;
+                nbv = nb;
+                leftv = ch.ctx - ch.c0 * kPageSize;
             }
             // no MMA runs on into the release of its memory
             if (!ok) {
@@ -332,47 +456,45 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == kAheadWarp) {
         // ------------------------------------------------ scales and queries
-        uint32_t c = 0;
+        constexpr int QL = D / 32;         // query values per lane, contiguous
+        const int d = lane * QL, panel = d / C::ROWB, dc = d % C::ROWB;
+        uint32_t c = 0, item = 0;
         int qbuf = 0;
         bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item it = load_item<NB>(A, i);
-            const int h = it.row % A.H;
-            const int32_t* bt = A.bt + (int64_t)it.row * A.width;
-            if (lane == 0 && it.split == 0)
-                report_status(A.status, __ldg(A.ctx + it.row) != it.ctx, BSA_STATUS_BAD_CONTEXT);
-            int c0 = it.b0;
-            do {
-                const int nb = min(it.step, it.b1 - c0);
-                const int buf = c & 1;
-                ok = c < 2 || mbar_wait(&c_empty[buf], ((c >> 1) - 1) & 1, quit);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
+        for (; !walk.done(); ++c) {
+            const Item it = walk.it;
+            const int i = walk.i, c0 = walk.c0, nb = walk.blocks(), h = it.row % A.H, buf = c % kDepth;
+            int32_t pg[Walk<NB>::R];
 #pragma unroll
-                for (int r = 0; r < (C::PAGES + 31) / 32; ++r) {
-                    const int p = r * 32 + lane;
-                    if (p >= nb * kPagesPerBlock) continue;
-                    float4 sc = make_float4(0.f, -INFINITY, 0.f, 0.f);
-                    if ((c0 * kPagesPerBlock + p) * kSubPage < it.ctx) {
-                        const int32_t pg = __ldg(bt + c0 * kPagesPerBlock + p);
-                        const bool good = pg >= 0 && pg < A.num_pages;
-                        report_status(A.status, !good, BSA_STATUS_BAD_PAGE);
-                        if (good) {
-                            const float vs = fmaxf(__ldg(A.vs + (int64_t)pg * A.H + h), 0x1p-100f);
-                            sc = make_float4(__ldg(A.ks + (int64_t)pg * A.H + h) * A.scale_log2e, log2f(vs),
-                                             __frcp_rn(vs), 0.f);
-                        }
+            for (int r = 0; r < Walk<NB>::R; ++r) pg[r] = walk.page[r];
+            if (lane == 0 && it.split == 0 && c0 == it.b0)
+                report_status(A.status, walk.ctx_raw != it.ctx, BSA_STATUS_BAD_CONTEXT);
+            walk.advance(A);
+            ok = c < kDepth || mbar_wait(&c_empty[buf], (c / kDepth - 1) & 1, quit);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            {
+                // the pages' scales
+                float ks[Walk<NB>::R], vs[Walk<NB>::R];
+#pragma unroll
+                for (int r = 0; r < Walk<NB>::R; ++r) {
+                    const bool good = pg[r] >= 0 && pg[r] < A.num_pages;
+                    report_status(A.status, !good && pg[r] != INT32_MIN, BSA_STATUS_BAD_PAGE);
+                    ks[r] = vs[r] = 0.f;
+                    if (good) {
+                        const int64_t at = (int64_t)pg[r] * A.H + h;
+                        ks[r] = __ldg(A.ks + at);
+                        vs[r] = __ldg(A.vs + at);
+                    } else {
+                        pg[r] = -1;
                     }
-                    page_scale[buf][p] = sc;
                 }
                 if (c0 == it.b0 && nb > 0) {
                     // the queries as two e4m3 terms
-                    qbuf ^= 1;
+                    qbuf = item++ % kDepth;
                     uint8_t* qd = qsm + qbuf * C::Q_BYTES;
-                    constexpr int QL = D / 32;         // values per lane, contiguous
-                    const int d = lane * QL, panel = d / C::ROWB, dc = d % C::ROWB;
 #pragma unroll 4
                     for (int g = 0; g < A.G; ++g) {
                         const uint16_t* q = A.q + ((int64_t)it.row * A.G + g) * D + d;
@@ -419,201 +541,211 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ CUtensorMap kmap,
                     }
                     if (lane >= A.G && lane < GP) qinv[qbuf][lane] = 0.f;
                 }
-                if (lane == 0)
-                    chunk[buf] = Chunk{it.row, it.ctx, c0, nb, i, qbuf, c0 == it.b0, c0 + nb == it.b1};
+#pragma unroll
+                for (int r = 0; r < Walk<NB>::R; ++r) {
+                    const int p = r * 32 + lane;
+                    if (p >= nb * kPagesPerBlock) continue;
+                    const float v = fmaxf(vs[r], 0x1p-100f);
+                    page_scale[buf][p] = pg[r] < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                                                   : make_float4(ks[r] * A.scale_log2e, log2f(v), __frcp_rn(v), 0.f);
+                }
+                if (lane == 0) chunk[buf] = Chunk{it.row, it.ctx, c0, nb, i, qbuf, c0 + nb == it.b1};
                 fence_async_smem();
                 mbar_arrive(&c_full[buf]);
-                ++c;
-                c0 += it.step;
-            } while (c0 < it.b1);
+            }
         }
-        if (ok) ok = c < 2 || mbar_wait(&c_empty[c & 1], ((c >> 1) - 1) & 1, quit);
+        if (ok) ok = c < kDepth || mbar_wait(&c_empty[c % kDepth], (c / kDepth - 1) & 1, quit);
         __syncwarp();
-        if (lane == 0) chunk[c & 1].nb = -1;
+        if (lane == 0) chunk[c % kDepth].nb = -1;
         __syncwarp();
-        mbar_arrive(&c_full[c & 1]);
+        mbar_arrive(&c_full[c % kDepth]);
     } else {
         // ------------------------------------------------ softmax and output
-        const uint32_t lanes = tmem + ((uint32_t)warp << 21);    // this warp's 32 TMEM lanes
-        const int part16 = tid >> 4;                               // byte tid's 16-byte part of a P row
-        uint32_t n = 0, s_phase = 0, o_phase = 0;
-        float acc[PANELS][GP], mt[GP], l[GP];
-        // These warps meet in barriers, so none leaves alone: a wait that ran
-        // out anywhere ends at the next chunk for all, or lets the loops go on
-        // with what there is; outputs are NaN then.
-        for (uint32_t c = 0;; ++c) {
-            mbar_wait(&c_full[c & 1], (c >> 1) & 1, quit);
-            softmax_sync();                  // also: red has been read
-            const bool gone = *quit;
-            const Chunk ch = chunk[c & 1];
-            int stop = gone || ch.nb < 0;
-            // one answer for the four warps
-            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %0, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-                         : "+r"(stop)::"memory");
-            if (stop) break;
-            const float4* scales = page_scale[c & 1];
-            const int nb = ch.nb;
-            if (ch.first) {
+        const int group = C::GROUPS == 1 ? 0 : warp >> 2, tok = tid & 127, quad = warp & 3;
+        const int g0 = group * HG;                                 // this group's first head
+        const uint32_t lanes = tmem + ((uint32_t)quad << 21) + g0;   // the warp's 32 TMEM lanes
+        const int part16 = tok >> 4;                               // byte tok's 16-byte part of a P row
+        uint32_t s_phase = 0, o_phase = 0, s = 0;      // s: chunks with blocks so far
+        float acc[PANELS][HG], mt[HG], l[HG], keep[HG];
 #pragma unroll
-                for (int g = 0; g < GP; ++g) {
+        for (int g = 0; g < HG; ++g) {
 #pragma unroll
-                    for (int p = 0; p < PANELS; ++p) acc[p][g] = 0.f;
-                    mt[g] = -INFINITY;
-                    l[g] = 0.f;
-                }
-            }
-            if (nb > 0) {
-                float qi[GP], ct[GP];
-#pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    qi[g] = qinv[ch.qbuf][g];
-                    ct[g] = -INFINITY;
-                }
-                // ---- the chunk's maxima, block by block as scores complete ----
-                for (int b = 0; b < nb; ++b) {
-                    mbar_wait(&s_full[b], (s_phase >> b) & 1, quit);
-                    __syncwarp();
-                    tc_fence_after();
-                    float s[2 * GP];
-                    load_cols<GP>(lanes + b * N, s);
-                    const float4 sc = scales[b * kPagesPerBlock + part16];
-                    const bool live = (ch.c0 + b) * kPageSize + tid < ch.ctx && sc.y != -INFINITY;
-                    if (live) {
-#pragma unroll
-                        for (int g = 0; g < GP; ++g)
-                            ct[g] = fmaxf(ct[g], fmaf(fmaf(s[GP + g], 0.0625f, s[g]), qi[g] * sc.x, sc.y));
-                    }
-                }
-#pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    const float t = max_warp(ct[g]);
-                    if (lane == 0) red[warp][g] = t;
-                }
-                softmax_sync();
-                float keep[GP], add[GP];
-#pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    ct[g] = fmaxf(fmaxf(red[0][g], red[1][g]), fmaxf(red[2][g], red[3][g]));
-                    const float top = fmaxf(mt[g], ct[g]);
-                    keep[g] = top == -INFINITY ? 1.f : ex2(mt[g] - top);
-                    add[g] = top == -INFINITY ? 0.f : ex2(ct[g] - top);
-                    mt[g] = top;
-                    l[g] *= keep[g];
-                    ct[g] = 8.f - ct[g];         // probabilities in units of 2^-8 of the largest
-                }
-                // ---- the probabilities ----
-                for (int b = 0; b < nb; ++b) {
-                    float s[2 * GP];
-                    load_cols<GP>(lanes + b * N, s);
-                    const float4 sc = scales[b * kPagesPerBlock + part16];
-                    const int left = ch.ctx - (ch.c0 + b) * kPageSize;       // context tokens from this block on
-                    const bool live = tid < left && sc.y != -INFINITY;
-                    float w[GP];
-#pragma unroll
-                    for (int g = 0; g < GP; ++g) {
-                        const float t = fmaf(fmaf(s[GP + g], 0.0625f, s[g]), qi[g] * sc.x, sc.y + ct[g]);
-                        w[g] = live ? ex2(t) : 0.f;
-                        l[g] = fmaf(w[g] * sc.z, add[g], l[g]);
-                    }
-                    uint8_t* pb = psm + b * N * 128 + (tid & 15);
-#pragma unroll
-                    for (int g = 0; g < GP; g += 2) {
-                        const uint32_t hi = pack_e4m3(w[g], w[g + 1]);
-                        const float2 f = unpack_e4m3(hi);
-                        const uint32_t lo = pack_e4m3((w[g] - f.x) * 16.f, (w[g + 1] - f.y) * 16.f);
-                        const int r0 = g, r1 = g + 1, r2 = GP + g, r3 = GP + g + 1;
-                        pb[r0 * 128 + ((part16 ^ (r0 & 7)) << 4)] = (uint8_t)hi;
-                        pb[r1 * 128 + ((part16 ^ (r1 & 7)) << 4)] = (uint8_t)(hi >> 8);
-                        pb[r2 * 128 + ((part16 ^ (r2 & 7)) << 4)] = (uint8_t)lo;
-                        pb[r3 * 128 + ((part16 ^ (r3 & 7)) << 4)] = (uint8_t)(lo >> 8);
-                    }
-                    if (left < kPageSize) {
-                        // the last block: no value behind the context's end
-#pragma unroll
-                        for (int panel = 0; panel < PANELS; ++panel) {
-                            const uint32_t k = n + (nb + b) * PANELS + panel, st = k % RING;
-                            mbar_wait(&full[st], (k / RING) & 1, quit);
-                            if (tid >= left) {
-#pragma unroll
-                                for (int x = 0; x < C::ROWB / 16; ++x)
-                                    *reinterpret_cast<uint4*>(ring + st * C::STAGE + tid * C::ROWB + x * 16) =
-                                        make_uint4(0, 0, 0, 0);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                    fence_async_smem();
-                    tc_fence_before();
-                    mbar_arrive(&p_full[b]);
-                }
-                s_phase ^= (1u << nb) - 1;
-                n += 2 * nb * PANELS;
-                // ---- the chunk's outputs join the item's ----
+            for (int p = 0; p < PANELS; ++p) acc[p][g] = 0.f;
+            mt[g] = -INFINITY;
+            l[g] = 0.f;
+            keep[g] = 1.f;
+        }
+        int row = 0, item = 0;
+        bool open = false, last = false;      // a chunk whose output is to come, and whether it ends its item
+
+        // Adds the open chunk's output, and writes the item's result at its end.
+        auto close_chunk = [&]() {
+            if (open) {
                 mbar_wait(&o_full, o_phase, quit);
                 __syncwarp();
                 o_phase ^= 1;
                 tc_fence_after();
 #pragma unroll
                 for (int p = 0; p < PANELS; ++p) {
-                    float s[2 * GP];
-                    load_cols<GP>(lanes + kScoreCols + p * N, s);
+                    float o[2 * HG];
+                    load_terms<HG, GP>(lanes + 2 * C::S_COLS + p * N, o);
 #pragma unroll
-                    for (int g = 0; g < GP; ++g)
-                        acc[p][g] = acc[p][g] * keep[g] + fmaf(s[GP + g], 0.0625f, s[g]) * add[g];
+                    for (int g = 0; g < HG; ++g) acc[p][g] = fmaf(acc[p][g], keep[g], fmaf(o[HG + g], 0.0625f, o[g]));
                 }
                 tc_fence_before();
             }
-            if (ch.last) {
-                // ---- the item's result: the sums over the four warps' tokens ----
-                softmax_sync();
+            if (last) {
+                // the sums over the group's tokens
+                group_sync(group);
 #pragma unroll
-                for (int g = 0; g < GP; ++g) {
+                for (int g = 0; g < HG; ++g) {
                     const float a = sum_warp(l[g]);
-                    if (lane == 0) red[warp][g] = a;
+                    if (lane == 0) red[group][quad][g] = a;
                 }
-                softmax_sync();
+                group_sync(group);
                 const bool bad = *quit;
-                uint16_t* o16 = A.out + (int64_t)ch.row * A.G * D;
-                float* o32 = A.part + (int64_t)ch.item * part_floats(A.G, D);
+                uint16_t* o16 = A.out + (int64_t)row * A.G * D;
+                float* o32 = A.part + (int64_t)item * part_floats(A.G, D);
 #pragma unroll
-                for (int g = 0; g < GP; ++g) {
-                    if (g >= A.G) break;
-                    const float sum = bad ? NAN : red[0][g] + red[1][g] + red[2][g] + red[3][g];
-                    if (A.part == nullptr) {
-                        const float f = sum == 0.f ? 0.f : 1.f / sum;
+                for (int g = 0; g < HG; ++g) {
+                    if (g0 + g < A.G) {
+                        const float sum = bad ? NAN
+                                              : red[group][0][g] + red[group][1][g] + red[group][2][g] + red[group][3][g];
+                        if (A.part == nullptr) {
+                            const float f = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-                        for (int p = 0; p < PANELS; ++p)
-                            if (tid < C::ROWB)
-                                o16[g * D + p * 128 + tid] =
-                                    __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : acc[p][g] * f));
-                    } else {
+                            for (int p = 0; p < PANELS; ++p)
+                                if (tok < C::ROWB)
+                                    o16[(g0 + g) * D + p * 128 + tok] =
+                                        __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : acc[p][g] * f));
+                        } else {
 #pragma unroll
-                        for (int p = 0; p < PANELS; ++p)
-                            if (tid < C::ROWB) o32[g * D + p * 128 + tid] = acc[p][g];
-                        if (tid == 0) {
-                            o32[A.G * D + g] = mt[g];
-                            o32[A.G * D + A.G + g] = sum;
+                            for (int p = 0; p < PANELS; ++p)
+                                if (tok < C::ROWB) o32[(g0 + g) * D + p * 128 + tok] = acc[p][g];
+                            if (tok == 0) {
+                                o32[A.G * D + g0 + g] = mt[g];
+                                o32[A.G * D + A.G + g0 + g] = sum;
+                            }
                         }
                     }
+#pragma unroll
+                    for (int p = 0; p < PANELS; ++p) acc[p][g] = 0.f;
+                    mt[g] = -INFINITY;
+                    l[g] = 0.f;
                 }
             }
-            mbar_arrive(&c_empty[c & 1]);
+            open = last = false;
+        };
+
+        // These warps meet in barriers, so none leaves alone: a wait that ran
+        // out anywhere ends at the next chunk for the whole group, or lets the
+        // loops go on with what there is; outputs are NaN then.
+        for (uint32_t c = 0;; ++c) {
+            const int buf = c % kDepth;
+            mbar_wait(&c_full[buf], (c / kDepth) & 1, quit);
+            const bool gone = *quit;
+            const Chunk ch = chunk[buf];
+            const int nb = ch.nb;
+            if (group_any(group, gone || nb < 0)) break;
+            const float4* scales = page_scale[buf];
+            float qi[HG], ct[HG];
+#pragma unroll
+            for (int g = 0; g < HG; ++g) {
+                qi[g] = qinv[ch.qbuf][g0 + g];
+                ct[g] = -INFINITY;
+            }
+            // ---- the chunk's maxima, block by block as scores complete ----
+            const uint32_t sbuf = s & 1;
+            const uint32_t s_cols = lanes + sbuf * C::S_COLS;
+            for (int b = 0; b < nb; ++b) {
+                mbar_wait(&s_full[sbuf][b], (s_phase >> (sbuf * 8 + b)) & 1, quit);
+                __syncwarp();
+                tc_fence_after();
+                float x[2 * HG];
+                load_terms<HG, GP>(s_cols + b * N, x);
+                const float4 sc = scales[b * kPagesPerBlock + part16];
+                const bool live = (ch.c0 + b) * kPageSize + tok < ch.ctx && sc.y != -INFINITY;
+                if (live) {
+#pragma unroll
+                    for (int g = 0; g < HG; ++g)
+                        ct[g] = fmaxf(ct[g], fmaf(fmaf(x[HG + g], 0.0625f, x[g]), qi[g] * sc.x, sc.y));
+                }
+            }
+            close_chunk();
+            row = ch.row;
+            item = ch.item;
+            last = ch.last;
+            if (nb > 0) {
+                open = true;
+                group_sync(group);                       // red has been read
+#pragma unroll
+                for (int g = 0; g < HG; ++g) {
+                    const float t = max_warp(ct[g]);
+                    if (lane == 0) red[group][quad][g] = t;
+                }
+                group_sync(group);
+#pragma unroll
+                for (int g = 0; g < HG; ++g) {
+                    const float t = fmaxf(fmaxf(red[group][0][g], red[group][1][g]), fmaxf(red[group][2][g], red[group][3][g]));
+                    const float top = fmaxf(mt[g], t);
+                    keep[g] = top == -INFINITY ? 1.f : ex2(mt[g] - top);
+                    mt[g] = top;
+                    l[g] *= keep[g];
+                    ct[g] = 8.f - top;           // probabilities in units of 2^-8 of the largest so far
+                }
+                // ---- the probabilities ----
+                for (int b = 0; b < nb; ++b) {
+                    float x[2 * HG];
+                    load_terms<HG, GP>(s_cols + b * N, x);
+                    const float4 sc = scales[b * kPagesPerBlock + part16];
+                    const bool live = (ch.c0 + b) * kPageSize + tok < ch.ctx && sc.y != -INFINITY;
+                    float w[HG];
+#pragma unroll
+                    for (int g = 0; g < HG; ++g) {
+                        const float t = fmaf(fmaf(x[HG + g], 0.0625f, x[g]), qi[g] * sc.x, sc.y + ct[g]);
+                        w[g] = live ? ex2(t) : 0.f;
+                        l[g] = fmaf(w[g], sc.z, l[g]);
+                    }
+                    uint8_t* pb = psm + b * N * 128 + (tok & 15) + g0 * 128;
+#pragma unroll
+                    for (int g = 0; g < HG; g += 2) {
+                        const uint32_t hi = pack_e4m3(w[g], w[g + 1]);
+                        const float2 f = unpack_e4m3(hi);
+                        const uint32_t lo = pack_e4m3((w[g] - f.x) * 16.f, (w[g + 1] - f.y) * 16.f);
+                        // rows g0 + g and GP + g0 + g; g0 and (from 8 heads on) GP are multiples of 8
+                        const int r0 = g, r1 = g + 1, r2 = GP + g, r3 = GP + g + 1;
+                        pb[r0 * 128 + ((part16 ^ (r0 & 7)) << 4)] = (uint8_t)hi;
+                        pb[r1 * 128 + ((part16 ^ (r1 & 7)) << 4)] = (uint8_t)(hi >> 8);
+                        pb[r2 * 128 + ((part16 ^ (r2 & 7)) << 4)] = (uint8_t)lo;
+                        pb[r3 * 128 + ((part16 ^ (r3 & 7)) << 4)] = (uint8_t)(lo >> 8);
+                    }
+                    fence_async_smem();
+                    tc_fence_before();
+                    mbar_arrive(&p_full[b]);
+                }
+                s_phase ^= ((1u << nb) - 1) << (sbuf * 8);
+                ++s;
+            }
+            mbar_arrive(&c_empty[buf]);
         }
+        close_chunk();
     }
     tc_fence_before();
     __syncthreads();
     if (tid == 0) report_status(A.status, gave_up != 0, BSA_STATUS_TIMEOUT);
-    if (warp == 5) tmem_free(tmem, kTmemCols);
+    if (warp == kMmaWarp) tmem_free(tmem, C::TMEM);
 }
 
 // Joins the partial results of a split row, head by head: a thread per
-// dimension.
+// dimension.  Launched to start beside the last items (programmatic dependent
+// launch), it waits for their end here.
 __global__ void __launch_bounds__(256)
-attention_q8_join_kernel(const float* __restrict__ part, uint16_t* __restrict__ out, int splits, int G, int D) {
+attention_q8_join_kernel(const float* part, uint16_t* out, int splits, int G, int D) {
     extern __shared__ float weight[];          // [splits]
     __shared__ float total[2];
     const int64_t row = blockIdx.x;
     const int g = blockIdx.y, tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written
     const int64_t len = part_floats(G, D);
     const float* base = part + row * splits * len;
     if (tid < 32) {
@@ -659,13 +791,13 @@ EncodeFn encode_fn() {
 }
 
 // The cache as a tensor of (dimension, head, token) bytes, read in boxes of
-// one page of one head (128 bytes of it at most).
-bool encode_cache(CUtensorMap* map, const void* base, int64_t tokens, int64_t H, int64_t D) {
+// `box_tokens` tokens of one head (128 bytes of it at most).
+bool encode_cache(CUtensorMap* map, const void* base, int64_t tokens, int64_t H, int64_t D, int box_tokens) {
     const EncodeFn fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)(H * D)};
-    const cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), 1, (cuuint32_t)kSubPage};
+    const cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), 1, (cuuint32_t)box_tokens};
     const cuuint32_t unit[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, unit,
               CU_TENSOR_MAP_INTERLEAVE_NONE, D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
@@ -673,26 +805,26 @@ bool encode_cache(CUtensorMap* map, const void* base, int64_t tokens, int64_t H,
 }
 
 template <int D, int GP>
-cudaError_t launch_q8(Q8Params& A, const CUtensorMap& km, const CUtensorMap& vm, bool e4m3, int sms, cudaStream_t st) {
+cudaError_t launch_q8(Q8Params& A, const Q8Maps& M, bool e4m3, int sms, cudaStream_t st) {
     using C = Q8Cfg<D, GP>;
     const uint32_t fmt = e4m3 ? 0 : 1;
     A.k_idesc = f8_idesc(fmt, 0, false, 128, C::N);
     A.v_idesc = f8_idesc(fmt, 0, true, 128, C::N);
     auto kern = attention_q8_kernel<D, GP>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static FuncOnce once;
+    const cudaError_t e = once.smem(reinterpret_cast<const void*>(kern), C::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)A.rows * A.splits;
-    const int64_t slots = (int64_t)sms * kQ8Ctas;
-    static_assert(C::RING >= 4 && C::SMEM + C::STATIC <= kQ8Smem, "the ring fits beside another CTA");
-    kern<<<(unsigned)(items < slots ? items : slots), kQ8Threads, C::SMEM, st>>>(A, km, vm);
+    const int64_t slots = (int64_t)sms * C::CTAS;
+    kern<<<(unsigned)(items < slots ? items : slots), C::THREADS, C::SMEM, st>>>(A, M);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_q8_g(Q8Params& A, const CUtensorMap& km, const CUtensorMap& vm, bool e4m3, int sms, cudaStream_t st) {
-    if (A.G <= 4) return launch_q8<D, 4>(A, km, vm, e4m3, sms, st);
-    if (A.G <= 8) return launch_q8<D, 8>(A, km, vm, e4m3, sms, st);
-    return launch_q8<D, 16>(A, km, vm, e4m3, sms, st);
+cudaError_t launch_q8_g(Q8Params& A, const Q8Maps& M, bool e4m3, int sms, cudaStream_t st) {
+    if (A.G <= 4) return launch_q8<D, 4>(A, M, e4m3, sms, st);
+    if (A.G <= 8) return launch_q8<D, 8>(A, M, e4m3, sms, st);
+    return launch_q8<D, 16>(A, M, e4m3, sms, st);
 }
 
 bool sizes_ok(int64_t T, int64_t H, int64_t G, int64_t D) {
@@ -700,20 +832,30 @@ bool sizes_ok(int64_t T, int64_t H, int64_t G, int64_t D) {
            G <= BSA_MAX_ATTN_Q8_GROUP && (D == 64 || D == 128 || D == 256);
 }
 
-// Items per row: the count with the least work on the longest CTA, a
-// block's copy against an item's fixed cost and the joining launch.
-int pick_splits(int64_t rows, int64_t D, int32_t K, int sms) {
+// Items per row.  For each number of rounds over the resident CTAs the largest
+// split that keeps to it, the fewest items of that block count, is weighed: the
+// longest CTA's blocks and items, not less than the copies of all blocks over
+// all SMs, and the join.
+int pick_splits(int64_t rows, int64_t G, int64_t D, int32_t K, int sms) {
+    const int64_t slots = (int64_t)sms * (G <= 8 ? 2 : 1);
+    const double copy_us = (double)rows * K * D * 256 / 6.0e6;     // 6 TB/s
+    auto cost = [&](int64_t s) {
+        const int64_t blocks = (K + s - 1) / s;
+        const double cta_us = (double)((rows * s + slots - 1) / slots) * (blocks * 0.7 + 2.0);
+        return (cta_us > copy_us ? cta_us : copy_us) + (s > 1 ? 3.0 + 0.004 * rows * s : 0.0);
+    };
     int best = 1;
-    double least = 0;
-    const int64_t slots = (int64_t)sms * kQ8Ctas;
-    for (int s = 1; s <= K; ++s) {
-        const int64_t waves = (rows * s + slots - 1) / slots;
-        const double us = waves * ((K + s - 1) / s * (D / 128.0) * 1.5 + 1.5) + (s > 1 ? 3.0 + 0.02 * s : 0.0);
-        if (s == 1 || us < least) {
-            best = s;
+    double least = cost(1);
+    for (int64_t rounds = 1; rounds <= 8; ++rounds) {
+        int64_t s = rounds * slots / rows;
+        if (s > K) s = K;
+        if (s < 2) continue;
+        s = (K + (K + s - 1) / s - 1) / ((K + s - 1) / s);
+        const double us = cost(s);
+        if (us < least) {
+            best = (int)s;
             least = us;
         }
-        if (waves > 8) break;      // enough items to even out
     }
     return best;
 }
@@ -729,7 +871,7 @@ using namespace bsa;
 
 extern "C" size_t bsa_attention_q8_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t D, int32_t K) {
     if (!sizes_ok(T, H, G, D) || T == 0 || K < 1 || K > BSA_MAX_TOPK) return 0;
-    return workspace_need(T * H, G, D, pick_splits(T * H, D, K, device_sm_count()));
+    return workspace_need(T * H, G, D, pick_splits(T * H, G, D, K, device_sm_count()));
 }
 
 extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache, const void* v_cache,
@@ -762,7 +904,7 @@ extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache
     A.H = (int32_t)H;
     A.G = (int32_t)G;
     A.width = K * kPagesPerBlock;
-    A.splits = pick_splits(T * H, D, K, sms);
+    A.splits = pick_splits(T * H, G, D, K, sms);
     A.scale_log2e = scale * 1.44269504f;
     A.status = current_status_word();
     if (A.splits > 1) {
@@ -772,21 +914,31 @@ extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache
         A.part = static_cast<float*>(workspace);
     }
     // an empty cache: no box lies inside, any address serves
-    CUtensorMap km, vm;
+    Q8Maps M;
     const int64_t tokens = (num_pages > 0 ? num_pages : 1) * kSubPage;
-    if (!encode_cache(&km, num_pages > 0 ? k_cache : q, tokens, H, D) ||
-        !encode_cache(&vm, num_pages > 0 ? v_cache : q, tokens, H, D))
+    const void* kb = num_pages > 0 ? k_cache : q;
+    const void* vb = num_pages > 0 ? v_cache : q;
+    if (!encode_cache(&M.k_page, kb, tokens, H, D, kSubPage) || !encode_cache(&M.v_page, vb, tokens, H, D, kSubPage) ||
+        !encode_cache(&M.k_block, kb, tokens, H, D, kPageSize) || !encode_cache(&M.v_block, vb, tokens, H, D, kPageSize))
         return (int)cudaErrorInvalidValue;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool e4m3 = cache_dtype == BSA_DTYPE_E4M3;
     cudaError_t e;
-    if (D == 64) e = launch_q8_g<64>(A, km, vm, e4m3, sms, st);
-    else if (D == 128) e = launch_q8_g<128>(A, km, vm, e4m3, sms, st);
-    else e = launch_q8_g<256>(A, km, vm, e4m3, sms, st);
+    if (D == 64) e = launch_q8_g<64>(A, M, e4m3, sms, st);
+    else if (D == 128) e = launch_q8_g<128>(A, M, e4m3, sms, st);
+    else e = launch_q8_g<256>(A, M, e4m3, sms, st);
     if (e == cudaSuccess && A.splits > 1) {
-        attention_q8_join_kernel<<<dim3((unsigned)A.rows, (unsigned)A.G), (unsigned)D, A.splits * sizeof(float), st>>>(
-            A.part, A.out, A.splits, A.G, (int)D);
-        e = cudaGetLastError();
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)A.rows, (unsigned)A.G);
+        cfg.blockDim = dim3((unsigned)D);
+        cfg.dynamicSmemBytes = A.splits * sizeof(float);
+        cfg.stream = st;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, attention_q8_join_kernel, (const float*)A.part, A.out, A.splits, A.G, (int)D);
     }
     return e == cudaSuccess ? BSA_OK : (int)e;
 }

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/bsa_topk.h"
 
 namespace bsa {
@@ -199,6 +201,15 @@ size_t split_workspace_bytes(int64_t rows, int32_t chunks, int32_t K);
 SplitWorkspace carve_split_workspace(void* base, int64_t rows, int32_t chunks, int32_t K);
 
 int device_sm_count();
+
+// Raises a kernel's dynamic shared-memory limit once per device.
+class FuncOnce {
+public:
+    cudaError_t smem(const void* kernel, int bytes);
+
+private:
+    std::atomic<uint64_t> done_{0};     // bit per device
+};
 
 // The status word registered for the current device (bsa_set_status_word), or null.
 uint32_t* current_status_word();

@@ -14,6 +14,16 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// One thread of a converged warp.  Written with elect.sync: under a test of the
+// lane's number the compiler cannot tell that one thread runs, and takes a
+// tcgen05.mma's operands through a loop over threads (205 instead of 80 cycles
+// an MMA, measured back to back).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---- mbarriers -----------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
@@ -120,6 +130,21 @@ __device__ __forceinline__ void tmem_ld8(uint32_t addr, float (&r)[8]) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(u[i]);
+}
+
+// 8 columns at each of two addresses
+__device__ __forceinline__ void tmem_ld8x2(uint32_t lo, uint32_t hi, float (&r)[16]) {
+    uint32_t u[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(lo), "r"(hi)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
 }
 
 // Shared-memory operand descriptor: start address, leading and stride byte

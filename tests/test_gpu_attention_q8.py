@@ -219,3 +219,23 @@ def test_attention_q8_refuses_small_or_misaligned_workspaces(cuda_device):
         with pytest.raises(bsa.BsaError) as e:
             bsa.bsa_sparse_decode_attention_q8(*args, workspace=bad)
         assert e.value.status == -5
+
+
+@pytest.mark.parametrize("H,G,D,fmt", [(1, 4, 64, "e4m3"), (2, 8, 128, "e5m2"), (1, 3, 256, "e4m3"), (2, 16, 128, "e4m3")])
+def test_attention_q8_blocks_in_runs(cuda_device, H, G, D, fmt):
+    """Tables as the selector writes them: a block's eight pages follow one
+    another (the last block of the cache among them), mixed with blocks whose
+    pages almost do."""
+    T, K, blocks = 5, 9, 60
+    q, c, s, bt, _, dtype, kind = _case(T, H, G, D, K, fmt, [0] * (T * H), 30 + D, pages=blocks * 8)
+    for x in c:                          # no NaN codes: every page is read somewhere
+        x[(x & 0x7F) == 0x7F] = 0x3A
+    g = torch.Generator().manual_seed(D)
+    phys = torch.stack([torch.randperm(blocks, generator=g)[:K] for _ in range(T * H)]).view(T, H, K)
+    phys[0, 0, 3] = blocks - 1
+    bt = (phys[..., None] * 8 + torch.arange(8)).view(T, H, K * 8).to(torch.int32)
+    bt[1, 0, 16:24] = bt[1, 0, 16:24].flip(0)
+    bt[1, 0, 31] += 1 if bt[1, 0, 31] < blocks * 8 - 1 else -1
+    bt[2, 0, 8:16] = torch.arange(blocks * 8 - 4, blocks * 8 + 4)      # runs out of the cache
+    ctx = torch.tensor([K * 128, 1100, 1027, 897, 128, 15, 1, 1151, 1040, 640][:T * H], dtype=torch.int32).view(T, H)
+    _check(cuda_device, q, c, s, bt, ctx, dtype, kind)
