@@ -72,7 +72,10 @@ struct Q8Cfg {
     static constexpr int TMEM = 512 / CTAS;
     static constexpr int PANELS = D == 256 ? 2 : 1;   // 128-byte parts of a head's row
     static constexpr int ROWB = D / PANELS;           // bytes of a row in a panel: 64 or 128
-    static constexpr int STAGE = 128 * ROWB;          // a panel of a block: 8 or 16 KB
+    static constexpr int PANEL = 128 * ROWB;          // a panel of a block: 8 or 16 KB
+    static constexpr int BPS = ROWB == 64 ? 2 : 1;    // blocks per ring stage
+    static constexpr int STAGE = BPS * PANEL;         // 16 KB
+    static constexpr int NU = NB / 2;                 // pairs of blocks: the warps' handshakes are a pair's
     static constexpr int P_BYTES = NB * N * 128;
     static constexpr int Q_PANEL = N * ROWB;
     static constexpr int Q_BYTES = PANELS * Q_PANEL;
@@ -83,6 +86,7 @@ struct Q8Cfg {
     static constexpr int SMEM = RING * STAGE + FIXED;
     static constexpr uint32_t SWIZZLE = ROWB == 128 ? 2 : 4;
     static constexpr uint32_t ATOM = 8 * ROWB;        // 8 rows: the swizzle's period
+    __host__ __device__ static constexpr int stages(int nb) { return (nb * PANELS + BPS - 1) / BPS; }
     static_assert(2 * S_COLS + PANELS * N <= TMEM, "two score buffers and the outputs fit");
     static_assert(RING >= 4, "the ring holds two blocks of the widest heads");
 };
@@ -248,7 +252,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
     uint8_t* qsm = psm + C::P_BYTES;           // [kDepth][PANELS][N][ROWB] swizzled, K-major
     // ks * scale * log2 e, log2 vs (-inf: no page), 1 / vs of the announced chunks' pages
     __shared__ float4 page_scale[kDepth][C::PAGES];
-    __shared__ uint64_t full[RING], empty[RING], s_full[2][NB], p_full[NB], c_full[kDepth], c_empty[kDepth];
+    __shared__ uint64_t full[RING], empty[RING], s_full[2][C::NU], p_full[C::NU], c_full[kDepth], c_empty[kDepth];
     __shared__ uint64_t o_full, drained;
     __shared__ Chunk chunk[kDepth];
     __shared__ float qinv[kDepth][GP];
@@ -267,7 +271,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < NB; ++i) {
+        for (int i = 0; i < C::NU; ++i) {
             mbar_init(&s_full[0][i], 1);
             mbar_init(&s_full[1][i], 1);
             mbar_init(&p_full[i], C::SOFTMAX);
@@ -303,19 +307,22 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         }
         __syncwarp();
         const int outside = (int)max((int64_t)1, A.num_pages) * kSubPage;   // past the tensor's end
-        uint32_t n = 0;   // panels copied so far: stage n % RING
+        uint32_t n = 0;   // stages filled so far: stage n % RING
         uint32_t issued = 0;      // the same as the elected thread counts them
         // One thread: nb blocks with page coordinates z; bit b of `runs`: block
-        // b's pages follow one another.  Panels from number n on.
+        // b's pages follow one another.  Stages from number n on.
         auto copy = [&](const CUtensorMap* page_map, const CUtensorMap* block_map, const int* z, uint32_t runs, int h,
                         int nb, uint32_t n) {
             uint32_t st = n % RING, use = n / RING;
             for (int b = 0; b < nb; ++b) {
 #pragma unroll
                 for (int panel = 0; panel < PANELS; ++panel) {
-                    if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1, quit)) return;
-                    uint8_t* dst = ring + st * C::STAGE;
-                    mbar_expect(&full[st], C::STAGE);
+                    const int sub = C::BPS == 1 ? 0 : b & 1;          // the block's place in its stage
+                    if (sub == 0) {
+                        if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1, quit)) return;
+                        mbar_expect(&full[st], C::PANEL * (C::BPS == 2 && b + 1 < nb ? 2 : 1));
+                    }
+                    uint8_t* dst = ring + st * C::STAGE + sub * C::PANEL;
                     if (runs >> b & 1) {
                         tma_load_3d(dst, block_map, panel * 128, h, z[b * kPagesPerBlock], &full[st]);
                     } else {
@@ -324,10 +331,12 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                             tma_load_3d(dst + p * kSubPage * C::ROWB, page_map, panel * 128, h,
                                         z[b * kPagesPerBlock + p], &full[st]);
                     }
-                    ++issued;
-                    if (++st == RING) {
-                        st = 0;
-                        ++use;
+                    if (sub == C::BPS - 1 || b + 1 == nb) {
+                        ++issued;
+                        if (++st == RING) {
+                            st = 0;
+                            ++use;
+                        }
                     }
                 }
             }
@@ -353,10 +362,10 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             walk.advance(A);
             if (elect_one()) {
                 copy(&M.k_page, &M.k_block, box_z[buf], runs, h, nb, n);
-                copy(&M.v_page, &M.v_block, box_z[buf ^ 1], runsv, hv, nbv, n + nb * PANELS);
+                copy(&M.v_page, &M.v_block, box_z[buf ^ 1], runsv, hv, nbv, n + C::stages(nb));
             }
             __syncwarp();
-            n += (nb + nbv) * PANELS;
+            n += C::stages(nb) + C::stages(nbv);
             runsv = runs;
             hv = h;
             nbv = nb;
@@ -394,36 +403,45 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 ++c;
                 // ---- the new chunk's scores ----
                 for (int b = 0; ok && b < nb; ++b) {
+                    const int sub = C::BPS == 1 ? 0 : b & 1;
+                    const bool ends = (b & 1) == 1 || b + 1 == nb;        // of a pair
 #pragma unroll
                     for (int panel = 0; panel < PANELS; ++panel) {
-                        ok = ok && mbar_wait(&full[st], use & 1, quit);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t kd = k_desc + st * (C::STAGE / 16);
+                        if (sub == 0) {
+                            ok = ok && mbar_wait(&full[st], use & 1, quit);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        const uint64_t kd = k_desc + (st * C::STAGE + sub * C::PANEL) / 16;
 #pragma unroll
                         for (uint32_t k = 0; k < kSteps; ++k)
                             mma_f8(tmem + (s & 1) * C::S_COLS + b * N, kd + k * 2, qb + panel * (C::Q_PANEL / 16) + k * 2,
                                    A.k_idesc, panel + k > 0);
-                        tc_commit(&empty[st]);
-                        if (panel == PANELS - 1) tc_commit(&s_full[s & 1][b]);
-                        if (++st == RING) {
-                            st = 0;
-                            ++use;
+                        if (C::BPS == 1 || ends) {
+                            tc_commit(&empty[st]);
+                            if (++st == RING) {
+                                st = 0;
+                                ++use;
+                            }
                         }
                     }
+                    if (ok && ends) tc_commit(&s_full[s & 1][b >> 1]);
                 }
                 // ---- the last chunk's output ----
                 for (int b = 0; ok && b < nbv; ++b) {
-                    ok = mbar_wait(&p_full[b], (p_phase >> b) & 1, quit);
-                    p_phase ^= 1u << b;
+                    const int sub = C::BPS == 1 ? 0 : b & 1;
+                    if ((b & 1) == 0) {
+                        ok = mbar_wait(&p_full[b >> 1], (p_phase >> (b >> 1)) & 1, quit);
+                        p_phase ^= 1u << (b >> 1);
+                    }
                     const int left = leftv - b * kPageSize;
 #pragma unroll
                     for (int panel = 0; panel < PANELS; ++panel) {
-                        ok = ok && mbar_wait(&full[st], use & 1, quit);
+                        if (sub == 0) ok = ok && mbar_wait(&full[st], use & 1, quit);
                         if (!ok) break;
                         if (left < kPageSize && left % kSubPage != 0) {
                             // the context ends in a page: the page's other values are not the row's
-                            uint4* v = reinterpret_cast<uint4*>(ring + st * C::STAGE + left * C::ROWB);
+                            uint4* v = reinterpret_cast<uint4*>(ring + st * C::STAGE + sub * C::PANEL + left * C::ROWB);
                             const int n = (kSubPage - left % kSubPage) * (C::ROWB / 16);
                             for (int i = 0; i < n; ++i) v[i] = make_uint4(0, 0, 0, 0);
                             fence_async_smem();
@@ -432,14 +450,17 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                         // values: 32 tokens a step; the head's dimensions run along
                         // the rows.  A 64-byte row fills 64 of the 128 MMA rows;
                         // the leading offset 0 reads it again for the others.
-                        const uint64_t vd = k_desc + st * (C::STAGE / 16), pd = p_desc + b * (N * 128 / 16);
+                        const uint64_t vd = k_desc + (st * C::STAGE + sub * C::PANEL) / 16;
+                        const uint64_t pd = p_desc + b * (N * 128 / 16);
 #pragma unroll
                         for (uint32_t k = 0; k < 4; ++k)
                             mma_f8(o_cols + panel * N, vd + k * (32 * C::ROWB / 16), pd + k * 2, A.v_idesc, b > 0 || k > 0);
-                        tc_commit(&empty[st]);
-                        if (++st == RING) {
-                            st = 0;
-                            ++use;
+                        if (C::BPS == 1 || sub == 1 || b + 1 == nbv) {
+                            tc_commit(&empty[st]);
+                            if (++st == RING) {
+                                st = 0;
+                                ++use;
+                            }
                         }
                     }
                 }
@@ -658,9 +679,11 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             const uint32_t sbuf = s & 1;
             const uint32_t s_cols = lanes + sbuf * C::S_COLS;
             for (int b = 0; b < nb; ++b) {
-                mbar_wait(&s_full[sbuf][b], (s_phase >> (sbuf * 8 + b)) & 1, quit);
-                __syncwarp();
-                tc_fence_after();
+                if ((b & 1) == 0) {
+                    mbar_wait(&s_full[sbuf][b >> 1], (s_phase >> (sbuf * 8 + (b >> 1))) & 1, quit);
+                    __syncwarp();
+                    tc_fence_after();
+                }
                 float x[2 * HG];
                 load_terms<HG, GP>(s_cols + b * N, x);
                 const float4 sc = scales[b * kPagesPerBlock + part16];
@@ -719,11 +742,13 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                         pb[r2 * 128 + ((part16 ^ (r2 & 7)) << 4)] = (uint8_t)lo;
                         pb[r3 * 128 + ((part16 ^ (r3 & 7)) << 4)] = (uint8_t)(lo >> 8);
                     }
-                    fence_async_smem();
-                    tc_fence_before();
-                    mbar_arrive(&p_full[b]);
+                    if ((b & 1) == 1 || b + 1 == nb) {
+                        fence_async_smem();
+                        tc_fence_before();
+                        mbar_arrive(&p_full[b >> 1]);
+                    }
                 }
-                s_phase ^= ((1u << nb) - 1) << (sbuf * 8);
+                s_phase ^= ((1u << ((nb + 1) >> 1)) - 1) << (sbuf * 8);
                 ++s;
             }
             mbar_arrive(&c_empty[buf]);
