@@ -7,11 +7,10 @@
 // and appends page by page: the row that is the call's first in its page (its
 // leader) stands for all of the call's tokens in that page, at most 16, which
 // follow it, possibly into the next tile.  A warp takes such a page's keys or
-// values of one head: it holds the tokens in registers, as they came, takes the
-// maximum of the rotated values, then rotates again to round them with the
-// page's scale (rotating twice costs two products per value; holding fp32
-// values would double the registers).  So a page has one writer, and the result
-// does not depend on how the work is spread.
+// values of one head: it takes the maximum of the rotated values, then rotates
+// again to round them with the page's scale (rotating twice costs two products
+// per value; holding fp32 values would take 64 registers a lane and more).  So a
+// page has one writer, and the result does not depend on how the work is spread.
 // Bound by memory in long calls (the queries' read and write are the most of
 // it) and by its chain of dependent loads (length, table entry, scale) in single
 // steps.
@@ -27,8 +26,11 @@ namespace bsa {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendCtas = 4;          // per SM
 constexpr int kAppendTile = 16;         // rows per CTA at most
 constexpr int kPageRows = BSA_SUB_PAGE_SIZE;
+constexpr int kPageBatch = 2;           // slots of a page in flight per lane
+constexpr int kQueryBatch = 2;          // slots of the queries in flight per thread
 
 struct AppendParams {
     bsa_append_args_t a;
@@ -110,8 +112,7 @@ struct Segment {
 };
 
 // One page's n tokens of one head, rows x + t * ts, into slots [off, off + n).
-// SL: slots of two 8-element groups a lane holds, of the page's 16 * D / 16.
-template <int FMT, int SL, bool PAIRS>
+template <int FMT, RopeMode MODE, bool KEEP>
 __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t* __restrict__ x, int64_t ts,
                                            const Segment& S, int h, const float* cs, bool rotate, void* cache,
                                            float* scales) {
@@ -123,55 +124,66 @@ __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t
     float* sp = FMT == BSA_DTYPE_BF16 ? nullptr : scales + S.page * P.a.H + h;
     float old = 0.f;
     if (FMT != BSA_DTYPE_BF16 && S.off > 0) old = *sp;
-    uint4 a[SL], b[SL];
-    int at[SL];                     // token << 8 | slot, or -1
+    const int total = S.n * ks;     // slots of the page's tokens
+    struct Batch {
+        uint4 a[kPageBatch], b[kPageBatch];
+        int at[kPageBatch];         // token << 8 | slot
+    };
+    auto load = [&](int i, Batch& B) {
 #pragma unroll
-    for (int j = 0; j < SL; ++j) {
-        const int i = j * 32 + lane;
-        const int t = i / ks, k = i - t * ks;
-        at[j] = t < S.n ? t << 8 | k : -1;
-        if (at[j] >= 0) {
+        for (int j = 0; j < kPageBatch; ++j) {
+            const int u = min(i + 32 * j, total - 1);
+            const int t = u / ks, k = u - t * ks;
             int o0, o1;
-            slot_groups<PAIRS, 8>(k, half, o0, o1);
-            a[j] = __ldg(reinterpret_cast<const uint4*>(x + t * ts + o0));
-            b[j] = __ldg(reinterpret_cast<const uint4*>(x + t * ts + o1));
+            slot_groups<MODE, 8>(k, half, o0, o1);
+            B.a[j] = __ldg(reinterpret_cast<const uint4*>(x + t * ts + o0));
+            B.b[j] = __ldg(reinterpret_cast<const uint4*>(x + t * ts + o1));
+            B.at[j] = t << 8 | k;
         }
-    }
-    auto value = [&](int j, float(&fa)[8], float(&fb)[8]) {
-        widen16(a[j], fa);
-        widen16(b[j], fb);
-        const int t = at[j] >> 8;
-        slot_rotate<PAIRS>(x + t * ts, at[j] & 255, cs + t * 2 * P.r.half, half, inter, fa, fb);
+    };
+    // Visits this lane's slots, a batch in flight: f(token, first and second
+    // group's offset, their rotated values).  KEEP: the first batch, all there
+    // is in a decode step, stays in registers for every visit.
+    Batch first;
+    if constexpr (KEEP) load(lane, first);
+    auto visit = [&](auto&& f) {
+        Batch B;
+        if constexpr (KEEP) B = first;
+        for (int i = lane; i < total; i += 32 * kPageBatch) {
+            if (!KEEP || i != lane) load(i, B);
+#pragma unroll
+            for (int j = 0; j < kPageBatch; ++j) {
+                if (i + 32 * j >= total) break;
+                const int t = B.at[j] >> 8, k = B.at[j] & 255;
+                float fa[8], fb[8];
+                widen16(B.a[j], fa);
+                widen16(B.b[j], fb);
+                slot_rotate<MODE>(x + t * ts, k, cs + t * 2 * P.r.half, half, inter, fa, fb);
+                int o0, o1;
+                slot_groups<MODE, 8>(k, half, o0, o1);
+                f(t, o0, o1, fa, fb);
+            }
+        }
     };
     if constexpr (FMT == BSA_DTYPE_BF16) {
         uint16_t* c = static_cast<uint16_t*>(cache) + base;
-#pragma unroll
-        for (int j = 0; j < SL; ++j) {
-            if (at[j] < 0) continue;
-            float fa[8], fb[8];
-            value(j, fa, fb);
-            int o0, o1;
-            slot_groups<PAIRS, 8>(at[j] & 255, half, o0, o1);
-            uint16_t* d = c + (at[j] >> 8) * row;
+        visit([&](int t, int o0, int o1, const float(&fa)[8], const float(&fb)[8]) {
+            uint16_t* d = c + t * row;
             *reinterpret_cast<uint4*>(d + o0) = narrow16(fa);
             *reinterpret_cast<uint4*>(d + o1) = narrow16(fb);
-        }
+        });
     } else {
         using F = Code<FMT>;
         uint8_t* c = static_cast<uint8_t*>(cache) + base;
         float m = 0.f;
-#pragma unroll
-        for (int j = 0; j < SL; ++j) {
-            if (at[j] < 0) continue;
-            float fa[8], fb[8];
-            value(j, fa, fb);
+        visit([&](int, int, int, const float(&fa)[8], const float(&fb)[8]) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float u = fabsf(fa[e]), v = fabsf(fb[e]);
                 if (u <= 3.402823466e38f) m = fmaxf(m, u);      // finite values only
                 if (v <= 3.402823466e38f) m = fmaxf(m, v);
             }
-        }
+        });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         float s = fmaxf(old, F::scale(m));
@@ -192,28 +204,22 @@ __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t
             }
         }
         const float inv = 1.f / s;      // exact: s is a power of two
-#pragma unroll
-        for (int j = 0; j < SL; ++j) {
-            if (at[j] < 0) continue;
-            float fa[8], fb[8];
-            value(j, fa, fb);
-            int o0, o1;
-            slot_groups<PAIRS, 8>(at[j] & 255, half, o0, o1);
-            uint8_t* d = c + (at[j] >> 8) * row;
+        visit([&](int t, int o0, int o1, const float(&fa)[8], const float(&fb)[8]) {
+            uint8_t* d = c + t * row;
             *reinterpret_cast<uint2*>(d + o0) =
                 make_uint2(F::pack(fa[0] * inv, fa[1] * inv, fa[2] * inv, fa[3] * inv),
                            F::pack(fa[4] * inv, fa[5] * inv, fa[6] * inv, fa[7] * inv));
             *reinterpret_cast<uint2*>(d + o1) =
                 make_uint2(F::pack(fb[0] * inv, fb[1] * inv, fb[2] * inv, fb[3] * inv),
                            F::pack(fb[4] * inv, fb[5] * inv, fb[6] * inv, fb[7] * inv));
-        }
+        });
         __syncwarp();                    // every lane has read the old scale
         if (lane == 0) *sp = s;
     }
 }
 
-template <int FMT, int SL, bool PAIRS>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams P) {
+template <int FMT, RopeMode MODE, bool KEEP>
+__global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppendCtas) append_kernel(const AppendParams P) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ Row rows[kAppendTile];
     __shared__ Segment segs[kAppendTile];
@@ -275,15 +281,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
         const int64_t t = t0 + S.row;
         const float* c = cs + S.row * 2 * half;
         if (side == 0)
-            store_page<FMT, SL, PAIRS>(P, static_cast<const uint16_t*>(P.a.k) + t * P.a.k_token_stride + h * P.a.k_head_stride,
+            store_page<FMT, MODE, KEEP>(P, static_cast<const uint16_t*>(P.a.k) + t * P.a.k_token_stride + h * P.a.k_head_stride,
                                        P.a.k_token_stride, S, h, c, true, P.a.k_cache, P.a.k_scale);
         else
-            store_page<FMT, SL, true>(P, static_cast<const uint16_t*>(P.a.v) + t * P.a.v_token_stride + h * P.a.v_head_stride,
+            store_page<FMT, kSplit, KEEP>(P, static_cast<const uint16_t*>(P.a.v) + t * P.a.v_token_stride + h * P.a.v_head_stride,
                                       P.a.v_token_stride, S, h, c, false, P.a.v_cache, P.a.v_scale);
     }
     // ---- queries: slots of two groups ----
     if (P.a.q == nullptr) return;
-    constexpr int B = 4;                             // slots in flight per thread
+    constexpr int B = kQueryBatch;
     const int ks = D / 16, Hq = (int)P.a.Hq, total = nt * Hq * ks;
     const uint16_t* __restrict__ q = static_cast<const uint16_t*>(P.a.q) + t0 * P.a.q_token_stride;
     uint16_t* __restrict__ o = static_cast<uint16_t*>(P.a.q_out) + t0 * Hq * D;
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             if (i + j * kAppendThreads < total) {
                 const uint16_t* xr = q + t * P.a.q_token_stride + h * P.a.q_head_stride;
                 int o0, o1;
-                slot_groups<PAIRS, 8>(k, half, o0, o1);
+                slot_groups<MODE, 8>(k, half, o0, o1);
                 a[j] = __ldg(reinterpret_cast<const uint4*>(xr + o0));
                 b[j] = __ldg(reinterpret_cast<const uint4*>(xr + o1));
             }
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             const uint16_t* xr = q + tt[j] * P.a.q_token_stride + hh[j] * P.a.q_head_stride;
             uint16_t* orow = o + ((int64_t)tt[j] * Hq + hh[j]) * D;
             int o0, o1;
-            slot_groups<PAIRS, 8>(kk[j], half, o0, o1);
+            slot_groups<MODE, 8>(kk[j], half, o0, o1);
             if (rows[tt[j]].pos < 0) {
                 // padding: zeros, whatever the query holds
                 *reinterpret_cast<uint4*>(orow + o0) = make_uint4(0, 0, 0, 0);
@@ -337,27 +343,30 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             float fa[8], fb[8];
             widen16(a[j], fa);
             widen16(b[j], fb);
-            slot_rotate<PAIRS>(xr, kk[j], cs + tt[j] * 2 * half, half, P.r.interleaved != 0, fa, fb);
+            slot_rotate<MODE>(xr, kk[j], cs + tt[j] * 2 * half, half, P.r.interleaved != 0, fa, fb);
             *reinterpret_cast<uint4*>(orow + o0) = narrow16(fa);
             *reinterpret_cast<uint4*>(orow + o1) = narrow16(fb);
         }
     }
 }
 
-template <int FMT, int SL>
-cudaError_t launch_pairs(const AppendParams& P, unsigned grid, size_t smem, cudaStream_t st) {
-    // pairs within a slot when half a head's rotated part is whole groups
-    const bool pairs = !P.r.interleaved && P.r.half % 8 == 0;
-    auto kern = pairs ? append_kernel<FMT, SL, true> : append_kernel<FMT, SL, false>;
-    kern<<<grid, kAppendThreads, smem, st>>>(P);
+template <int FMT, bool KEEP>
+cudaError_t launch_mode(const AppendParams& P, unsigned grid, size_t smem, cudaStream_t st) {
+    const RopeMode mode = rope_mode(P.r, 8);
+    if (mode == kSplit) append_kernel<FMT, kSplit, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
+    else if (mode == kInterleaved) append_kernel<FMT, kInterleaved, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
+    else append_kernel<FMT, kAny, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
     return cudaGetLastError();
 }
 
+// With fewer rows per CTA than a page the CTAs do not fill the SMs: registers
+// are free to keep what was read.  In long calls four CTAs per SM that read
+// the tokens twice, the second time from L1, are faster than two that keep
+// them (two 8192-token prompts 60 against 63 us); in the production decode step
+// (256 rows) keeping takes 4.9 us, reading twice 5.4.
 template <int FMT>
-cudaError_t launch_width(const AppendParams& P, unsigned grid, size_t smem, cudaStream_t st) {
-    if (P.a.D <= 64) return launch_pairs<FMT, 2>(P, grid, smem, st);
-    if (P.a.D <= 128) return launch_pairs<FMT, 4>(P, grid, smem, st);
-    return launch_pairs<FMT, 8>(P, grid, smem, st);
+cudaError_t launch_format(const AppendParams& P, unsigned grid, size_t smem, cudaStream_t st) {
+    return P.tile < kAppendTile ? launch_mode<FMT, true>(P, grid, smem, st) : launch_mode<FMT, false>(P, grid, smem, st);
 }
 
 int check_append(const bsa_append_args_t* a) {
@@ -404,9 +413,9 @@ int launch_append(AppendParams& P, cudaStream_t st) {
     const size_t smem = (size_t)(tile + kPageRows - 1) * 2 * P.r.half * sizeof(float) + P.r.half * sizeof(unsigned long long);
     const unsigned grid = (unsigned)((P.a.T + tile - 1) / tile);
     cudaError_t e;
-    if (P.a.cache_dtype == BSA_DTYPE_BF16) e = launch_width<BSA_DTYPE_BF16>(P, grid, smem, st);
-    else if (P.a.cache_dtype == BSA_DTYPE_E4M3) e = launch_width<BSA_DTYPE_E4M3>(P, grid, smem, st);
-    else e = launch_width<BSA_DTYPE_E5M2>(P, grid, smem, st);
+    if (P.a.cache_dtype == BSA_DTYPE_BF16) e = launch_format<BSA_DTYPE_BF16>(P, grid, smem, st);
+    else if (P.a.cache_dtype == BSA_DTYPE_E4M3) e = launch_format<BSA_DTYPE_E4M3>(P, grid, smem, st);
+    else e = launch_format<BSA_DTYPE_E5M2>(P, grid, smem, st);
     return e == cudaSuccess ? BSA_OK : (int)e;
 }
 

@@ -4,12 +4,15 @@
 // One CTA takes a few tokens and all their heads.  The tokens' cosines and
 // sines are formed once in shared memory and serve every head.  The work is
 // bound by memory: one read and one write of each element.
-//  rope_slots_kernel   16-byte loads and stores, four slots of two groups in
-//                      flight per thread (rows and strides aligned to 16
-//                      bytes, D a multiple of two groups); partners within
+//  rope_slots_kernel   16-byte loads and stores (rows and strides aligned to
+//                      16 bytes, D a multiple of two groups); partners within
 //                      the slot, or single loads where half a head's pairs
 //                      are no multiple of a group (not in place then: a
-//                      partner may belong to another thread),
+//                      partner may belong to another thread).  Many small CTAs
+//                      hide the loads: ten of 128 threads per SM with a slot
+//                      each in flight take 67 us where four of 256 with two
+//                      slots take 73 and two with four slots 85 (24 heads of
+//                      128, 32760 tokens, bf16: 6.0 TB/s),
 //  rope_kernel         pair by pair: any alignment, in place.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -20,10 +23,10 @@
 namespace bsa {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeTable = 4096;    // cosines or sines per CTA at most (32 KB both)
-constexpr int kRopeTile = 16;       // tokens per CTA at most
-constexpr int kRopeBatch = 4;       // slots in flight per thread
+constexpr int kRopeTile = 4;        // tokens per CTA at most
+constexpr int kRopeCtas = 10;       // per SM
 
 struct RopeArgs {
     RopeParams r;
@@ -54,15 +57,14 @@ __device__ __forceinline__ void rope_table(const RopeArgs& A, int64_t t0, int nt
     __syncthreads();
 }
 
-template <bool PAIRS, typename E>
-__global__ void __launch_bounds__(kRopeThreads) rope_slots_kernel(const RopeArgs A) {
+template <RopeMode MODE, typename E>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_slots_kernel(const RopeArgs A) {
     constexpr int GE = 16 / (int)sizeof(E);
     extern __shared__ __align__(16) unsigned char smem[];
     float* cs = reinterpret_cast<float*>(smem);
     const int half = A.r.half;
     const int64_t t0 = (int64_t)blockIdx.x * A.tile;
     const int nt = (int)min((int64_t)A.tile, A.T - t0);
-    rope_table(A, t0, nt, cs, reinterpret_cast<unsigned long long*>(cs + A.tile * 2 * half));
     const E* x = static_cast<const E*>(A.x);
     E* out = static_cast<E*>(A.out);
     const int ks = A.D / (2 * GE);
@@ -72,46 +74,39 @@ __global__ void __launch_bounds__(kRopeThreads) rope_slots_kernel(const RopeArgs
     int h = th % A.H, t = th / A.H;
     const int dk = kRopeThreads % ks, dth = kRopeThreads / ks;
     const int dh = dth % A.H, dt = dth / A.H;
-    for (int i = threadIdx.x; i < total; i += kRopeBatch * kRopeThreads) {
-        uint4 a[kRopeBatch], b[kRopeBatch];
-        int kk[kRopeBatch], tt[kRopeBatch], hh[kRopeBatch];
-#pragma unroll
-        for (int j = 0; j < kRopeBatch; ++j) {
-            kk[j] = k;
-            tt[j] = t;
-            hh[j] = h;
-            if (i + j * kRopeThreads < total) {
-                const E* xr = x + (t0 + t) * A.xts + h * A.xhs;
-                int o0, o1;
-                slot_groups<PAIRS, GE>(k, half, o0, o1);
-                a[j] = *reinterpret_cast<const uint4*>(xr + o0);
-                b[j] = *reinterpret_cast<const uint4*>(xr + o1);
-            }
-            k += dk;
-            h += dh;
-            t += dt;
-            if (k >= ks) {
-                k -= ks;
-                ++h;
-            }
-            if (h >= A.H) {
-                h -= A.H;
-                ++t;
-            }
+    uint4 a, b;
+    auto load = [&]() {
+        const E* xr = x + (t0 + t) * A.xts + h * A.xhs;
+        int o0, o1;
+        slot_groups<MODE, GE>(k, half, o0, o1);
+        a = *reinterpret_cast<const uint4*>(xr + o0);
+        b = *reinterpret_cast<const uint4*>(xr + o1);
+    };
+    // the first slot is on its way while the table is formed
+    if ((int)threadIdx.x < total) load();
+    rope_table(A, t0, nt, cs, reinterpret_cast<unsigned long long*>(cs + A.tile * 2 * half));
+    for (int i = threadIdx.x; i < total; i += kRopeThreads) {
+        if (i != (int)threadIdx.x) load();
+        const E* xr = x + (t0 + t) * A.xts + h * A.xhs;
+        E* orow = out + (t0 + t) * A.ots + h * A.ohs;
+        float fa[GE], fb[GE];
+        widen16(a, fa);
+        widen16(b, fb);
+        slot_rotate<MODE>(xr, k, cs + t * 2 * half, half, A.r.interleaved != 0, fa, fb);
+        int o0, o1;
+        slot_groups<MODE, GE>(k, half, o0, o1);
+        *reinterpret_cast<uint4*>(orow + o0) = narrow16(fa);
+        *reinterpret_cast<uint4*>(orow + o1) = narrow16(fb);
+        k += dk;
+        h += dh;
+        t += dt;
+        if (k >= ks) {
+            k -= ks;
+            ++h;
         }
-#pragma unroll
-        for (int j = 0; j < kRopeBatch; ++j) {
-            if (i + j * kRopeThreads >= total) break;
-            const E* xr = x + (t0 + tt[j]) * A.xts + hh[j] * A.xhs;
-            E* orow = out + (t0 + tt[j]) * A.ots + hh[j] * A.ohs;
-            float fa[GE], fb[GE];
-            widen16(a[j], fa);
-            widen16(b[j], fb);
-            slot_rotate<PAIRS>(xr, kk[j], cs + tt[j] * 2 * half, half, A.r.interleaved != 0, fa, fb);
-            int o0, o1;
-            slot_groups<PAIRS, GE>(kk[j], half, o0, o1);
-            *reinterpret_cast<uint4*>(orow + o0) = narrow16(fa);
-            *reinterpret_cast<uint4*>(orow + o1) = narrow16(fb);
+        if (h >= A.H) {
+            h -= A.H;
+            ++t;
         }
     }
 }
@@ -164,10 +159,13 @@ void launch_rope(const RopeArgs& A, cudaStream_t st) {
     const bool wide = A.D % (2 * GE) == 0 &&
                       ((A.xts | A.xhs | A.ots | A.ohs) % GE) == 0 &&
                       ((reinterpret_cast<uintptr_t>(A.x) | reinterpret_cast<uintptr_t>(A.out)) & 15) == 0;
-    if (wide && !A.r.interleaved && half % GE == 0)
-        rope_slots_kernel<true, E><<<grid, kRopeThreads, smem, st>>>(A);
+    const RopeMode mode = rope_mode(A.r, GE);
+    if (wide && mode == kSplit)
+        rope_slots_kernel<kSplit, E><<<grid, kRopeThreads, smem, st>>>(A);
+    else if (wide && mode == kInterleaved)
+        rope_slots_kernel<kInterleaved, E><<<grid, kRopeThreads, smem, st>>>(A);
     else if (wide && (A.r.interleaved || A.x != A.out))
-        rope_slots_kernel<false, E><<<grid, kRopeThreads, smem, st>>>(A);
+        rope_slots_kernel<kAny, E><<<grid, kRopeThreads, smem, st>>>(A);
     else
         rope_kernel<E><<<grid, kRopeThreads, smem, st>>>(A);
 }

@@ -46,9 +46,16 @@ __device__ __forceinline__ int rope_axis(const RopeParams& R, int i) {
 }
 
 // ---- 16-byte groups ----------------------------------------------------------
-// The kernels move heads as slots of two 16-byte groups of GE elements.  With
-// pairs (i, i + half) and half a multiple of GE, a slot's two groups are the two
-// sides of GE pairs (PAIRS); otherwise they are neighbours.
+// The kernels move heads as slots of two 16-byte groups of GE elements.  Where
+// half (the pairs of a head) is a multiple of GE, a slot holds GE whole pairs:
+// its two groups are the two sides of pairs (i, i + half) (kSplit) or
+// neighbours with pairs (2i, 2i + 1) (kInterleaved).  Otherwise (kAny) the groups
+// are neighbours and each element looks for its partner.
+enum RopeMode { kSplit = 0, kInterleaved = 1, kAny = 2 };
+inline RopeMode rope_mode(const RopeParams& R, int ge) {
+    if (R.half % ge != 0) return kAny;
+    return R.interleaved ? kInterleaved : kSplit;
+}
 __device__ __forceinline__ void widen16(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -86,13 +93,13 @@ __device__ __forceinline__ float turn_second(float a, float b, float c, float s)
 }
 
 // element offsets of slot k's two groups
-template <bool PAIRS, int GE>
+template <RopeMode MODE, int GE>
 __device__ __forceinline__ void slot_groups(int k, int half, int& o0, int& o1) {
-    if (PAIRS && GE * k < half) {
+    if (MODE == kSplit && GE * k < half) {
         o0 = GE * k;
         o1 = o0 + half;
     } else {
-        o0 = 2 * GE * k;                      // PAIRS: half / GE slots cover 2 half elements
+        o0 = 2 * GE * k;                      // kSplit: half / GE slots cover 2 half elements
         o1 = o0 + GE;
     }
 }
@@ -100,11 +107,11 @@ __device__ __forceinline__ void slot_groups(int k, int half, int& o0, int& o1) {
 // Rotates slot k of a head's row at `x` (its groups' values in a and b; x is
 // read again only for partners outside the slot).  cs: the row's cosines, then
 // its sines at cs + half.
-template <bool PAIRS, typename E, int GE>
+template <RopeMode MODE, typename E, int GE>
 __device__ __forceinline__ void slot_rotate(const E* x, int k, const float* cs, int half, bool interleaved,
                                             float (&a)[GE], float (&b)[GE]) {
     const float* sn = cs + half;
-    if constexpr (PAIRS) {
+    if constexpr (MODE != kAny) {
         if (GE * k >= half) return;
 #pragma unroll
         for (int i = 0; i < GE; i += 4) {
@@ -113,9 +120,14 @@ __device__ __forceinline__ void slot_rotate(const E* x, int k, const float* cs, 
             const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float u = a[i + j], v = b[i + j];
-                a[i + j] = turn_first(u, v, cc[j], ss[j]);
-                b[i + j] = turn_second(u, v, cc[j], ss[j]);
+                // pair i + j: the groups' elements i + j, or elements 2 (i + j) and the next
+                // of the groups in a row
+                const int e = 2 * (i + j);
+                float& first = MODE == kSplit ? a[i + j] : (e < GE ? a[e % GE] : b[e % GE]);
+                float& second = MODE == kSplit ? b[i + j] : (e < GE ? a[e % GE + 1] : b[e % GE + 1]);
+                const float u = first, v = second;
+                first = turn_first(u, v, cc[j], ss[j]);
+                second = turn_second(u, v, cc[j], ss[j]);
             }
         }
     } else if (interleaved) {
