@@ -12,6 +12,9 @@ PyTorch supplies device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import operator
 import os
 import threading
 
@@ -555,48 +558,25 @@ def bsa_read_status(clear: bool = True, device: torch.device | None = None) -> i
     return int(out.value)
 
 
-_CACHE_DTYPES = {torch.bfloat16: BSA_DTYPE_BF16, torch.float8_e4m3fn: BSA_DTYPE_E4M3,
-                 torch.float8_e5m2: BSA_DTYPE_E5M2}
+_binding_module = None
 
 
-def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, T: int | None,
-           D: int | None):
-    """A [T, heads, D] CUDA tensor whose head rows are contiguous; any token
-    and head strides, which are returned."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or t.dtype != dtype \
-            or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor [T, heads, D] on {device}")
-    shape, stride = t.shape, t.stride()
-    if (T is not None and shape[0] != T) or (D is not None and shape[2] != D):
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{T}, heads, {D}]")
-    if shape[2] > 1 and stride[2] != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    return stride[0], stride[1]
-
-
-def _rope_args(T: int, device: torch.device, positions: torch.Tensor | None,
-               inv_freq: torch.Tensor | None, freq_axis: torch.Tensor | None):
-    """(positions, axes, inv_freq, freq_axis, rot_dim) as the C calls take them."""
-    axes, half = 1, 0
-    if inv_freq is not None:
-        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float32 \
-                or inv_freq.device != device or inv_freq.dim() != 1 \
-                or not inv_freq.is_contiguous():
-            raise ValueError(f"inv_freq must be a contiguous fp32 tensor [rot_dim / 2] on {device}")
-        half = inv_freq.shape[0]
-    if positions is not None:
-        if isinstance(positions, torch.Tensor) and positions.dim() == 2:
-            axes = positions.shape[0]
-            _dev_i32(positions, "positions", device, (axes, T))
-        else:
-            _dev_i32(positions, "positions", device, (T,))
-    if freq_axis is not None:
-        _dev_i32(freq_axis, "freq_axis", device, (half,))
-    elif axes > 1 and half:
-        raise ValueError("freq_axis is needed with several position axes")
-    return (0 if positions is None else positions.data_ptr(), axes,
-            0 if inv_freq is None else inv_freq.data_ptr(),
-            0 if freq_axis is None else freq_axis.data_ptr(), 2 * half)
+def _binding():
+    """The module that checks and marshals the cache operators' arguments."""
+    global _binding_module
+    if _binding_module is None:
+        lib()
+        path = _build.BINDING_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m block_sparse_attention_topk_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("bsa_binding", path)
+        spec = importlib.util.spec_from_file_location("bsa_binding", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.setup(BsaError, torch._C._cuda_getCurrentRawStream, _workspace)
+        _binding_module = module
+    return _binding_module
 
 
 def bsa_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -608,85 +588,7 @@ def bsa_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     with several axes).  Returns out, by default a new contiguous tensor; x
     itself rotates in place.  ``inverse`` turns back: applied to the gradient
     of the output it gives the gradient of x."""
-    dt = _score_dtype(x) if isinstance(x, torch.Tensor) else None
-    dev = x.device
-    xs = _heads(x, "x", x.dtype, dev, None, None)
-    T, H, D = x.shape
-    if positions is None or inv_freq is None:
-        raise ValueError("positions and inv_freq are needed")
-    pos, axes, inv, axis, rot = _rope_args(T, dev, positions, inv_freq, freq_axis)
-    if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
-    os_ = _heads(out, "out", x.dtype, dev, T, D)
-    if out.shape[1] != H:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, H, D)}")
-    _call("bsa_rope", dev, x.data_ptr(), dt, T, H, D, *xs, pos, axes, inv, axis, rot,
-          (BSA_ROPE_INTERLEAVED if interleaved else 0) | (BSA_ROPE_INVERSE if inverse else 0),
-          out.data_ptr(), *os_, _stream(dev))
-    return out
-
-
-def _whole(t, dtype: torch.dtype, device: torch.device, shape: tuple) -> bool:
-    """Whether t is a contiguous tensor of this type, place and shape."""
-    return isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype \
-        and t.device == device and t.is_contiguous()
-
-
-def _q8_caches(k_cache, v_cache, k_scale, v_scale, device, H, D):
-    """(cache dtype code, num_pages) of a checked pair of caches and scales."""
-    dtype = getattr(k_cache, "dtype", None)
-    code = _CACHE_DTYPES.get(dtype)
-    if code is None:
-        raise ValueError("k_cache must be bfloat16, float8_e4m3fn or float8_e5m2")
-    n = k_cache.shape[0] if k_cache.dim() == 4 else -1
-    shape = (n, PAGES_PER_SPARSE_BLOCK * 2, H, D)
-    if not _whole(k_cache, dtype, device, shape) or not _whole(v_cache, dtype, device, shape):
-        raise ValueError(f"k_cache and v_cache must be contiguous {dtype} tensors [num_pages, "
-                         f"{shape[1]}, {H}, {D}] on {device} with one page count")
-    if code == BSA_DTYPE_BF16:
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("k_scale and v_scale must be None with a bfloat16 cache")
-    elif not _whole(k_scale, torch.float32, device, (n, H)) \
-            or not _whole(v_scale, torch.float32, device, (n, H)):
-        raise ValueError(f"k_scale and v_scale must be contiguous fp32 tensors [{n}, {H}] on "
-                         f"{device}")
-    return code, n
-
-
-def _append(k, v, k_cache, v_cache, block_table, num_reqs, q, inv_freq, positions, freq_axis,
-            interleaved, k_scale, v_scale, q_out):
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be a bf16 CUDA tensor [T, H, D]")
-    dev = k.device
-    ks = _heads(k, "k", torch.bfloat16, dev, None, None)
-    T, H, D = k.shape
-    vs = _heads(v, "v", torch.bfloat16, dev, T, D)
-    if v.shape[1] != H:
-        raise ValueError(f"v has {v.shape[1]} heads, expected {H}")
-    Hq, qs = 0, (0, 0)
-    if q is not None:
-        qs = _heads(q, "q", torch.bfloat16, dev, T, D)
-        Hq = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        if not _whole(q_out, torch.bfloat16, dev, (T, Hq, D)):
-            raise ValueError(f"q_out must be a contiguous bf16 tensor [{T}, {Hq}, {D}] on {dev}")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    code, pages = _q8_caches(k_cache, v_cache, k_scale, v_scale, dev, H, D)
-    _dev_i32(block_table, "block_table", dev)
-    if block_table.dim() != 2 or block_table.shape[0] != num_reqs:
-        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected "
-                         f"[{num_reqs}, max_blocks]")
-    pos, axes, inv, axis, rot = _rope_args(T, dev, positions, inv_freq, freq_axis)
-    args = AppendArgs(
-        k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(), T, H, Hq, D, *ks, *vs,
-        *qs, None if q is None else q_out.data_ptr(), pos, inv, axis, axes, rot,
-        BSA_ROPE_INTERLEAVED if interleaved else 0, code, k_cache.data_ptr(), v_cache.data_ptr(),
-        pages, None if k_scale is None else k_scale.data_ptr(),
-        None if v_scale is None else v_scale.data_ptr(), block_table.data_ptr(), num_reqs,
-        block_table.shape[1])
-    return dev, args, q_out
+    return _binding().rope(x, positions, inv_freq, freq_axis, interleaved, inverse, out)
 
 
 def bsa_append_kv_decode(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -707,15 +609,9 @@ def bsa_append_kv_decode(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
     appended tokens counted.  Rotary arguments as for bsa_rope; positions
     defaults to the position in the sequence, inv_freq None rotates nothing.
     Returns q_out bf16 [T, Hq, D] (None without q)."""
-    _dev_i32(seq_lens, "seq_lens")
-    if seq_lens.dim() != 1:
-        raise ValueError("seq_lens must be 1-D [num_reqs]")
-    dev, args, q_out = _append(k, v, k_cache, v_cache, block_table, seq_lens.shape[0], q, inv_freq,
-                               positions, freq_axis, interleaved, k_scale, v_scale, q_out)
-    if seq_lens.device != dev:
-        raise ValueError(f"seq_lens is on {seq_lens.device}, expected {dev}")
-    _call("bsa_append_kv_decode", dev, args, seq_lens.data_ptr(), decode_query_len, _stream(dev))
-    return q_out
+    return _binding().append(k, v, k_cache, v_cache, block_table, seq_lens,
+                             operator.index(decode_query_len), q, inv_freq, positions, freq_axis,
+                             interleaved, k_scale, v_scale, q_out)
 
 
 def bsa_append_kv_varlen(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -730,25 +626,17 @@ def bsa_append_kv_varlen(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
     """bsa_append_kv_decode for rows of varying count: sequence i owns rows
     [cu_seqlens_q[i], cu_seqlens_q[i + 1]) and its j-th token sits at position
     prefix_lens[i] + j (int32 [num_seqs + 1] and [num_seqs])."""
-    _dev_i32(prefix_lens, "prefix_lens")
-    if prefix_lens.dim() != 1:
-        raise ValueError("prefix_lens must be 1-D [num_seqs]")
-    N = prefix_lens.shape[0]
-    dev, args, q_out = _append(k, v, k_cache, v_cache, block_table, N, q, inv_freq, positions,
-                               freq_axis, interleaved, k_scale, v_scale, q_out)
-    if prefix_lens.device != dev:
-        raise ValueError(f"prefix_lens is on {prefix_lens.device}, expected {dev}")
-    _dev_i32(cu_seqlens_q, "cu_seqlens_q", dev, (N + 1,))
-    _call("bsa_append_kv_varlen", dev, args, cu_seqlens_q.data_ptr(), prefix_lens.data_ptr(),
-          _stream(dev))
-    return q_out
+    if not isinstance(cu_seqlens_q, torch.Tensor):
+        raise ValueError("cu_seqlens_q must be a tensor")
+    return _binding().append(k, v, k_cache, v_cache, block_table, prefix_lens, cu_seqlens_q, q,
+                             inv_freq, positions, freq_axis, interleaved, k_scale, v_scale, q_out)
 
 
 def bsa_attention_q8_workspace_bytes(T: int, H: int, G: int, D: int, K: int,
                                      device: torch.device | None = None) -> int:
     """Workspace bytes of bsa_sparse_decode_attention_q8 on `device` (default:
     the current one)."""
-    if device is None or device.index == torch.cuda.current_device():
+    if device is None:
         return int(lib().bsa_attention_q8_workspace_bytes(T, H, G, D, K))
     with torch.cuda.device(device):
         return int(lib().bsa_attention_q8_workspace_bytes(T, H, G, D, K))
@@ -764,29 +652,5 @@ def bsa_sparse_decode_attention_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     [num_pages, 16, H, D] with fp32 k_scale, v_scale [num_pages, H];
     sparse_bt int32 [T, H, K*8], sparse_ctx int32 [T, H]; returns bf16
     [T, H, G, D].  The scale defaults to 1 / sqrt(D)."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4 \
-            or q.dtype != torch.bfloat16 or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 CUDA tensor [T, H, G, D]")
-    dev = q.device
-    T, H, G, D = q.shape
-    code, pages = _q8_caches(k_cache, v_cache, k_scale, v_scale, dev, H, D)
-    if code == BSA_DTYPE_BF16:
-        raise ValueError("the caches must be float8_e4m3fn or float8_e5m2")
-    _dev_i32(sparse_bt, "sparse_bt", dev)
-    width = sparse_bt.shape[2] if sparse_bt.dim() == 3 else 1
-    if width % PAGES_PER_SPARSE_BLOCK or sparse_bt.shape != (T, H, width):
-        raise ValueError(f"sparse_bt must be [{T}, {H}, K*8]")
-    K = width // PAGES_PER_SPARSE_BLOCK
-    _dev_i32(sparse_ctx, "sparse_ctx", dev, (T, H))
-    if out is None:
-        out = torch.empty((T, H, G, D), dtype=torch.bfloat16, device=dev)
-    elif not _whole(out, torch.bfloat16, dev, (T, H, G, D)):
-        raise ValueError(f"out must be a contiguous bf16 tensor [{T}, {H}, {G}, {D}] on {dev}")
-    need = bsa_attention_q8_workspace_bytes(T, H, G, D, K, dev)
-    workspace, wbytes = _workspace_arg(workspace, dev, need)
-    _call("bsa_sparse_decode_attention_q8", dev, q.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), code, k_scale.data_ptr(), v_scale.data_ptr(), pages,
-          sparse_bt.data_ptr(), sparse_ctx.data_ptr(), T, H, G, D, K,
-          D ** -0.5 if scale is None else scale, out.data_ptr(),
-          0 if workspace is None else workspace.data_ptr(), wbytes, _stream(dev))
-    return out
+    return _binding().attention_q8(q, k_cache, v_cache, k_scale, v_scale, sparse_bt, sparse_ctx,
+                                   scale, out, workspace)

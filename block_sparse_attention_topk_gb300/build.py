@@ -3,7 +3,9 @@
 The library is compiled for sm_103a only (GB300), from the sources in
 ``csrc/``, with nvcc.  Translation units compile in parallel; the link pulls
 in the static CUDA runtime so the library loads without a CUDA runtime on the
-loader path.  Run ``python -m block_sparse_attention_topk_gb300.build`` or
+loader path.  Beside it, ``_build/bsa_binding.so`` is the Python module that
+checks and marshals the arguments of the cache operators (host compiler,
+PyTorch's headers).  Run ``python -m block_sparse_attention_topk_gb300.build`` or
 call ``build()``.
 """
 from __future__ import annotations
@@ -13,6 +15,7 @@ import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +26,8 @@ LIB_NAME = f"libbsa_topk_{platform.machine()}.so"
 LIB_PATH = os.path.join(BUILD, LIB_NAME)
 SOURCES = ["bsa_select.cu", "bsa_table.cu", "bsa_capi.cu", "bsa_noalloc.cu", "bsa_attention.cu",
            "bsa_rope.cu", "bsa_append.cu", "bsa_attention_q8.cu"]
+BINDING = "bsa_binding.cpp"
+BINDING_PATH = os.path.join(BUILD, f"bsa_binding_{platform.machine()}.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,7 +39,7 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES]
+    files = [os.path.join(CSRC, s) for s in SOURCES + [BINDING]]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     files.append(os.path.join(INCLUDE, "bsa_topk.h"))
     files.append(os.path.abspath(__file__))
@@ -42,9 +47,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -56,6 +61,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                      "-I", INCLUDE, *extra_flags]
     objs = []
+
+    def compile_binding():
+        import torch
+        torch_dir = os.path.dirname(torch.__file__)
+        obj = os.path.join(BUILD, f"bsa_binding_{platform.machine()}.o")
+        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-c",
+               "-D_GLIBCXX_USE_CXX11_ABI=" + str(int(torch._C._GLIBCXX_USE_CXX11_ABI)),
+               "-isystem", os.path.join(torch_dir, "include"),
+               "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, BINDING), "-o", obj]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"the host compiler failed on {BINDING}:\n{res.stdout}\n{res.stderr}")
+        return obj, os.path.join(torch_dir, "lib")
 
     def compile_one(src):
         obj = os.path.join(BUILD, f"{os.path.splitext(src)[0]}_{platform.machine()}.o")
@@ -69,14 +88,24 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(res.stdout, res.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        binding = pool.submit(compile_binding)
         objs = list(pool.map(compile_one, SOURCES))
+        binding_obj, torch_lib = binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-shared", "-o", tmp, binding_obj, "-L", BUILD,
+           f"-l:{LIB_NAME}", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"linking {BINDING} failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING_PATH)
     return LIB_PATH
 
 

@@ -96,62 +96,62 @@ def test_attention_q8_refusals(bsa, bad, code):
     assert _attend(bsa.lib(), **bad) == code
 
 
-def test_binding_refuses_before_any_launch(bsa, monkeypatch):
-    """Wrong shapes, types, devices and strides raise ValueError and reach no
-    entry point (a recorder stands in for the library)."""
-    calls = []
+def test_binding_refuses_before_any_launch(bsa):
+    """Wrong shapes, types, devices and strides raise ValueError naming the
+    argument; the arguments that pass end at the check that they are on a GPU
+    (CPU tensors stand in for device tensors, so nothing can be launched)."""
 
-    class Recorder:
-        def __getattr__(self, name):
-            def rec(*a):
-                calls.append(name)
-                return 0
-            return rec
+    def t(*shape, dtype=torch.bfloat16):
+        return torch.zeros(shape, dtype=dtype)
 
-    monkeypatch.setattr(bsa, "lib", lambda: Recorder())
-    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda self: True))
+    def refuses(fn, good, bad, match):
+        with pytest.raises(ValueError, match="CUDA device"):
+            fn(**good)
+        for name, value in bad:
+            with pytest.raises((ValueError, TypeError), match=match.get(name, name)):
+                fn(**{**good, name: value})
 
-    def meta(*shape, dtype=torch.bfloat16):
-        return torch.empty(shape, dtype=dtype, device="meta")
-
-    i32, f8 = torch.int32, torch.float8_e4m3fn
-    x, pos, inv = meta(5, 3, 64), meta(5, dtype=i32), meta(32, dtype=torch.float32)
-    for bad in (dict(x=meta(5, 64)), dict(x=meta(5, 3, 64, dtype=torch.float16)),
-                dict(x=meta(5, 64, 3).transpose(1, 2)), dict(positions=meta(4, dtype=i32)),
-                dict(positions=meta(5, dtype=torch.int64)), dict(positions=meta(3, 5, dtype=i32)),
-                dict(positions=None), dict(inv_freq=None), dict(inv_freq=meta(32, dtype=torch.float64)),
-                dict(freq_axis=meta(31, dtype=i32)), dict(out=meta(5, 2, 64)),
-                dict(out=meta(5, 3, 64, dtype=torch.float32))):
-        with pytest.raises(ValueError):
-            bsa.bsa_rope(**{**dict(x=x, positions=pos, inv_freq=inv), **bad})
-    good = dict(k=meta(6, 2, 64), v=meta(6, 2, 64), k_cache=meta(24, 16, 2, 64, dtype=f8),
-                v_cache=meta(24, 16, 2, 64, dtype=f8), block_table=meta(3, 4, dtype=i32),
-                q=meta(6, 8, 64), q_out=meta(6, 8, 64), inv_freq=inv,
-                k_scale=meta(24, 2, dtype=torch.float32), v_scale=meta(24, 2, dtype=torch.float32))
-    for bad in (dict(k=meta(6, 2, 64, dtype=torch.float32)), dict(v=meta(6, 3, 64)), dict(v=meta(5, 2, 64)),
-                dict(q=meta(6, 8, 32)), dict(q_out=meta(6, 7, 64)), dict(q=None),
-                dict(k_cache=meta(24, 16, 2, 64)), dict(k_cache=meta(24, 8, 2, 64, dtype=f8)),
-                dict(v_cache=meta(23, 16, 2, 64, dtype=f8)), dict(k_scale=None),
-                dict(v_scale=meta(24, 1, dtype=torch.float32)), dict(block_table=meta(2, 4, dtype=i32)),
-                dict(block_table=meta(3, 4)), dict(positions=meta(2, 6, dtype=i32))):
-        args = {**good, **bad}
-        with pytest.raises(ValueError):
-            bsa.bsa_append_kv_decode(seq_lens=meta(3, dtype=i32), decode_query_len=2, **args)
-        with pytest.raises(ValueError):
-            bsa.bsa_append_kv_varlen(cu_seqlens_q=meta(4, dtype=i32), prefix_lens=meta(3, dtype=i32), **args)
-    with pytest.raises(ValueError):
-        bsa.bsa_append_kv_varlen(cu_seqlens_q=meta(3, dtype=i32), prefix_lens=meta(3, dtype=i32), **good)
-    with pytest.raises(ValueError):
-        bsa.bsa_append_kv_decode(seq_lens=meta(3, 1, dtype=i32), decode_query_len=2, **good)
-    good = dict(q=meta(6, 2, 4, 64), k_cache=good["k_cache"], v_cache=good["v_cache"],
-                k_scale=good["k_scale"], v_scale=good["v_scale"], sparse_bt=meta(6, 2, 32, dtype=i32),
-                sparse_ctx=meta(6, 2, dtype=i32))
-    for bad in (dict(q=meta(6, 2, 64)), dict(q=meta(6, 2, 4, 64, dtype=torch.float32)),
-                dict(k_cache=meta(24, 16, 2, 64)), dict(v_cache=meta(24, 16, 2, 32, dtype=f8)),
-                dict(v_cache=meta(24, 16, 2, 64, dtype=torch.float8_e5m2)),
-                dict(k_scale=None), dict(v_scale=meta(23, 2, dtype=torch.float32)),
-                dict(sparse_bt=meta(6, 2, 30, dtype=i32)), dict(sparse_ctx=meta(6, dtype=i32)),
-                dict(out=meta(6, 2, 4, 32)), dict(out=meta(6, 2, 4, 64, dtype=torch.float32))):
-        with pytest.raises(ValueError):
-            bsa.bsa_sparse_decode_attention_q8(**{**good, **bad})
-    assert calls == [], calls
+    i32, f32, f8 = torch.int32, torch.float32, torch.float8_e4m3fn
+    meta = torch.empty((5,), dtype=i32, device="meta")
+    refuses(bsa.bsa_rope, dict(x=t(5, 3, 64), positions=t(5, dtype=i32), inv_freq=t(32, dtype=f32)), [
+        ("x", t(5, 64)), ("x", t(5, 3, 64, dtype=torch.float16)), ("x", t(5, 64, 3).transpose(1, 2)),
+        ("x", None), ("x", 3), ("positions", t(4, dtype=i32)), ("positions", t(5, dtype=torch.int64)),
+        ("positions", t(3, 4, dtype=i32)), ("positions", t(1, 1, 5, dtype=i32)), ("positions", None),
+        ("positions", t(10, dtype=i32)[::2]), ("positions", meta), ("inv_freq", None),
+        ("inv_freq", t(32, dtype=torch.float64)), ("inv_freq", t(32, 1, dtype=f32)),
+        ("freq_axis", t(31, dtype=i32)), ("out", t(5, 2, 64)), ("out", t(5, 3, 64, dtype=f32)),
+    ], {})
+    with pytest.raises(ValueError, match="freq_axis"):
+        bsa.bsa_rope(t(5, 3, 64), t(2, 5, dtype=i32), t(32, dtype=f32))
+    good = dict(k=t(6, 2, 64), v=t(6, 2, 64), k_cache=t(24, 16, 2, 64, dtype=f8),
+                v_cache=t(24, 16, 2, 64, dtype=f8), block_table=t(3, 4, dtype=i32), q=t(6, 8, 64),
+                q_out=t(6, 8, 64), inv_freq=t(32, dtype=f32), k_scale=t(24, 2, dtype=f32),
+                v_scale=t(24, 2, dtype=f32))
+    bad = [("k", t(6, 2, 64, dtype=f32)), ("v", t(6, 3, 64)), ("v", t(5, 2, 64)), ("q", t(6, 8, 32)),
+           ("q_out", t(6, 7, 64)), ("q", None), ("k_cache", t(24, 8, 2, 64, dtype=f8)),
+           ("k_cache", t(24, 16, 2, 64, dtype=f32)), ("v_cache", t(23, 16, 2, 64, dtype=f8)),
+           ("v_cache", t(24, 16, 2, 64)), ("k_scale", None), ("v_scale", t(24, 1, dtype=f32)),
+           ("block_table", t(2, 4, dtype=i32)), ("block_table", t(3, 4)), ("positions", t(2, 5, dtype=i32)),
+           ("positions", meta)]
+    match = {"k_cache": "cache", "q": "q"}
+    refuses(bsa.bsa_append_kv_decode, dict(good, seq_lens=t(3, dtype=i32), decode_query_len=2),
+            bad + [("seq_lens", t(3, 1, dtype=i32)), ("seq_lens", None), ("decode_query_len", 2.0)],
+            dict(match, decode_query_len="float"))
+    refuses(bsa.bsa_append_kv_varlen, dict(good, cu_seqlens_q=t(4, dtype=i32), prefix_lens=t(3, dtype=i32)),
+            bad + [("cu_seqlens_q", t(3, dtype=i32)), ("cu_seqlens_q", 4), ("prefix_lens", t(3))], match)
+    with pytest.raises(ValueError, match="bfloat16 cache"):
+        bsa.bsa_append_kv_decode(**dict(good, k_cache=t(24, 16, 2, 64), v_cache=t(24, 16, 2, 64)),
+                                 seq_lens=t(3, dtype=i32), decode_query_len=2)
+    refuses(bsa.bsa_sparse_decode_attention_q8,
+            dict(q=t(6, 2, 4, 64), k_cache=good["k_cache"], v_cache=good["v_cache"], k_scale=good["k_scale"],
+                 v_scale=good["v_scale"], sparse_bt=t(6, 2, 32, dtype=i32), sparse_ctx=t(6, 2, dtype=i32)),
+            [("q", t(6, 2, 64)), ("q", t(6, 2, 4, 64, dtype=f32)), ("q", t(6, 2, 64, 4).transpose(2, 3)),
+             ("k_cache", t(24, 16, 2, 64)), ("v_cache", t(24, 16, 2, 32, dtype=f8)),
+             ("v_cache", t(24, 16, 2, 64, dtype=torch.float8_e5m2)), ("k_scale", None),
+             ("v_scale", t(23, 2, dtype=f32)), ("sparse_bt", t(6, 2, 30, dtype=i32)),
+             ("sparse_bt", t(6, 1, 32, dtype=i32)), ("sparse_ctx", t(6, dtype=i32)), ("out", t(6, 2, 4, 32)),
+             ("out", t(6, 2, 4, 64, dtype=f32)), ("scale", "x")], dict(match, scale="number"))
+    bf = t(24, 16, 2, 64)
+    with pytest.raises(ValueError, match="float8"):
+        bsa.bsa_sparse_decode_attention_q8(t(6, 2, 4, 64), bf, bf, None, None, t(6, 2, 32, dtype=i32),
+                                           t(6, 2, dtype=i32))
