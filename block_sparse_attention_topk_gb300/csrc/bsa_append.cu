@@ -118,7 +118,6 @@ __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t
                                            float* scales) {
     const int lane = threadIdx.x & 31;
     const int D = (int)P.a.D, ks = D / 16, half = rotate ? P.r.half : 0;
-    const bool inter = P.r.interleaved != 0;
     const int64_t row = P.a.H * D;
     const int64_t base = S.page * kPageRows * row + (int64_t)h * D + S.off * row;
     float* sp = FMT == BSA_DTYPE_BF16 ? nullptr : scales + S.page * P.a.H + h;
@@ -158,7 +157,7 @@ __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t
                 float fa[8], fb[8];
                 widen16(B.a[j], fa);
                 widen16(B.b[j], fb);
-                slot_rotate<MODE>(x + t * ts, k, cs + t * 2 * P.r.half, half, inter, fa, fb);
+                slot_rotate<MODE>(x + t * ts, k, cs + t * 2 * rope_pad(P.r.half), half, fa, fb);
                 int o0, o1;
                 slot_groups<MODE, 8>(k, half, o0, o1);
                 f(t, o0, o1, fa, fb);
@@ -225,8 +224,8 @@ __global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppe
     __shared__ Segment segs[kAppendTile];
     __shared__ int nseg, more;
     const int half = P.r.half, D = (int)P.a.D, tid = threadIdx.x;
-    float* cs = reinterpret_cast<float*>(smem);      // [tile + 15][2 half]
-    unsigned long long* steps = reinterpret_cast<unsigned long long*>(cs + (P.tile + kPageRows - 1) * 2 * half);
+    float* cs = reinterpret_cast<float*>(smem);      // [tile + 15][2 rope_pad(half)]
+    unsigned long long* steps = reinterpret_cast<unsigned long long*>(cs + (P.tile + kPageRows - 1) * 2 * rope_pad(half));
     const int64_t t0 = (int64_t)blockIdx.x * P.tile;
     const int nt = (int)min((int64_t)P.tile, P.a.T - t0);
     if (tid == 0) nseg = more = 0;
@@ -268,8 +267,8 @@ __global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppe
             p = t < nt ? rows[t].pos : rows[nt - 1].pos + (t - nt + 1);
         }
         const float2 c = rope_turn(p, steps[f]);
-        cs[t * 2 * half + f] = c.x;
-        cs[t * 2 * half + half + f] = P.r.inverse ? -c.y : c.y;
+        cs[t * 2 * rope_pad(half) + f] = c.x;
+        cs[(t * 2 + 1) * rope_pad(half) + f] = P.r.inverse ? -c.y : c.y;
     }
     __syncthreads();
     // ---- pages: a warp per page, head and side ----
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppe
         const int i = sh / (int)P.a.H, h = sh - i * (int)P.a.H;
         const Segment S = segs[i];
         const int64_t t = t0 + S.row;
-        const float* c = cs + S.row * 2 * half;
+        const float* c = cs + S.row * 2 * rope_pad(half);
         if (side == 0)
             store_page<FMT, MODE, KEEP>(P, static_cast<const uint16_t*>(P.a.k) + t * P.a.k_token_stride + h * P.a.k_head_stride,
                                        P.a.k_token_stride, S, h, c, true, P.a.k_cache, P.a.k_scale);
@@ -343,7 +342,7 @@ __global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppe
             float fa[8], fb[8];
             widen16(a[j], fa);
             widen16(b[j], fb);
-            slot_rotate<MODE>(xr, kk[j], cs + tt[j] * 2 * half, half, P.r.interleaved != 0, fa, fb);
+            slot_rotate<MODE>(xr, kk[j], cs + tt[j] * 2 * rope_pad(half), half, fa, fb);
             *reinterpret_cast<uint4*>(orow + o0) = narrow16(fa);
             *reinterpret_cast<uint4*>(orow + o1) = narrow16(fb);
         }
@@ -355,7 +354,7 @@ cudaError_t launch_mode(const AppendParams& P, unsigned grid, size_t smem, cudaS
     const RopeMode mode = rope_mode(P.r, 8);
     if (mode == kSplit) append_kernel<FMT, kSplit, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
     else if (mode == kInterleaved) append_kernel<FMT, kInterleaved, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
-    else append_kernel<FMT, kAny, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
+    else append_kernel<FMT, kSplitAny, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
     return cudaGetLastError();
 }
 
@@ -410,7 +409,7 @@ int launch_append(AppendParams& P, cudaStream_t st) {
     const int64_t want = 2 * (int64_t)device_sm_count();
     while (tile > 1 && (P.a.T + tile - 1) / tile < want) tile /= 2;
     P.tile = tile;
-    const size_t smem = (size_t)(tile + kPageRows - 1) * 2 * P.r.half * sizeof(float) + P.r.half * sizeof(unsigned long long);
+    const size_t smem = (size_t)(tile + kPageRows - 1) * 2 * rope_pad(P.r.half) * sizeof(float) + P.r.half * sizeof(unsigned long long);
     const unsigned grid = (unsigned)((P.a.T + tile - 1) / tile);
     cudaError_t e;
     if (P.a.cache_dtype == BSA_DTYPE_BF16) e = launch_format<BSA_DTYPE_BF16>(P, grid, smem, st);

@@ -5,10 +5,9 @@
 // sines are formed once in shared memory and serve every head.  The work is
 // bound by memory: one read and one write of each element.
 //  rope_slots_kernel   16-byte loads and stores (rows and strides aligned to
-//                      16 bytes, D a multiple of two groups); partners within
-//                      the slot, or single loads where half a head's pairs
-//                      are no multiple of a group (not in place then: a
-//                      partner may belong to another thread).  Many small CTAs
+//                      16 bytes, D a multiple of two groups); not in place
+//                      where a partner may belong to another thread
+//                      (kSplitAny).  Many small CTAs
 //                      hide the loads: ten of 128 threads per SM with a slot
 //                      each in flight take 67 us where four of 256 with two
 //                      slots take 73 and two with four slots 85 (24 heads of
@@ -25,7 +24,8 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeTable = 4096;    // cosines or sines per CTA at most (32 KB both)
-constexpr int kRopeTile = 4;        // tokens per CTA at most
+constexpr int kRopeTile = 4;        // tokens per CTA, more when they are short
+constexpr int kRopeSlots = 512;     // slots per CTA that are enough
 constexpr int kRopeCtas = 10;       // per SM
 
 struct RopeArgs {
@@ -42,17 +42,17 @@ __device__ __forceinline__ void narrow(float f, uint16_t& o) {
     o = __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
-// The tile's table: cs[t][0 .. half) cosines, cs[t][half .. 2 half) sines.
+// The tile's table (a row's cosines, then its sines).
 __device__ __forceinline__ void rope_table(const RopeArgs& A, int64_t t0, int nt, float* cs,
                                            unsigned long long* steps) {
-    const int half = A.r.half;
+    const int half = A.r.half, pad = rope_pad(half);
     for (int i = threadIdx.x; i < half; i += kRopeThreads) steps[i] = rope_step(__ldg(A.r.inv_freq + i));
     __syncthreads();
     for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
         const int t = i / half, f = i - t * half;
         const float2 c = rope_turn(__ldg(A.r.positions + rope_axis(A.r, f) * A.T + t0 + t), steps[f]);
-        cs[t * 2 * half + f] = c.x;
-        cs[t * 2 * half + half + f] = A.r.inverse ? -c.y : c.y;
+        cs[t * 2 * pad + f] = c.x;
+        cs[t * 2 * pad + pad + f] = A.r.inverse ? -c.y : c.y;
     }
     __syncthreads();
 }
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_slots_kernel(con
     };
     // the first slot is on its way while the table is formed
     if ((int)threadIdx.x < total) load();
-    rope_table(A, t0, nt, cs, reinterpret_cast<unsigned long long*>(cs + A.tile * 2 * half));
+    rope_table(A, t0, nt, cs, reinterpret_cast<unsigned long long*>(cs + A.tile * 2 * rope_pad(half)));
     for (int i = threadIdx.x; i < total; i += kRopeThreads) {
         if (i != (int)threadIdx.x) load();
         const E* xr = x + (t0 + t) * A.xts + h * A.xhs;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_slots_kernel(con
         float fa[GE], fb[GE];
         widen16(a, fa);
         widen16(b, fb);
-        slot_rotate<MODE>(xr, k, cs + t * 2 * half, half, A.r.interleaved != 0, fa, fb);
+        slot_rotate<MODE>(xr, k, cs + t * 2 * rope_pad(half), half, fa, fb);
         int o0, o1;
         slot_groups<MODE, GE>(k, half, o0, o1);
         *reinterpret_cast<uint4*>(orow + o0) = narrow16(fa);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs A) {
     const int half = A.r.half;
     const int64_t t0 = (int64_t)blockIdx.x * A.tile;
     const int nt = (int)min((int64_t)A.tile, A.T - t0);
-    rope_table(A, t0, nt, cs, reinterpret_cast<unsigned long long*>(cs + A.tile * 2 * half));
+    rope_table(A, t0, nt, cs, reinterpret_cast<unsigned long long*>(cs + A.tile * 2 * rope_pad(half)));
     const int units = A.D - half;      // pairs, then values that pass through
     const E* x = static_cast<const E*>(A.x);
     E* out = static_cast<E*>(A.out);
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs A) {
             const int ia = A.r.interleaved ? 2 * u : u;
             const int ib = A.r.interleaved ? 2 * u + 1 : u + half;
             const float a = widen(xr[ia]), b = widen(xr[ib]);
-            const float c = cs[t * 2 * half + u], s = cs[t * 2 * half + half + u];
+            const float c = cs[t * 2 * rope_pad(half) + u], s = cs[(t * 2 + 1) * rope_pad(half) + u];
             narrow(turn_first(a, b, c, s), orow[ia]);
             narrow(turn_second(a, b, c, s), orow[ib]);
         } else {
@@ -154,7 +154,7 @@ template <typename E>
 void launch_rope(const RopeArgs& A, cudaStream_t st) {
     constexpr int GE = 16 / (int)sizeof(E);
     const int half = A.r.half;
-    const size_t smem = (size_t)A.tile * 2 * half * sizeof(float) + half * sizeof(unsigned long long);
+    const size_t smem = (size_t)A.tile * 2 * rope_pad(half) * sizeof(float) + half * sizeof(unsigned long long);
     const unsigned grid = (unsigned)((A.T + A.tile - 1) / A.tile);
     const bool wide = A.D % (2 * GE) == 0 &&
                       ((A.xts | A.xhs | A.ots | A.ohs) % GE) == 0 &&
@@ -164,8 +164,8 @@ void launch_rope(const RopeArgs& A, cudaStream_t st) {
         rope_slots_kernel<kSplit, E><<<grid, kRopeThreads, smem, st>>>(A);
     else if (wide && mode == kInterleaved)
         rope_slots_kernel<kInterleaved, E><<<grid, kRopeThreads, smem, st>>>(A);
-    else if (wide && (A.r.interleaved || A.x != A.out))
-        rope_slots_kernel<kAny, E><<<grid, kRopeThreads, smem, st>>>(A);
+    else if (wide && A.x != A.out)
+        rope_slots_kernel<kSplitAny, E><<<grid, kRopeThreads, smem, st>>>(A);
     else
         rope_kernel<E><<<grid, kRopeThreads, smem, st>>>(A);
 }
@@ -207,12 +207,16 @@ extern "C" int bsa_rope(const void* x, int32_t dtype, int64_t T, int64_t H, int6
     A.T = T;
     A.H = (int32_t)H;
     A.D = (int32_t)D;
-    // tokens per CTA: as many as share a table, fewer while SMs would idle
-    int tile = rot_dim > 0 ? kRopeTable / (rot_dim / 2) : kRopeTile;
-    if (tile > kRopeTile) tile = kRopeTile;
+    // tokens per CTA: four, or as many as fill its threads four times over (one
+    // 32-wide head a token: 80146 tokens take 24 us in CTAs of four tokens), within the table
+    const int64_t row_bytes = H * D * (int64_t)size;
+    int64_t tile = kRopeSlots * 32 / row_bytes;
+    if (tile < kRopeTile) tile = kRopeTile;
+    if (rot_dim > 0 && tile > kRopeTable / (rot_dim / 2)) tile = kRopeTable / (rot_dim / 2);
+    if (tile > 256) tile = 256;
     const int64_t want = 4 * (int64_t)device_sm_count();
     while (tile > 1 && (T + tile - 1) / tile < want) tile /= 2;
-    A.tile = tile;
+    A.tile = (int)tile;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == BSA_DTYPE_BF16) launch_rope<uint16_t>(A, st);
     else launch_rope<float>(A, st);

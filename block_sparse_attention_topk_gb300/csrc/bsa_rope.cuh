@@ -46,16 +46,19 @@ __device__ __forceinline__ int rope_axis(const RopeParams& R, int i) {
 }
 
 // ---- 16-byte groups ----------------------------------------------------------
-// The kernels move heads as slots of two 16-byte groups of GE elements.  Where
-// half (the pairs of a head) is a multiple of GE, a slot holds GE whole pairs:
-// its two groups are the two sides of pairs (i, i + half) (kSplit) or
-// neighbours with pairs (2i, 2i + 1) (kInterleaved).  Otherwise (kAny) the groups
-// are neighbours and each element looks for its partner.
-enum RopeMode { kSplit = 0, kInterleaved = 1, kAny = 2 };
+// The kernels move heads as slots of two 16-byte groups of GE elements:
+//  kSplit        the two sides of GE pairs (i, i + half), half a multiple of GE,
+//  kInterleaved  neighbours, pairs (2i, 2i + 1), any half,
+//  kSplitAny     neighbours, pairs (i, i + half), any half: an element's partner
+//                lies elsewhere in the row and is loaded by itself.
+enum RopeMode { kSplit = 0, kInterleaved = 1, kSplitAny = 2 };
 inline RopeMode rope_mode(const RopeParams& R, int ge) {
-    if (R.half % ge != 0) return kAny;
-    return R.interleaved ? kInterleaved : kSplit;
+    if (R.interleaved) return kInterleaved;
+    return R.half % ge == 0 ? kSplit : kSplitAny;
 }
+// A row of the table in shared memory: its cosines, padded to 16 bytes, then
+// its sines.
+__host__ __device__ inline int rope_pad(int half) { return (half + 3) & ~3; }
 __device__ __forceinline__ void widen16(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -106,15 +109,18 @@ __device__ __forceinline__ void slot_groups(int k, int half, int& o0, int& o1) {
 
 // Rotates slot k of a head's row at `x` (its groups' values in a and b; x is
 // read again only for partners outside the slot).  cs: the row's cosines, then
-// its sines at cs + half.
+// its sines at cs + rope_pad(half).
 template <RopeMode MODE, typename E, int GE>
-__device__ __forceinline__ void slot_rotate(const E* x, int k, const float* cs, int half, bool interleaved,
-                                            float (&a)[GE], float (&b)[GE]) {
-    const float* sn = cs + half;
-    if constexpr (MODE != kAny) {
+__device__ __forceinline__ void slot_rotate(const E* x, int k, const float* cs, int half, float (&a)[GE],
+                                            float (&b)[GE]) {
+    const float* sn = cs + rope_pad(half);
+    if constexpr (MODE != kSplitAny) {
         if (GE * k >= half) return;
+        // an interleaved slot may end past the last pair
+        const bool whole = MODE == kSplit || GE * k + GE <= half;
 #pragma unroll
         for (int i = 0; i < GE; i += 4) {
+            if (!whole && GE * k + i >= half) break;
             const float4 c = *reinterpret_cast<const float4*>(cs + GE * k + i);
             const float4 s = *reinterpret_cast<const float4*>(sn + GE * k + i);
             const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
@@ -126,39 +132,30 @@ __device__ __forceinline__ void slot_rotate(const E* x, int k, const float* cs, 
                 float& first = MODE == kSplit ? a[i + j] : (e < GE ? a[e % GE] : b[e % GE]);
                 float& second = MODE == kSplit ? b[i + j] : (e < GE ? a[e % GE + 1] : b[e % GE + 1]);
                 const float u = first, v = second;
-                first = turn_first(u, v, cc[j], ss[j]);
-                second = turn_second(u, v, cc[j], ss[j]);
-            }
-        }
-    } else if (interleaved) {
-        const int d0 = 2 * GE * k;
-#pragma unroll
-        for (int i = 0; i < GE; i += 2) {
-#pragma unroll
-            for (int side = 0; side < 2; ++side) {
-                float* f = side ? b : a;
-                const int p = (d0 + side * GE + i) >> 1;
-                if (p < half) {
-                    const float c = cs[p], s = sn[p];
-                    const float u = f[i], v = f[i + 1];
-                    f[i] = turn_first(u, v, c, s);
-                    f[i + 1] = turn_second(u, v, c, s);
-                }
+                const bool turns = whole || GE * k + i + j < half;
+                first = turns ? turn_first(u, v, cc[j], ss[j]) : u;
+                second = turns ? turn_second(u, v, cc[j], ss[j]) : v;
             }
         }
     } else {
         const int d0 = 2 * GE * k;
+        if (d0 >= 2 * half) return;
+        // every load is issued, of the element itself where it has no partner
+        float o[2 * GE];
 #pragma unroll
         for (int i = 0; i < 2 * GE; ++i) {
             const int d = d0 + i;
-            if (d < 2 * half) {
-                float& f = i < GE ? a[i] : b[i - GE];
-                const bool first = d < half;
-                const int p = first ? d : d - half;
-                const float c = cs[p], s = sn[p];
-                const float o = widen(x[first ? d + half : p]);
-                f = first ? turn_first(f, o, c, s) : turn_second(o, f, c, s);
-            }
+            o[i] = widen(x[d < half ? d + half : (d < 2 * half ? d - half : d)]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * GE; ++i) {
+            const int d = d0 + i;
+            const bool first = d < half;
+            const int p = min(first ? d : d - half, half - 1);
+            const float c = cs[p], s = sn[p];
+            float& f = i < GE ? a[i] : b[i - GE];
+            const float y = first ? turn_first(f, o[i], c, s) : turn_second(o[i], f, c, s);
+            if (d < 2 * half) f = y;
         }
     }
 }

@@ -41,7 +41,7 @@ def _case(T, H, D, rot, axes, dtype, seed, far=1 << 20):
 @pytest.mark.parametrize("T,H,D,rot,axes", [
     (1, 1, 2, 2, 1), (1, 8, 128, 128, 1), (3, 5, 80, 80, 3), (257, 3, 128, 64, 2), (33, 2, 96, 62, 3),
     (17, 1, 7, 4, 1), (5, 2, 1024, 1024, 8), (4099, 4, 64, 64, 3), (40, 7, 256, 16, 4), (9, 3, 65, 0, 1),
-    (130, 16, 128, 128, 3), (65, 1, 24, 20, 2),
+    (130, 16, 128, 128, 3), (65, 1, 24, 20, 2), (2500, 1, 32, 20, 3), (3001, 2, 16, 16, 1),
 ])
 def test_rope(cuda_device, T, H, D, rot, axes, interleaved, dtype):
     x, pos, inv, axis = _case(T, H, D, rot, axes, dtype, T + D + rot)
