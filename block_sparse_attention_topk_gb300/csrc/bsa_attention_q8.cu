@@ -479,8 +479,9 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         __syncwarp();
     } else if (warp == kAheadWarp) {
         // ------------------------------------------------ scales and queries
-        constexpr int QL = D / 32;         // query values per lane, contiguous
-        const int d = lane * QL, panel = d / C::ROWB, dc = d % C::ROWB;
+        constexpr int LPH = D / 8;         // lanes per query head, 8 values each
+        constexpr int HPP = 32 / LPH;      // heads a pass
+        const int d = lane % LPH * 8, panel = d / C::ROWB, dc = d % C::ROWB;
         uint32_t c = 0, item = 0;
         int qbuf = 0;
         bool ok = true;
@@ -516,49 +517,52 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     // the queries as two e4m3 terms
                     qbuf = item++ % kDepth;
                     uint8_t* qd = qsm + qbuf * C::Q_BYTES;
-#pragma unroll 4
-                    for (int g = 0; g < A.G; ++g) {
-                        const uint16_t* q = A.q + ((int64_t)it.row * A.G + g) * D + d;
-                        uint32_t w[QL / 2];
-                        if constexpr (QL == 2) w[0] = __ldg(reinterpret_cast<const unsigned*>(q));
-                        else if constexpr (QL == 4) {
-                            const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
-                            w[0] = v.x, w[1] = v.y;
-                        } else {
-                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q));
-                            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                        }
-                        float x[QL], m = 0.f;
+                    constexpr int PASSES = (GP + HPP - 1) / HPP;
+                    uint4 w[PASSES];
 #pragma unroll
-                        for (int k = 0; k < QL; ++k) {
-                            x[k] = __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+                    for (int r = 0; r < PASSES; ++r) {
+                        const int g = r * HPP + lane / LPH;
+                        w[r] = make_uint4(0, 0, 0, 0);
+                        if (g < A.G)
+                            w[r] = __ldg(reinterpret_cast<const uint4*>(A.q + ((int64_t)it.row * A.G + g) * D + d));
+                    }
+#pragma unroll
+                    for (int r = 0; r < PASSES; ++r) {
+                        const int g = r * HPP + lane / LPH;
+                        if (r * HPP >= A.G) break;
+                        const uint32_t v[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+                        float x[8], m = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            x[k] = __uint_as_float(k & 1 ? v[k / 2] & 0xFFFF0000u : v[k / 2] << 16);
                             m = fmaxf(m, fabsf(x[k]));
                         }
-                        m = max_warp(m);
+#pragma unroll
+                        for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
                         // scale by a power of two: the largest magnitude to [128, 256)
                         const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
                         const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-                        uint32_t hi[QL / 2], lo[QL / 2];
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int k = 0; k < QL; k += 2) {
+                        for (int k = 0; k < 4; ++k) {
                             // an infinite query has no finite result: NaN
-                            const float a = (x[k] - x[k] == 0.f) ? x[k] * up : NAN;
-                            const float b = (x[k + 1] - x[k + 1] == 0.f) ? x[k + 1] * up : NAN;
-                            hi[k / 2] = pack_e4m3(a, b);
-                            const float2 f = unpack_e4m3(hi[k / 2]);
-                            lo[k / 2] = pack_e4m3((a - f.x) * 16.f, (b - f.y) * 16.f);
+                            const float a = (x[2 * k] - x[2 * k] == 0.f) ? x[2 * k] * up : NAN;
+                            const float b = (x[2 * k + 1] - x[2 * k + 1] == 0.f) ? x[2 * k + 1] * up : NAN;
+                            hi[k] = pack_e4m3(a, b);
+                            const float2 f = unpack_e4m3(hi[k]);
+                            lo[k] = pack_e4m3((a - f.x) * 16.f, (b - f.y) * 16.f);
                         }
+                        if (g < A.G) {
 #pragma unroll
-                        for (int term = 0; term < 2; ++term) {
-                            const uint32_t* v = term ? lo : hi;
-                            const int row = term * GP + g;
-                            const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
-                            uint8_t* dst = qd + panel * C::Q_PANEL + row * C::ROWB + (((dc >> 4) ^ sw) << 4) + (dc & 15);
-                            if constexpr (QL == 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)v[0];
-                            else if constexpr (QL == 4) *reinterpret_cast<uint32_t*>(dst) = v[0] | v[1] << 16;
-                            else *reinterpret_cast<uint2*>(dst) = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+                            for (int term = 0; term < 2; ++term) {
+                                const uint32_t* t = term ? lo : hi;
+                                const int row = term * GP + g;
+                                const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
+                                uint8_t* dst = qd + panel * C::Q_PANEL + row * C::ROWB + (((dc >> 4) ^ sw) << 4) + (dc & 15);
+                                *reinterpret_cast<uint2*>(dst) = make_uint2(t[0] | t[1] << 16, t[2] | t[3] << 16);
+                            }
+                            if (lane % LPH == 0) qinv[qbuf][g] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
                         }
-                        if (lane == 0) qinv[qbuf][g] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
                     }
                     if (lane >= A.G && lane < GP) qinv[qbuf][lane] = 0.f;
                 }
