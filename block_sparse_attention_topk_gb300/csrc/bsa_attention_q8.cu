@@ -122,9 +122,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 __device__ __forceinline__ float max_warp(float x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-    return x;
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ float sum_warp(float x) {
 #pragma unroll
@@ -682,20 +682,22 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             // ---- the chunk's maxima, block by block as scores complete ----
             const uint32_t sbuf = s & 1;
             const uint32_t s_cols = lanes + sbuf * C::S_COLS;
-            for (int b = 0; b < nb; ++b) {
-                if ((b & 1) == 0) {
-                    mbar_wait(&s_full[sbuf][b >> 1], (s_phase >> (sbuf * 8 + (b >> 1))) & 1, quit);
-                    __syncwarp();
-                    tc_fence_after();
-                }
-                float x[2 * HG];
-                load_terms<HG, GP>(s_cols + b * N, x);
-                const float4 sc = scales[b * kPagesPerBlock + part16];
-                const bool live = (ch.c0 + b) * kPageSize + tok < ch.ctx && sc.y != -INFINITY;
-                if (live) {
+            for (int b = 0; b < nb; b += 2) {
+                mbar_wait(&s_full[sbuf][b >> 1], (s_phase >> (sbuf * 8 + (b >> 1))) & 1, quit);
+                __syncwarp();
+                tc_fence_after();
+                // both blocks of the pair; one that is not there has no live token
 #pragma unroll
-                    for (int g = 0; g < HG; ++g)
-                        ct[g] = fmaxf(ct[g], fmaf(fmaf(x[HG + g], 0.0625f, x[g]), qi[g] * sc.x, sc.y));
+                for (int j = 0; j < 2; ++j) {
+                    float x[2 * HG];
+                    load_terms<HG, GP>(s_cols + (b + j) * N, x);
+                    const float4 sc = scales[(b + j) * kPagesPerBlock + part16];
+                    const bool live = b + j < nb && (ch.c0 + b + j) * kPageSize + tok < ch.ctx && sc.y != -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < HG; ++g) {
+                        const float t = fmaf(fmaf(x[HG + g], 0.0625f, x[g]), qi[g] * sc.x, sc.y);
+                        if (live) ct[g] = fmaxf(ct[g], t);
+                    }
                 }
             }
             close_chunk();
@@ -721,36 +723,37 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     ct[g] = 8.f - top;           // probabilities in units of 2^-8 of the largest so far
                 }
                 // ---- the probabilities ----
-                for (int b = 0; b < nb; ++b) {
-                    float x[2 * HG];
-                    load_terms<HG, GP>(s_cols + b * N, x);
-                    const float4 sc = scales[b * kPagesPerBlock + part16];
-                    const bool live = (ch.c0 + b) * kPageSize + tok < ch.ctx && sc.y != -INFINITY;
-                    float w[HG];
+                for (int b = 0; b < nb; b += 2) {
 #pragma unroll
-                    for (int g = 0; g < HG; ++g) {
-                        const float t = fmaf(fmaf(x[HG + g], 0.0625f, x[g]), qi[g] * sc.x, sc.y + ct[g]);
-                        w[g] = live ? ex2(t) : 0.f;
-                        l[g] = fmaf(w[g], sc.z, l[g]);
-                    }
-                    uint8_t* pb = psm + b * N * 128 + (tok & 15) + g0 * 128;
+                    for (int j = 0; j < 2; ++j) {
+                        float x[2 * HG];
+                        load_terms<HG, GP>(s_cols + (b + j) * N, x);
+                        const float4 sc = scales[(b + j) * kPagesPerBlock + part16];
+                        const bool live = b + j < nb && (ch.c0 + b + j) * kPageSize + tok < ch.ctx && sc.y != -INFINITY;
+                        float w[HG];
 #pragma unroll
-                    for (int g = 0; g < HG; g += 2) {
-                        const uint32_t hi = pack_e4m3(w[g], w[g + 1]);
-                        const float2 f = unpack_e4m3(hi);
-                        const uint32_t lo = pack_e4m3((w[g] - f.x) * 16.f, (w[g + 1] - f.y) * 16.f);
-                        // rows g0 + g and GP + g0 + g; g0 and (from 8 heads on) GP are multiples of 8
-                        const int r0 = g, r1 = g + 1, r2 = GP + g, r3 = GP + g + 1;
-                        pb[r0 * 128 + ((part16 ^ (r0 & 7)) << 4)] = (uint8_t)hi;
-                        pb[r1 * 128 + ((part16 ^ (r1 & 7)) << 4)] = (uint8_t)(hi >> 8);
-                        pb[r2 * 128 + ((part16 ^ (r2 & 7)) << 4)] = (uint8_t)lo;
-                        pb[r3 * 128 + ((part16 ^ (r3 & 7)) << 4)] = (uint8_t)(lo >> 8);
+                        for (int g = 0; g < HG; ++g) {
+                            const float t = fmaf(fmaf(x[HG + g], 0.0625f, x[g]), qi[g] * sc.x, sc.y + ct[g]);
+                            w[g] = live ? ex2(t) : 0.f;
+                            l[g] = fmaf(w[g], live ? sc.z : 0.f, l[g]);
+                        }
+                        uint8_t* pb = psm + (b + j) * N * 128 + (tok & 15) + g0 * 128;
+#pragma unroll
+                        for (int g = 0; g < HG; g += 2) {
+                            const uint32_t hi = pack_e4m3(w[g], w[g + 1]);
+                            const float2 f = unpack_e4m3(hi);
+                            const uint32_t lo = pack_e4m3((w[g] - f.x) * 16.f, (w[g + 1] - f.y) * 16.f);
+                            // rows g0 + g and GP + g0 + g; g0 and (from 8 heads on) GP are multiples of 8
+                            const int r0 = g, r1 = g + 1, r2 = GP + g, r3 = GP + g + 1;
+                            pb[r0 * 128 + ((part16 ^ (r0 & 7)) << 4)] = (uint8_t)hi;
+                            pb[r1 * 128 + ((part16 ^ (r1 & 7)) << 4)] = (uint8_t)(hi >> 8);
+                            pb[r2 * 128 + ((part16 ^ (r2 & 7)) << 4)] = (uint8_t)lo;
+                            pb[r3 * 128 + ((part16 ^ (r3 & 7)) << 4)] = (uint8_t)(lo >> 8);
+                        }
                     }
-                    if ((b & 1) == 1 || b + 1 == nb) {
-                        fence_async_smem();
-                        tc_fence_before();
-                        mbar_arrive(&p_full[b >> 1]);
-                    }
+                    fence_async_smem();
+                    tc_fence_before();
+                    mbar_arrive(&p_full[b >> 1]);
                 }
                 s_phase ^= ((1u << ((nb + 1) >> 1)) - 1) << (sbuf * 8);
                 ++s;
