@@ -768,18 +768,28 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
     if (warp == kMmaWarp) tmem_free(tmem, C::TMEM);
 }
 
-// Joins the partial results of a split row, head by head: a thread per
-// dimension.  Launched to start beside the last items (programmatic dependent
-// launch), it waits for their end here.
-__global__ void __launch_bounds__(256)
+// Joins the partial results of a split row, head by head: D threads wide, and
+// several such slices that take every so many-th part, the first kJoinAhead of
+// each read before the parts' weights are known.  Launched to start beside the
+// last items (programmatic dependent launch), it waits for their end here.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinAhead = 4;
+__global__ void __launch_bounds__(kJoinThreads)
 attention_q8_join_kernel(const float* part, uint16_t* out, int splits, int G, int D) {
-    extern __shared__ float weight[];          // [splits]
-    __shared__ float total[2];
+    extern __shared__ float weight[];          // [splits], then a sum per thread
+    __shared__ float total;
     const int64_t row = blockIdx.x;
-    const int g = blockIdx.y, tid = threadIdx.x;
+    const int g = blockIdx.y, tid = threadIdx.x, d = tid % D, slice = tid / D, slices = blockDim.x / D;
     asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written
     const int64_t len = part_floats(G, D);
     const float* base = part + row * splits * len;
+    const float* src = base + g * D + d;
+    float ahead[kJoinAhead];
+#pragma unroll
+    for (int j = 0; j < kJoinAhead; ++j) {
+        const int s = slice + j * slices;
+        ahead[j] = s < splits ? src[s * len] : 0.f;
+    }
     if (tid < 32) {
         float m = -INFINITY, sum = 0.f;
         for (int s = tid; s < splits; s += 32) m = fmaxf(m, base[s * len + G * D + g]);
@@ -791,18 +801,28 @@ attention_q8_join_kernel(const float* part, uint16_t* out, int splits, int G, in
             sum += l * w;
         }
         sum = sum_warp(sum);
-        if (tid == 0) total[0] = sum;
+        if (tid == 0) total = sum;
     }
     __syncthreads();
-    const float sum = total[0];
+    // a part without tokens has weight 0 and no defined output
     float o = 0.f;
-    const float* src = base + g * D + tid;
-#pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
-        const float w = weight[s];
-        o = fmaf(w == 0.f ? 0.f : src[s * len], w, o);
+#pragma unroll
+    for (int j = 0; j < kJoinAhead; ++j) {
+        const int s = slice + j * slices;
+        const float w = s < splits ? weight[s] : 0.f;
+        if (w != 0.f) o = fmaf(ahead[j], w, o);
     }
-    out[(row * G + g) * D + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : o / sum));
+#pragma unroll 4
+    for (int s = slice + kJoinAhead * slices; s < splits; s += slices) {
+        const float w = weight[s];
+        if (w != 0.f) o = fmaf(src[s * len], w, o);
+    }
+    float* sums = weight + splits;
+    sums[tid] = o;
+    __syncthreads();
+    if (slice > 0) return;
+    for (int i = 1; i < slices; ++i) o += sums[i * D + d];
+    out[(row * G + g) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(total == 0.f ? 0.f : o / total));
 }
 
 // ---- host ------------------------------------------------------------------
@@ -867,26 +887,33 @@ bool sizes_ok(int64_t T, int64_t H, int64_t G, int64_t D) {
 // Items per row.  For each number of rounds over the resident CTAs the largest
 // split that keeps to it, the fewest items of that block count, is weighed: the
 // longest CTA's blocks and items, not less than the copies of all blocks over
-// all SMs, and the join.
+// all SMs, and the join.  The constants are in us, fitted to sweeps of 1 to 50
+// items per row over 14 shapes: e.g. one row of 16 blocks takes 16.3 unsplit,
+// 10.0 in 8; 160 rows of 16 blocks 32 unsplit, 33 in 3; 111 rows of 17
+// blocks 256 wide 28 unsplit, 25 in 2; six rows of 1024 blocks 675
+// unsplit, 44 in 25, 57 in 32.
 int pick_splits(int64_t rows, int64_t G, int64_t D, int32_t K, int sms) {
     const int64_t slots = (int64_t)sms * (G <= 8 ? 2 : 1);
     const double copy_us = (double)rows * K * D * 256 / 6.0e6;     // 6 TB/s
+    const double block_us = D == 256 ? 1.4 : 0.7, item_us = 4.0, join_us = 2.5;
     auto cost = [&](int64_t s) {
         const int64_t blocks = (K + s - 1) / s;
-        const double cta_us = (double)((rows * s + slots - 1) / slots) * (blocks * 0.7 + 2.0);
-        return (cta_us > copy_us ? cta_us : copy_us) + (s > 1 ? 3.0 + 0.004 * rows * s : 0.0);
+        const double cta_us = (double)((rows * s + slots - 1) / slots) * (blocks * block_us + item_us);
+        return (cta_us > copy_us ? cta_us : copy_us) + (s > 1 ? join_us + 0.1 * s + 0.004 * rows * s : 0.0);
     };
     int best = 1;
     double least = cost(1);
     for (int64_t rounds = 1; rounds <= 8; ++rounds) {
         int64_t s = rounds * slots / rows;
         if (s > K) s = K;
-        if (s < 2) continue;
-        s = (K + (K + s - 1) / s - 1) / ((K + s - 1) / s);
-        const double us = cost(s);
-        if (us < least) {
-            best = (int)s;
-            least = us;
+        // the halves too: fewer items may cost less to join than their blocks save
+        for (; s >= 2; s /= 2) {
+            const int64_t even = (K + (K + s - 1) / s - 1) / ((K + s - 1) / s);
+            const double us = cost(even);
+            if (us < least) {
+                best = (int)even;
+                least = us;
+            }
         }
     }
     return best;
@@ -962,8 +989,11 @@ extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache
     if (e == cudaSuccess && A.splits > 1) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)A.rows, (unsigned)A.G);
-        cfg.blockDim = dim3((unsigned)D);
-        cfg.dynamicSmemBytes = A.splits * sizeof(float);
+        // slices: four parts each at least
+        int slices = (A.splits + kJoinAhead - 1) / kJoinAhead;
+        if (slices > kJoinThreads / (int)D) slices = kJoinThreads / (int)D;
+        cfg.blockDim = dim3((unsigned)(slices * D));
+        cfg.dynamicSmemBytes = (A.splits + kJoinThreads) * sizeof(float);
         cfg.stream = st;
         cudaLaunchAttribute attr{};
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
