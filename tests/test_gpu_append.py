@@ -269,3 +269,35 @@ def test_append_on_a_side_stream_and_in_a_graph(cuda_device):
         out, k2, v2, ks2, vs2 = _run(dev, "decode", new, H, 4, table, before, kind, inv.cpu(), None, None, False, rows)
         for a, b in ((qo, out), (kc, k2), (vc, v2), (ks, ks2), (vs, vs2)):
             assert torch.equal(a.float().nan_to_num(), b.float().nan_to_num())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_append_offsets_past_32_bits(cuda_device, fmt):
+    """Pages whose elements lie past 2^32 in the cache; an empty call."""
+    dev = cuda_device
+    H, D, B = 4, 256, 5
+    qkv, table, caches, dtype, kind = _setup(B, H, 3, D, B, 1, fmt, 23)
+    seq = torch.tensor([1, 17, 128, 40, 9], dtype=torch.int32)
+    inv = (1e4 ** (-torch.arange(64) / 64)).float()
+    out, kc, vc, ks, vs = _run(dev, "decode", qkv, H, 3, table, caches, kind, inv, None, None, False, (seq, 1))
+    small = kc.shape[0]
+    pages = (1 << 32) // (16 * H * D) // 8 * 8 + small
+    base = (pages - small) // 8
+    far = torch.empty((2, pages, 16, H, D), dtype=dtype, device=dev)
+    fars = torch.empty((2, pages, H), device=dev) if kind else None
+    for i, (c, s) in enumerate(caches):
+        far[i].view(torch.uint8)[pages - small:] = c.to(dev).view(torch.uint8)
+        if kind:
+            fars[i, pages - small:] = s.to(dev)
+    q, k, v = qkv.to(dev).split([3, H, H], dim=1)
+    args = dict(q=q, inv_freq=inv.to(dev), k_scale=fars[0] if kind else None, v_scale=fars[1] if kind else None)
+    got = bsa.bsa_append_kv_decode(k, v, far[0], far[1], (table + base).to(dev), seq.to(dev), 1, **args)
+    torch.cuda.synchronize()
+    assert torch.equal(got, out)
+    for a, b in ((far[0], kc), (far[1], vc)):
+        assert torch.equal(a.view(torch.uint8)[pages - small:], b.view(torch.uint8))
+    if kind:
+        assert torch.equal(fars[0, pages - small:], ks) and torch.equal(fars[1, pages - small:], vs)
+    none = bsa.bsa_append_kv_decode(k[:0], v[:0], far[0], far[1], table[:0].to(dev), seq[:0].to(dev), 1,
+                                    **{**args, "q": q[:0]})
+    assert none.shape == (0, 3, D)

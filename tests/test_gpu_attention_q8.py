@@ -239,3 +239,38 @@ def test_attention_q8_blocks_in_runs(cuda_device, H, G, D, fmt):
     bt[2, 0, 8:16] = torch.arange(blocks * 8 - 4, blocks * 8 + 4)      # runs out of the cache
     ctx = torch.tensor([K * 128, 1100, 1027, 897, 128, 15, 1, 1151, 1040, 640][:T * H], dtype=torch.int32).view(T, H)
     _check(cuda_device, q, c, s, bt, ctx, dtype, kind)
+
+
+def test_attention_q8_empty_cache_and_empty_batch(cuda_device):
+    """No page at all: every token's page is out of range, so zeros; no rows:
+    nothing is launched."""
+    dev = cuda_device
+    q = synth.normal_scores((3, 2, 4, 128), torch.bfloat16, seed=1).to(dev)
+    kc = torch.empty((0, 16, 2, 128), dtype=torch.float8_e4m3fn, device=dev)
+    sc = torch.empty((0, 2), device=dev)
+    bt = torch.zeros((3, 2, 16), dtype=torch.int32, device=dev)
+    ctx = torch.full((3, 2), 200, dtype=torch.int32, device=dev)
+    got = bsa.bsa_sparse_decode_attention_q8(q, kc, kc, sc, sc, bt, ctx)
+    torch.cuda.synchronize()
+    assert (got == 0).all()
+    none = bsa.bsa_sparse_decode_attention_q8(q[:0], kc, kc, sc, sc, bt[:0], ctx[:0])
+    assert none.shape == (0, 2, 4, 128)
+
+
+def test_attention_q8_offsets_past_32_bits(cuda_device):
+    """Pages whose bytes lie past 2^32 in the cache."""
+    dev = cuda_device
+    H, D, G, K = 4, 256, 4, 2
+    pages = (1 << 32) // (16 * H * D) + 100
+    q, c, s, bt, ctx, dtype, kind = _case(2, H, G, D, K, "e4m3", [256, 200, 17, 128, 1, 255, 100, 31], 5)
+    small = c[0].shape[0]
+    far = torch.empty((2, pages, 16, H, D), dtype=torch.uint8, device=dev)
+    fars = torch.empty((2, pages, H), device=dev)
+    for i in range(2):
+        far[i, pages - small:] = c[i].to(dev)
+        fars[i, pages - small:] = s[i].to(dev)
+    near = _check(dev, q, c, s, bt, ctx, dtype, kind)
+    got = bsa.bsa_sparse_decode_attention_q8(q.to(dev), far[0].view(dtype), far[1].view(dtype), fars[0], fars[1],
+                                             (bt + pages - small).to(dev), ctx.to(dev))
+    torch.cuda.synchronize()
+    assert torch.equal(got, near)
