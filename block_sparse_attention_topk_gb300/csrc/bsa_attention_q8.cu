@@ -19,7 +19,7 @@
 // The sums, maxima and accumulators are fp32.
 //
 // The work: a CTA takes items (a row, or a share of its 128-token blocks when
-// rows are few) and walks each in chunks of up to 6 blocks.  A chunk's scores are
+// rows are few; a cluster of CTAs or a second launch joins the shares) and walks each in chunks of up to 6 blocks.  A chunk's scores are
 // complete in TMEM before its probabilities are formed, so there is one maximum
 // per chunk and the accumulators in TMEM start anew with each chunk.
 //  softmax    thread i of a group of four warps is token i of a block
@@ -62,6 +62,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kDepth = 4;                // chunks announced ahead
+constexpr int kMaxCluster = 8;           // items per row that a cluster joins
 constexpr int kSmSmem = 233472;          // an SM's shared memory; 1 KB of it goes to each CTA
 
 template <int D, int GP>
@@ -103,10 +104,11 @@ struct Q8Params {
     const int32_t* bt;
     const int32_t* ctx;
     uint16_t* out;
-    float* part;             // partial results of split rows, or null
+    float* part;             // partial results of split rows joined by a launch of their own, or null
     int64_t num_pages;
     int32_t rows, H, G, width;
     int32_t splits;          // items per row
+    int32_t cluster;         // 1: a row's items are one cluster's CTAs, which join them
     uint32_t k_idesc, v_idesc;
     float scale_log2e;
     uint32_t* status;
@@ -635,13 +637,15 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 group_sync(group);
                 const bool bad = *quit;
                 uint16_t* o16 = A.out + (int64_t)row * A.G * D;
-                float* o32 = A.part + (int64_t)item * part_floats(A.G, D);
+                // a split row's part: to the workspace, or to this CTA's own
+                // memory, where its probabilities are no longer needed
+                float* o32 = A.cluster ? reinterpret_cast<float*>(psm) : A.part + (int64_t)item * part_floats(A.G, D);
 #pragma unroll
                 for (int g = 0; g < HG; ++g) {
                     if (g0 + g < A.G) {
                         const float sum = bad ? NAN
                                               : red[group][0][g] + red[group][1][g] + red[group][2][g] + red[group][3][g];
-                        if (A.part == nullptr) {
+                        if (A.splits == 1) {
                             const float f = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
                             for (int p = 0; p < PANELS; ++p)
@@ -771,6 +775,37 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
     __syncthreads();
     if (tid == 0) report_status(A.status, gave_up != 0, BSA_STATUS_TIMEOUT);
     if (warp == kMmaWarp) tmem_free(tmem, C::TMEM);
+    if (A.cluster) {
+        // the row's parts lie in the cluster's CTAs: each joins every so many-th head
+        cluster_sync();
+        const uint32_t rank = cluster_rank(), base = smem_addr(psm);
+        const int heads = (int)rank < A.G ? (A.G - (int)rank + A.splits - 1) / A.splits : 0;
+        const int64_t row = blockIdx.x / A.splits;
+        for (int i = tid; i < heads * D; i += C::THREADS) {
+            const int g = (int)rank + i / D * A.splits, d = i % D;
+            float mt[kMaxCluster], l[kMaxCluster], o[kMaxCluster], top = -INFINITY;
+#pragma unroll
+            for (int s = 0; s < kMaxCluster; ++s) {
+                mt[s] = -INFINITY;
+                l[s] = o[s] = 0.f;
+                if (s < A.splits) {
+                    mt[s] = cluster_read(base + 4 * (A.G * D + g), s);
+                    l[s] = cluster_read(base + 4 * (A.G * D + A.G + g), s);
+                    o[s] = cluster_read(base + 4 * (g * D + d), s);
+                }
+                top = fmaxf(top, mt[s]);
+            }
+            float sum = 0.f, acc = 0.f;
+#pragma unroll
+            for (int s = 0; s < kMaxCluster; ++s) {
+                const float w = l[s] == 0.f ? 0.f : ex2(mt[s] - top);
+                sum = fmaf(l[s], w, sum);
+                if (w != 0.f) acc = fmaf(o[s], w, acc);
+            }
+            A.out[(row * A.G + g) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum));
+        }
+        cluster_sync();          // no CTA leaves while another reads its memory
+    }
 }
 
 // Joins the partial results of a split row, head by head: D threads wide, and
@@ -873,8 +908,23 @@ cudaError_t launch_q8(Q8Params& A, const Q8Maps& M, bool e4m3, int sms, cudaStre
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)A.rows * A.splits;
     const int64_t slots = (int64_t)sms * C::CTAS;
-    kern<<<(unsigned)(items < slots ? items : slots), C::THREADS, C::SMEM, st>>>(A, M);
-    return cudaGetLastError();
+    static_assert((GP * D + 2 * GP) * (int)sizeof(float) <= C::P_BYTES, "a part fits where the probabilities were");
+    if (!A.cluster) {
+        kern<<<(unsigned)(items < slots ? items : slots), C::THREADS, C::SMEM, st>>>(A, M);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)items);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)A.splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, (const Q8Params)A, M);
 }
 
 template <int D>
@@ -896,36 +946,43 @@ bool sizes_ok(int64_t T, int64_t H, int64_t G, int64_t D) {
 // items per row over 14 shapes: e.g. one row of 16 blocks takes 16.3 unsplit,
 // 10.0 in 8; 160 rows of 16 blocks 32 unsplit, 33 in 3; 111 rows of 17
 // blocks 256 wide 28 unsplit, 25 in 2; six rows of 1024 blocks 675
-// unsplit, 44 in 25, 57 in 32.
-int pick_splits(int64_t rows, int64_t G, int64_t D, int32_t K, int sms) {
+// unsplit, 44 in 25, 57 in 32.  2, 4 or 8 items of a row, all resident at once, are
+// the CTAs of a cluster, which join them through its shared memory (no second
+// launch, no workspace).
+struct Split {
+    int items;         // per row
+    bool cluster;      // joined by their cluster
+};
+Split pick_splits(int64_t rows, int64_t G, int64_t D, int32_t K, int sms) {
     const int64_t slots = (int64_t)sms * (G <= 8 ? 2 : 1);
     const double copy_us = (double)rows * K * D * 256 / 6.0e6;     // 6 TB/s
-    const double block_us = D == 256 ? 1.4 : 0.7, item_us = 4.0, join_us = 2.5;
-    auto cost = [&](int64_t s) {
+    const double block_us = D == 256 ? 1.4 : 0.7, item_us = 4.0, join_us = 2.5, cluster_us = 1.0;
+    auto cost = [&](int64_t s, double joined) {
         const int64_t blocks = (K + s - 1) / s;
         const double cta_us = (double)((rows * s + slots - 1) / slots) * (blocks * block_us + item_us);
-        return (cta_us > copy_us ? cta_us : copy_us) + (s > 1 ? join_us + 0.1 * s + 0.004 * rows * s : 0.0);
+        return (cta_us > copy_us ? cta_us : copy_us) + joined;
     };
-    int best = 1;
-    double least = cost(1);
+    Split best{1, false};
+    double least = cost(1, 0.0);
+    auto weigh = [&](int64_t s, bool cluster) {
+        const double us = cost(s, cluster ? cluster_us : join_us + 0.1 * s + 0.004 * rows * s);
+        if (us < least) {
+            best = Split{(int)s, cluster};
+            least = us;
+        }
+    };
     for (int64_t rounds = 1; rounds <= 8; ++rounds) {
         int64_t s = rounds * slots / rows;
         if (s > K) s = K;
         // the halves too: fewer items may cost less to join than their blocks save
-        for (; s >= 2; s /= 2) {
-            const int64_t even = (K + (K + s - 1) / s - 1) / ((K + s - 1) / s);
-            const double us = cost(even);
-            if (us < least) {
-                best = (int)even;
-                least = us;
-            }
-        }
+        for (; s >= 2; s /= 2) weigh((K + (K + s - 1) / s - 1) / ((K + s - 1) / s), false);   // the fewest of that block count
     }
+    for (int s = 2; s <= kMaxCluster && s <= K && rows * s <= slots; s *= 2) weigh(s, true);
     return best;
 }
 
-size_t workspace_need(int64_t rows, int64_t G, int64_t D, int splits) {
-    return splits > 1 ? (size_t)(rows * splits * part_floats((int)G, (int)D)) * sizeof(float) : 0;
+size_t workspace_need(int64_t rows, int64_t G, int64_t D, Split s) {
+    return s.items > 1 && !s.cluster ? (size_t)(rows * s.items * part_floats((int)G, (int)D)) * sizeof(float) : 0;
 }
 
 }  // namespace
@@ -968,12 +1025,14 @@ extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache
     A.H = (int32_t)H;
     A.G = (int32_t)G;
     A.width = K * kPagesPerBlock;
-    A.splits = pick_splits(T * H, G, D, K, sms);
+    const Split split = pick_splits(T * H, G, D, K, sms);
+    A.splits = split.items;
+    A.cluster = split.cluster;
     A.scale_log2e = scale * 1.44269504f;
     A.status = current_status_word();
-    if (A.splits > 1) {
-        if (workspace == nullptr || workspace_bytes < workspace_need(A.rows, G, D, A.splits) ||
-            (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
+    const size_t need = workspace_need(A.rows, G, D, split);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
             return BSA_ERR_WORKSPACE;
         A.part = static_cast<float*>(workspace);
     }
@@ -991,7 +1050,7 @@ extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache
     if (D == 64) e = launch_q8_g<64>(A, M, e4m3, sms, st);
     else if (D == 128) e = launch_q8_g<128>(A, M, e4m3, sms, st);
     else e = launch_q8_g<256>(A, M, e4m3, sms, st);
-    if (e == cudaSuccess && A.splits > 1) {
+    if (e == cudaSuccess && A.part != nullptr) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)A.rows, (unsigned)A.G);
         // slices: four parts each at least
