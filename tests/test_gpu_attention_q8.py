@@ -274,3 +274,28 @@ def test_attention_q8_offsets_past_32_bits(cuda_device):
                                              (bt + pages - small).to(dev), ctx.to(dev))
     torch.cuda.synchronize()
     assert torch.equal(got, near)
+
+
+@pytest.mark.parametrize("T,H,G,D,K,joins", [(1, 1, 8, 128, 16, "cluster"), (3, 1, 12, 64, 8, "cluster"), (2, 1, 3, 256, 2, "cluster"),
+                                             (1, 2, 8, 64, 512, "launch"), (1, 1, 16, 128, 1024, "launch")])
+def test_attention_q8_joined_rows_in_a_graph(cuda_device, T, H, G, D, K, joins):
+    """Rows joined by their cluster, or by a launch with a workspace, captured and
+    replayed on contexts of all lengths, empty shares among them."""
+    dev = cuda_device
+    q, c, s, bt, ctx, dtype, kind = _case(T, H, G, D, K, "e4m3", [K * 128] * (T * H), 7, pages=700)
+    for x in c:                          # no NaN codes: every page is read somewhere
+        x[(x & 0x7F) == 0x7F] = 0x31
+    assert (bsa.bsa_attention_q8_workspace_bytes(T, H, G, D, K) > 0) == (joins == "launch")
+    args = [x.to(dev) for x in (q, c[0].view(dtype), c[1].view(dtype), s[0], s[1], bt, ctx)]
+    out = torch.empty_like(args[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream(dev)):
+        bsa.bsa_sparse_decode_attention_q8(*args, out=out)
+    for n in (K * 128, 1, 0, 129, K * 64 + 5, 3 * 128):
+        n = min(n, K * 128)
+        args[6].fill_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        want = _check(dev, q, c, s, bt, torch.full_like(ctx, n), dtype, kind)
+        assert torch.equal(got, want), n
