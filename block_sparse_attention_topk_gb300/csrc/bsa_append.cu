@@ -370,7 +370,6 @@ cudaError_t launch_format(const AppendParams& P, unsigned grid, size_t smem, cud
 }
 
 int check_append(const bsa_append_args_t* a) {
-    if (a == nullptr) return BSA_ERR_NULL;
     if (a->cache_dtype != BSA_DTYPE_BF16 && a->cache_dtype != BSA_DTYPE_E4M3 && a->cache_dtype != BSA_DTYPE_E5M2)
         return BSA_ERR_DTYPE;
     if (a->T < 0 || a->T > INT32_MAX || a->H < 1 || a->H > 65536 || a->Hq < 0 || a->Hq > 65536 ||
@@ -400,6 +399,15 @@ int check_append(const bsa_append_args_t* a) {
     return BSA_OK;
 }
 
+// The arguments with the strides along dimensions of one entry set to 0: they
+// may be anything.
+bsa_append_args_t plain_strides(bsa_append_args_t a) {
+    if (a.T == 1) a.k_token_stride = a.v_token_stride = a.q_token_stride = 0;
+    if (a.H == 1) a.k_head_stride = a.v_head_stride = 0;
+    if (a.Hq == 1) a.q_head_stride = 0;
+    return a;
+}
+
 int launch_append(AppendParams& P, cudaStream_t st) {
     P.r = RopeParams{P.a.positions, P.a.T, P.a.inv_freq, P.a.freq_axis, P.a.axes, P.a.rot_dim / 2,
                      (P.a.flags & BSA_ROPE_INTERLEAVED) != 0, (P.a.flags & BSA_ROPE_INVERSE) != 0};
@@ -426,14 +434,15 @@ using namespace bsa;
 
 extern "C" int bsa_append_kv_decode(const bsa_append_args_t* args, const int32_t* seq_lens,
                                     int32_t decode_query_len, void* stream) {
-    const int rc = check_append(args);
+    if (args == nullptr) return BSA_ERR_NULL;
+    AppendParams P{};
+    P.a = plain_strides(*args);
+    const int rc = check_append(&P.a);
     if (rc != BSA_OK) return rc;
     if (decode_query_len < 1) return BSA_ERR_SHAPE;
-    if (args->T != args->num_reqs * decode_query_len) return BSA_ERR_ROWS;
-    if (args->T == 0) return BSA_OK;
+    if (P.a.T != P.a.num_reqs * decode_query_len) return BSA_ERR_ROWS;
+    if (P.a.T == 0) return BSA_OK;
     if (seq_lens == nullptr) return BSA_ERR_NULL;
-    AppendParams P{};
-    P.a = *args;
     P.seq_lens = seq_lens;
     P.dql = decode_query_len;
     return launch_append(P, static_cast<cudaStream_t>(stream));
@@ -441,12 +450,13 @@ extern "C" int bsa_append_kv_decode(const bsa_append_args_t* args, const int32_t
 
 extern "C" int bsa_append_kv_varlen(const bsa_append_args_t* args, const int32_t* cu_seqlens_q,
                                     const int32_t* prefix_lens, void* stream) {
-    const int rc = check_append(args);
-    if (rc != BSA_OK) return rc;
-    if (args->T == 0) return BSA_OK;
-    if (cu_seqlens_q == nullptr || (args->num_reqs > 0 && prefix_lens == nullptr)) return BSA_ERR_NULL;
+    if (args == nullptr) return BSA_ERR_NULL;
     AppendParams P{};
-    P.a = *args;
+    P.a = plain_strides(*args);
+    const int rc = check_append(&P.a);
+    if (rc != BSA_OK) return rc;
+    if (P.a.T == 0) return BSA_OK;
+    if (cu_seqlens_q == nullptr || (P.a.num_reqs > 0 && prefix_lens == nullptr)) return BSA_ERR_NULL;
     P.cu = cu_seqlens_q;
     P.prefix = prefix_lens;
     return launch_append(P, static_cast<cudaStream_t>(stream));

@@ -309,8 +309,9 @@ int bsa_rope(const void* x, int32_t dtype, int64_t T, int64_t H, int64_t D,
 typedef struct bsa_append_args {
     /* bf16 [T, H, D] keys and values and (or NULL) [T, Hq, D] queries:
      * element (t, h, d) at t * token_stride + h * head_stride + d; pointers
-     * 16-byte aligned, strides and D multiples of 8 (D of 16), D <=
-     * BSA_MAX_CACHE_DIM.  They may be parts of one fused buffer. */
+     * 16-byte aligned, strides multiples of 8 (of no account along a
+     * dimension of one entry), D a multiple of 16, D <= BSA_MAX_CACHE_DIM.
+     * They may be parts of one fused buffer. */
     const void* k;
     const void* v;
     const void* q;
@@ -319,8 +320,8 @@ typedef struct bsa_append_args {
     int64_t v_token_stride, v_head_stride;
     int64_t q_token_stride, q_head_stride;
     /* rotated queries, bf16 [T, Hq, D] contiguous, 16-byte aligned (NULL
-     * exactly when q is).  Rows of no sequence or at a negative position
-     * are padding: their queries are written as zeros. */
+     * exactly when q is), apart from q.  Rows of no sequence or at a negative
+     * position are padding: their queries are written as zeros. */
     void* q_out;
     /* rotary positions as above; positions NULL: the position in the
      * sequence (axes 1).  rot_dim 0: no rotation (inv_freq may be NULL). */
@@ -378,7 +379,8 @@ int bsa_append_kv_varlen(const bsa_append_args_t* args, const int32_t* cu_seqlen
 #define BSA_MAX_ATTN_Q8_GROUP 16
 
 /* Device workspace of bsa_sparse_decode_attention_q8 for these sizes on the
- * current device (0 when every row is taken by one CTA).  Host-only. */
+ * current device (0 unless rows are split over more CTAs than a cluster
+ * joins).  Host-only. */
 size_t bsa_attention_q8_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t D, int32_t K);
 
 /* bsa_sparse_decode_attention over a cache held in 8 bits with one scale per
@@ -390,7 +392,7 @@ size_t bsa_attention_q8_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t
  *   q, out: bf16 [T, H, G, D], 16-byte aligned; k_cache, v_cache: dtype
  *   BSA_DTYPE_E4M3 or BSA_DTYPE_E5M2, [num_pages, 16, H, D], 16-byte aligned,
  *   num_pages < 2^27; k_scale, v_scale: float [num_pages, H], positive; D in
- *   {64, 128, 256}; 1 <= G <= BSA_MAX_ATTN_Q8_GROUP.  The slots of a page
+ *   {64, 128, 256}; 1 <= G <= BSA_MAX_ATTN_Q8_GROUP; T * H <= 2^24.  The slots of a page
  *   past the context may hold anything, NaN codes included.
  *   workspace: at least bsa_attention_q8_workspace_bytes(...) bytes, 256-byte
  *   aligned, any contents; may be NULL when that is 0.  Calls that share a

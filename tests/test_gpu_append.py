@@ -301,3 +301,18 @@ def test_append_offsets_past_32_bits(cuda_device, fmt):
     none = bsa.bsa_append_kv_decode(k[:0], v[:0], far[0], far[1], table[:0].to(dev), seq[:0].to(dev), 1,
                                     **{**args, "q": q[:0]})
     assert none.shape == (0, 3, D)
+
+
+def test_append_strides_of_single_entries_do_not_matter(cuda_device):
+    """One token, one head: whatever strides its dimensions of one entry have."""
+    dev = cuda_device
+    D = 64
+    qkv, table, caches, _, kind = _setup(1, 1, 1, D, 1, 1, "e4m3", 31)
+    seq = torch.tensor([7], dtype=torch.int32)
+    out, kc, vc, ks, vs = _run(dev, "decode", qkv, 1, 1, table, caches, kind, None, None, None, False, (seq, 1))
+    odd = [t.to(dev).contiguous().as_strided((1, 1, D), (5, 3, 1)) for t in qkv.split([1, 1, 1], dim=1)]
+    (k2, s2), (v2, t2) = [(c.to(dev), s.to(dev)) for c, s in caches]
+    got = bsa.bsa_append_kv_decode(odd[1], odd[2], k2, v2, table.to(dev), seq.to(dev), 1, q=odd[0], k_scale=s2, v_scale=t2)
+    torch.cuda.synchronize()
+    for a, b in ((got, out), (k2, kc), (v2, vc), (s2, ks), (t2, vs)):
+        assert torch.equal(a.float().nan_to_num(), b.float().nan_to_num())
