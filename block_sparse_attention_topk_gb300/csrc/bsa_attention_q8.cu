@@ -269,20 +269,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
     __shared__ int box_z[2][C::PAGES];          // page coordinates of the copied chunks
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // the first item's queries and chunk's pages are on their way while the CTA
-    // sets itself up; queries: lane % kLanes holds 8 values of head r * kHeads + lane / kLanes
-    constexpr int kLanes = D / 8, kHeads = 32 / kLanes, kPasses = (GP + kHeads - 1) / kHeads;
-    uint4 queries[kPasses];
-    auto read_queries = [&](int row) {
-#pragma unroll
-        for (int r = 0; r < kPasses; ++r) {
-            const int g = r * kHeads + lane / kLanes;
-            queries[r] = make_uint4(0, 0, 0, 0);
-            if (g < A.G)
-                queries[r] = __ldg(reinterpret_cast<const uint4*>(A.q + ((int64_t)row * A.G + g) * D + lane % kLanes * 8));
-        }
-    };
-    if (warp == kAheadWarp && (int64_t)blockIdx.x < (int64_t)A.rows * A.splits) read_queries(blockIdx.x / A.splits);
+    // the first chunk's pages are on their way while the CTA sets itself up
     Walk<NB> walk;
     if (warp == kCopyWarp || warp == kAheadWarp) walk.begin(A);
     if (warp == kMmaWarp) tmem_alloc(&tmem_base, C::TMEM);
@@ -499,7 +486,9 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         __syncwarp();
     } else if (warp == kAheadWarp) {
         // ------------------------------------------------ scales and queries
-        const int d = lane % kLanes * 8, panel = d / C::ROWB, dc = d % C::ROWB;
+        constexpr int LPH = D / 8;         // lanes per query head, 8 values each
+        constexpr int HPP = 32 / LPH;      // heads a pass
+        const int d = lane % LPH * 8, panel = d / C::ROWB, dc = d % C::ROWB;
         uint32_t c = 0, item = 0;
         int qbuf = 0;
         bool ok = true;
@@ -535,11 +524,20 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     // the queries as two e4m3 terms
                     qbuf = item++ % kDepth;
                     uint8_t* qd = qsm + qbuf * C::Q_BYTES;
+                    constexpr int PASSES = (GP + HPP - 1) / HPP;
+                    uint4 w[PASSES];
 #pragma unroll
-                    for (int r = 0; r < kPasses; ++r) {
-                        const int g = r * kHeads + lane / kLanes;
-                        if (r * kHeads >= A.G) break;
-                        const uint32_t v[4] = {queries[r].x, queries[r].y, queries[r].z, queries[r].w};
+                    for (int r = 0; r < PASSES; ++r) {
+                        const int g = r * HPP + lane / LPH;
+                        w[r] = make_uint4(0, 0, 0, 0);
+                        if (g < A.G)
+                            w[r] = __ldg(reinterpret_cast<const uint4*>(A.q + ((int64_t)it.row * A.G + g) * D + d));
+                    }
+#pragma unroll
+                    for (int r = 0; r < PASSES; ++r) {
+                        const int g = r * HPP + lane / LPH;
+                        if (r * HPP >= A.G) break;
+                        const uint32_t v[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
                         float x[8], m = 0.f;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
@@ -547,7 +545,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                             m = fmaxf(m, fabsf(x[k]));
                         }
 #pragma unroll
-                        for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                        for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
                         // scale by a power of two: the largest magnitude to [128, 256)
                         const int e = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
                         const float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
@@ -570,7 +568,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                                 uint8_t* dst = qd + panel * C::Q_PANEL + row * C::ROWB + (((dc >> 4) ^ sw) << 4) + (dc & 15);
                                 *reinterpret_cast<uint2*>(dst) = make_uint2(t[0] | t[1] << 16, t[2] | t[3] << 16);
                             }
-                            if (lane % kLanes == 0) qinv[qbuf][g] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
+                            if (lane % LPH == 0) qinv[qbuf][g] = __uint_as_float((uint32_t)(127 - 7 + e) << 23);
                         }
                     }
                     if (lane >= A.G && lane < GP) qinv[qbuf][lane] = 0.f;
@@ -587,7 +585,6 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 fence_async_smem();
                 mbar_arrive(&c_full[buf]);
             }
-            if (!walk.done() && walk.c0 == walk.it.b0) read_queries(walk.it.row);
         }
         if (ok) ok = c < kDepth || mbar_wait(&c_empty[c % kDepth], (c / kDepth - 1) & 1, quit);
         __syncwarp();
