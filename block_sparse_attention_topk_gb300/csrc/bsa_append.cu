@@ -12,7 +12,7 @@
 // per value; holding fp32 values would take 64 registers a lane and more).  So a
 // page has one writer, and the result does not depend on how the work is spread.
 // Bound by memory in long calls, where the queries' read and write are the most
-// of it (two 8192-token prompts, 32 query and 4 KV heads of 128, e4m3: 58 us, 5.5
+// of it (two 8192-token prompts, 32 query and 4 KV heads of 128, e4m3: 60 us, 5.3
 // TB/s), and by its chain of dependent loads (length, table entry, scale) in single
 // steps (4 us a token).
 #include <cuda_bf16.h>

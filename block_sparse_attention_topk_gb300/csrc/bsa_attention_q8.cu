@@ -42,7 +42,7 @@
 // keys only reach their own scores.
 //
 // Bound by the copies, 2 D bytes a token: 256 rows of 8192 tokens (8 query heads,
-// D 128) take 87 us, 6.2 TB/s, with DRAM reads of just those bytes; rows whose
+// D 128) take 86 us, 6.3 TB/s, with DRAM reads of just those bytes; rows whose
 // blocks lie in L2 reach 10 TB/s.  64-wide heads are bound by the copies' rows, of
 // 64 bytes each, at about 3.4 cycles a row and SM (1024 rows of up to 2048
 // tokens 47 us); 9 to 16 query heads by the softmax of the SM's one CTA.
@@ -948,7 +948,8 @@ bool sizes_ok(int64_t T, int64_t H, int64_t G, int64_t D) {
 // blocks 256 wide 28 unsplit, 25 in 2; six rows of 1024 blocks 675
 // unsplit, 44 in 25, 57 in 32.  2, 4 or 8 items of a row, all resident at once, are
 // the CTAs of a cluster, which join them through its shared memory (no second
-// launch, no workspace).
+// launch, no workspace): one row of 16 blocks 9.1 us, joined by a launch 10.0; 32 such
+// rows 11.0 and 13.1.
 struct Split {
     int items;         // per row
     bool cluster;      // joined by their cluster

@@ -9,9 +9,9 @@
 //                      where a partner may belong to another thread
 //                      (kSplitAny).  Many small CTAs
 //                      hide the loads: ten of 128 threads per SM with a slot
-//                      each in flight take 67 us where four of 256 with two
+//                      each in flight take 68 us where four of 256 with two
 //                      slots take 73 and two with four slots 85 (24 heads of
-//                      128, 32760 tokens, bf16: 6.0 TB/s),
+//                      128, 32760 tokens, bf16: 5.9 TB/s),
 //  rope_kernel         pair by pair: any alignment, in place.
 #include <cuda_runtime.h>
 #include <stdint.h>
