@@ -5,9 +5,10 @@
 // sines are formed once in shared memory and serve every head.  The work is
 // bound by memory: one read and one write of each element.
 //  rope_slots_kernel   16-byte loads and stores (rows and strides aligned to
-//                      16 bytes, D a multiple of two groups); not in place
-//                      where a partner may belong to another thread
-//                      (kSplitAny).  Many small CTAs
+//                      16 bytes, D a multiple of two groups), or 8-byte ones of
+//                      bf16 where rows or half-split partners are only that
+//                      aligned; not in place where a partner may belong to
+//                      another thread (kSplitAny).  Many small CTAs
 //                      hide the loads: ten of 128 threads per SM with a slot
 //                      each in flight take 68 us where four of 256 with two
 //                      slots take 73 and two with four slots 85 (24 heads of
@@ -57,9 +58,29 @@ __device__ __forceinline__ void rope_table(const RopeArgs& A, int64_t t0, int nt
     __syncthreads();
 }
 
-template <RopeMode MODE, typename E>
+// GE elements as they are loaded and stored: 16 bytes, or 8 bytes of bf16.
+template <typename E, int GE>
+struct Group {
+    using V = uint4;
+    __device__ static void widen(const V& v, float (&f)[GE]) { widen16(v, f); }
+    __device__ static V narrow(const float (&f)[GE]) { return narrow16(f); }
+};
+template <>
+struct Group<uint16_t, 4> {
+    using V = uint2;
+    __device__ static void widen(const V& v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x << 16);
+        f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        f[2] = __uint_as_float(v.y << 16);
+        f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+    __device__ static V narrow(const float (&f)[4]) { return make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])); }
+};
+
+template <RopeMode MODE, typename E, int GE>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_slots_kernel(const RopeArgs A) {
-    constexpr int GE = 16 / (int)sizeof(E);
+    using G = Group<E, GE>;
+    using V = typename G::V;
     extern __shared__ __align__(16) unsigned char smem[];
     float* cs = reinterpret_cast<float*>(smem);
     const int half = A.r.half;
@@ -74,13 +95,13 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_slots_kernel(con
     int h = th % A.H, t = th / A.H;
     const int dk = kRopeThreads % ks, dth = kRopeThreads / ks;
     const int dh = dth % A.H, dt = dth / A.H;
-    uint4 a, b;
+    V a, b;
     auto load = [&]() {
         const E* xr = x + (t0 + t) * A.xts + h * A.xhs;
         int o0, o1;
         slot_groups<MODE, GE>(k, half, o0, o1);
-        a = *reinterpret_cast<const uint4*>(xr + o0);
-        b = *reinterpret_cast<const uint4*>(xr + o1);
+        a = *reinterpret_cast<const V*>(xr + o0);
+        b = *reinterpret_cast<const V*>(xr + o1);
     };
     // the first slot is on its way while the table is formed
     if ((int)threadIdx.x < total) load();
@@ -90,13 +111,13 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_slots_kernel(con
         const E* xr = x + (t0 + t) * A.xts + h * A.xhs;
         E* orow = out + (t0 + t) * A.ots + h * A.ohs;
         float fa[GE], fb[GE];
-        widen16(a, fa);
-        widen16(b, fb);
+        G::widen(a, fa);
+        G::widen(b, fb);
         slot_rotate<MODE>(xr, k, cs + t * 2 * rope_pad(half), half, fa, fb);
         int o0, o1;
         slot_groups<MODE, GE>(k, half, o0, o1);
-        *reinterpret_cast<uint4*>(orow + o0) = narrow16(fa);
-        *reinterpret_cast<uint4*>(orow + o1) = narrow16(fb);
+        *reinterpret_cast<V*>(orow + o0) = G::narrow(fa);
+        *reinterpret_cast<V*>(orow + o1) = G::narrow(fb);
         k += dk;
         h += dh;
         t += dt;
@@ -156,16 +177,34 @@ void launch_rope(const RopeArgs& A, cudaStream_t st) {
     const int half = A.r.half;
     const size_t smem = (size_t)A.tile * 2 * rope_pad(half) * sizeof(float) + half * sizeof(unsigned long long);
     const unsigned grid = (unsigned)((A.T + A.tile - 1) / A.tile);
-    const bool wide = A.D % (2 * GE) == 0 &&
-                      ((A.xts | A.xhs | A.ots | A.ohs) % GE) == 0 &&
-                      ((reinterpret_cast<uintptr_t>(A.x) | reinterpret_cast<uintptr_t>(A.out)) & 15) == 0;
+    // the rows lie at multiples of ge elements, and are whole slots of them
+    auto rows_of = [&](int ge) {
+        return A.D % (2 * ge) == 0 && ((A.xts | A.xhs | A.ots | A.ohs) % ge) == 0 &&
+               ((reinterpret_cast<uintptr_t>(A.x) | reinterpret_cast<uintptr_t>(A.out)) & (ge * sizeof(E) - 1)) == 0;
+    };
+    const bool wide = rows_of(GE);
     const RopeMode mode = rope_mode(A.r, GE);
-    if (wide && mode == kSplit)
-        rope_slots_kernel<kSplit, E><<<grid, kRopeThreads, smem, st>>>(A);
-    else if (wide && mode == kInterleaved)
-        rope_slots_kernel<kInterleaved, E><<<grid, kRopeThreads, smem, st>>>(A);
-    else if (wide && A.x != A.out)
-        rope_slots_kernel<kSplitAny, E><<<grid, kRopeThreads, smem, st>>>(A);
+    if (wide && mode == kSplit) {
+        rope_slots_kernel<kSplit, E, GE><<<grid, kRopeThreads, smem, st>>>(A);
+        return;
+    }
+    if (wide && mode == kInterleaved) {
+        rope_slots_kernel<kInterleaved, E, GE><<<grid, kRopeThreads, smem, st>>>(A);
+        return;
+    }
+    // Groups of 8 bytes: 24 heads of 72, 19112 tokens, take 36 us half-split and 32
+    // interleaved, 79 pair by pair; 24 heads of 128 with 104 rotated half-split,
+    // 32760 tokens, 86 where single partners (kSplitAny) take 123.
+    if constexpr (GE == 8) {
+        const RopeMode narrow_mode = rope_mode(A.r, 4);
+        if (rows_of(4) && narrow_mode != kSplitAny) {
+            if (narrow_mode == kSplit) rope_slots_kernel<kSplit, E, 4><<<grid, kRopeThreads, smem, st>>>(A);
+            else rope_slots_kernel<kInterleaved, E, 4><<<grid, kRopeThreads, smem, st>>>(A);
+            return;
+        }
+    }
+    if (wide && A.x != A.out)
+        rope_slots_kernel<kSplitAny, E, GE><<<grid, kRopeThreads, smem, st>>>(A);
     else
         rope_kernel<E><<<grid, kRopeThreads, smem, st>>>(A);
 }

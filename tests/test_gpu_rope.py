@@ -141,3 +141,30 @@ def test_rope_special_values_and_streams(cuda_device):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out.nan_to_num(5, 6, 7), got.nan_to_num(5, 6, 7))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,H,D,rot,offset", [
+    (1, 1, 8, 8, 0), (301, 3, 72, 72, 0), (37, 5, 72, 64, 4), (33, 2, 80, 72, 4), (9, 4, 136, 40, 0),
+    (2050, 2, 64, 24, 4), (5, 1, 1016, 1016, 4), (65, 3, 128, 104, 0), (12, 2, 88, 0, 4), (12, 2, 72, 62, 4),
+])
+def test_rope_rows_at_multiples_of_8_bytes(cuda_device, T, H, D, rot, offset, interleaved):
+    """bf16 rows that start at odd multiples of 8 bytes, or pairs whose distance
+    is one: out of place, and in place with the same bits."""
+    x, pos, inv, axis = _case(T, H, D, rot, 2, torch.bfloat16, T + D + rot + offset)
+    dev = cuda_device
+    fused = torch.full((T, H * D + 12), 9.0, dtype=torch.bfloat16, device=dev)
+    view = fused[:, offset:offset + H * D].unflatten(1, (H, D))
+    view.copy_(x.to(dev))
+    dp, di, da = pos.to(dev), inv.to(dev), axis.to(dev)
+    for inverse in (False, True):
+        got = bsa.bsa_rope(view, dp, di, da, interleaved=interleaved, inverse=inverse)
+        torch.cuda.synchronize()
+        want = oracle.rope(x.double().numpy(), pos.numpy(), inv.numpy(), axis.numpy(), interleaved, inverse)
+        err = np.abs(got.double().cpu().numpy() - want)
+        assert (err <= bound(x.double().numpy(), want, 1 << 20, True)).all(), err.max()
+        assert torch.equal(got[..., rot:], view[..., rot:])
+    bsa.bsa_rope(view, dp, di, da, interleaved=interleaved, inverse=True, out=view)
+    torch.cuda.synchronize()
+    assert torch.equal(view, got)
+    assert (fused[:, :offset] == 9).all() and (fused[:, offset + H * D:] == 9).all()
