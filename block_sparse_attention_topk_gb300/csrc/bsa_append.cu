@@ -62,6 +62,13 @@ struct Code {
         const float2 x = __half22float2(lo), y = __half22float2(hi);
         return pack(x.x * f, x.y * f, y.x * f, y.y * f);
     }
+    __device__ __forceinline__ static void store(uint8_t* d, const float (&f)[8], float inv) {
+        *reinterpret_cast<uint2*>(d) = make_uint2(pack(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                                                  pack(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+    }
+    __device__ __forceinline__ static void store(uint8_t* d, const float (&f)[4], float inv) {
+        *reinterpret_cast<uint32_t*>(d) = pack(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+    }
     // scale of the largest magnitude (0: none)
     __device__ static float scale(float amax) {
         if (!(amax > 0.f)) return 0.f;
@@ -112,13 +119,16 @@ struct Segment {
     int32_t n, off;   // tokens, first slot
 };
 
-// One page's n tokens of one head, rows x + t * ts, into slots [off, off + n).
-template <int FMT, RopeMode MODE, bool KEEP>
+// One page's n tokens of one head, rows x + t * ts, into slots [off, off + n),
+// by groups of GE elements.
+template <int FMT, RopeMode MODE, int GE, bool KEEP>
 __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t* __restrict__ x, int64_t ts,
                                            const Segment& S, int h, const float* cs, bool rotate, void* cache,
                                            float* scales) {
+    using G = Group<uint16_t, GE>;
+    using V = typename G::V;
     const int lane = threadIdx.x & 31;
-    const int D = (int)P.a.D, ks = D / 16, half = rotate ? P.r.half : 0;
+    const int D = (int)P.a.D, ks = D / (2 * GE), half = rotate ? P.r.half : 0;
     const int64_t row = P.a.H * D;
     const int64_t base = S.page * kPageRows * row + (int64_t)h * D + S.off * row;
     float* sp = FMT == BSA_DTYPE_BF16 ? nullptr : scales + S.page * P.a.H + h;
@@ -126,7 +136,7 @@ __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t
     if (FMT != BSA_DTYPE_BF16 && S.off > 0) old = *sp;
     const int total = S.n * ks;     // slots of the page's tokens
     struct Batch {
-        uint4 a[kPageBatch], b[kPageBatch];
+        V a[kPageBatch], b[kPageBatch];
         int at[kPageBatch];         // token << 8 | slot
     };
     auto load = [&](int i, Batch& B) {
@@ -135,9 +145,9 @@ __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t
             const int u = min(i + 32 * j, total - 1);
             const int t = u / ks, k = u - t * ks;
             int o0, o1;
-            slot_groups<MODE, 8>(k, half, o0, o1);
-            B.a[j] = __ldg(reinterpret_cast<const uint4*>(x + t * ts + o0));
-            B.b[j] = __ldg(reinterpret_cast<const uint4*>(x + t * ts + o1));
+            slot_groups<MODE, GE>(k, half, o0, o1);
+            B.a[j] = __ldg(reinterpret_cast<const V*>(x + t * ts + o0));
+            B.b[j] = __ldg(reinterpret_cast<const V*>(x + t * ts + o1));
             B.at[j] = t << 8 | k;
         }
     };
@@ -155,30 +165,30 @@ __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t
             for (int j = 0; j < kPageBatch; ++j) {
                 if (i + 32 * j >= total) break;
                 const int t = B.at[j] >> 8, k = B.at[j] & 255;
-                float fa[8], fb[8];
-                widen16(B.a[j], fa);
-                widen16(B.b[j], fb);
+                float fa[GE], fb[GE];
+                G::widen(B.a[j], fa);
+                G::widen(B.b[j], fb);
                 slot_rotate<MODE>(x + t * ts, k, cs + t * 2 * rope_pad(P.r.half), half, fa, fb);
                 int o0, o1;
-                slot_groups<MODE, 8>(k, half, o0, o1);
+                slot_groups<MODE, GE>(k, half, o0, o1);
                 f(t, o0, o1, fa, fb);
             }
         }
     };
     if constexpr (FMT == BSA_DTYPE_BF16) {
         uint16_t* c = static_cast<uint16_t*>(cache) + base;
-        visit([&](int t, int o0, int o1, const float(&fa)[8], const float(&fb)[8]) {
+        visit([&](int t, int o0, int o1, const float(&fa)[GE], const float(&fb)[GE]) {
             uint16_t* d = c + t * row;
-            *reinterpret_cast<uint4*>(d + o0) = narrow16(fa);
-            *reinterpret_cast<uint4*>(d + o1) = narrow16(fb);
+            *reinterpret_cast<V*>(d + o0) = G::narrow(fa);
+            *reinterpret_cast<V*>(d + o1) = G::narrow(fb);
         });
     } else {
         using F = Code<FMT>;
         uint8_t* c = static_cast<uint8_t*>(cache) + base;
         float m = 0.f;
-        visit([&](int, int, int, const float(&fa)[8], const float(&fb)[8]) {
+        visit([&](int, int, int, const float(&fa)[GE], const float(&fb)[GE]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < GE; ++e) {
                 const float u = fabsf(fa[e]), v = fabsf(fb[e]);
                 if (u <= 3.402823466e38f) m = fmaxf(m, u);      // finite values only
                 if (v <= 3.402823466e38f) m = fmaxf(m, v);
@@ -204,21 +214,17 @@ __device__ __forceinline__ void store_page(const AppendParams& P, const uint16_t
             }
         }
         const float inv = 1.f / s;      // exact: s is a power of two
-        visit([&](int t, int o0, int o1, const float(&fa)[8], const float(&fb)[8]) {
+        visit([&](int t, int o0, int o1, const float(&fa)[GE], const float(&fb)[GE]) {
             uint8_t* d = c + t * row;
-            *reinterpret_cast<uint2*>(d + o0) =
-                make_uint2(F::pack(fa[0] * inv, fa[1] * inv, fa[2] * inv, fa[3] * inv),
-                           F::pack(fa[4] * inv, fa[5] * inv, fa[6] * inv, fa[7] * inv));
-            *reinterpret_cast<uint2*>(d + o1) =
-                make_uint2(F::pack(fb[0] * inv, fb[1] * inv, fb[2] * inv, fb[3] * inv),
-                           F::pack(fb[4] * inv, fb[5] * inv, fb[6] * inv, fb[7] * inv));
+            F::store(d + o0, fa, inv);
+            F::store(d + o1, fb, inv);
         });
         __syncwarp();                    // every lane has read the old scale
         if (lane == 0) *sp = s;
     }
 }
 
-template <int FMT, RopeMode MODE, bool KEEP>
+template <int FMT, RopeMode MODE, int GE, bool KEEP>
 __global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppendCtas) append_kernel(const AppendParams P) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ Row rows[kAppendTile];
@@ -281,16 +287,18 @@ __global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppe
         const int64_t t = t0 + S.row;
         const float* c = cs + S.row * 2 * rope_pad(half);
         if (side == 0)
-            store_page<FMT, MODE, KEEP>(P, static_cast<const uint16_t*>(P.a.k) + t * P.a.k_token_stride + h * P.a.k_head_stride,
+            store_page<FMT, MODE, GE, KEEP>(P, static_cast<const uint16_t*>(P.a.k) + t * P.a.k_token_stride + h * P.a.k_head_stride,
                                        P.a.k_token_stride, S, h, c, true, P.a.k_cache, P.a.k_scale);
         else
-            store_page<FMT, kSplit, KEEP>(P, static_cast<const uint16_t*>(P.a.v) + t * P.a.v_token_stride + h * P.a.v_head_stride,
+            store_page<FMT, kSplit, 8, KEEP>(P, static_cast<const uint16_t*>(P.a.v) + t * P.a.v_token_stride + h * P.a.v_head_stride,
                                       P.a.v_token_stride, S, h, c, false, P.a.v_cache, P.a.v_scale);
     }
     // ---- queries: slots of two groups ----
     if (P.a.q == nullptr) return;
+    using G = Group<uint16_t, GE>;
+    using V = typename G::V;
     constexpr int B = kQueryBatch;
-    const int ks = D / 16, Hq = (int)P.a.Hq, total = nt * Hq * ks;
+    const int ks = D / (2 * GE), Hq = (int)P.a.Hq, total = nt * Hq * ks;
     const uint16_t* __restrict__ q = static_cast<const uint16_t*>(P.a.q) + t0 * P.a.q_token_stride;
     uint16_t* __restrict__ o = static_cast<uint16_t*>(P.a.q_out) + t0 * Hq * D;
     // (row, head, slot) of this thread, advanced by the CTA's width; the
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppe
     const int dk = kAppendThreads % ks, dth = kAppendThreads / ks;
     const int dh = Hq > 0 ? dth % Hq : 0, dt = Hq > 0 ? dth / Hq : 0;
     for (int i = first; i < total; i += B * kAppendThreads) {
-        uint4 a[B], b[B];
+        V a[B], b[B];
         int kk[B], tt[B], hh[B];
 #pragma unroll
         for (int j = 0; j < B; ++j) {
@@ -311,9 +319,9 @@ __global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppe
             if (i + j * kAppendThreads < total) {
                 const uint16_t* xr = q + t * P.a.q_token_stride + h * P.a.q_head_stride;
                 int o0, o1;
-                slot_groups<MODE, 8>(k, half, o0, o1);
-                a[j] = __ldg(reinterpret_cast<const uint4*>(xr + o0));
-                b[j] = __ldg(reinterpret_cast<const uint4*>(xr + o1));
+                slot_groups<MODE, GE>(k, half, o0, o1);
+                a[j] = __ldg(reinterpret_cast<const V*>(xr + o0));
+                b[j] = __ldg(reinterpret_cast<const V*>(xr + o1));
             }
             k += dk;
             h += dh;
@@ -333,29 +341,33 @@ __global__ void __launch_bounds__(kAppendThreads, KEEP ? kAppendCtas / 2 : kAppe
             const uint16_t* xr = q + tt[j] * P.a.q_token_stride + hh[j] * P.a.q_head_stride;
             uint16_t* orow = o + ((int64_t)tt[j] * Hq + hh[j]) * D;
             int o0, o1;
-            slot_groups<MODE, 8>(kk[j], half, o0, o1);
+            slot_groups<MODE, GE>(kk[j], half, o0, o1);
             if (rows[tt[j]].pos < 0) {
                 // padding: zeros, whatever the query holds
-                *reinterpret_cast<uint4*>(orow + o0) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(orow + o1) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<V*>(orow + o0) = V{};
+                *reinterpret_cast<V*>(orow + o1) = V{};
                 continue;
             }
-            float fa[8], fb[8];
-            widen16(a[j], fa);
-            widen16(b[j], fb);
+            float fa[GE], fb[GE];
+            G::widen(a[j], fa);
+            G::widen(b[j], fb);
             slot_rotate<MODE>(xr, kk[j], cs + tt[j] * 2 * rope_pad(half), half, fa, fb);
-            *reinterpret_cast<uint4*>(orow + o0) = narrow16(fa);
-            *reinterpret_cast<uint4*>(orow + o1) = narrow16(fb);
+            *reinterpret_cast<V*>(orow + o0) = G::narrow(fa);
+            *reinterpret_cast<V*>(orow + o1) = G::narrow(fb);
         }
     }
 }
 
+// Half-split pairs whose distance is a multiple of 4 go by groups of 4 (two
+// 8192-token prompts with 104 of 128 rotated 72 us, by single partners 128; 1452
+// decode rows with 40 of 64 rotated 8.0 and 19.1).
 template <int FMT, bool KEEP>
 cudaError_t launch_mode(const AppendParams& P, unsigned grid, size_t smem, cudaStream_t st) {
     const RopeMode mode = rope_mode(P.r, 8);
-    if (mode == kSplit) append_kernel<FMT, kSplit, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
-    else if (mode == kInterleaved) append_kernel<FMT, kInterleaved, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
-    else append_kernel<FMT, kSplitAny, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
+    if (mode == kSplit) append_kernel<FMT, kSplit, 8, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
+    else if (mode == kInterleaved) append_kernel<FMT, kInterleaved, 8, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
+    else if (rope_mode(P.r, 4) == kSplit) append_kernel<FMT, kSplit, 4, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
+    else append_kernel<FMT, kSplitAny, 8, KEEP><<<grid, kAppendThreads, smem, st>>>(P);
     return cudaGetLastError();
 }
 

@@ -58,25 +58,6 @@ __device__ __forceinline__ void rope_table(const RopeArgs& A, int64_t t0, int nt
     __syncthreads();
 }
 
-// GE elements as they are loaded and stored: 16 bytes, or 8 bytes of bf16.
-template <typename E, int GE>
-struct Group {
-    using V = uint4;
-    __device__ static void widen(const V& v, float (&f)[GE]) { widen16(v, f); }
-    __device__ static V narrow(const float (&f)[GE]) { return narrow16(f); }
-};
-template <>
-struct Group<uint16_t, 4> {
-    using V = uint2;
-    __device__ static void widen(const V& v, float (&f)[4]) {
-        f[0] = __uint_as_float(v.x << 16);
-        f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-        f[2] = __uint_as_float(v.y << 16);
-        f[3] = __uint_as_float(v.y & 0xFFFF0000u);
-    }
-    __device__ static V narrow(const float (&f)[4]) { return make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])); }
-};
-
 template <RopeMode MODE, typename E, int GE>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_slots_kernel(const RopeArgs A) {
     using G = Group<E, GE>;

@@ -83,6 +83,25 @@ __device__ __forceinline__ uint4 narrow16(const float (&f)[8]) {
 __device__ __forceinline__ uint4 narrow16(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
+// GE elements as they are loaded and stored: 16 bytes, or 8 bytes of bf16.
+template <typename E, int GE>
+struct Group {
+    using V = uint4;
+    __device__ __forceinline__ static void widen(const V& v, float (&f)[GE]) { widen16(v, f); }
+    __device__ __forceinline__ static V narrow(const float (&f)[GE]) { return narrow16(f); }
+};
+template <>
+struct Group<uint16_t, 4> {
+    using V = uint2;
+    __device__ __forceinline__ static void widen(const V& v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x << 16);
+        f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        f[2] = __uint_as_float(v.y << 16);
+        f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ static V narrow(const float (&f)[4]) { return make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])); }
+};
+
 __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ float widen(float f) { return f; }
 

@@ -316,3 +316,26 @@ def test_append_strides_of_single_entries_do_not_matter(cuda_device):
     torch.cuda.synchronize()
     for a, b in ((got, out), (k2, kc), (v2, vc), (s2, ks), (t2, vs)):
         assert torch.equal(a.float().nan_to_num(), b.float().nan_to_num())
+
+
+@pytest.mark.parametrize("fmt", list(TYPES))
+@pytest.mark.parametrize("lens,pre,H,Hq,D,rot,axes", [
+    ([15, 0, 17, 1], [1, 3, 31, 255], 2, 4, 128, 104, 3), ([300, 7, 129], [5, 120, 0], 1, 3, 80, 72, 1),
+    ([1], [47], 1, 8, 64, 24, 1), ([64, 33], [64, 7], 3, 0, 256, 232, 2), ([200], [-20], 1, 1, 16, 8, 1),
+    ([311] * 17, list(range(17)), 1, 2, 64, 56, 1),
+])
+def test_append_pairs_at_multiples_of_four(cuda_device, fmt, lens, pre, H, Hq, D, rot, axes):
+    """Half-split pairs whose distance is a multiple of 4 and not of 8, in short
+    calls and in one with 16 rows per CTA."""
+    assert rot // 2 % 8 == 4
+    B, MB = len(lens), 4
+    T = sum(lens) + 5
+    qkv, table, caches, _, kind = _setup(T, H, Hq, D, B, MB, fmt, T + D + rot)
+    cu = torch.tensor([2] + lens).cumsum(0).to(torch.int32)
+    g = torch.Generator().manual_seed(T)
+    positions = axis = None
+    if axes > 1:
+        positions = torch.randint(0, 100000, (axes, T), generator=g, dtype=torch.int32)
+        axis = torch.randint(0, axes, (rot // 2,), generator=g, dtype=torch.int32)
+    _compare(cuda_device, "varlen", qkv, H, Hq, D, table, caches, kind, rot, axes, False,
+             (cu, torch.tensor(pre, dtype=torch.int32)), positions, axis)
