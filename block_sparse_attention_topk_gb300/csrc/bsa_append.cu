@@ -371,14 +371,30 @@ cudaError_t launch_mode(const AppendParams& P, unsigned grid, size_t smem, cudaS
     return cudaGetLastError();
 }
 
-// With fewer rows per CTA than a page the CTAs do not fill the SMs: registers
-// are free to keep what was read.  In long calls four CTAs per SM that read
-// the tokens twice, the second time from L1, are faster than two that keep
-// them (two 8192-token prompts 60 against 63 us); in the production decode step
-// (256 rows) keeping takes 4.9 us, reading twice 5.4.
 template <int FMT>
-cudaError_t launch_format(const AppendParams& P, unsigned grid, size_t smem, cudaStream_t st) {
-    return P.tile < kAppendTile ? launch_mode<FMT, true>(P, grid, smem, st) : launch_mode<FMT, false>(P, grid, smem, st);
+cudaError_t launch_format(const AppendParams& P, bool keep, unsigned grid, size_t smem, cudaStream_t st) {
+    return keep ? launch_mode<FMT, true>(P, grid, smem, st) : launch_mode<FMT, false>(P, grid, smem, st);
+}
+
+// Rows per CTA, and whether its lanes keep what they read of the tokens or read
+// it twice, the second time from L1.  Keeping takes registers for two CTAs per SM,
+// reading twice leaves four.  So calls whose CTAs of up to 8 rows fit at two
+// per SM keep, in CTAs of as few rows as fit; longer ones do not, in CTAs of 8
+// rows while those fit at four per SM, then of 16, a page's.  A sixteenth more than fits
+// still counts as fitting: the CTAs left over are few and start early.
+// (4 KV x 8 query heads of 128, e4m3, us, kept / not: 256 production rows 4.9 / 5.4;
+// 2500 rows, 8 per CTA, 16.6 / 19.0; 3360 rows, 8 per CTA, 22.4 / 19.9; two 8192-token
+// prompts 63 / 60.  750 rows kept, 2 and 4 per CTA, 10.9 and 9.2; 4758 rows not
+// kept, 8 and 16 per CTA, 23.8 and 28.3; 8547 rows 38.8 and 37.1.)
+struct Tiling {
+    int rows;
+    bool keep;
+};
+Tiling pick_tiling(int64_t T, int64_t sms) {
+    auto fits = [&](int rows, int64_t ctas) { return (T + rows - 1) / rows <= sms * ctas * 17 / 16; };
+    for (int rows = 1; rows < kAppendTile; rows *= 2)
+        if (fits(rows, kAppendCtas / 2)) return {rows, true};
+    return {fits(kAppendTile / 2, kAppendCtas) ? kAppendTile / 2 : kAppendTile, false};
 }
 
 int check_append(const bsa_append_args_t* a) {
@@ -425,17 +441,15 @@ int launch_append(AppendParams& P, cudaStream_t st) {
                      (P.a.flags & BSA_ROPE_INTERLEAVED) != 0, (P.a.flags & BSA_ROPE_INVERSE) != 0};
     P.status = current_status_word();
     if (P.a.q == nullptr) P.a.Hq = 0;
-    // rows per CTA: a page's worth in long calls, fewer while SMs would idle
-    int tile = kAppendTile;
-    const int64_t want = 2 * (int64_t)device_sm_count();
-    while (tile > 1 && (P.a.T + tile - 1) / tile < want) tile /= 2;
+    const Tiling tiling = pick_tiling(P.a.T, device_sm_count());
+    const int tile = tiling.rows;
     P.tile = tile;
     const size_t smem = (size_t)(tile + kPageRows - 1) * 2 * rope_pad(P.r.half) * sizeof(float) + P.r.half * sizeof(unsigned long long);
     const unsigned grid = (unsigned)((P.a.T + tile - 1) / tile);
     cudaError_t e;
-    if (P.a.cache_dtype == BSA_DTYPE_BF16) e = launch_format<BSA_DTYPE_BF16>(P, grid, smem, st);
-    else if (P.a.cache_dtype == BSA_DTYPE_E4M3) e = launch_format<BSA_DTYPE_E4M3>(P, grid, smem, st);
-    else e = launch_format<BSA_DTYPE_E5M2>(P, grid, smem, st);
+    if (P.a.cache_dtype == BSA_DTYPE_BF16) e = launch_format<BSA_DTYPE_BF16>(P, tiling.keep, grid, smem, st);
+    else if (P.a.cache_dtype == BSA_DTYPE_E4M3) e = launch_format<BSA_DTYPE_E4M3>(P, tiling.keep, grid, smem, st);
+    else e = launch_format<BSA_DTYPE_E5M2>(P, tiling.keep, grid, smem, st);
     return e == cudaSuccess ? BSA_OK : (int)e;
 }
 

@@ -339,3 +339,15 @@ def test_append_pairs_at_multiples_of_four(cuda_device, fmt, lens, pre, H, Hq, D
         axis = torch.randint(0, axes, (rot // 2,), generator=g, dtype=torch.int32)
     _compare(cuda_device, "varlen", qkv, H, Hq, D, table, caches, kind, rot, axes, False,
              (cu, torch.tensor(pre, dtype=torch.int32)), positions, axis)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [323, 324, 647, 1293, 2584, 2590, 3000, 5168, 5175, 9000])
+def test_append_calls_of_every_length(cuda_device, fmt, T):
+    """One KV head in calls on both sides of each number of rows per CTA."""
+    lens = [449] * (T // 449) + [T % 449]
+    pre = [(7 * i) % 60 for i in range(len(lens))]
+    qkv, table, caches, _, kind = _setup(T + 5, 1, 1, 16, len(lens), 4, fmt, T)
+    cu = torch.tensor([2] + lens).cumsum(0).to(torch.int32)
+    _compare(cuda_device, "varlen", qkv, 1, 1, 16, table, caches, kind, 16, 1, False,
+             (cu, torch.tensor(pre, dtype=torch.int32)), None, None)
