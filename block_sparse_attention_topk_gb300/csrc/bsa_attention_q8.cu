@@ -9,14 +9,23 @@
 // Both products run on the tensor core on the cached codes as they are, with
 // no widening pass: the tokens (or, for the values, the head's dimensions) are
 // the 128 rows of a tcgen05 f8 MMA and the G query heads its few columns.  The
-// other operand is made 8-bit too, as a sum of two terms in their own
-// columns, x = hi + lo / 16 with hi = e4m3(x), lo = e4m3(16 (x - hi)).
-//  - A bf16 query has 8 significant bits; scaled by a power of two so that the
-//    head's largest magnitude lies in [128, 256), hi takes 4 of them and the
-//    rounded rest of at most 2^-4 fits lo: exact down to 2^-21 of the largest.
-//  - A probability keeps a relative error below 2^-8 (bf16's), down to 2^-22
-//    of the row's largest p_j vs_j, which is scaled to 256.
-// The sums, maxima and accumulators are fp32.
+// other operand is made 8-bit too, as a sum of terms in their own columns.
+//  - A query is two e4m3 terms, x = hi + lo / 16 with hi = e4m3(x), lo =
+//    e4m3(16 (x - hi)).  A bf16 query has 8 significant bits; scaled by a power of
+//    two so that the head's largest magnitude lies in [128, 256), hi takes 4 of
+//    them and the rounded rest of at most 2^-4 fits lo: exact down to 2^-21 of the
+//    largest.
+//  - A weight w_j = p_j vs_j, scaled so that the chunk's largest is 2^15, is
+//    rounded to fp16 and cut into four e5m2 terms of three bits each, the last two
+//    64-fold: they hold the fp16 value exactly down to 2^-27 of the chunk's
+//    largest (so w_j within 2^-12 of itself), and within 2^-37 of that below.
+//    e5m2 has that range, e4m3 would end at 2^-22: a token that takes the probability
+//    and has no value, or a page with a larger scale than others, leaves the others'
+//    weights their bits.  A page of zeros (the append gives it the scale 1) whose scale
+//    is far above the chunk's least takes that one instead, as its codes are zero
+//    under any scale.
+// Probabilities are summed in fp32 before their rounding, chunks are joined in
+// fp32, and maxima and accumulators are fp32.
 //
 // The work: a CTA takes items (a row, or a share of its 128-token blocks when
 // rows are few; a cluster of CTAs or a second launch joins the shares) and walks each in chunks of up to 6 blocks.  A chunk's scores are
@@ -42,12 +51,13 @@
 // keys only reach their own scores.
 //
 // Bound by the copies, 2 D bytes a token: 256 rows of 8192 tokens (8 query heads,
-// D 128) take 86 us, 6.3 TB/s, with DRAM reads of just those bytes; rows whose
+// D 128) take 86 to 88 us, 6.2 TB/s, with DRAM reads of just those bytes; rows whose
 // blocks lie in L2 reach 10 TB/s.  64-wide heads are bound by the copies' rows, of
 // 64 bytes each, at about 3.4 cycles a row and SM (1024 rows of up to 2048
 // tokens 47 us); 9 to 16 query heads by the softmax of the SM's one CTA.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -61,9 +71,33 @@ namespace bsa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kDepth = 4;                // chunks announced ahead
+constexpr int kDepth = 3;                // chunks announced ahead
+constexpr int kMaxRing = 12;             // stages of 16 KB
 constexpr int kMaxCluster = 8;           // items per row that a cluster joins
 constexpr int kSmSmem = 233472;          // an SM's shared memory; 1 KB of it goes to each CTA
+constexpr int kTerms = 4;                // terms of a weight
+constexpr float kTop = 15.f;             // log2 of a chunk's largest weight as it is rounded
+constexpr float kSpread = 65536.f;       // scales this much above the chunk's least may be a page of zeros
+
+// A chunk as it is announced to the other warps.
+struct Chunk {
+    int row, ctx, c0, nb;    // nb < 0: no more
+    int item, qbuf, last;
+    float mid;               // log2 of the value scales' middle
+};
+
+template <int PAGES, int GP, int NU, int GROUPS, int HG>
+struct Q8Shared {
+    float2 page_scale[kDepth][PAGES];       // ks * scale * log2 e, log2 vs (-inf: no page) of the announced chunks
+    uint64_t full[kMaxRing], empty[kMaxRing], s_full[2][NU], p_full[NU], c_full[kDepth], c_empty[kDepth];
+    uint64_t o_full, drained;
+    Chunk chunk[kDepth];
+    float qinv[kDepth][GP];
+    float red[GROUPS][4][HG];
+    int box_z[2][PAGES];                    // page coordinates of the copied chunks
+    uint32_t tmem_base;
+    int gave_up;
+};
 
 template <int D, int GP>
 struct Q8Cfg {
@@ -72,7 +106,8 @@ struct Q8Cfg {
     static constexpr int CTAS = GROUPS == 1 ? 2 : 1;  // per SM
     static constexpr int SOFTMAX = 128 * GROUPS;
     static constexpr int THREADS = SOFTMAX + 96;
-    static constexpr int N = GP <= 8 ? 16 : 32;       // MMA columns: two terms of each head
+    static constexpr int N = GP <= 8 ? 16 : 32;       // MMA columns of the scores: two terms of each head
+    static constexpr int NP = kTerms * GP;            // of the outputs: four terms
     static constexpr int NB = 6;                      // blocks per chunk
     static constexpr int S_COLS = NB * N;             // TMEM columns of a chunk's scores
     static constexpr int TMEM = 512 / CTAS;
@@ -82,25 +117,26 @@ struct Q8Cfg {
     static constexpr int BPS = ROWB == 64 ? 2 : 1;    // blocks per ring stage
     static constexpr int STAGE = BPS * PANEL;         // 16 KB
     static constexpr int NU = NB / 2;                 // pairs of blocks: the warps' handshakes are a pair's
-    static constexpr int P_BYTES = NB * N * 128;
+    static constexpr int P_BYTES = NB * NP * 128;
     static constexpr int Q_PANEL = N * ROWB;
     static constexpr int Q_BYTES = PANELS * Q_PANEL;
     static constexpr int PAGES = NB * kPagesPerBlock;
-    static constexpr int STATIC = kDepth * (PAGES + 4) * 16 + 1664;   // scales, barriers and the rest
-    static constexpr int FIXED = P_BYTES + kDepth * Q_BYTES + 1024;
-    static constexpr int RING = (kSmSmem / CTAS - 1024 - STATIC - FIXED) / STAGE;
+    using Shared = Q8Shared<PAGES, GP, NU, GROUPS, HG>;
+    static constexpr int FIXED = P_BYTES + kDepth * Q_BYTES + (int)sizeof(Shared);
+    static constexpr int RING = (kSmSmem / CTAS - 1024 - FIXED) / STAGE;
     static constexpr int SMEM = RING * STAGE + FIXED;
     static constexpr uint32_t SWIZZLE = ROWB == 128 ? 2 : 4;
     static constexpr uint32_t ATOM = 8 * ROWB;        // 8 rows: the swizzle's period
     __host__ __device__ static constexpr int stages(int nb) { return (nb * PANELS + BPS - 1) / BPS; }
-    static_assert(2 * S_COLS + PANELS * N <= TMEM, "two score buffers and the outputs fit");
-    static_assert(RING >= 4, "the ring holds two blocks of the widest heads");
+    static_assert(2 * S_COLS + PANELS * NP <= TMEM, "two score buffers and the outputs fit");
+    static_assert(RING >= 4 && RING <= kMaxRing, "the ring holds two blocks of the widest heads");
 };
 
 struct Q8Params {
     const uint16_t* q;
     const float* ks;
     const float* vs;
+    const uint8_t* v;
     const int32_t* bt;
     const int32_t* ctx;
     uint16_t* out;
@@ -119,8 +155,8 @@ struct Q8Maps {
     CUtensorMap k_page, v_page, k_block, v_block;
 };
 
-// floats of one partial result: G x D outputs, then per head the largest
-// weighted score and the sum
+// floats of one partial result: G x D outputs, then per head the reference m
+// and the sum of 2^(y - m)
 __host__ __device__ inline int64_t part_floats(int G, int D) { return (int64_t)G * D + 2 * G; }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -233,12 +269,6 @@ struct Walk {
     }
 };
 
-// A chunk as it is announced to the other warps.
-struct Chunk {
-    int row, ctx, c0, nb;    // nb < 0: no more
-    int item, qbuf, last;
-};
-
 // two terms of HG heads: columns [0, HG) and [GP, GP + HG) at addr
 template <int HG, int GP>
 __device__ __forceinline__ void load_terms(uint32_t addr, float (&s)[2 * HG]) {
@@ -247,32 +277,62 @@ __device__ __forceinline__ void load_terms(uint32_t addr, float (&s)[2 * HG]) {
     else tmem_ld8x2(addr, addr + GP, s);
 }
 
+__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// The four lanes of a quad exchange their words' bytes: lane i gets byte i of each.
+__device__ __forceinline__ void turn_bytes(uint32_t& a, uint32_t& b, const uint32_t (&s)[6]) {
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+        const uint32_t x = __shfl_xor_sync(kFull, __byte_perm(a, b, s[3 * step]), 1 + step);
+        a = __byte_perm(a, x, s[3 * step + 1]);
+        b = __byte_perm(b, x, s[3 * step + 2]);
+    }
+}
+
+// the four terms of HG heads' outputs, joined
+template <int HG, int GP>
+__device__ __forceinline__ void load_output(uint32_t addr, float (&o)[HG]) {
+    if constexpr (HG == 4) {
+        float x[16];
+        tmem_ld16(addr, x);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) o[g] = fmaf(x[8 + g] + x[12 + g], 0x1p-6f, x[g] + x[4 + g]);
+    } else {
+        float x[16], y[16];
+        tmem_ld8x2(addr + 2 * GP, addr + 3 * GP, y);
+        tmem_ld8x2(addr, addr + GP, x);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) o[g] = fmaf(y[g] + y[8 + g], 0x1p-6f, x[g] + x[8 + g]);
+    }
+}
+
 template <int D, int GP>
 __global__ void __launch_bounds__(Q8Cfg<D, GP>::THREADS, Q8Cfg<D, GP>::CTAS)
 attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
     using C = Q8Cfg<D, GP>;
-    constexpr int N = C::N, NB = C::NB, RING = C::RING, PANELS = C::PANELS, HG = C::HG;
+    constexpr int N = C::N, NP = C::NP, NB = C::NB, RING = C::RING, PANELS = C::PANELS, HG = C::HG;
     constexpr int kCopyWarp = C::SOFTMAX / 32, kMmaWarp = kCopyWarp + 1, kAheadWarp = kCopyWarp + 2;
-    extern __shared__ uint8_t raw[];
-    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t* psm = ring + RING * C::STAGE;     // [NB][N][128] swizzled, K-major
+    extern __shared__ __align__(1024) uint8_t ring[];
+    uint8_t* psm = ring + RING * C::STAGE;     // [NB][NP][128] swizzled, K-major
     uint8_t* qsm = psm + C::P_BYTES;           // [kDepth][PANELS][N][ROWB] swizzled, K-major
-    // ks * scale * log2 e, log2 vs (-inf: no page), 1 / vs of the announced chunks' pages
-    __shared__ float4 page_scale[kDepth][C::PAGES];
-    __shared__ uint64_t full[RING], empty[RING], s_full[2][C::NU], p_full[C::NU], c_full[kDepth], c_empty[kDepth];
-    __shared__ uint64_t o_full, drained;
-    __shared__ Chunk chunk[kDepth];
-    __shared__ float qinv[kDepth][GP];
-    __shared__ float red[C::GROUPS][4][HG];
-    __shared__ uint32_t tmem_base;
-    __shared__ int gave_up;
-    __shared__ int box_z[2][C::PAGES];          // page coordinates of the copied chunks
+    typename C::Shared& S = *reinterpret_cast<typename C::Shared*>(qsm + kDepth * C::Q_BYTES);
+    auto& page_scale = S.page_scale;
+    auto &full = S.full, &empty = S.empty;
+    auto& s_full = S.s_full;
+    auto& p_full = S.p_full;
+    auto &c_full = S.c_full, &c_empty = S.c_empty;
+    auto &o_full = S.o_full, &drained = S.drained;
+    auto& chunk = S.chunk;
+    auto& qinv = S.qinv;
+    auto& red = S.red;
+    auto& box_z = S.box_z;
+    int& gave_up = S.gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // the first chunk's pages are on their way while the CTA sets itself up
     Walk<NB> walk;
     if (warp == kCopyWarp || warp == kAheadWarp) walk.begin(A);
-    if (warp == kMmaWarp) tmem_alloc(&tmem_base, C::TMEM);
+    if (warp == kMmaWarp) tmem_alloc(&S.tmem_base, C::TMEM);
     if (tid == 0) {
         for (int i = 0; i < RING; ++i) {
             mbar_init(&full[i], 1);
@@ -292,16 +352,15 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         gave_up = 0;
         mbar_fence_init();
     }
-    // query columns past G and, with 4 heads, the upper half of the
-    // probabilities' columns stay zero
-    for (int i = tid; i < (C::P_BYTES + kDepth * C::Q_BYTES) / 16; i += C::THREADS)
-        reinterpret_cast<uint4*>(psm)[i] = make_uint4(0, 0, 0, 0);
+    // query columns past G stay zero
+    for (int i = tid; i < kDepth * C::Q_BYTES / 16; i += C::THREADS)
+        reinterpret_cast<uint4*>(qsm)[i] = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     asm volatile("griddepcontrol.launch_dependents;");
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = S.tmem_base;
     volatile int* quit = &gave_up;
 
     if (warp == kCopyWarp) {
@@ -458,10 +517,10 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                         // the rows.  A 64-byte row fills 64 of the 128 MMA rows;
                         // the leading offset 0 reads it again for the others.
                         const uint64_t vd = k_desc + (st * C::STAGE + sub * C::PANEL) / 16;
-                        const uint64_t pd = p_desc + b * (N * 128 / 16);
+                        const uint64_t pd = p_desc + b * (NP * 128 / 16);
 #pragma unroll
                         for (uint32_t k = 0; k < 4; ++k)
-                            mma_f8(o_cols + panel * N, vd + k * (32 * C::ROWB / 16), pd + k * 2, A.v_idesc, b > 0 || k > 0);
+                            mma_f8(o_cols + panel * NP, vd + k * (32 * C::ROWB / 16), pd + k * 2, A.v_idesc, b > 0 || k > 0);
                         if (C::BPS == 1 || sub == 1 || b + 1 == nbv) {
                             tc_commit(&empty[st]);
                             if (++st == RING) {
@@ -573,15 +632,53 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     }
                     if (lane >= A.G && lane < GP) qinv[qbuf][lane] = 0.f;
                 }
+                // the least and the largest of the values' scales
+                uint32_t least = 0x7F800000u, most = 0;
+#pragma unroll
+                for (int r = 0; r < Walk<NB>::R; ++r) {
+                    if (pg[r] < 0) continue;
+                    vs[r] = fmaxf(vs[r], 0x1p-100f);
+                    least = min(least, __float_as_uint(vs[r]));
+                    most = max(most, __float_as_uint(vs[r]));
+                }
+                least = __reduce_min_sync(kFull, least);
+                most = __reduce_max_sync(kFull, most);
+                const float low = __uint_as_float(least);
+                if (__uint_as_float(most) > low * kSpread) {
+                    // pages of zeros do not set the weights' scale
+                    most = 0;
+#pragma unroll
+                    for (int r = 0; r < Walk<NB>::R; ++r) {
+                        for (uint32_t far = __ballot_sync(kFull, pg[r] >= 0 && vs[r] > low * kSpread); far != 0; far &= far - 1) {
+                            const int l = __ffs(far) - 1, tokens = it.ctx - (c0 * kPagesPerBlock + r * 32 + l) * kSubPage;
+                            const uint8_t* v = A.v + ((int64_t)__shfl_sync(kFull, pg[r], l) * kSubPage * A.H + h) * D;
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int k = 0; k < D / 32; ++k) {
+                                const int u = lane + 32 * k, slot = u / (D / 16);
+                                if (slot < tokens) {
+                                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(v + (int64_t)slot * A.H * D) + u % (D / 16));
+                                    any |= x.x | x.y | x.z | x.w;
+                                }
+                            }
+                            if (!__any_sync(kFull, (any & 0x7F7F7F7Fu) != 0) && lane == l) vs[r] = low;
+                        }
+                        if (pg[r] >= 0) most = max(most, __float_as_uint(vs[r]));
+                    }
+                    most = __reduce_max_sync(kFull, most);
+                }
+                // a weight 2^-100 of the largest possible one counts for its probability alone
+                const float floor_vs = fmaxf(low, __uint_as_float(most) * 0x1p-100f);
 #pragma unroll
                 for (int r = 0; r < Walk<NB>::R; ++r) {
                     const int p = r * 32 + lane;
                     if (p >= nb * kPagesPerBlock) continue;
-                    const float v = fmaxf(vs[r], 0x1p-100f);
-                    page_scale[buf][p] = pg[r] < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
-                                                   : make_float4(ks[r] * A.scale_log2e, log2f(v), __frcp_rn(v), 0.f);
+                    page_scale[buf][p] = pg[r] < 0 ? make_float2(0.f, -INFINITY)
+                                                   : make_float2(ks[r] * A.scale_log2e, log2f(fmaxf(vs[r], floor_vs)));
                 }
-                if (lane == 0) chunk[buf] = Chunk{it.row, it.ctx, c0, nb, i, qbuf, c0 + nb == it.b1};
+                if (lane == 0)
+                    chunk[buf] = Chunk{it.row, it.ctx, c0, nb, i, qbuf, c0 + nb == it.b1,
+                                       most == 0 ? 0.f : 0.5f * (log2f(floor_vs) + log2f(__uint_as_float(most)))};
                 fence_async_smem();
                 mbar_arrive(&c_full[buf]);
             }
@@ -597,15 +694,23 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         const int g0 = group * HG;                                 // this group's first head
         const uint32_t lanes = tmem + ((uint32_t)quad << 21) + g0;   // the warp's 32 TMEM lanes
         const int part16 = tok >> 4;                               // byte tok's 16-byte part of a P row
+        // the place of this lane's four tokens in row g0 + lane % 4 of a block's weights, and
+        // in the row four further
+        const uint32_t row0 = (uint32_t)(g0 + (lane & 3)) * 128 + (tok & 12);
+        const uint32_t place[2] = {row0 + ((part16 ^ (lane & 3)) << 4), row0 + 512 + ((part16 ^ (4 + (lane & 3))) << 4)};
+        // bytes that go to a neighbouring lane, and that stay with those that come (turn_bytes)
+        const uint32_t turn[6] = {lane & 1 ? 0x6420u : 0x7531u, lane & 1 ? 0x3514u : 0x5240u, lane & 1 ? 0x3716u : 0x7260u,
+                                  lane & 2 ? 0x5410u : 0x7632u, lane & 2 ? 0x3254u : 0x5410u, lane & 2 ? 0x3276u : 0x7610u};
         uint32_t s_phase = 0, o_phase = 0, s = 0;      // s: chunks with blocks so far
-        float acc[PANELS][HG], mt[HG], l[HG], keep[HG];
+        // outputs in units of 2^mt and sums in units of 2^ml, the open chunk's outputs
+        // in units of 2^mt / take
+        float acc[PANELS][HG], mt[HG], ml[HG], l[HG], take[HG];
 #pragma unroll
         for (int g = 0; g < HG; ++g) {
 #pragma unroll
             for (int p = 0; p < PANELS; ++p) acc[p][g] = 0.f;
-            mt[g] = -INFINITY;
-            l[g] = 0.f;
-            keep[g] = 1.f;
+            mt[g] = ml[g] = -INFINITY;
+            l[g] = take[g] = 0.f;
         }
         int row = 0, item = 0;
         bool open = false, last = false;      // a chunk whose output is to come, and whether it ends its item
@@ -619,10 +724,10 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 tc_fence_after();
 #pragma unroll
                 for (int p = 0; p < PANELS; ++p) {
-                    float o[2 * HG];
-                    load_terms<HG, GP>(lanes + 2 * C::S_COLS + p * N, o);
+                    float o[HG];
+                    load_output<HG, GP>(lanes + 2 * C::S_COLS + p * NP, o);
 #pragma unroll
-                    for (int g = 0; g < HG; ++g) acc[p][g] = fmaf(acc[p][g], keep[g], fmaf(o[HG + g], 0.0625f, o[g]));
+                    for (int g = 0; g < HG; ++g) acc[p][g] = fmaf(o[g], take[g], acc[p][g]);
                 }
                 tc_fence_before();
             }
@@ -645,26 +750,26 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     if (g0 + g < A.G) {
                         const float sum = bad ? NAN
                                               : red[group][0][g] + red[group][1][g] + red[group][2][g] + red[group][3][g];
-                        if (A.splits == 1) {
-                            const float f = sum == 0.f ? 0.f : 1.f / sum;
+                        // 2^(mt - ml) in two factors: it may lie outside fp32's range where
+                        // the output does not
+                        const float f = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ex2(0.5f * (mt[g] - ml[g]));
 #pragma unroll
-                            for (int p = 0; p < PANELS; ++p)
-                                if (tok < C::ROWB)
-                                    o16[(g0 + g) * D + p * 128 + tok] =
-                                        __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : acc[p][g] * f));
-                        } else {
-#pragma unroll
-                            for (int p = 0; p < PANELS; ++p)
-                                if (tok < C::ROWB) o32[(g0 + g) * D + p * 128 + tok] = acc[p][g];
-                            if (tok == 0) {
-                                o32[A.G * D + g0 + g] = mt[g];
-                                o32[A.G * D + A.G + g0 + g] = sum;
+                        for (int p = 0; p < PANELS; ++p) {
+                            const float o = acc[p][g] * e * f * e;
+                            const int at = (g0 + g) * D + p * 128 + tok;
+                            if (tok < C::ROWB) {
+                                if (A.splits == 1) o16[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+                                else o32[at] = o;
                             }
+                        }
+                        if (A.splits > 1 && tok == 0) {
+                            o32[A.G * D + g0 + g] = ml[g];
+                            o32[A.G * D + A.G + g0 + g] = sum;
                         }
                     }
 #pragma unroll
                     for (int p = 0; p < PANELS; ++p) acc[p][g] = 0.f;
-                    mt[g] = -INFINITY;
+                    mt[g] = ml[g] = -INFINITY;
                     l[g] = 0.f;
                 }
             }
@@ -681,7 +786,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             const Chunk ch = chunk[buf];
             const int nb = ch.nb;
             if (group_any(group, gone || nb < 0)) break;
-            const float4* scales = page_scale[buf];
+            const float2* scales = page_scale[buf];
             float qi[HG], ct[HG];
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
@@ -700,7 +805,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 for (int j = 0; j < 2; ++j) {
                     float x[2 * HG];
                     load_terms<HG, GP>(s_cols + (b + j) * N, x);
-                    const float4 sc = scales[(b + j) * kPagesPerBlock + part16];
+                    const float2 sc = scales[(b + j) * kPagesPerBlock + part16];
                     const bool live = b + j < nb && (ch.c0 + b + j) * kPageSize + tok < ch.ctx && sc.y != -INFINITY;
 #pragma unroll
                     for (int g = 0; g < HG; ++g) {
@@ -725,45 +830,71 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
 #pragma unroll
                 for (int g = 0; g < HG; ++g) {
                     const float t = fmaxf(fmaxf(red[group][0][g], red[group][1][g]), fmaxf(red[group][2][g], red[group][3][g]));
-                    const float top = fmaxf(mt[g], t);
-                    keep[g] = top == -INFINITY ? 1.f : ex2(mt[g] - top);
+                    const float top = fmaxf(mt[g], t), m = fmaxf(ml[g], t - ch.mid);
+                    if (t > -INFINITY) {
+                        const float keep = ex2(mt[g] - top);
+#pragma unroll
+                        for (int p = 0; p < PANELS; ++p) acc[p][g] *= keep;
+                        l[g] *= ex2(ml[g] - m);
+                    }
+                    take[g] = t > -INFINITY ? ex2(t - top - kTop) : 0.f;
                     mt[g] = top;
-                    l[g] *= keep[g];
-                    ct[g] = 8.f - top;           // probabilities in units of 2^-8 of the largest so far
+                    ml[g] = m;
+                    ct[g] = kTop - t;
                 }
-                // ---- the probabilities ----
+                // ---- the weights, and the probabilities' sums in units of 2^(t - mid) ----
+                float lc[HG];
+#pragma unroll
+                for (int g = 0; g < HG; ++g) lc[g] = 0.f;
                 for (int b = 0; b < nb; b += 2) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         float x[2 * HG];
                         load_terms<HG, GP>(s_cols + (b + j) * N, x);
-                        const float4 sc = scales[(b + j) * kPagesPerBlock + part16];
+                        const float2 sc = scales[(b + j) * kPagesPerBlock + part16];
                         const bool live = b + j < nb && (ch.c0 + b + j) * kPageSize + tok < ch.ctx && sc.y != -INFINITY;
+                        const float per_w = live ? ex2(ch.mid - sc.y - kTop) : 0.f;     // p_j / w_j
                         float w[HG];
 #pragma unroll
                         for (int g = 0; g < HG; ++g) {
                             const float t = fmaf(fmaf(x[HG + g], 0.0625f, x[g]), qi[g] * sc.x, sc.y + ct[g]);
                             w[g] = live ? ex2(t) : 0.f;
-                            l[g] = fmaf(w[g], live ? sc.z : 0.f, l[g]);
+                            lc[g] = fmaf(w[g], per_w, lc[g]);
                         }
-                        uint8_t* pb = psm + (b + j) * N * 128 + (tok & 15) + g0 * 128;
+                        uint8_t* pb = psm + (b + j) * NP * 128;
+                        __half2 rest[HG / 2];
 #pragma unroll
-                        for (int g = 0; g < HG; g += 2) {
-                            const uint32_t hi = pack_e4m3(w[g], w[g + 1]);
-                            const float2 f = unpack_e4m3(hi);
-                            const uint32_t lo = pack_e4m3((w[g] - f.x) * 16.f, (w[g + 1] - f.y) * 16.f);
-                            // rows g0 + g and GP + g0 + g; g0 and (from 8 heads on) GP are multiples of 8
-                            const int r0 = g, r1 = g + 1, r2 = GP + g, r3 = GP + g + 1;
-                            pb[r0 * 128 + ((part16 ^ (r0 & 7)) << 4)] = (uint8_t)hi;
-                            pb[r1 * 128 + ((part16 ^ (r1 & 7)) << 4)] = (uint8_t)(hi >> 8);
-                            pb[r2 * 128 + ((part16 ^ (r2 & 7)) << 4)] = (uint8_t)lo;
-                            pb[r3 * 128 + ((part16 ^ (r3 & 7)) << 4)] = (uint8_t)(lo >> 8);
+                        for (int g = 0; g < HG / 2; ++g) rest[g] = __floats2half2_rn(w[2 * g], w[2 * g + 1]);
+                        uint32_t word[HG / 4 * kTerms];
+#pragma unroll
+                        for (int term = 0; term < kTerms; ++term) {
+                            // a term is the upper byte of the fp16 values
+#pragma unroll
+                            for (int g = 0; g < HG / 4; ++g)
+                                word[term * (HG / 4) + g] = __byte_perm(bits_of(rest[2 * g]), bits_of(rest[2 * g + 1]), 0x7531);
+#pragma unroll
+                            for (int g = 0; g < HG / 2; ++g) {
+                                const uint32_t top = bits_of(rest[g]) & 0xFF00FF00u;
+                                rest[g] = __hsub2_rn(rest[g], *reinterpret_cast<const __half2*>(&top));
+                                if (term == 1) rest[g] = __hmul2_rn(rest[g], __float2half2_rn(64.f));
+                            }
+                        }
+                        // word i has one token's terms of rows R(i), R(i) + 1, ..; turned, row
+                        // R(i) + lane % 4's of four tokens
+#pragma unroll
+                        for (int i = 0; i < HG / 4 * kTerms; i += 2) {
+                            turn_bytes(word[i], word[i + 1], turn);
+                            const int r0 = HG == 4 ? 4 * i : (i / 2) * GP;
+                            *reinterpret_cast<uint32_t*>(pb + place[0] + r0 * 128) = word[i];
+                            *reinterpret_cast<uint32_t*>(pb + place[1] + r0 * 128) = word[i + 1];
                         }
                     }
                     fence_async_smem();
                     tc_fence_before();
                     mbar_arrive(&p_full[b >> 1]);
                 }
+#pragma unroll
+                for (int g = 0; g < HG; ++g) l[g] = fmaf(lc[g], ct[g] < INFINITY ? ex2(kTop - ct[g] - ch.mid - ml[g]) : 1.f, l[g]);
                 s_phase ^= ((1u << ((nb + 1) >> 1)) - 1) << (sbuf * 8);
                 ++s;
             }
@@ -798,8 +929,8 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             float sum = 0.f, acc = 0.f;
 #pragma unroll
             for (int s = 0; s < kMaxCluster; ++s) {
-                const float w = l[s] == 0.f ? 0.f : ex2(mt[s] - top);
-                sum = fmaf(l[s], w, sum);
+                const float w = l[s] == 0.f ? 0.f : l[s] * ex2(mt[s] - top);
+                sum += w;
                 if (w != 0.f) acc = fmaf(o[s], w, acc);
             }
             A.out[(row * A.G + g) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum));
@@ -836,15 +967,15 @@ attention_q8_join_kernel(const float* part, uint16_t* out, int splits, int G, in
         m = max_warp(m);
         for (int s = tid; s < splits; s += 32) {
             const float l = base[s * len + G * D + G + g];
-            const float w = l == 0.f ? 0.f : ex2(base[s * len + G * D + g] - m);
+            const float w = l == 0.f ? 0.f : l * ex2(base[s * len + G * D + g] - m);
             weight[s] = w;
-            sum += l * w;
+            sum += w;
         }
         sum = sum_warp(sum);
         if (tid == 0) total = sum;
     }
     __syncthreads();
-    // a part without tokens has weight 0 and no defined output
+    // a part without tokens has weight 0
     float o = 0.f;
 #pragma unroll
     for (int j = 0; j < kJoinAhead; ++j) {
@@ -901,7 +1032,7 @@ cudaError_t launch_q8(Q8Params& A, const Q8Maps& M, bool e4m3, int sms, cudaStre
     using C = Q8Cfg<D, GP>;
     const uint32_t fmt = e4m3 ? 0 : 1;
     A.k_idesc = f8_idesc(fmt, 0, false, 128, C::N);
-    A.v_idesc = f8_idesc(fmt, 0, true, 128, C::N);
+    A.v_idesc = f8_idesc(fmt, 1, true, 128, C::NP);
     auto kern = attention_q8_kernel<D, GP>;
     static FuncOnce once;
     const cudaError_t e = once.smem(reinterpret_cast<const void*>(kern), C::SMEM);
@@ -1018,6 +1149,7 @@ extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache
     A.q = static_cast<const uint16_t*>(q);
     A.ks = k_scale;
     A.vs = v_scale;
+    A.v = static_cast<const uint8_t*>(v_cache);
     A.bt = sparse_bt;
     A.ctx = sparse_ctx;
     A.out = static_cast<uint16_t*>(out);
