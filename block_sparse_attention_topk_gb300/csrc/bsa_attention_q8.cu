@@ -21,9 +21,9 @@
 //    largest (so w_j within 2^-12 of itself), and within 2^-37 of that below.
 //    e5m2 has that range, e4m3 would end at 2^-22: a token that takes the probability
 //    and has no value, or a page with a larger scale than others, leaves the others'
-//    weights their bits.  A page of zeros (the append gives it the scale 1) whose scale
-//    is far above the chunk's least takes that one instead, as its codes are zero
-//    under any scale.
+//    weights their bits.  Pages of zeros (the append gives them the scale 1) whose
+//    scale is the chunk's largest, and far above its least, take the least instead, as
+//    their codes are zero under any scale.
 // Probabilities are summed in fp32 before their rounding, chunks are joined in
 // fp32, and maxima and accumulators are fp32.
 //
@@ -77,7 +77,7 @@ constexpr int kMaxCluster = 8;           // items per row that a cluster joins
 constexpr int kSmSmem = 233472;          // an SM's shared memory; 1 KB of it goes to each CTA
 constexpr int kTerms = 4;                // terms of a weight
 constexpr float kTop = 15.f;             // log2 of a chunk's largest weight as it is rounded
-constexpr float kSpread = 65536.f;       // scales this much above the chunk's least may be a page of zeros
+constexpr float kSpread = 65536.f;       // a largest scale this much above the chunk's least may be that of zeros
 
 // A chunk as it is announced to the other warps.
 struct Chunk {
@@ -644,13 +644,14 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 least = __reduce_min_sync(kFull, least);
                 most = __reduce_max_sync(kFull, most);
                 const float low = __uint_as_float(least);
-                if (__uint_as_float(most) > low * kSpread) {
-                    // pages of zeros do not set the weights' scale
-                    most = 0;
+                // the pages of the largest scale, and while they are all zeros of the next
+                while (__uint_as_float(most) > low * kSpread) {
+                    bool zeros = true;
 #pragma unroll
                     for (int r = 0; r < Walk<NB>::R; ++r) {
-                        for (uint32_t far = __ballot_sync(kFull, pg[r] >= 0 && vs[r] > low * kSpread); far != 0; far &= far - 1) {
-                            const int l = __ffs(far) - 1, tokens = it.ctx - (c0 * kPagesPerBlock + r * 32 + l) * kSubPage;
+                        uint32_t top = __ballot_sync(kFull, pg[r] >= 0 && __float_as_uint(vs[r]) == most);
+                        for (; zeros && top != 0; top &= top - 1) {
+                            const int l = __ffs(top) - 1, tokens = it.ctx - (c0 * kPagesPerBlock + r * 32 + l) * kSubPage;
                             const uint8_t* v = A.v + ((int64_t)__shfl_sync(kFull, pg[r], l) * kSubPage * A.H + h) * D;
                             uint32_t any = 0;
 #pragma unroll
@@ -661,10 +662,15 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                                     any |= x.x | x.y | x.z | x.w;
                                 }
                             }
-                            if (!__any_sync(kFull, (any & 0x7F7F7F7Fu) != 0) && lane == l) vs[r] = low;
+                            zeros = !__any_sync(kFull, (any & 0x7F7F7F7Fu) != 0);
+                            if (zeros && lane == l) vs[r] = low;
                         }
-                        if (pg[r] >= 0) most = max(most, __float_as_uint(vs[r]));
                     }
+                    if (!zeros) break;
+                    most = least;
+#pragma unroll
+                    for (int r = 0; r < Walk<NB>::R; ++r)
+                        if (pg[r] >= 0) most = max(most, __float_as_uint(vs[r]));
                     most = __reduce_max_sync(kFull, most);
                 }
                 // a weight 2^-100 of the largest possible one counts for its probability alone
