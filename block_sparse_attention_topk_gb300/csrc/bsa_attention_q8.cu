@@ -637,7 +637,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
 #pragma unroll
                 for (int r = 0; r < Walk<NB>::R; ++r) {
                     if (pg[r] < 0) continue;
-                    vs[r] = fmaxf(vs[r], 0x1p-100f);
+                    vs[r] = fmaxf(vs[r], 0x1p-149f);         // a scale of 0 has a logarithm too
                     least = min(least, __float_as_uint(vs[r]));
                     most = max(most, __float_as_uint(vs[r]));
                 }

@@ -391,9 +391,10 @@ size_t bsa_attention_q8_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t
  * and out-of-range rules (and status bits) of bsa_sparse_decode_attention.
  *   q, out: bf16 [T, H, G, D], 16-byte aligned; k_cache, v_cache: dtype
  *   BSA_DTYPE_E4M3 or BSA_DTYPE_E5M2, [num_pages, 16, H, D], 16-byte aligned,
- *   num_pages < 2^27; k_scale, v_scale: float [num_pages, H], positive; D in
- *   {64, 128, 256}; 1 <= G <= BSA_MAX_ATTN_Q8_GROUP; T * H <= 2^24.  The slots of a page
- *   past the context may hold anything, NaN codes included.
+ *   num_pages < 2^27; k_scale, v_scale: float [num_pages, H], finite, not
+ *   negative; D in {64, 128, 256}; 1 <= G <= BSA_MAX_ATTN_Q8_GROUP; T * H <= 2^24.
+ *   The slots of a page past the context may hold anything, NaN codes included.
+ *   An infinite code in the context (E5M2; the append writes none) may give NaN.
  *   workspace: at least bsa_attention_q8_workspace_bytes(...) bytes, 256-byte
  *   aligned, any contents; may be NULL when that is 0.  Calls that share a
  *   workspace must not overlap on the GPU.

@@ -10,7 +10,7 @@ import torch
 
 import block_sparse_attention_topk_gb300 as bsa
 import oracle
-from tests.test_gpu_attention_q8 import KIND, _case, _check
+from tests.test_gpu_attention_q8 import KIND, _bound, _case, _check
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,45 @@ def test_attention_q8_error_is_that_of_rounding_the_output(cuda_device):
     rounded = torch.from_numpy(want).to(torch.bfloat16).double().numpy()
     own = np.linalg.norm(rounded - want)
     assert np.linalg.norm(got.double().cpu().numpy() - want) <= 1.01 * own
+
+
+def _check_small(dev, q, codes, scales, bt, ctx, dtype, kind):
+    """_check without its absolute slack: half a step of bf16's subnormals."""
+    cn, sn = [x.numpy() for x in codes], [x.numpy() for x in scales]
+    sc = q.shape[-1] ** -0.5
+    want = oracle.sparse_decode_attention_q8(q, cn[0], cn[1], kind, sn[0], sn[1], bt.numpy(), ctx.numpy(), sc)
+    got = bsa.bsa_sparse_decode_attention_q8(*(x.to(dev) for x in (q, codes[0].view(dtype), codes[1].view(dtype),
+                                                                   scales[0], scales[1], bt, ctx)))
+    torch.cuda.synchronize()
+    tol = _bound(q, cn, sn, bt.numpy(), ctx.numpy(), kind, sc, want) - 1e-30 + 2.0 ** -134
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all(), (err.max(), np.abs(want).max())
+
+
+@pytest.mark.parametrize("fmt", list(KIND))
+@pytest.mark.parametrize("T,G,D", [(2, 8, 128), (1, 16, 64), (400, 2, 256)])
+@pytest.mark.parametrize("std", [1e-28, 1e-31, 1e-34, 1e-37, 1e-39])
+def test_attention_q8_tiny_values(cuda_device, fmt, T, G, D, std):
+    """Scales as the append writes them, down to 2^-126: whole rows of tiny values,
+    in one CTA and joined, and rows with tiny values beside ordinary ones."""
+    n, H = 1300, 1
+    g = torch.Generator().manual_seed(G + D)
+    v = std * torch.randn((n, H, D), generator=g)
+    keys = torch.randn((n, H, D), generator=g)
+    q = torch.randn((T, H, G, D), generator=g).to(torch.bfloat16)
+    for ordinary in (0, 5):
+        v[600:600 + ordinary] = torch.randn((ordinary, H, D), generator=g)
+        codes, scales, pages, dtype, kind = _appended(cuda_device, fmt, H, D, v, keys)
+        assert scales[1].min() <= 4.5 * std / 8 or scales[1].min() == 2.0 ** -126
+        bt = pages.expand(T, H, -1).contiguous()
+        ctx = (torch.arange(T, dtype=torch.int32) % 7 * -100 + n).view(T, H)
+        _check_small(cuda_device, q, codes, scales, bt, ctx, dtype, kind)
+
+
+def test_attention_q8_scales_of_zero_and_subnormal_scales(cuda_device):
+    """A page whose value scale is 0 or subnormal counts for its probability."""
+    q, c, s, bt, ctx, dtype, kind = _case(3, 1, 4, 128, 4, "e4m3", [512, 300, 64], 12)
+    s[1][bt[0, 0, 3]] = 0
+    s[1][bt[1, 0, ::2].long()] = 2.0 ** -140
+    s[1][bt[2, 0, :4].long()] = 0
+    _check_small(cuda_device, q, c, s, bt, ctx, dtype, kind)
