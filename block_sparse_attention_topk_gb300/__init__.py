@@ -223,27 +223,34 @@ def _score_dtype(scores: torch.Tensor) -> int:
     raise ValueError(f"scores must be bfloat16 or float32, not {scores.dtype}")
 
 
-# One workspace per (device, stream), grown on demand (the library clears the
-# parts it needs cleared on every call).  Calls on one stream run in order,
-# so they may share it; calls on different streams get different buffers.
-# A buffer handed out during a graph capture stays alive: replays write to it
-# even after a later call has needed, and cached, a larger one.
+# Eager calls have one workspace per (device, stream), grown on demand (the
+# library clears the parts it needs cleared on every call).  Calls on one stream
+# run in order, so they may share it; calls on different streams get different
+# buffers.  A captured call runs on whatever streams its graph is replayed on, so
+# it gets memory of its own, which torch.cuda.graph takes from the graph's pool
+# and keeps for it; a capture by other means needs the caller's own workspace.
 _ws_cache: dict = {}
-_ws_captured: list = []
 _ws_lock = threading.Lock()
+
+
+def _capturing(device: torch.device) -> bool:
+    if device.index is None or device.index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def _workspace(device: torch.device, nbytes: int) -> torch.Tensor | None:
     if nbytes == 0:
         return None
+    if _capturing(device):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (device.type, device.index, _stream(device))
     with _ws_lock:
         ws = _ws_cache.get(key)
         if ws is None or ws.numel() < nbytes:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
             _ws_cache[key] = ws
-        if torch.cuda.is_current_stream_capturing() and all(w is not ws for w in _ws_captured):
-            _ws_captured.append(ws)
         return ws
 
 
