@@ -49,3 +49,25 @@ def test_two_graphs_replayed_at_once(cuda_device):
         torch.cuda.synchronize()
         for o, r in zip(outs, ref):
             assert torch.equal(o, r)
+
+
+def test_a_callers_workspace_is_used_within_its_bytes(cuda_device):
+    """Full of old bytes, on a side stream: the same bits, written up to the bytes
+    asked for and not behind them; less, or misaligned, is refused."""
+    dev = cuda_device
+    need = bsa.bsa_attention_q8_workspace_bytes(*SHAPE)
+    assert need > 0
+    args, = _calls(dev, 1)
+    ref = bsa.bsa_sparse_decode_attention_q8(*args)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=dev)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream(dev)
+    with torch.cuda.stream(stream):
+        got = [bsa.bsa_sparse_decode_attention_q8(*args, workspace=ws[:need]) for _ in range(2)]
+    stream.synchronize()
+    assert all(torch.equal(g, ref) for g in got)
+    assert (ws[need:] == 0xFF).all() and (ws[:need] != 0xFF).any()
+    for bad in (ws[:need - 1], ws[16:need + 16], torch.empty(0, dtype=torch.uint8, device=dev)):
+        with pytest.raises(bsa.BsaError) as e:
+            bsa.bsa_sparse_decode_attention_q8(*args, workspace=bad)
+        assert e.value.status == -5
