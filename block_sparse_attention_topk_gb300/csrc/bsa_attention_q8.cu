@@ -62,6 +62,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "bsa_internal.h"
@@ -82,7 +83,7 @@ constexpr float kSpread = 65536.f;       // a largest scale this much above the 
 // A chunk as it is announced to the other warps.
 struct Chunk {
     int row, ctx, c0, nb;    // nb < 0: no more
-    int item, qbuf, last;
+    int qbuf, last;
     float mid;               // log2 of the value scales' middle
 };
 
@@ -148,6 +149,8 @@ struct Q8Params {
     uint32_t k_idesc, v_idesc;
     float scale_log2e;
     uint32_t* status;
+    unsigned long long wait_ns;     // a wait's limit
+    uint32_t stall;                 // stages after which a CTA's copies stop, for tests
 };
 
 // The caches as tensors read in boxes of one page and of one block of a head.
@@ -328,6 +331,8 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
     auto& box_z = S.box_z;
     int& gave_up = S.gave_up;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = C::GROUPS == 1 ? 0 : warp >> 2;      // of a softmax warp
+    int item = blockIdx.x;                                 // the first that it has not written
 
     // the first chunk's pages are on their way while the CTA sets itself up
     Walk<NB> walk;
@@ -376,16 +381,19 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         uint32_t n = 0;   // stages filled so far: stage n % RING
         uint32_t issued = 0;      // the same as the elected thread counts them
         // One thread: nb blocks with page coordinates z; bit b of `runs`: block
-        // b's pages follow one another.  Stages from number n on.
+        // b's pages follow one another.  Stages from number n on.  False when a wait
+        // ran out; nothing is copied after that, as the stages' uses would no longer be
+        // in order.
         auto copy = [&](const CUtensorMap* page_map, const CUtensorMap* block_map, const int* z, uint32_t runs, int h,
-                        int nb, uint32_t n) {
+                        int nb, uint32_t n) -> bool {
             uint32_t st = n % RING, use = n / RING;
             for (int b = 0; b < nb; ++b) {
 #pragma unroll
                 for (int panel = 0; panel < PANELS; ++panel) {
                     const int sub = C::BPS == 1 ? 0 : b & 1;          // the block's place in its stage
                     if (sub == 0) {
-                        if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1, quit)) return;
+                        if (issued == A.stall) return false;
+                        if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1, quit, A.wait_ns)) return false;
                         mbar_expect(&full[st], C::PANEL * (C::BPS == 2 && b + 1 < nb ? 2 : 1));
                     }
                     uint8_t* dst = ring + st * C::STAGE + sub * C::PANEL;
@@ -406,7 +414,9 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     }
                 }
             }
+            return true;
         };
+        bool ok = true;
         int hv = 0, nbv = 0;      // the chunk whose values are still to come
         uint32_t runsv = 0, buf = 0;
         for (; !walk.done() && !__any_sync(kFull, *quit); buf ^= 1) {
@@ -427,8 +437,8 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             __syncwarp();
             walk.advance(A);
             if (elect_one()) {
-                copy(&M.k_page, &M.k_block, box_z[buf], runs, h, nb, n);
-                copy(&M.v_page, &M.v_block, box_z[buf ^ 1], runsv, hv, nbv, n + C::stages(nb));
+                ok = ok && copy(&M.k_page, &M.k_block, box_z[buf], runs, h, nb, n);
+                ok = ok && copy(&M.v_page, &M.v_block, box_z[buf ^ 1], runsv, hv, nbv, n + C::stages(nb));
             }
             __syncwarp();
             n += C::stages(nb) + C::stages(nbv);
@@ -436,11 +446,10 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             hv = h;
             nbv = nb;
         }
-        if (elect_one()) copy(&M.v_page, &M.v_block, box_z[buf ^ 1], runsv, hv, nbv, n);
-        __syncwarp();
-        // after a wait that ran out: the copies in flight land before the CTA's
-        // memory goes away
-        if (elect_one() && *quit) {
+        // the copies in flight land before the CTA's memory goes away, also when
+        // nobody waits for them any more
+        if (elect_one()) {
+            if (ok) copy(&M.v_page, &M.v_block, box_z[buf ^ 1], runsv, hv, nbv, n);
             int none = 0;
             for (uint32_t k = issued > RING ? issued - RING : 0; k < issued; ++k)
                 mbar_wait(&full[k % RING], (k / RING) & 1, &none);
@@ -459,7 +468,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             int nbv = 0, leftv = 0;              // the chunk whose output is to come: blocks, context tokens
             bool ok = true, more = true;
             while (ok && more) {
-                ok = mbar_wait(&c_full[c % kDepth], (c / kDepth) & 1, quit);
+                ok = mbar_wait(&c_full[c % kDepth], (c / kDepth) & 1, quit, A.wait_ns);
                 if (!ok) break;
                 const Chunk ch = chunk[c % kDepth];
                 const int nb = ch.nb;
@@ -474,7 +483,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
 #pragma unroll
                     for (int panel = 0; panel < PANELS; ++panel) {
                         if (sub == 0) {
-                            ok = ok && mbar_wait(&full[st], use & 1, quit);
+                            ok = ok && mbar_wait(&full[st], use & 1, quit, A.wait_ns);
                             if (!ok) break;
                             tc_fence_after();
                         }
@@ -497,13 +506,13 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 for (int b = 0; ok && b < nbv; ++b) {
                     const int sub = C::BPS == 1 ? 0 : b & 1;
                     if ((b & 1) == 0) {
-                        ok = mbar_wait(&p_full[b >> 1], (p_phase >> (b >> 1)) & 1, quit);
+                        ok = mbar_wait(&p_full[b >> 1], (p_phase >> (b >> 1)) & 1, quit, A.wait_ns);
                         p_phase ^= 1u << (b >> 1);
                     }
                     const int left = leftv - b * kPageSize;
 #pragma unroll
                     for (int panel = 0; panel < PANELS; ++panel) {
-                        if (sub == 0) ok = ok && mbar_wait(&full[st], use & 1, quit);
+                        if (sub == 0) ok = ok && mbar_wait(&full[st], use & 1, quit, A.wait_ns);
                         if (!ok) break;
                         if (left < kPageSize && left % kSubPage != 0) {
                             // the context ends in a page: the page's other values are not the row's
@@ -535,12 +544,11 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 nbv = nb;
                 leftv = ch.ctx - ch.c0 * kPageSize;
             }
-            // no MMA runs on into the release of its memory
-            if (!ok) {
-                int none = 0;
-                tc_commit(&drained);
-                mbar_wait(&drained, 0, &none);
-            }
+            // no MMA runs on into the release of its memory, also when nobody waits
+            // for it any more
+            int none = 0;
+            tc_commit(&drained);
+            mbar_wait(&drained, 0, &none);
         }
         __syncwarp();
     } else if (warp == kAheadWarp) {
@@ -548,19 +556,19 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         constexpr int LPH = D / 8;         // lanes per query head, 8 values each
         constexpr int HPP = 32 / LPH;      // heads a pass
         const int d = lane % LPH * 8, panel = d / C::ROWB, dc = d % C::ROWB;
-        uint32_t c = 0, item = 0;
+        uint32_t c = 0, queries = 0;
         int qbuf = 0;
         bool ok = true;
         for (; !walk.done(); ++c) {
             const Item it = walk.it;
-            const int i = walk.i, c0 = walk.c0, nb = walk.blocks(), h = it.row % A.H, buf = c % kDepth;
+            const int c0 = walk.c0, nb = walk.blocks(), h = it.row % A.H, buf = c % kDepth;
             int32_t pg[Walk<NB>::R];
 #pragma unroll
             for (int r = 0; r < Walk<NB>::R; ++r) pg[r] = walk.page[r];
             if (lane == 0 && it.split == 0 && c0 == it.b0)
                 report_status(A.status, walk.ctx_raw != it.ctx, BSA_STATUS_BAD_CONTEXT);
             walk.advance(A);
-            ok = c < kDepth || mbar_wait(&c_empty[buf], (c / kDepth - 1) & 1, quit);
+            ok = c < kDepth || mbar_wait(&c_empty[buf], (c / kDepth - 1) & 1, quit, A.wait_ns);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
             {
@@ -581,7 +589,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 }
                 if (c0 == it.b0 && nb > 0) {
                     // the queries as two e4m3 terms
-                    qbuf = item++ % kDepth;
+                    qbuf = queries++ % kDepth;
                     uint8_t* qd = qsm + qbuf * C::Q_BYTES;
                     constexpr int PASSES = (GP + HPP - 1) / HPP;
                     uint4 w[PASSES];
@@ -683,20 +691,20 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                                                    : make_float2(ks[r] * A.scale_log2e, log2f(fmaxf(vs[r], floor_vs)));
                 }
                 if (lane == 0)
-                    chunk[buf] = Chunk{it.row, it.ctx, c0, nb, i, qbuf, c0 + nb == it.b1,
+                    chunk[buf] = Chunk{it.row, it.ctx, c0, nb, qbuf, c0 + nb == it.b1,
                                        most == 0 ? 0.f : 0.5f * (log2f(floor_vs) + log2f(__uint_as_float(most)))};
                 fence_async_smem();
                 mbar_arrive(&c_full[buf]);
             }
         }
-        if (ok) ok = c < kDepth || mbar_wait(&c_empty[c % kDepth], (c / kDepth - 1) & 1, quit);
+        if (ok) ok = c < kDepth || mbar_wait(&c_empty[c % kDepth], (c / kDepth - 1) & 1, quit, A.wait_ns);
         __syncwarp();
         if (lane == 0) chunk[c % kDepth].nb = -1;
         __syncwarp();
         mbar_arrive(&c_full[c % kDepth]);
     } else {
         // ------------------------------------------------ softmax and output
-        const int group = C::GROUPS == 1 ? 0 : warp >> 2, tok = tid & 127, quad = warp & 3;
+        const int tok = tid & 127, quad = warp & 3;
         const int g0 = group * HG;                                 // this group's first head
         const uint32_t lanes = tmem + ((uint32_t)quad << 21) + g0;   // the warp's 32 TMEM lanes
         const int part16 = tok >> 4;                               // byte tok's 16-byte part of a P row
@@ -718,13 +726,13 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             mt[g] = ml[g] = -INFINITY;
             l[g] = take[g] = 0.f;
         }
-        int row = 0, item = 0;
+        int row = 0;
         bool open = false, last = false;      // a chunk whose output is to come, and whether it ends its item
 
         // Adds the open chunk's output, and writes the item's result at its end.
         auto close_chunk = [&]() {
             if (open) {
-                mbar_wait(&o_full, o_phase, quit);
+                mbar_wait(&o_full, o_phase, quit, A.wait_ns);
                 __syncwarp();
                 o_phase ^= 1;
                 tc_fence_after();
@@ -746,16 +754,15 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     if (lane == 0) red[group][quad][g] = a;
                 }
                 group_sync(group);
-                const bool bad = *quit;
+                const bool bad = *quit;             // what was not waited for is not a result
                 uint16_t* o16 = A.out + (int64_t)row * A.G * D;
                 // a split row's part: to the workspace, or to this CTA's own
                 // memory, where its probabilities are no longer needed
                 float* o32 = A.cluster ? reinterpret_cast<float*>(psm) : A.part + (int64_t)item * part_floats(A.G, D);
 #pragma unroll
                 for (int g = 0; g < HG; ++g) {
-                    if (g0 + g < A.G) {
-                        const float sum = bad ? NAN
-                                              : red[group][0][g] + red[group][1][g] + red[group][2][g] + red[group][3][g];
+                    if (g0 + g < A.G && !bad) {
+                        const float sum = red[group][0][g] + red[group][1][g] + red[group][2][g] + red[group][3][g];
                         // 2^(mt - ml) in two factors: it may lie outside fp32's range where
                         // the output does not
                         const float f = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ex2(0.5f * (mt[g] - ml[g]));
@@ -778,16 +785,17 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     mt[g] = ml[g] = -INFINITY;
                     l[g] = 0.f;
                 }
+                if (!bad) item += gridDim.x;
             }
             open = last = false;
         };
 
         // These warps meet in barriers, so none leaves alone: a wait that ran
         // out anywhere ends at the next chunk for the whole group, or lets the
-        // loops go on with what there is; outputs are NaN then.
+        // loops go on with what there is; the items from that on are not written here.
         for (uint32_t c = 0;; ++c) {
             const int buf = c % kDepth;
-            mbar_wait(&c_full[buf], (c / kDepth) & 1, quit);
+            mbar_wait(&c_full[buf], (c / kDepth) & 1, quit, A.wait_ns);
             const bool gone = *quit;
             const Chunk ch = chunk[buf];
             const int nb = ch.nb;
@@ -803,7 +811,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             const uint32_t sbuf = s & 1;
             const uint32_t s_cols = lanes + sbuf * C::S_COLS;
             for (int b = 0; b < nb; b += 2) {
-                mbar_wait(&s_full[sbuf][b >> 1], (s_phase >> (sbuf * 8 + (b >> 1))) & 1, quit);
+                mbar_wait(&s_full[sbuf][b >> 1], (s_phase >> (sbuf * 8 + (b >> 1))) & 1, quit, A.wait_ns);
                 __syncwarp();
                 tc_fence_after();
                 // both blocks of the pair; one that is not there has no live token
@@ -822,7 +830,6 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
             }
             close_chunk();
             row = ch.row;
-            item = ch.item;
             last = ch.last;
             if (nb > 0) {
                 open = true;
@@ -910,6 +917,25 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
     }
     tc_fence_before();
     __syncthreads();
+    if (warp < kCopyWarp) {
+        // after a wait that ran out: NaN for the items not written (every thread has its
+        // own count; without such a wait none is left)
+        for (; item < A.rows * A.splits; item += gridDim.x) {
+            const int h0 = group * HG, h1 = min(A.G, h0 + HG), t = tid & 127;
+            float* o32 = A.cluster ? reinterpret_cast<float*>(psm) : A.part + (int64_t)item * part_floats(A.G, D);
+            for (int g = h0; g < h1; ++g) {
+                for (int d = t; d < D; d += 128) {
+                    const int at = g * D + d;
+                    if (A.splits == 1) A.out[(int64_t)item * A.G * D + at] = 0x7FFF;
+                    else o32[at] = NAN;
+                }
+                if (A.splits > 1 && t == 0) {
+                    o32[A.G * D + g] = -INFINITY;
+                    o32[A.G * D + A.G + g] = NAN;
+                }
+            }
+        }
+    }
     if (tid == 0) report_status(A.status, gave_up != 0, BSA_STATUS_TIMEOUT);
     if (warp == kMmaWarp) tmem_free(tmem, C::TMEM);
     if (A.cluster) {
@@ -1003,6 +1029,9 @@ attention_q8_join_kernel(const float* part, uint16_t* out, int splits, int G, in
 }
 
 // ---- host ------------------------------------------------------------------
+
+std::atomic<unsigned long long> g_wait_ns{kWaitNs};
+std::atomic<uint32_t> g_stall{UINT32_MAX};
 
 using EncodeFn = decltype(&cuTensorMapEncodeTiled);
 
@@ -1128,6 +1157,11 @@ size_t workspace_need(int64_t rows, int64_t G, int64_t D, Split s) {
 
 using namespace bsa;
 
+extern "C" void bsa_attention_q8_stall(uint32_t stages, uint64_t wait_ns) {
+    g_stall.store(stages, std::memory_order_relaxed);
+    g_wait_ns.store(wait_ns == 0 ? kWaitNs : wait_ns, std::memory_order_relaxed);
+}
+
 extern "C" size_t bsa_attention_q8_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t D, int32_t K) {
     if (!sizes_ok(T, H, G, D) || T == 0 || K < 1 || K > BSA_MAX_TOPK) return 0;
     return workspace_need(T * H, G, D, pick_splits(T * H, G, D, K, device_sm_count()));
@@ -1169,6 +1203,8 @@ extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache
     A.cluster = split.cluster;
     A.scale_log2e = scale * 1.44269504f;
     A.status = current_status_word();
+    A.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    A.stall = g_stall.load(std::memory_order_relaxed);
     const size_t need = workspace_need(A.rows, G, D, split);
     if (need > 0) {
         if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)

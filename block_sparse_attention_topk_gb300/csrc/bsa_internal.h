@@ -211,6 +211,11 @@ private:
     std::atomic<uint64_t> done_{0};     // bit per device
 };
 
+// For tests, not part of the ABI: in later calls of the 8-bit attention each CTA's copies
+// stop after `stages` stages (UINT32_MAX: never) and the waits for them give up
+// after `wait_ns` (0: the usual four seconds).
+extern "C" void bsa_attention_q8_stall(uint32_t stages, uint64_t wait_ns);
+
 // The status word registered for the current device (bsa_set_status_word), or null.
 uint32_t* current_status_word();
 

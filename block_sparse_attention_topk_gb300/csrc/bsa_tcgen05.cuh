@@ -46,22 +46,23 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
         : "memory");
     return done != 0;
 }
-// Waits for the phase of `parity` to end.  Gives up after four seconds, or when
-// another thread of the CTA has (*gave_up set); false then.
+// Waits for the phase of `parity` to end.  Gives up after `limit` nanoseconds, or
+// when another thread of the CTA has (*gave_up set); false then.
 constexpr unsigned long long kWaitNs = 4000000000ull;
 __device__ __forceinline__ unsigned long long now_ns() {
     unsigned long long t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
     return t;
 }
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up,
+                                          unsigned long long limit = kWaitNs) {
     unsigned long long begin = 0;
     for (uint32_t i = 1;; ++i) {
         if (mbar_try(bar, parity)) return true;
         if ((i & 63) != 0) continue;
         if (*gave_up) return false;
         if (begin == 0) begin = now_ns();
-        if (now_ns() - begin > kWaitNs) {
+        if (now_ns() - begin > limit) {
             *gave_up = 1;
             return false;
         }

@@ -471,9 +471,9 @@ int bsa_select_policy(int64_t rows, int64_t M, int32_t K, int32_t dtype, int32_t
  *                            entry below 0 or above K * 128 (clamped); or the
  *                            append met a token past the block table (not
  *                            stored).
- *   BSA_STATUS_TIMEOUT       a wait inside the 8-bit attention ran out and the
- *                            call's outputs are incomplete (a defect or a
- *                            device problem, never an input's doing). */
+ *   BSA_STATUS_TIMEOUT       a wait inside the 8-bit attention ran out (a defect
+ *                            or a device problem, never an input's doing); the
+ *                            rows not finished are NaN. */
 #define BSA_STATUS_BAD_BLOCK_ID 0x1u
 #define BSA_STATUS_BAD_PAGE 0x2u
 #define BSA_STATUS_BAD_CONTEXT 0x4u
