@@ -586,6 +586,24 @@ def _binding():
     return _binding_module
 
 
+class _Rope(torch.autograd.Function):
+    """bsa_rope and its gradient, the inverse rotation."""
+
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, freq_axis, interleaved, inverse):
+        ctx.save_for_backward(positions, inv_freq, freq_axis)
+        ctx.turn = interleaved, inverse
+        return _binding().rope(x, positions, inv_freq, freq_axis, interleaved, inverse, None)
+
+    @staticmethod
+    def backward(ctx, dy):
+        positions, inv_freq, freq_axis = ctx.saved_tensors
+        interleaved, inverse = ctx.turn
+        if dy.stride(2) != 1:
+            dy = dy.contiguous()         # e.g. the gradient of a sum, one value expanded
+        return bsa_rope(dy, positions, inv_freq, freq_axis, interleaved, not inverse), None, None, None, None, None
+
+
 def bsa_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
              freq_axis: torch.Tensor | None = None, interleaved: bool = False,
              inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -594,7 +612,18 @@ def bsa_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     freq_axis int32 [rot_dim / 2] (the axis each frequency turns with; needed
     with several axes).  Returns out, by default a new contiguous tensor; x
     itself rotates in place.  ``inverse`` turns back: applied to the gradient
-    of the output it gives the gradient of x."""
+    of the output it gives the gradient of x, which is what autograd does with
+    it when x takes part in a gradient (out has to be None then; inv_freq has
+    no gradient)."""
+    if torch.is_grad_enabled():
+        if getattr(x, "requires_grad", False) or getattr(out, "requires_grad", False):
+            if out is not None:
+                raise ValueError("out must be None where x or out takes part in a gradient")
+            if getattr(inv_freq, "requires_grad", False):
+                raise ValueError("inv_freq has no gradient")
+            return _Rope.apply(x, positions, inv_freq, freq_axis, interleaved, inverse)
+        if getattr(inv_freq, "requires_grad", False):
+            raise ValueError("inv_freq has no gradient")
     return _binding().rope(x, positions, inv_freq, freq_axis, interleaved, inverse, out)
 
 
@@ -615,7 +644,7 @@ def bsa_append_kv_decode(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
     block_table int32 [num_reqs, max_blocks]; seq_lens int32 [num_reqs], the
     appended tokens counted.  Rotary arguments as for bsa_rope; positions
     defaults to the position in the sequence, inv_freq None rotates nothing.
-    Returns q_out bf16 [T, Hq, D] (None without q)."""
+    Returns q_out bf16 [T, Hq, D] (None without q), which carries no gradient."""
     return _binding().append(k, v, k_cache, v_cache, block_table, seq_lens,
                              operator.index(decode_query_len), q, inv_freq, positions, freq_axis,
                              interleaved, k_scale, v_scale, q_out)
@@ -658,6 +687,6 @@ def bsa_sparse_decode_attention_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     bits.  q bf16 [T, H, G, D]; k_cache, v_cache float8_e4m3fn or float8_e5m2
     [num_pages, 16, H, D] with fp32 k_scale, v_scale [num_pages, H];
     sparse_bt int32 [T, H, K*8], sparse_ctx int32 [T, H]; returns bf16
-    [T, H, G, D].  The scale defaults to 1 / sqrt(D)."""
+    [T, H, G, D], without a gradient.  The scale defaults to 1 / sqrt(D)."""
     return _binding().attention_q8(q, k_cache, v_cache, k_scale, v_scale, sparse_bt, sparse_ctx,
                                    scale, out, workspace)
