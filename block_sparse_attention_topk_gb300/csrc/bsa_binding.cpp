@@ -145,6 +145,11 @@ bool caches(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso, const at::
 const void* data(const Tensor* t) { return t == nullptr ? nullptr : t->const_data_ptr(); }
 void* data_rw(const Tensor* t) { return t == nullptr ? nullptr : t->data_ptr(); }
 
+// A call has written to the tensor: autograd's version counter moves.
+void changed(const Tensor* t) {
+    if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 bool on_gpu(const at::Device& device, const char* name) {
     return device.is_cuda() || fail("%s must be on a CUDA device, not %s", name, device.str().c_str());
 }
@@ -211,6 +216,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       oh.hs, stream);
     Py_END_ALLOW_THREADS
     if (!done("bsa_rope", status)) return nullptr;
+    changed(out);
     return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(a[6]);
     END_HANDLE_TH_ERRORS
 }
@@ -296,6 +302,8 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     : bsa_append_kv_decode(&p, row_ptr, (int32_t)dql, stream);
     Py_END_ALLOW_THREADS
     if (!done(varlen ? "bsa_append_kv_varlen" : "bsa_append_kv_decode", status)) return nullptr;
+    for (const Tensor* t : c) changed(t);
+    changed(q_out);
     return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(a[14]);
     END_HANDLE_TH_ERRORS
 }
@@ -364,6 +372,7 @@ PyObject* py_attention_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_END_ALLOW_THREADS
     Py_XDECREF(held);
     if (!done("bsa_sparse_decode_attention_q8", status)) return nullptr;
+    changed(out);
     return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(a[8]);
     END_HANDLE_TH_ERRORS
 }

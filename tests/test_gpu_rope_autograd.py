@@ -85,6 +85,34 @@ def test_what_has_no_gradient_is_refused(cuda_device):
         assert not bsa.bsa_rope(leaf, pd, fd).requires_grad
 
 
+def test_writing_calls_count_as_changes(cuda_device):
+    """A tensor that a graph has saved and a call then writes to is found out."""
+    dev = cuda_device
+    x, pos, inv, _ = _case(4, 2, 16, 16, 1, torch.float32, 10)
+    pd, fd = pos[0].to(dev), inv.to(dev)
+    buf = x.to(dev)
+    w = torch.ones_like(buf, requires_grad=True)
+    y = (w * buf).sum()
+    before = buf._version
+    bsa.bsa_rope(buf, pd, fd, out=buf)
+    assert buf._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    kv = torch.randn((2, 1, 16), device=dev).to(torch.bfloat16)
+    caches = [torch.zeros((8, 16, 1, 16), dtype=torch.float8_e4m3fn, device=dev) for _ in range(2)]
+    scales = [torch.ones((8, 1), device=dev) for _ in range(2)]
+    q_out = torch.empty_like(kv)
+    old = [t._version for t in (*caches, *scales, q_out)]
+    bsa.bsa_append_kv_decode(kv, kv, *caches, torch.zeros((1, 1), dtype=torch.int32, device=dev),
+                             torch.tensor([2], dtype=torch.int32, device=dev), 2, q=kv, k_scale=scales[0],
+                             v_scale=scales[1], q_out=q_out)
+    assert all(t._version > v for t, v in zip((*caches, *scales, q_out), old))
+    with torch.inference_mode():
+        frozen = x.to(dev)
+    bsa.bsa_rope(frozen, pd, fd, out=frozen)       # no counter to move
+    torch.cuda.synchronize()
+
+
 def test_gradient_in_a_graph(cuda_device):
     """Forward and backward captured together, replayed on new inputs."""
     T, H, D = 33, 2, 64
