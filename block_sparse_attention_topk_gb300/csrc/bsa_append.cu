@@ -21,6 +21,7 @@
 #include <stdint.h>
 
 #include "bsa_internal.h"
+#include "bsa_overlap.h"
 #include "bsa_rope.cuh"
 
 namespace bsa {
@@ -436,7 +437,24 @@ bsa_append_args_t plain_strides(bsa_append_args_t a) {
     return a;
 }
 
+// Nothing that the call writes shares memory with anything else of it.
+bool outputs_apart(const bsa_append_args_t& a) {
+    auto heads = [&](const void* p, int64_t H, int64_t ts, int64_t hs) { return Rows{p, p != nullptr ? a.T : 0, H, a.D * 2, ts * 2, hs * 2}; };
+    const int64_t cache = a.num_pages * kPageRows * a.H * a.D * (a.cache_dtype == BSA_DTYPE_BF16 ? 2 : 1);
+    const int64_t scales = a.cache_dtype == BSA_DTYPE_BF16 ? 0 : a.num_pages * a.H * 4;
+    const Rows r[8] = {whole_rows(a.q_out, a.q_out != nullptr ? a.T * a.Hq * a.D * 2 : 0),
+                       whole_rows(a.k_cache, cache), whole_rows(a.v_cache, cache),
+                       whole_rows(a.k_scale, scales), whole_rows(a.v_scale, scales),
+                       heads(a.q, a.Hq, a.q_token_stride, a.q_head_stride),
+                       heads(a.k, a.H, a.k_token_stride, a.k_head_stride), heads(a.v, a.H, a.v_token_stride, a.v_head_stride)};
+    for (int i = 0; i < 5; ++i)
+        for (int j = i + 1; j < 8; ++j)
+            if (rows_overlap(r[i], r[j])) return false;
+    return true;
+}
+
 int launch_append(AppendParams& P, cudaStream_t st) {
+    if (!outputs_apart(P.a)) return BSA_ERR_SHAPE;
     P.r = RopeParams{P.a.positions, P.a.T, P.a.inv_freq, P.a.freq_axis, P.a.axes, P.a.rot_dim / 2,
                      (P.a.flags & BSA_ROPE_INTERLEAVED) != 0, (P.a.flags & BSA_ROPE_INVERSE) != 0};
     P.status = current_status_word();

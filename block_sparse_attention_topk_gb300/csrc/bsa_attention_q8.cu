@@ -66,6 +66,7 @@
 #include <mutex>
 
 #include "bsa_internal.h"
+#include "bsa_overlap.h"
 #include "bsa_tcgen05.cuh"
 
 namespace bsa {
@@ -1184,6 +1185,13 @@ extern "C" int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache
     const void* wide[4] = {q, k_cache, v_cache, out};
     for (const void* p : wide)
         if ((reinterpret_cast<uintptr_t>(p) & 15) != 0) return BSA_ERR_ALIGN;
+    // out may be q itself: a row is written when its queries have been read
+    const int64_t row_bytes = T * H * G * D * 2, cache_bytes = num_pages * kSubPage * H * D, scale_bytes = num_pages * H * 4;
+    const Rows o = whole_rows(out, row_bytes);
+    if ((q != out && rows_overlap(o, whole_rows(q, row_bytes))) || rows_overlap(o, whole_rows(k_cache, cache_bytes)) ||
+        rows_overlap(o, whole_rows(v_cache, cache_bytes)) || rows_overlap(o, whole_rows(k_scale, scale_bytes)) ||
+        rows_overlap(o, whole_rows(v_scale, scale_bytes)))
+        return BSA_ERR_SHAPE;
     const int sms = device_sm_count();
     Q8Params A{};
     A.q = static_cast<const uint16_t*>(q);

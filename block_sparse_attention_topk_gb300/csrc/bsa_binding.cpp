@@ -21,6 +21,7 @@
 #include <string>
 
 #include "../../include/bsa_topk.h"
+#include "bsa_overlap.h"
 
 namespace {
 
@@ -82,6 +83,16 @@ bool heads(const Tensor& t, const char* name, at::ScalarType type, const at::Dev
                     (long long)out->H, (long long)out->D, (long long)T, (long long)H, (long long)D);
     if (out->D > 1 && t.stride(2) != 1) return fail("%s must be contiguous along its last dimension", name);
     return true;
+}
+
+// The memory of a tensor with these heads, and of a contiguous one.
+bsa::Rows rows_of(const Tensor* t, const Heads& h) {
+    if (t == nullptr) return bsa::whole_rows(nullptr, 0);
+    const int64_t size = (int64_t)t->element_size();
+    return bsa::Rows{t->const_data_ptr(), h.T, h.H, h.D * size, h.ts * size, h.hs * size};
+}
+bsa::Rows rows_of(const Tensor* t) {
+    return t == nullptr ? bsa::whole_rows(nullptr, 0) : bsa::whole_rows(t->const_data_ptr(), (int64_t)t->nbytes());
 }
 
 struct Rope {
@@ -198,7 +209,12 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int interleaved = PyObject_IsTrue(a[4]), inverse = PyObject_IsTrue(a[5]);
     if (interleaved < 0 || inverse < 0) return nullptr;
     Tensor made;
-    if (out != nullptr && !heads(*out, "out", type, device, xh.T, xh.H, xh.D, &oh)) return nullptr;
+    if (out != nullptr) {
+        if (!heads(*out, "out", type, device, xh.T, xh.H, xh.D, &oh)) return nullptr;
+        const bool same = x->const_data_ptr() == out->const_data_ptr() && (xh.T == 1 || xh.ts == oh.ts) && (xh.H == 1 || xh.hs == oh.hs);
+        if (!same && bsa::rows_overlap(rows_of(x, xh), rows_of(out, oh)))
+            return fail("out must not overlap x, unless it is x"), nullptr;
+    }
     if (!on_gpu(device, "x")) return nullptr;
     if (out == nullptr) {
         made = at::empty({xh.T, xh.H, xh.D}, x->options().requires_grad(false));
@@ -261,7 +277,16 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Rope r;
     if (!rope_args(a[9], a[8], a[10], kh.T, device, &r)) return nullptr;
     const int interleaved = PyObject_IsTrue(a[11]);
-    if (interleaved < 0 || !on_gpu(device, "k")) return nullptr;
+    if (interleaved < 0) return nullptr;
+    {
+        const char* name[8] = {"q_out", "k_cache", "v_cache", "k_scale", "v_scale", "q", "k", "v"};
+        const bsa::Rows r[8] = {rows_of(q_out), rows_of(c[0]), rows_of(c[1]), rows_of(c[2]), rows_of(c[3]),
+                                rows_of(q, qh), rows_of(k, kh), rows_of(v, vh)};
+        for (int i = 0; i < 5; ++i)
+            for (int j = i + 1; j < 8; ++j)
+                if (bsa::rows_overlap(r[i], r[j])) return fail("%s must not overlap %s", name[i], name[j]), nullptr;
+    }
+    if (!on_gpu(device, "k")) return nullptr;
     Tensor made;
     if (q != nullptr && q_out == nullptr) {
         made = at::empty({qh.T, qh.H, qh.D}, q->options().requires_grad(false));
@@ -334,7 +359,14 @@ PyObject* py_attention_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
         scale = 1.0 / std::sqrt((double)D);
     }
-    if (out != nullptr && !whole(*out, "out", at::kBFloat16, device, {T, H, G, D})) return nullptr;
+    if (out != nullptr) {
+        if (!whole(*out, "out", at::kBFloat16, device, {T, H, G, D})) return nullptr;
+        const char* name[4] = {"k_cache", "v_cache", "k_scale", "v_scale"};
+        for (int i = 0; i < 4; ++i)
+            if (bsa::rows_overlap(rows_of(out), rows_of(c[i]))) return fail("out must not overlap %s", name[i]), nullptr;
+        if (out->const_data_ptr() != q->const_data_ptr() && bsa::rows_overlap(rows_of(out), rows_of(q)))
+            return fail("out must not overlap q, unless it is q"), nullptr;
+    }
     if (ws != nullptr && (ws->device() != device || !ws->is_contiguous()))
         return fail("workspace must be a contiguous tensor on %s", device.str().c_str()), nullptr;
     if (!on_gpu(device, "q")) return nullptr;

@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include "bsa_internal.h"
+#include "bsa_overlap.h"
 #include "bsa_rope.cuh"
 
 namespace bsa {
@@ -212,7 +213,10 @@ extern "C" int bsa_rope(const void* x, int32_t dtype, int64_t T, int64_t H, int6
     const uintptr_t size = dtype == BSA_DTYPE_BF16 ? 2 : 4;
     if (reinterpret_cast<uintptr_t>(x) % size != 0 || reinterpret_cast<uintptr_t>(out) % size != 0)
         return BSA_ERR_ALIGN;
-    if (x == out && ((T > 1 && token_stride != out_token_stride) || (H > 1 && head_stride != out_head_stride)))
+    const bool same = x == out && (T == 1 || token_stride == out_token_stride) && (H == 1 || head_stride == out_head_stride);
+    const int64_t row = D * (int64_t)size, es = (int64_t)size;
+    if (!same && rows_overlap(Rows{x, T, H, row, token_stride * es, head_stride * es},
+                              Rows{out, T, H, row, out_token_stride * es, out_head_stride * es}))
         return BSA_ERR_SHAPE;
     RopeArgs A{};
     A.r = RopeParams{positions, T, inv_freq, freq_axis, axes, rot_dim / 2,

@@ -295,7 +295,8 @@ int bsa_sparse_decode_attention(const void* q, const void* k_cache, const void* 
  * t * token_stride + h * head_stride + d, dtype BSA_DTYPE_BF16 or
  * BSA_DTYPE_FP32, 1 <= D <= BSA_MAX_ROPE_DIM, any element alignment; 32-bit
  * arithmetic, rounded once.  out may be x itself with the same strides (in
- * place) and must not overlap it otherwise; its rows must not overlap.
+ * place) and must not overlap it otherwise (BSA_ERR_SHAPE); its rows must not
+ * overlap.
  * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_DTYPE, BSA_ERR_ALIGN. */
 int bsa_rope(const void* x, int32_t dtype, int64_t T, int64_t H, int64_t D,
              int64_t token_stride, int64_t head_stride, const int32_t* positions, int32_t axes,
@@ -320,8 +321,9 @@ typedef struct bsa_append_args {
     int64_t v_token_stride, v_head_stride;
     int64_t q_token_stride, q_head_stride;
     /* rotated queries, bf16 [T, Hq, D] contiguous, 16-byte aligned (NULL
-     * exactly when q is), apart from q.  Rows of no sequence or at a negative
-     * position are padding: their queries are written as zeros. */
+     * exactly when q is).  Rows of no sequence or at a negative position are
+     * padding: their queries are written as zeros.  What the call writes (q_out,
+     * caches, scales) shares no memory with the rest (BSA_ERR_SHAPE). */
     void* q_out;
     /* rotary positions as above; positions NULL: the position in the
      * sequence (axes 1).  rot_dim 0: no rotation (inv_freq may be NULL). */
@@ -389,7 +391,7 @@ size_t bsa_attention_q8_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t
  *   out[t, h, g] = sum_j softmax_j(scale * q[t, h, g] . k_j) v_j
  * over the first sparse_ctx[t, h] table tokens, with the page, slot, empty
  * and out-of-range rules (and status bits) of bsa_sparse_decode_attention.
- *   q, out: bf16 [T, H, G, D], 16-byte aligned; k_cache, v_cache: dtype
+ *   q, out: bf16 [T, H, G, D], 16-byte aligned, the same or apart; k_cache, v_cache: dtype
  *   BSA_DTYPE_E4M3 or BSA_DTYPE_E5M2, [num_pages, 16, H, D], 16-byte aligned,
  *   num_pages < 2^27; k_scale, v_scale: float [num_pages, H], finite, not
  *   negative; D in {64, 128, 256}; 1 <= G <= BSA_MAX_ATTN_Q8_GROUP; T * H <= 2^24.
