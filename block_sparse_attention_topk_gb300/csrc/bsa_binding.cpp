@@ -109,24 +109,26 @@ bool rope_args(PyObject* positions, PyObject* inv_freq, PyObject* freq_axis, int
         return false;
     if (f != nullptr) {
         if (!whole(*f, "inv_freq", at::kFloat, device, {-1})) return false;
+        if (f->size(0) > INT32_MAX / 2) return fail("inv_freq is too long");
         r->rot_dim = (int32_t)(2 * f->size(0));
-        r->inv_freq = f->const_data_ptr<float>();
     }
     if (p != nullptr) {
         if (p->dim() == 2) {
             if (!whole(*p, "positions", at::kInt, device, {-1, T})) return false;
+            if (p->size(0) > INT32_MAX) return fail("positions has too many axes");
             r->axes = (int32_t)p->size(0);
         } else if (!whole(*p, "positions", at::kInt, device, {T})) {
             return false;
         }
-        r->positions = p->const_data_ptr<int32_t>();
     }
     if (a != nullptr) {
         if (!whole(*a, "freq_axis", at::kInt, device, {r->rot_dim / 2})) return false;
-        r->freq_axis = a->const_data_ptr<int32_t>();
     } else if (r->axes > 1 && r->rot_dim > 0) {
         return fail("freq_axis is needed with several position axes");
     }
+    if (f != nullptr) r->inv_freq = f->const_data_ptr<float>();
+    if (p != nullptr) r->positions = p->const_data_ptr<int32_t>();
+    if (a != nullptr) r->freq_axis = a->const_data_ptr<int32_t>();
     return true;
 }
 
