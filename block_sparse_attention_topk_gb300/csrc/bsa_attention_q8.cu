@@ -85,15 +85,16 @@ constexpr float kSpread = 65536.f;       // a largest scale this much above the 
 struct Chunk {
     int row, ctx, c0, nb;    // nb < 0: no more
     int qbuf, last;
-    float mid;               // log2 of the value scales' middle
 };
 
 template <int PAGES, int GP, int NU, int GROUPS, int HG>
 struct Q8Shared {
     float2 page_scale[kDepth][PAGES];       // ks * scale * log2 e, log2 vs (-inf: no page) of the announced chunks
-    uint64_t full[kMaxRing], empty[kMaxRing], s_full[2][NU], p_full[NU], c_full[kDepth], c_empty[kDepth];
+    // c_full: a chunk's queries are there, x_full: its scales too
+    uint64_t full[kMaxRing], empty[kMaxRing], s_full[2][NU], p_full[NU], c_full[kDepth], x_full[kDepth], c_empty[kDepth];
     uint64_t o_full, drained;
     Chunk chunk[kDepth];
+    float mid[kDepth];                      // log2 of the middle of a chunk's value scales
     float qinv[kDepth][GP];
     float red[GROUPS][4][HG];
     int box_z[2][PAGES];                    // page coordinates of the copied chunks
@@ -324,7 +325,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
     auto &full = S.full, &empty = S.empty;
     auto& s_full = S.s_full;
     auto& p_full = S.p_full;
-    auto &c_full = S.c_full, &c_empty = S.c_empty;
+    auto &c_full = S.c_full, &x_full = S.x_full, &c_empty = S.c_empty;
     auto &o_full = S.o_full, &drained = S.drained;
     auto& chunk = S.chunk;
     auto& qinv = S.qinv;
@@ -351,6 +352,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         }
         for (int i = 0; i < kDepth; ++i) {
             mbar_init(&c_full[i], 32);
+            mbar_init(&x_full[i], 32);
             mbar_init(&c_empty[i], C::SOFTMAX + 1);      // and the MMA warp
         }
         mbar_init(&o_full, 1);
@@ -641,6 +643,10 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     }
                     if (lane >= A.G && lane < GP) qinv[qbuf][lane] = 0.f;
                 }
+                // the scores may start; their scales follow
+                if (lane == 0) chunk[buf] = Chunk{it.row, it.ctx, c0, nb, qbuf, c0 + nb == it.b1};
+                fence_async_smem();
+                mbar_arrive(&c_full[buf]);
                 // the least and the largest of the values' scales
                 uint32_t least = 0x7F800000u, most = 0;
 #pragma unroll
@@ -691,11 +697,8 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     page_scale[buf][p] = pg[r] < 0 ? make_float2(0.f, -INFINITY)
                                                    : make_float2(ks[r] * A.scale_log2e, log2f(fmaxf(vs[r], floor_vs)));
                 }
-                if (lane == 0)
-                    chunk[buf] = Chunk{it.row, it.ctx, c0, nb, qbuf, c0 + nb == it.b1,
-                                       most == 0 ? 0.f : 0.5f * (log2f(floor_vs) + log2f(__uint_as_float(most)))};
-                fence_async_smem();
-                mbar_arrive(&c_full[buf]);
+                if (lane == 0) S.mid[buf] = most == 0 ? 0.f : 0.5f * (log2f(floor_vs) + log2f(__uint_as_float(most)));
+                mbar_arrive(&x_full[buf]);
             }
         }
         if (ok) ok = c < kDepth || mbar_wait(&c_empty[c % kDepth], (c / kDepth - 1) & 1, quit, A.wait_ns);
@@ -703,6 +706,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         if (lane == 0) chunk[c % kDepth].nb = -1;
         __syncwarp();
         mbar_arrive(&c_full[c % kDepth]);
+        mbar_arrive(&x_full[c % kDepth]);
     } else {
         // ------------------------------------------------ softmax and output
         const int tok = tid & 127, quad = warp & 3;
@@ -796,12 +800,13 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         // loops go on with what there is; the items from that on are not written here.
         for (uint32_t c = 0;; ++c) {
             const int buf = c % kDepth;
-            mbar_wait(&c_full[buf], (c / kDepth) & 1, quit, A.wait_ns);
+            mbar_wait(&x_full[buf], (c / kDepth) & 1, quit, A.wait_ns);
             const bool gone = *quit;
             const Chunk ch = chunk[buf];
             const int nb = ch.nb;
             if (group_any(group, gone || nb < 0)) break;
             const float2* scales = page_scale[buf];
+            const float mid = S.mid[buf];
             float qi[HG], ct[HG];
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
@@ -844,7 +849,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
 #pragma unroll
                 for (int g = 0; g < HG; ++g) {
                     const float t = fmaxf(fmaxf(red[group][0][g], red[group][1][g]), fmaxf(red[group][2][g], red[group][3][g]));
-                    const float top = fmaxf(mt[g], t), m = fmaxf(ml[g], t - ch.mid);
+                    const float top = fmaxf(mt[g], t), m = fmaxf(ml[g], t - mid);
                     if (t > -INFINITY) {
                         const float keep = ex2(mt[g] - top);
 #pragma unroll
@@ -867,7 +872,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                         load_terms<HG, GP>(s_cols + (b + j) * N, x);
                         const float2 sc = scales[(b + j) * kPagesPerBlock + part16];
                         const bool live = b + j < nb && (ch.c0 + b + j) * kPageSize + tok < ch.ctx && sc.y != -INFINITY;
-                        const float per_w = live ? ex2(ch.mid - sc.y - kTop) : 0.f;     // p_j / w_j
+                        const float per_w = live ? ex2(mid - sc.y - kTop) : 0.f;     // p_j / w_j
                         float w[HG];
 #pragma unroll
                         for (int g = 0; g < HG; ++g) {
@@ -908,7 +913,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     mbar_arrive(&p_full[b >> 1]);
                 }
 #pragma unroll
-                for (int g = 0; g < HG; ++g) l[g] = fmaf(lc[g], ct[g] < INFINITY ? ex2(kTop - ct[g] - ch.mid - ml[g]) : 1.f, l[g]);
+                for (int g = 0; g < HG; ++g) l[g] = fmaf(lc[g], ct[g] < INFINITY ? ex2(kTop - ct[g] - mid - ml[g]) : 1.f, l[g]);
                 s_phase ^= ((1u << ((nb + 1) >> 1)) - 1) << (sbuf * 8);
                 ++s;
             }
