@@ -32,7 +32,9 @@ __device__ __forceinline__ unsigned long long rope_step(float f) {
     return (unsigned long long)(t * 18446744073709551616.0);
 }
 
-// (cos, sin) of p turns-steps; the fraction of a turn as [-1, 1) half turns.
+// (cos, sin) of p turns-steps; the fraction of a turn as [-1, 1) half turns, rounded
+// to fp32's 24 bits (the angle by pi 2^-25 at most: the rotated fp32 values' error is
+// 3.9e-8 relative in norm, 3.0e-8 with 64-bit angles).
 __device__ __forceinline__ float2 rope_turn(int32_t p, unsigned long long step) {
     const long long phase = (long long)((unsigned long long)(long long)p * step);
     float2 r;

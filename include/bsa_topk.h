@@ -285,7 +285,8 @@ int bsa_sparse_decode_attention(const void* q, const void* k_cache, const void* 
  * [axes, T] and pair i turns with axis freq_axis[i] (clamped into
  * [0, axes)); freq_axis may be NULL when axes is 1.  The product
  * p * inv_freq[i] is reduced to a fraction of a turn in 64-bit fixed point,
- * so far positions lose nothing.  inv_freq: float[rot_dim / 2]. */
+ * so far positions lose nothing; the fraction is rounded to 24 bits before its
+ * cosine and sine.  inv_freq: float[rot_dim / 2], finite. */
 #define BSA_ROPE_INTERLEAVED 1
 #define BSA_ROPE_INVERSE 2      /* turn back: the gradient of the rotation */
 #define BSA_MAX_ROPE_DIM 1024
@@ -464,8 +465,8 @@ int bsa_select_policy(int64_t rows, int64_t M, int32_t K, int32_t dtype, int32_t
  *                            still written as computed); or the index scoring
  *                            met an entry of a causal block below max_blocks
  *                            outside [0, num_phys_blocks) (scored -inf); or
-                            the append met a token whose page lies outside
-                            the cache (not stored).
+ *                            the append met a token whose page lies outside
+ *                            the cache (not stored).
  *   BSA_STATUS_BAD_PAGE      the sparse decode attention met a table entry of
  *                            a context token outside [0, num_pages) (the token
  *                            takes no part).
