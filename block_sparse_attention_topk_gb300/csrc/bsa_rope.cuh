@@ -32,14 +32,16 @@ __device__ __forceinline__ unsigned long long rope_step(float f) {
     return (unsigned long long)(t * 18446744073709551616.0);
 }
 
-// (cos, sin) of p turns-steps; the fraction of a turn as [-1, 1) half turns, rounded
-// to fp32's 24 bits (the angle by pi 2^-25 at most: the rotated fp32 values' error is
-// 3.9e-8 relative in norm, 3.0e-8 with 64-bit angles).
+// (cos, sin) of p turns-steps.  The nearest quarter turn is taken off in fixed point,
+// so that what is rounded to fp32's 24 bits is an eighth of a turn at most: the angle is
+// off by pi 2^-28 (rounded as it is, up to half a turn, pi 2^-25).
 __device__ __forceinline__ float2 rope_turn(int32_t p, unsigned long long step) {
-    const long long phase = (long long)((unsigned long long)(long long)p * step);
-    float2 r;
-    sincospif(__ll2float_rn(phase) * 0x1p-63f, &r.y, &r.x);
-    return r;
+    const unsigned long long phase = (unsigned long long)(long long)p * step;
+    const uint32_t k = (uint32_t)((phase + (1ull << 61)) >> 62);
+    float c, s;
+    sincospif(__ll2float_rn((long long)(phase - ((unsigned long long)k << 62))) * 0x1p-63f, &s, &c);
+    const float x = k & 1 ? s : c, y = k & 1 ? c : s;
+    return make_float2(k == 1 || k == 2 ? -x : x, k >= 2 ? -y : y);
 }
 
 __device__ __forceinline__ int rope_axis(const RopeParams& R, int i) {

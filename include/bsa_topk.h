@@ -285,8 +285,8 @@ int bsa_sparse_decode_attention(const void* q, const void* k_cache, const void* 
  * [axes, T] and pair i turns with axis freq_axis[i] (clamped into
  * [0, axes)); freq_axis may be NULL when axes is 1.  The product
  * p * inv_freq[i] is reduced to a fraction of a turn in 64-bit fixed point,
- * so far positions lose nothing; the fraction is rounded to 24 bits before its
- * cosine and sine.  inv_freq: float[rot_dim / 2], finite. */
+ * so far positions lose nothing; cosines and sines are fp32.  inv_freq:
+ * float[rot_dim / 2], finite. */
 #define BSA_ROPE_INTERLEAVED 1
 #define BSA_ROPE_INVERSE 2      /* turn back: the gradient of the rotation */
 #define BSA_MAX_ROPE_DIM 1024
