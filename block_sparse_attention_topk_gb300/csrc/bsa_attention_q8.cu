@@ -723,8 +723,9 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
         const uint32_t turn[6] = {lane & 1 ? 0x6420u : 0x7531u, lane & 1 ? 0x3514u : 0x5240u, lane & 1 ? 0x3716u : 0x7260u,
                                   lane & 2 ? 0x5410u : 0x7632u, lane & 2 ? 0x3254u : 0x5410u, lane & 2 ? 0x3276u : 0x7610u};
         uint32_t s_phase = 0, o_phase = 0, s = 0;      // s: chunks with blocks so far
-        // outputs in units of 2^mt and sums in units of 2^ml, the open chunk's outputs
-        // in units of 2^mt / take
+        // sums in units of 2^ml, outputs in units of 2^(mt - kTop), the open chunk's in
+        // units of take^2 of those.  Chunks of zeros among tiny values lie further apart than
+        // fp32's powers of two, their products with outputs do not: hence in two factors.
         float acc[PANELS][HG], mt[HG], ml[HG], l[HG], take[HG];
 #pragma unroll
         for (int g = 0; g < HG; ++g) {
@@ -748,7 +749,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     float o[HG];
                     load_output<HG, GP>(lanes + 2 * C::S_COLS + p * NP, o);
 #pragma unroll
-                    for (int g = 0; g < HG; ++g) acc[p][g] = fmaf(o[g], take[g], acc[p][g]);
+                    for (int g = 0; g < HG; ++g) acc[p][g] = fmaf(o[g] * take[g], take[g], acc[p][g]);
                 }
                 tc_fence_before();
             }
@@ -770,9 +771,7 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                 for (int g = 0; g < HG; ++g) {
                     if (g0 + g < A.G && !bad) {
                         const float sum = red[group][0][g] + red[group][1][g] + red[group][2][g] + red[group][3][g];
-                        // 2^(mt - ml) in two factors: it may lie outside fp32's range where
-                        // the output does not
-                        const float f = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ex2(0.5f * (mt[g] - ml[g]));
+                        const float f = sum == 0.f ? 0.f : 1.f / sum, e = sum == 0.f ? 0.f : ex2(0.5f * (mt[g] - ml[g] - kTop));
 #pragma unroll
                         for (int p = 0; p < PANELS; ++p) {
                             const float o = acc[p][g] * e * f * e;
@@ -853,12 +852,12 @@ attention_q8_kernel(const Q8Params A, const __grid_constant__ Q8Maps M) {
                     const float t = fmaxf(fmaxf(red[group][0][g], red[group][1][g]), fmaxf(red[group][2][g], red[group][3][g]));
                     const float top = fmaxf(mt[g], t), m = fmaxf(ml[g], t - mid);
                     if (t > -INFINITY) {
-                        const float keep = ex2(mt[g] - top);
+                        const float keep = ex2(0.5f * (mt[g] - top));
 #pragma unroll
-                        for (int p = 0; p < PANELS; ++p) acc[p][g] *= keep;
+                        for (int p = 0; p < PANELS; ++p) acc[p][g] = acc[p][g] * keep * keep;
                         l[g] *= ex2(ml[g] - m);
                     }
-                    take[g] = t > -INFINITY ? ex2(t - top - kTop) : 0.f;
+                    take[g] = t > -INFINITY ? ex2(0.5f * (t - top)) : 0.f;
                     mt[g] = top;
                     ml[g] = m;
                     ct[g] = kTop - t;

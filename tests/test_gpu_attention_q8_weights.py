@@ -127,3 +127,32 @@ def test_attention_q8_scales_of_zero_and_subnormal_scales(cuda_device):
     s[1][bt[1, 0, ::2].long()] = 2.0 ** -140
     s[1][bt[2, 0, :4].long()] = 0
     _check_small(cuda_device, q, c, s, bt, ctx, dtype, kind)
+
+
+@pytest.mark.parametrize("fmt", list(KIND))
+@pytest.mark.parametrize("G,D", [(8, 128), (16, 64), (2, 256)])
+@pytest.mark.parametrize("std", [1e-25, 1e-31, 1e-34, 1e-37])
+def test_attention_q8_tiny_values_beside_blocks_of_zeros(cuda_device, fmt, G, D, std):
+    """Whole chunks of zeros, with the scale 1, before, between and behind tokens with
+    tiny values, in rows that one CTA walks."""
+    n, H, T = 3000, 1, 320
+    g = torch.Generator().manual_seed(G + D)
+    keys = torch.randn((n, H, D), generator=g)
+    q = torch.randn((T, H, G, D), generator=g).to(torch.bfloat16)
+    assert bsa.bsa_attention_q8_workspace_bytes(T, H, G, D, 24) == 0
+    for first, last in ((0, 768), (768, 1536), (2304, 3000)):
+        v = std * torch.randn((n, H, D), generator=g)
+        v[first:last] = 0
+        codes, scales, pages, dtype, kind = _appended(cuda_device, fmt, H, D, v, keys)
+        bt = pages.expand(T, H, -1).contiguous()
+        rows = [0, 1, 317]
+        ctx = torch.full((T, H), n, dtype=torch.int32)
+        got = bsa.bsa_sparse_decode_attention_q8(*(x.to(cuda_device) for x in (
+            q, codes[0].view(dtype), codes[1].view(dtype), scales[0], scales[1], bt, ctx)))
+        torch.cuda.synchronize()
+        cn, sn, sc = [x.numpy() for x in codes], [x.numpy() for x in scales], D ** -0.5
+        sub = (q[rows], cn, sn, bt[rows].numpy(), ctx[rows].numpy(), kind, sc)
+        want = oracle.sparse_decode_attention_q8(sub[0], cn[0], cn[1], kind, sn[0], sn[1], sub[3], sub[4], sc)
+        tol = _bound(*sub, want) - 1e-30 + 2.0 ** -134
+        err = np.abs(got[rows].double().cpu().numpy() - want)
+        assert (err <= tol).all(), (err.max(), np.abs(want).max())
