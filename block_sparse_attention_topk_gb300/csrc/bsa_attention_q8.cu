@@ -28,9 +28,10 @@
 // fp32, and maxima and accumulators are fp32.
 //
 // The work: a CTA takes items (a row, or a share of its 128-token blocks when
-// rows are few; a cluster of CTAs or a second launch joins the shares) and walks each in chunks of up to 6 blocks.  A chunk's scores are
-// complete in TMEM before its probabilities are formed, so there is one maximum
-// per chunk and the accumulators in TMEM start anew with each chunk.
+// rows are few; a cluster of CTAs or a second launch joins the shares) and walks
+// each in chunks of up to 6 blocks.  A chunk's scores are complete in TMEM before
+// its probabilities are formed, so there is one maximum per chunk and the
+// accumulators in TMEM start anew with each chunk.
 //  softmax    thread i of a group of four warps is token i of a block
 //             (probabilities) and dimension i of the head (output); a second
 //             group takes query heads 8 to 15,
@@ -54,9 +55,9 @@
 // D 128) take 86 to 88 us, 6.2 TB/s, with DRAM reads of just those bytes; rows whose
 // blocks lie in L2 reach 10 TB/s.  64-wide heads are bound by the copies' rows, of
 // 64 bytes each, at about 3.4 cycles a row and SM (1024 rows of up to 2048
-// tokens 47 us); 9 to 16 query heads by the softmax of the SM's one CTA.  A CTA of
-// up to 8 heads of 128 has a ring of five blocks beside its weights, with three chunks announced
-// ahead (two chunks: 2000 rows of one prompt take 107 us, three 97).
+// tokens 47 us); 9 to 16 query heads by the softmax of the SM's one CTA.  With 8
+// heads of 128 a CTA has a ring of five blocks beside its weights and three chunks
+// announced ahead (with two, 2000 rows of one prompt take 107 us instead of 97).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
