@@ -51,17 +51,23 @@ EXPORTED = [
     "bsa_index_score_topk_select", "bsa_sparse_decode_attention", "bsa_set_status_word",
     "bsa_read_status", "bsa_rope", "bsa_append_kv_decode", "bsa_append_kv_varlen",
     "bsa_attention_q8_workspace_bytes", "bsa_sparse_decode_attention_q8",
+    "bsa_paged_attention_workspace_bytes", "bsa_paged_attention_decode",
+    "bsa_paged_attention_varlen", "bsa_fork_workspace_bytes", "bsa_compact_workspace_bytes",
+    "bsa_fork_requests", "bsa_compact_blocks",
 ]
 # bits of the device status word (bsa_set_status_word)
 BSA_STATUS_BAD_BLOCK_ID = 0x1
 BSA_STATUS_BAD_PAGE = 0x2
 BSA_STATUS_BAD_CONTEXT = 0x4
 BSA_STATUS_TIMEOUT = 0x8
+BSA_STATUS_NO_BLOCK = 0x10
 MAX_ATTN_GROUP = 8
 MAX_INDEX_DIM = 1024
 MAX_INDEX_QUERIES = 16
 MAX_ATTN_Q8_GROUP = 16
 MAX_CACHE_DIM = 256
+MAX_PAGED_GROUP = 64
+MAX_BLOCK_TENSORS = 512
 BSA_ROPE_INTERLEAVED = 1
 BSA_ROPE_INVERSE = 2
 
@@ -97,6 +103,24 @@ class AppendArgs(ctypes.Structure):
                    ("num_pages", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
                    ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                    ("num_reqs", ctypes.c_int64), ("max_blocks", ctypes.c_int64)])
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    """bsa_paged_attention_args_t of include/bsa_topk.h."""
+    _fields_ = ([("q", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("T", "H", "G", "D")]
+                + [("out", ctypes.c_void_p), ("cache_dtype", ctypes.c_int32),
+                   ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                   ("num_pages", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
+                   ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                   ("num_reqs", ctypes.c_int64), ("max_blocks", ctypes.c_int64),
+                   ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                   ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                   ("workspace_bytes", ctypes.c_size_t)])
+
+
+class BlockTensor(ctypes.Structure):
+    """bsa_block_tensor_t of include/bsa_topk.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("bytes_per_block", ctypes.c_int64)]
 
 
 _lib = None
@@ -154,6 +178,17 @@ def lib() -> ctypes.CDLL:
             L.bsa_sparse_decode_attention_q8.argtypes = [vp, vp, vp, i32, vp, vp, i64, vp, vp, i64,
                                                          i64, i64, i64, i32, ctypes.c_float, vp, vp,
                                                          sz, vp]
+            paged = ctypes.POINTER(PagedAttentionArgs)
+            L.bsa_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, i64]
+            L.bsa_paged_attention_decode.argtypes = [paged, vp, i32, vp]
+            L.bsa_paged_attention_varlen.argtypes = [paged, vp, vp, vp]
+            L.bsa_fork_workspace_bytes.argtypes = [i64, i64, i64, i64]
+            L.bsa_compact_workspace_bytes.argtypes = [i64]
+            for name in ("paged_attention", "fork", "compact"):
+                getattr(L, f"bsa_{name}_workspace_bytes").restype = sz
+            blocks = [ctypes.POINTER(BlockTensor), i32, vp, vp, vp, i64, i64, i64]
+            L.bsa_fork_requests.argtypes = blocks + [vp, vp, i64, vp, vp, vp, vp, sz, vp]
+            L.bsa_compact_blocks.argtypes = blocks + [vp, vp, vp, vp, sz, vp]
             for name in EXPORTED[1:]:
                 if not name.endswith("_workspace_bytes"):
                     getattr(L, name).restype = ctypes.c_int
@@ -690,3 +725,94 @@ def bsa_sparse_decode_attention_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     [T, H, G, D], without a gradient.  The scale defaults to 1 / sqrt(D)."""
     return _binding().attention_q8(q, k_cache, v_cache, k_scale, v_scale, sparse_bt, sparse_ctx,
                                    scale, out, workspace)
+
+
+def bsa_paged_attention_workspace_bytes(T: int, H: int, G: int, D: int,
+                                        device: torch.device | None = None) -> int:
+    """Workspace bytes of bsa_paged_attention_* on `device` (default: the
+    current one)."""
+    if device is None:
+        return int(lib().bsa_paged_attention_workspace_bytes(T, H, G, D))
+    with torch.cuda.device(device):
+        return int(lib().bsa_paged_attention_workspace_bytes(T, H, G, D))
+
+
+def bsa_paged_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               block_table: torch.Tensor, seq_lens: torch.Tensor,
+                               decode_query_len: int, window: int | None = None, sinks: int = 0,
+                               k_scale: torch.Tensor | None = None,
+                               v_scale: torch.Tensor | None = None, scale: float | None = None,
+                               out: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention of the decode rows over everything their requests hold
+    in the paged cache, the new tokens among it.  q bf16 [T, H, G, D]; the
+    caches, scales, block_table and seq_lens as for bsa_append_kv_decode.
+    With a window a row at position p sees the tokens j <= p with
+    j > p - window or j < sinks.  Returns bf16 [T, H, G, D], zeros where a row
+    sees nothing, without a gradient.  The scale defaults to 1 / sqrt(D)."""
+    return _binding().paged_attention(q, k_cache, v_cache, block_table, seq_lens,
+                                      operator.index(decode_query_len), _window(window), sinks,
+                                      k_scale, v_scale, scale, out, workspace)
+
+
+def bsa_paged_attention_varlen(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               block_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                               prefix_lens: torch.Tensor, window: int | None = None,
+                               sinks: int = 0, k_scale: torch.Tensor | None = None,
+                               v_scale: torch.Tensor | None = None, scale: float | None = None,
+                               out: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """bsa_paged_attention_decode for rows of varying count, e.g. a chunk of a
+    prompt: sequence i owns rows [cu_seqlens_q[i], cu_seqlens_q[i + 1]) and its
+    j-th token sits at position prefix_lens[i] + j.  Rows of no sequence are
+    zeros."""
+    if not isinstance(cu_seqlens_q, torch.Tensor):
+        raise ValueError("cu_seqlens_q must be a tensor")
+    return _binding().paged_attention(q, k_cache, v_cache, block_table, prefix_lens, cu_seqlens_q,
+                                      _window(window), sinks, k_scale, v_scale, scale, out,
+                                      workspace)
+
+
+def _window(window: int | None) -> int:
+    """0 for none; a window of no token is refused."""
+    if window is None:
+        return 0
+    if operator.index(window) < 1:
+        raise ValueError("window must be at least 1, or None")
+    return window
+
+
+def bsa_fork_requests(tensors, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                      block_refs: torch.Tensor, parent: torch.Tensor,
+                      new_tokens: torch.Tensor | None = None,
+                      table_out: torch.Tensor | None = None,
+                      lens_out: torch.Tensor | None = None,
+                      refs_out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None):
+    """The requests' next state: row r has the tokens of request parent[r]
+    (none for -1) and room for new_tokens[r] more.  Forks, reorders, grows and
+    frees requests in one call without a synchronisation: full blocks are
+    shared, an unfinished last block goes to the lowest row that descends from
+    its request and is copied for the others, in every one of `tensors` (each
+    [num_blocks, ...] or [8 * num_blocks, ...]: caches, scales, pooled index
+    keys, of every layer).  block_table int32 [num_reqs, max_blocks], seq_lens
+    int32 [num_reqs], block_refs int32 [num_blocks] (how many rows hold each
+    block), parent and new_tokens int32 [num_out].  Returns (table_out,
+    lens_out, refs_out), by default new; block_table, seq_lens and block_refs
+    themselves may be given."""
+    return _binding().fork(tensors, block_table, seq_lens, block_refs, parent, new_tokens,
+                           table_out, lens_out, refs_out, workspace)
+
+
+def bsa_compact_blocks(tensors, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                       block_refs: torch.Tensor, table_out: torch.Tensor | None = None,
+                       refs_out: torch.Tensor | None = None,
+                       new_ids: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None):
+    """Moves the blocks in use to the lowest ids, with their contents in every
+    one of `tensors` (as for bsa_fork_requests).  Returns (table_out, refs_out,
+    new_ids): block_table and block_refs in the new ids, by default new tensors
+    (the inputs themselves may be given), and each block's new id, -1 for a
+    free one."""
+    return _binding().compact(tensors, block_table, seq_lens, block_refs, table_out, refs_out,
+                              new_ids, workspace)

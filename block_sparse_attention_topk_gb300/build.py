@@ -25,7 +25,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_NAME = f"libbsa_topk_{platform.machine()}.so"
 LIB_PATH = os.path.join(BUILD, LIB_NAME)
 SOURCES = ["bsa_select.cu", "bsa_table.cu", "bsa_capi.cu", "bsa_noalloc.cu", "bsa_attention.cu",
-           "bsa_rope.cu", "bsa_append.cu", "bsa_attention_q8.cu"]
+           "bsa_rope.cu", "bsa_append.cu", "bsa_attention_q8.cu", "bsa_blocks.cu",
+           "bsa_paged_attention.cu"]
 BINDING = "bsa_binding.cpp"
 BINDING_PATH = os.path.join(BUILD, f"bsa_binding_{platform.machine()}.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,5 +1,6 @@
 // bsa_binding.cpp -- argument checks and marshalling of the cache operators
-// (bsa_rope, bsa_append_kv_*, bsa_sparse_decode_attention_q8) for Python.
+// (bsa_rope, bsa_append_kv_*, bsa_sparse_decode_attention_q8,
+// bsa_paged_attention_*, bsa_fork_requests, bsa_compact_blocks) for Python.
 //
 // A decode step calls these on a few rows, where a call's kernels take 4 to 10
 // us.  Checking a dozen tensors attribute by attribute in Python and passing 20
@@ -411,6 +412,250 @@ PyObject* py_attention_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The package's workspace of the tensor's device and stream, held for a call.
+struct Workspace {
+    PyObject* held = nullptr;
+    ~Workspace() { Py_XDECREF(held); }
+    // `given`: the caller's, or null; `like`: the Python tensor whose device it is for
+    bool take(const Tensor** given, PyObject* like, size_t need) {
+        if (*given != nullptr || need == 0) return true;
+        PyObject* dev = PyObject_GetAttrString(like, "device");
+        if (dev == nullptr) return false;
+        held = PyObject_CallFunction(g_workspace, "On", dev, (Py_ssize_t)need);
+        Py_DECREF(dev);
+        if (held == nullptr) return false;
+        *given = &THPVariable_Unpack(held);
+        return true;
+    }
+};
+bool workspace_arg(PyObject* o, const at::Device& device, const Tensor** ws) {
+    if (!tensor(o, "workspace", ws)) return false;
+    if (*ws != nullptr && ((*ws)->device() != device || !(*ws)->is_contiguous()))
+        return fail("workspace must be a contiguous tensor on %s", device.str().c_str());
+    return true;
+}
+
+bool small_int(PyObject* o, const char* name, long long lo, int32_t* v) {
+    const long long n = PyLong_AsLongLong(o);
+    if (n == -1 && PyErr_Occurred()) return false;
+    if (n < lo || n > INT32_MAX) return fail("%s is out of range", name);
+    *v = (int32_t)n;
+    return true;
+}
+
+// paged_attention(q, k_cache, v_cache, block_table, rows, more, window, sinks, k_scale, v_scale, scale,
+//                 out, workspace) -> out.  rows and more as for append; window 0: none.
+PyObject* py_paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const Tensor *q, *table, *rows, *cu = nullptr, *out, *ws, *c[4];
+    if (!count(n, 13) || !needed(a[0], "q", &q) || !needed(a[3], "block_table", &table)) return nullptr;
+    const bool varlen = THPVariable_Check(a[5]);
+    if (!needed(a[4], varlen ? "prefix_lens" : "seq_lens", &rows) || !tensor(a[11], "out", &out)) return nullptr;
+    const at::Device device = q->device();
+    if (!whole(*q, "q", at::kBFloat16, device, {-1, -1, -1, -1})) return nullptr;
+    bsa_paged_attention_args_t p{};
+    p.T = q->size(0);
+    p.H = q->size(1);
+    p.G = q->size(2);
+    p.D = q->size(3);
+    if (!caches(a[1], a[2], a[8], a[9], device, p.H, p.D, &p.cache_dtype, &p.num_pages, c)) return nullptr;
+    if (!whole(*rows, varlen ? "prefix_lens" : "seq_lens", at::kInt, device, {-1})) return nullptr;
+    p.num_reqs = rows->size(0);
+    if (!whole(*table, "block_table", at::kInt, device, {p.num_reqs, -1})) return nullptr;
+    p.max_blocks = table->size(1);
+    int32_t dql = 0;
+    if (varlen) {
+        if (!needed(a[5], "cu_seqlens_q", &cu) || !whole(*cu, "cu_seqlens_q", at::kInt, device, {p.num_reqs + 1}))
+            return nullptr;
+    } else if (!small_int(a[5], "decode_query_len", INT32_MIN, &dql)) {
+        return nullptr;
+    }
+    if (!small_int(a[6], "window", 0, &p.window) || !small_int(a[7], "sinks", 0, &p.sinks)) return nullptr;
+    if (a[10] != Py_None) {
+        const double scale = PyFloat_AsDouble(a[10]);
+        if (scale == -1.0 && PyErr_Occurred()) return nullptr;
+        p.scale = (float)scale;
+    } else {
+        p.scale = (float)(1.0 / std::sqrt((double)p.D));
+    }
+    if (out != nullptr) {
+        if (!whole(*out, "out", at::kBFloat16, device, {p.T, p.H, p.G, p.D})) return nullptr;
+        const char* name[8] = {"q", "k_cache", "v_cache", "k_scale", "v_scale", "block_table", "the rows' lengths", "cu_seqlens_q"};
+        const Tensor* in[8] = {q, c[0], c[1], c[2], c[3], table, rows, cu};
+        for (int i = 0; i < 8; ++i)
+            if (bsa::rows_overlap(rows_of(out), rows_of(in[i]))) return fail("out must not overlap %s", name[i]), nullptr;
+    }
+    if (!workspace_arg(a[12], device, &ws) || !on_gpu(device, "q")) return nullptr;
+    const c10::DeviceGuard guard(device);
+    Tensor made;
+    if (out == nullptr) {
+        made = at::empty({p.T, p.H, p.G, p.D}, q->options().requires_grad(false));
+        out = &made;
+    }
+    Workspace held;
+    if (!held.take(&ws, a[0], bsa_paged_attention_workspace_bytes(p.T, p.H, p.G, p.D))) return nullptr;
+    void* stream;
+    if (!stream_of(device, &stream)) return nullptr;
+    p.q = data(q);
+    p.out = data_rw(out);
+    p.k_cache = data(c[0]);
+    p.v_cache = data(c[1]);
+    p.k_scale = static_cast<const float*>(data(c[2]));
+    p.v_scale = static_cast<const float*>(data(c[3]));
+    p.block_table = static_cast<const int32_t*>(data(table));
+    p.workspace = data_rw(ws);
+    p.workspace_bytes = ws == nullptr ? 0 : (size_t)ws->nbytes();
+    const int32_t* row_ptr = static_cast<const int32_t*>(data(rows));
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = varlen ? bsa_paged_attention_varlen(&p, static_cast<const int32_t*>(data(cu)), row_ptr, stream)
+                    : bsa_paged_attention_decode(&p, row_ptr, dql, stream);
+    Py_END_ALLOW_THREADS
+    if (!done(varlen ? "bsa_paged_attention_varlen" : "bsa_paged_attention_decode", status)) return nullptr;
+    changed(out);
+    return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(a[11]);
+    END_HANDLE_TH_ERRORS
+}
+
+// The tensors that a block's id stands for: contiguous, num_blocks blocks each along
+// their first dimension (or eight pages a block).
+struct BlockTensors {
+    bsa_block_tensor_t t[BSA_MAX_BLOCK_TENSORS];
+    const Tensor* of[BSA_MAX_BLOCK_TENSORS];
+    int32_t n = 0;
+
+    bool take(PyObject* list, const at::Device& device, int64_t num_blocks) {
+        PyObject* seq = PySequence_Fast(list, "tensors must be a list or tuple of tensors");
+        if (seq == nullptr) return false;
+        const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq);
+        bool ok = count <= BSA_MAX_BLOCK_TENSORS || fail("more than %d tensors", BSA_MAX_BLOCK_TENSORS);
+        for (Py_ssize_t i = 0; ok && i < count; ++i) {
+            const Tensor* x;
+            ok = needed(PySequence_Fast_GET_ITEM(seq, i), "each of tensors", &x);
+            if (!ok) break;
+            const bool shaped = x->dim() >= 1 && (x->size(0) == num_blocks || x->size(0) == num_blocks * BSA_PAGES_PER_SPARSE_BLOCK);
+            if (x->device() != device || !x->is_contiguous() || !shaped) {
+                ok = fail("tensors[%lld] must be contiguous on %s, with one entry per block (%lld) or page along its first dimension",
+                          (long long)i, device.str().c_str(), (long long)num_blocks);
+                break;
+            }
+            of[n] = x;
+            t[n++] = bsa_block_tensor_t{x->data_ptr(), num_blocks > 0 ? (int64_t)x->nbytes() / num_blocks : 0};
+        }
+        Py_DECREF(seq);      // the list, or a copy of it, whose tensors the caller holds
+        return ok;
+    }
+    void moved() const {
+        for (int32_t i = 0; i < n; ++i) changed(of[i]);
+    }
+};
+
+// An int32 output: the given one, or a new one in `made`.
+bool int_output(PyObject* o, const char* name, const at::Device& device, const Tensor& like, std::initializer_list<int64_t> shape,
+                Tensor* made, const Tensor** t) {
+    if (!tensor(o, name, t)) return false;
+    if (*t != nullptr) return whole(**t, name, at::kInt, device, shape);
+    *made = at::empty(at::IntArrayRef(shape.begin(), shape.size()), like.options().requires_grad(false));
+    *t = made;
+    return true;
+}
+
+PyObject* give(const Tensor& made, PyObject* given) { return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(given); }
+
+PyObject* give3(const Tensor (&made)[3], PyObject* const* given) {
+    PyObject* out = PyTuple_New(3);
+    for (int i = 0; out != nullptr && i < 3; ++i) {
+        PyObject* o = give(made[i], given[i]);
+        if (o == nullptr) Py_CLEAR(out);
+        else PyTuple_SET_ITEM(out, i, o);
+    }
+    return out;
+}
+
+// fork(tensors, block_table, seq_lens, block_refs, parent, new_tokens, table_out, lens_out, refs_out, workspace)
+//   -> (table_out, lens_out, refs_out)
+PyObject* py_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const Tensor *table, *lens, *refs, *parent, *more, *ws, *out[3];
+    if (!count(n, 10) || !needed(a[1], "block_table", &table) || !needed(a[2], "seq_lens", &lens) ||
+        !needed(a[3], "block_refs", &refs) || !needed(a[4], "parent", &parent) || !tensor(a[5], "new_tokens", &more))
+        return nullptr;
+    const at::Device device = table->device();
+    if (!on_gpu(device, "block_table") || !whole(*lens, "seq_lens", at::kInt, device, {-1}) ||
+        !whole(*table, "block_table", at::kInt, device, {lens->size(0), -1}) ||
+        !whole(*refs, "block_refs", at::kInt, device, {-1}) || !whole(*parent, "parent", at::kInt, device, {-1}))
+        return nullptr;
+    const int64_t R = lens->size(0), MB = table->size(1), N = refs->size(0), R2 = parent->size(0);
+    if (more != nullptr && !whole(*more, "new_tokens", at::kInt, device, {R2})) return nullptr;
+    BlockTensors X;
+    if (!X.take(a[0], device, N) || !workspace_arg(a[9], device, &ws)) return nullptr;
+    const c10::DeviceGuard guard(device);
+    Tensor made[3];
+    if (!int_output(a[6], "table_out", device, *table, {R2, MB}, &made[0], &out[0]) ||
+        !int_output(a[7], "lens_out", device, *table, {R2}, &made[1], &out[1]) ||
+        !int_output(a[8], "refs_out", device, *table, {N}, &made[2], &out[2]))
+        return nullptr;
+    Workspace held;
+    if (!held.take(&ws, a[1], bsa_fork_workspace_bytes(R, R2, MB, N))) return nullptr;
+    void* stream;
+    if (!stream_of(device, &stream)) return nullptr;
+    const auto ints = [](const Tensor* t) { return static_cast<const int32_t*>(data(t)); };
+    int32_t* o[3];
+    for (int i = 0; i < 3; ++i) o[i] = static_cast<int32_t*>(data_rw(out[i]));
+    void* ws_ptr = data_rw(ws);
+    const size_t ws_bytes = ws == nullptr ? 0 : (size_t)ws->nbytes();
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = bsa_fork_requests(X.t, X.n, ints(table), ints(lens), ints(refs), R, MB, N, ints(parent), ints(more), R2, o[0], o[1], o[2],
+                               ws_ptr, ws_bytes, stream);
+    Py_END_ALLOW_THREADS
+    if (!done("bsa_fork_requests", status)) return nullptr;
+    X.moved();
+    for (const Tensor* t : out) changed(t);
+    return give3(made, a + 6);
+    END_HANDLE_TH_ERRORS
+}
+
+// compact(tensors, block_table, seq_lens, block_refs, table_out, refs_out, new_ids, workspace)
+//   -> (table_out, refs_out, new_ids)
+PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const Tensor *table, *lens, *refs, *ws, *out[3];
+    if (!count(n, 8) || !needed(a[1], "block_table", &table) || !needed(a[2], "seq_lens", &lens) || !needed(a[3], "block_refs", &refs))
+        return nullptr;
+    const at::Device device = table->device();
+    if (!on_gpu(device, "block_table") || !whole(*lens, "seq_lens", at::kInt, device, {-1}) ||
+        !whole(*table, "block_table", at::kInt, device, {lens->size(0), -1}) || !whole(*refs, "block_refs", at::kInt, device, {-1}))
+        return nullptr;
+    const int64_t R = lens->size(0), MB = table->size(1), N = refs->size(0);
+    BlockTensors X;
+    if (!X.take(a[0], device, N) || !workspace_arg(a[7], device, &ws)) return nullptr;
+    const c10::DeviceGuard guard(device);
+    Tensor made[3];
+    if (!int_output(a[4], "table_out", device, *table, {R, MB}, &made[0], &out[0]) ||
+        !int_output(a[5], "refs_out", device, *table, {N}, &made[1], &out[1]) ||
+        !int_output(a[6], "new_ids", device, *table, {N}, &made[2], &out[2]))
+        return nullptr;
+    Workspace held;
+    if (!held.take(&ws, a[1], bsa_compact_workspace_bytes(N))) return nullptr;
+    void* stream;
+    if (!stream_of(device, &stream)) return nullptr;
+    const auto ints = [](const Tensor* t) { return static_cast<const int32_t*>(data(t)); };
+    int32_t* o[3];
+    for (int i = 0; i < 3; ++i) o[i] = static_cast<int32_t*>(data_rw(out[i]));
+    void* ws_ptr = data_rw(ws);
+    const size_t ws_bytes = ws == nullptr ? 0 : (size_t)ws->nbytes();
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = bsa_compact_blocks(X.t, X.n, ints(table), ints(lens), ints(refs), R, MB, N, o[0], o[1], o[2], ws_ptr, ws_bytes, stream);
+    Py_END_ALLOW_THREADS
+    if (!done("bsa_compact_blocks", status)) return nullptr;
+    X.moved();
+    for (const Tensor* t : out) changed(t);
+    return give3(made, a + 4);
+    END_HANDLE_TH_ERRORS
+}
+
 // setup(BsaError, raw_stream, workspace)
 PyObject* py_setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!count(n, 3)) return nullptr;
@@ -425,6 +670,9 @@ PyMethodDef g_methods[] = {
     {"rope", FAST(py_rope), nullptr},
     {"append", FAST(py_append), nullptr},
     {"attention_q8", FAST(py_attention_q8), nullptr},
+    {"paged_attention", FAST(py_paged_attention), nullptr},
+    {"fork", FAST(py_fork), nullptr},
+    {"compact", FAST(py_compact), nullptr},
     {"setup", FAST(py_setup), nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -411,6 +411,135 @@ int bsa_sparse_decode_attention_q8(const void* q, const void* k_cache, const voi
                                    float scale, void* out, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
+/* ---- attention of new tokens over the whole paged cache ------------------ */
+/* Arguments of bsa_paged_attention_* (HOST struct of device pointers, read
+ * during the call). */
+typedef struct bsa_paged_attention_args {
+    /* bf16 [T, H, G, D], 16-byte aligned: G query heads share each of the H
+     * KV heads; 1 <= G <= BSA_MAX_PAGED_GROUP, D a multiple of 16,
+     * 16 <= D <= BSA_MAX_CACHE_DIM; T * H * G < 2^31. */
+    const void* q;
+    int64_t T, H, G, D;
+    /* bf16 [T, H, G, D], 16-byte aligned; shares no memory with the rest
+     * (BSA_ERR_SHAPE).  Written in full: rows of no sequence, rows at a
+     * negative position and rows that see no token are zeros. */
+    void* out;
+    /* the cache, [num_pages, 16, H, D] contiguous, 16-byte aligned, of
+     * cache_dtype BSA_DTYPE_BF16, BSA_DTYPE_E4M3 or BSA_DTYPE_E5M2;
+     * num_pages < 2^27.  8 bits: float [num_pages, H] scales, finite, not
+     * negative, k = code * k_scale[page, h], v likewise (NULL for bf16). */
+    int32_t cache_dtype;
+    const void* k_cache;
+    const void* v_cache;
+    int64_t num_pages;
+    const float* k_scale;
+    const float* v_scale;
+    /* int32 [num_reqs, max_blocks]: physical 128-token blocks; max_blocks < 2^24 */
+    const int32_t* block_table;
+    int64_t num_reqs, max_blocks;
+    /* a row at position p sees the tokens j <= p of its sequence; with
+     * window > 0 only those with j > p - window or j < sinks */
+    int32_t window, sinks;
+    float scale;
+    /* at least bsa_paged_attention_workspace_bytes(...) bytes, 256-byte
+     * aligned, any contents; may be NULL when that is 0.  Calls that share a
+     * workspace must not overlap on the GPU. */
+    void* workspace;
+    size_t workspace_bytes;
+} bsa_paged_attention_args_t;
+#define BSA_MAX_PAGED_GROUP 64
+
+/* Device workspace of bsa_paged_attention_* for these sizes on the current
+ * device.  Host-only. */
+size_t bsa_paged_attention_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t D);
+
+/* Causal attention of new tokens over everything their sequences hold in the
+ * cache, the new tokens themselves among it (append them first):
+ *   out[t, h, g] = sum_j softmax_j(scale * q[t, h, g] . k_j) v_j
+ * over the tokens j that row t sees, token j of sequence i lying in block
+ * block_table[i, j / 128], page j % 128 / 16, slot j % 16.  Keys and values
+ * that no row sees may be anything, NaN included.  A token past
+ * max_blocks * 128 (BSA_STATUS_BAD_CONTEXT) or whose page lies outside
+ * [0, num_pages) (BSA_STATUS_BAD_BLOCK_ID) takes no part.
+ *
+ * Rows are owned, and placed at positions, as in bsa_append_kv_*:
+ * _decode: T = num_reqs * decode_query_len rows, row t of request
+ *   t / decode_query_len at position seq_lens[req] - decode_query_len +
+ *   t % decode_query_len (seq_lens counts the new tokens).
+ * _varlen: sequence i owns rows [cu_seqlens_q[i], cu_seqlens_q[i + 1]), the
+ *   j-th at position prefix_lens[i] + j; cu_seqlens_q does not fall.
+ * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_DTYPE, BSA_ERR_ALIGN,
+ * BSA_ERR_ROWS, BSA_ERR_WORKSPACE. */
+int bsa_paged_attention_decode(const bsa_paged_attention_args_t* args, const int32_t* seq_lens,
+                               int32_t decode_query_len, void* stream);
+int bsa_paged_attention_varlen(const bsa_paged_attention_args_t* args,
+                               const int32_t* cu_seqlens_q, const int32_t* prefix_lens,
+                               void* stream);
+
+/* ---- the cache's blocks between steps ------------------------------------- */
+/* What a block's id stands for: `data` holds num_blocks blocks of
+ * bytes_per_block bytes, one after the other (a cache's keys or values, eight
+ * pages a block; their scales; pooled index keys; of every layer).  16-byte
+ * aligned, bytes_per_block a multiple of 16. */
+typedef struct bsa_block_tensor {
+    void* data;
+    int64_t bytes_per_block;
+} bsa_block_tensor_t;
+#define BSA_MAX_BLOCK_TENSORS 512
+
+/* Device workspace of the two calls below.  Host-only. */
+size_t bsa_fork_workspace_bytes(int64_t num_reqs, int64_t num_out, int64_t max_blocks,
+                                int64_t num_blocks);
+size_t bsa_compact_workspace_bytes(int64_t num_blocks);
+
+/* The requests' next state from the old one: requests forked, reordered,
+ * grown and freed, with no synchronisation.  Request i holds the first
+ * cdiv(seq_lens[i], 128) blocks of its row of block_table, and
+ * block_refs[b] counts the rows that hold block b (rows of other tables
+ * among them); a request's last block, where it is not full, is held by that
+ * request alone.  Row r of the new state has the tokens of request
+ * parent[r] (none for -1) and room for new_tokens[r] more (NULL: 0):
+ *   - it shares its parent's full blocks;
+ *   - the parent's unfinished last block goes to the lowest r that descends
+ *     from it; each other gets a block of its own with the contents copied,
+ *     in every tensor;
+ *   - blocks for the new tokens follow.
+ * All rows read the old state.  Blocks that nobody holds any more are free,
+ * at once; fresh blocks are the lowest ids without a reference, in order of
+ * (row, block).
+ *   tensors: HOST array of num_tensors <= BSA_MAX_BLOCK_TENSORS;
+ *   block_table int32 [num_reqs, max_blocks], seq_lens int32 [num_reqs],
+ *   block_refs int32 [num_blocks]; parent, new_tokens int32 [num_out];
+ *   table_out int32 [num_out, max_blocks] (-1 past a row's blocks), lens_out
+ *   int32 [num_out], refs_out int32 [num_blocks]: each new, or in the place
+ *   of block_table, seq_lens, block_refs; sharing no other memory
+ *   (BSA_ERR_SHAPE).  rows * max_blocks < 2^31, num_blocks < 2^28.
+ *   workspace: 256-byte aligned, as for the attention.
+ * A parent outside [-1, num_reqs), a length past max_blocks * 128 (clamped) or
+ * a negative count sets BSA_STATUS_BAD_CONTEXT; a held entry outside
+ * [0, num_blocks), which is carried on, BSA_STATUS_BAD_BLOCK_ID; a block that
+ * no free one is left for, whose entry becomes -1, BSA_STATUS_NO_BLOCK.
+ * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_ALIGN, BSA_ERR_WORKSPACE. */
+int bsa_fork_requests(const bsa_block_tensor_t* tensors, int32_t num_tensors,
+                      const int32_t* block_table, const int32_t* seq_lens,
+                      const int32_t* block_refs, int64_t num_reqs, int64_t max_blocks,
+                      int64_t num_blocks, const int32_t* parent, const int32_t* new_tokens,
+                      int64_t num_out, int32_t* table_out, int32_t* lens_out, int32_t* refs_out,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* The n blocks with a reference moved to the ids 0 to n - 1: those below n
+ * stay, the others go, in order, to the free ids below n, in order, with
+ * their contents in every tensor.  new_ids int32 [num_blocks] has each
+ * block's new id (-1 for a free one), for tables other than block_table;
+ * table_out is block_table in new ids (-1 past a row's blocks), refs_out
+ * block_refs; the first two outputs may stand in the place of their inputs.
+ * The rest as for bsa_fork_requests. */
+int bsa_compact_blocks(const bsa_block_tensor_t* tensors, int32_t num_tensors,
+                       const int32_t* block_table, const int32_t* seq_lens,
+                       const int32_t* block_refs, int64_t num_reqs, int64_t max_blocks,
+                       int64_t num_blocks, int32_t* table_out, int32_t* refs_out,
+                       int32_t* new_ids, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Size of the device scratch array behind bsa_topk_select_noalloc. */
 #define BSA_NOALLOC_SCRATCH_BYTES (16u << 20)
 
@@ -476,11 +605,17 @@ int bsa_select_policy(int64_t rows, int64_t M, int32_t K, int32_t dtype, int32_t
  *                            stored).
  *   BSA_STATUS_TIMEOUT       a wait inside the 8-bit attention ran out (a defect
  *                            or a device problem, never an input's doing); the
- *                            rows not finished are NaN. */
+ *                            rows not finished are NaN; also inside the paged
+ *                            attention.
+ *   BSA_STATUS_NO_BLOCK      bsa_fork_requests found fewer free blocks than it
+ *                            needed (the entries left over are -1).
+ * bsa_paged_attention_*, bsa_fork_requests and bsa_compact_blocks say above
+ * which of the bits they set. */
 #define BSA_STATUS_BAD_BLOCK_ID 0x1u
 #define BSA_STATUS_BAD_PAGE 0x2u
 #define BSA_STATUS_BAD_CONTEXT 0x4u
 #define BSA_STATUS_TIMEOUT 0x8u
+#define BSA_STATUS_NO_BLOCK 0x10u
 #define BSA_MAX_PHYS_BLOCK 0x0FFFFFFF  /* largest block id whose page ids fit int32 */
 
 /* Registers `word`, a DEVICE pointer to one uint32 on the current device

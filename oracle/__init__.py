@@ -79,7 +79,10 @@ def _declare(lib):
     lib.oracle_sparse_decode_attention_q8.argtypes = [
         u16p, u8p, u8p, ctypes.c_int, f32p, f32p, i64, i32p, i32p, i64, i64, i64, i64, i32,
         ctypes.c_double, f64p]
-    for name in ("oracle_rope", "oracle_append", "oracle_sparse_decode_attention_q8",
+    lib.oracle_paged_attention.argtypes = [
+        u16p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, f32p, f32p, i64, i32p, i64, i32p, i32p,
+        i64, i64, i64, i64, i32, i32, ctypes.c_double, f64p]
+    for name in ("oracle_paged_attention", "oracle_rope", "oracle_append", "oracle_sparse_decode_attention_q8",
                  "oracle_num_valid_pages_decode", "oracle_num_valid_pages_varlen",
                  "oracle_topk_select", "oracle_build_sparse_block_table",
                  "oracle_topk_select_sparse_table", "oracle_index_scores",
@@ -364,6 +367,46 @@ def sparse_decode_attention_q8(q, k_codes, v_codes, kind, k_scale, v_scale, spar
     rc = _load().oracle_sparse_decode_attention_q8(
         qb.ctypes.data_as(ctypes.POINTER(ctypes.c_uint16)), kp, vp, kind, ksp, vsp, k.shape[0], btp,
         cp, T, H, G, D, bt.shape[2] // 8, float(scale),
+        out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)))
+    assert rc == 0
+    return out
+
+
+def rows_decode(seq_lens, dql):
+    """(sequence, position) of each decode row."""
+    s = np.asarray(seq_lens, dtype=np.int64)
+    req = np.repeat(np.arange(s.size), dql)
+    return req, s[req] - dql + np.tile(np.arange(dql), s.size)
+
+
+def rows_varlen(cu_seqlens_q, prefix_lens, T):
+    """(sequence, position) of each of T varlen rows, position -1 for rows of none."""
+    req, pos = np.zeros(T, dtype=np.int64), np.full(T, -1, dtype=np.int64)
+    for i, p in enumerate(np.asarray(prefix_lens)):
+        a, b = int(cu_seqlens_q[i]), int(cu_seqlens_q[i + 1])
+        req[a:b], pos[a:b] = i, p + np.arange(b - a)
+    return req, pos
+
+
+def paged_attention(q, k_cache, v_cache, kind, k_scale, v_scale, block_table, req, pos, scale,
+                    window=0, sinks=0, lib=None) -> np.ndarray:
+    """q bf16 [T, H, G, D] (torch tensor or bits); caches [num_pages, 16, H, D]: bf16 bits
+    (kind 0, scales None) or uint8 codes; returns double [T, H, G, D]."""
+    qb = _bf16_bits(q)
+    T, H, G, D = qb.shape
+    dtype = np.uint16 if kind == 0 else np.uint8
+    k, v = (np.ascontiguousarray(x, dtype=dtype) for x in (k_cache, v_cache))
+    ksp = vsp = None
+    if kind != 0:
+        ks, ksp = _as(k_scale, np.float32, ctypes.c_float)
+        vs, vsp = _as(v_scale, np.float32, ctypes.c_float)
+    t, tp = _as(block_table, np.int32, ctypes.c_int32)
+    r, rp = _as(req, np.int32, ctypes.c_int32)
+    p, pp = _as(pos, np.int32, ctypes.c_int32)
+    out = np.empty((T, H, G, D))
+    rc = _load(lib).oracle_paged_attention(
+        qb.ctypes.data_as(ctypes.POINTER(ctypes.c_uint16)), k.ctypes.data, v.ctypes.data, kind, ksp,
+        vsp, k.shape[0], tp, t.shape[1], rp, pp, T, H, G, D, window, sinks, float(scale),
         out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)))
     assert rc == 0
     return out

@@ -597,3 +597,54 @@ int oracle_sparse_decode_attention_q8(const uint16_t* q, const uint8_t* k_cache,
     free(s);
     return 0;
 }
+
+/* Causal attention over the whole paged cache: row t belongs to sequence
+ * req[t] at position pos[t] (negative: padding, zeros) and sees the tokens
+ * j <= pos[t], with window > 0 only j > pos[t] - window or j < sinks.  kind 0:
+ * bf16 bits in the caches, no scales; else 8-bit codes with a scale per page
+ * and head.  Tokens past the block table or on pages outside the cache take
+ * no part; a row without tokens is zeros. */
+int oracle_paged_attention(const uint16_t* q, const void* k_cache, const void* v_cache, int kind,
+                           const float* k_scale, const float* v_scale, int64_t num_pages,
+                           const int32_t* block_table, int64_t max_blocks, const int32_t* req,
+                           const int32_t* pos, int64_t T, int64_t H, int64_t G, int64_t D,
+                           int32_t window, int32_t sinks, double scale, double* out) {
+    double* s = (double*)malloc(sizeof(double) * (size_t)(max_blocks * ORACLE_PAGE_SIZE + 1));
+    double lut[256];
+    if (!s) return -2;
+    for (int c = 0; kind != 0 && c < 256; ++c) lut[c] = code_value((uint8_t)c, kind);
+#define ORACLE_CACHED(cache, at) \
+    (kind == 0 ? decode_bits(((const uint16_t*)(cache))[at], 8, 7).value : lut[((const uint8_t*)(cache))[at]])
+    for (int64_t t = 0; t < T; ++t)
+        for (int64_t h = 0; h < H; ++h)
+            for (int64_t g = 0; g < G; ++g) {
+                const int64_t row = (t * H + h) * G + g;
+                double mx = -INFINITY, sum = 0.0;
+                for (int64_t d = 0; d < D; ++d) out[row * D + d] = 0.0;
+                for (int pass = 0; pass < 2; ++pass) {
+                    for (int64_t j = 0; j <= pos[t] && j < max_blocks * ORACLE_PAGE_SIZE; ++j) {
+                        if (window > 0 && j <= (int64_t)pos[t] - window && j >= sinks) continue;
+                        const int64_t page = (int64_t)block_table[req[t] * max_blocks + j / ORACLE_PAGE_SIZE] * ORACLE_PAGES_PER_BLOCK +
+                                             j % ORACLE_PAGE_SIZE / ORACLE_SUB_PAGE;
+                        if (page < 0 || page >= num_pages) continue;
+                        const int64_t at = ((page * ORACLE_SUB_PAGE + j % ORACLE_SUB_PAGE) * H + h) * D;
+                        if (pass == 0) {
+                            double dot = 0.0;
+                            for (int64_t d = 0; d < D; ++d) dot += decode_bits(q[row * D + d], 8, 7).value * ORACLE_CACHED(k_cache, at + d);
+                            s[j] = dot * scale * (kind == 0 ? 1.0 : (double)k_scale[page * H + h]);
+                            if (s[j] > mx) mx = s[j];
+                        } else {
+                            const double p = exp(s[j] - mx);
+                            sum += p;
+                            for (int64_t d = 0; d < D; ++d)
+                                out[row * D + d] += p * (kind == 0 ? 1.0 : (double)v_scale[page * H + h]) * ORACLE_CACHED(v_cache, at + d);
+                        }
+                    }
+                }
+                if (mx > -INFINITY)
+                    for (int64_t d = 0; d < D; ++d) out[row * D + d] /= sum;
+            }
+#undef ORACLE_CACHED
+    free(s);
+    return 0;
+}
