@@ -3,122 +3,1257 @@
 // sinks, from a bf16 cache or an 8-bit one.
 //
 // What it computes, for query head g of KV head h in the row at position p:
-//   out = sum_j softmax_j(scale q . k_j) v_j
+//   y_j = log2(e) scale q . k_j,   out = sum_j 2^(y_j - m) v_j / sum_j 2^(y_j - m)
 // over the tokens j <= p of the row's sequence, with a window only those with
 // j > p - window or j < sinks; in 8 bits k_j and v_j are codes times the scale of
 // their page and head.
 //
-// A warp takes a row's query head and walks its tokens one at a time with a
-// running maximum and sum; each lane holds D / 32 of its dimensions.
+// Both products run on the tensor core.  The 128 rows of an MMA are the G query
+// heads of 128 / G tokens (they share the KV head's keys and values); a KV tile is
+// one 128-token block of the cache, which lies there as one TMA box.  S = Q K^T
+// goes to TMEM, the softmax turns a row a thread (one TMEM lane, so no shuffles)
+// into bf16 probabilities in the place of the scores, and O += P V takes them from
+// there as its A operand.  O stays in TMEM; it is rescaled only when a row's
+// maximum has grown by more than 2^8 since the last time.
+//  streams    two softmax groups of four warps, each with its own S and O, so that
+//             one's products run under the other's exponentials.  An item of more
+//             than 128 rows gives each its own 128 rows of the same KV tiles; a
+//             smaller one (decode steps, ends of chunks) gives each every other KV
+//             tile of the same rows, joined in shared memory.  Heads of up to 256
+//             leave TMEM for one stream, with two S buffers;
+//  copies     one warp copies queries and blocks by TMA into a ring of stages,
+//  MMAs       one thread issues them,
+//  values     two warps go over the value rows of tiles that some rows do not see
+//             in full: 0 * NaN is NaN, so what no row sees (the unused end of a block)
+//             is set to zero, and so is what is not finite, which the epilogue gives
+//             back to the rows that do see it;
+//  widening   (8 bits) four warps turn codes into bf16, exactly, into the ring, and go over
+//             the values as they do.  A key page's scale multiplies its scores, a value page's
+//             its probabilities, so any scale is as exact as a power of two.
+// The scores are rounded nowhere (fp32 from the tensor core); probabilities are
+// rounded to bf16 once, as the tensor core takes them with bf16 values; sums,
+// maxima and outputs are fp32.
+//
+// The work is cut evenly: the KV steps of all items, in order of (sequence, head,
+// rows), are one line of units that the CTAs share in equal parts, wherever in an
+// item a part begins or ends.  Lengths are known on the device alone, so each CTA
+// finds its part from the lengths at its start.  Parts of an item leave their
+// maxima, sums and outputs in the workspace in fp32, and a second launch joins
+// them in order.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <mutex>
+#include <type_traits>
+
 #include "bsa_internal.h"
 #include "bsa_overlap.h"
+#include "bsa_tcgen05.cuh"
 
 namespace bsa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kWarps = 4;
+constexpr int kRows = 128;               // rows of an MMA, tokens of a KV tile
+constexpr int kTile = kPageSize;
+constexpr int kAtom = kTile * 128;       // 128 tokens of 64 bf16 dimensions: 16 KB, swizzled by 128 bytes
+constexpr int kMaxStages = 12;
+constexpr int kInfo = 16;                // tiles whose facts are kept: more than the ring holds
+constexpr int kWindow = 512;             // sequences whose units a CTA holds at a time while it finds its part
+constexpr float kGrow = 8.f;             // log2 of what a maximum may grow by before O is rescaled
+constexpr int kJoinThreads = 256;
+constexpr int kMinUnits = 2;             // the least part of a CTA
 
 struct PagedParams {
-    bsa_paged_attention_args_t a;
+    const uint16_t* q;
+    uint16_t* out;
+    const uint8_t* v;             // the cache's values, for the epilogue of rows that see infinities
+    const float* ks;
+    const float* vs;
+    const int32_t* table;
     const int32_t* seq_lens;      // decode form
-    int32_t dql;
     const int32_t* cu;            // varlen form
     const int32_t* prefix;
+    int64_t T;
+    int64_t num_pages;
+    int32_t dql, num_reqs, max_blocks, H, G, D;
+    int32_t tokens;               // of an MMA's rows: 128 / G
+    int32_t window, sinks, cache_dtype;
+    int32_t min_units;            // the least part of a CTA
+    int32_t part_rows;            // rows of a part in the workspace
+    float scale_log2e;            // not negative; q_neg holds the sign
+    uint32_t s_idesc, o_idesc;
+    struct PartHead* heads;       // [grid]
+    float* parts;                 // [grid][2][part_rows][D]
+    float2* sums;                 // [grid][2][part_rows]: maximum, sum
     uint32_t* status;
+    unsigned long long wait_ns;   // a wait's limit
+    uint32_t stall;               // stages after which a CTA's copies stop, for tests
 };
 
-// The sequence and position of row t; false for rows of no sequence.
-__device__ __forceinline__ bool place_row(const PagedParams& P, int64_t t, int64_t* req, int64_t* pos) {
-    if (P.cu == nullptr) {
-        *req = t / P.dql;
-        *pos = (int64_t)__ldg(P.seq_lens + *req) - P.dql + t % P.dql;
-        return true;
+struct PagedMaps {
+    CUtensorMap q, k, v;
+};
+
+// The item that a CTA began and left to the next `more` CTAs to finish.
+struct PartHead {
+    int64_t row0;                 // first token row
+    int32_t tokens, h, more;
+    int32_t pad;
+};
+
+struct alignas(16) Start {
+    int64_t lo, hi, first;        // this CTA's units, and the first unit of the item that holds lo
+    int64_t U, N;
+    int32_t b, h, qt;
+};
+
+template <int D_, bool BITS8>
+struct Cfg {
+    static constexpr int D = D_;                           // dimensions, padded with zeros
+    static constexpr int NS = D <= 128 ? 2 : 1;            // streams
+    static constexpr int PD = D < 128 ? D : 128;           // dimensions of a panel, a ring stage's
+    static constexpr int PANELS = D / PD;
+    static constexpr int ATOMS = PD / 64;
+    static constexpr int STAGE = ATOMS * kAtom;
+    static constexpr int Q_TILE = D / 64 * kAtom;
+    static constexpr int CODES = BITS8 ? kTile * PD : 0;   // bytes of a stage of codes
+    static constexpr int RING = BITS8 ? 98304 / STAGE : (229376 - NS * Q_TILE) / STAGE;
+    static constexpr int CRING = BITS8 ? (229376 - NS * Q_TILE - RING * STAGE) / CODES : 0;
+    static constexpr int SOFTMAX = NS * 4;                 // warps
+    static constexpr int COPY = SOFTMAX, MMA = SOFTMAX + 1, VALUES = SOFTMAX + 2;
+    static constexpr int VALUE_WARPS = BITS8 ? 4 : 2;
+    static constexpr int WARPS = SOFTMAX + 2 + VALUE_WARPS;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr uint32_t O_COL = 256;                 // TMEM: scores in columns 0 to 255, outputs behind
+    static constexpr bool HOLD = !BITS8;                   // a row's scores stay in registers
+    static_assert(RING >= 3 && RING <= kMaxStages && CRING <= kMaxStages, "ring");
+};
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages], code_full[kMaxStages], code_empty[kMaxStages];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], to_fix, fixed, drained;
+    float scale[kInfo][2][kPagesPerBlock];     // 8 bits: key scales times scale log2 e, value scales
+    int valid[kInfo];                          // tokens of a tile inside the cache
+    int poison[4];                             // 1 + the number of the last portion with values that are not finite
+    float2 other[kRows];                       // the second stream's maximum and sum
+    long long total;
+    Start start;
+    uint32_t tmem_base;
+    int gave_up;
+};
+
+// ---- the work --------------------------------------------------------------
+
+struct Seq {
+    int64_t t0, p0;     // first row, its position
+    int n;              // rows
+};
+__device__ __forceinline__ Seq sequence(const PagedParams& A, int b) {
+    Seq s;
+    if (A.cu == nullptr) {
+        s.t0 = (int64_t)b * A.dql;
+        s.n = A.dql;
+        s.p0 = (int64_t)__ldg(A.seq_lens + b) - A.dql;
+    } else {
+        const int64_t a = __ldg(A.cu + b), e = __ldg(A.cu + b + 1);
+        s.t0 = a < 0 ? 0 : a < A.T ? a : A.T;
+        const int64_t to = e < s.t0 ? s.t0 : e < A.T ? e : A.T;
+        s.n = (int)(to - s.t0);
+        s.p0 = (int64_t)__ldg(A.prefix + b) + (s.t0 - a);
     }
-    int64_t lo = 0, hi = P.a.num_reqs;      // the last sequence that starts at or before t
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (__ldg(P.cu + mid + 1) <= t) lo = mid + 1;
-        else hi = mid;
-    }
-    if (lo >= P.a.num_reqs || __ldg(P.cu + lo) > t) return false;
-    *req = lo;
-    *pos = (int64_t)__ldg(P.prefix + lo) + t - __ldg(P.cu + lo);
-    return true;
+    return s;
 }
 
-template <int DTYPE>
-__device__ __forceinline__ float load_value(const void* p, int64_t i) {
-    if constexpr (DTYPE == BSA_DTYPE_BF16) return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16);
-    const __nv_fp8_storage_t c = __ldg(static_cast<const uint8_t*>(p) + i);
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, DTYPE == BSA_DTYPE_E4M3 ? __NV_E4M3 : __NV_E5M2)));
+// The KV tiles that rows at positions [first, last] see: sink tiles [0, st), then
+// tiles [wst, ...), nk in all; `end`: the first token that none of them sees any more.
+struct Range {
+    int nk, st, wst, end;
+    __device__ __forceinline__ int tile(int i) const { return i < st ? i : i - st + wst; }
+};
+__device__ __forceinline__ Range range(const PagedParams& A, int64_t first, int64_t last) {
+    Range r;
+    const int64_t top = (int64_t)A.max_blocks * kTile;
+    r.end = (int)(last + 1 < 0 ? 0 : last + 1 < top ? last + 1 : top);
+    const int te = (r.end + kTile - 1) / kTile;
+    r.st = r.wst = 0;
+    if (A.window > 0) {
+        const int64_t lo = (first > 0 ? first : 0) - A.window + 1;
+        const int sink_end = A.sinks < r.end ? A.sinks : r.end;
+        r.st = (sink_end + kTile - 1) / kTile;
+        const int64_t w = lo > 0 ? lo / kTile : 0;
+        r.wst = (int)(w < te ? w : te);
+        if (r.wst < r.st) r.wst = r.st;
+    }
+    r.nk = r.st + te - r.wst;
+    return r;
 }
 
-template <int DTYPE>
-__global__ void __launch_bounds__(kWarps * 32) paged_attention_kernel(const PagedParams P) {
-    constexpr int R = BSA_MAX_CACHE_DIM / 32;
-    const auto& a = P.a;
+template <class C>
+__device__ __forceinline__ int item_tokens(const PagedParams& A) {
+    return C::NS * A.tokens;
+}
+// KV steps of an item: tiles, or pairs of tiles where both streams take its rows.
+template <class C>
+__device__ __forceinline__ int item_steps(const PagedParams& A, const Seq& s, int qt, Range* out = nullptr, bool* split = nullptr) {
+    const int t = qt * item_tokens<C>(A), n = min(item_tokens<C>(A), s.n - t);
+    const Range r = range(A, s.p0 + t, s.p0 + t + n - 1);
+    const bool two = C::NS == 2 && n <= A.tokens;
+    if (out != nullptr) *out = r;
+    if (split != nullptr) *split = two;
+    return two ? (r.nk + 1) / 2 : r.nk;
+}
+template <class C>
+__device__ __forceinline__ int item_count(const PagedParams& A, const Seq& s) {
+    return (s.n + item_tokens<C>(A) - 1) / item_tokens<C>(A);
+}
+
+// The units of sequences [b0, b0 + n) (an item's are its steps and one for its
+// beginning and end), per head.
+template <class C>
+__device__ void count_units(const PagedParams& A, long long* units, int b0, int n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i0 = warp * 32; i0 < n; i0 += C::THREADS) {
+        const int i = i0 + lane;
+        Seq s{};
+        int items = 0;
+        long long u = 0;
+        if (i < n) {
+            s = sequence(A, b0 + i);
+            items = item_count<C>(A, s);
+            if (items <= 4)
+                for (int k = 0; k < items; ++k) u += item_steps<C>(A, s, k) + 1;
+        }
+        // sequences of many items: the warp together
+        for (uint32_t many = __ballot_sync(kFull, items > 4); many != 0; many &= many - 1) {
+            const int l = __ffs(many) - 1;
+            const Seq x = sequence(A, b0 + i0 + l);
+            const int m = item_count<C>(A, x);
+            long long v = 0;
+            for (int k = lane; k < m; k += 32) v += item_steps<C>(A, x, k) + 1;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+            if (lane == l) u = v;
+        }
+        if (i < n) units[i] = u;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+// Exclusive sum over the lanes.
+__device__ __forceinline__ long long warp_before(long long v) {
     const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= a.T * a.H * a.G) return;
-    const int64_t t = row / (a.H * a.G), h = row / a.G % a.H;
-    float q[R], o[R], m = -INFINITY, l = 0.f;
+    long long x = v;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int d = lane + 32 * r;
-        q[r] = d < a.D ? load_value<BSA_DTYPE_BF16>(a.q, row * a.D + d) : 0.f;
-        o[r] = 0.f;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
     }
-    int64_t req, pos;
-    if (place_row(P, t, &req, &pos) && pos >= 0) {
-        const int64_t top = a.max_blocks * kPageSize;
-        report_status(P.status, pos >= top && lane == 0, BSA_STATUS_BAD_CONTEXT);
-        const int64_t end = pos < top ? pos + 1 : top;
-        int64_t j = 0;
-        while (j < end) {
-            if (a.window > 0 && j >= a.sinks && j <= pos - a.window) {
-                j = pos - a.window + 1;
-                continue;
+    return x - v;
+}
+
+// This CTA's part of the units, and the item in which it begins.  `units`: kWindow words.
+template <class C>
+__device__ void find_start(const PagedParams& A, Shared& S, long long* units) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long all = 0;
+    for (int b0 = 0; b0 < A.num_reqs; b0 += kWindow) {
+        const int n = min(kWindow, A.num_reqs - b0);
+        count_units<C>(A, units, b0, n);
+        if (warp == 0) {
+            long long v = 0;
+            for (int i = lane; i < n; i += 32) v += units[i];
+            v = warp_sum(v);
+            if (lane == 0) S.total = v;
+        }
+        __syncthreads();
+        all += S.total;
+        __syncthreads();
+    }
+    const int64_t U = all * A.H;
+    int64_t N = U / A.min_units;
+    N = N < 1 ? 1 : N < gridDim.x ? N : gridDim.x;
+    const int64_t c = blockIdx.x;
+    const int64_t lo = c < N ? c * U / N : 0, hi = c < N ? (c + 1) * U / N : 0;
+    if (threadIdx.x == 0) {
+        S.start = Start{lo, hi, 0, U, N, 0, 0, 0};
+    }
+    __syncthreads();
+    if (lo >= hi) return;
+    long long before = 0;      // of the sequences so far, all heads
+    for (int b0 = 0; b0 < A.num_reqs; b0 += kWindow) {
+        const int n = min(kWindow, A.num_reqs - b0);
+        if (A.num_reqs > kWindow) count_units<C>(A, units, b0, n);
+        if (warp == 0) {
+            constexpr int EACH = kWindow / 32;
+            long long mine = 0;
+            for (int i = 0; i < EACH; ++i)
+                if (lane * EACH + i < n) mine += units[lane * EACH + i];
+            long long at = before + warp_before(mine) * A.H;
+            const bool here = at <= lo && lo < at + mine * A.H;
+            if (here) {
+                int i = lane * EACH;
+                while (lo >= at + units[i] * A.H) at += units[i++] * A.H;
+                S.start.b = b0 + i;
+                S.start.h = (int32_t)((lo - at) / units[i]);
+                S.start.first = at + S.start.h * units[i];      // of the head's items
             }
-            const int64_t page = (int64_t)__ldg(a.block_table + req * a.max_blocks + j / kPageSize) * kPagesPerBlock + j % kPageSize / kSubPage;
-            if (page < 0 || page >= a.num_pages) {
-                report_status(P.status, lane == 0, BSA_STATUS_BAD_BLOCK_ID);
-                ++j;
-                continue;
+            const long long sum = warp_sum(mine);
+            const bool found = __any_sync(kFull, here);
+            if (lane == 0) S.total = found ? -1 : sum;
+        }
+        __syncthreads();
+        const long long t = S.total;
+        __syncthreads();
+        if (t < 0) break;
+        before += t * A.H;
+    }
+    // the item among the head's
+    if (warp == 0) {
+        const Seq s = sequence(A, S.start.b);
+        const int items = item_count<C>(A, s);
+        long long at = S.start.first;
+        __syncwarp();
+        for (int k0 = 0; k0 < items; k0 += 32) {
+            const int k = k0 + lane;
+            const long long w = k < items ? item_steps<C>(A, s, k) + 1 : 0;
+            const long long mine = at + warp_before(w);
+            if (mine <= lo && lo < mine + w) {
+                S.start.qt = k;
+                S.start.first = mine;
             }
-            const int64_t at = ((page * kSubPage + j % kSubPage) * a.H + h) * a.D;
-            float s = 0.f;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (lane + 32 * r < a.D) s = fmaf(q[r], load_value<DTYPE>(a.k_cache, at + lane + 32 * r), s);
-#pragma unroll
-            for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(kFull, s, i);
-            float ks = 1.f, vs = 1.f;
-            if (DTYPE != BSA_DTYPE_BF16) {
-                ks = __ldg(a.k_scale + page * a.H + h);
-                vs = __ldg(a.v_scale + page * a.H + h);
-            }
-            s *= ks * a.scale * 1.44269504f;
-            const float m_new = fmaxf(m, s), base = m_new == -INFINITY ? 0.f : m_new;
-            const float keep = exp2f(m - base), p = exp2f(s - base);
-            l = fmaf(l, keep, p);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (lane + 32 * r < a.D) o[r] = fmaf(o[r], keep, p * vs * load_value<DTYPE>(a.v_cache, at + lane + 32 * r));
-            m = m_new;
-            ++j;
+            at += warp_sum(w);
+            if (at > lo) break;
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __syncthreads();
+}
+
+// What a CTA does of one item.
+struct Portion {
+    Seq s;
+    Range r;
+    int b, h, tok0, ntok;        // first token within the sequence, tokens
+    int i0, i1;                  // KV tiles of the range
+    int number;                  // of the portion
+    bool split, begins, ends;    // both streams take the same rows; the item's first and last steps are here
+    int64_t first, steps;        // units before the item, its steps
+};
+
+// The portions of a CTA in order; every warp that needs them walks them by itself.
+template <class C>
+struct Walk {
+    int b, h, qt, items, number;
+    int64_t at, lo, hi;
+    Seq s;
+    __device__ __forceinline__ Walk(const PagedParams& A, const Start& st)
+        : b(st.b), h(st.h), qt(st.qt), items(0), number(-1), at(st.first), lo(st.lo), hi(st.hi) {
+        if (lo < hi) {
+            s = sequence(A, b);
+            items = item_count<C>(A, s);
+        }
+    }
+    __device__ __forceinline__ bool next(const PagedParams& A, Portion* P) {
+        while (at < hi) {
+            const int64_t first = at;
+            const int steps = item_steps<C>(A, s, qt, &P->r, &P->split);
+            P->s = s;
+            P->b = b;
+            P->h = h;
+            P->tok0 = qt * item_tokens<C>(A);
+            P->ntok = min(item_tokens<C>(A), s.n - P->tok0);
+            at += steps + 1;
+            if (++qt == items) {
+                qt = 0;
+                if (++h == A.H) {
+                    h = 0;
+                    while (at < hi) {      // there is a sequence with items behind
+                        s = sequence(A, ++b);
+                        items = item_count<C>(A, s);
+                        if (items > 0) break;
+                    }
+                }
+            }
+            const int a = (int)(lo > first ? lo - first : 0), e = (int)(hi - first < steps ? hi - first : steps);
+            if (a >= e && !(steps == 0 && first >= lo)) continue;
+            P->begins = a == 0;
+            P->ends = e == steps;
+            P->i0 = P->split ? 2 * a : a;
+            P->i1 = P->split ? min(2 * e, P->r.nk) : e;
+            P->first = first;
+            P->steps = steps;
+            ++number;
+            P->number = number;
+            return true;
+        }
+        return false;
+    }
+};
+
+// Whether rows at positions [first, last] see all 128 tokens of the tile at `tf`.
+__device__ __forceinline__ bool sees_all(const PagedParams& A, int64_t first, int64_t last, int tf) {
+    return tf + kTile - 1 <= first && (A.window == 0 || tf > last - A.window || tf + kTile <= A.sinks);
+}
+
+// ---- small arithmetic ------------------------------------------------------
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void fma2(float& a, float& b, float x0, float x1, float y0, float y1, float z0, float z1) {
+    asm("{\n\t.reg .b64 x, y, z, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, x, y, z;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "f"(x0), "f"(x1), "f"(y0), "f"(y1), "f"(z0), "f"(z1));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x0, float x1) {
+    asm("{\n\t.reg .b64 x, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 r, {%0, %1};\n\t"
+        "add.rn.f32x2 r, r, x;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(x0), "f"(x1));
+}
+// two values as bf16, a in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ bool odd_bf16(uint32_t w) {      // either half infinite or NaN
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+// a bf16 half set to zero where it is not finite
+__device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+    return w;
+}
+// two 8-bit codes as bf16, exactly
+template <bool E4M3>
+__device__ __forceinline__ uint32_t widen(uint32_t codes) {
+    uint32_t h;
+    if constexpr (E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_bf16(f.x, f.y);
+}
+// bits [0, n) of 32
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+
+// ---- the kernel ------------------------------------------------------------
+
+// Adds what the values' warps took out to the row's outputs [d0, d0 + 32): values that
+// are not finite of tokens that the row sees.
+template <class C, bool BITS8>
+__device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion& P, int stream, int hi, int lo, int d0, float* o) {
+    const int64_t first = P.s.p0 + P.tok0, last = first + P.ntok - 1;      // as the values' warps have it
+    for (int i = P.i0; i < P.i1; ++i) {
+        if (P.split && ((i - P.i0) & 1) != stream) continue;
+        const int tf = P.r.tile(i) * kTile;
+        if (sees_all(A, first, last, tf)) continue;
+        const int64_t id = __ldg(A.table + (int64_t)P.b * A.max_blocks + P.r.tile(i));
+        for (int c = 0; c < kTile; ++c) {
+            const int j = tf + c;
+            const int64_t page = id * kPagesPerBlock + c / kSubPage;
+            if (j > hi || (A.window > 0 && j < lo && j >= A.sinks) || page < 0 || page >= A.num_pages) continue;
+            const int64_t at = ((page * kSubPage + c % kSubPage) * A.H + P.h) * A.D;
+            for (int k = 0; k < 32 && d0 + k < A.D; ++k) {
+                uint32_t w;
+                if constexpr (BITS8) {
+                    const uint32_t x = __ldg(A.v + at + d0 + k);
+                    w = A.cache_dtype == BSA_DTYPE_E4M3 ? widen<true>(x) : widen<false>(x);
+                } else {
+                    w = __ldg(reinterpret_cast<const uint16_t*>(A.v) + at + d0 + k);
+                }
+                if ((w & 0x7F80u) != 0x7F80u) continue;
+                float x = __uint_as_float(w << 16);
+                if constexpr (BITS8) x *= __ldg(A.vs + page * A.H + P.h);
+                o[k] += x;
+            }
+        }
+    }
+}
+
+template <int D_, bool BITS8>
+__global__ void __launch_bounds__(Cfg<D_, BITS8>::THREADS, 1)
+paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M) {
+    using C = Cfg<D_, BITS8>;
+    constexpr int RING = C::RING, PANELS = C::PANELS, NS = C::NS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* qsm = smem;                             // [NS] query tiles
+    uint8_t* ring = qsm + NS * C::Q_TILE;            // [RING] stages of bf16 keys and values
+    uint8_t* codes = ring + RING * C::STAGE;         // [CRING] stages of codes
+    Shared& S = *reinterpret_cast<Shared*>(codes + C::CRING * C::CODES);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == C::MMA) tmem_alloc(&S.tmem_base, 512);
+    if (tid == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&S.full[i], BITS8 ? 128 : 1);
+            mbar_init(&S.empty[i], 1);
+            mbar_init(&S.code_full[i], 1);
+            mbar_init(&S.code_empty[i], 128);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_full[i], kRows);
+            mbar_init(&S.o_full[i], 1);
+        }
+        mbar_init(&S.q_full, 1);
+        mbar_init(&S.q_empty, 2);            // the products, and the join of the streams
+        mbar_init(&S.to_fix, 1);
+        mbar_init(&S.fixed, 64);
+        mbar_init(&S.drained, 1);
+        for (int i = 0; i < 4; ++i) S.poison[i] = 0;
+        S.gave_up = 0;
+        mbar_fence_init();
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");
+    // rows of no sequence
+    if (A.cu != nullptr) {
+        const int64_t from = min(max((int64_t)__ldg(A.cu), (int64_t)0), A.T), to = min(max((int64_t)__ldg(A.cu + A.num_reqs), from), A.T);
+        const int64_t row = (int64_t)A.H * A.G * A.D / 8, gap = (from + A.T - to) * row;
+        for (int64_t i = (int64_t)blockIdx.x * C::THREADS + tid; i < gap; i += (int64_t)gridDim.x * C::THREADS)
+            reinterpret_cast<uint4*>(A.out)[i < from * row ? i : to * row + i - from * row] = make_uint4(0, 0, 0, 0);
+    }
+    find_start<C>(A, S, reinterpret_cast<long long*>(ring));      // the ring is still free
+    fence_async_smem();
+    __syncthreads();
+    const uint32_t tmem = S.tmem_base;
+    volatile int* quit = &S.gave_up;
+
+    if (warp == C::COPY) {
+        // ------------------------------------------------ copies
+        Walk<C> walk(A, S.start);
+        Portion P;
+        // the ring that TMA fills: of codes or of bf16
+        constexpr int N = BITS8 ? C::CRING : RING;
+        uint64_t* const filled = BITS8 ? S.code_full : S.full;
+        uint64_t* const drained = BITS8 ? S.code_empty : S.empty;
+        uint8_t* const base = BITS8 ? codes : ring;
+        constexpr int BYTES = BITS8 ? C::CODES : C::STAGE;
+        uint32_t st = 0, use = 0, issued = 0;
+        bool ok = true;
+        const int outside = (int)(A.num_pages * kSubPage);       // past the tensor's end: arrives as zeros
+        auto copy = [&](const CUtensorMap* map, int token, int h) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (lane + 32 * r < a.D) static_cast<__nv_bfloat16*>(a.out)[row * a.D + lane + 32 * r] = __float2bfloat16_rn(l == 0.f ? 0.f : o[r] * inv);
+            for (int p = 0; p < PANELS; ++p) {
+                ok = issued != A.stall && (use == 0 || mbar_wait(&drained[st], (use - 1) & 1, quit, A.wait_ns));
+                ok = __all_sync(kFull, ok);
+                if (ok && elect_one()) {
+                    mbar_expect(&filled[st], BYTES);
+                    if constexpr (BITS8) {
+                        tma_load_3d(base + st * BYTES, map, p * C::PD, h, token, &filled[st]);
+                    } else {
+#pragma unroll
+                        for (int a = 0; a < C::ATOMS; ++a)
+                            tma_load_3d(base + st * BYTES + a * kAtom, map, p * C::PD + a * 64, h, token, &filled[st]);
+                    }
+                }
+                __syncwarp();
+                if (!ok) return;
+                ++issued;
+                if (++st == N) {
+                    st = 0;
+                    ++use;
+                }
+            }
+        };
+        uint32_t tiles = 0, loads = 0;
+        while (ok && walk.next(A, &P)) {
+            const int64_t pos0 = P.s.p0 + P.tok0;
+            if (lane == 0 && P.begins)
+                report_status(A.status, pos0 + P.ntok > (int64_t)A.max_blocks * kTile, BSA_STATUS_BAD_CONTEXT);
+            if (P.i0 == P.i1) continue;
+            ok = loads == 0 || mbar_wait(&S.q_empty, (loads - 1) & 1, quit, A.wait_ns);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            ++loads;
+            const int mtiles = P.ntok > A.tokens ? 2 : 1;
+            if (elect_one()) {
+                mbar_expect(&S.q_full, mtiles * (C::Q_TILE / kRows) * A.tokens * A.G);
+                for (int m = 0; m < mtiles; ++m)
+                    for (int a = 0; a < C::D / 64; ++a)
+                        tma_load_4d(qsm + m * C::Q_TILE + a * kAtom, &M.q, a * 64, 0, P.h, (int)(P.s.t0 + P.tok0 + m * A.tokens), &S.q_full);
+            }
+            __syncwarp();
+            int32_t ids = 0;      // of 32 tiles
+            int before = 0;       // the last tile's token coordinate
+            float scale = 0.f;
+            const bool ahead = NS == 1 || P.split;       // keys run one tile ahead of values
+            for (int i = P.i0; ok && i <= P.i1; ++i) {
+                int at = 0;
+                if (i < P.i1) {
+                    const int k = i - P.i0;
+                    if ((k & 31) == 0) {
+                        ids = i + lane < P.i1 ? __ldg(A.table + (int64_t)P.b * A.max_blocks + P.r.tile(i + lane)) : -1;
+                    }
+                    const int id = __shfl_sync(kFull, ids, k & 31);
+                    const int64_t left = id < 0 ? 0 : (A.num_pages - (int64_t)id * kPagesPerBlock) * kSubPage;
+                    const int valid = (int)(left < 0 ? 0 : left < kTile ? left : kTile);
+                    at = valid > 0 ? id * kTile : outside;
+                    if (lane == 0) {
+                        const int t = P.r.tile(i), tf = t * kTile;
+                        int need = min(kTile, P.r.end - tf);
+                        if (A.window > 0 && t < P.r.wst) need = min(need, A.sinks - tf);
+                        report_status(A.status, valid < need, BSA_STATUS_BAD_BLOCK_ID);
+                        S.valid[(tiles + k) % kInfo] = valid;
+                    }
+                    if constexpr (BITS8) {
+                        // lanes 0 to 7: the pages' key scales, 8 to 15: their value scales
+                        if (lane < 16) {
+                            const int pg = lane & 7;
+                            const int64_t where = ((int64_t)id * kPagesPerBlock + pg) * A.H + P.h;
+                            scale = pg * kSubPage < valid ? (lane < 8 ? __ldg(A.ks + where) * A.scale_log2e : __ldg(A.vs + where)) : 0.f;
+                            S.scale[(tiles + k) % kInfo][lane >> 3][pg] = scale;
+                        }
+                    }
+                    __syncwarp();
+                    copy(&M.k, at, P.h);
+                    if (!ahead && ok) copy(&M.v, at, P.h);
+                }
+                if (ahead && i > P.i0 && ok) copy(&M.v, before, P.h);
+                before = at;
+            }
+            tiles += P.i1 - P.i0;
+        }
+        // copies in flight land before the CTA's memory goes away, also when nobody waits
+        // for them any more
+        int none = 0;
+        for (uint32_t k = issued > N ? issued - N : 0; k < issued; ++k) mbar_wait(&filled[k % N], (k / N) & 1, &none);
+        if (loads > 0) mbar_wait(&S.q_full, (loads - 1) & 1, &none);
+    } else if (warp == C::MMA) {
+        // ------------------------------------------------ MMAs
+        if (elect_one()) {
+            Walk<C> walk(A, S.start);
+            Portion P;
+            const uint64_t q_desc = smem_desc(smem_addr(qsm), 0, 1024, 2);
+            const uint64_t k_desc = smem_desc(smem_addr(ring), 0, 1024, 2);
+            const uint64_t v_desc = smem_desc(smem_addr(ring), kAtom, 1024, 2);
+            uint32_t st = 0, use = 0, p_phase = 0, fixes = 0, nq = 0, loads = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity, quit, A.wait_ns); };
+            auto step = [&](uint32_t& s, uint32_t& u) {
+                if (++s == RING) {
+                    s = 0;
+                    ++u;
+                }
+            };
+            auto take = [&](uint32_t s, uint32_t u) {
+                wait(&S.full[s], u & 1);
+                tc_fence_after();
+            };
+            // scores of query tile m and one panel of a key stage
+            auto scores = [&](int buf, int m, int p, uint32_t s) {
+                const uint64_t qd = q_desc + (m * C::Q_TILE + p * C::ATOMS * kAtom) / 16, kd = k_desc + s * (C::STAGE / 16);
+#pragma unroll
+                for (int k = 0; k < C::PD / 16; ++k) {
+                    const int at = (k / 4) * (kAtom / 16) + (k % 4) * 2;
+                    mma_f16(tmem + buf * kTile, qd + at, kd + at, A.s_idesc, p + k > 0);
+                }
+            };
+            // outputs of the probabilities in `buf` and a value stage
+            auto outputs = [&](int buf, int o, int p, uint32_t s, bool more) {
+                const uint64_t vd = v_desc + s * (C::STAGE / 16);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_f16_ts(tmem + C::O_COL + o * C::D + p * C::PD, tmem + buf * kTile + k * 8, vd + k * 128, A.o_idesc, more || k > 0);
+            };
+            auto probabilities = [&](int buf) {
+                wait(&S.p_full[buf], (p_phase >> buf) & 1);
+                p_phase ^= 1u << buf;
+                tc_fence_after();
+            };
+            while (ok && walk.next(A, &P)) {
+                const int n = P.i1 - P.i0;
+                if (n == 0) continue;
+                const int64_t first = P.s.p0 + P.tok0, last = first + P.ntok - 1;
+                wait(&S.q_full, loads & 1);
+                ++loads;
+                // bf16: tiles that some rows do not see in full pass through the values' warps,
+                // while their probabilities are formed
+                auto partly = [&](int i) { return !BITS8 && !sees_all(A, first, last, P.r.tile(i) * kTile); };
+                auto fixed = [&]() {
+                    wait(&S.fixed, fixes & 1);
+                    ++fixes;
+                };
+                if (NS == 2 && !P.split) {
+                    take(st, use);
+                    if (!ok) break;
+                    for (int s = 0; s < 2; ++s) {
+                        scores(s, s, 0, st);
+                        tc_commit(&S.s_full[s]);
+                    }
+                    tc_commit(&S.empty[st]);
+                    if (n == 1) tc_commit(&S.q_empty);
+                    step(st, use);
+                    for (int i = P.i0; ok && i < P.i1; ++i) {
+                        const bool next = i + 1 < P.i1, fix = partly(i);
+                        uint32_t ks = st, ku = use;
+                        step(ks, ku);
+                        take(st, use);
+                        if (ok && fix) mbar_arrive(&S.to_fix);
+                        for (int s = 0; s < 2; ++s) {
+                            probabilities(s);
+                            if (fix && s == 0) fixed();
+                            if (!ok) break;
+                            outputs(s, s, 0, st, i > P.i0);
+                            if (s == 1) tc_commit(&S.empty[st]);
+                            if (next) {
+                                if (s == 0) take(ks, ku);
+                                if (!ok) break;
+                                scores(s, s, 0, ks);
+                                tc_commit(&S.s_full[s]);
+                                if (s == 1) {
+                                    tc_commit(&S.empty[ks]);
+                                    if (i + 2 == P.i1) tc_commit(&S.q_empty);
+                                }
+                            } else {
+                                tc_commit(&S.o_full[s]);
+                            }
+                        }
+                        step(st, use);
+                        if (next) step(st, use);
+                    }
+                } else {
+                    // keys one tile ahead (with two streams: of each stream)
+                    auto keys = [&](int k) {
+                        const int buf = NS == 2 ? k & 1 : (nq + k) & 1;
+#pragma unroll
+                        for (int p = 0; p < PANELS; ++p) {
+                            take(st, use);
+                            if (!ok) return;
+                            scores(buf, 0, p, st);
+                            tc_commit(&S.empty[st]);
+                            step(st, use);
+                        }
+                        tc_commit(&S.s_full[buf]);
+                        if (k + 1 == n) tc_commit(&S.q_empty);
+                    };
+                    keys(0);
+                    for (int k = 0; ok && k < n; ++k) {
+                        const int buf = NS == 2 ? k & 1 : (nq + k) & 1;
+                        if (k + 1 < n && (NS == 1 || k == 0)) keys(k + 1);
+                        if (!ok) break;
+                        const bool fix = partly(P.i0 + k);
+                        uint32_t vs = st, vu = use;
+                        for (int p = 0; p < PANELS; ++p) {
+                            take(vs, vu);
+                            step(vs, vu);
+                        }
+                        if (ok && fix) mbar_arrive(&S.to_fix);
+                        probabilities(buf);
+                        if (fix) fixed();
+                        if (!ok) break;
+#pragma unroll
+                        for (int p = 0; p < PANELS; ++p) {
+                            outputs(buf, NS == 2 ? buf : 0, p, st, k >= NS);
+                            tc_commit(&S.empty[st]);
+                            step(st, use);
+                        }
+                        if (NS == 1) {
+                            tc_commit(&S.o_full[0]);
+                        } else if (k + 2 < n) {
+                            keys(k + 2);
+                        } else {
+                            tc_commit(&S.o_full[buf]);
+                        }
+                    }
+                    if (NS == 1) nq += n;
+                }
+            }
+            // no MMA runs on into the release of its memory
+            int none = 0;
+            tc_commit(&S.drained);
+            mbar_wait(&S.drained, 0, &none);
+        }
+        __syncwarp();
+    } else if (warp >= C::VALUES) {
+        // ------------------------------------------------ values, and codes to bf16
+        Walk<C> walk(A, S.start);
+        Portion P;
+        const int me = tid - C::VALUES * 32;
+        uint32_t st = 0, use = 0, cst = 0, cuse = 0, fixes = 0;
+        bool ok = true;
+        while (ok && walk.next(A, &P)) {
+            const int n = P.i1 - P.i0;
+            const int64_t first = P.s.p0 + P.tok0, last = first + P.ntok - 1;
+            const int64_t lo = A.window > 0 ? (first > 0 ? first : 0) - A.window + 1 : 0;      // the first row's first token
+            bool odd = false;
+            // whether some row of the item sees the token
+            auto seen = [&](int j) { return j < P.r.end && (j >= lo || j < A.sinks); };
+            if constexpr (!BITS8) {
+                // K and V stages in the copies' order; only V stages of partly seen tiles matter
+                const bool ahead = NS == 1 || P.split;
+                for (int i = 0; ok && i < n; ++i) {
+                    const int tf = P.r.tile(P.i0 + i) * kTile;
+                    // stages before this tile's values
+                    const int before = (ahead ? min(i + 2, n) + i : 2 * i + 1) * PANELS;
+                    if (sees_all(A, first, last, tf)) continue;
+                    const uint32_t s0 = st + before;
+                    // the MMAs' thread has them in the ring, and waits
+                    ok = mbar_wait(&S.to_fix, fixes & 1, quit, A.wait_ns);
+                    ok = __all_sync(kFull, ok);
+                    ++fixes;
+                    for (int p = 0; ok && p < PANELS; ++p) {
+                        const uint32_t s = (s0 + p) % RING, u = use + (s0 + p) / RING;
+                        ok = mbar_wait(&S.full[s], u & 1, quit, A.wait_ns);
+                        ok = __all_sync(kFull, ok);
+                        if (!ok) break;
+                        uint4* v = reinterpret_cast<uint4*>(ring + s * C::STAGE);
+#pragma unroll 8
+                        for (int k = me; k < C::STAGE / 16; k += 64) {
+                            const int row = k % (kAtom / 16) / 8;
+                            uint4 x = v[k];
+                            const bool sees = seen(tf + row);
+                            if (!sees) {
+                                v[k] = make_uint4(0, 0, 0, 0);
+                            } else if (odd_bf16(x.x) || odd_bf16(x.y) || odd_bf16(x.z) || odd_bf16(x.w)) {
+                                odd = true;
+                                v[k] = make_uint4(finite_bf16(x.x), finite_bf16(x.y), finite_bf16(x.z), finite_bf16(x.w));
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    if (odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
+                    fence_async_smem();
+                    mbar_arrive(&S.fixed);
+                }
+                const uint32_t total = st + 2 * n * PANELS;
+                use += total / RING;
+                st = total % RING;
+            } else {
+                const bool ahead = NS == 1 || P.split;
+                for (int i = 0; ok && i < 2 * n; ++i) {
+                    // the copies' order: K V K V ..., or K K V K V ... V V
+                    const bool value = ahead ? (i > 0 && (i % 2 == 0 || i == 2 * n - 1)) : (i & 1);
+                    const int tile = ahead ? (value ? (i == 2 * n - 1 ? n - 1 : i / 2 - 1) : (i + 1) / 2) : i / 2;
+                    const int tf = P.r.tile(P.i0 + tile) * kTile;
+                    const bool fix = value && !sees_all(A, first, last, tf);
+                    for (int p = 0; ok && p < PANELS; ++p) {
+                        ok = mbar_wait(&S.code_full[cst], cuse & 1, quit, A.wait_ns) &&
+                             (use == 0 || mbar_wait(&S.empty[st], (use - 1) & 1, quit, A.wait_ns));
+                        ok = __all_sync(kFull, ok);
+                        if (!ok) break;
+                        const uint4* from = reinterpret_cast<const uint4*>(codes + cst * C::CODES);
+                        uint8_t* to = ring + st * C::STAGE;
+                        constexpr int PER_ROW = C::PD / 16;
+                        auto turn = [&](auto e4m3) {
+#pragma unroll 4
+                            for (int k = me; k < kTile * PER_ROW; k += 128) {
+                                const uint4 x = from[k];
+                                const int row = k / PER_ROW, c = k % PER_ROW;
+                                uint32_t w[8];
+                                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    w[2 * e] = widen<decltype(e4m3)::value>(in[e]);
+                                    w[2 * e + 1] = widen<decltype(e4m3)::value>(in[e] >> 16);
+                                }
+                                if (fix) {
+                                    const bool sees = seen(tf + row);
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) {
+                                        odd |= sees && odd_bf16(w[e]);
+                                        w[e] = sees ? finite_bf16(w[e]) : 0u;
+                                    }
+                                }
+                                // 16 dimensions are two of a row's 16-byte words; lanes of the second
+                                // half of a row store theirs in the other order (no two on one bank)
+                                uint8_t* at = to + (c / 4) * kAtom + row * 128;
+                                const int word = (c % 4) * 2, other = c / 4 & 1;
+                                const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
+                                *reinterpret_cast<uint4*>(at + (((word + other) ^ (row & 7)) << 4)) = other ? b : a;
+                                *reinterpret_cast<uint4*>(at + (((word + 1 - other) ^ (row & 7)) << 4)) = other ? a : b;
+                            }
+                        };
+                        if (A.cache_dtype == BSA_DTYPE_E4M3) turn(std::true_type{});
+                        else turn(std::false_type{});
+                        if (fix && odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
+                        mbar_arrive(&S.code_empty[cst]);
+                        fence_async_smem();
+                        mbar_arrive(&S.full[st]);
+                        if (++cst == C::CRING) {
+                            cst = 0;
+                            ++cuse;
+                        }
+                        if (++st == RING) {
+                            st = 0;
+                            ++use;
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------ softmax and output
+        Walk<C> walk(A, S.start);
+        Portion P;
+        const int stream = warp >> 2, row = tid & 127, token = row / A.G;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t o_addr = lanes + C::O_COL + stream * C::D;
+        uint32_t s_phase = 0, o_phase = 0, tiles = 0, nq = 0;
+        bool ok = true, left_head = false;
+        while (walk.next(A, &P)) {
+            const int n = P.i1 - P.i0;
+            const int m = NS == 2 && !P.split ? stream : 0;              // its query tile
+            const int mine = min(A.tokens, P.ntok - m * A.tokens);       // tokens of it
+            const bool valid = row < A.tokens * A.G && token < mine;
+            const bool live = __any_sync(kFull, valid);
+            const int64_t first = P.s.p0 + P.tok0 + m * A.tokens, last = first + mine - 1;
+            const int64_t pos = valid ? first + token : last;            // rows beyond do as the last
+            const int64_t top = (int64_t)A.max_blocks * kTile;
+            const int hi = (int)(pos < 0 ? -1 : pos < top ? pos : top - 1);
+            const int lo = A.window > 0 ? (int)(pos - A.window + 1 < 0 ? 0 : pos - A.window + 1 < top ? pos - A.window + 1 : top) : 0;
+            float mx = -INFINITY, l0 = 0.f, l1 = 0.f;
+            bool written = false;                                        // O holds something
+            const int stride = P.split ? 2 : 1;
+            for (int k = P.split ? stream : 0; k < n; k += stride) {
+                const int buf = NS == 2 ? stream : (nq + k) & 1;
+                ok = ok && mbar_wait(&S.s_full[buf], (s_phase >> buf) & 1, quit, A.wait_ns);
+                s_phase ^= 1u << buf;
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (!P.split && tid == 0 && k == 0) mbar_arrive(&S.q_empty);
+                bool settled = NS == 2 || k == 0;      // the last values' product is done
+                // one stream: it may still run under this tile's scores
+                auto settle = [&]() {
+                    if (settled) return;
+                    ok = ok && mbar_wait(&S.o_full[0], o_phase ^ 1, quit, A.wait_ns);
+                    ok = __all_sync(kFull, ok);
+                    tc_fence_after();
+                    settled = true;
+                };
+                if (live) {
+                    const int tf = P.r.tile(P.i0 + k) * kTile, slot = (tiles + k) % kInfo;
+                    const int inside = S.valid[slot];
+                    const bool whole = inside == kTile && sees_all(A, first, last, tf);
+                    const uint32_t s_addr = lanes + buf * kTile;
+                    // the columns [32 c, 32 c + 32) that the row sees
+                    auto mask = [&](int c) {
+                        const int base = tf + 32 * c;
+                        uint32_t b = low_bits(min(hi + 1 - base, inside - 32 * c));
+                        if (A.window > 0) b &= ~low_bits(lo - base) | low_bits(A.sinks - base);
+                        return b;
+                    };
+                    float s[C::HOLD ? 4 : 1][32];
+                    float top_s = -INFINITY;
+                    // scores of columns [32 c, ...), in units of log2 with 8 bits, hidden ones -inf
+                    auto load = [&](int c, float (&x)[32]) {
+                        tmem_wait32(x);
+                        if constexpr (BITS8) {
+                            const float k0 = S.scale[slot][0][2 * c], k1 = S.scale[slot][0][2 * c + 1];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[j] *= j < 16 ? k0 : k1;
+                        }
+                        if (!whole) {
+                            const uint32_t b = mask(c);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[j] = b >> j & 1 ? x[j] : -INFINITY;
+                        }
+                    };
+                    auto most = [&](const float (&x)[32]) {
+                        float a = top_s, b = x[0];
+#pragma unroll
+                        for (int j = 1; j < 31; j += 2) (j & 2 ? a : b) = fmaxf(fmaxf(j & 2 ? a : b, x[j]), x[j + 1]);
+                        top_s = fmaxf(fmaxf(a, b), x[31]);
+                    };
+                    if constexpr (C::HOLD) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, s[c]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            load(c, s[c]);
+                            most(s[c]);
+                        }
+                        top_s *= A.scale_log2e;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_ld32(s_addr + 32 * c, s[0]);
+                            load(c, s[0]);
+                            most(s[0]);
+                        }
+                    }
+                    // a row whose maximum has grown by more than 2^kGrow takes it over
+                    const bool grow = valid && top_s > mx + kGrow;
+                    if (__any_sync(kFull, grow)) {
+                        const float keep = grow ? ex2(mx - top_s) : 1.f;
+                        if (grow) mx = top_s;
+                        l0 *= keep;
+                        l1 *= keep;
+                        if (written) {
+                            settle();
+#pragma unroll
+                            for (int c = 0; c < C::D / 32; ++c) {
+                                float o[32];
+                                tmem_ld32(o_addr + 32 * c, o);
+                                tmem_wait32(o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] *= keep;
+                                tmem_st32(o_addr + 32 * c, o);
+                            }
+                        }
+                    }
+                    const float base = mx == -INFINITY ? 0.f : -mx;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float(&x)[32] = s[C::HOLD ? c : 0];
+                        if constexpr (!C::HOLD) {
+                            tmem_ld32(s_addr + 32 * c, x);
+                            load(c, x);
+                        }
+                        uint32_t w[16];
+                        float v0 = 1.f, v1 = 1.f;
+                        if constexpr (BITS8) {
+                            v0 = S.scale[slot][1][2 * c];
+                            v1 = S.scale[slot][1][2 * c + 1];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float a, b;
+                            if constexpr (BITS8) {
+                                a = x[j] + base;
+                                b = x[j + 1] + base;
+                            } else {
+                                fma2(a, b, x[j], x[j + 1], A.scale_log2e, A.scale_log2e, base, base);
+                            }
+                            a = ex2(a);
+                            b = ex2(b);
+                            add2(l0, l1, a, b);
+                            if constexpr (BITS8) w[j / 2] = pack_bf16(a * (j < 16 ? v0 : v1), b * (j < 16 ? v0 : v1));
+                            else w[j / 2] = pack_bf16(a, b);
+                        }
+                        tmem_st16(s_addr + 16 * c, w);
+                    }
+                    tmem_wait_st();
+                    written = true;
+                }
+                settle();
+                if (NS == 1) o_phase ^= 1;      // as many products as tiles
+                tc_fence_before();
+                mbar_arrive(&S.p_full[buf]);
+            }
+            if (NS == 1) nq += n;
+            tiles += n;
+            // ---- the portion's result
+            const bool any = n > (P.split ? stream : 0);
+            if (NS == 1) {
+                if (n > 0) ok = ok && mbar_wait(&S.o_full[0], o_phase ^ 1, quit, A.wait_ns);
+            } else if (any) {
+                ok = ok && mbar_wait(&S.o_full[stream], o_phase, quit, A.wait_ns);
+                o_phase ^= 1;
+            }
+            ok = __all_sync(kFull, ok);
+            tc_fence_after();
+            float sum = l0 + l1;
+            if (!ok) mx = sum = NAN;
+            const bool odd = any && S.poison[P.number & 3] == P.number + 1;
+            // 32 of the row's outputs, not yet divided by the sum
+            auto result = [&](int c, float (&o)[32]) {
+                if (ok && any && live) {
+                    tmem_ld32(o_addr + 32 * c, o);
+                    tmem_wait32(o);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = ok ? 0.f : NAN;
+                }
+                if (odd && valid) {
+                    float x[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = 0.f;
+                    add_odd_values<C, BITS8>(A, P, stream, hi, lo, 32 * c, x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] += x[j];
+                }
+            };
+            const bool join = P.split && n > 1;      // both streams have a part of the rows
+            float f0 = 1.f, f1 = 0.f;
+            float* xch = reinterpret_cast<float*>(qsm + C::Q_TILE);      // the second query tile's place: [D / 2][128]
+            if (NS == 2 && join) {
+                if (stream == 1) S.other[row] = make_float2(mx, sum);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (stream == 0) {
+                    const float2 y = S.other[row];
+                    const float m2 = fmaxf(mx, y.x);
+                    f0 = mx == -INFINITY ? 0.f : ex2(mx - m2);
+                    f1 = y.x == -INFINITY ? 0.f : ex2(y.x - m2);
+                    sum = sum * f0 + y.y * f1;
+                    mx = m2;
+                    if (!(y.y == y.y)) sum = NAN;
+                }
+            }
+            const bool whole_item = P.begins && P.ends;
+            const float scale = whole_item ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+            const int64_t t = P.s.t0 + P.tok0 + m * A.tokens + token;
+            uint16_t* out = A.out + ((t * A.H + P.h) * A.G + row % A.G) * A.D;
+            const int64_t slot = (int64_t)blockIdx.x * 2 + (P.begins ? 1 : 0);
+            const int part_row = m * kRows + row;
+            const bool writes = valid && (stream == 0 || !P.split);
+            if (!whole_item && writes) A.sums[slot * A.part_rows + part_row] = make_float2(mx, sum);
+            float* part = A.parts + (slot * A.part_rows + part_row) * A.D;
+            if (!whole_item && P.begins && tid == 0) {
+                PartHead head;
+                head.row0 = P.s.t0 + P.tok0;
+                head.tokens = P.ntok;
+                head.h = P.h;
+                // the CTA of the item's last step: lo(c) = c U / N <= e for the c up to ((e + 1) N - 1) / U
+                head.more = (int32_t)(((P.first + P.steps) * S.start.N - 1) / S.start.U - blockIdx.x);
+                head.pad = 0;
+                A.heads[blockIdx.x] = head;
+                left_head = true;
+            }
+#pragma unroll
+            for (int half = 0; half < (NS == 2 ? 2 : 1); ++half) {
+                constexpr int CH = C::D / 32 / (NS == 2 ? 2 : 1);      // chunks of 32 a half
+                if (NS == 2 && join) {
+                    if (stream == 1) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            float o[32];
+                            result(half * CH + c, o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) xch[(c * 32 + j) * kRows + row] = o[j];
+                        }
+                    }
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                }
+                if (live && (stream == 0 || !P.split)) {
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const int d0 = (half * CH + c) * 32;
+                        float o[32];
+                        result(half * CH + c, o);
+                        if (NS == 2 && join) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + xch[(c * 32 + j) * kRows + row] * f1;
+                        }
+                        if (!writes) continue;
+                        if (whole_item) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8)
+                                if (d0 + j < A.D)
+                                    *reinterpret_cast<uint4*>(out + d0 + j) =
+                                        make_uint4(pack_bf16(o[j] * scale, o[j + 1] * scale), pack_bf16(o[j + 2] * scale, o[j + 3] * scale),
+                                                   pack_bf16(o[j + 4] * scale, o[j + 5] * scale), pack_bf16(o[j + 6] * scale, o[j + 7] * scale));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                if (d0 + j < A.D) *reinterpret_cast<float4*>(part + d0 + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
+                    }
+                }
+                if (NS == 2 && join) {
+                    fence_async_smem();      // queries of the next item come to this place by TMA
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                }
+            }
+            tc_fence_before();
+            if (P.split && tid == 0 && n > 0) mbar_arrive(&S.q_empty);
+        }
+        if (tid == 0 && !left_head) A.heads[blockIdx.x].more = 0;
+        if (tid == 0) report_status(A.status, S.gave_up != 0, BSA_STATUS_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA) tmem_free(tmem, 512);
+}
+
+// Joins the parts of items that CTAs left to one another: block x takes the item that
+// CTA x began, a slice of its rows; a thread takes 8 dimensions of a row.
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams A) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PartHead head = A.heads[blockIdx.x];
+    if (head.more <= 0) return;
+    const int words = A.D / 8, rows = head.tokens * A.G;
+    for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < rows * words; i += gridDim.y * kJoinThreads) {
+        const int r = i / words, d = i - r * words;
+        const int token = r / A.G, g = r - token * A.G, tile = token / A.tokens;
+        const int64_t part_row = tile * kRows + (token - tile * A.tokens) * A.G + g;
+        float m = -INFINITY, l = 0.f, o[8] = {};
+        for (int k = 0; k <= head.more; ++k) {
+            const int64_t at = ((int64_t)(blockIdx.x + k) * 2 + (k == 0)) * A.part_rows + part_row;
+            const float2 s = A.sums[at];
+            const float4* p = reinterpret_cast<const float4*>(A.parts + at * A.D + d * 8);
+            const float4 x = p[0], y = p[1];
+            const float m2 = fmaxf(m, s.x), base = m2 == -INFINITY ? 0.f : m2;
+            const float f0 = ex2(m - base), f1 = s.x != s.x ? NAN : ex2(s.x - base);
+            m = m2;
+            l = l * f0 + s.y * f1;
+            const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = o[j] * f0 + v[j] * f1;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t row = ((head.row0 + token) * A.H + head.h) * A.G + g;
+        *reinterpret_cast<uint4*>(A.out + row * A.D + d * 8) =
+            make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv), pack_bf16(o[4] * inv, o[5] * inv),
+                       pack_bf16(o[6] * inv, o[7] * inv));
+    }
+}
+
+// ---- host ------------------------------------------------------------------
+
+std::atomic<unsigned long long> g_paged_wait_ns{kWaitNs};
+std::atomic<uint32_t> g_paged_stall{UINT32_MAX};
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+EncodeFn encode_fn() {
+    static EncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(p);
+    });
+    return fn;
+}
+
+// The cache as a tensor of (dimension, head, token), read in boxes of a block of one
+// head: bf16 64 dimensions at a time, swizzled as the tensor core reads them; codes a
+// panel at a time, as they are.
+bool encode_cache(CUtensorMap* map, const void* base, int64_t tokens, int64_t H, int64_t D, bool bits8) {
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t size = bits8 ? 1 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {D * size, H * D * size};
+    const cuuint32_t box[3] = {(cuuint32_t)(bits8 && D > 64 ? 128 : 64), 1, (cuuint32_t)kTile};
+    const cuuint32_t unit[3] = {1, 1, 1};
+    return fn(map, bits8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+              box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, bits8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The queries as a tensor of (dimension, query head of a KV head, KV head, token), read in
+// boxes of `tokens` tokens' heads: the rows of an MMA.
+bool encode_queries(CUtensorMap* map, const void* base, int64_t T, int64_t H, int64_t G, int64_t D, int tokens) {
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)G, (cuuint64_t)H, (cuuint64_t)T};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)(G * D) * 2, (cuuint64_t)(H * G * D) * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)tokens};
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, unit,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool paged_sizes_ok(int64_t T, int64_t H, int64_t G, int64_t D) {
@@ -150,13 +1285,100 @@ int check_paged(const bsa_paged_attention_args_t& a, const Rows (&ints)[2]) {
     return BSA_OK;
 }
 
-int launch_paged(PagedParams& P, cudaStream_t st) {
-    P.status = current_status_word();
-    const unsigned grid = (unsigned)((P.a.T * P.a.H * P.a.G + kWarps - 1) / kWarps);
-    if (P.a.cache_dtype == BSA_DTYPE_BF16) paged_attention_kernel<BSA_DTYPE_BF16><<<grid, kWarps * 32, 0, st>>>(P);
-    else if (P.a.cache_dtype == BSA_DTYPE_E4M3) paged_attention_kernel<BSA_DTYPE_E4M3><<<grid, kWarps * 32, 0, st>>>(P);
-    else paged_attention_kernel<BSA_DTYPE_E5M2><<<grid, kWarps * 32, 0, st>>>(P);
-    const cudaError_t e = cudaGetLastError();
+// Rows of an item's part in the workspace.
+int part_rows(int64_t T, int64_t G, int64_t D) {
+    const int64_t tokens = kRows / G;
+    return (int)(T <= tokens ? T * G : D <= 128 ? 2 * kRows : kRows);
+}
+
+struct Parts {
+    size_t heads, sums, bytes;      // offsets, and all of it
+};
+Parts place_parts(int64_t T, int64_t G, int64_t D, int grid) {
+    const size_t rows = (size_t)grid * 2 * part_rows(T, G, D);
+    Parts p;
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    p.heads = up(rows * D * sizeof(float));
+    p.sums = p.heads + up((size_t)grid * sizeof(PartHead));
+    p.bytes = p.sums + up(rows * sizeof(float2));
+    return p;
+}
+
+template <int D, bool BITS8>
+cudaError_t launch_kernel(const PagedParams& A, const PagedMaps& M, int grid, cudaStream_t st) {
+    using C = Cfg<D, BITS8>;
+    constexpr int SMEM = C::NS * C::Q_TILE + C::RING * C::STAGE + C::CRING * C::CODES + (int)sizeof(Shared);
+    static_assert(SMEM <= 232448, "a CTA's shared memory");
+    static_assert(kWindow * 8 <= C::RING * C::STAGE, "units fit in the ring");
+    auto kern = paged_attention_kernel<D, BITS8>;
+    static FuncOnce once;
+    const cudaError_t e = once.smem(reinterpret_cast<const void*>(kern), SMEM);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, C::THREADS, SMEM, st>>>(A, M);
+    return cudaGetLastError();
+}
+
+int launch_paged(const bsa_paged_attention_args_t& a, PagedParams& A, cudaStream_t st) {
+    const int grid = device_sm_count();
+    const Parts parts = place_parts(a.T, a.G, a.D, grid);
+    if (a.workspace == nullptr || a.workspace_bytes < parts.bytes || (reinterpret_cast<uintptr_t>(a.workspace) & 255) != 0)
+        return BSA_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    const bool bits8 = a.cache_dtype != BSA_DTYPE_BF16;
+    A.q = static_cast<const uint16_t*>(a.q);
+    A.out = static_cast<uint16_t*>(a.out);
+    A.v = static_cast<const uint8_t*>(a.v_cache);
+    A.ks = a.k_scale;
+    A.vs = a.v_scale;
+    A.table = a.block_table;
+    A.T = a.T;
+    A.num_pages = a.num_pages;
+    A.num_reqs = (int32_t)a.num_reqs;
+    A.max_blocks = (int32_t)a.max_blocks;
+    A.H = (int32_t)a.H;
+    A.G = (int32_t)a.G;
+    A.D = (int32_t)a.D;
+    A.tokens = kRows / A.G;
+    A.window = a.window;
+    A.sinks = a.sinks;
+    A.cache_dtype = a.cache_dtype;
+    A.min_units = kMinUnits;
+    A.part_rows = part_rows(a.T, a.G, a.D);
+    // a scale of zero must not meet the -inf of hidden scores; any tiny one has its result
+    const float scale = fabsf(a.scale) * 1.44269504f;
+    A.scale_log2e = scale == 0.f ? 1e-30f : scale;
+    A.s_idesc = bf16_idesc(a.scale < 0.f, false, kRows, kTile);
+    A.o_idesc = bf16_idesc(false, true, kRows, a.D <= 64 ? 64 : 128);
+    A.parts = reinterpret_cast<float*>(ws);
+    A.heads = reinterpret_cast<PartHead*>(ws + parts.heads);
+    A.sums = reinterpret_cast<float2*>(ws + parts.sums);
+    A.status = current_status_word();
+    A.wait_ns = g_paged_wait_ns.load(std::memory_order_relaxed);
+    A.stall = g_paged_stall.load(std::memory_order_relaxed);
+    PagedMaps M;
+    // an empty cache: no box lies inside, any address serves
+    const int64_t tokens = (a.num_pages > 0 ? a.num_pages : 1) * kSubPage;
+    if (!encode_queries(&M.q, a.q, a.T, a.H, a.G, a.D, A.tokens) ||
+        !encode_cache(&M.k, a.num_pages > 0 ? a.k_cache : a.q, tokens, a.H, a.D, bits8) ||
+        !encode_cache(&M.v, a.num_pages > 0 ? a.v_cache : a.q, tokens, a.H, a.D, bits8))
+        return (int)cudaErrorInvalidValue;
+    cudaError_t e;
+    if (a.D <= 64) e = bits8 ? launch_kernel<64, true>(A, M, grid, st) : launch_kernel<64, false>(A, M, grid, st);
+    else if (a.D <= 128) e = bits8 ? launch_kernel<128, true>(A, M, grid, st) : launch_kernel<128, false>(A, M, grid, st);
+    else e = bits8 ? launch_kernel<256, true>(A, M, grid, st) : launch_kernel<256, false>(A, M, grid, st);
+    if (e != cudaSuccess) return (int)e;
+    cudaLaunchConfig_t cfg{};
+    const int words = A.part_rows * A.D / 8;
+    const int slices = (words + kJoinThreads - 1) / kJoinThreads;
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(slices < 8 ? slices : 8));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_join_kernel, (const PagedParams)A);
     return e == cudaSuccess ? BSA_OK : (int)e;
 }
 
@@ -165,36 +1387,46 @@ int launch_paged(PagedParams& P, cudaStream_t st) {
 
 using namespace bsa;
 
-extern "C" size_t bsa_paged_attention_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t D) { return 0; }
+// For tests, not part of the ABI: in later calls each CTA's copies stop after `stages`
+// stages (UINT32_MAX: never) and waits give up after `wait_ns` (0: the usual four seconds).
+extern "C" void bsa_paged_attention_stall(uint32_t stages, uint64_t wait_ns) {
+    g_paged_stall.store(stages, std::memory_order_relaxed);
+    g_paged_wait_ns.store(wait_ns == 0 ? kWaitNs : wait_ns, std::memory_order_relaxed);
+}
+
+extern "C" size_t bsa_paged_attention_workspace_bytes(int64_t T, int64_t H, int64_t G, int64_t D) {
+    if (!paged_sizes_ok(T, H, G, D) || T == 0) return 0;
+    return place_parts(T, G, D, device_sm_count()).bytes;
+}
 
 extern "C" int bsa_paged_attention_decode(const bsa_paged_attention_args_t* args, const int32_t* seq_lens, int32_t decode_query_len,
                                           void* stream) {
     if (args == nullptr) return BSA_ERR_NULL;
-    PagedParams P{};
-    P.a = *args;
-    const Rows ints[2] = {whole_rows(seq_lens, P.a.num_reqs * 4), whole_rows(nullptr, 0)};
-    const int rc = check_paged(P.a, ints);
+    const bsa_paged_attention_args_t& a = *args;
+    const Rows ints[2] = {whole_rows(seq_lens, a.num_reqs * 4), whole_rows(nullptr, 0)};
+    const int rc = check_paged(a, ints);
     if (rc != BSA_OK) return rc;
     if (decode_query_len < 1) return BSA_ERR_SHAPE;
-    if (P.a.T != P.a.num_reqs * decode_query_len) return BSA_ERR_ROWS;
-    if (P.a.T == 0) return BSA_OK;
+    if (a.T != a.num_reqs * decode_query_len) return BSA_ERR_ROWS;
+    if (a.T == 0) return BSA_OK;
     if (seq_lens == nullptr) return BSA_ERR_NULL;
-    P.seq_lens = seq_lens;
-    P.dql = decode_query_len;
-    return launch_paged(P, static_cast<cudaStream_t>(stream));
+    PagedParams A{};
+    A.seq_lens = seq_lens;
+    A.dql = decode_query_len;
+    return launch_paged(a, A, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int bsa_paged_attention_varlen(const bsa_paged_attention_args_t* args, const int32_t* cu_seqlens_q,
                                           const int32_t* prefix_lens, void* stream) {
     if (args == nullptr) return BSA_ERR_NULL;
-    PagedParams P{};
-    P.a = *args;
-    const Rows ints[2] = {whole_rows(cu_seqlens_q, (P.a.num_reqs + 1) * 4), whole_rows(prefix_lens, P.a.num_reqs * 4)};
-    const int rc = check_paged(P.a, ints);
+    const bsa_paged_attention_args_t& a = *args;
+    const Rows ints[2] = {whole_rows(cu_seqlens_q, (a.num_reqs + 1) * 4), whole_rows(prefix_lens, a.num_reqs * 4)};
+    const int rc = check_paged(a, ints);
     if (rc != BSA_OK) return rc;
-    if (P.a.T == 0) return BSA_OK;
-    if (cu_seqlens_q == nullptr || (P.a.num_reqs > 0 && prefix_lens == nullptr)) return BSA_ERR_NULL;
-    P.cu = cu_seqlens_q;
-    P.prefix = prefix_lens;
-    return launch_paged(P, static_cast<cudaStream_t>(stream));
+    if (a.T == 0) return BSA_OK;
+    if (cu_seqlens_q == nullptr || (a.num_reqs > 0 && prefix_lens == nullptr)) return BSA_ERR_NULL;
+    PagedParams A{};
+    A.cu = cu_seqlens_q;
+    A.prefix = prefix_lens;
+    return launch_paged(a, A, static_cast<cudaStream_t>(stream));
 }
