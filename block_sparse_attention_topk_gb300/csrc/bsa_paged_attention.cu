@@ -125,11 +125,17 @@ struct Cfg {
     static constexpr int CODES = BITS8 ? kTile * PD : 0;   // bytes of a stage of codes
     static constexpr int RING = BITS8 ? 98304 / STAGE : (229376 - NS * Q_TILE) / STAGE;
     static constexpr int CRING = BITS8 ? (229376 - NS * Q_TILE - RING * STAGE) / CODES : 0;
-    static constexpr int SOFTMAX = NS * 4;                 // warps
-    static constexpr int COPY = SOFTMAX, MMA = SOFTMAX + 1, VALUES = SOFTMAX + 2;
-    static constexpr int VALUE_WARPS = BITS8 ? 4 : 2;
-    static constexpr int WARPS = SOFTMAX + 2 + VALUE_WARPS;
+    // warps: softmax, then a group of four with the copies' and the MMAs' and with bf16 two for the
+    // values; with 8 bits the values have a group of their own
+    static constexpr int SOFTMAX = NS * 4;
+    static constexpr int COPY = SOFTMAX, MMA = SOFTMAX + 1, VALUES = SOFTMAX + (BITS8 ? 4 : 2);
+    static constexpr int WARPS = SOFTMAX + (BITS8 ? 8 : 4);
     static constexpr int THREADS = WARPS * 32;
+    // registers of a softmax thread and of the others, out of what the launch gives all
+    static constexpr int GIVEN = 65536 / THREADS / 8 * 8 < 255 ? 65536 / THREADS / 8 * 8 : 248;
+    static constexpr int OTHERS = BITS8 ? 80 : 72;
+    static constexpr int MORE = (GIVEN * THREADS - OTHERS * (THREADS - SOFTMAX * 32)) / (SOFTMAX * 32) / 8 * 8;
+    static constexpr int MINE = MORE < 255 ? MORE : 248;
     static constexpr uint32_t O_COL = 256;                 // TMEM: scores in columns 0 to 255, outputs behind
     static constexpr bool HOLD = !BITS8;                   // a row's scores stay in registers
     static_assert(RING >= 3 && RING <= kMaxStages && CRING <= kMaxStages, "ring");
@@ -405,6 +411,13 @@ __device__ __forceinline__ bool sees_all(const PagedParams& A, int64_t first, in
     return tf + kTile - 1 <= first && (A.window == 0 || tf > last - A.window || tf + kTile <= A.sinks);
 }
 
+// The registers of a role's threads; a group of four warps asks as one.
+template <int N, bool MORE>
+__device__ __forceinline__ void take_registers() {
+    if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---- small arithmetic ------------------------------------------------------
 
 __device__ __forceinline__ float ex2(float x) {
@@ -537,6 +550,7 @@ paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M)
     volatile int* quit = &S.gave_up;
 
     if (warp == C::COPY) {
+        take_registers<C::OTHERS, false>();
         // ------------------------------------------------ copies
         Walk<C> walk(A, S.start);
         Portion P;
@@ -637,6 +651,7 @@ paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M)
         for (uint32_t k = issued > N ? issued - N : 0; k < issued; ++k) mbar_wait(&filled[k % N], (k / N) & 1, &none);
         if (loads > 0) mbar_wait(&S.q_full, (loads - 1) & 1, &none);
     } else if (warp == C::MMA) {
+        take_registers<C::OTHERS, false>();
         // ------------------------------------------------ MMAs
         if (elect_one()) {
             Walk<C> walk(A, S.start);
@@ -783,6 +798,7 @@ paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M)
         }
         __syncwarp();
     } else if (warp >= C::VALUES) {
+        take_registers<C::OTHERS, false>();
         // ------------------------------------------------ values, and codes to bf16
         Walk<C> walk(A, S.start);
         Portion P;
@@ -899,7 +915,10 @@ paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M)
                 }
             }
         }
+    } else if (warp >= C::SOFTMAX) {
+        take_registers<C::OTHERS, false>();      // warps without work, of a group of four
     } else {
+        take_registers<C::MINE, true>();
         // ------------------------------------------------ softmax and output
         Walk<C> walk(A, S.start);
         Portion P;
