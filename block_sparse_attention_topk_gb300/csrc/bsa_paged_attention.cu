@@ -130,14 +130,13 @@ struct Cfg {
     static constexpr int SOFTMAX = NS * 4;
     static constexpr int COPY = SOFTMAX, MMA = SOFTMAX + 1, VALUES = SOFTMAX + (BITS8 ? 4 : 2);
     static constexpr int WARPS = SOFTMAX + (BITS8 ? 8 : 4);
-    static constexpr int THREADS = WARPS * 32;
+    static constexpr int THREADS = WARPS * 32, VALUE_THREADS = BITS8 ? 128 : 64;
     // registers of a softmax thread and of the others, out of what the launch gives all
     static constexpr int GIVEN = 65536 / THREADS / 8 * 8 < 255 ? 65536 / THREADS / 8 * 8 : 248;
     static constexpr int OTHERS = BITS8 ? 80 : 72;
     static constexpr int MORE = (GIVEN * THREADS - OTHERS * (THREADS - SOFTMAX * 32)) / (SOFTMAX * 32) / 8 * 8;
     static constexpr int MINE = MORE < 255 ? MORE : 248;
     static constexpr uint32_t O_COL = 256;                 // TMEM: scores in columns 0 to 255, outputs behind
-    static constexpr bool HOLD = !BITS8;                   // a row's scores stay in registers
     static_assert(RING >= 3 && RING <= kMaxStages && CRING <= kMaxStages, "ring");
 };
 
@@ -437,6 +436,12 @@ __device__ __forceinline__ void add2(float& a, float& b, float x0, float x1) {
         : "+f"(a), "+f"(b)
         : "f"(x0), "f"(x1));
 }
+__device__ __forceinline__ void mul2(float& a, float& b, float y) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(y));
+}
 // two values as bf16, a in the low half
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     uint32_t r;
@@ -452,14 +457,31 @@ __device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
     if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
     return w;
 }
-// two 8-bit codes as bf16, exactly
-template <bool E4M3>
-__device__ __forceinline__ uint32_t widen(uint32_t codes) {
+// An 8-bit code as bf16, exactly, its NaN and infinities among them.
+__device__ __forceinline__ uint32_t widen_one(uint32_t code, bool e4m3) {
     uint32_t h;
-    if constexpr (E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return pack_bf16(f.x, f.y);
+    if (e4m3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
+    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
+    return __float_as_uint(__low2float(*reinterpret_cast<const __half2*>(&h))) >> 16;
+}
+// Four finite codes as bf16: the bits after the sign, moved so that the exponents' low ends
+// meet, are the value times 2^-120 (e4m3) or 2^-112 (e5m2), subnormals too.  The
+// conversion instructions, by way of half and single, share a slow pipe with the exponentials.
+template <bool E4M3>
+__device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    const uint32_t a = __byte_perm(codes, 0, 0x1404), b = __byte_perm(codes, 0, 0x3424);      // codes in the upper bytes
+    constexpr int DOWN = E4M3 ? 4 : 3;
+    constexpr uint32_t BITS = E4M3 ? 0x07F007F0u : 0x0FE00FE0u;
+    lo = (a & 0x80008000u) | ((a >> DOWN) & BITS);
+    hi = (b & 0x80008000u) | ((b >> DOWN) & BITS);
+    constexpr uint32_t UP = E4M3 ? 0x7B807B80u : 0x77807780u;
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(UP));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(UP));
+}
+// Nonzero where a code of four is not finite.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t odd_codes(uint32_t codes) {
+    return ((codes & 0x7F7F7F7Fu) + (E4M3 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
 }
 // bits [0, n) of 32
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
@@ -469,7 +491,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 
 // Adds what the values' warps took out to the row's outputs [d0, d0 + 32): values that
 // are not finite of tokens that the row sees.
 template <class C, bool BITS8>
-__device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion& P, int stream, int hi, int lo, int d0, float* o) {
+__device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion P, int stream, int hi, int lo, int d0, float* o) {
     const int64_t first = P.s.p0 + P.tok0, last = first + P.ntok - 1;      // as the values' warps have it
     for (int i = P.i0; i < P.i1; ++i) {
         if (P.split && ((i - P.i0) & 1) != stream) continue;
@@ -485,7 +507,7 @@ __device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion&
                 uint32_t w;
                 if constexpr (BITS8) {
                     const uint32_t x = __ldg(A.v + at + d0 + k);
-                    w = A.cache_dtype == BSA_DTYPE_E4M3 ? widen<true>(x) : widen<false>(x);
+                    w = widen_one(x, A.cache_dtype == BSA_DTYPE_E4M3);
                 } else {
                     w = __ldg(reinterpret_cast<const uint16_t*>(A.v) + at + d0 + k);
                 }
@@ -498,9 +520,73 @@ __device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion&
     }
 }
 
+// Where 16 dimensions of a row, a word of codes, go in a stage of bf16: two 16-byte words,
+// swizzled.
+template <class C>
+__device__ __forceinline__ uint8_t* place(uint8_t* to, int k, int half) {
+    constexpr int PER_ROW = C::PD / 16;
+    const int row = k / PER_ROW, c = k % PER_ROW;
+    return to + (c / 4) * kAtom + row * 128 + ((((c % 4) * 2 + half) ^ (row & 7)) << 4);
+}
+
+// A stage of codes widened by 128 threads; whether this thread met codes that are not finite.
+template <class C, bool E4M3>
+__device__ __forceinline__ bool widen_stage(const uint4* from, uint8_t* to, int me) {
+    constexpr int EACH = C::CODES / 16 / 128, BATCH = 4;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; i += BATCH) {
+        uint4 x[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) x[j] = from[me + (i + j) * 128];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int k = me + (i + j) * 128;
+            uint32_t w[8];
+            widen<E4M3>(x[j].x, w[0], w[1]);
+            widen<E4M3>(x[j].y, w[2], w[3]);
+            widen<E4M3>(x[j].z, w[4], w[5]);
+            widen<E4M3>(x[j].w, w[6], w[7]);
+            bad |= odd_codes<E4M3>(x[j].x) | odd_codes<E4M3>(x[j].y) | odd_codes<E4M3>(x[j].z) | odd_codes<E4M3>(x[j].w);
+            // lanes of the second half of a row store in the other order: no two on one bank
+            const int other = k % (C::PD / 16) / 4 & 1;
+            const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
+            *reinterpret_cast<uint4*>(place<C>(to, k, other)) = other ? b : a;
+            *reinterpret_cast<uint4*>(place<C>(to, k, 1 - other)) = other ? a : b;
+        }
+    }
+    return bad != 0;
+}
+// The same by the conversion instructions, NaN and infinities among the codes.
+template <class C>
+__device__ __noinline__ void widen_odd(const uint4* from, uint8_t* to, int me, bool e4m3) {
+    for (int k = me; k < C::CODES / 16; k += 128)
+        for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<uint16_t*>(place<C>(to, k, e / 8) + e % 8 * 2) =
+                (uint16_t)widen_one(reinterpret_cast<const uint8_t*>(from + k)[e], e4m3);
+}
+// Value rows that no row sees set to zero, and what is not finite in the others; whether there was
+// such.
+template <class C, class Seen>
+__device__ __forceinline__ bool clean_stage(uint8_t* stage, int me, Seen seen) {
+    bool odd = false;
+    uint4* v = reinterpret_cast<uint4*>(stage);
+#pragma unroll 4
+    for (int k = me; k < C::STAGE / 16; k += C::VALUE_THREADS) {
+        const uint4 x = v[k];
+        if (!seen(k % (kAtom / 16) / 8)) {
+            v[k] = make_uint4(0, 0, 0, 0);
+        } else if (odd_bf16(x.x) || odd_bf16(x.y) || odd_bf16(x.z) || odd_bf16(x.w)) {
+            odd = true;
+            v[k] = make_uint4(finite_bf16(x.x), finite_bf16(x.y), finite_bf16(x.z), finite_bf16(x.w));
+        }
+    }
+    return odd;
+}
+
 template <int D_, bool BITS8>
 __global__ void __launch_bounds__(Cfg<D_, BITS8>::THREADS, 1)
-paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M) {
+paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_constant__ PagedMaps M) {
     using C = Cfg<D_, BITS8>;
     constexpr int RING = C::RING, PANELS = C::PANELS, NS = C::NS;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -830,19 +916,7 @@ paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M)
                         ok = mbar_wait(&S.full[s], u & 1, quit, A.wait_ns);
                         ok = __all_sync(kFull, ok);
                         if (!ok) break;
-                        uint4* v = reinterpret_cast<uint4*>(ring + s * C::STAGE);
-#pragma unroll 8
-                        for (int k = me; k < C::STAGE / 16; k += 64) {
-                            const int row = k % (kAtom / 16) / 8;
-                            uint4 x = v[k];
-                            const bool sees = seen(tf + row);
-                            if (!sees) {
-                                v[k] = make_uint4(0, 0, 0, 0);
-                            } else if (odd_bf16(x.x) || odd_bf16(x.y) || odd_bf16(x.z) || odd_bf16(x.w)) {
-                                odd = true;
-                                v[k] = make_uint4(finite_bf16(x.x), finite_bf16(x.y), finite_bf16(x.z), finite_bf16(x.w));
-                            }
-                        }
+                        odd |= clean_stage<C>(ring + s * C::STAGE, me, [&](int row) { return seen(tf + row); });
                     }
                     if (!ok) break;
                     if (odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
@@ -867,38 +941,11 @@ paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M)
                         if (!ok) break;
                         const uint4* from = reinterpret_cast<const uint4*>(codes + cst * C::CODES);
                         uint8_t* to = ring + st * C::STAGE;
-                        constexpr int PER_ROW = C::PD / 16;
-                        auto turn = [&](auto e4m3) {
-#pragma unroll 4
-                            for (int k = me; k < kTile * PER_ROW; k += 128) {
-                                const uint4 x = from[k];
-                                const int row = k / PER_ROW, c = k % PER_ROW;
-                                uint32_t w[8];
-                                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    w[2 * e] = widen<decltype(e4m3)::value>(in[e]);
-                                    w[2 * e + 1] = widen<decltype(e4m3)::value>(in[e] >> 16);
-                                }
-                                if (fix) {
-                                    const bool sees = seen(tf + row);
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        odd |= sees && odd_bf16(w[e]);
-                                        w[e] = sees ? finite_bf16(w[e]) : 0u;
-                                    }
-                                }
-                                // 16 dimensions are two of a row's 16-byte words; lanes of the second
-                                // half of a row store theirs in the other order (no two on one bank)
-                                uint8_t* at = to + (c / 4) * kAtom + row * 128;
-                                const int word = (c % 4) * 2, other = c / 4 & 1;
-                                const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
-                                *reinterpret_cast<uint4*>(at + (((word + other) ^ (row & 7)) << 4)) = other ? b : a;
-                                *reinterpret_cast<uint4*>(at + (((word + 1 - other) ^ (row & 7)) << 4)) = other ? a : b;
-                            }
-                        };
-                        if (A.cache_dtype == BSA_DTYPE_E4M3) turn(std::true_type{});
-                        else turn(std::false_type{});
+                        const bool e4m3 = A.cache_dtype == BSA_DTYPE_E4M3;
+                        const bool bad = e4m3 ? widen_stage<C, true>(from, to, me) : widen_stage<C, false>(from, to, me);
+                        if (bad) widen_odd<C>(from, to, me, e4m3);
+                        if (fix) asm volatile("bar.sync 2, 128;" ::: "memory");
+                        if (fix) odd |= clean_stage<C>(to, me, [&](int row) { return seen(tf + row); });
                         if (fix && odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
                         mbar_arrive(&S.code_empty[cst]);
                         fence_async_smem();
@@ -938,7 +985,7 @@ paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M)
             const int64_t top = (int64_t)A.max_blocks * kTile;
             const int hi = (int)(pos < 0 ? -1 : pos < top ? pos : top - 1);
             const int lo = A.window > 0 ? (int)(pos - A.window + 1 < 0 ? 0 : pos - A.window + 1 < top ? pos - A.window + 1 : top) : 0;
-            float mx = -INFINITY, l0 = 0.f, l1 = 0.f;
+            float mx = -INFINITY, l[4] = {};
             bool written = false;                                        // O holds something
             const int stride = P.split ? 2 : 1;
             for (int k = P.split ? stream : 0; k < n; k += stride) {
@@ -963,100 +1010,91 @@ paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M)
                     const int inside = S.valid[slot];
                     const bool whole = inside == kTile && sees_all(A, first, last, tf);
                     const uint32_t s_addr = lanes + buf * kTile;
-                    // the columns [32 c, 32 c + 32) that the row sees
-                    auto mask = [&](int c) {
-                        const int base = tf + 32 * c;
-                        uint32_t b = low_bits(min(hi + 1 - base, inside - 32 * c));
-                        if (A.window > 0) b &= ~low_bits(lo - base) | low_bits(A.sinks - base);
-                        return b;
-                    };
-                    float s[C::HOLD ? 4 : 1][32];
-                    float top_s = -INFINITY;
-                    // scores of columns [32 c, ...), in units of log2 with 8 bits, hidden ones -inf
-                    auto load = [&](int c, float (&x)[32]) {
-                        tmem_wait32(x);
+                    float x[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, x[c]);
+                    // what a score is multiplied by: 8 bits, each page its own
+                    float ks[BITS8 ? kPagesPerBlock : 1];
+                    if constexpr (BITS8) {
+#pragma unroll
+                        for (int p = 0; p < kPagesPerBlock; ++p) ks[p] = S.scale[slot][0][p];
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_wait32(x[c]);
+                    if (!whole) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            // the columns [32 c, 32 c + 32) that the row sees
+                            const int from = tf + 32 * c;
+                            uint32_t seen = low_bits(min(hi + 1 - from, inside - 32 * c));
+                            if (A.window > 0) seen &= ~low_bits(lo - from) | low_bits(A.sinks - from);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                // a scale of zero must not meet -inf
+                                if constexpr (BITS8) x[c][j] *= ks[2 * c + j / 16];
+                                x[c][j] = seen >> j & 1 ? x[c][j] : -INFINITY;
+                            }
+                        }
                         if constexpr (BITS8) {
-                            const float k0 = S.scale[slot][0][2 * c], k1 = S.scale[slot][0][2 * c + 1];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] *= j < 16 ? k0 : k1;
-                        }
-                        if (!whole) {
-                            const uint32_t b = mask(c);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] = b >> j & 1 ? x[j] : -INFINITY;
-                        }
-                    };
-                    auto most = [&](const float (&x)[32]) {
-                        float a = top_s, b = x[0];
-#pragma unroll
-                        for (int j = 1; j < 31; j += 2) (j & 2 ? a : b) = fmaxf(fmaxf(j & 2 ? a : b, x[j]), x[j + 1]);
-                        top_s = fmaxf(fmaxf(a, b), x[31]);
-                    };
-                    if constexpr (C::HOLD) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, s[c]);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            load(c, s[c]);
-                            most(s[c]);
-                        }
-                        top_s *= A.scale_log2e;
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            tmem_ld32(s_addr + 32 * c, s[0]);
-                            load(c, s[0]);
-                            most(s[0]);
+                            for (int p = 0; p < kPagesPerBlock; ++p) ks[p] = 1.f;
                         }
                     }
+                    // maxima of 16 columns each, side by side
+                    float most[8];
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) most[p] = x[p / 2][p % 2 * 16];
+#pragma unroll
+                    for (int j = 1; j < 15; j += 2)
+#pragma unroll
+                        for (int p = 0; p < 8; ++p)
+                            most[p] = fmaxf(fmaxf(most[p], x[p / 2][p % 2 * 16 + j]), x[p / 2][p % 2 * 16 + j + 1]);
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        most[p] = fmaxf(most[p], x[p / 2][p % 2 * 16 + 15]);
+                        if constexpr (BITS8) most[p] *= ks[p];
+                    }
+                    float top_s = fmaxf(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])), fmaxf(fmaxf(most[4], most[5]), fmaxf(most[6], most[7])));
+                    if constexpr (!BITS8) top_s *= A.scale_log2e;
                     // a row whose maximum has grown by more than 2^kGrow takes it over
                     const bool grow = valid && top_s > mx + kGrow;
                     if (__any_sync(kFull, grow)) {
                         const float keep = grow ? ex2(mx - top_s) : 1.f;
                         if (grow) mx = top_s;
-                        l0 *= keep;
-                        l1 *= keep;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) l[i] *= keep;
                         if (written) {
                             settle();
+#pragma unroll 1
+                            for (int c = 0; c < C::D / 16; ++c) {
+                                float o[16];
+                                tmem_ld16(o_addr + 16 * c, o);
+                                uint32_t w[16];
 #pragma unroll
-                            for (int c = 0; c < C::D / 32; ++c) {
-                                float o[32];
-                                tmem_ld32(o_addr + 32 * c, o);
-                                tmem_wait32(o);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] *= keep;
-                                tmem_st32(o_addr + 32 * c, o);
+                                for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * keep);
+                                tmem_st16(o_addr + 16 * c, w);
                             }
                         }
                     }
                     const float base = mx == -INFINITY ? 0.f : -mx;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        float(&x)[32] = s[C::HOLD ? c : 0];
-                        if constexpr (!C::HOLD) {
-                            tmem_ld32(s_addr + 32 * c, x);
-                            load(c, x);
-                        }
                         uint32_t w[16];
-                        float v0 = 1.f, v1 = 1.f;
+                        float vs[2];
                         if constexpr (BITS8) {
-                            v0 = S.scale[slot][1][2 * c];
-                            v1 = S.scale[slot][1][2 * c + 1];
+                            vs[0] = S.scale[slot][1][2 * c];
+                            vs[1] = S.scale[slot][1][2 * c + 1];
                         }
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
+                            const float k = BITS8 ? ks[2 * c + j / 16] : A.scale_log2e;
                             float a, b;
-                            if constexpr (BITS8) {
-                                a = x[j] + base;
-                                b = x[j + 1] + base;
-                            } else {
-                                fma2(a, b, x[j], x[j + 1], A.scale_log2e, A.scale_log2e, base, base);
-                            }
+                            fma2(a, b, x[c][j], x[c][j + 1], k, k, base, base);
                             a = ex2(a);
                             b = ex2(b);
-                            add2(l0, l1, a, b);
-                            if constexpr (BITS8) w[j / 2] = pack_bf16(a * (j < 16 ? v0 : v1), b * (j < 16 ? v0 : v1));
-                            else w[j / 2] = pack_bf16(a, b);
+                            add2(l[c % 2 * 2], l[c % 2 * 2 + 1], a, b);
+                            if constexpr (BITS8) mul2(a, b, vs[j / 16]);
+                            w[j / 2] = pack_bf16(a, b);
                         }
                         tmem_st16(s_addr + 16 * c, w);
                     }
@@ -1080,7 +1118,7 @@ paged_attention_kernel(const PagedParams A, const __grid_constant__ PagedMaps M)
             }
             ok = __all_sync(kFull, ok);
             tc_fence_after();
-            float sum = l0 + l1;
+            float sum = (l[0] + l[1]) + (l[2] + l[3]);
             if (!ok) mx = sum = NAN;
             const bool odd = any && S.poison[P.number & 3] == P.number + 1;
             // 32 of the row's outputs, not yet divided by the sum
