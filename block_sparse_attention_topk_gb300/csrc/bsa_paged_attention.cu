@@ -63,7 +63,7 @@ constexpr int kRows = 128;               // rows of an MMA, tokens of a KV tile
 constexpr int kTile = kPageSize;
 constexpr int kAtom = kTile * 128;       // 128 tokens of 64 bf16 dimensions: 16 KB, swizzled by 128 bytes
 constexpr int kMaxStages = 12;
-constexpr int kInfo = 16;                // tiles whose facts are kept: more than the ring holds
+constexpr int kInfo = 16;                // tiles whose facts are kept: more than the rings hold, and one
 constexpr int kWindow = 512;             // sequences whose units a CTA holds at a time while it finds its part
 constexpr float kGrow = 8.f;             // log2 of what a maximum may grow by before O is rescaled
 constexpr int kJoinThreads = 256;
@@ -126,14 +126,14 @@ struct Cfg {
     static constexpr int RING = BITS8 ? 98304 / STAGE : (229376 - NS * Q_TILE) / STAGE;
     static constexpr int CRING = BITS8 ? (229376 - NS * Q_TILE - RING * STAGE) / CODES : 0;
     // warps: softmax, then a group of four with the copies' and the MMAs' and with bf16 two for the
-    // values; with 8 bits the values have a group of their own
+    // values; with 8 bits the values have two groups of their own
     static constexpr int SOFTMAX = NS * 4;
     static constexpr int COPY = SOFTMAX, MMA = SOFTMAX + 1, VALUES = SOFTMAX + (BITS8 ? 4 : 2);
-    static constexpr int WARPS = SOFTMAX + (BITS8 ? 8 : 4);
+    static constexpr int WARPS = SOFTMAX + (BITS8 ? 12 : 4);
     static constexpr int THREADS = WARPS * 32, VALUE_THREADS = BITS8 ? 128 : 64;
     // registers of a softmax thread and of the others, out of what the launch gives all
     static constexpr int GIVEN = 65536 / THREADS / 8 * 8 < 255 ? 65536 / THREADS / 8 * 8 : 248;
-    static constexpr int OTHERS = BITS8 ? 80 : 72;
+    static constexpr int OTHERS = BITS8 ? 64 : 72;
     static constexpr int MORE = (GIVEN * THREADS - OTHERS * (THREADS - SOFTMAX * 32)) / (SOFTMAX * 32) / 8 * 8;
     static constexpr int MINE = MORE < 255 ? MORE : 248;
     static constexpr uint32_t O_COL = 256;                 // TMEM: scores in columns 0 to 255, outputs behind
@@ -532,9 +532,9 @@ __device__ __forceinline__ uint8_t* place(uint8_t* to, int k, int half) {
 // A stage of codes widened by 128 threads; whether this thread met codes that are not finite.
 template <class C, bool E4M3>
 __device__ __forceinline__ bool widen_stage(const uint4* from, uint8_t* to, int me) {
-    constexpr int EACH = C::CODES / 16 / 128, BATCH = 4;
+    constexpr int EACH = C::CODES / 16 / 128, BATCH = 2;
     uint32_t bad = 0;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < EACH; i += BATCH) {
         uint4 x[BATCH];
 #pragma unroll
@@ -693,14 +693,26 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             __syncwarp();
             int32_t ids = 0;      // of 32 tiles
             int before = 0;       // the last tile's token coordinate
-            float scale = 0.f;
+            const int n = P.i1 - P.i0;
             const bool ahead = NS == 1 || P.split;       // keys run one tile ahead of values
+            // 8 bits: scales of two tiles, lanes 0 to 15 and 16 to 31, the pages' for keys, then for
+            // values; read two tiles ahead, as they may come from DRAM
+            float scale = 0.f;
+            auto read_scales = [&](int k) {
+                const int t = k + (lane >> 4), pg = lane & 7;
+                const int id = __shfl_sync(kFull, ids, t & 31);
+                scale = 0.f;
+                if (t >= n || id < 0 || (int64_t)id * kPagesPerBlock + pg >= A.num_pages) return;
+                const int64_t where = ((int64_t)id * kPagesPerBlock + pg) * A.H + P.h;
+                scale = lane & 8 ? __ldg(A.vs + where) : __ldg(A.ks + where) * A.scale_log2e;
+            };
             for (int i = P.i0; ok && i <= P.i1; ++i) {
                 int at = 0;
                 if (i < P.i1) {
                     const int k = i - P.i0;
                     if ((k & 31) == 0) {
                         ids = i + lane < P.i1 ? __ldg(A.table + (int64_t)P.b * A.max_blocks + P.r.tile(i + lane)) : -1;
+                        if constexpr (BITS8) read_scales(k);
                     }
                     const int id = __shfl_sync(kFull, ids, k & 31);
                     const int64_t left = id < 0 ? 0 : (A.num_pages - (int64_t)id * kPagesPerBlock) * kSubPage;
@@ -714,12 +726,9 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         S.valid[(tiles + k) % kInfo] = valid;
                     }
                     if constexpr (BITS8) {
-                        // lanes 0 to 7: the pages' key scales, 8 to 15: their value scales
-                        if (lane < 16) {
-                            const int pg = lane & 7;
-                            const int64_t where = ((int64_t)id * kPagesPerBlock + pg) * A.H + P.h;
-                            scale = pg * kSubPage < valid ? (lane < 8 ? __ldg(A.ks + where) * A.scale_log2e : __ldg(A.vs + where)) : 0.f;
-                            S.scale[(tiles + k) % kInfo][lane >> 3][pg] = scale;
+                        if ((k & 1) == 0) {
+                            if (k + (lane >> 4) < n) S.scale[(tiles + k + (lane >> 4)) % kInfo][lane >> 3 & 1][lane & 7] = scale;
+                            if (((k + 2) & 31) != 0) read_scales(k + 2);
                         }
                     }
                     __syncwarp();
@@ -888,8 +897,8 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         // ------------------------------------------------ values, and codes to bf16
         Walk<C> walk(A, S.start);
         Portion P;
-        const int me = tid - C::VALUES * 32;
-        uint32_t st = 0, use = 0, cst = 0, cuse = 0, fixes = 0;
+        const int me = (tid - C::VALUES * 32) % C::VALUE_THREADS, group = (warp - C::VALUES) / 4;
+        uint32_t st = 0, use = 0, cst = 0, cuse = 0, fixes = 0, stages = 0;
         bool ok = true;
         while (ok && walk.next(A, &P)) {
             const int n = P.i1 - P.i0;
@@ -935,21 +944,26 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     const int tf = P.r.tile(P.i0 + tile) * kTile;
                     const bool fix = value && !sees_all(A, first, last, tf);
                     for (int p = 0; ok && p < PANELS; ++p) {
-                        ok = mbar_wait(&S.code_full[cst], cuse & 1, quit, A.wait_ns) &&
-                             (use == 0 || mbar_wait(&S.empty[st], (use - 1) & 1, quit, A.wait_ns));
-                        ok = __all_sync(kFull, ok);
-                        if (!ok) break;
-                        const uint4* from = reinterpret_cast<const uint4*>(codes + cst * C::CODES);
-                        uint8_t* to = ring + st * C::STAGE;
-                        const bool e4m3 = A.cache_dtype == BSA_DTYPE_E4M3;
-                        const bool bad = e4m3 ? widen_stage<C, true>(from, to, me) : widen_stage<C, false>(from, to, me);
-                        if (bad) widen_odd<C>(from, to, me, e4m3);
-                        if (fix) asm volatile("bar.sync 2, 128;" ::: "memory");
-                        if (fix) odd |= clean_stage<C>(to, me, [&](int row) { return seen(tf + row); });
-                        if (fix && odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
-                        mbar_arrive(&S.code_empty[cst]);
-                        fence_async_smem();
-                        mbar_arrive(&S.full[st]);
+                        // the two groups take stages in turn
+                        if ((stages++ & 1) == group) {
+                            ok = mbar_wait(&S.code_full[cst], cuse & 1, quit, A.wait_ns) &&
+                                 (use == 0 || mbar_wait(&S.empty[st], (use - 1) & 1, quit, A.wait_ns));
+                            ok = __all_sync(kFull, ok);
+                            if (!ok) break;
+                            const uint4* from = reinterpret_cast<const uint4*>(codes + cst * C::CODES);
+                            uint8_t* to = ring + st * C::STAGE;
+                            const bool e4m3 = A.cache_dtype == BSA_DTYPE_E4M3;
+                            const bool bad = e4m3 ? widen_stage<C, true>(from, to, me) : widen_stage<C, false>(from, to, me);
+                            if (bad) widen_odd<C>(from, to, me, e4m3);
+                            if (fix) {
+                                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+                                odd |= clean_stage<C>(to, me, [&](int row) { return seen(tf + row); });
+                                if (odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
+                            }
+                            mbar_arrive(&S.code_empty[cst]);
+                            fence_async_smem();
+                            mbar_arrive(&S.full[st]);
+                        }
                         if (++cst == C::CRING) {
                             cst = 0;
                             ++cuse;
@@ -1010,51 +1024,49 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     const int inside = S.valid[slot];
                     const bool whole = inside == kTile && sees_all(A, first, last, tf);
                     const uint32_t s_addr = lanes + buf * kTile;
-                    float x[4][32];
+                    float x[2][32];      // half a row's scores
+                    // 64 columns of the row; hidden scores are -inf
+                    auto fetch = [&](int half) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, x[c]);
-                    // what a score is multiplied by: 8 bits, each page its own
-                    float ks[BITS8 ? kPagesPerBlock : 1];
-                    if constexpr (BITS8) {
+                        for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + 64 * half + 32 * c, x[c]);
 #pragma unroll
-                        for (int p = 0; p < kPagesPerBlock; ++p) ks[p] = S.scale[slot][0][p];
-                    }
+                        for (int c = 0; c < 2; ++c) tmem_wait32(x[c]);
+                        if (whole) return;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_wait32(x[c]);
-                    if (!whole) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            // the columns [32 c, 32 c + 32) that the row sees
-                            const int from = tf + 32 * c;
-                            uint32_t seen = low_bits(min(hi + 1 - from, inside - 32 * c));
+                        for (int c = 0; c < 2; ++c) {
+                            const int column = 64 * half + 32 * c, from = tf + column;
+                            uint32_t seen = low_bits(min(hi + 1 - from, inside - column));
                             if (A.window > 0) seen &= ~low_bits(lo - from) | low_bits(A.sinks - from);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
                                 // a scale of zero must not meet -inf
-                                if constexpr (BITS8) x[c][j] *= ks[2 * c + j / 16];
+                                if constexpr (BITS8) x[c][j] *= S.scale[slot][0][4 * half + 2 * c + j / 16];
                                 x[c][j] = seen >> j & 1 ? x[c][j] : -INFINITY;
                             }
                         }
-                        if constexpr (BITS8) {
+                    };
+                    // what page p's scores are still multiplied by
+                    auto key_scale = [&](int p) { return whole ? S.scale[slot][0][p] : 1.f; };
+                    float top_s = -INFINITY;
+                    // The loops over halves stay loops: the SM's warps run four programs, and unrolled they
+                    // wait for instructions (2.7 of 11 cycles an issue with 8 bits).
+#pragma unroll 1
+                    for (int half = 1; half >= 0; --half) {
+                        fetch(half);
+                        float m[8];      // strands of 8 columns, side by side
 #pragma unroll
-                            for (int p = 0; p < kPagesPerBlock; ++p) ks[p] = 1.f;
+                        for (int p = 0; p < 8; ++p) m[p] = x[p / 4][p % 4 * 8];
+#pragma unroll
+                        for (int j = 1; j < 7; j += 2)
+#pragma unroll
+                            for (int p = 0; p < 8; ++p) m[p] = fmaxf(fmaxf(m[p], x[p / 4][p % 4 * 8 + j]), x[p / 4][p % 4 * 8 + j + 1]);
+#pragma unroll
+                        for (int p = 0; p < 8; p += 2) {
+                            m[p] = fmaxf(fmaxf(m[p], x[p / 4][p % 4 * 8 + 7]), fmaxf(m[p + 1], x[p / 4][p % 4 * 8 + 15]));
+                            if constexpr (BITS8) m[p] *= key_scale(4 * half + p / 2);
                         }
+                        top_s = fmaxf(fmaxf(top_s, m[0]), fmaxf(m[2], fmaxf(m[4], m[6])));
                     }
-                    // maxima of 16 columns each, side by side
-                    float most[8];
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) most[p] = x[p / 2][p % 2 * 16];
-#pragma unroll
-                    for (int j = 1; j < 15; j += 2)
-#pragma unroll
-                        for (int p = 0; p < 8; ++p)
-                            most[p] = fmaxf(fmaxf(most[p], x[p / 2][p % 2 * 16 + j]), x[p / 2][p % 2 * 16 + j + 1]);
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        most[p] = fmaxf(most[p], x[p / 2][p % 2 * 16 + 15]);
-                        if constexpr (BITS8) most[p] *= ks[p];
-                    }
-                    float top_s = fmaxf(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])), fmaxf(fmaxf(most[4], most[5]), fmaxf(most[6], most[7])));
                     if constexpr (!BITS8) top_s *= A.scale_log2e;
                     // a row whose maximum has grown by more than 2^kGrow takes it over
                     const bool grow = valid && top_s > mx + kGrow;
@@ -1077,26 +1089,31 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         }
                     }
                     const float base = mx == -INFINITY ? 0.f : -mx;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        // the first half is there; the second was not touched by its probabilities
+                        if (half == 1) fetch(1);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[16];
-                        float vs[2];
-                        if constexpr (BITS8) {
-                            vs[0] = S.scale[slot][1][2 * c];
-                            vs[1] = S.scale[slot][1][2 * c + 1];
-                        }
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float k = BITS8 ? ks[2 * c + j / 16] : A.scale_log2e;
-                            float a, b;
-                            fma2(a, b, x[c][j], x[c][j + 1], k, k, base, base);
-                            a = ex2(a);
-                            b = ex2(b);
-                            add2(l[c % 2 * 2], l[c % 2 * 2 + 1], a, b);
-                            if constexpr (BITS8) mul2(a, b, vs[j / 16]);
-                            w[j / 2] = pack_bf16(a, b);
+                            for (int g = 0; g < 2; ++g) {
+                                const int page = 4 * half + 2 * c + g;
+                                const float k = BITS8 ? key_scale(page) : A.scale_log2e;
+                                const float vs = BITS8 ? S.scale[slot][1][page] : 1.f;
+#pragma unroll
+                                for (int j = 16 * g; j < 16 * g + 16; j += 2) {
+                                    float a, b;
+                                    fma2(a, b, x[c][j], x[c][j + 1], k, k, base, base);
+                                    a = ex2(a);
+                                    b = ex2(b);
+                                    add2(l[2 * c], l[2 * c + 1], a, b);
+                                    if constexpr (BITS8) mul2(a, b, vs);
+                                    w[j / 2] = pack_bf16(a, b);
+                                }
+                            }
+                            tmem_st16(s_addr + 32 * half + 16 * c, w);
                         }
-                        tmem_st16(s_addr + 16 * c, w);
                     }
                     tmem_wait_st();
                     written = true;
@@ -1296,7 +1313,7 @@ bool encode_cache(CUtensorMap* map, const void* base, int64_t tokens, int64_t H,
     const cuuint32_t unit[3] = {1, 1, 1};
     return fn(map, bits8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
               box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, bits8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              bits8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The queries as a tensor of (dimension, query head of a KV head, KV head, token), read in
