@@ -457,31 +457,23 @@ __device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
     if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
     return w;
 }
-// An 8-bit code as bf16, exactly, its NaN and infinities among them.
-__device__ __forceinline__ uint32_t widen_one(uint32_t code, bool e4m3) {
+// 8-bit codes as bf16, exactly (NaN and infinities too): to half by the conversion instruction, on
+// by way of single.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t widen_two(uint16_t codes) {
     uint32_t h;
-    if (e4m3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
-    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
-    return __float_as_uint(__low2float(*reinterpret_cast<const __half2*>(&h))) >> 16;
+    if constexpr (E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(codes));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_bf16(f.x, f.y);
 }
-// Four finite codes as bf16: the bits after the sign, moved so that the exponents' low ends
-// meet, are the value times 2^-120 (e4m3) or 2^-112 (e5m2), subnormals too.  The
-// conversion instructions, by way of half and single, share a slow pipe with the exponentials.
+__device__ __forceinline__ uint32_t widen_one(uint32_t code, bool e4m3) {
+    return (e4m3 ? widen_two<true>((uint16_t)code) : widen_two<false>((uint16_t)code)) & 0xFFFFu;
+}
 template <bool E4M3>
 __device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-    const uint32_t a = __byte_perm(codes, 0, 0x1404), b = __byte_perm(codes, 0, 0x3424);      // codes in the upper bytes
-    constexpr int DOWN = E4M3 ? 4 : 3;
-    constexpr uint32_t BITS = E4M3 ? 0x07F007F0u : 0x0FE00FE0u;
-    lo = (a & 0x80008000u) | ((a >> DOWN) & BITS);
-    hi = (b & 0x80008000u) | ((b >> DOWN) & BITS);
-    constexpr uint32_t UP = E4M3 ? 0x7B807B80u : 0x77807780u;
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(UP));
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(UP));
-}
-// Nonzero where a code of four is not finite.
-template <bool E4M3>
-__device__ __forceinline__ uint32_t odd_codes(uint32_t codes) {
-    return ((codes & 0x7F7F7F7Fu) + (E4M3 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
+    lo = widen_two<E4M3>((uint16_t)codes);
+    hi = widen_two<E4M3>((uint16_t)(codes >> 16));
 }
 // bits [0, n) of 32
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
@@ -529,11 +521,10 @@ __device__ __forceinline__ uint8_t* place(uint8_t* to, int k, int half) {
     return to + (c / 4) * kAtom + row * 128 + ((((c % 4) * 2 + half) ^ (row & 7)) << 4);
 }
 
-// A stage of codes widened by 128 threads; whether this thread met codes that are not finite.
+// A stage of codes widened by 128 threads.
 template <class C, bool E4M3>
-__device__ __forceinline__ bool widen_stage(const uint4* from, uint8_t* to, int me) {
+__device__ __forceinline__ void widen_stage(const uint4* from, uint8_t* to, int me) {
     constexpr int EACH = C::CODES / 16 / 128, BATCH = 2;
-    uint32_t bad = 0;
 #pragma unroll 1
     for (int i = 0; i < EACH; i += BATCH) {
         uint4 x[BATCH];
@@ -547,7 +538,6 @@ __device__ __forceinline__ bool widen_stage(const uint4* from, uint8_t* to, int 
             widen<E4M3>(x[j].y, w[2], w[3]);
             widen<E4M3>(x[j].z, w[4], w[5]);
             widen<E4M3>(x[j].w, w[6], w[7]);
-            bad |= odd_codes<E4M3>(x[j].x) | odd_codes<E4M3>(x[j].y) | odd_codes<E4M3>(x[j].z) | odd_codes<E4M3>(x[j].w);
             // lanes of the second half of a row store in the other order: no two on one bank
             const int other = k % (C::PD / 16) / 4 & 1;
             const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
@@ -555,15 +545,6 @@ __device__ __forceinline__ bool widen_stage(const uint4* from, uint8_t* to, int 
             *reinterpret_cast<uint4*>(place<C>(to, k, 1 - other)) = other ? a : b;
         }
     }
-    return bad != 0;
-}
-// The same by the conversion instructions, NaN and infinities among the codes.
-template <class C>
-__device__ __noinline__ void widen_odd(const uint4* from, uint8_t* to, int me, bool e4m3) {
-    for (int k = me; k < C::CODES / 16; k += 128)
-        for (int e = 0; e < 16; ++e)
-            *reinterpret_cast<uint16_t*>(place<C>(to, k, e / 8) + e % 8 * 2) =
-                (uint16_t)widen_one(reinterpret_cast<const uint8_t*>(from + k)[e], e4m3);
 }
 // Value rows that no row sees set to zero, and what is not finite in the others; whether there was
 // such.
@@ -952,9 +933,8 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                             if (!ok) break;
                             const uint4* from = reinterpret_cast<const uint4*>(codes + cst * C::CODES);
                             uint8_t* to = ring + st * C::STAGE;
-                            const bool e4m3 = A.cache_dtype == BSA_DTYPE_E4M3;
-                            const bool bad = e4m3 ? widen_stage<C, true>(from, to, me) : widen_stage<C, false>(from, to, me);
-                            if (bad) widen_odd<C>(from, to, me, e4m3);
+                            if (A.cache_dtype == BSA_DTYPE_E4M3) widen_stage<C, true>(from, to, me);
+                            else widen_stage<C, false>(from, to, me);
                             if (fix) {
                                 asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
                                 odd |= clean_stage<C>(to, me, [&](int row) { return seen(tf + row); });
