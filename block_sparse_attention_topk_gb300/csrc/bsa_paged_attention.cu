@@ -90,7 +90,7 @@ struct PagedParams {
     uint32_t s_idesc, o_idesc;
     struct PartHead* heads;       // [grid]
     float* parts;                 // [grid][2][part_rows][D]
-    float2* sums;                 // [grid][2][part_rows]: maximum, sum
+    float4* sums;                 // [grid][2][part_rows]: maximum, sum, outputs' unit
     uint32_t* status;
     unsigned long long wait_ns;   // a wait's limit
     uint32_t stall;               // stages after which a CTA's copies stop, for tests
@@ -137,16 +137,16 @@ struct Cfg {
     static constexpr int MORE = (GIVEN * THREADS - OTHERS * (THREADS - SOFTMAX * 32)) / (SOFTMAX * 32) / 8 * 8;
     static constexpr int MINE = MORE < 255 ? MORE : 248;
     static constexpr uint32_t O_COL = 256;                 // TMEM: scores in columns 0 to 255, outputs behind
-    static_assert(RING >= 3 && RING <= kMaxStages && CRING <= kMaxStages, "ring");
+    static_assert(RING >= 3 && RING <= kMaxStages && CRING <= kMaxStages && CRING % 2 == 0, "rings; the groups take stages of codes in turn");
 };
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], code_full[kMaxStages], code_empty[kMaxStages];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], to_fix, fixed, drained;
-    float scale[kInfo][2][kPagesPerBlock];     // 8 bits: key scales times scale log2 e, value scales
+    uint64_t q_full, q_ready, q_empty, s_full[2], p_full[2], o_full[2], to_fix, fixed, drained;
+    float scale[kInfo][2][kPagesPerBlock];     // 8 bits: key scales times scale log2 e, log2 of value scales
     int valid[kInfo];                          // tokens of a tile inside the cache
     int poison[4];                             // 1 + the number of the last portion with values that are not finite
-    float2 other[kRows];                       // the second stream's maximum and sum
+    uint8_t q_power[2][2][kRows];              // 8 bits: the exponent (by 127) of what a row of queries was divided by, of two portions
     long long total;
     Start start;
     uint32_t tmem_base;
@@ -405,10 +405,21 @@ struct Walk {
     }
 };
 
-// Whether rows at positions [first, last] see all 128 tokens of the tile at `tf`.
-__device__ __forceinline__ bool sees_all(const PagedParams& A, int64_t first, int64_t last, int tf) {
-    return tf + kTile - 1 <= first && (A.window == 0 || tf > last - A.window || tf + kTile <= A.sinks);
+// The first token in the window of a row at position `first`.
+__device__ __forceinline__ int first_seen(const PagedParams& A, int64_t first) {
+    const int64_t lo = A.window > 0 ? (first > 0 ? first : 0) - A.window + 1 : 0;
+    return (int)(lo < 0 ? 0 : lo < INT32_MAX ? lo : INT32_MAX);
 }
+// The tiles that rows at positions [first, last] see in full.
+struct Whole {
+    int end, window, sinks;      // tiles before `end` and from `window` on, or before `sinks`
+    __device__ __forceinline__ Whole(const PagedParams& A, int64_t first, int64_t last) {
+        end = (int)(first < 0 ? 0 : (first + 1) / kTile);
+        window = A.window > 0 && last >= A.window ? (int)((last - A.window) / kTile) + 1 : 0;
+        sinks = A.sinks / kTile;
+    }
+    __device__ __forceinline__ bool has(int tile) const { return tile < end && (tile >= window || tile < sinks); }
+};
 
 // The registers of a role's threads; a group of four warps asks as one.
 template <int N, bool MORE>
@@ -448,32 +459,31 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-__device__ __forceinline__ bool odd_bf16(uint32_t w) {      // either half infinite or NaN
-    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
 }
-// a bf16 half set to zero where it is not finite
-__device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
-    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-    return w;
-}
-// 8-bit codes as bf16, exactly (NaN and infinities too): to half by the conversion instruction, on
-// by way of single.
+// two 8-bit codes as halves, exactly (NaN and infinities too)
 template <bool E4M3>
-__device__ __forceinline__ uint32_t widen_two(uint16_t codes) {
+__device__ __forceinline__ uint32_t widen(uint32_t codes) {
     uint32_t h;
-    if constexpr (E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
-    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(codes));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return pack_bf16(f.x, f.y);
+    if constexpr (E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return h;
 }
-__device__ __forceinline__ uint32_t widen_one(uint32_t code, bool e4m3) {
-    return (e4m3 ? widen_two<true>((uint16_t)code) : widen_two<false>((uint16_t)code)) & 0xFFFFu;
+// Whether either half of a word of values is infinite or NaN, and the word with zeros there.
+template <bool HALF>
+__device__ __forceinline__ bool odd_word(uint32_t w) {
+    constexpr uint32_t E = HALF ? 0x7C00u : 0x7F80u;
+    return (w & E) == E || (w & E << 16) == E << 16;
 }
-template <bool E4M3>
-__device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-    lo = widen_two<E4M3>((uint16_t)codes);
-    hi = widen_two<E4M3>((uint16_t)(codes >> 16));
+template <bool HALF>
+__device__ __forceinline__ uint32_t finite_word(uint32_t w) {
+    constexpr uint32_t E = HALF ? 0x7C00u : 0x7F80u;
+    if ((w & E) == E) w &= 0xFFFF0000u;
+    if ((w & E << 16) == E << 16) w &= 0x0000FFFFu;
+    return w;
 }
 // bits [0, n) of 32
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
@@ -484,11 +494,11 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 
 // are not finite of tokens that the row sees.
 template <class C, bool BITS8>
 __device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion P, int stream, int hi, int lo, int d0, float* o) {
-    const int64_t first = P.s.p0 + P.tok0, last = first + P.ntok - 1;      // as the values' warps have it
+    const Whole whole(A, P.s.p0 + P.tok0, P.s.p0 + P.tok0 + P.ntok - 1);      // as the values' warps have it
     for (int i = P.i0; i < P.i1; ++i) {
         if (P.split && ((i - P.i0) & 1) != stream) continue;
         const int tf = P.r.tile(i) * kTile;
-        if (sees_all(A, first, last, tf)) continue;
+        if (whole.has(P.r.tile(i))) continue;
         const int64_t id = __ldg(A.table + (int64_t)P.b * A.max_blocks + P.r.tile(i));
         for (int c = 0; c < kTile; ++c) {
             const int j = tf + c;
@@ -496,16 +506,15 @@ __device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion 
             if (j > hi || (A.window > 0 && j < lo && j >= A.sinks) || page < 0 || page >= A.num_pages) continue;
             const int64_t at = ((page * kSubPage + c % kSubPage) * A.H + P.h) * A.D;
             for (int k = 0; k < 32 && d0 + k < A.D; ++k) {
-                uint32_t w;
+                float x;
                 if constexpr (BITS8) {
-                    const uint32_t x = __ldg(A.v + at + d0 + k);
-                    w = widen_one(x, A.cache_dtype == BSA_DTYPE_E4M3);
+                    const uint32_t c = __ldg(A.v + at + d0 + k);
+                    const uint32_t w = A.cache_dtype == BSA_DTYPE_E4M3 ? widen<true>(c) : widen<false>(c);
+                    x = __low2float(*reinterpret_cast<const __half2*>(&w)) * __ldg(A.vs + page * A.H + P.h);
                 } else {
-                    w = __ldg(reinterpret_cast<const uint16_t*>(A.v) + at + d0 + k);
+                    x = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(A.v) + at + d0 + k) << 16);
                 }
-                if ((w & 0x7F80u) != 0x7F80u) continue;
-                float x = __uint_as_float(w << 16);
-                if constexpr (BITS8) x *= __ldg(A.vs + page * A.H + P.h);
+                if (x - x == 0.f) continue;
                 o[k] += x;
             }
         }
@@ -533,11 +542,10 @@ __device__ __forceinline__ void widen_stage(const uint4* from, uint8_t* to, int 
 #pragma unroll
         for (int j = 0; j < BATCH; ++j) {
             const int k = me + (i + j) * 128;
+            const uint32_t in[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
             uint32_t w[8];
-            widen<E4M3>(x[j].x, w[0], w[1]);
-            widen<E4M3>(x[j].y, w[2], w[3]);
-            widen<E4M3>(x[j].z, w[4], w[5]);
-            widen<E4M3>(x[j].w, w[6], w[7]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = widen<E4M3>(in[e / 2] >> (e % 2 * 16));
             // lanes of the second half of a row store in the other order: no two on one bank
             const int other = k % (C::PD / 16) / 4 & 1;
             const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
@@ -548,7 +556,7 @@ __device__ __forceinline__ void widen_stage(const uint4* from, uint8_t* to, int 
 }
 // Value rows that no row sees set to zero, and what is not finite in the others; whether there was
 // such.
-template <class C, class Seen>
+template <class C, bool HALF, class Seen>
 __device__ __forceinline__ bool clean_stage(uint8_t* stage, int me, Seen seen) {
     bool odd = false;
     uint4* v = reinterpret_cast<uint4*>(stage);
@@ -557,12 +565,41 @@ __device__ __forceinline__ bool clean_stage(uint8_t* stage, int me, Seen seen) {
         const uint4 x = v[k];
         if (!seen(k % (kAtom / 16) / 8)) {
             v[k] = make_uint4(0, 0, 0, 0);
-        } else if (odd_bf16(x.x) || odd_bf16(x.y) || odd_bf16(x.z) || odd_bf16(x.w)) {
+        } else if (odd_word<HALF>(x.x) || odd_word<HALF>(x.y) || odd_word<HALF>(x.z) || odd_word<HALF>(x.w)) {
             odd = true;
-            v[k] = make_uint4(finite_bf16(x.x), finite_bf16(x.y), finite_bf16(x.z), finite_bf16(x.w));
+            v[k] = make_uint4(finite_word<HALF>(x.x), finite_word<HALF>(x.y), finite_word<HALF>(x.z), finite_word<HALF>(x.w));
         }
     }
     return odd;
+}
+
+// A row of queries from bf16 to half, multiplied by a power of two that takes its largest magnitude
+// to [2^14, 2^15): exact down to 2^-28 of that, and off by at most 2^-40 of it below.
+// Returns the exponent, by 127, of what the row was divided by.
+template <class C>
+__device__ __forceinline__ int halve_row(uint8_t* tile, int row) {
+    auto word = [&](int c) { return reinterpret_cast<uint4*>(tile + c / 8 * kAtom + row * 128 + ((c % 8 ^ (row & 7)) << 4)); };
+    uint32_t most = 0;
+#pragma unroll 4
+    for (int c = 0; c < C::D / 8; ++c) {
+        const uint4 x = *word(c);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
+    }
+    const int e = min(max((int)(most >> 7) - 127, -112), 126);      // of the largest; NaN and infinities as the largest finite
+    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+#pragma unroll 4
+    for (int c = 0; c < C::D / 8; ++c) {
+        uint4* at = word(c);
+        const uint4 x = *at;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = pack_half(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+        *at = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    return 127 - 14 + e;
 }
 
 template <int D_, bool BITS8>
@@ -590,6 +627,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             mbar_init(&S.o_full[i], 1);
         }
         mbar_init(&S.q_full, 1);
+        mbar_init(&S.q_ready, 256);
         mbar_init(&S.q_empty, 2);            // the products, and the join of the streams
         mbar_init(&S.to_fix, 1);
         mbar_init(&S.fixed, 64);
@@ -685,7 +723,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 scale = 0.f;
                 if (t >= n || id < 0 || (int64_t)id * kPagesPerBlock + pg >= A.num_pages) return;
                 const int64_t where = ((int64_t)id * kPagesPerBlock + pg) * A.H + P.h;
-                scale = lane & 8 ? __ldg(A.vs + where) : __ldg(A.ks + where) * A.scale_log2e;
+                scale = lane & 8 ? log2f(__ldg(A.vs + where)) : __ldg(A.ks + where) * A.scale_log2e;
             };
             for (int i = P.i0; ok && i <= P.i1; ++i) {
                 int at = 0;
@@ -772,12 +810,13 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             while (ok && walk.next(A, &P)) {
                 const int n = P.i1 - P.i0;
                 if (n == 0) continue;
-                const int64_t first = P.s.p0 + P.tok0, last = first + P.ntok - 1;
-                wait(&S.q_full, loads & 1);
+                const Whole seen_whole(A, P.s.p0 + P.tok0, P.s.p0 + P.tok0 + P.ntok - 1);
+                wait(BITS8 ? &S.q_ready : &S.q_full, loads & 1);
+                tc_fence_after();
                 ++loads;
                 // bf16: tiles that some rows do not see in full pass through the values' warps,
                 // while their probabilities are formed
-                auto partly = [&](int i) { return !BITS8 && !sees_all(A, first, last, P.r.tile(i) * kTile); };
+                auto partly = [&](int i) { return !BITS8 && !seen_whole.has(P.r.tile(i)); };
                 auto fixed = [&]() {
                     wait(&S.fixed, fixes & 1);
                     ++fixes;
@@ -879,24 +918,21 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         Walk<C> walk(A, S.start);
         Portion P;
         const int me = (tid - C::VALUES * 32) % C::VALUE_THREADS, group = (warp - C::VALUES) / 4;
-        uint32_t st = 0, use = 0, cst = 0, cuse = 0, fixes = 0, stages = 0;
         bool ok = true;
-        while (ok && walk.next(A, &P)) {
-            const int n = P.i1 - P.i0;
-            const int64_t first = P.s.p0 + P.tok0, last = first + P.ntok - 1;
-            const int64_t lo = A.window > 0 ? (first > 0 ? first : 0) - A.window + 1 : 0;      // the first row's first token
-            bool odd = false;
-            // whether some row of the item sees the token
-            auto seen = [&](int j) { return j < P.r.end && (j >= lo || j < A.sinks); };
-            if constexpr (!BITS8) {
-                // K and V stages in the copies' order; only V stages of partly seen tiles matter
+        if constexpr (!BITS8) {
+            uint32_t st = 0, use = 0, fixes = 0;      // stages so far
+            while (ok && walk.next(A, &P)) {
+                const int n = P.i1 - P.i0;
+                const int64_t first = P.s.p0 + P.tok0;
+                const Whole whole(A, first, first + P.ntok - 1);
+                const int lo = first_seen(A, first);
+                bool odd = false;
                 const bool ahead = NS == 1 || P.split;
                 for (int i = 0; ok && i < n; ++i) {
-                    const int tf = P.r.tile(P.i0 + i) * kTile;
-                    // stages before this tile's values
-                    const int before = (ahead ? min(i + 2, n) + i : 2 * i + 1) * PANELS;
-                    if (sees_all(A, first, last, tf)) continue;
-                    const uint32_t s0 = st + before;
+                    const int tile = P.r.tile(P.i0 + i);
+                    if (whole.has(tile)) continue;
+                    // K and V stages in the copies' order: those before this tile's values
+                    const uint32_t s0 = st + (ahead ? min(i + 2, n) + i : 2 * i + 1) * PANELS;
                     // the MMAs' thread has them in the ring, and waits
                     ok = mbar_wait(&S.to_fix, fixes & 1, quit, A.wait_ns);
                     ok = __all_sync(kFull, ok);
@@ -906,7 +942,10 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         ok = mbar_wait(&S.full[s], u & 1, quit, A.wait_ns);
                         ok = __all_sync(kFull, ok);
                         if (!ok) break;
-                        odd |= clean_stage<C>(ring + s * C::STAGE, me, [&](int row) { return seen(tf + row); });
+                        odd |= clean_stage<C, false>(ring + s * C::STAGE, me, [&](int row) {
+                            const int j = tile * kTile + row;
+                            return j < P.r.end && (j >= lo || j < A.sinks);
+                        });
                     }
                     if (!ok) break;
                     if (odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
@@ -916,44 +955,70 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 const uint32_t total = st + 2 * n * PANELS;
                 use += total / RING;
                 st = total % RING;
-            } else {
+            }
+        } else {
+            // the two groups take stages in turn, each the ring's every other
+            uint32_t cst = group, cuse = 0, st = group, use = 0, stages = 0, loads = 0;
+            while (ok && walk.next(A, &P)) {
+                const int n = P.i1 - P.i0;
+                if (n == 0) continue;
+                const int64_t first = P.s.p0 + P.tok0;
+                const Whole whole(A, first, first + P.ntok - 1);
+                const int lo = first_seen(A, first);
+                bool odd = false, queries = false;
                 const bool ahead = NS == 1 || P.split;
-                for (int i = 0; ok && i < 2 * n; ++i) {
+                for (int q = (stages & 1) != group; ok && q < 2 * n * PANELS; q += 2) {
                     // the copies' order: K V K V ..., or K K V K V ... V V
+                    const int i = q / PANELS;
                     const bool value = ahead ? (i > 0 && (i % 2 == 0 || i == 2 * n - 1)) : (i & 1);
-                    const int tile = ahead ? (value ? (i == 2 * n - 1 ? n - 1 : i / 2 - 1) : (i + 1) / 2) : i / 2;
-                    const int tf = P.r.tile(P.i0 + tile) * kTile;
-                    const bool fix = value && !sees_all(A, first, last, tf);
-                    for (int p = 0; ok && p < PANELS; ++p) {
-                        // the two groups take stages in turn
-                        if ((stages++ & 1) == group) {
-                            ok = mbar_wait(&S.code_full[cst], cuse & 1, quit, A.wait_ns) &&
-                                 (use == 0 || mbar_wait(&S.empty[st], (use - 1) & 1, quit, A.wait_ns));
-                            ok = __all_sync(kFull, ok);
-                            if (!ok) break;
-                            const uint4* from = reinterpret_cast<const uint4*>(codes + cst * C::CODES);
-                            uint8_t* to = ring + st * C::STAGE;
-                            if (A.cache_dtype == BSA_DTYPE_E4M3) widen_stage<C, true>(from, to, me);
-                            else widen_stage<C, false>(from, to, me);
-                            if (fix) {
-                                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
-                                odd |= clean_stage<C>(to, me, [&](int row) { return seen(tf + row); });
-                                if (odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
-                            }
-                            mbar_arrive(&S.code_empty[cst]);
-                            fence_async_smem();
-                            mbar_arrive(&S.full[st]);
-                        }
-                        if (++cst == C::CRING) {
-                            cst = 0;
-                            ++cuse;
-                        }
-                        if (++st == RING) {
-                            st = 0;
-                            ++use;
+                    const int k = ahead ? (value ? (i == 2 * n - 1 ? n - 1 : i / 2 - 1) : (i + 1) / 2) : i / 2;
+                    ok = mbar_wait(&S.code_full[cst], cuse & 1, quit, A.wait_ns) &&
+                         (use == 0 || mbar_wait(&S.empty[st], (use - 1) & 1, quit, A.wait_ns));
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    const uint4* from = reinterpret_cast<const uint4*>(codes + cst * C::CODES);
+                    uint8_t* to = ring + st * C::STAGE;
+                    if (A.cache_dtype == BSA_DTYPE_E4M3) widen_stage<C, true>(from, to, me);
+                    else widen_stage<C, false>(from, to, me);
+                    if (value) {
+                        const int tile = P.r.tile(P.i0 + k);
+                        if (!whole.has(tile)) {
+                            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+                            odd |= clean_stage<C, true>(to, me, [&](int row) {
+                                const int j = tile * kTile + row;
+                                return j < P.r.end && (j >= lo || j < A.sinks);
+                            });
+                            if (odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
                         }
                     }
+                    mbar_arrive(&S.code_empty[cst]);
+                    fence_async_smem();
+                    mbar_arrive(&S.full[st]);
+                    cst += 2;
+                    if (cst >= C::CRING) {
+                        cst -= C::CRING;
+                        ++cuse;
+                    }
+                    st += 2;
+                    if (st >= RING) {
+                        st -= RING;
+                        ++use;
+                    }
+                    if (!queries) {
+                        // each group a query tile, the first group the only one
+                        queries = true;
+                        ok = mbar_wait(&S.q_full, loads & 1, quit, A.wait_ns);
+                        ok = __all_sync(kFull, ok);
+                        if (!ok) break;
+                        const int m = P.ntok > A.tokens ? group : 0;
+                        const int rows = min(A.tokens, P.ntok - m * A.tokens) * A.G;
+                        if (me < rows && (m == group || group == 0)) S.q_power[loads & 1][m][me] = (uint8_t)halve_row<C>(qsm + m * C::Q_TILE, me);
+                        fence_async_smem();
+                        mbar_arrive(&S.q_ready);
+                        ++loads;
+                    }
                 }
+                stages += 2 * n * PANELS;
             }
         }
     } else if (warp >= C::SOFTMAX) {
@@ -966,7 +1031,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         const int stream = warp >> 2, row = tid & 127, token = row / A.G;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const uint32_t o_addr = lanes + C::O_COL + stream * C::D;
-        uint32_t s_phase = 0, o_phase = 0, tiles = 0, nq = 0;
+        uint32_t s_phase = 0, o_phase = 0, tiles = 0, nq = 0, loads = 0;      // loads: of queries
         bool ok = true, left_head = false;
         while (walk.next(A, &P)) {
             const int n = P.i1 - P.i0;
@@ -979,7 +1044,11 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             const int64_t top = (int64_t)A.max_blocks * kTile;
             const int hi = (int)(pos < 0 ? -1 : pos < top ? pos : top - 1);
             const int lo = A.window > 0 ? (int)(pos - A.window + 1 < 0 ? 0 : pos - A.window + 1 < top ? pos - A.window + 1 : top) : 0;
-            float mx = -INFINITY, l[4] = {};
+            const Whole seen_whole(A, first, last);
+            // The row's sums are in units of 2^mx and its outputs in units of 2^mo: with bf16 the same; with 8
+            // bits mo goes by the largest probability times value scale, so that those are halves of
+            // 11 bits in either's place, whatever the scales of pages that do not count.
+            float mx = -INFINITY, mo = -INFINITY, l[4] = {};
             bool written = false;                                        // O holds something
             const int stride = P.split ? 2 : 1;
             for (int k = P.split ? stream : 0; k < n; k += stride) {
@@ -1002,57 +1071,75 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 if (live) {
                     const int tf = P.r.tile(P.i0 + k) * kTile, slot = (tiles + k) % kInfo;
                     const int inside = S.valid[slot];
-                    const bool whole = inside == kTile && sees_all(A, first, last, tf);
+                    const bool whole = inside == kTile && seen_whole.has(P.r.tile(P.i0 + k));
                     const uint32_t s_addr = lanes + buf * kTile;
-                    float x[2][32];      // half a row's scores
-                    // 64 columns of the row; hidden scores are -inf
-                    auto fetch = [&](int half) {
+                    constexpr int N = BITS8 ? 2 : 4;      // chunks of 32 columns in registers
+                    float x[N][32];
+                    const float qs = BITS8 ? __uint_as_float((uint32_t)S.q_power[loads & 1][m][row] << 23) : 1.f;
+                    // what page p's scores are multiplied by
+                    auto key_scale = [&](int p) { return S.scale[slot][0][p] * qs; };
+                    // chunk c of the row's scores: hidden ones are -inf (with 8 bits after their scale, as that
+                    // may be zero)
+                    auto hide = [&](int c, float (&v)[32]) {
+                        const int from = tf + 32 * c;
+                        uint32_t seen = low_bits(min(hi + 1 - from, inside - 32 * c));
+                        if (A.window > 0) seen &= ~low_bits(lo - from) | low_bits(A.sinks - from);
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + 64 * half + 32 * c, x[c]);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) tmem_wait32(x[c]);
-                        if (whole) return;
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int column = 64 * half + 32 * c, from = tf + column;
-                            uint32_t seen = low_bits(min(hi + 1 - from, inside - column));
-                            if (A.window > 0) seen &= ~low_bits(lo - from) | low_bits(A.sinks - from);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                // a scale of zero must not meet -inf
-                                if constexpr (BITS8) x[c][j] *= S.scale[slot][0][4 * half + 2 * c + j / 16];
-                                x[c][j] = seen >> j & 1 ? x[c][j] : -INFINITY;
-                            }
+                        for (int j = 0; j < 32; ++j) {
+                            if constexpr (BITS8) v[j] *= key_scale(2 * c + j / 16);
+                            v[j] = seen >> j & 1 ? v[j] : -INFINITY;
                         }
                     };
-                    // what page p's scores are still multiplied by
-                    auto key_scale = [&](int p) { return whole ? S.scale[slot][0][p] : 1.f; };
-                    float top_s = -INFINITY;
-                    // The loops over halves stay loops: the SM's warps run four programs, and unrolled they
-                    // wait for instructions (2.7 of 11 cycles an issue with 8 bits).
-#pragma unroll 1
-                    for (int half = 1; half >= 0; --half) {
-                        fetch(half);
-                        float m[8];      // strands of 8 columns, side by side
+                    auto fetch = [&](int c0) {
 #pragma unroll
-                        for (int p = 0; p < 8; ++p) m[p] = x[p / 4][p % 4 * 8];
+                        for (int c = 0; c < N; ++c) tmem_ld32(s_addr + 32 * (c0 + c), x[c]);
+#pragma unroll
+                        for (int c = 0; c < N; ++c) tmem_wait32(x[c]);
+                        if (!whole) {
+#pragma unroll
+                            for (int c = 0; c < N; ++c) hide(c0 + c, x[c]);
+                        }
+                    };
+                    // maxima of 16 columns, the largest in `top_s`, with their pages' value scales in `top_o`
+                    float top_s = -INFINITY, top_o = -INFINITY;
+                    auto maxima = [&](int c0) {
+                        float m8[4 * N];      // strands of 8 columns, side by side
+#pragma unroll
+                        for (int p = 0; p < 4 * N; ++p) m8[p] = x[p / 4][p % 4 * 8];
 #pragma unroll
                         for (int j = 1; j < 7; j += 2)
 #pragma unroll
-                            for (int p = 0; p < 8; ++p) m[p] = fmaxf(fmaxf(m[p], x[p / 4][p % 4 * 8 + j]), x[p / 4][p % 4 * 8 + j + 1]);
+                            for (int p = 0; p < 4 * N; ++p) m8[p] = fmaxf(fmaxf(m8[p], x[p / 4][p % 4 * 8 + j]), x[p / 4][p % 4 * 8 + j + 1]);
 #pragma unroll
-                        for (int p = 0; p < 8; p += 2) {
-                            m[p] = fmaxf(fmaxf(m[p], x[p / 4][p % 4 * 8 + 7]), fmaxf(m[p + 1], x[p / 4][p % 4 * 8 + 15]));
-                            if constexpr (BITS8) m[p] *= key_scale(4 * half + p / 2);
+                        for (int p = 0; p < 4 * N; p += 2) {
+                            m8[p] = fmaxf(fmaxf(m8[p], x[p / 4][p % 4 * 8 + 7]), fmaxf(m8[p + 1], x[p / 4][p % 4 * 8 + 15]));
+                            if constexpr (BITS8) {
+                                if (whole) m8[p] *= key_scale(2 * c0 + p / 2);
+                                top_o = fmaxf(top_o, m8[p] + S.scale[slot][1][2 * c0 + p / 2]);
+                            }
+                            top_s = fmaxf(top_s, m8[p]);
                         }
-                        top_s = fmaxf(fmaxf(top_s, m[0]), fmaxf(m[2], fmaxf(m[4], m[6])));
+                    };
+                    if constexpr (BITS8) {
+                        // The loops over halves stay loops here: the SM's warps run five programs, and waited for
+                        // instructions for 2.7 of 11 cycles an issue with this one unrolled.
+#pragma unroll 1
+                        for (int c0 = 2; c0 >= 0; c0 -= 2) {
+                            fetch(c0);
+                            maxima(c0);
+                        }
+                    } else {
+                        fetch(0);
+                        maxima(0);
+                        top_s *= A.scale_log2e;
+                        top_o = top_s;
                     }
-                    if constexpr (!BITS8) top_s *= A.scale_log2e;
                     // a row whose maximum has grown by more than 2^kGrow takes it over
-                    const bool grow = valid && top_s > mx + kGrow;
-                    if (__any_sync(kFull, grow)) {
-                        const float keep = grow ? ex2(mx - top_s) : 1.f;
+                    const bool grow = valid && top_s > mx + kGrow, grow_o = BITS8 ? valid && top_o > mo + kGrow : grow;
+                    if (__any_sync(kFull, grow || grow_o)) {
+                        const float keep = grow ? ex2(mx - top_s) : 1.f, keep_o = grow_o ? ex2(mo - top_o) : 1.f;
                         if (grow) mx = top_s;
+                        if (grow_o) mo = top_o;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) l[i] *= keep;
                         if (written) {
@@ -1063,37 +1150,50 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                                 tmem_ld16(o_addr + 16 * c, o);
                                 uint32_t w[16];
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * keep);
+                                for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * keep_o);
                                 tmem_st16(o_addr + 16 * c, w);
                             }
                         }
                     }
                     const float base = mx == -INFINITY ? 0.f : -mx;
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        // the first half is there; the second was not touched by its probabilities
-                        if (half == 1) fetch(1);
+                    const float unit = mo == -INFINITY ? -INFINITY : mx - mo;
+                    // the probabilities of chunks [c0, c0 + N) in x, to the scores' place
+                    auto turn = [&](int c0) {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
+                        for (int c = 0; c < N; ++c) {
                             uint32_t w[16];
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
-                                const int page = 4 * half + 2 * c + g;
-                                const float k = BITS8 ? key_scale(page) : A.scale_log2e;
-                                const float vs = BITS8 ? S.scale[slot][1][page] : 1.f;
+                                const int page = 2 * (c0 + c) + g;
+                                const float k = !BITS8 ? A.scale_log2e : whole ? key_scale(page) : 1.f;
+                                const float v = BITS8 ? ex2(S.scale[slot][1][page] + unit) : 1.f;
 #pragma unroll
                                 for (int j = 16 * g; j < 16 * g + 16; j += 2) {
                                     float a, b;
                                     fma2(a, b, x[c][j], x[c][j + 1], k, k, base, base);
                                     a = ex2(a);
                                     b = ex2(b);
-                                    add2(l[2 * c], l[2 * c + 1], a, b);
-                                    if constexpr (BITS8) mul2(a, b, vs);
-                                    w[j / 2] = pack_bf16(a, b);
+                                    add2(l[c % 2 * 2], l[c % 2 * 2 + 1], a, b);
+                                    if constexpr (BITS8) {
+                                        mul2(a, b, v);
+                                        w[j / 2] = pack_half(a, b);
+                                    } else {
+                                        w[j / 2] = pack_bf16(a, b);
+                                    }
                                 }
                             }
-                            tmem_st16(s_addr + 32 * half + 16 * c, w);
+                            tmem_st16(s_addr + 16 * (c0 + c), w);
                         }
+                    };
+                    if constexpr (BITS8) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 4; c0 += 2) {
+                            // the lower half is there; the upper was not touched by its probabilities
+                            if (c0 > 0) fetch(c0);
+                            turn(c0);
+                        }
+                    } else {
+                        turn(0);
                     }
                     tmem_wait_st();
                     written = true;
@@ -1105,6 +1205,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             }
             if (NS == 1) nq += n;
             tiles += n;
+            loads += n > 0;
             // ---- the portion's result
             const bool any = n > (P.split ? stream : 0);
             if (NS == 1) {
@@ -1116,7 +1217,8 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             ok = __all_sync(kFull, ok);
             tc_fence_after();
             float sum = (l[0] + l[1]) + (l[2] + l[3]);
-            if (!ok) mx = sum = NAN;
+            if constexpr (!BITS8) mo = mx;
+            if (!ok) mx = mo = sum = NAN;
             const bool odd = any && S.poison[P.number & 3] == P.number + 1;
             // 32 of the row's outputs, not yet divided by the sum
             auto result = [&](int c, float (&o)[32]) {
@@ -1138,28 +1240,34 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             };
             const bool join = P.split && n > 1;      // both streams have a part of the rows
             float f0 = 1.f, f1 = 0.f;
-            float* xch = reinterpret_cast<float*>(qsm + C::Q_TILE);      // the second query tile's place: [D / 2][128]
+            // the second stream's maxima, sums and units, and half of its outputs, in the queries' place: its
+            // last product is behind all scores
+            float4* other = reinterpret_cast<float4*>(qsm);
+            float* xch = reinterpret_cast<float*>(qsm + C::Q_TILE);      // [D / 2][128]
             if (NS == 2 && join) {
-                if (stream == 1) S.other[row] = make_float2(mx, sum);
+                if (stream == 1) other[row] = make_float4(mx, sum, mo, 0.f);
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 if (stream == 0) {
-                    const float2 y = S.other[row];
-                    const float m2 = fmaxf(mx, y.x);
-                    f0 = mx == -INFINITY ? 0.f : ex2(mx - m2);
-                    f1 = y.x == -INFINITY ? 0.f : ex2(y.x - m2);
-                    sum = sum * f0 + y.y * f1;
+                    const float4 y = other[row];
+                    const float m2 = fmaxf(mx, y.x), o2 = fmaxf(mo, y.z);
+                    f0 = mo == -INFINITY ? 0.f : ex2(mo - o2);
+                    f1 = y.z == -INFINITY ? 0.f : ex2(y.z - o2);
+                    sum = (mx == -INFINITY ? 0.f : sum * ex2(mx - m2)) + (y.x == -INFINITY ? 0.f : y.y * ex2(y.x - m2));
                     mx = m2;
+                    mo = o2;
                     if (!(y.y == y.y)) sum = NAN;
                 }
             }
             const bool whole_item = P.begins && P.ends;
-            const float scale = whole_item ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+            // from the outputs' unit to the sums', in two factors where it may pass the range of one
+            const float back = BITS8 && whole_item && mo > -INFINITY ? ex2(0.5f * (mo - mx)) : 1.f;
+            const float scale = whole_item ? (sum == 0.f ? 0.f : back / sum) : 1.f;
             const int64_t t = P.s.t0 + P.tok0 + m * A.tokens + token;
             uint16_t* out = A.out + ((t * A.H + P.h) * A.G + row % A.G) * A.D;
             const int64_t slot = (int64_t)blockIdx.x * 2 + (P.begins ? 1 : 0);
             const int part_row = m * kRows + row;
             const bool writes = valid && (stream == 0 || !P.split);
-            if (!whole_item && writes) A.sums[slot * A.part_rows + part_row] = make_float2(mx, sum);
+            if (!whole_item && writes) A.sums[slot * A.part_rows + part_row] = make_float4(mx, sum, mo, 0.f);
             float* part = A.parts + (slot * A.part_rows + part_row) * A.D;
             if (!whole_item && P.begins && tid == 0) {
                 PartHead head;
@@ -1199,6 +1307,10 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         }
                         if (!writes) continue;
                         if (whole_item) {
+                            if constexpr (BITS8) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] *= back;
+                            }
 #pragma unroll
                             for (int j = 0; j < 32; j += 8)
                                 if (d0 + j < A.D)
@@ -1239,21 +1351,26 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedPar
         const int r = i / words, d = i - r * words;
         const int token = r / A.G, g = r - token * A.G, tile = token / A.tokens;
         const int64_t part_row = tile * kRows + (token - tile * A.tokens) * A.G + g;
-        float m = -INFINITY, l = 0.f, o[8] = {};
+        float m = -INFINITY, mo = -INFINITY, l = 0.f, o[8] = {};
         for (int k = 0; k <= head.more; ++k) {
             const int64_t at = ((int64_t)(blockIdx.x + k) * 2 + (k == 0)) * A.part_rows + part_row;
-            const float2 s = A.sums[at];
+            const float4 s = A.sums[at];
             const float4* p = reinterpret_cast<const float4*>(A.parts + at * A.D + d * 8);
             const float4 x = p[0], y = p[1];
-            const float m2 = fmaxf(m, s.x), base = m2 == -INFINITY ? 0.f : m2;
-            const float f0 = ex2(m - base), f1 = s.x != s.x ? NAN : ex2(s.x - base);
+            const float m2 = fmaxf(m, s.x), o2 = fmaxf(mo, s.z);
+            // a part without tokens has -inf for its maximum; one that is not finished NaN
+            l = (m == -INFINITY ? 0.f : l * ex2(m - m2)) + (s.x == -INFINITY ? 0.f : s.y * ex2(s.x != s.x ? NAN : s.x - m2));
+            const float f0 = mo == -INFINITY ? 0.f : ex2(mo - o2), f1 = s.z == -INFINITY ? 0.f : ex2(s.z != s.z ? NAN : s.z - o2);
             m = m2;
-            l = l * f0 + s.y * f1;
+            mo = o2;
             const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = o[j] * f0 + v[j] * f1;
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float back = mo > -INFINITY ? ex2(0.5f * (mo - m)) : 1.f;
+        const float inv = l == 0.f ? 0.f : back / l;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] *= back;
         const int64_t row = ((head.row0 + token) * A.H + head.h) * A.G + g;
         *reinterpret_cast<uint4*>(A.out + row * A.D + d * 8) =
             make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv), pack_bf16(o[4] * inv, o[5] * inv),
@@ -1354,7 +1471,7 @@ Parts place_parts(int64_t T, int64_t G, int64_t D, int grid) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     p.heads = up(rows * D * sizeof(float));
     p.sums = p.heads + up((size_t)grid * sizeof(PartHead));
-    p.bytes = p.sums + up(rows * sizeof(float2));
+    p.bytes = p.sums + up(rows * sizeof(float4));
     return p;
 }
 
@@ -1401,11 +1518,11 @@ int launch_paged(const bsa_paged_attention_args_t& a, PagedParams& A, cudaStream
     // a scale of zero must not meet the -inf of hidden scores; any tiny one has its result
     const float scale = fabsf(a.scale) * 1.44269504f;
     A.scale_log2e = scale == 0.f ? 1e-30f : scale;
-    A.s_idesc = bf16_idesc(a.scale < 0.f, false, kRows, kTile);
-    A.o_idesc = bf16_idesc(false, true, kRows, a.D <= 64 ? 64 : 128);
+    A.s_idesc = f16_idesc(!bits8, a.scale < 0.f, false, kRows, kTile);
+    A.o_idesc = f16_idesc(!bits8, false, true, kRows, a.D <= 64 ? 64 : 128);
     A.parts = reinterpret_cast<float*>(ws);
     A.heads = reinterpret_cast<PartHead*>(ws + parts.heads);
-    A.sums = reinterpret_cast<float2*>(ws + parts.sums);
+    A.sums = reinterpret_cast<float4*>(ws + parts.sums);
     A.status = current_status_word();
     A.wait_ns = g_paged_wait_ns.load(std::memory_order_relaxed);
     A.stall = g_paged_stall.load(std::memory_order_relaxed);

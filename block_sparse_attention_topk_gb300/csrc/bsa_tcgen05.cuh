@@ -146,7 +146,7 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
-// bf16 operands, both in shared memory, or A in tensor memory (two values a column).
+// 16-bit operands, both in shared memory, or A in tensor memory (two values a column).
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -163,10 +163,10 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
-// Instruction descriptor of kind::f16 with bf16 operands and fp32 accumulators: A negated, B
-// read N-major.
-constexpr uint32_t bf16_idesc(bool a_neg, bool b_mn, uint32_t M, uint32_t N) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_neg ? 1u : 0u) << 13) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) |
+// Instruction descriptor of kind::f16 with fp32 accumulators: both operands bf16 or both half, A
+// negated, B read N-major.
+constexpr uint32_t f16_idesc(bool bf16, bool a_neg, bool b_mn, uint32_t M, uint32_t N) {
+    return (1u << 4) | (bf16 ? 1u << 7 | 1u << 10 : 0u) | ((a_neg ? 1u : 0u) << 13) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) |
            ((M >> 4) << 24);
 }
 
