@@ -64,6 +64,7 @@ constexpr int kTile = kPageSize;
 constexpr int kAtom = kTile * 128;       // 128 tokens of 64 bf16 dimensions: 16 KB, swizzled by 128 bytes
 constexpr int kMaxStages = 12;
 constexpr int kInfo = 16;                // tiles whose facts are kept: more than the rings hold, and one
+constexpr int kPortions = 4;             // portions announced ahead
 constexpr int kWindow = 512;             // sequences whose units a CTA holds at a time while it finds its part
 constexpr float kGrow = 8.f;             // log2 of what a maximum may grow by before O is rescaled
 constexpr int kJoinThreads = 256;
@@ -88,6 +89,7 @@ struct PagedParams {
     int32_t part_rows;            // rows of a part in the workspace
     float scale_log2e;            // not negative; q_neg holds the sign
     uint32_t s_idesc, o_idesc;
+    bool wide_out;                // out is 32-byte aligned
     struct PartHead* heads;       // [grid]
     float* parts;                 // [grid][2][part_rows][D]
     float4* sums;                 // [grid][2][part_rows]: maximum, sum, outputs' unit
@@ -130,7 +132,7 @@ struct Cfg {
     static constexpr int SOFTMAX = NS * 4;
     static constexpr int COPY = SOFTMAX, MMA = SOFTMAX + 1, VALUES = SOFTMAX + (BITS8 ? 4 : 2);
     static constexpr int WARPS = SOFTMAX + (BITS8 ? 12 : 4);
-    static constexpr int THREADS = WARPS * 32, VALUE_THREADS = BITS8 ? 128 : 64;
+    static constexpr int THREADS = WARPS * 32, VALUE_THREADS = BITS8 ? 128 : 64, VALUE_WARPS = BITS8 ? 8 : 2;
     // registers of a softmax thread and of the others, out of what the launch gives all
     static constexpr int GIVEN = 65536 / THREADS / 8 * 8 < 255 ? 65536 / THREADS / 8 * 8 : 248;
     static constexpr int OTHERS = BITS8 ? 64 : 72;
@@ -140,12 +142,46 @@ struct Cfg {
     static_assert(RING >= 3 && RING <= kMaxStages && CRING <= kMaxStages && CRING % 2 == 0, "rings; the groups take stages of codes in turn");
 };
 
+// The KV tiles that rows at positions [first, last] see: sink tiles [0, st), then
+// tiles [wst, ...), nk in all; `end`: the first token that none of them sees any more.
+struct Range {
+    int nk, st, wst, end;
+    __device__ __forceinline__ int tile(int i) const { return i < st ? i : i - st + wst; }
+};
+// The tiles that rows at positions [first, last] see in full.
+struct Whole {
+    int end, window, sinks;      // tiles before `end` and from `window` on, or before `sinks`
+    __device__ __forceinline__ void set(const PagedParams& A, int64_t first, int64_t last) {
+        end = (int)(first < 0 ? 0 : (first + 1) / kTile);
+        window = A.window > 0 && last >= A.window ? (int)((last - A.window) / kTile) + 1 : 0;
+        sinks = A.sinks / kTile;
+    }
+    __device__ __forceinline__ bool has(int tile) const { return tile < end && (tile >= window || tile < sinks); }
+};
+
+// What a CTA does of one item.  The copies' warp makes it, the others read it from shared memory:
+// in registers it cost each of them 40.
+struct Portion {
+    int64_t row0, pos0;          // first token row, its position
+    Range r;
+    Whole item, tile[2];         // of all rows, and of each query tile's
+    int b, h, tokens;
+    int i0, i1;                  // KV tiles of the range
+    int number;                  // of the portion, and of those with tiles
+    int loads;
+    int lo;                      // the first token that the first row's window holds
+    int more;                    // CTAs that finish an item begun here
+    int split, begins, ends;     // both streams take the same rows; the item's first and last steps are here
+    int over;                    // no portion: the end
+};
+
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], code_full[kMaxStages], code_empty[kMaxStages];
-    uint64_t q_full, q_ready, q_empty, s_full[2], p_full[2], o_full[2], to_fix, fixed, drained;
+    uint64_t q_full, q_ready, q_empty, s_full[2], p_half[2], p_full[2], o_full[2], portion_full[kPortions], portion_empty[kPortions], to_fix, fixed, drained;
     float scale[kInfo][2][kPagesPerBlock];     // 8 bits: key scales times scale log2 e, log2 of value scales
     int valid[kInfo];                          // tokens of a tile inside the cache
-    int poison[4];                             // 1 + the number of the last portion with values that are not finite
+    Portion portion[kPortions];
+    int poison[kPortions];                     // 1 + the number of the last portion with values that are not finite
     uint8_t q_power[2][2][kRows];              // 8 bits: the exponent (by 127) of what a row of queries was divided by, of two portions
     long long total;
     Start start;
@@ -175,12 +211,6 @@ __device__ __forceinline__ Seq sequence(const PagedParams& A, int b) {
     return s;
 }
 
-// The KV tiles that rows at positions [first, last] see: sink tiles [0, st), then
-// tiles [wst, ...), nk in all; `end`: the first token that none of them sees any more.
-struct Range {
-    int nk, st, wst, end;
-    __device__ __forceinline__ int tile(int i) const { return i < st ? i : i - st + wst; }
-};
 __device__ __forceinline__ Range range(const PagedParams& A, int64_t first, int64_t last) {
     Range r;
     const int64_t top = (int64_t)A.max_blocks * kTile;
@@ -344,39 +374,34 @@ __device__ void find_start(const PagedParams& A, Shared& S, long long* units) {
     __syncthreads();
 }
 
-// What a CTA does of one item.
-struct Portion {
-    Seq s;
-    Range r;
-    int b, h, tok0, ntok;        // first token within the sequence, tokens
-    int i0, i1;                  // KV tiles of the range
-    int number;                  // of the portion
-    bool split, begins, ends;    // both streams take the same rows; the item's first and last steps are here
-    int64_t first, steps;        // units before the item, its steps
-};
-
-// The portions of a CTA in order; every warp that needs them walks them by itself.
+// The first token in the window of a row at position `first`.
+__device__ __forceinline__ int first_seen(const PagedParams& A, int64_t first) {
+    const int64_t lo = A.window > 0 ? (first > 0 ? first : 0) - A.window + 1 : 0;
+    return (int)(lo < 0 ? 0 : lo < INT32_MAX ? lo : INT32_MAX);
+}
+// The portions of a CTA in order.
 template <class C>
 struct Walk {
-    int b, h, qt, items, number;
+    int b, h, qt, items, number, loads;
     int64_t at, lo, hi;
     Seq s;
     __device__ __forceinline__ Walk(const PagedParams& A, const Start& st)
-        : b(st.b), h(st.h), qt(st.qt), items(0), number(-1), at(st.first), lo(st.lo), hi(st.hi) {
+        : b(st.b), h(st.h), qt(st.qt), items(0), number(-1), loads(0), at(st.first), lo(st.lo), hi(st.hi) {
         if (lo < hi) {
             s = sequence(A, b);
             items = item_count<C>(A, s);
         }
     }
-    __device__ __forceinline__ bool next(const PagedParams& A, Portion* P) {
+    // The next one, in *P.
+    __device__ bool next(const PagedParams& A, const Start& st, Portion* P) {
         while (at < hi) {
             const int64_t first = at;
-            const int steps = item_steps<C>(A, s, qt, &P->r, &P->split);
-            P->s = s;
-            P->b = b;
-            P->h = h;
-            P->tok0 = qt * item_tokens<C>(A);
-            P->ntok = min(item_tokens<C>(A), s.n - P->tok0);
+            Range r;
+            bool split;
+            const int steps = item_steps<C>(A, s, qt, &r, &split);
+            const int tok0 = qt * item_tokens<C>(A), tokens = min(item_tokens<C>(A), s.n - tok0);
+            const int64_t row0 = s.t0 + tok0, pos0 = s.p0 + tok0;
+            const int item_b = b, item_h = h;
             at += steps + 1;
             if (++qt == items) {
                 qt = 0;
@@ -391,34 +416,39 @@ struct Walk {
             }
             const int a = (int)(lo > first ? lo - first : 0), e = (int)(hi - first < steps ? hi - first : steps);
             if (a >= e && !(steps == 0 && first >= lo)) continue;
+            P->row0 = row0;
+            P->pos0 = pos0;
+            P->r = r;
+            P->item.set(A, pos0, pos0 + tokens - 1);
+            P->tile[0].set(A, pos0, pos0 + min(tokens, A.tokens) - 1);
+            P->tile[1].set(A, pos0 + A.tokens, pos0 + tokens - 1);
+            P->b = item_b;
+            P->h = item_h;
+            P->tokens = tokens;
+            P->i0 = split ? 2 * a : a;
+            P->i1 = split ? min(2 * e, r.nk) : e;
+            P->number = ++number;
+            P->loads = loads;
+            if (P->i1 > P->i0) ++loads;
+            P->lo = first_seen(A, pos0);
+            // the CTA of the item's last step: lo(c) = c U / N <= e for the c up to ((e + 1) N - 1) / U
+            P->more = a == 0 && e < steps ? (int)(((first + steps) * st.N - 1) / st.U - blockIdx.x) : 0;
+            P->split = split;
             P->begins = a == 0;
             P->ends = e == steps;
-            P->i0 = P->split ? 2 * a : a;
-            P->i1 = P->split ? min(2 * e, P->r.nk) : e;
-            P->first = first;
-            P->steps = steps;
-            ++number;
-            P->number = number;
+            P->over = 0;
             return true;
         }
+        P->over = 1;
         return false;
     }
 };
 
-// The first token in the window of a row at position `first`.
-__device__ __forceinline__ int first_seen(const PagedParams& A, int64_t first) {
-    const int64_t lo = A.window > 0 ? (first > 0 ? first : 0) - A.window + 1 : 0;
-    return (int)(lo < 0 ? 0 : lo < INT32_MAX ? lo : INT32_MAX);
-}
-// The tiles that rows at positions [first, last] see in full.
-struct Whole {
-    int end, window, sinks;      // tiles before `end` and from `window` on, or before `sinks`
-    __device__ __forceinline__ Whole(const PagedParams& A, int64_t first, int64_t last) {
-        end = (int)(first < 0 ? 0 : (first + 1) / kTile);
-        window = A.window > 0 && last >= A.window ? (int)((last - A.window) / kTile) + 1 : 0;
-        sinks = A.sinks / kTile;
-    }
-    __device__ __forceinline__ bool has(int tile) const { return tile < end && (tile >= window || tile < sinks); }
+// A role's place among the portions: waits for the next, reads it where it lies, and gives it back.
+struct Reader {
+    uint32_t number = 0;
+    __device__ __forceinline__ const Portion* next(Shared& S, unsigned long long wait_ns);
+    __device__ __forceinline__ void done(Shared& S);
 };
 
 // The registers of a role's threads; a group of four warps asks as one.
@@ -485,31 +515,55 @@ __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
     if ((w & E << 16) == E << 16) w &= 0x0000FFFFu;
     return w;
 }
+// 32 bytes, a whole sector, or two halves of it
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
+    if (wide) {
+        int32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (int32_t)w[j];
+        st_v8(static_cast<int32_t*>(p), v);
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
 // bits [0, n) of 32
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
 // ---- the kernel ------------------------------------------------------------
 
+__device__ __forceinline__ const Portion* Reader::next(Shared& S, unsigned long long wait_ns) {
+    int none = 0;
+    const uint32_t slot = number % kPortions;
+    if (!mbar_wait(&S.portion_full[slot], (number / kPortions) & 1, &none, wait_ns)) {
+        S.gave_up = 1;
+        return nullptr;
+    }
+    const Portion* P = &S.portion[slot];
+    return P->over ? nullptr : P;
+}
+// by one thread of a warp, behind the others
+__device__ __forceinline__ void Reader::done(Shared& S) { mbar_arrive(&S.portion_empty[number++ % kPortions]); }
+
 // Adds what the values' warps took out to the row's outputs [d0, d0 + 32): values that
 // are not finite of tokens that the row sees.
 template <class C, bool BITS8>
-__device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion P, int stream, int hi, int lo, int d0, float* o) {
-    const Whole whole(A, P.s.p0 + P.tok0, P.s.p0 + P.tok0 + P.ntok - 1);      // as the values' warps have it
+__device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion& P, int stream, int hi, int lo, int d0, float* o) {
     for (int i = P.i0; i < P.i1; ++i) {
         if (P.split && ((i - P.i0) & 1) != stream) continue;
-        const int tf = P.r.tile(i) * kTile;
-        if (whole.has(P.r.tile(i))) continue;
-        const int64_t id = __ldg(A.table + (int64_t)P.b * A.max_blocks + P.r.tile(i));
+        const int tile = P.r.tile(i);
+        if (P.item.has(tile)) continue;      // as the values' warps have it
+        const int64_t id = __ldg(A.table + (int64_t)P.b * A.max_blocks + tile);
         for (int c = 0; c < kTile; ++c) {
-            const int j = tf + c;
+            const int j = tile * kTile + c;
             const int64_t page = id * kPagesPerBlock + c / kSubPage;
             if (j > hi || (A.window > 0 && j < lo && j >= A.sinks) || page < 0 || page >= A.num_pages) continue;
             const int64_t at = ((page * kSubPage + c % kSubPage) * A.H + P.h) * A.D;
             for (int k = 0; k < 32 && d0 + k < A.D; ++k) {
                 float x;
                 if constexpr (BITS8) {
-                    const uint32_t c = __ldg(A.v + at + d0 + k);
-                    const uint32_t w = A.cache_dtype == BSA_DTYPE_E4M3 ? widen<true>(c) : widen<false>(c);
+                    const uint32_t code = __ldg(A.v + at + d0 + k);
+                    const uint32_t w = A.cache_dtype == BSA_DTYPE_E4M3 ? widen<true>(code) : widen<false>(code);
                     x = __low2float(*reinterpret_cast<const __half2*>(&w)) * __ldg(A.vs + page * A.H + P.h);
                 } else {
                     x = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(A.v) + at + d0 + k) << 16);
@@ -609,7 +663,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
     constexpr int RING = C::RING, PANELS = C::PANELS, NS = C::NS;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* qsm = smem;                             // [NS] query tiles
-    uint8_t* ring = qsm + NS * C::Q_TILE;            // [RING] stages of bf16 keys and values
+    uint8_t* ring = qsm + NS * C::Q_TILE;            // [RING] stages of keys and values of 16 bits
     uint8_t* codes = ring + RING * C::STAGE;         // [CRING] stages of codes
     Shared& S = *reinterpret_cast<Shared*>(codes + C::CRING * C::CODES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -623,8 +677,13 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_half[i], kRows);
             mbar_init(&S.p_full[i], kRows);
             mbar_init(&S.o_full[i], 1);
+        }
+        for (int i = 0; i < kPortions; ++i) {
+            mbar_init(&S.portion_full[i], 1);
+            mbar_init(&S.portion_empty[i], C::SOFTMAX + 1 + C::VALUE_WARPS);
         }
         mbar_init(&S.q_full, 1);
         mbar_init(&S.q_ready, 256);
@@ -632,7 +691,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         mbar_init(&S.to_fix, 1);
         mbar_init(&S.fixed, 64);
         mbar_init(&S.drained, 1);
-        for (int i = 0; i < 4; ++i) S.poison[i] = 0;
+        for (int i = 0; i < kPortions; ++i) S.poison[i] = 0;
         S.gave_up = 0;
         mbar_fence_init();
     }
@@ -653,19 +712,19 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
     __syncthreads();
     const uint32_t tmem = S.tmem_base;
     volatile int* quit = &S.gave_up;
+    Reader reader;
 
     if (warp == C::COPY) {
         take_registers<C::OTHERS, false>();
-        // ------------------------------------------------ copies
+        // ------------------------------------------------ portions and copies
         Walk<C> walk(A, S.start);
-        Portion P;
         // the ring that TMA fills: of codes or of bf16
         constexpr int N = BITS8 ? C::CRING : RING;
         uint64_t* const filled = BITS8 ? S.code_full : S.full;
         uint64_t* const drained = BITS8 ? S.code_empty : S.empty;
         uint8_t* const base = BITS8 ? codes : ring;
         constexpr int BYTES = BITS8 ? C::CODES : C::STAGE;
-        uint32_t st = 0, use = 0, issued = 0;
+        uint32_t st = 0, use = 0, issued = 0, tiles = 0, loads = 0;
         bool ok = true;
         const int outside = (int)(A.num_pages * kSubPage);       // past the tensor's end: arrives as zeros
         auto copy = [&](const CUtensorMap* map, int token, int h) {
@@ -673,7 +732,11 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             for (int p = 0; p < PANELS; ++p) {
                 ok = issued != A.stall && (use == 0 || mbar_wait(&drained[st], (use - 1) & 1, quit, A.wait_ns));
                 ok = __all_sync(kFull, ok);
-                if (ok && elect_one()) {
+                if (!ok) {
+                    S.gave_up = 1;
+                    return;
+                }
+                if (elect_one()) {
                     mbar_expect(&filled[st], BYTES);
                     if constexpr (BITS8) {
                         tma_load_3d(base + st * BYTES, map, p * C::PD, h, token, &filled[st]);
@@ -684,7 +747,6 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     }
                 }
                 __syncwarp();
-                if (!ok) return;
                 ++issued;
                 if (++st == N) {
                     st = 0;
@@ -692,27 +754,37 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 }
             }
         };
-        uint32_t tiles = 0, loads = 0;
-        while (ok && walk.next(A, &P)) {
-            const int64_t pos0 = P.s.p0 + P.tok0;
-            if (lane == 0 && P.begins)
-                report_status(A.status, pos0 + P.ntok > (int64_t)A.max_blocks * kTile, BSA_STATUS_BAD_CONTEXT);
-            if (P.i0 == P.i1) continue;
+        for (uint32_t number = 0;; ++number) {
+            // also when a wait has run out: the softmax warps fill the rows that are left with NaN
+            const uint32_t slot = number % kPortions;
+            int none = 0;
+            if (number >= kPortions && !mbar_wait(&S.portion_empty[slot], (number / kPortions - 1) & 1, &none, A.wait_ns)) break;
+            Portion& P = S.portion[slot];
+            bool more = false;
+            if (lane == 0) more = walk.next(A, S.start, &P);
+            more = __shfl_sync(kFull, more, 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.portion_full[slot]);
+            if (!more) break;
+            if (lane == 0 && P.begins) report_status(A.status, P.pos0 + P.tokens > (int64_t)A.max_blocks * kTile, BSA_STATUS_BAD_CONTEXT);
+            const int i0 = P.i0, i1 = P.i1, n = i1 - i0, b = P.b, h = P.h;
+            if (n == 0 || !ok) continue;
             ok = loads == 0 || mbar_wait(&S.q_empty, (loads - 1) & 1, quit, A.wait_ns);
             ok = __all_sync(kFull, ok);
-            if (!ok) break;
+            if (!ok) continue;
             ++loads;
-            const int mtiles = P.ntok > A.tokens ? 2 : 1;
+            const int mtiles = P.tokens > A.tokens ? 2 : 1;
             if (elect_one()) {
                 mbar_expect(&S.q_full, mtiles * (C::Q_TILE / kRows) * A.tokens * A.G);
                 for (int m = 0; m < mtiles; ++m)
                     for (int a = 0; a < C::D / 64; ++a)
-                        tma_load_4d(qsm + m * C::Q_TILE + a * kAtom, &M.q, a * 64, 0, P.h, (int)(P.s.t0 + P.tok0 + m * A.tokens), &S.q_full);
+                        tma_load_4d(qsm + m * C::Q_TILE + a * kAtom, &M.q, a * 64, 0, h, (int)(P.row0 + m * A.tokens), &S.q_full);
             }
             __syncwarp();
+            const Range r = P.r;
+            const int32_t* table = A.table + (int64_t)b * A.max_blocks;
             int32_t ids = 0;      // of 32 tiles
             int before = 0;       // the last tile's token coordinate
-            const int n = P.i1 - P.i0;
             const bool ahead = NS == 1 || P.split;       // keys run one tile ahead of values
             // 8 bits: scales of two tiles, lanes 0 to 15 and 16 to 31, the pages' for keys, then for
             // values; read two tiles ahead, as they may come from DRAM
@@ -722,15 +794,14 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 const int id = __shfl_sync(kFull, ids, t & 31);
                 scale = 0.f;
                 if (t >= n || id < 0 || (int64_t)id * kPagesPerBlock + pg >= A.num_pages) return;
-                const int64_t where = ((int64_t)id * kPagesPerBlock + pg) * A.H + P.h;
+                const int64_t where = ((int64_t)id * kPagesPerBlock + pg) * A.H + h;
                 scale = lane & 8 ? log2f(__ldg(A.vs + where)) : __ldg(A.ks + where) * A.scale_log2e;
             };
-            for (int i = P.i0; ok && i <= P.i1; ++i) {
+            for (int k = 0; ok && k <= n; ++k) {
                 int at = 0;
-                if (i < P.i1) {
-                    const int k = i - P.i0;
+                if (k < n) {
                     if ((k & 31) == 0) {
-                        ids = i + lane < P.i1 ? __ldg(A.table + (int64_t)P.b * A.max_blocks + P.r.tile(i + lane)) : -1;
+                        ids = k + lane < n ? __ldg(table + r.tile(i0 + k + lane)) : -1;
                         if constexpr (BITS8) read_scales(k);
                     }
                     const int id = __shfl_sync(kFull, ids, k & 31);
@@ -738,9 +809,9 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     const int valid = (int)(left < 0 ? 0 : left < kTile ? left : kTile);
                     at = valid > 0 ? id * kTile : outside;
                     if (lane == 0) {
-                        const int t = P.r.tile(i), tf = t * kTile;
-                        int need = min(kTile, P.r.end - tf);
-                        if (A.window > 0 && t < P.r.wst) need = min(need, A.sinks - tf);
+                        const int t = r.tile(i0 + k), tf = t * kTile;
+                        int need = min(kTile, r.end - tf);
+                        if (A.window > 0 && t < r.wst) need = min(need, A.sinks - tf);
                         report_status(A.status, valid < need, BSA_STATUS_BAD_BLOCK_ID);
                         S.valid[(tiles + k) % kInfo] = valid;
                     }
@@ -751,13 +822,13 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         }
                     }
                     __syncwarp();
-                    copy(&M.k, at, P.h);
-                    if (!ahead && ok) copy(&M.v, at, P.h);
+                    copy(&M.k, at, h);
+                    if (!ahead && ok) copy(&M.v, at, h);
                 }
-                if (ahead && i > P.i0 && ok) copy(&M.v, before, P.h);
+                if (ahead && k > 0 && ok) copy(&M.v, before, h);
                 before = at;
             }
-            tiles += P.i1 - P.i0;
+            tiles += n;
         }
         // copies in flight land before the CTA's memory goes away, also when nobody waits
         // for them any more
@@ -768,8 +839,6 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         take_registers<C::OTHERS, false>();
         // ------------------------------------------------ MMAs
         if (elect_one()) {
-            Walk<C> walk(A, S.start);
-            Portion P;
             const uint64_t q_desc = smem_desc(smem_addr(qsm), 0, 1024, 2);
             const uint64_t k_desc = smem_desc(smem_addr(ring), 0, 1024, 2);
             const uint64_t v_desc = smem_desc(smem_addr(ring), kAtom, 1024, 2);
@@ -795,53 +864,61 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     mma_f16(tmem + buf * kTile, qd + at, kd + at, A.s_idesc, p + k > 0);
                 }
             };
-            // outputs of the probabilities in `buf` and a value stage
-            auto outputs = [&](int buf, int o, int p, uint32_t s, bool more) {
+            // outputs of half the probabilities in `buf` (tokens 0 to 63, or 64 to 127) and a value stage
+            auto outputs = [&](int half, int buf, int o, int p, uint32_t s, bool more) {
                 const uint64_t vd = v_desc + s * (C::STAGE / 16);
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
+                for (int k = half * 4; k < half * 4 + 4; ++k)
                     mma_f16_ts(tmem + C::O_COL + o * C::D + p * C::PD, tmem + buf * kTile + k * 8, vd + k * 128, A.o_idesc, more || k > 0);
             };
-            auto probabilities = [&](int buf) {
-                wait(&S.p_full[buf], (p_phase >> buf) & 1);
-                p_phase ^= 1u << buf;
+            auto probabilities = [&](uint64_t* bar, int buf) {
+                wait(&bar[buf], (p_phase >> buf) & 1);
                 tc_fence_after();
             };
-            while (ok && walk.next(A, &P)) {
-                const int n = P.i1 - P.i0;
-                if (n == 0) continue;
-                const Whole seen_whole(A, P.s.p0 + P.tok0, P.s.p0 + P.tok0 + P.ntok - 1);
-                wait(BITS8 ? &S.q_ready : &S.q_full, loads & 1);
-                tc_fence_after();
-                ++loads;
+            while (const Portion* at = reader.next(S, A.wait_ns)) {
+                const Portion& P = *at;
+                const int n = P.i1 - P.i0, i0 = P.i0;
                 // bf16: tiles that some rows do not see in full pass through the values' warps,
                 // while their probabilities are formed
-                auto partly = [&](int i) { return !BITS8 && !seen_whole.has(P.r.tile(i)); };
+                auto partly = [&](int k) { return !BITS8 && !P.item.has(P.r.tile(i0 + k)); };
                 auto fixed = [&]() {
                     wait(&S.fixed, fixes & 1);
                     ++fixes;
                 };
-                if (NS == 2 && !P.split) {
+                if (ok && n > 0) {
+                    wait(BITS8 ? &S.q_ready : &S.q_full, loads & 1);
+                    tc_fence_after();
+                    ++loads;
+                }
+                if (n == 0 || !ok) {
+                    // nothing to do
+                } else if (NS == 2 && !P.split) {
                     take(st, use);
-                    if (!ok) break;
-                    for (int s = 0; s < 2; ++s) {
-                        scores(s, s, 0, st);
-                        tc_commit(&S.s_full[s]);
+                    if (ok) {
+                        for (int s = 0; s < 2; ++s) {
+                            scores(s, s, 0, st);
+                            tc_commit(&S.s_full[s]);
+                        }
+                        tc_commit(&S.empty[st]);
+                        if (n == 1) tc_commit(&S.q_empty);
+                        step(st, use);
                     }
-                    tc_commit(&S.empty[st]);
-                    if (n == 1) tc_commit(&S.q_empty);
-                    step(st, use);
-                    for (int i = P.i0; ok && i < P.i1; ++i) {
-                        const bool next = i + 1 < P.i1, fix = partly(i);
+                    for (int k = 0; ok && k < n; ++k) {
+                        const bool next = k + 1 < n, fix = partly(k);
                         uint32_t ks = st, ku = use;
                         step(ks, ku);
                         take(st, use);
                         if (ok && fix) mbar_arrive(&S.to_fix);
+#pragma unroll 1
                         for (int s = 0; s < 2; ++s) {
-                            probabilities(s);
+                            probabilities(S.p_half, s);
                             if (fix && s == 0) fixed();
                             if (!ok) break;
-                            outputs(s, s, 0, st, i > P.i0);
+                            outputs(0, s, s, 0, st, k > 0);
+                            probabilities(S.p_full, s);
+                            if (!ok) break;
+                            p_phase ^= 1u << s;
+                            outputs(1, s, s, 0, st, true);
                             if (s == 1) tc_commit(&S.empty[st]);
                             if (next) {
                                 if (s == 0) take(ks, ku);
@@ -850,7 +927,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                                 tc_commit(&S.s_full[s]);
                                 if (s == 1) {
                                     tc_commit(&S.empty[ks]);
-                                    if (i + 2 == P.i1) tc_commit(&S.q_empty);
+                                    if (k + 2 == n) tc_commit(&S.q_empty);
                                 }
                             } else {
                                 tc_commit(&S.o_full[s]);
@@ -860,7 +937,8 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         if (next) step(st, use);
                     }
                 } else {
-                    // keys one tile ahead (with two streams: of each stream)
+                    // Keys one tile ahead (with two streams: of each stream).  With one stream the buffer of
+                    // tile k + 1 was read by the product of tile k - 1, issued before.
                     auto keys = [&](int k) {
                         const int buf = NS == 2 ? k & 1 : (nq + k) & 1;
 #pragma unroll
@@ -874,37 +952,44 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         tc_commit(&S.s_full[buf]);
                         if (k + 1 == n) tc_commit(&S.q_empty);
                     };
-                    keys(0);
+                    int asked = 0;      // tiles whose scores are issued
+#pragma unroll 1
                     for (int k = 0; ok && k < n; ++k) {
-                        const int buf = NS == 2 ? k & 1 : (nq + k) & 1;
-                        if (k + 1 < n && (NS == 1 || k == 0)) keys(k + 1);
+#pragma unroll 1
+                        for (; ok && asked < n && asked <= k + 1; ++asked) keys(asked);
                         if (!ok) break;
-                        const bool fix = partly(P.i0 + k);
+                        const int buf = NS == 2 ? k & 1 : (nq + k) & 1;
+                        const bool fix = partly(k);
                         uint32_t vs = st, vu = use;
                         for (int p = 0; p < PANELS; ++p) {
                             take(vs, vu);
                             step(vs, vu);
                         }
                         if (ok && fix) mbar_arrive(&S.to_fix);
-                        probabilities(buf);
-                        if (fix) fixed();
-                        if (!ok) break;
+#pragma unroll 1
+                        for (int half = 0; ok && half < 2; ++half) {
+                            probabilities(half == 0 ? S.p_half : S.p_full, buf);
+                            if (fix && half == 0) fixed();
+                            if (!ok) break;
+                            vs = st;
+                            vu = use;
 #pragma unroll
-                        for (int p = 0; p < PANELS; ++p) {
-                            outputs(buf, NS == 2 ? buf : 0, p, st, k >= NS);
-                            tc_commit(&S.empty[st]);
-                            step(st, use);
+                            for (int p = 0; p < PANELS; ++p) {
+                                outputs(half, buf, NS == 2 ? buf : 0, p, vs, k >= NS || half > 0);
+                                if (half == 1) tc_commit(&S.empty[vs]);
+                                step(vs, vu);
+                            }
                         }
-                        if (NS == 1) {
-                            tc_commit(&S.o_full[0]);
-                        } else if (k + 2 < n) {
-                            keys(k + 2);
-                        } else {
-                            tc_commit(&S.o_full[buf]);
-                        }
+                        if (!ok) break;
+                        p_phase ^= 1u << buf;
+                        st = vs;
+                        use = vu;
+                        if (NS == 1) tc_commit(&S.o_full[0]);
+                        else if (k + 2 >= n) tc_commit(&S.o_full[buf]);
                     }
                     if (NS == 1) nq += n;
                 }
+                reader.done(S);
             }
             // no MMA runs on into the release of its memory
             int none = 0;
@@ -914,59 +999,49 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         __syncwarp();
     } else if (warp >= C::VALUES) {
         take_registers<C::OTHERS, false>();
-        // ------------------------------------------------ values, and codes to bf16
-        Walk<C> walk(A, S.start);
-        Portion P;
+        // ------------------------------------------------ values, and codes to halves
         const int me = (tid - C::VALUES * 32) % C::VALUE_THREADS, group = (warp - C::VALUES) / 4;
         bool ok = true;
-        if constexpr (!BITS8) {
-            uint32_t st = 0, use = 0, fixes = 0;      // stages so far
-            while (ok && walk.next(A, &P)) {
-                const int n = P.i1 - P.i0;
-                const int64_t first = P.s.p0 + P.tok0;
-                const Whole whole(A, first, first + P.ntok - 1);
-                const int lo = first_seen(A, first);
-                bool odd = false;
-                const bool ahead = NS == 1 || P.split;
+        uint32_t st = group, use = 0, cst = group, cuse = 0, stages = 0, fixes = 0, loads = 0;
+        while (const Portion* at = reader.next(S, A.wait_ns)) {
+            const Portion& P = *at;
+            const int n = P.i1 - P.i0;
+            const bool ahead = NS == 1 || P.split;
+            // sets a stage of the tile's values right where some row of the item does not see it in full
+            auto clean = [&](uint8_t* stage, int tile) {
+                const int end = P.r.end, lo = P.lo;
+                const bool odd = clean_stage<C, BITS8>(stage, me, [&](int row) {
+                    const int j = tile * kTile + row;
+                    return j < end && (j >= lo || j < A.sinks);
+                });
+                if (odd) *(volatile int*)&S.poison[P.number % kPortions] = P.number + 1;
+            };
+            if constexpr (!BITS8) {
                 for (int i = 0; ok && i < n; ++i) {
                     const int tile = P.r.tile(P.i0 + i);
-                    if (whole.has(tile)) continue;
+                    if (P.item.has(tile)) continue;
                     // K and V stages in the copies' order: those before this tile's values
                     const uint32_t s0 = st + (ahead ? min(i + 2, n) + i : 2 * i + 1) * PANELS;
                     // the MMAs' thread has them in the ring, and waits
                     ok = mbar_wait(&S.to_fix, fixes & 1, quit, A.wait_ns);
-                    ok = __all_sync(kFull, ok);
                     ++fixes;
-                    for (int p = 0; ok && p < PANELS; ++p) {
+                    for (int p = 0; p < PANELS; ++p) {
                         const uint32_t s = (s0 + p) % RING, u = use + (s0 + p) / RING;
-                        ok = mbar_wait(&S.full[s], u & 1, quit, A.wait_ns);
+                        ok = ok && mbar_wait(&S.full[s], u & 1, quit, A.wait_ns);
                         ok = __all_sync(kFull, ok);
-                        if (!ok) break;
-                        odd |= clean_stage<C, false>(ring + s * C::STAGE, me, [&](int row) {
-                            const int j = tile * kTile + row;
-                            return j < P.r.end && (j >= lo || j < A.sinks);
-                        });
+                        if (ok) clean(ring + s * C::STAGE, tile);
                     }
                     if (!ok) break;
-                    if (odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
                     fence_async_smem();
                     mbar_arrive(&S.fixed);
                 }
                 const uint32_t total = st + 2 * n * PANELS;
                 use += total / RING;
                 st = total % RING;
-            }
-        } else {
-            // the two groups take stages in turn, each the ring's every other
-            uint32_t cst = group, cuse = 0, st = group, use = 0, stages = 0, loads = 0;
-            while (ok && walk.next(A, &P)) {
-                const int n = P.i1 - P.i0;
-                if (n == 0) continue;
-                const int64_t first = P.s.p0 + P.tok0;
-                const Whole whole(A, first, first + P.ntok - 1);
-                const int lo = first_seen(A, first);
-                bool odd = false, queries = false;
-                const bool ahead = NS == 1 || P.split;
+            } else {
+                // the two groups take stages in turn, each the ring's every other
+                bool queries = false;
+#pragma unroll 1
                 for (int q = (stages & 1) != group; ok && q < 2 * n * PANELS; q += 2) {
                     // the copies' order: K V K V ..., or K K V K V ... V V
                     const int i = q / PANELS;
@@ -982,13 +1057,9 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     else widen_stage<C, false>(from, to, me);
                     if (value) {
                         const int tile = P.r.tile(P.i0 + k);
-                        if (!whole.has(tile)) {
+                        if (!P.item.has(tile)) {
                             asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
-                            odd |= clean_stage<C, true>(to, me, [&](int row) {
-                                const int j = tile * kTile + row;
-                                return j < P.r.end && (j >= lo || j < A.sinks);
-                            });
-                            if (odd) *(volatile int*)&S.poison[P.number & 3] = P.number + 1;
+                            clean(to, tile);
                         }
                     }
                     mbar_arrive(&S.code_empty[cst]);
@@ -1010,8 +1081,8 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         ok = mbar_wait(&S.q_full, loads & 1, quit, A.wait_ns);
                         ok = __all_sync(kFull, ok);
                         if (!ok) break;
-                        const int m = P.ntok > A.tokens ? group : 0;
-                        const int rows = min(A.tokens, P.ntok - m * A.tokens) * A.G;
+                        const int m = P.tokens > A.tokens ? group : 0;
+                        const int rows = min(A.tokens, P.tokens - m * A.tokens) * A.G;
                         if (me < rows && (m == group || group == 0)) S.q_power[loads & 1][m][me] = (uint8_t)halve_row<C>(qsm + m * C::Q_TILE, me);
                         fence_async_smem();
                         mbar_arrive(&S.q_ready);
@@ -1020,40 +1091,43 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 }
                 stages += 2 * n * PANELS;
             }
+            __syncwarp();
+            if (lane == 0) reader.done(S);
+            else ++reader.number;
         }
     } else if (warp >= C::SOFTMAX) {
         take_registers<C::OTHERS, false>();      // warps without work, of a group of four
     } else {
         take_registers<C::MINE, true>();
         // ------------------------------------------------ softmax and output
-        Walk<C> walk(A, S.start);
-        Portion P;
         const int stream = warp >> 2, row = tid & 127, token = row / A.G;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const uint32_t o_addr = lanes + C::O_COL + stream * C::D;
-        uint32_t s_phase = 0, o_phase = 0, tiles = 0, nq = 0, loads = 0;      // loads: of queries
+        uint32_t s_phase = 0, o_phase = 0, tiles = 0, nq = 0;
         bool ok = true, left_head = false;
-        while (walk.next(A, &P)) {
+        while (const Portion* at = reader.next(S, A.wait_ns)) {
+            const Portion& P = *at;
             const int n = P.i1 - P.i0;
             const int m = NS == 2 && !P.split ? stream : 0;              // its query tile
-            const int mine = min(A.tokens, P.ntok - m * A.tokens);       // tokens of it
+            const int mine = min(A.tokens, P.tokens - m * A.tokens);     // tokens of it
             const bool valid = row < A.tokens * A.G && token < mine;
             const bool live = __any_sync(kFull, valid);
-            const int64_t first = P.s.p0 + P.tok0 + m * A.tokens, last = first + mine - 1;
-            const int64_t pos = valid ? first + token : last;            // rows beyond do as the last
-            const int64_t top = (int64_t)A.max_blocks * kTile;
-            const int hi = (int)(pos < 0 ? -1 : pos < top ? pos : top - 1);
-            const int lo = A.window > 0 ? (int)(pos - A.window + 1 < 0 ? 0 : pos - A.window + 1 < top ? pos - A.window + 1 : top) : 0;
-            const Whole seen_whole(A, first, last);
+            int hi, lo;                                                  // the last token that the row sees, its window's first
+            {
+                const int64_t first = P.pos0 + m * A.tokens, pos = valid ? first + token : first + mine - 1;   // rows beyond do as the last
+                const int64_t top = (int64_t)A.max_blocks * kTile;
+                hi = (int)(pos < 0 ? -1 : pos < top ? pos : top - 1);
+                lo = A.window > 0 ? (int)(pos - A.window + 1 < 0 ? 0 : pos - A.window + 1 < top ? pos - A.window + 1 : top) : 0;
+            }
             // The row's sums are in units of 2^mx and its outputs in units of 2^mo: with bf16 the same; with 8
             // bits mo goes by the largest probability times value scale, so that those are halves of
             // 11 bits in either's place, whatever the scales of pages that do not count.
             float mx = -INFINITY, mo = -INFINITY, l[4] = {};
             bool written = false;                                        // O holds something
             const int stride = P.split ? 2 : 1;
-            for (int k = P.split ? stream : 0; k < n; k += stride) {
+            for (int k = P.split ? stream : 0; ok && k < n; k += stride) {
                 const int buf = NS == 2 ? stream : (nq + k) & 1;
-                ok = ok && mbar_wait(&S.s_full[buf], (s_phase >> buf) & 1, quit, A.wait_ns);
+                ok = mbar_wait(&S.s_full[buf], (s_phase >> buf) & 1, quit, A.wait_ns);
                 s_phase ^= 1u << buf;
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
@@ -1069,19 +1143,19 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     settled = true;
                 };
                 if (live) {
-                    const int tf = P.r.tile(P.i0 + k) * kTile, slot = (tiles + k) % kInfo;
+                    const int tile = P.r.tile(P.i0 + k), slot = (tiles + k) % kInfo;
                     const int inside = S.valid[slot];
-                    const bool whole = inside == kTile && seen_whole.has(P.r.tile(P.i0 + k));
+                    const bool whole = inside == kTile && P.tile[m].has(tile);
                     const uint32_t s_addr = lanes + buf * kTile;
                     constexpr int N = BITS8 ? 2 : 4;      // chunks of 32 columns in registers
                     float x[N][32];
-                    const float qs = BITS8 ? __uint_as_float((uint32_t)S.q_power[loads & 1][m][row] << 23) : 1.f;
+                    const float qs = BITS8 ? __uint_as_float((uint32_t)S.q_power[P.loads & 1][m][row] << 23) : 1.f;
                     // what page p's scores are multiplied by
                     auto key_scale = [&](int p) { return S.scale[slot][0][p] * qs; };
                     // chunk c of the row's scores: hidden ones are -inf (with 8 bits after their scale, as that
                     // may be zero)
                     auto hide = [&](int c, float (&v)[32]) {
-                        const int from = tf + 32 * c;
+                        const int from = tile * kTile + 32 * c;
                         uint32_t seen = low_bits(min(hi + 1 - from, inside - 32 * c));
                         if (A.window > 0) seen &= ~low_bits(lo - from) | low_bits(A.sinks - from);
 #pragma unroll
@@ -1157,46 +1231,57 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     }
                     const float base = mx == -INFINITY ? 0.f : -mx;
                     const float unit = mo == -INFINITY ? -INFINITY : mx - mo;
-                    // the probabilities of chunks [c0, c0 + N) in x, to the scores' place
-                    auto turn = [&](int c0) {
+                    // the probabilities of chunk c0 + c, to the scores' place
+                    auto turn = [&](int c0, int c) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int c = 0; c < N; ++c) {
-                            uint32_t w[16];
+                        for (int g = 0; g < 2; ++g) {
+                            const int page = 2 * (c0 + c) + g;
+                            const float k = !BITS8 ? A.scale_log2e : whole ? key_scale(page) : 1.f;
+                            const float v = BITS8 ? ex2(S.scale[slot][1][page] + unit) : 1.f;
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                const int page = 2 * (c0 + c) + g;
-                                const float k = !BITS8 ? A.scale_log2e : whole ? key_scale(page) : 1.f;
-                                const float v = BITS8 ? ex2(S.scale[slot][1][page] + unit) : 1.f;
-#pragma unroll
-                                for (int j = 16 * g; j < 16 * g + 16; j += 2) {
-                                    float a, b;
-                                    fma2(a, b, x[c][j], x[c][j + 1], k, k, base, base);
-                                    a = ex2(a);
-                                    b = ex2(b);
-                                    add2(l[c % 2 * 2], l[c % 2 * 2 + 1], a, b);
-                                    if constexpr (BITS8) {
-                                        mul2(a, b, v);
-                                        w[j / 2] = pack_half(a, b);
-                                    } else {
-                                        w[j / 2] = pack_bf16(a, b);
-                                    }
+                            for (int j = 16 * g; j < 16 * g + 16; j += 2) {
+                                float a, b;
+                                fma2(a, b, x[c][j], x[c][j + 1], k, k, base, base);
+                                a = ex2(a);
+                                b = ex2(b);
+                                add2(l[c % 2 * 2], l[c % 2 * 2 + 1], a, b);
+                                if constexpr (BITS8) {
+                                    mul2(a, b, v);
+                                    w[j / 2] = pack_half(a, b);
+                                } else {
+                                    w[j / 2] = pack_bf16(a, b);
                                 }
                             }
-                            tmem_st16(s_addr + 16 * (c0 + c), w);
                         }
+                        tmem_st16(s_addr + 16 * (c0 + c), w);
+                    };
+                    // the product of the first 64 tokens starts under the others' exponentials
+                    auto half_done = [&]() {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(&S.p_half[buf]);
                     };
                     if constexpr (BITS8) {
 #pragma unroll 1
                         for (int c0 = 0; c0 < 4; c0 += 2) {
                             // the lower half is there; the upper was not touched by its probabilities
                             if (c0 > 0) fetch(c0);
-                            turn(c0);
+                            turn(c0, 0);
+                            turn(c0, 1);
+                            if (c0 == 0) half_done();
                         }
                     } else {
-                        turn(0);
+                        turn(0, 0);
+                        turn(0, 1);
+                        half_done();
+                        turn(0, 2);
+                        turn(0, 3);
                     }
                     tmem_wait_st();
                     written = true;
+                } else {
+                    mbar_arrive(&S.p_half[buf]);
                 }
                 settle();
                 if (NS == 1) o_phase ^= 1;      // as many products as tiles
@@ -1205,7 +1290,6 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             }
             if (NS == 1) nq += n;
             tiles += n;
-            loads += n > 0;
             // ---- the portion's result
             const bool any = n > (P.split ? stream : 0);
             if (NS == 1) {
@@ -1219,7 +1303,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             float sum = (l[0] + l[1]) + (l[2] + l[3]);
             if constexpr (!BITS8) mo = mx;
             if (!ok) mx = mo = sum = NAN;
-            const bool odd = any && S.poison[P.number & 3] == P.number + 1;
+            const bool odd = any && S.poison[P.number % kPortions] == P.number + 1;
             // 32 of the row's outputs, not yet divided by the sum
             auto result = [&](int c, float (&o)[32]) {
                 if (ok && any && live) {
@@ -1262,30 +1346,22 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             // from the outputs' unit to the sums', in two factors where it may pass the range of one
             const float back = BITS8 && whole_item && mo > -INFINITY ? ex2(0.5f * (mo - mx)) : 1.f;
             const float scale = whole_item ? (sum == 0.f ? 0.f : back / sum) : 1.f;
-            const int64_t t = P.s.t0 + P.tok0 + m * A.tokens + token;
+            const int64_t t = P.row0 + m * A.tokens + token;
             uint16_t* out = A.out + ((t * A.H + P.h) * A.G + row % A.G) * A.D;
-            const int64_t slot = (int64_t)blockIdx.x * 2 + (P.begins ? 1 : 0);
-            const int part_row = m * kRows + row;
+            const int64_t part_row = ((int64_t)blockIdx.x * 2 + (P.begins ? 1 : 0)) * A.part_rows + m * kRows + row;
             const bool writes = valid && (stream == 0 || !P.split);
-            if (!whole_item && writes) A.sums[slot * A.part_rows + part_row] = make_float4(mx, sum, mo, 0.f);
-            float* part = A.parts + (slot * A.part_rows + part_row) * A.D;
-            if (!whole_item && P.begins && tid == 0) {
-                PartHead head;
-                head.row0 = P.s.t0 + P.tok0;
-                head.tokens = P.ntok;
-                head.h = P.h;
-                // the CTA of the item's last step: lo(c) = c U / N <= e for the c up to ((e + 1) N - 1) / U
-                head.more = (int32_t)(((P.first + P.steps) * S.start.N - 1) / S.start.U - blockIdx.x);
-                head.pad = 0;
-                A.heads[blockIdx.x] = head;
+            if (!whole_item && writes) A.sums[part_row] = make_float4(mx, sum, mo, 0.f);
+            float* part = A.parts + part_row * A.D;
+            if (P.more > 0 && tid == 0) {
+                A.heads[blockIdx.x] = PartHead{P.row0, P.tokens, P.h, P.more, 0};
                 left_head = true;
             }
-#pragma unroll
+#pragma unroll 1
             for (int half = 0; half < (NS == 2 ? 2 : 1); ++half) {
                 constexpr int CH = C::D / 32 / (NS == 2 ? 2 : 1);      // chunks of 32 a half
                 if (NS == 2 && join) {
                     if (stream == 1) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < CH; ++c) {
                             float o[32];
                             result(half * CH + c, o);
@@ -1296,7 +1372,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     asm volatile("bar.sync 1, 256;" ::: "memory");
                 }
                 if (live && (stream == 0 || !P.split)) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < CH; ++c) {
                         const int d0 = (half * CH + c) * 32;
                         float o[32];
@@ -1307,20 +1383,19 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         }
                         if (!writes) continue;
                         if (whole_item) {
-                            if constexpr (BITS8) {
+                            uint32_t w[16];
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] *= back;
+                            for (int j = 0; j < 16; ++j) {
+                                const float b = BITS8 ? back : 1.f;
+                                w[j] = pack_bf16(o[2 * j] * b * scale, o[2 * j + 1] * b * scale);
                             }
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8)
-                                if (d0 + j < A.D)
-                                    *reinterpret_cast<uint4*>(out + d0 + j) =
-                                        make_uint4(pack_bf16(o[j] * scale, o[j + 1] * scale), pack_bf16(o[j + 2] * scale, o[j + 3] * scale),
-                                                   pack_bf16(o[j + 4] * scale, o[j + 5] * scale), pack_bf16(o[j + 6] * scale, o[j + 7] * scale));
+                            for (int j = 0; j < 2; ++j)
+                                if (d0 + 16 * j < A.D) store32(out + d0 + 16 * j, &w[8 * j], A.wide_out);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                if (d0 + j < A.D) *reinterpret_cast<float4*>(part + d0 + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                            for (int j = 0; j < 4; ++j)
+                                if (d0 + 8 * j < A.D) store32(part + d0 + 8 * j, reinterpret_cast<const uint32_t*>(&o[8 * j]), true);
                         }
                     }
                 }
@@ -1331,6 +1406,9 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             }
             tc_fence_before();
             if (P.split && tid == 0 && n > 0) mbar_arrive(&S.q_empty);
+            __syncwarp();
+            if (lane == 0) reader.done(S);
+            else ++reader.number;
         }
         if (tid == 0 && !left_head) A.heads[blockIdx.x].more = 0;
         if (tid == 0) report_status(A.status, S.gave_up != 0, BSA_STATUS_TIMEOUT);
@@ -1518,6 +1596,7 @@ int launch_paged(const bsa_paged_attention_args_t& a, PagedParams& A, cudaStream
     // a scale of zero must not meet the -inf of hidden scores; any tiny one has its result
     const float scale = fabsf(a.scale) * 1.44269504f;
     A.scale_log2e = scale == 0.f ? 1e-30f : scale;
+    A.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     A.s_idesc = f16_idesc(!bits8, a.scale < 0.f, false, kRows, kTile);
     A.o_idesc = f16_idesc(!bits8, false, true, kRows, a.D <= 64 ? 64 : 128);
     A.parts = reinterpret_cast<float*>(ws);
