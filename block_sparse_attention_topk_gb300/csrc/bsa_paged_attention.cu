@@ -183,7 +183,6 @@ struct Shared {
     Portion portion[kPortions];
     int poison[kPortions];                     // 1 + the number of the last portion with values that are not finite
     uint8_t q_power[2][2][kRows];              // 8 bits: the exponent (by 127) of what a row of queries was divided by, of two portions
-    long long total;
     Start start;
     uint32_t tmem_base;
     int gave_up;
@@ -297,64 +296,69 @@ __device__ __forceinline__ long long warp_before(long long v) {
     return x - v;
 }
 
-// This CTA's part of the units, and the item in which it begins.  `units`: kWindow words.
+// x * y / z, of numbers that mostly fit in 32 bits.
+__device__ __forceinline__ int64_t mul_div(int64_t x, int64_t y, int64_t z) {
+    const int64_t p = x * y;
+    return p < INT32_MAX && z < INT32_MAX ? (int32_t)p / (int32_t)z : p / z;
+}
+
+// This CTA's part of the units, and the item in which it begins.  `units`: kWindow words.  One
+// request on its own waits for this: up to kWindow sequences take two barriers.
 template <class C>
 __device__ void find_start(const PagedParams& A, Shared& S, long long* units) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int EACH = kWindow / 32;
     long long all = 0;
     for (int b0 = 0; b0 < A.num_reqs; b0 += kWindow) {
         const int n = min(kWindow, A.num_reqs - b0);
+        if (b0 > 0) __syncthreads();
         count_units<C>(A, units, b0, n);
         if (warp == 0) {
             long long v = 0;
             for (int i = lane; i < n; i += 32) v += units[i];
-            v = warp_sum(v);
-            if (lane == 0) S.total = v;
+            all += warp_sum(v);
         }
-        __syncthreads();
-        all += S.total;
-        __syncthreads();
     }
-    const int64_t U = all * A.H;
-    int64_t N = U / A.min_units;
-    N = N < 1 ? 1 : N < gridDim.x ? N : gridDim.x;
-    const int64_t c = blockIdx.x;
-    const int64_t lo = c < N ? c * U / N : 0, hi = c < N ? (c + 1) * U / N : 0;
-    if (threadIdx.x == 0) {
-        S.start = Start{lo, hi, 0, U, N, 0, 0, 0};
+    if (warp == 0 && lane == 0) {
+        const int64_t U = all * A.H;
+        int64_t N = mul_div(U, 1, A.min_units);
+        N = N < 1 ? 1 : N < gridDim.x ? N : gridDim.x;
+        const int64_t c = blockIdx.x;
+        S.start = Start{c < N ? mul_div(c, U, N) : 0, c < N ? mul_div(c + 1, U, N) : 0, 0, U, N, 0, 0, 0};
     }
-    __syncthreads();
-    if (lo >= hi) return;
+    if (A.num_reqs > kWindow) __syncthreads();
+    else __syncwarp();
     long long before = 0;      // of the sequences so far, all heads
     for (int b0 = 0; b0 < A.num_reqs; b0 += kWindow) {
         const int n = min(kWindow, A.num_reqs - b0);
-        if (A.num_reqs > kWindow) count_units<C>(A, units, b0, n);
+        if (A.num_reqs > kWindow) {
+            __syncthreads();
+            count_units<C>(A, units, b0, n);
+        }
         if (warp == 0) {
-            constexpr int EACH = kWindow / 32;
+            const int64_t lo = S.start.lo;
             long long mine = 0;
-            for (int i = 0; i < EACH; ++i)
-                if (lane * EACH + i < n) mine += units[lane * EACH + i];
+            if (n <= 32) {
+                if (lane < n) mine = units[lane];
+            } else {
+                for (int i = 0; i < EACH; ++i)
+                    if (lane * EACH + i < n) mine += units[lane * EACH + i];
+            }
             long long at = before + warp_before(mine) * A.H;
-            const bool here = at <= lo && lo < at + mine * A.H;
-            if (here) {
-                int i = lane * EACH;
+            if (lo < S.start.hi && at <= lo && lo < at + mine * A.H) {
+                int i = n <= 32 ? lane : lane * EACH;
                 while (lo >= at + units[i] * A.H) at += units[i++] * A.H;
                 S.start.b = b0 + i;
-                S.start.h = (int32_t)((lo - at) / units[i]);
+                S.start.h = (int32_t)mul_div(lo - at, 1, units[i]);
                 S.start.first = at + S.start.h * units[i];      // of the head's items
             }
-            const long long sum = warp_sum(mine);
-            const bool found = __any_sync(kFull, here);
-            if (lane == 0) S.total = found ? -1 : sum;
+            before += warp_sum(mine) * A.H;
         }
-        __syncthreads();
-        const long long t = S.total;
-        __syncthreads();
-        if (t < 0) break;
-        before += t * A.H;
     }
     // the item among the head's
-    if (warp == 0) {
+    __syncwarp();
+    if (warp == 0 && S.start.lo < S.start.hi) {
+        const int64_t lo = S.start.lo;
         const Seq s = sequence(A, S.start.b);
         const int items = item_count<C>(A, s);
         long long at = S.start.first;
@@ -371,7 +375,6 @@ __device__ void find_start(const PagedParams& A, Shared& S, long long* units) {
             if (at > lo) break;
         }
     }
-    __syncthreads();
 }
 
 // The first token in the window of a row at position `first`.
@@ -668,7 +671,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
     Shared& S = *reinterpret_cast<Shared*>(codes + C::CRING * C::CODES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == C::MMA) tmem_alloc(&S.tmem_base, 512);
-    if (tid == 0) {
+    if (tid == 32) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&S.full[i], BITS8 ? 128 : 1);
             mbar_init(&S.empty[i], 1);
@@ -1147,11 +1150,16 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     const int inside = S.valid[slot];
                     const bool whole = inside == kTile && P.tile[m].has(tile);
                     const uint32_t s_addr = lanes + buf * kTile;
-                    constexpr int N = BITS8 ? 2 : 4;      // chunks of 32 columns in registers
+                    constexpr int N = BITS8 ? 1 : 4;      // chunks of 32 columns in registers
                     float x[N][32];
                     const float qs = BITS8 ? __uint_as_float((uint32_t)S.q_power[P.loads & 1][m][row] << 23) : 1.f;
-                    // what page p's scores are multiplied by
-                    auto key_scale = [&](int p) { return S.scale[slot][0][p] * qs; };
+                    // 8 bits: what the scores of a chunk's two pages are multiplied by, and log2 of their value
+                    // scales; read before the chunk is waited for (shared memory is busy: a read takes long)
+                    float2 ks = make_float2(1.f, 1.f), lv = ks;
+                    auto scales = [&](int c) {
+                        ks = *reinterpret_cast<const float2*>(&S.scale[slot][0][2 * c]);
+                        lv = *reinterpret_cast<const float2*>(&S.scale[slot][1][2 * c]);
+                    };
                     // chunk c of the row's scores: hidden ones are -inf (with 8 bits after their scale, as that
                     // may be zero)
                     auto hide = [&](int c, float (&v)[32]) {
@@ -1160,13 +1168,19 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         if (A.window > 0) seen &= ~low_bits(lo - from) | low_bits(A.sinks - from);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            if constexpr (BITS8) v[j] *= key_scale(2 * c + j / 16);
+                            if constexpr (BITS8) v[j] *= j < 16 ? ks.x : ks.y;
                             v[j] = seen >> j & 1 ? v[j] : -INFINITY;
                         }
+                        if (BITS8) ks = make_float2(1.f, 1.f);
                     };
                     auto fetch = [&](int c0) {
 #pragma unroll
                         for (int c = 0; c < N; ++c) tmem_ld32(s_addr + 32 * (c0 + c), x[c]);
+                        if constexpr (BITS8) {
+                            scales(c0);
+                            ks.x *= qs;
+                            ks.y *= qs;
+                        }
 #pragma unroll
                         for (int c = 0; c < N; ++c) tmem_wait32(x[c]);
                         if (!whole) {
@@ -1188,8 +1202,8 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         for (int p = 0; p < 4 * N; p += 2) {
                             m8[p] = fmaxf(fmaxf(m8[p], x[p / 4][p % 4 * 8 + 7]), fmaxf(m8[p + 1], x[p / 4][p % 4 * 8 + 15]));
                             if constexpr (BITS8) {
-                                if (whole) m8[p] *= key_scale(2 * c0 + p / 2);
-                                top_o = fmaxf(top_o, m8[p] + S.scale[slot][1][2 * c0 + p / 2]);
+                                m8[p] *= p == 0 ? ks.x : ks.y;
+                                top_o = fmaxf(top_o, m8[p] + (p == 0 ? lv.x : lv.y));
                             }
                             top_s = fmaxf(top_s, m8[p]);
                         }
@@ -1198,7 +1212,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         // The loops over halves stay loops here: the SM's warps run five programs, and waited for
                         // instructions for 2.7 of 11 cycles an issue with this one unrolled.
 #pragma unroll 1
-                        for (int c0 = 2; c0 >= 0; c0 -= 2) {
+                        for (int c0 = 3; c0 >= 0; --c0) {
                             fetch(c0);
                             maxima(c0);
                         }
@@ -1236,16 +1250,15 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         uint32_t w[16];
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            const int page = 2 * (c0 + c) + g;
-                            const float k = !BITS8 ? A.scale_log2e : whole ? key_scale(page) : 1.f;
-                            const float v = BITS8 ? ex2(S.scale[slot][1][page] + unit) : 1.f;
+                            const float k = !BITS8 ? A.scale_log2e : g == 0 ? ks.x : ks.y;
+                            const float v = BITS8 ? ex2((g == 0 ? lv.x : lv.y) + unit) : 1.f;
 #pragma unroll
                             for (int j = 16 * g; j < 16 * g + 16; j += 2) {
                                 float a, b;
                                 fma2(a, b, x[c][j], x[c][j + 1], k, k, base, base);
                                 a = ex2(a);
                                 b = ex2(b);
-                                add2(l[c % 2 * 2], l[c % 2 * 2 + 1], a, b);
+                                add2(l[j / 2 % 2 * 2], l[j / 2 % 2 * 2 + 1], a, b);
                                 if constexpr (BITS8) {
                                     mul2(a, b, v);
                                     w[j / 2] = pack_half(a, b);
@@ -1264,12 +1277,11 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     };
                     if constexpr (BITS8) {
 #pragma unroll 1
-                        for (int c0 = 0; c0 < 4; c0 += 2) {
-                            // the lower half is there; the upper was not touched by its probabilities
+                        for (int c0 = 0; c0 < 4; ++c0) {
+                            // the first chunk is there; the others were not touched by its probabilities
                             if (c0 > 0) fetch(c0);
                             turn(c0, 0);
-                            turn(c0, 1);
-                            if (c0 == 0) half_done();
+                            if (c0 == 1) half_done();
                         }
                     } else {
                         turn(0, 0);
@@ -1419,40 +1431,73 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
 }
 
 // Joins the parts of items that CTAs left to one another: block x takes the item that
-// CTA x began, a slice of its rows; a thread takes 8 dimensions of a row.
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams A) {
+// CTA x began, a slice of its rows.  A thread takes 8 dimensions of a row; of many
+// parts (one request on its own has one in each of dozens of CTAs, each a read from L2
+// or beyond) four lanes take every fourth, then join theirs, always in the same order.
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedParams A) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PartHead head = A.heads[blockIdx.x];
     if (head.more <= 0) return;
-    const int words = A.D / 8, rows = head.tokens * A.G;
-    for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < rows * words; i += gridDim.y * kJoinThreads) {
-        const int r = i / words, d = i - r * words;
-        const int token = r / A.G, g = r - token * A.G, tile = token / A.tokens;
-        const int64_t part_row = tile * kRows + (token - tile * A.tokens) * A.G + g;
-        float m = -INFINITY, mo = -INFINITY, l = 0.f, o[8] = {};
-        for (int k = 0; k <= head.more; ++k) {
-            const int64_t at = ((int64_t)(blockIdx.x + k) * 2 + (k == 0)) * A.part_rows + part_row;
-            const float4 s = A.sums[at];
-            const float4* p = reinterpret_cast<const float4*>(A.parts + at * A.D + d * 8);
-            const float4 x = p[0], y = p[1];
-            const float m2 = fmaxf(m, s.x), o2 = fmaxf(mo, s.z);
-            // a part without tokens has -inf for its maximum; one that is not finished NaN
-            l = (m == -INFINITY ? 0.f : l * ex2(m - m2)) + (s.x == -INFINITY ? 0.f : s.y * ex2(s.x != s.x ? NAN : s.x - m2));
-            const float f0 = mo == -INFINITY ? 0.f : ex2(mo - o2), f1 = s.z == -INFINITY ? 0.f : ex2(s.z != s.z ? NAN : s.z - o2);
+    struct Sum {
+        float m, mo, l, o[8];
+        // another's maximum, sum, unit and outputs; a part without tokens has -inf for its maximum, one that is not
+        // finished NaN
+        __device__ __forceinline__ void add(float ym, float yl, float yo, const float (&v)[8]) {
+            const float m2 = fmaxf(m, ym), o2 = fmaxf(mo, yo);
+            l = (m == -INFINITY ? 0.f : l * ex2(m - m2)) + (ym == -INFINITY ? 0.f : yl * ex2(ym != ym ? NAN : ym - m2));
+            const float f0 = mo == -INFINITY ? 0.f : ex2(mo - o2), f1 = yo == -INFINITY ? 0.f : ex2(yo != yo ? NAN : yo - o2);
             m = m2;
             mo = o2;
-            const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = o[j] * f0 + v[j] * f1;
         }
-        const float back = mo > -INFINITY ? ex2(0.5f * (mo - m)) : 1.f;
-        const float inv = l == 0.f ? 0.f : back / l;
+    };
+    const int words = A.D / 8, rows = head.tokens * A.G;
+    const int lanes = head.more >= 4 ? 4 : 1, lane = threadIdx.x % lanes, each = kJoinThreads / lanes;
+    for (int i0 = blockIdx.y * each; i0 < rows * words; i0 += gridDim.y * each) {
+        const int i = i0 + (int)threadIdx.x / lanes;
+        const bool here = i < rows * words;
+        const int r = here ? i / words : 0, d = here ? i - r * words : 0;
+        const int token = r / A.G, g = r - token * A.G, tile = token / A.tokens;
+        const int64_t part_row = tile * kRows + (token - tile * A.tokens) * A.G + g;
+        Sum t{-INFINITY, -INFINITY, 0.f, {}};
+        constexpr int AHEAD = 4;
+        for (int k0 = lane; k0 <= head.more; k0 += lanes * AHEAD) {
+            float4 s[AHEAD], x[AHEAD], y[AHEAD];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] *= back;
+            for (int e = 0; e < AHEAD; ++e) {
+                const int k = k0 + lanes * e;
+                if (k > head.more) continue;
+                const int64_t at = ((int64_t)(blockIdx.x + k) * 2 + (k == 0)) * A.part_rows + part_row;
+                const float4* p = reinterpret_cast<const float4*>(A.parts + at * A.D + d * 8);
+                s[e] = A.sums[at];
+                x[e] = p[0];
+                y[e] = p[1];
+            }
+#pragma unroll
+            for (int e = 0; e < AHEAD; ++e) {
+                if (k0 + lanes * e > head.more) continue;
+                const float v[8] = {x[e].x, x[e].y, x[e].z, x[e].w, y[e].x, y[e].y, y[e].z, y[e].w};
+                t.add(s[e].x, s[e].y, s[e].z, v);
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            if (o >= lanes) break;
+            float v[8];
+            const float ym = __shfl_down_sync(kFull, t.m, o, 4), yl = __shfl_down_sync(kFull, t.l, o, 4), yo = __shfl_down_sync(kFull, t.mo, o, 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __shfl_down_sync(kFull, t.o[j], o, 4);
+            t.add(ym, yl, yo, v);      // of use in the lanes that have a partner
+        }
+        if (!here || lane != 0) continue;
+        const float back = t.mo > -INFINITY ? ex2(0.5f * (t.mo - t.m)) : 1.f;
+        const float inv = t.l == 0.f ? 0.f : back / t.l;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack_bf16(t.o[2 * j] * back * inv, t.o[2 * j + 1] * back * inv);
         const int64_t row = ((head.row0 + token) * A.H + head.h) * A.G + g;
-        *reinterpret_cast<uint4*>(A.out + row * A.D + d * 8) =
-            make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv), pack_bf16(o[4] * inv, o[5] * inv),
-                       pack_bf16(o[6] * inv, o[7] * inv));
+        *reinterpret_cast<uint4*>(A.out + row * A.D + d * 8) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -1618,8 +1663,7 @@ int launch_paged(const bsa_paged_attention_args_t& a, PagedParams& A, cudaStream
     else e = bits8 ? launch_kernel<256, true>(A, M, grid, st) : launch_kernel<256, false>(A, M, grid, st);
     if (e != cudaSuccess) return (int)e;
     cudaLaunchConfig_t cfg{};
-    const int words = A.part_rows * A.D / 8;
-    const int slices = (words + kJoinThreads - 1) / kJoinThreads;
+    const int slices = (A.part_rows * A.D / 8 * 4 + kJoinThreads - 1) / kJoinThreads;
     cfg.gridDim = dim3((unsigned)grid, (unsigned)(slices < 8 ? slices : 8));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
