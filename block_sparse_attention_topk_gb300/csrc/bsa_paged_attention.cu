@@ -548,7 +548,7 @@ __device__ __forceinline__ const Portion* Reader::next(Shared& S, unsigned long 
 // by one thread of a warp, behind the others
 __device__ __forceinline__ void Reader::done(Shared& S) { mbar_arrive(&S.portion_empty[number++ % kPortions]); }
 
-// Adds what the values' warps took out to the row's outputs [d0, d0 + 32): values that
+// Adds what the values' warps took out to the row's outputs [d0, d0 + 16): values that
 // are not finite of tokens that the row sees.
 template <class C, bool BITS8>
 __device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion& P, int stream, int hi, int lo, int d0, float* o) {
@@ -562,7 +562,7 @@ __device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion&
             const int64_t page = id * kPagesPerBlock + c / kSubPage;
             if (j > hi || (A.window > 0 && j < lo && j >= A.sinks) || page < 0 || page >= A.num_pages) continue;
             const int64_t at = ((page * kSubPage + c % kSubPage) * A.H + P.h) * A.D;
-            for (int k = 0; k < 32 && d0 + k < A.D; ++k) {
+            for (int k = 0; k < 16 && d0 + k < A.D; ++k) {
                 float x;
                 if constexpr (BITS8) {
                     const uint32_t code = __ldg(A.v + at + d0 + k);
@@ -1145,21 +1145,20 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     tc_fence_after();
                     settled = true;
                 };
+                bool halved = false;      // the product of the first 64 tokens may start
                 if (live) {
                     const int tile = P.r.tile(P.i0 + k), slot = (tiles + k) % kInfo;
                     const int inside = S.valid[slot];
                     const bool whole = inside == kTile && P.tile[m].has(tile);
                     const uint32_t s_addr = lanes + buf * kTile;
                     constexpr int N = BITS8 ? 1 : 4;      // chunks of 32 columns in registers
+                    using One = std::integral_constant<int, 1>;
+                    using All = std::integral_constant<int, N>;
                     float x[N][32];
                     const float qs = BITS8 ? __uint_as_float((uint32_t)S.q_power[P.loads & 1][m][row] << 23) : 1.f;
                     // 8 bits: what the scores of a chunk's two pages are multiplied by, and log2 of their value
                     // scales; read before the chunk is waited for (shared memory is busy: a read takes long)
                     float2 ks = make_float2(1.f, 1.f), lv = ks;
-                    auto scales = [&](int c) {
-                        ks = *reinterpret_cast<const float2*>(&S.scale[slot][0][2 * c]);
-                        lv = *reinterpret_cast<const float2*>(&S.scale[slot][1][2 * c]);
-                    };
                     // chunk c of the row's scores: hidden ones are -inf (with 8 bits after their scale, as that
                     // may be zero)
                     auto hide = [&](int c, float (&v)[32]) {
@@ -1171,35 +1170,37 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                             if constexpr (BITS8) v[j] *= j < 16 ? ks.x : ks.y;
                             v[j] = seen >> j & 1 ? v[j] : -INFINITY;
                         }
-                        if (BITS8) ks = make_float2(1.f, 1.f);
+                        if constexpr (BITS8) ks = make_float2(1.f, 1.f);
                     };
-                    auto fetch = [&](int c0) {
+                    auto fetch = [&](auto count, int c0) {
 #pragma unroll
-                        for (int c = 0; c < N; ++c) tmem_ld32(s_addr + 32 * (c0 + c), x[c]);
+                        for (int c = 0; c < count.value; ++c) tmem_ld32(s_addr + 32 * (c0 + c), x[c]);
                         if constexpr (BITS8) {
-                            scales(c0);
+                            ks = *reinterpret_cast<const float2*>(&S.scale[slot][0][2 * c0]);
+                            lv = *reinterpret_cast<const float2*>(&S.scale[slot][1][2 * c0]);
                             ks.x *= qs;
                             ks.y *= qs;
                         }
 #pragma unroll
-                        for (int c = 0; c < N; ++c) tmem_wait32(x[c]);
+                        for (int c = 0; c < count.value; ++c) tmem_wait32(x[c]);
                         if (!whole) {
 #pragma unroll
-                            for (int c = 0; c < N; ++c) hide(c0 + c, x[c]);
+                            for (int c = 0; c < count.value; ++c) hide(c0 + c, x[c]);
                         }
                     };
                     // maxima of 16 columns, the largest in `top_s`, with their pages' value scales in `top_o`
                     float top_s = -INFINITY, top_o = -INFINITY;
-                    auto maxima = [&](int c0) {
-                        float m8[4 * N];      // strands of 8 columns, side by side
+                    auto maxima = [&](auto count) {
+                        constexpr int STRANDS = 4 * count.value;
+                        float m8[STRANDS];      // of 8 columns, side by side
 #pragma unroll
-                        for (int p = 0; p < 4 * N; ++p) m8[p] = x[p / 4][p % 4 * 8];
+                        for (int p = 0; p < STRANDS; ++p) m8[p] = x[p / 4][p % 4 * 8];
 #pragma unroll
                         for (int j = 1; j < 7; j += 2)
 #pragma unroll
-                            for (int p = 0; p < 4 * N; ++p) m8[p] = fmaxf(fmaxf(m8[p], x[p / 4][p % 4 * 8 + j]), x[p / 4][p % 4 * 8 + j + 1]);
+                            for (int p = 0; p < STRANDS; ++p) m8[p] = fmaxf(fmaxf(m8[p], x[p / 4][p % 4 * 8 + j]), x[p / 4][p % 4 * 8 + j + 1]);
 #pragma unroll
-                        for (int p = 0; p < 4 * N; p += 2) {
+                        for (int p = 0; p < STRANDS; p += 2) {
                             m8[p] = fmaxf(fmaxf(m8[p], x[p / 4][p % 4 * 8 + 7]), fmaxf(m8[p + 1], x[p / 4][p % 4 * 8 + 15]));
                             if constexpr (BITS8) {
                                 m8[p] *= p == 0 ? ks.x : ks.y;
@@ -1208,19 +1209,19 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                             top_s = fmaxf(top_s, m8[p]);
                         }
                     };
-                    if constexpr (BITS8) {
-                        // The loops over halves stay loops here: the SM's warps run five programs, and waited for
-                        // instructions for 2.7 of 11 cycles an issue with this one unrolled.
-#pragma unroll 1
-                        for (int c0 = 3; c0 >= 0; --c0) {
-                            fetch(c0);
-                            maxima(c0);
-                        }
-                    } else {
-                        fetch(0);
-                        maxima(0);
+                    if constexpr (!BITS8) {
+                        fetch(All{}, 0);
+                        maxima(All{});
                         top_s *= A.scale_log2e;
                         top_o = top_s;
+                    } else {
+                        // The loops over chunks stay loops: the SM's warps run five programs with 8 bits, and
+                        // waited for instructions for 2.7 of 11 cycles an issue with this one unrolled.
+#pragma unroll 1
+                        for (int c = 3; c >= 0; --c) {
+                            fetch(One{}, c);
+                            maxima(One{});
+                        }
                     }
                     // a row whose maximum has grown by more than 2^kGrow takes it over
                     const bool grow = valid && top_s > mx + kGrow, grow_o = BITS8 ? valid && top_o > mo + kGrow : grow;
@@ -1245,56 +1246,56 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     }
                     const float base = mx == -INFINITY ? 0.f : -mx;
                     const float unit = mo == -INFINITY ? -INFINITY : mx - mo;
-                    // the probabilities of chunk c0 + c, to the scores' place
-                    auto turn = [&](int c0, int c) {
+                    // the probabilities of chunk c, in v, to the scores' place
+                    auto turn = [&](int c, const float (&v)[32]) {
                         uint32_t w[16];
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             const float k = !BITS8 ? A.scale_log2e : g == 0 ? ks.x : ks.y;
-                            const float v = BITS8 ? ex2((g == 0 ? lv.x : lv.y) + unit) : 1.f;
+                            const float f = BITS8 ? ex2((g == 0 ? lv.x : lv.y) + unit) : 1.f;
 #pragma unroll
                             for (int j = 16 * g; j < 16 * g + 16; j += 2) {
                                 float a, b;
-                                fma2(a, b, x[c][j], x[c][j + 1], k, k, base, base);
+                                fma2(a, b, v[j], v[j + 1], k, k, base, base);
                                 a = ex2(a);
                                 b = ex2(b);
                                 add2(l[j / 2 % 2 * 2], l[j / 2 % 2 * 2 + 1], a, b);
                                 if constexpr (BITS8) {
-                                    mul2(a, b, v);
+                                    mul2(a, b, f);
                                     w[j / 2] = pack_half(a, b);
                                 } else {
                                     w[j / 2] = pack_bf16(a, b);
                                 }
                             }
                         }
-                        tmem_st16(s_addr + 16 * (c0 + c), w);
+                        tmem_st16(s_addr + 16 * c, w);
                     };
-                    // the product of the first 64 tokens starts under the others' exponentials
                     auto half_done = [&]() {
                         tmem_wait_st();
                         tc_fence_before();
                         mbar_arrive(&S.p_half[buf]);
+                        halved = true;
                     };
-                    if constexpr (BITS8) {
-#pragma unroll 1
-                        for (int c0 = 0; c0 < 4; ++c0) {
-                            // the first chunk is there; the others were not touched by its probabilities
-                            if (c0 > 0) fetch(c0);
-                            turn(c0, 0);
-                            if (c0 == 1) half_done();
-                        }
-                    } else {
-                        turn(0, 0);
-                        turn(0, 1);
+                    if constexpr (!BITS8) {
+                        turn(0, x[0]);
+                        turn(1, x[1]);
                         half_done();
-                        turn(0, 2);
-                        turn(0, 3);
+                        turn(2, x[2]);
+                        turn(3, x[3]);
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            // the first chunk is there; the others were not touched by its probabilities
+                            if (c > 0) fetch(One{}, c);
+                            turn(c, x[0]);
+                            if (c == 1) half_done();
+                        }
                     }
                     tmem_wait_st();
                     written = true;
-                } else {
-                    mbar_arrive(&S.p_half[buf]);
                 }
+                tc_fence_before();
+                if (!halved) mbar_arrive(&S.p_half[buf]);
                 settle();
                 if (NS == 1) o_phase ^= 1;      // as many products as tiles
                 tc_fence_before();
@@ -1316,22 +1317,21 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             if constexpr (!BITS8) mo = mx;
             if (!ok) mx = mo = sum = NAN;
             const bool odd = any && S.poison[P.number % kPortions] == P.number + 1;
-            // 32 of the row's outputs, not yet divided by the sum
-            auto result = [&](int c, float (&o)[32]) {
+            // 16 of the row's outputs, not yet divided by the sum
+            auto result = [&](int c, float (&o)[16]) {
                 if (ok && any && live) {
-                    tmem_ld32(o_addr + 32 * c, o);
-                    tmem_wait32(o);
+                    tmem_ld16(o_addr + 16 * c, o);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = ok ? 0.f : NAN;
+                    for (int j = 0; j < 16; ++j) o[j] = ok ? 0.f : NAN;
                 }
                 if (odd && valid) {
-                    float x[32];
+                    float x[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = 0.f;
-                    add_odd_values<C, BITS8>(A, P, stream, hi, lo, 32 * c, x);
+                    for (int j = 0; j < 16; ++j) x[j] = 0.f;
+                    add_odd_values<C, BITS8>(A, P, stream, hi, lo, 16 * c, x);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] += x[j];
+                    for (int j = 0; j < 16; ++j) o[j] += x[j];
                 }
             };
             const bool join = P.split && n > 1;      // both streams have a part of the rows
@@ -1370,15 +1370,15 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             }
 #pragma unroll 1
             for (int half = 0; half < (NS == 2 ? 2 : 1); ++half) {
-                constexpr int CH = C::D / 32 / (NS == 2 ? 2 : 1);      // chunks of 32 a half
+                constexpr int CH = C::D / 16 / (NS == 2 ? 2 : 1);      // chunks of 16 a half
                 if (NS == 2 && join) {
                     if (stream == 1) {
 #pragma unroll 1
                         for (int c = 0; c < CH; ++c) {
-                            float o[32];
+                            float o[16];
                             result(half * CH + c, o);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) xch[(c * 32 + j) * kRows + row] = o[j];
+                            for (int j = 0; j < 16; ++j) xch[(c * 16 + j) * kRows + row] = o[j];
                         }
                     }
                     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1386,28 +1386,25 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 if (live && (stream == 0 || !P.split)) {
 #pragma unroll 1
                     for (int c = 0; c < CH; ++c) {
-                        const int d0 = (half * CH + c) * 32;
-                        float o[32];
+                        const int d0 = (half * CH + c) * 16;
+                        float o[16];
                         result(half * CH + c, o);
                         if (NS == 2 && join) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + xch[(c * 32 + j) * kRows + row] * f1;
+                            for (int j = 0; j < 16; ++j) o[j] = o[j] * f0 + xch[(c * 16 + j) * kRows + row] * f1;
                         }
-                        if (!writes) continue;
+                        if (!writes || d0 >= A.D) continue;
                         if (whole_item) {
-                            uint32_t w[16];
+                            uint32_t w[8];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
+                            for (int j = 0; j < 8; ++j) {
                                 const float b = BITS8 ? back : 1.f;
                                 w[j] = pack_bf16(o[2 * j] * b * scale, o[2 * j + 1] * b * scale);
                             }
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                if (d0 + 16 * j < A.D) store32(out + d0 + 16 * j, &w[8 * j], A.wide_out);
+                            store32(out + d0, w, A.wide_out);
                         } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (d0 + 8 * j < A.D) store32(part + d0 + 8 * j, reinterpret_cast<const uint32_t*>(&o[8 * j]), true);
+                            store32(part + d0, reinterpret_cast<const uint32_t*>(o), true);
+                            store32(part + d0 + 8, reinterpret_cast<const uint32_t*>(o + 8), true);
                         }
                     }
                 }
