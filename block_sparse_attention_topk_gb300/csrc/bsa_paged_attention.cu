@@ -68,7 +68,7 @@ constexpr int kPortions = 4;             // portions announced ahead
 constexpr int kWindow = 512;             // sequences whose units a CTA holds at a time while it finds its part
 constexpr float kGrow = 8.f;             // log2 of what a maximum may grow by before O is rescaled
 constexpr int kJoinThreads = 256;
-constexpr int kMinUnits = 2;             // the least part of a CTA
+constexpr int kMinSteps = 2;             // the least part of a CTA, in steps
 
 struct PagedParams {
     const uint16_t* q;
@@ -138,6 +138,11 @@ struct Cfg {
     static constexpr int OTHERS = BITS8 ? 64 : 72;
     static constexpr int MORE = (GIVEN * THREADS - OTHERS * (THREADS - SOFTMAX * 32)) / (SOFTMAX * 32) / 8 * 8;
     static constexpr int MINE = MORE < 255 ? MORE : 248;
+    // Units of work: a step in which each stream has its own rows of one tile, one in which both have the
+    // same rows of two tiles, and an item's beginning and end.  With 8 bits the second widens twice the codes:
+    // 1.25 times as long (without, the CTAs with such steps were last: 1650 us instead of 1510 for 1639
+    // tokens at the end of a context of 114500, 2 x 8 heads).
+    static constexpr int PAIR_UNITS = 4, SPLIT_UNITS = BITS8 && NS == 2 ? 5 : 4, END_UNITS = 4;
     static constexpr uint32_t O_COL = 256;                 // TMEM: scores in columns 0 to 255, outputs behind
     static_assert(RING >= 3 && RING <= kMaxStages && CRING <= kMaxStages && CRING % 2 == 0, "rings; the groups take stages of codes in turn");
 };
@@ -242,13 +247,23 @@ __device__ __forceinline__ int item_steps(const PagedParams& A, const Seq& s, in
     if (split != nullptr) *split = two;
     return two ? (r.nk + 1) / 2 : r.nk;
 }
+// What a step of such an item is worth, and the whole item.
+template <class C>
+__device__ __forceinline__ int step_units(bool split) {
+    return split ? C::SPLIT_UNITS : C::PAIR_UNITS;
+}
+template <class C>
+__device__ __forceinline__ int64_t item_units(const PagedParams& A, const Seq& s, int qt) {
+    bool split;
+    const int steps = item_steps<C>(A, s, qt, nullptr, &split);
+    return (int64_t)steps * step_units<C>(split) + C::END_UNITS;
+}
 template <class C>
 __device__ __forceinline__ int item_count(const PagedParams& A, const Seq& s) {
     return (s.n + item_tokens<C>(A) - 1) / item_tokens<C>(A);
 }
 
-// The units of sequences [b0, b0 + n) (an item's are its steps and one for its
-// beginning and end), per head.
+// The units of sequences [b0, b0 + n), per head.
 template <class C>
 __device__ void count_units(const PagedParams& A, long long* units, int b0, int n) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -261,7 +276,7 @@ __device__ void count_units(const PagedParams& A, long long* units, int b0, int 
             s = sequence(A, b0 + i);
             items = item_count<C>(A, s);
             if (items <= 4)
-                for (int k = 0; k < items; ++k) u += item_steps<C>(A, s, k) + 1;
+                for (int k = 0; k < items; ++k) u += item_units<C>(A, s, k);
         }
         // sequences of many items: the warp together
         for (uint32_t many = __ballot_sync(kFull, items > 4); many != 0; many &= many - 1) {
@@ -269,7 +284,7 @@ __device__ void count_units(const PagedParams& A, long long* units, int b0, int 
             const Seq x = sequence(A, b0 + i0 + l);
             const int m = item_count<C>(A, x);
             long long v = 0;
-            for (int k = lane; k < m; k += 32) v += item_steps<C>(A, x, k) + 1;
+            for (int k = lane; k < m; k += 32) v += item_units<C>(A, x, k);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
             if (lane == l) u = v;
@@ -365,7 +380,7 @@ __device__ void find_start(const PagedParams& A, Shared& S, long long* units) {
         __syncwarp();
         for (int k0 = 0; k0 < items; k0 += 32) {
             const int k = k0 + lane;
-            const long long w = k < items ? item_steps<C>(A, s, k) + 1 : 0;
+            const long long w = k < items ? item_units<C>(A, s, k) : 0;
             const long long mine = at + warp_before(w);
             if (mine <= lo && lo < mine + w) {
                 S.start.qt = k;
@@ -405,7 +420,8 @@ struct Walk {
             const int tok0 = qt * item_tokens<C>(A), tokens = min(item_tokens<C>(A), s.n - tok0);
             const int64_t row0 = s.t0 + tok0, pos0 = s.p0 + tok0;
             const int item_b = b, item_h = h;
-            at += steps + 1;
+            const int unit = step_units<C>(split);
+            at += (int64_t)steps * unit + C::END_UNITS;
             if (++qt == items) {
                 qt = 0;
                 if (++h == A.H) {
@@ -417,7 +433,9 @@ struct Walk {
                     }
                 }
             }
-            const int a = (int)(lo > first ? lo - first : 0), e = (int)(hi - first < steps ? hi - first : steps);
+            // a step is of the part in which its last unit lies
+            const int64_t from = lo > first ? (lo - first) / unit : 0, to = (hi - first) / unit;
+            const int a = (int)(from < steps ? from : steps), e = (int)(to < steps ? to : steps);
             if (a >= e && !(steps == 0 && first >= lo)) continue;
             P->row0 = row0;
             P->pos0 = pos0;
@@ -434,8 +452,8 @@ struct Walk {
             P->loads = loads;
             if (P->i1 > P->i0) ++loads;
             P->lo = first_seen(A, pos0);
-            // the CTA of the item's last step: lo(c) = c U / N <= e for the c up to ((e + 1) N - 1) / U
-            P->more = a == 0 && e < steps ? (int)(((first + steps) * st.N - 1) / st.U - blockIdx.x) : 0;
+            // the CTA of the last step's last unit u: lo(c) = c U / N <= u for the c up to ((u + 1) N - 1) / U
+            P->more = a == 0 && e < steps ? (int)(((first + (int64_t)steps * unit) * st.N - 1) / st.U - blockIdx.x) : 0;
             P->split = split;
             P->begins = a == 0;
             P->ends = e == steps;
@@ -1633,7 +1651,7 @@ int launch_paged(const bsa_paged_attention_args_t& a, PagedParams& A, cudaStream
     A.window = a.window;
     A.sinks = a.sinks;
     A.cache_dtype = a.cache_dtype;
-    A.min_units = kMinUnits;
+    A.min_units = kMinSteps * (bits8 ? Cfg<128, true>::SPLIT_UNITS : Cfg<128, false>::SPLIT_UNITS);
     A.part_rows = part_rows(a.T, a.G, a.D);
     // a scale of zero must not meet the -inf of hidden scores; any tiny one has its result
     const float scale = fabsf(a.scale) * 1.44269504f;
