@@ -5,6 +5,7 @@
 // Both operators are a plan and its application.  The plan is integer work on
 // tables of kilobytes to a few megabytes with a chain of dependent phases
 // (counts before a scan, a scan before ids), so it is one cluster of 8 CTAs
+// (or one CTA, where there is little to read)
 // whose barrier separates the phases: no second launch for each, and no
 // waiting on CTAs that may not be resident.  The application writes the table
 // and copies whole blocks of every tensor, over the whole GPU.
@@ -27,7 +28,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kCluster = 8;
 constexpr int kPlanThreads = 1024;
-constexpr int kAll = kCluster * kPlanThreads;
+constexpr int64_t kOneCta = 16384;                          // entries and counts that one CTA plans
 constexpr int kCopyThreads = 256;
 constexpr int kUnroll = 8;                                   // 16-byte words of a thread in flight
 constexpr int kChunk = kCopyThreads * kUnroll * 16;          // bytes of a tensor's block that a CTA copies at a time
@@ -59,6 +60,7 @@ struct ForkParams {
     int32_t* fresh;                   // fresh block ids in order
     int64_t fresh_cap;
     uint32_t* status;
+    int32_t ranks;                    // CTAs of the plan: 1 or kCluster
 };
 
 struct CompactParams {
@@ -72,6 +74,7 @@ struct CompactParams {
     Head* head;
     int32_t *src, *dst, *src_refs;
     uint32_t* status;
+    int32_t ranks;                    // CTAs of the plan: 1 or kCluster
 };
 
 // What a block's id stands for, as a launch's argument.
@@ -87,8 +90,12 @@ using AllTensors = Tensors<BSA_MAX_BLOCK_TENSORS>;
 
 __device__ __forceinline__ int64_t blocks_of(int64_t tokens) { return (tokens + kPageSize - 1) / kPageSize; }
 
-// Phases of the plan: global memory written before is read after.
-__device__ __forceinline__ void phase() {
+// Phases of the plan: global memory written before is read after (from L2: __ldcg).
+__device__ __forceinline__ void phase(int ranks) {
+    if (ranks == 1) {
+        __syncthreads();
+        return;
+    }
     __threadfence();
     cluster_sync();
 }
@@ -141,26 +148,26 @@ __device__ __forceinline__ Row new_row(const ForkParams& P, int64_t r, uint32_t*
     return w;
 }
 
-__global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParams P) {
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParams P) {
     __shared__ int warps[32];
-    const int tid = threadIdx.x, rank = (int)cluster_rank(), all = rank * kPlanThreads + tid;
+    const int tid = threadIdx.x, rank = blockIdx.x, all = rank * kPlanThreads + tid, everyone = P.ranks * kPlanThreads;
     const int lane = tid & 31, gwarp = all >> 5;
     asm volatile("griddepcontrol.launch_dependents;");
     // ---- the old state, where the new one takes its place; counts to start from
     if (P.refs_out != P.refs_in)
-        for (int64_t i = all; i < P.num_blocks; i += kAll) P.refs_out[i] = __ldg(P.refs_in + i);
+        for (int64_t i = all; i < P.num_blocks; i += everyone) P.refs_out[i] = __ldg(P.refs_in + i);
     if (P.snap_table != nullptr)
-        for (int64_t i = all; i < P.rows_in * P.max_blocks; i += kAll) P.snap_table[i] = P.table_in[i];
+        for (int64_t i = all; i < P.rows_in * P.max_blocks; i += everyone) P.snap_table[i] = P.table_in[i];
     if (P.snap_lens != nullptr)
-        for (int64_t i = all; i < P.rows_in; i += kAll) P.snap_lens[i] = P.lens_in[i];
-    for (int64_t i = all; i < P.rows_in; i += kAll) P.first[i] = INT_MAX;
-    phase();
+        for (int64_t i = all; i < P.rows_in; i += everyone) P.snap_lens[i] = P.lens_in[i];
+    for (int64_t i = all; i < P.rows_in; i += everyone) P.first[i] = INT_MAX;
+    phase(P.ranks);
     // ---- references of whole blocks: a warp per old and per new row
-    for (int64_t i = all; i < P.rows_out; i += kAll) {
+    for (int64_t i = all; i < P.rows_out; i += everyone) {
         const Row w = new_row(P, i, P.status);
         if (w.parent >= 0) atomicMin(P.first + w.parent, (int)i);
     }
-    for (int64_t r = gwarp; r < P.rows_in; r += kAll / 32) {
+    for (int64_t r = gwarp; r < P.rows_in; r += everyone / 32) {
         const int64_t len = checked_len(__ldcg(P.lens + r), P.max_blocks, lane == 0 ? P.status : nullptr);
         const bool stays = r < P.rows_out && __ldg(P.parent + r) == r;      // its whole blocks stay its own
         for (int64_t j = (stays ? len / kPageSize : 0) + lane; j < blocks_of(len); j += 32) {
@@ -170,7 +177,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads) fork_
             if (good) atomicSub(P.refs_out + b, 1);
         }
     }
-    for (int64_t r = gwarp; r < P.rows_out; r += kAll / 32) {
+    for (int64_t r = gwarp; r < P.rows_out; r += everyone / 32) {
         const Row w = new_row(P, r, nullptr);
         if (w.parent < 0 || w.parent == r) continue;
         for (int64_t j = lane; j < w.base / kPageSize; j += 32) {
@@ -178,7 +185,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads) fork_
             if (b >= 0 && b < P.num_blocks) atomicAdd(P.refs_out + b, 1);
         }
     }
-    phase();
+    phase(P.ranks);
     // ---- unfinished blocks go to the first child; fresh blocks of each row, in order
     if (rank == 0) {
         int before = 0;
@@ -209,17 +216,17 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads) fork_
         }
         if (tid == 0) P.head->needed = before;
     }
-    phase();
+    phase(P.ranks);
     // ---- the lowest free blocks: counted per CTA's share, then listed
-    const int64_t lo = P.num_blocks * rank / kCluster, hi = P.num_blocks * (rank + 1) / kCluster;
+    const int64_t lo = P.num_blocks * rank / P.ranks, hi = P.num_blocks * (rank + 1) / P.ranks;
     int mine = 0;
     for (int64_t i = lo + tid; i < hi; i += kPlanThreads) mine += __ldcg(P.refs_out + i) <= 0;
     int total;
     cta_scan(mine, warps, &total);
     if (tid == 0) P.head->count[0][rank] = total;
-    phase();
+    phase(P.ranks);
     int before = 0, available = 0;
-    for (int i = 0; i < kCluster; ++i) {
+    for (int i = 0; i < P.ranks; ++i) {
         const int n = __ldcg(&P.head->count[0][i]);
         if (i < rank) before += n;
         available += n;
@@ -241,18 +248,18 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads) fork_
     }
 }
 
-__global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactParams P) {
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactParams P) {
     __shared__ int warps[32];
-    const int tid = threadIdx.x, rank = (int)cluster_rank();
+    const int tid = threadIdx.x, rank = blockIdx.x, everyone = P.ranks * kPlanThreads;
     asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t lo = P.num_blocks * rank / kCluster, hi = P.num_blocks * (rank + 1) / kCluster;
+    const int64_t lo = P.num_blocks * rank / P.ranks, hi = P.num_blocks * (rank + 1) / P.ranks;
     int mine = 0, total;
     for (int64_t i = lo + tid; i < hi; i += kPlanThreads) mine += __ldcg(P.refs_in + i) > 0;
     cta_scan(mine, warps, &total);
     if (tid == 0) P.head->count[0][rank] = total;
-    phase();
+    phase(P.ranks);
     int live = 0;
-    for (int i = 0; i < kCluster; ++i) live += __ldcg(&P.head->count[0][i]);
+    for (int i = 0; i < P.ranks; ++i) live += __ldcg(&P.head->count[0][i]);
     // ---- blocks to move and holes to fill, counted per share
     int moving = 0, holes = 0;
     for (int64_t i = lo + tid; i < hi; i += kPlanThreads) {
@@ -264,9 +271,9 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads) compa
     if (tid == 0) P.head->count[1][rank] = total;
     cta_scan(holes, warps, &total);
     if (tid == 0) P.head->count[2][rank] = total;
-    phase();
+    phase(P.ranks);
     int moved_before = 0, holes_before = 0, moves = 0;
-    for (int i = 0; i < kCluster; ++i) {
+    for (int i = 0; i < P.ranks; ++i) {
         const int m = __ldcg(&P.head->count[1][i]), h = __ldcg(&P.head->count[2][i]);
         if (i < rank) {
             moved_before += m;
@@ -294,8 +301,8 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads) compa
         moved_before += m_total;
         holes_before += h_total;
     }
-    phase();
-    for (int64_t k = rank * kPlanThreads + tid; k < moves; k += kAll) {
+    phase(P.ranks);
+    for (int64_t k = rank * kPlanThreads + tid; k < moves; k += everyone) {
         const int32_t from = __ldcg(P.src + k), to = __ldcg(P.dst + k);
         P.new_ids[from] = to;
         P.refs_out[to] = __ldcg(P.src_refs + k);
@@ -438,8 +445,17 @@ template <typename Params>
 cudaError_t launch_pair(void (*plan)(const Params), void (*apply_few)(const Params, const Tensors<kFewTensors>),
                         void (*apply_all)(const Params, const AllTensors), const Params& P, const AllTensors& X, int64_t want,
                         cudaStream_t st) {
-    plan<<<kCluster, kPlanThreads, 0, st>>>(P);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t one{};
+    one.gridDim = dim3((unsigned)P.ranks);
+    one.blockDim = dim3(kPlanThreads);
+    one.stream = st;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = (unsigned)P.ranks;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    one.attrs = &cluster;
+    one.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&one, plan, P);
     if (e != cudaSuccess) return e;
     const int64_t most = (int64_t)device_sm_count() * 8;
     cudaLaunchConfig_t cfg{};
@@ -551,6 +567,7 @@ extern "C" int bsa_fork_requests(const bsa_block_tensor_t* tensors, int32_t num_
     P.lens_out = lens_out;
     P.refs_out = refs_out;
     P.status = current_status_word();
+    P.ranks = in + out + num_blocks <= kOneCta ? 1 : kCluster;
     const int64_t work = num_out * X.chunks[X.n], entries = (out + kCopyThreads - 1) / kCopyThreads;
     const cudaError_t e = launch_pair<ForkParams>(fork_plan_kernel, fork_apply_kernel<kFewTensors>, fork_apply_kernel<BSA_MAX_BLOCK_TENSORS>, P, X,
                                                    work > entries ? work : entries, static_cast<cudaStream_t>(stream));
@@ -587,6 +604,7 @@ extern "C" int bsa_compact_blocks(const bsa_block_tensor_t* tensors, int32_t num
     P.refs_out = refs_out;
     P.new_ids = new_ids;
     P.status = current_status_word();
+    P.ranks = num_blocks <= kOneCta ? 1 : kCluster;
     // how many blocks move is known on the device alone: a full grid where many could
     const int64_t work = num_blocks * X.chunks[X.n], tables = (entries + kCopyThreads - 1) / kCopyThreads;
     const cudaError_t e = launch_pair<CompactParams>(compact_plan_kernel, compact_apply_kernel<kFewTensors>, compact_apply_kernel<BSA_MAX_BLOCK_TENSORS>, P, X,

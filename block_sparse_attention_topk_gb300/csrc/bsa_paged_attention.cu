@@ -747,7 +747,8 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         constexpr int BYTES = BITS8 ? C::CODES : C::STAGE;
         uint32_t st = 0, use = 0, issued = 0, tiles = 0, loads = 0;
         bool ok = true;
-        const int outside = (int)(A.num_pages * kSubPage);       // past the tensor's end: arrives as zeros
+        // past the tensor's end (an empty cache's stands for a page): arrives as zeros
+        const int outside = (int)(max(A.num_pages, (int64_t)1) * kSubPage);
         auto copy = [&](const CUtensorMap* map, int token, int h) {
 #pragma unroll
             for (int p = 0; p < PANELS; ++p) {

@@ -104,6 +104,36 @@ def test_fork_patterns(cuda_device, parent, more, in_place):
     check_fork(State(11, 90, 8, cuda_device), parent, more, in_place)
 
 
+@pytest.mark.parametrize("which", [("table",), ("lens",), ("refs",), ("table", "refs"), ("lens", "refs")])
+def test_fork_with_some_outputs_in_place(cuda_device, which):
+    """Each output in the place of its input by itself: the same state."""
+    st = State(18, 90, 8, cuda_device)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_device)      # noqa: E731
+    parent, more = i32([3, 3, 0, -1, 0, 5]), i32([1, 140, 0, 3, 7, 1])
+    tensors, table, lens, refs = st.on_device()
+    want = bsa.bsa_fork_requests(tensors, table, lens, refs, parent, more)
+    mine, table, lens, refs = st.on_device()
+    given = {f"{k}_out": v for k, v in (("table", table), ("lens", lens), ("refs", refs)) if k in which}
+    got = bsa.bsa_fork_requests(mine, table, lens, refs, parent, more, **given)
+    for a, b in zip((*got, *mine), (*want, *tensors)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert all(any(g is v for g in got) for v in given.values())
+
+
+def test_parents_in_one_buffer_with_lengths(cuda_device):
+    """Inputs may share memory with each other; a row's parent may be any, several times over."""
+    st = State(19, 300, 8, cuda_device)
+    tensors, table, lens, refs = st.on_device()
+    both = torch.cat([torch.tensor([2, 2, 2, 5, 5, 2], dtype=torch.int32, device=cuda_device), lens % 50])
+    got = bsa.bsa_fork_requests(tensors, table, lens, refs, both[:6], both[6:])
+    contents = st.contents()
+    (rows, new_lens, new_refs), _ = blocks.fork(st.rows, st.lens, st.refs, [2, 2, 2, 5, 5, 2], [n % 50 for n in st.lens],
+                                                contents, st.MB)
+    assert np.array_equal(got[0].cpu().numpy(), st.table(rows, -1)) and got[1].tolist() == new_lens
+    assert got[2].tolist() == new_refs
+    same_tensors(tensors, contents)
+
+
 @pytest.mark.parametrize("rows", [0, 1, 3, 40])
 def test_fork_to_another_number_of_rows(cuda_device, rows):
     st = State(12, 200, 8, cuda_device)
