@@ -460,7 +460,9 @@ size_t bsa_paged_attention_workspace_bytes(int64_t T, int64_t H, int64_t G, int6
  * block_table[i, j / 128], page j % 128 / 16, slot j % 16.  Keys and values
  * that no row sees may be anything, NaN included.  A token past
  * max_blocks * 128 (BSA_STATUS_BAD_CONTEXT) or whose page lies outside
- * [0, num_pages) (BSA_STATUS_BAD_BLOCK_ID) takes no part.
+ * [0, num_pages) (BSA_STATUS_BAD_BLOCK_ID) takes no part.  Where the work of
+ * a row is cut depends on the whole batch, and with it the row's last bit; a
+ * call's bits are the same every time.
  *
  * Rows are owned, and placed at positions, as in bsa_append_kv_*:
  * _decode: T = num_reqs * decode_query_len rows, row t of request
