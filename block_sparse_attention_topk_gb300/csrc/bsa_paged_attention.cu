@@ -537,11 +537,11 @@ __device__ __forceinline__ uint32_t widen(uint32_t codes) {
     else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
     return h;
 }
-// Whether either half of a word of values is infinite or NaN, and the word with zeros there.
+// Nonzero in bits 15 and 31 where a half of a word of values is infinite or NaN (its exponent all
+// ones, so that one more carries); and the word with zeros there.
 template <bool HALF>
-__device__ __forceinline__ bool odd_word(uint32_t w) {
-    constexpr uint32_t E = HALF ? 0x7C00u : 0x7F80u;
-    return (w & E) == E || (w & E << 16) == E << 16;
+__device__ __forceinline__ uint32_t odd_word(uint32_t w) {
+    return (w & (HALF ? 0x7C007C00u : 0x7F807F80u)) + (HALF ? 0x04000400u : 0x00800080u);
 }
 template <bool HALF>
 __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
@@ -647,19 +647,22 @@ __device__ __forceinline__ void widen_stage(const uint4* from, uint8_t* to, int 
 // such.
 template <class C, bool HALF, class Seen>
 __device__ __forceinline__ bool clean_stage(uint8_t* stage, int me, Seen seen) {
-    bool odd = false;
     uint4* v = reinterpret_cast<uint4*>(stage);
-#pragma unroll 4
+    uint32_t odd = 0;
+    // the search alone is on the way of every such tile (its product waits for it)
+#pragma unroll 8
     for (int k = me; k < C::STAGE / 16; k += C::VALUE_THREADS) {
         const uint4 x = v[k];
-        if (!seen(k % (kAtom / 16) / 8)) {
-            v[k] = make_uint4(0, 0, 0, 0);
-        } else if (odd_word<HALF>(x.x) || odd_word<HALF>(x.y) || odd_word<HALF>(x.z) || odd_word<HALF>(x.w)) {
-            odd = true;
-            v[k] = make_uint4(finite_word<HALF>(x.x), finite_word<HALF>(x.y), finite_word<HALF>(x.z), finite_word<HALF>(x.w));
-        }
+        if (seen(k % (kAtom / 16) / 8)) odd |= odd_word<HALF>(x.x) | odd_word<HALF>(x.y) | odd_word<HALF>(x.z) | odd_word<HALF>(x.w);
+        else v[k] = make_uint4(0, 0, 0, 0);
     }
-    return odd;
+    if ((odd & 0x80008000u) == 0) return false;
+#pragma unroll 1
+    for (int k = me; k < C::STAGE / 16; k += C::VALUE_THREADS) {
+        const uint4 x = v[k];
+        v[k] = make_uint4(finite_word<HALF>(x.x), finite_word<HALF>(x.y), finite_word<HALF>(x.z), finite_word<HALF>(x.w));
+    }
+    return true;
 }
 
 // A row of queries from bf16 to half, multiplied by a power of two that takes its largest magnitude
