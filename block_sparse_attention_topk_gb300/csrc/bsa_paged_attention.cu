@@ -48,12 +48,11 @@
 // maxima, sums and outputs in the workspace in fp32, and a second launch joins
 // them in order.
 //
-// Measured (us): two prompts of up to 8192 tokens, 4 x 8 heads of 128, bf16, 1300
-// (1270 TFLOP/s); what bounds it is the chain of
-// one stream's softmax (about 1500 cycles a tile) and its products (1024) against the other's,
-// with the tensor pipe half busy.  128 requests of 16384 to 32768 tokens, 2 x 8 heads, bf16, 468: the copies, at
-// DRAM's rate.  The same in e4m3 512: shared memory, 224 KB a tile with the codes' way through it, and the chain of
-// a tile through four programs of warps that share an instruction cache.
+// Measured: two prompts of about 8192 tokens behind up to 8000, 4 x 8 heads of 128, bf16: 1287 us, 1456 TFLOP/s,
+// with the tensor pipe busy for 54 % of the cycles: what bounds it is the chain of one stream's softmax (1500
+// cycles a tile) and products (1024) against the other's.  128 requests of 16384 to 32768 tokens, 2 x 8 heads of
+// 128, bf16: 462 us, DRAM's rate.  The same in e4m3: 516 us, 3.1 TB/s; 224 KB go through shared memory a tile
+// (codes in, read, widened, read by the products), and the chain through four programs of warps is long.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -85,7 +84,6 @@ constexpr int kJoinThreads = 256;
 constexpr int kMinSteps = 2;             // the least part of a CTA, in steps
 
 struct PagedParams {
-    const uint16_t* q;
     uint16_t* out;
     const uint8_t* v;             // the cache's values, for the epilogue of rows that see infinities
     const float* ks;
@@ -1652,7 +1650,6 @@ int launch_paged(const bsa_paged_attention_args_t& a, PagedParams& A, cudaStream
         return BSA_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const bool bits8 = a.cache_dtype != BSA_DTYPE_BF16;
-    A.q = static_cast<const uint16_t*>(a.q);
     A.out = static_cast<uint16_t*>(a.out);
     A.v = static_cast<const uint8_t*>(a.v_cache);
     A.ks = a.k_scale;
