@@ -55,12 +55,19 @@ struct ForkParams {
     int64_t rows_in, rows_out, max_blocks, num_blocks;
     Head* head;
     int32_t* first;                   // [rows_in] lowest new row of each old one
-    int32_t* offset;                  // [rows_out] a row's first fresh block's place in `fresh`
-    int32_t* copied;                  // [rows_out] the unfinished block to copy, or -1
+    struct RowPlan* rows;             // [rows_out]
     int32_t* fresh;                   // fresh block ids in order
     int64_t fresh_cap;
     uint32_t* status;
     int32_t ranks;                    // CTAs of the plan: 1 or kCluster
+};
+
+// What the application needs of a row, in one read.
+struct alignas(32) RowPlan {
+    int32_t parent, shared, blocks;   // shared: the parent's blocks that are this row's too, its first
+    int32_t offset;                   // its first fresh block's place in `fresh`
+    int32_t copied;                   // the unfinished block to copy into that, or -1
+    int32_t pad[3];
 };
 
 struct CompactParams {
@@ -136,20 +143,23 @@ struct Row {
     int64_t base, len;     // the parent's tokens, and the row's
     int32_t parent;        // or -1
 };
-__device__ __forceinline__ Row new_row(const ForkParams& P, int64_t r, uint32_t* status) {
+__device__ __forceinline__ Row new_row(const ForkParams& P, const int32_t* lens, int64_t r, uint32_t* status) {
     Row w;
     const int32_t p = __ldg(P.parent + r);
     w.parent = p < 0 || p >= P.rows_in ? -1 : p;
     report_status(status, w.parent != p && p != -1, BSA_STATUS_BAD_CONTEXT);
-    w.base = w.parent < 0 ? 0 : checked_len(__ldcg(P.lens + w.parent), P.max_blocks, nullptr);
+    w.base = w.parent < 0 ? 0 : checked_len(__ldcg(lens + w.parent), P.max_blocks, nullptr);
     const int64_t more = P.new_tokens == nullptr ? 0 : __ldg(P.new_tokens + r);
     report_status(status, more < 0, BSA_STATUS_BAD_CONTEXT);
     w.len = checked_len(w.base + (more < 0 ? 0 : more), P.max_blocks, status);
     return w;
 }
 
+constexpr int kRowsKept = 1024;       // rows whose parents and lengths a CTA of the plan keeps
+
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParams P) {
     __shared__ int warps[32];
+    __shared__ Row kept[kRowsKept];
     const int tid = threadIdx.x, rank = blockIdx.x, all = rank * kPlanThreads + tid, everyone = P.ranks * kPlanThreads;
     const int lane = tid & 31, gwarp = all >> 5;
     asm volatile("griddepcontrol.launch_dependents;");
@@ -161,10 +171,15 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
     if (P.snap_lens != nullptr)
         for (int64_t i = all; i < P.rows_in; i += everyone) P.snap_lens[i] = P.lens_in[i];
     for (int64_t i = all; i < P.rows_in; i += everyone) P.first[i] = INT_MAX;
+    // a row is a chain of reads (its parent, that one's length): once for all phases where they fit.  From the
+    // caller's lengths: they are not written before the third phase
+    const bool keep = P.rows_out <= kRowsKept;
+    if (keep && tid < P.rows_out) kept[tid] = new_row(P, P.lens_in, tid, rank == 0 ? P.status : nullptr);
+    auto row = [&](int64_t r) { return keep ? kept[r] : new_row(P, P.lens, r, nullptr); };
     phase(P.ranks);
     // ---- references of whole blocks: a warp per old and per new row
     for (int64_t i = all; i < P.rows_out; i += everyone) {
-        const Row w = new_row(P, i, P.status);
+        const Row w = keep ? kept[i] : new_row(P, P.lens, i, P.status);
         if (w.parent >= 0) atomicMin(P.first + w.parent, (int)i);
     }
     for (int64_t r = gwarp; r < P.rows_in; r += everyone / 32) {
@@ -178,7 +193,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
         }
     }
     for (int64_t r = gwarp; r < P.rows_out; r += everyone / 32) {
-        const Row w = new_row(P, r, nullptr);
+        const Row w = row(r);
         if (w.parent < 0 || w.parent == r) continue;
         for (int64_t j = lane; j < w.base / kPageSize; j += 32) {
             const int32_t b = __ldcg(P.table + w.parent * P.max_blocks + j);
@@ -192,8 +207,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
         for (int64_t r0 = 0; r0 < P.rows_out; r0 += kPlanThreads) {
             const int64_t r = r0 + tid;
             int need = 0, copy = -1;
+            Row w{0, 0, -1};
             if (r < P.rows_out) {
-                const Row w = new_row(P, r, nullptr);
+                w = row(r);
                 need = (int)(blocks_of(w.len) - blocks_of(w.base));
                 if (w.base % kPageSize != 0) {
                     const int32_t b = __ldcg(P.table + w.parent * P.max_blocks + w.base / kPageSize);
@@ -209,8 +225,13 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
             int total;
             const int upto = before + cta_scan(need, warps, &total);
             if (r < P.rows_out) {
-                P.offset[r] = upto - need;
-                P.copied[r] = copy;
+                RowPlan p;
+                p.parent = w.parent;
+                p.shared = (int32_t)blocks_of(w.base) - (copy >= 0);
+                p.blocks = (int32_t)blocks_of(w.len);
+                p.offset = upto - need;
+                p.copied = copy;
+                P.rows[r] = p;
             }
             before += total;
         }
@@ -333,23 +354,21 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const ForkPara
     const int chunks = X.chunks[X.n];
     for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < P.rows_out * P.max_blocks; i += (int64_t)gridDim.x * kCopyThreads) {
         const int64_t r = i / P.max_blocks, j = i - r * P.max_blocks;
-        const Row w = new_row(P, r, nullptr);
-        const int64_t kept = blocks_of(w.base);
-        const int copied = __ldcg(P.copied + r) >= 0;
+        const RowPlan w = P.rows[r];
         int32_t b = -1;
-        if (j < kept - copied) {
+        if (j < w.shared) {
             b = __ldcg(P.table + w.parent * P.max_blocks + j);
-        } else if (j < blocks_of(w.len)) {
-            const int64_t k = __ldcg(P.offset + r) + (j - (kept - copied));
+        } else if (j < w.blocks) {
+            const int64_t k = w.offset + (j - w.shared);
             if (k < available) b = __ldcg(P.fresh + k);
         }
         P.table_out[i] = b;
     }
     for (int64_t i = blockIdx.x; i < P.rows_out * chunks; i += gridDim.x) {
         const int64_t r = i / chunks;
-        const int32_t src = __ldcg(P.copied + r), k = __ldcg(P.offset + r);
-        if (src < 0 || src == INT_MAX || k >= available) continue;
-        copy_chunk(X, (int)(i - r * chunks), src, __ldcg(P.fresh + k));
+        const RowPlan w = P.rows[r];
+        if (w.copied < 0 || w.copied == INT_MAX || w.offset >= available) continue;
+        copy_chunk(X, (int)(i - r * chunks), w.copied, __ldcg(P.fresh + w.offset));
     }
 }
 
@@ -395,8 +414,7 @@ size_t carve_fork(uint8_t* base, ForkParams* P, bool in_place) {
     Carve c{base};
     P->head = c.take<Head>(1);
     P->first = c.take<int32_t>(P->rows_in);
-    P->offset = c.take<int32_t>(P->rows_out);
-    P->copied = c.take<int32_t>(P->rows_out);
+    P->rows = c.take<RowPlan>(P->rows_out);
     // each row needs max_blocks fresh blocks at most
     const int64_t all = P->rows_out * P->max_blocks;
     P->fresh_cap = all < P->num_blocks ? all : P->num_blocks;

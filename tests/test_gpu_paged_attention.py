@@ -285,6 +285,28 @@ def test_long_rows(cuda_device, form, rows, H, G, D, fmt, window, sinks):
     assert not bad.any(), (bad.nonzero()[:4], got[bad][:4], want[bad][:4], float(bad.double().mean()))
 
 
+@pytest.mark.parametrize("fmt,form,H,G,D", [("bf16", "decode", 2, 4, 64), ("e4m3", "decode", 1, 8, 128), ("bf16", "varlen", 1, 3, 128),
+                                            ("e5m2", "varlen", 2, 2, 64), ("bf16", "decode", 1, 2, 256)])
+def test_many_sequences(cuda_device, fmt, form, H, G, D):
+    """More sequences than a CTA counts at a time, empty ones among them, first and last too."""
+    rng = np.random.default_rng(31)
+    if form == "decode":
+        lens = rng.integers(0, 300, 1300)
+        lens[:600] *= rng.integers(0, 2, 600)
+        lens[-3:] = 0
+        case = Case("decode", (1, lens.tolist()), H, G, D, fmt, seed=31)
+    else:
+        rows = [(int(n), int(p)) for n, p in zip(rng.integers(0, 4, 1100), rng.integers(0, 260, 1100))]
+        rows[:520] = [(0, 5)] * 520
+        rows[700] = (150, 40)
+        case = Case("varlen", (2, rows), H, G, D, fmt, seed=32)
+    got = case.run(cuda_device).double()
+    want, mag = _plain(case, cuda_device)
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2 * 2.0 ** -10) * (1 + 2.0 ** -8) * mag + 1e-30
+    assert torch.isfinite(got).all() and ((got - want).abs() <= tol).all()
+    assert (got[torch.from_numpy(case.pos < 0).to(got.device)] == 0).all()
+
+
 @pytest.mark.parametrize("fmt", list(KIND))
 def test_same_bits_again_in_a_graph_and_on_a_side_stream(cuda_device, fmt):
     """A call's bits do not depend on what else runs: again, captured and replayed
