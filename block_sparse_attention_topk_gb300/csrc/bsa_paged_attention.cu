@@ -876,9 +876,11 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         take_registers<C::OTHERS, false>();
         // ------------------------------------------------ MMAs
         if (elect_one()) {
-            const uint64_t q_desc = smem_desc(smem_addr(qsm), 0, 1024, 2);
-            const uint64_t k_desc = smem_desc(smem_addr(ring), 0, 1024, 2);
-            const uint64_t v_desc = smem_desc(smem_addr(ring), kAtom, 1024, 2);
+            // lower halves of operand descriptors; a byte offset adds offset / 16
+            const uint32_t q_desc = (uint32_t)smem_desc(smem_addr(qsm), 0, 1024, 2);
+            const uint32_t k_desc = (uint32_t)smem_desc(smem_addr(ring), 0, 1024, 2);
+            const uint32_t v_desc = (uint32_t)smem_desc(smem_addr(ring), kAtom, 1024, 2);
+            const uint32_t upper = (uint32_t)(smem_desc(0, 0, 1024, 2) >> 32);
             uint32_t st = 0, use = 0, p_phase = 0, fixes = 0, nq = 0, loads = 0;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity, quit, A.wait_ns); };
@@ -894,19 +896,19 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             };
             // scores of query tile m and one panel of a key stage
             auto scores = [&](int buf, int m, int p, uint32_t s) {
-                const uint64_t qd = q_desc + (m * C::Q_TILE + p * C::ATOMS * kAtom) / 16, kd = k_desc + s * (C::STAGE / 16);
+                const uint32_t qd = q_desc + (m * C::Q_TILE + p * C::ATOMS * kAtom) / 16, kd = k_desc + s * (C::STAGE / 16);
 #pragma unroll
                 for (int k = 0; k < C::PD / 16; ++k) {
                     const int at = (k / 4) * (kAtom / 16) + (k % 4) * 2;
-                    mma_f16(tmem + buf * kTile, qd + at, kd + at, A.s_idesc, p + k > 0);
+                    mma_f16(tmem + buf * kTile, qd + at, kd + at, upper, A.s_idesc, p + k > 0);
                 }
             };
             // outputs of half the probabilities in `buf` (tokens 0 to 63, or 64 to 127) and a value stage
             auto outputs = [&](int half, int buf, int o, int p, uint32_t s, bool more) {
-                const uint64_t vd = v_desc + s * (C::STAGE / 16);
+                const uint32_t vd = v_desc + s * (C::STAGE / 16);
 #pragma unroll
                 for (int k = half * 4; k < half * 4 + 4; ++k)
-                    mma_f16_ts(tmem + C::O_COL + o * C::D + p * C::PD, tmem + buf * kTile + k * 8, vd + k * 128, A.o_idesc, more || k > 0);
+                    mma_f16_ts(tmem + C::O_COL + o * C::D + p * C::PD, tmem + buf * kTile + k * 8, vd + k * 128, upper, A.o_idesc, more || k > 0);
             };
             auto probabilities = [&](uint64_t* bar, int buf) {
                 wait(&bar[buf], (p_phase >> buf) & 1);
