@@ -48,7 +48,7 @@
 // maxima, sums and outputs in the workspace in fp32, and a second launch joins
 // them in order.
 //
-// Measured: two prompts of about 8192 tokens behind up to 8000, 4 x 8 heads of 128, bf16: 1287 us, 1456 TFLOP/s,
+// Measured: two prompts of about 8192 tokens behind up to 8000, 4 x 8 heads of 128, bf16: 1247 us, 1504 TFLOP/s,
 // with the tensor pipe busy for 54 % of the cycles: what bounds it is the chain of one stream's softmax (1500
 // cycles a tile) and products (1024) against the other's.  128 requests of 16384 to 32768 tokens, 2 x 8 heads of
 // 128, bf16: 462 us, DRAM's rate.  The same in e4m3: 516 us, 3.1 TB/s; 224 KB go through shared memory a tile
