@@ -572,6 +572,14 @@ PyObject* give3(const Tensor (&made)[3], PyObject* const* given) {
     return out;
 }
 
+// A call's own scratch from PyTorch's allocator, which keeps it to the stream that the call runs on (in
+// a capture, to the graph): a microsecond less than the package's shared workspace, for kernels of ten.
+void own_scratch(const Tensor** ws, Tensor* own, const Tensor& like, size_t need) {
+    if (*ws != nullptr) return;
+    *own = at::empty({(int64_t)need}, like.options().dtype(at::kByte).requires_grad(false));
+    *ws = own;
+}
+
 // fork(tensors, block_table, seq_lens, block_refs, parent, new_tokens, table_out, lens_out, refs_out, workspace)
 //   -> (table_out, lens_out, refs_out)
 PyObject* py_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -595,8 +603,8 @@ PyObject* py_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !int_output(a[7], "lens_out", device, *table, {R2}, &made[1], &out[1]) ||
         !int_output(a[8], "refs_out", device, *table, {N}, &made[2], &out[2]))
         return nullptr;
-    Workspace held;
-    if (!held.take(&ws, a[1], bsa_fork_workspace_bytes(R, R2, MB, N))) return nullptr;
+    Tensor own;
+    own_scratch(&ws, &own, *table, bsa_fork_workspace_bytes(R, R2, MB, N));
     void* stream;
     if (!stream_of(device, &stream)) return nullptr;
     const auto ints = [](const Tensor* t) { return static_cast<const int32_t*>(data(t)); };
@@ -636,8 +644,8 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !int_output(a[5], "refs_out", device, *table, {N}, &made[1], &out[1]) ||
         !int_output(a[6], "new_ids", device, *table, {N}, &made[2], &out[2]))
         return nullptr;
-    Workspace held;
-    if (!held.take(&ws, a[1], bsa_compact_workspace_bytes(N))) return nullptr;
+    Tensor own;
+    own_scratch(&ws, &own, *table, bsa_compact_workspace_bytes(N));
     void* stream;
     if (!stream_of(device, &stream)) return nullptr;
     const auto ints = [](const Tensor* t) { return static_cast<const int32_t*>(data(t)); };
