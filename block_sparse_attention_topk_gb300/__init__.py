@@ -793,9 +793,9 @@ def bsa_fork_requests(tensors, block_table: torch.Tensor, seq_lens: torch.Tensor
     (none for -1) and room for new_tokens[r] more.  Forks, reorders, grows and
     frees requests in one call without a synchronisation: full blocks are
     shared, an unfinished last block goes to the lowest row that descends from
-    its request and is copied for the others, in every one of `tensors` (each
-    [num_blocks, ...] or [8 * num_blocks, ...]: caches, scales, pooled index
-    keys, of every layer).  block_table int32 [num_reqs, max_blocks], seq_lens
+    its request and is copied for the others, in every one of `tensors` (a
+    list or other iterable; each [num_blocks, ...] or [8 * num_blocks, ...]:
+    caches, scales, pooled index keys, of every layer).  block_table int32 [num_reqs, max_blocks], seq_lens
     int32 [num_reqs], block_refs int32 [num_blocks] (how many rows hold each
     block), parent and new_tokens int32 [num_out].  Returns (table_out,
     lens_out, refs_out), by default new; block_table, seq_lens and block_refs

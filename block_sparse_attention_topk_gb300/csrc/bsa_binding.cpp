@@ -13,6 +13,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/util/SmallVector.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -518,14 +519,16 @@ PyObject* py_paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // The tensors that a block's id stands for: contiguous, num_blocks blocks each along
-// their first dimension (or eight pages a block).
+// their first dimension (or eight pages a block).  Held until the call is over: what an
+// iteration makes (views of a stacked tensor, a generator's) nobody else may hold, and
+// another thread may change a list while the GIL is released.
 struct BlockTensors {
     bsa_block_tensor_t t[BSA_MAX_BLOCK_TENSORS];
-    const Tensor* of[BSA_MAX_BLOCK_TENSORS];
+    c10::SmallVector<Tensor, 16> of;
     int32_t n = 0;
 
     bool take(PyObject* list, const at::Device& device, int64_t num_blocks) {
-        PyObject* seq = PySequence_Fast(list, "tensors must be a list or tuple of tensors");
+        PyObject* seq = PySequence_Fast(list, "tensors must be a list, tuple or other iterable of tensors");
         if (seq == nullptr) return false;
         const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq);
         bool ok = count <= BSA_MAX_BLOCK_TENSORS || fail("more than %d tensors", BSA_MAX_BLOCK_TENSORS);
@@ -539,14 +542,14 @@ struct BlockTensors {
                           (long long)i, device.str().c_str(), (long long)num_blocks);
                 break;
             }
-            of[n] = x;
+            of.push_back(*x);
             t[n++] = bsa_block_tensor_t{x->data_ptr(), num_blocks > 0 ? (int64_t)x->nbytes() / num_blocks : 0};
         }
-        Py_DECREF(seq);      // the list, or a copy of it, whose tensors the caller holds
+        Py_DECREF(seq);
         return ok;
     }
     void moved() const {
-        for (int32_t i = 0; i < n; ++i) changed(of[i]);
+        for (const Tensor& x : of) changed(&x);
     }
 };
 
