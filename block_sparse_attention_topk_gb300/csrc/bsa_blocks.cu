@@ -361,7 +361,9 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const ForkPara
         const RowPlan w = P.rows[r];
         int32_t b = -1;
         if (j < w.shared) {
+            // the plan reads the full blocks of requests that change rows alone
             b = __ldcg(P.table + w.parent * P.max_blocks + j);
+            report_status(P.status, b < 0 || b >= P.num_blocks, BSA_STATUS_BAD_BLOCK_ID);
         } else if (j < w.blocks) {
             const int64_t k = w.offset + (j - w.shared);
             if (k < available) b = __ldcg(P.fresh + k);
