@@ -383,9 +383,12 @@ __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const Compa
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t moves = __ldcg(&P.head->needed);
     const int chunks = X.chunks[X.n];
+    // row by row, as a table of no columns has rows too
+    for (int64_t r = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; r < P.rows; r += (int64_t)gridDim.x * kCopyThreads)
+        checked_len(__ldg(P.lens + r), P.max_blocks, P.status);
     for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < P.rows * P.max_blocks; i += (int64_t)gridDim.x * kCopyThreads) {
         const int64_t r = i / P.max_blocks, j = i - r * P.max_blocks;
-        const int64_t len = checked_len(__ldg(P.lens + r), P.max_blocks, j == 0 ? P.status : nullptr);
+        const int64_t len = checked_len(__ldg(P.lens + r), P.max_blocks, nullptr);
         int32_t b = -1;
         if (j < blocks_of(len)) {
             const int32_t old = P.table[i];

@@ -1,6 +1,5 @@
 """What forks and compactions report of a state that is not right: nothing stays unsaid
 because a request keeps its row, or because the table is empty."""
-import numpy as np
 import pytest
 import torch
 
@@ -41,3 +40,18 @@ def test_bad_entries_of_requests_that_keep_their_rows(cuda_device, word, entry, 
         bsa.bsa_fork_requests(tensors, table, lens, refs, i32(range(6)))
         assert bsa.bsa_read_status() == 0
     assert seen > 0
+
+
+@pytest.mark.parametrize("R", [1, 7, 3000])
+def test_lengths_past_a_table_without_columns(cuda_device, word, R):
+    """Requests that hold tokens in a table of no blocks: forks and compactions say so."""
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device=cuda_device)      # noqa: E731
+    table, refs, parent = z(R, 0), z(20), torch.arange(R, dtype=torch.int32, device=cuda_device)
+    last = z(R)
+    last[-1] = 5
+    for lens, bad in ((z(R), False), (z(R) + 1, True), (z(R) - 1, True), (last, True)):
+        want = bsa.BSA_STATUS_BAD_CONTEXT if bad else 0
+        out = bsa.bsa_compact_blocks([], table, lens, refs)
+        assert bsa.bsa_read_status() == want and out[0].shape == (R, 0) and int(out[1].sum()) == 0
+        out = bsa.bsa_fork_requests([], table, lens, refs, parent)
+        assert bsa.bsa_read_status() == want and int(out[1].abs().sum()) == 0
