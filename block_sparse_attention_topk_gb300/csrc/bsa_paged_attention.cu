@@ -824,15 +824,30 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             int before = 0;       // the last tile's token coordinate
             const bool ahead = NS == 1 || P.split;       // keys run one tile ahead of values
             // 8 bits: scales of two tiles, lanes 0 to 15 and 16 to 31, the pages' for keys, then for
-            // values; read two tiles ahead, as they may come from DRAM
+            // values; read two tiles ahead, as they may come from DRAM.  A page that no row of the item sees may
+            // have any: it counts as one of scale zero.  One that is seen and has a value scale that is not
+            // finite or is negative makes the scores of its tokens NaN, so that just the rows that see it are.
             float scale = 0.f;
+            const int seen_from = P.lo;
             auto read_scales = [&](int k) {
                 const int t = k + (lane >> 4), pg = lane & 7;
                 const int id = __shfl_sync(kFull, ids, t & 31);
-                scale = 0.f;
-                if (t >= n || id < 0 || (int64_t)id * kPagesPerBlock + pg >= A.num_pages) return;
-                const int64_t where = ((int64_t)id * kPagesPerBlock + pg) * A.H + h;
-                scale = lane & 8 ? log2f(__ldg(A.vs + where)) : __ldg(A.ks + where) * A.scale_log2e;
+                scale = lane & 8 ? -INFINITY : 0.f;
+                bool odd = false;
+                const int token = t < n ? r.tile(i0 + t) * kTile + pg * kSubPage : r.end;
+                const bool seen = token < r.end && (token + kSubPage > seen_from || token < A.sinks);
+                if (seen && id >= 0 && (int64_t)id * kPagesPerBlock + pg < A.num_pages) {
+                    const int64_t where = ((int64_t)id * kPagesPerBlock + pg) * A.H + h;
+                    if (lane & 8) {
+                        const float x = __ldg(A.vs + where);
+                        odd = !(x >= 0.f && x < INFINITY);
+                        scale = odd ? -INFINITY : log2f(x);
+                    } else {
+                        scale = __ldg(A.ks + where) * A.scale_log2e;
+                    }
+                }
+                const uint32_t odds = __ballot_sync(kFull, odd);
+                if (odds >> (lane | 8) & 1 && !(lane & 8)) scale = NAN;
             };
             for (int k = 0; ok && k <= n; ++k) {
                 int at = 0;
@@ -1288,7 +1303,8 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             const float k = !BITS8 ? A.scale_log2e : g == 0 ? ks.x : ks.y;
-                            const float f = BITS8 ? ex2((g == 0 ? lv.x : lv.y) + unit) : 1.f;
+                            // of a page that the row does not see it may pass fp32's range, and meets zeros
+                            const float f = BITS8 ? ex2(fminf((g == 0 ? lv.x : lv.y) + unit, 127.f)) : 1.f;
 #pragma unroll
                             for (int j = 16 * g; j < 16 * g + 16; j += 2) {
                                 float a, b;

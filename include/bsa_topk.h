@@ -426,8 +426,9 @@ typedef struct bsa_paged_attention_args {
     void* out;
     /* the cache, [num_pages, 16, H, D] contiguous, 16-byte aligned, of
      * cache_dtype BSA_DTYPE_BF16, BSA_DTYPE_E4M3 or BSA_DTYPE_E5M2;
-     * num_pages < 2^27.  8 bits: float [num_pages, H] scales, finite, not
-     * negative, k = code * k_scale[page, h], v likewise (NULL for bf16). */
+     * num_pages < 2^27.  8 bits: float [num_pages, H] scales, k = code *
+     * k_scale[page, h], v likewise (NULL for bf16).  Those of pages that a
+     * row sees are finite and not negative (others make the row NaN). */
     int32_t cache_dtype;
     const void* k_cache;
     const void* v_cache;
@@ -457,8 +458,8 @@ size_t bsa_paged_attention_workspace_bytes(int64_t T, int64_t H, int64_t G, int6
  * cache, the new tokens themselves among it (append them first):
  *   out[t, h, g] = sum_j softmax_j(scale * q[t, h, g] . k_j) v_j
  * over the tokens j that row t sees, token j of sequence i lying in block
- * block_table[i, j / 128], page j % 128 / 16, slot j % 16.  Keys and values
- * that no row sees may be anything, NaN included.  A token past
+ * block_table[i, j / 128], page j % 128 / 16, slot j % 16.  Keys, values
+ * and page scales that no row sees may be anything, NaN included.  A token past
  * max_blocks * 128 (BSA_STATUS_BAD_CONTEXT) or whose page lies outside
  * [0, num_pages) (BSA_STATUS_BAD_BLOCK_ID) takes no part.  Where the work of
  * a row is cut depends on the whole batch, and with it the row's last bit; a
