@@ -26,18 +26,23 @@
 //             stages;
 //  MMAs       one thread issues them.  The product of half the probabilities
 //             starts under the exponentials of the others;
-//  values     two warps go over the value rows of tiles that some rows do not see
+//  values     (bf16) two warps go over the value rows of tiles that some rows do not see
 //             in full: 0 * NaN is NaN, so what no row sees (the unused end of a block)
 //             is set to zero, and so is what is not finite, which the epilogue gives
 //             back to the rows that do see it;
-//  widening   (8 bits) two groups of four warps turn codes into halves, exactly,
-//             on their way from a ring of codes to the ring, a stage each, and go over
-//             the values as they do.  Queries become halves too, a row divided by a power of two.
-//             A key page's scale multiplies its scores, a value page's its probabilities,
-//             so any scale is as exact as a power of two.
-// Rounding: scores, maxima, sums and outputs are fp32.  Probabilities are rounded
-// once, to the type of the values beside them: bf16 (2^-8 of each, as much as the
-// rounding of the output, and averaged over tokens) or, with 8 bits, half (2^-12).
+//  widening   (8 bits) two groups of four warps turn codes into 16 bits, exactly, on
+//             their way from a ring of codes to the ring, a stage each: keys into halves,
+//             values into bf16, where what is not finite comes out as a number and is noted for
+//             the epilogue.  Queries become halves too, a row divided by a power of two.
+//             A key page's scale multiplies its scores, a value page's its probabilities.
+// Rounding: scores, maxima, sums and outputs are fp32.  From a bf16 cache probabilities
+// are rounded once, to bf16 (2^-8 of each, as much as the rounding of the output, and
+// averaged over tokens).  With 8 bits a token's weight, its probability times its page's
+// scale, is two bf16 terms, the second of what the rounding of the first leaves (2^-16 of
+// it; with its exponentials and the logarithm of the scale 2^-15).  Both have fp32's range:
+// the output may be made of weights far below the row's largest, where that one's value is
+// zero (an attention sink, a page of zeros, to which the append gives the scale 1).  One
+// half had a fixed step of 2^-24 of the largest there.
 // Where the CTAs cut an item depends on the whole batch, so a row's last bit may too; a
 // call's bits are the same every time.
 //
@@ -48,11 +53,11 @@
 // maxima, sums and outputs in the workspace in fp32, and a second launch joins
 // them in order.
 //
-// Measured: two prompts of about 8192 tokens behind up to 8000, 4 x 8 heads of 128, bf16: 1247 us, 1504 TFLOP/s,
-// with the tensor pipe busy for 54 % of the cycles: what bounds it is the chain of one stream's softmax (1500
-// cycles a tile) and products (1024) against the other's.  128 requests of 16384 to 32768 tokens, 2 x 8 heads of
-// 128, bf16: 462 us, DRAM's rate.  The same in e4m3: 516 us, 3.1 TB/s; 224 KB go through shared memory a tile
-// (codes in, read, widened, read by the products), and the chain through four programs of warps is long.
+// Measured: two prompts of about 8192 tokens behind up to 8000, 4 x 8 heads of 128, bf16: 1240 us, 1512 TFLOP/s;
+// what bounds it is the chain of one stream's softmax (1500 cycles a tile) and products (1024) against the
+// other's.  1639 tokens at the end of a context of 114500, 2 x 8 heads of 128, e4m3: 1849 us, 865 TFLOP/s, of which
+// second terms are about 100 and values in bf16 in place of half 200; 224 KB go through shared memory a tile (codes in,
+// read, widened, read by the products), and the chain through four programs of warps is long.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -80,6 +85,8 @@ constexpr int kInfo = 16;                // tiles whose facts are kept: more tha
 constexpr int kPortions = 4;             // portions announced ahead
 constexpr int kWindow = 512;             // sequences whose units a CTA holds at a time while it finds its part
 constexpr float kGrow = 8.f;             // log2 of what a maximum may grow by before O is rescaled
+constexpr float kLift = 60.f;            // 8 bits: log2 of a row's largest probability and weight in their units
+constexpr float kFar = 100.f;            // 8 bits: log2 of how far a page's exponentials may lie below its probabilities
 constexpr int kJoinThreads = 256;
 constexpr int kMinSteps = 2;             // the least part of a CTA, in steps
 
@@ -152,8 +159,7 @@ struct Cfg {
     static constexpr int MINE = MORE < 255 ? MORE : 248;
     // Units of work: a step in which each stream has its own rows of one tile, one in which both have the
     // same rows of two tiles, and an item's beginning and end.  With 8 bits the second widens twice the codes:
-    // 1.25 times as long (without, the CTAs with such steps were last: 1650 us instead of 1510 for 1639
-    // tokens at the end of a context of 114500, 2 x 8 heads).
+    // 1.25 times as long (without, the CTAs with such steps were last).
     static constexpr int PAIR_UNITS = 4, SPLIT_UNITS = BITS8 && NS == 2 ? 5 : 4, END_UNITS = 4;
     static constexpr uint32_t O_COL = 256;                 // TMEM: scores in columns 0 to 255, outputs behind
     static_assert(RING >= 3 && RING <= kMaxStages && CRING <= kMaxStages && CRING % 2 == 0, "rings; the groups take stages of codes in turn");
@@ -199,6 +205,7 @@ struct Shared {
     int valid[kInfo];                          // tokens of a tile inside the cache
     Portion portion[kPortions];
     int poison[kPortions];                     // 1 + the number of the last portion with values that are not finite
+    uint32_t odd_dims[kPortions][2][8];        // 8 bits: dimensions with those in tiles that all rows see: that add infinity, minus infinity (NaN: both)
     uint8_t q_power[2][2][kRows];              // 8 bits: the exponent (by 127) of what a row of queries was divided by, of two portions
     Start start;
     uint32_t tmem_base;
@@ -527,6 +534,22 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
+// four 8-bit codes as bf16, exactly: their bits in place, times what the exponents' biases differ by.
+// Codes that are not finite come out as numbers (480; 2^16 and more), which odd_codes tells.
+template <bool E4M3>
+__device__ __forceinline__ void widen_values(uint32_t w, uint32_t& a, uint32_t& b) {
+    const uint32_t hi = (w & 0x80808080u) | (E4M3 ? w >> 4 & 0x07070707u : w >> 3 & 0x0F0F0F0Fu);
+    const uint32_t lo = E4M3 ? w << 4 & 0xF0F0F0F0u : w << 5 & 0xE0E0E0E0u;
+    constexpr uint32_t UP = E4M3 ? 0x7B807B80u : 0x77807780u;      // 2^120, 2^112
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(__byte_perm(lo, hi, 0x5140)), "r"(UP));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(__byte_perm(lo, hi, 0x7362)), "r"(UP));
+}
+// `odd` with bit 7 of a byte set whose code is infinite or NaN: all ones from some bit up to bit 6, so that one more carries.  (The
+// byte behind such a code may be set with it.)
+template <bool E4M3>
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w, uint32_t odd) {
+    return odd | ((w + (E4M3 ? 0x01010101u : 0x04040404u)) ^ w);
+}
 // two 8-bit codes as halves, exactly (NaN and infinities too)
 template <bool E4M3>
 __device__ __forceinline__ uint32_t widen(uint32_t codes) {
@@ -537,13 +560,9 @@ __device__ __forceinline__ uint32_t widen(uint32_t codes) {
 }
 // Nonzero in bits 15 and 31 where a half of a word of values is infinite or NaN (its exponent all
 // ones, so that one more carries); and the word with zeros there.
-template <bool HALF>
-__device__ __forceinline__ uint32_t odd_word(uint32_t w) {
-    return (w & (HALF ? 0x7C007C00u : 0x7F807F80u)) + (HALF ? 0x04000400u : 0x00800080u);
-}
-template <bool HALF>
+__device__ __forceinline__ uint32_t odd_word(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
-    constexpr uint32_t E = HALF ? 0x7C00u : 0x7F80u;
+    constexpr uint32_t E = 0x7F80u;
     if ((w & E) == E) w &= 0xFFFF0000u;
     if ((w & E << 16) == E << 16) w &= 0x0000FFFFu;
     return w;
@@ -579,11 +598,16 @@ __device__ __forceinline__ const Portion* Reader::next(Shared& S, unsigned long 
 __device__ __forceinline__ void Reader::done(Shared& S) { mbar_arrive(&S.portion_empty[number++ % kPortions]); }
 
 // Adds what the values' warps took out to the row's outputs [d0, d0 + 16): values that
-// are not finite of tokens that the row sees.
+// are not finite of tokens that the row sees.  With 8 bits `dims` has those of the tiles that all rows see.
 template <class C, bool BITS8>
-__device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion& P, int stream, int hi, int lo, int d0, float* o) {
+__device__ __noinline__ void add_odd_values(const PagedParams& A, const Portion& P, const uint32_t (&dims)[2][8], int hi, int lo, int d0, float* o) {
+    if constexpr (BITS8) {
+        for (int k = 0; k < 16; ++k) {
+            if (dims[0][d0 / 32] >> (d0 % 32 + k) & 1) o[k] += INFINITY;
+            if (dims[1][d0 / 32] >> (d0 % 32 + k) & 1) o[k] -= INFINITY;
+        }
+    }
     for (int i = P.i0; i < P.i1; ++i) {
-        if (P.split && ((i - P.i0) & 1) != stream) continue;
         const int tile = P.r.tile(i);
         if (P.item.has(tile)) continue;      // as the values' warps have it
         const int64_t id = __ldg(A.table + (int64_t)P.b * A.max_blocks + tile);
@@ -617,7 +641,7 @@ __device__ __forceinline__ uint8_t* place(uint8_t* to, int k, int half) {
     return to + (c / 4) * kAtom + row * 128 + ((((c % 4) * 2 + half) ^ (row & 7)) << 4);
 }
 
-// A stage of codes widened by 128 threads.
+// A stage of key codes widened by 128 threads.
 template <class C, bool E4M3>
 __device__ __forceinline__ void widen_stage(const uint4* from, uint8_t* to, int me) {
     constexpr int EACH = C::CODES / 16 / 128, BATCH = 2;
@@ -641,9 +665,62 @@ __device__ __forceinline__ void widen_stage(const uint4* from, uint8_t* to, int 
         }
     }
 }
+// The tokens of a tile that some row of an item sees: rows before `end` that lie at `window` or behind, or before `sinks`.
+struct Seen {
+    int end, window, sinks;
+    __device__ __forceinline__ bool has(int row) const { return row < end && (row >= window || row < sinks); }
+};
+
+// What is not finite among a thread's value codes, of tokens that some row sees; whether there was such.  In a tile that all
+// rows see (`dims`) it goes down by dimension, from d0 on.
+template <class C, bool E4M3>
+__device__ __noinline__ bool note_odd_codes(const uint4* from, int me, Seen seen, uint32_t (*dims)[8], int d0, const float* log_scales) {
+    constexpr int PER_ROW = C::PD / 16;
+    bool any = false;
+    for (int k = me; k < C::CODES / 16; k += 128) {
+        const int row = k / PER_ROW;
+        if (!seen.has(row)) continue;
+        const uint4 x = from[k];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int e = 0; e < 16; ++e) {
+            const uint32_t code = w[e / 4] >> (e % 4 * 8) & 0xFF, low = code & 0x7F;
+            if (E4M3 ? low != 0x7F : low < 0x7C) continue;
+            any = true;
+            if (dims == nullptr) continue;
+            const bool nan = E4M3 || low > 0x7C || log_scales[row / kSubPage] == -INFINITY;      // times a scale of zero
+            const int d = d0 + k % PER_ROW * 16 + e;
+            for (int sign = 0; sign < 2; ++sign)
+                if (nan || (int)(code >> 7) == sign) atomicOr(&dims[sign][d / 32], 1u << (d % 32));
+        }
+    }
+    return any;
+}
+
+// A stage of value codes widened by 128 threads; whether some of this thread's may not be finite.  16 codes at a time: with
+// 32 the instruction cache makes more of it than the latency (production decode 161 instead of 166 us).
+template <class C, bool E4M3>
+__device__ __forceinline__ bool widen_value_stage(const uint4* from, uint8_t* to, int me) {
+    uint32_t odd = 0;
+#pragma unroll 1
+    for (int k = me; k < C::CODES / 16; k += 128) {
+        const uint4 x = from[k];
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            widen_values<E4M3>(in[e], w[2 * e], w[2 * e + 1]);
+            odd = odd_codes<E4M3>(in[e], odd);
+        }
+        const int other = k % (C::PD / 16) / 4 & 1;
+        const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(place<C>(to, k, other)) = other ? b : a;
+        *reinterpret_cast<uint4*>(place<C>(to, k, 1 - other)) = other ? a : b;
+    }
+    return (odd & 0x80808080u) != 0;
+}
 // Value rows that no row sees set to zero, and what is not finite in the others; whether there was
 // such.
-template <class C, bool HALF, class Seen>
+template <class C, class Seen>
 __device__ __forceinline__ bool clean_stage(uint8_t* stage, int me, Seen seen) {
     uint4* v = reinterpret_cast<uint4*>(stage);
     uint32_t odd = 0;
@@ -651,14 +728,14 @@ __device__ __forceinline__ bool clean_stage(uint8_t* stage, int me, Seen seen) {
 #pragma unroll 8
     for (int k = me; k < C::STAGE / 16; k += C::VALUE_THREADS) {
         const uint4 x = v[k];
-        if (seen(k % (kAtom / 16) / 8)) odd |= odd_word<HALF>(x.x) | odd_word<HALF>(x.y) | odd_word<HALF>(x.z) | odd_word<HALF>(x.w);
+        if (seen(k % (kAtom / 16) / 8)) odd |= odd_word(x.x) | odd_word(x.y) | odd_word(x.z) | odd_word(x.w);
         else v[k] = make_uint4(0, 0, 0, 0);
     }
     if ((odd & 0x80008000u) == 0) return false;
 #pragma unroll 1
     for (int k = me; k < C::STAGE / 16; k += C::VALUE_THREADS) {
         const uint4 x = v[k];
-        v[k] = make_uint4(finite_word<HALF>(x.x), finite_word<HALF>(x.y), finite_word<HALF>(x.z), finite_word<HALF>(x.w));
+        v[k] = make_uint4(finite_word(x.x), finite_word(x.y), finite_word(x.z), finite_word(x.w));
     }
     return true;
 }
@@ -798,6 +875,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             if (number >= kPortions && !mbar_wait(&S.portion_empty[slot], (number / kPortions - 1) & 1, &none, A.wait_ns)) break;
             Portion& P = S.portion[slot];
             bool more = false;
+            if (BITS8 && lane < 16) S.odd_dims[slot][lane >> 3][lane & 7] = 0;
             if (lane == 0) more = walk.next(A, S.start, &P);
             more = __shfl_sync(kFull, more, 0);
             __syncwarp();
@@ -918,12 +996,17 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     mma_f16(tmem + buf * kTile, qd + at, kd + at, upper, A.s_idesc, p + k > 0);
                 }
             };
-            // outputs of half the probabilities in `buf` (tokens 0 to 63, or 64 to 127) and a value stage
+            // outputs of half the probabilities in `buf` (tokens 0 to 63, or 64 to 127) and a value stage; with
+            // 8 bits of both terms
             auto outputs = [&](int half, int buf, int o, int p, uint32_t s, bool more) {
                 const uint32_t vd = v_desc + s * (C::STAGE / 16);
+                constexpr int TERMS = BITS8 ? 2 : 1;
 #pragma unroll
                 for (int k = half * 4; k < half * 4 + 4; ++k)
-                    mma_f16_ts(tmem + C::O_COL + o * C::D + p * C::PD, tmem + buf * kTile + k * 8, vd + k * 128, upper, A.o_idesc, more || k > 0);
+#pragma unroll
+                    for (int t = 0; t < TERMS; ++t)
+                        mma_f16_ts(tmem + C::O_COL + o * C::D + p * C::PD, tmem + buf * kTile + (k * TERMS + t) * 8, vd + k * 128, upper,
+                                   A.o_idesc, more || k > 0 || t > 0);
             };
             auto probabilities = [&](uint64_t* bar, int buf) {
                 wait(&bar[buf], (p_phase >> buf) & 1);
@@ -1053,28 +1136,22 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
         __syncwarp();
     } else if (warp >= C::VALUES) {
         take_registers<C::OTHERS, false>();
-        // ------------------------------------------------ values, and codes to halves
+        // ------------------------------------------------ values, and codes to 16 bits
         const int me = (tid - C::VALUES * 32) % C::VALUE_THREADS, group = (warp - C::VALUES) / 4;
         bool ok = true;
-        uint32_t st = group, use = 0, cst = group, cuse = 0, stages = 0, fixes = 0, loads = 0;
+        uint32_t st = group, use = 0, cst = group, cuse = 0, stages = 0, fixes = 0, loads = 0, tiles = 0;
         while (const Portion* at = reader.next(S, A.wait_ns)) {
             const Portion& P = *at;
             const int n = P.i1 - P.i0;
             const bool ahead = NS == 1 || P.split;
-            // sets a stage of the tile's values right where some row of the item does not see it in full
-            auto clean = [&](uint8_t* stage, int tile) {
-                const int end = P.r.end, lo = P.lo;
-                const bool odd = clean_stage<C, BITS8>(stage, me, [&](int row) {
-                    const int j = tile * kTile + row;
-                    return j < end && (j >= lo || j < A.sinks);
-                });
-                if (odd) *(volatile int*)&S.poison[P.number % kPortions] = P.number + 1;
-            };
+            auto seen = [&](int tile) { return Seen{P.r.end - tile * kTile, P.lo - tile * kTile, A.sinks - tile * kTile}; };
+            auto poison = [&]() { *(volatile int*)&S.poison[P.number % kPortions] = P.number + 1; };
             if constexpr (!BITS8) {
                 for (int i = 0; ok && i < n; ++i) {
                     const int tile = P.r.tile(P.i0 + i);
                     if (P.item.has(tile)) continue;
                     // K and V stages in the copies' order: those before this tile's values
+                    const Seen rows = seen(tile);
                     const uint32_t s0 = st + (ahead ? min(i + 2, n) + i : 2 * i + 1) * PANELS;
                     // the MMAs' thread has them in the ring, and waits
                     ok = mbar_wait(&S.to_fix, fixes & 1, quit, A.wait_ns);
@@ -1083,7 +1160,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         const uint32_t s = (s0 + p) % RING, u = use + (s0 + p) / RING;
                         ok = ok && mbar_wait(&S.full[s], u & 1, quit, A.wait_ns);
                         ok = __all_sync(kFull, ok);
-                        if (ok) clean(ring + s * C::STAGE, tile);
+                        if (ok && clean_stage<C>(ring + s * C::STAGE, me, [&](int row) { return rows.has(row); })) poison();
                     }
                     if (!ok) break;
                     fence_async_smem();
@@ -1107,14 +1184,21 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     if (!ok) break;
                     const uint4* from = reinterpret_cast<const uint4*>(codes + cst * C::CODES);
                     uint8_t* to = ring + st * C::STAGE;
-                    if (A.cache_dtype == BSA_DTYPE_E4M3) widen_stage<C, true>(from, to, me);
-                    else widen_stage<C, false>(from, to, me);
                     if (value) {
-                        const int tile = P.r.tile(P.i0 + k);
-                        if (!P.item.has(tile)) {
-                            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
-                            clean(to, tile);
+                        const bool e4m3 = A.cache_dtype == BSA_DTYPE_E4M3;
+                        const bool odd = e4m3 ? widen_value_stage<C, true>(from, to, me) : widen_value_stage<C, false>(from, to, me);
+                        if (odd) {
+                            const int tile = P.r.tile(P.i0 + k), d0 = q % PANELS * C::PD;
+                            uint32_t(*dims)[8] = P.item.has(tile) ? S.odd_dims[P.number % kPortions] : nullptr;
+                            const float* log_scales = S.scale[(tiles + k) % kInfo][1];
+                            if (e4m3 ? note_odd_codes<C, true>(from, me, seen(tile), dims, d0, log_scales)
+                                     : note_odd_codes<C, false>(from, me, seen(tile), dims, d0, log_scales))
+                                poison();
                         }
+                    } else if (A.cache_dtype == BSA_DTYPE_E4M3) {
+                        widen_stage<C, true>(from, to, me);
+                    } else {
+                        widen_stage<C, false>(from, to, me);
                     }
                     mbar_arrive(&S.code_empty[cst]);
                     fence_async_smem();
@@ -1144,6 +1228,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                     }
                 }
                 stages += 2 * n * PANELS;
+                tiles += n;
             }
             __syncwarp();
             if (lane == 0) reader.done(S);
@@ -1174,8 +1259,9 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 lo = A.window > 0 ? (int)(pos - A.window + 1 < 0 ? 0 : pos - A.window + 1 < top ? pos - A.window + 1 : top) : 0;
             }
             // The row's sums are in units of 2^mx and its outputs in units of 2^mo: with bf16 the same; with 8
-            // bits mo goes by the largest probability times value scale, so that those are halves of
-            // 11 bits in either's place, whatever the scales of pages that do not count.
+            // bits mo goes by the largest weight, a probability times its page's scale.  Both units lie 2^kLift
+            // below: a probability may fall 2^186 below the largest before it is lost, and a weight, whose second
+            // term is 2^-8 of the first, as far.
             float mx = -INFINITY, mo = -INFINITY, l[4] = {};
             bool written = false;                                        // O holds something
             const int stride = P.split ? 2 : 1;
@@ -1275,13 +1361,18 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         }
                     }
                     // a row whose maximum has grown by more than 2^kGrow takes it over
+                    constexpr float LIFT = BITS8 ? kLift : 0.f;
+                    top_s -= LIFT;
+                    top_o -= LIFT;
                     const bool grow = valid && top_s > mx + kGrow, grow_o = BITS8 ? valid && top_o > mo + kGrow : grow;
                     if (__any_sync(kFull, grow || grow_o)) {
-                        const float keep = grow ? ex2(mx - top_s) : 1.f, keep_o = grow_o ? ex2(mo - top_o) : 1.f;
+                        // in two factors with 8 bits, as units may lie further apart than fp32's range
+                        constexpr float PART = BITS8 ? 0.5f : 1.f;
+                        const float keep = grow ? ex2(PART * (mx - top_s)) : 1.f, keep_o = grow_o ? ex2(PART * (mo - top_o)) : 1.f;
                         if (grow) mx = top_s;
                         if (grow_o) mo = top_o;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) l[i] *= keep;
+                        for (int i = 0; i < 4; ++i) l[i] = BITS8 ? l[i] * keep * keep : l[i] * keep;
                         if (written) {
                             settle();
 #pragma unroll 1
@@ -1290,37 +1381,54 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                                 tmem_ld16(o_addr + 16 * c, o);
                                 uint32_t w[16];
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * keep_o);
+                                for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(BITS8 ? o[j] * keep_o * keep_o : o[j] * keep_o);
                                 tmem_st16(o_addr + 16 * c, w);
                             }
                         }
                     }
                     const float base = mx == -INFINITY ? 0.f : -mx;
-                    const float unit = mo == -INFINITY ? -INFINITY : mx - mo;
-                    // the probabilities of chunk c, in v, to the scores' place
+                    const float base_o = mo == -INFINITY ? 0.f : -mo;
+                    // the probabilities of chunk c, in v, to the scores' place: 16 columns of 32 tokens' or, with 8
+                    // bits, 8 of a page's first terms and 8 of its second
                     auto turn = [&](int c, const float (&v)[32]) {
-                        uint32_t w[16];
+                        if constexpr (!BITS8) {
+                            uint32_t w[16];
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const float k = !BITS8 ? A.scale_log2e : g == 0 ? ks.x : ks.y;
-                            // of a page that the row does not see it may pass fp32's range, and meets zeros
-                            const float f = BITS8 ? ex2(fminf((g == 0 ? lv.x : lv.y) + unit, 127.f)) : 1.f;
-#pragma unroll
-                            for (int j = 16 * g; j < 16 * g + 16; j += 2) {
+                            for (int j = 0; j < 32; j += 2) {
                                 float a, b;
-                                fma2(a, b, v[j], v[j + 1], k, k, base, base);
+                                fma2(a, b, v[j], v[j + 1], A.scale_log2e, A.scale_log2e, base, base);
                                 a = ex2(a);
                                 b = ex2(b);
                                 add2(l[j / 2 % 2 * 2], l[j / 2 % 2 * 2 + 1], a, b);
-                                if constexpr (BITS8) {
+                                w[j / 2] = pack_bf16(a, b);
+                            }
+                            tmem_st16(s_addr + 16 * c, w);
+                        } else {
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                // A page's weights are 2^x of its probabilities, in these units, for any x: its exponentials take
+                                // 2^h of that, all of it unless the scale is zero or far below those that count, the sum of the
+                                // probabilities gives it back, and f is the rest.
+                                const float k = g == 0 ? ks.x : ks.y, x = (g == 0 ? lv.x : lv.y) + (base_o - base);
+                                const float h = fmaxf(x, -kFar), from = base + h, u = ex2(-h), f = ex2(x - h);
+                                uint32_t w[16];
+#pragma unroll
+                                for (int j = 0; j < 16; j += 2) {
+                                    float a, b;
+                                    fma2(a, b, v[16 * g + j], v[16 * g + j + 1], k, k, from, from);
+                                    a = ex2(a);
+                                    b = ex2(b);
+                                    float& l0 = l[j / 2 % 2 * 2];
+                                    float& l1 = l[j / 2 % 2 * 2 + 1];
+                                    fma2(l0, l1, a, b, u, u, l0, l1);
                                     mul2(a, b, f);
-                                    w[j / 2] = pack_half(a, b);
-                                } else {
                                     w[j / 2] = pack_bf16(a, b);
+                                    fma2(a, b, __uint_as_float(w[j / 2] << 16), __uint_as_float(w[j / 2] & 0xFFFF0000u), -1.f, -1.f, a, b);
+                                    w[8 + j / 2] = pack_bf16(a, b);
                                 }
+                                tmem_st16(s_addr + 32 * c + 16 * g, w);
                             }
                         }
-                        tmem_st16(s_addr + 16 * c, w);
                     };
                     auto half_done = [&]() {
                         tmem_wait_st();
@@ -1368,7 +1476,6 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
             float sum = (l[0] + l[1]) + (l[2] + l[3]);
             if constexpr (!BITS8) mo = mx;
             if (!ok) mx = mo = sum = NAN;
-            const bool odd = any && S.poison[P.number % kPortions] == P.number + 1;
             // 16 of the row's outputs, not yet divided by the sum
             auto result = [&](int c, float (&o)[16]) {
                 if (ok && any && live) {
@@ -1376,14 +1483,6 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[j] = ok ? 0.f : NAN;
-                }
-                if (odd && valid) {
-                    float x[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] = 0.f;
-                    add_odd_values<C, BITS8>(A, P, stream, hi, lo, 16 * c, x);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] += x[j];
                 }
             };
             const bool join = P.split && n > 1;      // both streams have a part of the rows
@@ -1398,18 +1497,22 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 if (stream == 0) {
                     const float4 y = other[row];
                     const float m2 = fmaxf(mx, y.x), o2 = fmaxf(mo, y.z);
-                    f0 = mo == -INFINITY ? 0.f : ex2(mo - o2);
-                    f1 = y.z == -INFINITY ? 0.f : ex2(y.z - o2);
-                    sum = (mx == -INFINITY ? 0.f : sum * ex2(mx - m2)) + (y.x == -INFINITY ? 0.f : y.y * ex2(y.x - m2));
+                    constexpr float PART = BITS8 ? 0.5f : 1.f;
+                    auto times = [](float x, float f) { return BITS8 ? x * f * f : x * f; };
+                    f0 = mo == -INFINITY ? 0.f : ex2(PART * (mo - o2));
+                    f1 = y.z == -INFINITY ? 0.f : ex2(PART * (y.z - o2));
+                    sum = (mx == -INFINITY ? 0.f : times(sum, ex2(PART * (mx - m2)))) + (y.x == -INFINITY ? 0.f : times(y.y, ex2(PART * (y.x - m2))));
                     mx = m2;
                     mo = o2;
                     if (!(y.y == y.y)) sum = NAN;
                 }
             }
+            // behind the join: the other stream's tiles have been gone over too
+            const bool odd = any && *(volatile int*)&S.poison[P.number % kPortions] == P.number + 1;
             const bool whole_item = P.begins && P.ends;
             // from the outputs' unit to the sums', in two factors where it may pass the range of one
             const float back = BITS8 && whole_item && mo > -INFINITY ? ex2(0.5f * (mo - mx)) : 1.f;
-            const float scale = whole_item ? (sum == 0.f ? 0.f : back / sum) : 1.f;
+            const float scale = whole_item ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const int64_t t = P.row0 + m * A.tokens + token;
             uint16_t* out = A.out + ((t * A.H + P.h) * A.G + row % A.G) * A.D;
             const int64_t part_row = ((int64_t)blockIdx.x * 2 + (P.begins ? 1 : 0)) * A.part_rows + m * kRows + row;
@@ -1443,7 +1546,19 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                         result(half * CH + c, o);
                         if (NS == 2 && join) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = o[j] * f0 + xch[(c * 16 + j) * kRows + row] * f1;
+                            for (int j = 0; j < 16; ++j) {
+                                const float y = xch[(c * 16 + j) * kRows + row];
+                                o[j] = BITS8 ? o[j] * f0 * f0 + y * f1 * f1 : o[j] * f0 + y * f1;
+                            }
+                        }
+                        // behind the join, whose factors may be zero
+                        if (odd && valid) {
+                            float x[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) x[j] = 0.f;
+                            add_odd_values<C, BITS8>(A, P, S.odd_dims[P.number % kPortions], hi, lo, d0, x);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] += x[j];
                         }
                         if (!writes || d0 >= A.D) continue;
                         if (whole_item) {
@@ -1451,7 +1566,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const float b = BITS8 ? back : 1.f;
-                                w[j] = pack_bf16(o[2 * j] * b * scale, o[2 * j + 1] * b * scale);
+                                w[j] = pack_bf16(o[2 * j] * scale * b * b, o[2 * j + 1] * scale * b * b);
                             }
                             store32(out + d0, w, A.wide_out);
                         } else {
@@ -1483,6 +1598,7 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
 // CTA x began, a slice of its rows.  A thread takes 8 dimensions of a row; of many
 // parts (one request on its own has one in each of dozens of CTAs, each a read from L2
 // or beyond) four lanes take every fourth, then join theirs, always in the same order.
+template <bool BITS8>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedParams A) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PartHead head = A.heads[blockIdx.x];
@@ -1493,12 +1609,19 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         // finished NaN
         __device__ __forceinline__ void add(float ym, float yl, float yo, const float (&v)[8]) {
             const float m2 = fmaxf(m, ym), o2 = fmaxf(mo, yo);
-            l = (m == -INFINITY ? 0.f : l * ex2(m - m2)) + (ym == -INFINITY ? 0.f : yl * ex2(ym != ym ? NAN : ym - m2));
-            const float f0 = mo == -INFINITY ? 0.f : ex2(mo - o2), f1 = yo == -INFINITY ? 0.f : ex2(yo != yo ? NAN : yo - o2);
+            // 8 bits: in two factors, as units may lie further apart than fp32's range; outputs that are not finite stay
+            constexpr float PART = BITS8 ? 0.5f : 1.f;
+            auto times = [](float x, float f) {
+                if constexpr (BITS8) return x - x == 0.f ? x * f * f : x;
+                else return x * f;
+            };
+            l = (m == -INFINITY ? 0.f : times(l, ex2(PART * (m - m2)))) +
+                (ym == -INFINITY ? 0.f : times(yl, ex2(ym != ym ? NAN : PART * (ym - m2))));
+            const float f0 = mo == -INFINITY ? 0.f : ex2(PART * (mo - o2)), f1 = yo == -INFINITY ? 0.f : ex2(yo != yo ? NAN : PART * (yo - o2));
             m = m2;
             mo = o2;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = o[j] * f0 + v[j] * f1;
+            for (int j = 0; j < 8; ++j) o[j] = times(o[j], f0) + times(v[j], f1);
         }
     };
     const int words = A.D / 8, rows = head.tokens * A.G;
@@ -1540,11 +1663,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
             t.add(ym, yl, yo, v);      // of use in the lanes that have a partner
         }
         if (!here || lane != 0) continue;
-        const float back = t.mo > -INFINITY ? ex2(0.5f * (t.mo - t.m)) : 1.f;
-        const float inv = t.l == 0.f ? 0.f : back / t.l;
+        const float back = BITS8 && t.mo > -INFINITY ? ex2(0.5f * (t.mo - t.m)) : 1.f;
+        const float inv = t.l == 0.f ? 0.f : 1.f / t.l;
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack_bf16(t.o[2 * j] * back * inv, t.o[2 * j + 1] * back * inv);
+        for (int j = 0; j < 4; ++j) w[j] = BITS8 ? pack_bf16(t.o[2 * j] * inv * back * back, t.o[2 * j + 1] * inv * back * back) : pack_bf16(t.o[2 * j] * inv, t.o[2 * j + 1] * inv);
         const int64_t row = ((head.row0 + token) * A.H + head.h) * A.G + g;
         *reinterpret_cast<uint4*>(A.out + row * A.D + d * 8) = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -1691,7 +1814,7 @@ int launch_paged(const bsa_paged_attention_args_t& a, PagedParams& A, cudaStream
     A.scale_log2e = scale == 0.f ? 1e-30f : scale;
     A.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     A.s_idesc = f16_idesc(!bits8, a.scale < 0.f, false, kRows, kTile);
-    A.o_idesc = f16_idesc(!bits8, false, true, kRows, a.D <= 64 ? 64 : 128);
+    A.o_idesc = f16_idesc(true, false, true, kRows, a.D <= 64 ? 64 : 128);
     A.parts = reinterpret_cast<float*>(ws);
     A.heads = reinterpret_cast<PartHead*>(ws + parts.heads);
     A.sums = reinterpret_cast<float4*>(ws + parts.sums);
@@ -1720,7 +1843,7 @@ int launch_paged(const bsa_paged_attention_args_t& a, PagedParams& A, cudaStream
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_join_kernel, (const PagedParams)A);
+    e = bits8 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<true>, (const PagedParams)A) : cudaLaunchKernelEx(&cfg, paged_join_kernel<false>, (const PagedParams)A);
     return e == cudaSuccess ? BSA_OK : (int)e;
 }
 
