@@ -506,6 +506,17 @@ cudaError_t launch_pair(void (*plan)(const Params), void (*apply_few)(const Para
 
 Rows ints(const void* p, int64_t n) { return whole_rows(p, n * 4); }
 
+// Nothing shares memory with the workspace.
+bool apart_from(const Rows& scratch, const Rows* out, const Rows* in, int n_out, int n_in, const AllTensors& X, int64_t num_blocks) {
+    for (int i = 0; i < n_out; ++i)
+        if (rows_overlap(scratch, out[i])) return false;
+    for (int j = 0; j < n_in; ++j)
+        if (rows_overlap(scratch, in[j])) return false;
+    for (int t = 0; t < X.n; ++t)
+        if (rows_overlap(scratch, whole_rows(X.p[t], X.bytes[t] * num_blocks))) return false;
+    return true;
+}
+
 // No output shares memory with an input (unless it is that input), another output or
 // a tensor, and no tensor with another.
 bool apart(const Rows* out, const Rows* in, int n_out, int n_in, const AllTensors& X, int64_t num_blocks) {
@@ -579,9 +590,9 @@ extern "C" int bsa_fork_requests(const bsa_block_tensor_t* tensors, int32_t num_
     P.max_blocks = max_blocks;
     P.num_blocks = num_blocks;
     const bool in_place = (in > 0 && table_out == block_table) || (num_reqs > 0 && lens_out == seq_lens);
-    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 ||
-        workspace_bytes < carve_fork(static_cast<uint8_t*>(workspace), &P, in_place))
-        return BSA_ERR_WORKSPACE;
+    const size_t need = carve_fork(static_cast<uint8_t*>(workspace), &P, in_place);
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < need) return BSA_ERR_WORKSPACE;
+    if (!apart_from(whole_rows(workspace, (int64_t)need), outs, ins, 3, 5, X, num_blocks)) return BSA_ERR_SHAPE;
     P.table_in = block_table;
     P.lens_in = seq_lens;
     P.table = in_place ? P.snap_table : block_table;
@@ -620,9 +631,9 @@ extern "C" int bsa_compact_blocks(const bsa_block_tensor_t* tensors, int32_t num
     P.rows = num_reqs;
     P.max_blocks = max_blocks;
     P.num_blocks = num_blocks;
-    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 ||
-        workspace_bytes < carve_compact(static_cast<uint8_t*>(workspace), &P))
-        return BSA_ERR_WORKSPACE;
+    const size_t need = carve_compact(static_cast<uint8_t*>(workspace), &P);
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < need) return BSA_ERR_WORKSPACE;
+    if (!apart_from(whole_rows(workspace, (int64_t)need), outs, ins, 3, 3, X, num_blocks)) return BSA_ERR_SHAPE;
     P.table = block_table;
     P.lens = seq_lens;
     P.refs_in = block_refs;

@@ -1727,7 +1727,19 @@ bool paged_sizes_ok(int64_t T, int64_t H, int64_t G, int64_t D) {
            D >= 16 && D <= BSA_MAX_CACHE_DIM && D % 16 == 0;
 }
 
-// The checks that both forms share; `ints`: the form's own index tensors.
+// Whether a call's inputs share memory with `x`; `ints`: the form's own index tensors.
+bool meets_inputs(const Rows& x, const bsa_paged_attention_args_t& a, const Rows (&ints)[2]) {
+    const bool bits8 = a.cache_dtype != BSA_DTYPE_BF16;
+    const int64_t cache = a.num_pages * kSubPage * a.H * a.D * (bits8 ? 1 : 2), scales = bits8 ? a.num_pages * a.H * 4 : 0;
+    const Rows in[8] = {whole_rows(a.q, a.T * a.H * a.G * a.D * 2), whole_rows(a.k_cache, cache), whole_rows(a.v_cache, cache),
+                        whole_rows(a.k_scale, scales), whole_rows(a.v_scale, scales),
+                        whole_rows(a.block_table, a.num_reqs * a.max_blocks * 4), ints[0], ints[1]};
+    for (const Rows& r : in)
+        if (rows_overlap(x, r)) return true;
+    return false;
+}
+
+// The checks that both forms share.
 int check_paged(const bsa_paged_attention_args_t& a, const Rows (&ints)[2]) {
     if (a.cache_dtype != BSA_DTYPE_BF16 && a.cache_dtype != BSA_DTYPE_E4M3 && a.cache_dtype != BSA_DTYPE_E5M2) return BSA_ERR_DTYPE;
     if (!paged_sizes_ok(a.T, a.H, a.G, a.D) || a.num_pages < 0 || a.num_pages >= (1ll << 27) || a.num_reqs < 0 ||
@@ -1741,14 +1753,7 @@ int check_paged(const bsa_paged_attention_args_t& a, const Rows (&ints)[2]) {
     const void* wide[4] = {a.q, a.out, a.k_cache, a.v_cache};
     for (const void* p : wide)
         if ((reinterpret_cast<uintptr_t>(p) & 15) != 0) return BSA_ERR_ALIGN;
-    const int64_t rows = a.T * a.H * a.G * a.D * 2, cache = a.num_pages * kSubPage * a.H * a.D * (bits8 ? 1 : 2);
-    const int64_t scales = bits8 ? a.num_pages * a.H * 4 : 0;
-    const Rows in[8] = {whole_rows(a.q, rows), whole_rows(a.k_cache, cache), whole_rows(a.v_cache, cache),
-                        whole_rows(a.k_scale, scales), whole_rows(a.v_scale, scales),
-                        whole_rows(a.block_table, a.num_reqs * a.max_blocks * 4), ints[0], ints[1]};
-    for (const Rows& r : in)
-        if (rows_overlap(whole_rows(a.out, rows), r)) return BSA_ERR_SHAPE;
-    return BSA_OK;
+    return meets_inputs(whole_rows(a.out, a.T * a.H * a.G * a.D * 2), a, ints) ? BSA_ERR_SHAPE : BSA_OK;
 }
 
 // Rows of an item's part in the workspace.
@@ -1784,11 +1789,13 @@ cudaError_t launch_kernel(const PagedParams& A, const PagedMaps& M, int grid, cu
     return cudaGetLastError();
 }
 
-int launch_paged(const bsa_paged_attention_args_t& a, PagedParams& A, cudaStream_t st) {
+int launch_paged(const bsa_paged_attention_args_t& a, const Rows (&ints)[2], PagedParams& A, cudaStream_t st) {
     const int grid = device_sm_count();
     const Parts parts = place_parts(a.T, a.G, a.D, grid);
     if (a.workspace == nullptr || a.workspace_bytes < parts.bytes || (reinterpret_cast<uintptr_t>(a.workspace) & 255) != 0)
         return BSA_ERR_WORKSPACE;
+    const Rows scratch = whole_rows(a.workspace, (int64_t)parts.bytes);
+    if (rows_overlap(scratch, whole_rows(a.out, a.T * a.H * a.G * a.D * 2)) || meets_inputs(scratch, a, ints)) return BSA_ERR_SHAPE;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const bool bits8 = a.cache_dtype != BSA_DTYPE_BF16;
     A.out = static_cast<uint16_t*>(a.out);
@@ -1878,7 +1885,7 @@ extern "C" int bsa_paged_attention_decode(const bsa_paged_attention_args_t* args
     PagedParams A{};
     A.seq_lens = seq_lens;
     A.dql = decode_query_len;
-    return launch_paged(a, A, static_cast<cudaStream_t>(stream));
+    return launch_paged(a, ints, A, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int bsa_paged_attention_varlen(const bsa_paged_attention_args_t* args, const int32_t* cu_seqlens_q,
@@ -1893,5 +1900,5 @@ extern "C" int bsa_paged_attention_varlen(const bsa_paged_attention_args_t* args
     PagedParams A{};
     A.cu = cu_seqlens_q;
     A.prefix = prefix_lens;
-    return launch_paged(a, A, static_cast<cudaStream_t>(stream));
+    return launch_paged(a, ints, A, static_cast<cudaStream_t>(stream));
 }

@@ -443,8 +443,9 @@ typedef struct bsa_paged_attention_args {
     int32_t window, sinks;
     float scale;
     /* at least bsa_paged_attention_workspace_bytes(...) bytes, 256-byte
-     * aligned, any contents; may be NULL when that is 0.  Calls that share a
-     * workspace must not overlap on the GPU. */
+     * aligned, any contents; may be NULL when that is 0.  These bytes share no
+     * memory with the rest (BSA_ERR_SHAPE).  Calls that share a workspace must
+     * not overlap on the GPU. */
     void* workspace;
     size_t workspace_bytes;
 } bsa_paged_attention_args_t;
