@@ -1816,9 +1816,10 @@ int launch_paged(const bsa_paged_attention_args_t& a, const Rows (&ints)[2], Pag
     A.cache_dtype = a.cache_dtype;
     A.min_units = kMinSteps * (bits8 ? Cfg<128, true>::SPLIT_UNITS : Cfg<128, false>::SPLIT_UNITS);
     A.part_rows = part_rows(a.T, a.G, a.D);
-    // a scale of zero must not meet the -inf of hidden scores; any tiny one has its result
+    // a scale of zero must not meet the -inf of hidden scores; the least one has its result: times the largest
+    // score it is 2^-21
     const float scale = fabsf(a.scale) * 1.44269504f;
-    A.scale_log2e = scale == 0.f ? 1e-30f : scale;
+    A.scale_log2e = scale == 0.f ? 0x1p-149f : scale;
     A.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     A.s_idesc = f16_idesc(!bits8, a.scale < 0.f, false, kRows, kTile);
     A.o_idesc = f16_idesc(true, false, true, kRows, a.D <= 64 ? 64 : 128);
