@@ -79,3 +79,20 @@ def test_what_is_no_iterable_of_tensors(cuda_device):
     for bad, error in ((5, TypeError), ({"k": tensors[0]}, ValueError), (broken(), KeyError)):
         with pytest.raises(error):
             bsa.bsa_compact_blocks(bad, table, lens, refs)
+
+
+def test_a_compaction_leaves_its_inputs(cuda_device):
+    """The table, lengths and reference counts, where the outputs are new; the lengths always."""
+    st = State(34, 300, 8, cuda_device)
+    for in_place in (False, True):
+        tensors, table, lens, refs = st.on_device()
+        kept = [x.clone() for x in (table, lens, refs)]
+        versions = [x._version for x in (table, lens, refs)]
+        out = bsa.bsa_compact_blocks(tensors, table, lens, refs, **(dict(table_out=table, refs_out=refs) if in_place else {}))
+        assert torch.equal(lens, kept[1]) and lens._version == versions[1]
+        if in_place:
+            assert out[0] is table and out[1] is refs and table._version > versions[0] and refs._version > versions[2]
+        else:
+            assert torch.equal(table, kept[0]) and torch.equal(refs, kept[2])
+            assert [table._version, refs._version] == [versions[0], versions[2]]
+            assert not torch.equal(out[0], table) and not torch.equal(out[1], refs)
