@@ -10,9 +10,9 @@
 // waiting on CTAs that may not be resident.  The application writes the table
 // and copies whole blocks of every tensor, over the whole GPU.
 //
-// Measured: 20480 blocks of 4 heads of 128 in bf16 (5.4 GB), 5100 of them moved, 431 us, 0.92 of a copy's rate,
+// Measured: 20480 blocks of 4 heads of 128 in bf16 (5.4 GB), 5100 of them moved, 425 us, 0.94 of a copy's rate,
 // with 32 KB a CTA in flight; 512 beams of 128 requests, about 155 unfinished blocks copied (262 KB each), 31 us, of
-// which the plan is about 12 (five phases, each a chain of reads from L2); four beams 10 us, by one CTA (by the
+// which the plan is about 12 (five phases, each a chain of reads from L2); four beams 11 us, by one CTA (by the
 // cluster 13), a small compaction 9 us (14).
 //
 // Order and ties: free blocks are taken from the lowest id on, in order of
@@ -118,7 +118,7 @@ __device__ __forceinline__ int64_t checked_len(int64_t n, int64_t max_blocks, ui
     return m;
 }
 
-// Inclusive sum over the CTA's 1024 threads, and the total.  `warps`: 33 words.
+// Inclusive sum over the CTA's 1024 threads, and the total.  `warps`: 32 words.
 __device__ __forceinline__ int cta_scan(int x, int* warps, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll

@@ -106,7 +106,7 @@ struct PagedParams {
     int32_t window, sinks, cache_dtype;
     int32_t min_units;            // the least part of a CTA
     int32_t part_rows;            // rows of a part in the workspace
-    float scale_log2e;            // not negative; q_neg holds the sign
+    float scale_log2e;            // not negative; the scores' instruction negates the queries where the scale is
     uint32_t s_idesc, o_idesc;
     bool wide_out;                // out is 32-byte aligned
     struct PartHead* heads;       // [grid]
