@@ -1259,9 +1259,9 @@ paged_attention_kernel(const __grid_constant__ PagedParams A, const __grid_const
                 lo = A.window > 0 ? (int)(pos - A.window + 1 < 0 ? 0 : pos - A.window + 1 < top ? pos - A.window + 1 : top) : 0;
             }
             // The row's sums are in units of 2^mx and its outputs in units of 2^mo: with bf16 the same; with 8
-            // bits mo goes by the largest weight, a probability times its page's scale.  Both units lie 2^kLift
-            // below: a probability may fall 2^186 below the largest before it is lost, and a weight, whose second
-            // term is 2^-8 of the first, as far.
+            // bits mo goes by the largest weight, a probability times its page's scale.  Both units lie 2^kLift below
+            // the largest: a weight may fall 2^178 below it before its second term is lost, and a probability 2^86
+            // (126 + kLift - kFar; its page's weights are then 2^186 below theirs).
             float mx = -INFINITY, mo = -INFINITY, l[4] = {};
             bool written = false;                                        // O holds something
             const int stride = P.split ? 2 : 1;
